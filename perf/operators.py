@@ -497,7 +497,7 @@ def _exact_adamw(s, case):
 
     def blocks8(x, salt, positive):
         pad = torch.cat([x, x.new_zeros(-x.numel() % 32)]).view(-1, 32)
-        most = pad.abs().max(1).values.clamp(min=2.0 ** -118)
+        most = pad.abs().max(1).values.clamp(min=448 * 2.0 ** -127)
         e = torch.ceil(torch.log2(most / 448.0))
         y = dithered((pad.abs() / torch.exp2(e)[:, None]).view(-1)[: x.numel()], -6, 3, salt)
         if positive:
