@@ -3,21 +3,27 @@
 The fused lm_head projection, log-softmax and GRPO objective (reverse-KL
 estimator plus the exp(q - q.detach()) * A advantage term) over the
 flattened token axis, in hand-written sm_103a CUDA kernels behind the C ABI
-of include/grpo.h. Importing the package does not load the library; the
-first call does, and raises if it has not been built.
+of include/grpo.h; and the operators around that loss in a GRPO iteration: the
+draw of completion tokens (``sample``), the norm before the head with its
+gradients (``layer_norm``) and the optimizer step (``AdamW``). Importing the
+package does not load the library; the first call does, and raises if it has
+not been built.
 """
 from __future__ import annotations
+
+from typing import Optional, Sequence
 
 import torch
 
 from . import _lib
-from ._lib import (GrpoError, Problem, advantages, device_status, loss_bwd, loss_bwd_e4m3,
-                   loss_fwd, loss_fwd_e4m3, make_problem, profile_collect, profile_enable,
-                   quantize_e4m3_rows, workspace_size)
+from ._lib import (GrpoError, Problem, advantages, device_status, layernorm_bwd, layernorm_fwd,
+                   loss_bwd, loss_bwd_e4m3, loss_fwd, loss_fwd_e4m3, make_problem,
+                   profile_collect, profile_enable, quantize_e4m3_rows, sample, workspace_size)
 
-__all__ = ["GrpoError", "Problem", "advantages", "device_status", "loss_bwd", "loss_bwd_e4m3",
-           "loss_fwd", "loss_fwd_e4m3", "make_problem", "profile_collect", "profile_enable",
-           "quantize_e4m3_rows", "workspace_size", "GRPOLoss", "grpo_loss"]
+__all__ = ["GrpoError", "Problem", "advantages", "device_status", "layernorm_bwd",
+           "layernorm_fwd", "loss_bwd", "loss_bwd_e4m3", "loss_fwd", "loss_fwd_e4m3",
+           "make_problem", "profile_collect", "profile_enable", "quantize_e4m3_rows", "sample",
+           "workspace_size", "GRPOLoss", "grpo_loss", "layer_norm", "AdamW"]
 
 
 _CTRL_BYTES = 256  # control block at the start of every workspace (error word, counts)
@@ -163,3 +169,128 @@ def grpo_loss(H_pol, H_ref, W, ids, mask, adv, engine: GRPOLoss):
     was built with ``compute_dW`` (the reference model is frozen; kl_mean is a
     metric and carries no gradient)."""
     return _GRPOLossFn.apply(H_pol, H_ref, W, ids, mask, adv, engine)
+
+
+class _LayerNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, rms):
+        y, mean, rstd = layernorm_fwd(x, weight, bias, eps=eps, rms=rms)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.rms, ctx.bias_dtype = rms, None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        if dy.stride(-1) != 1 or (dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]):
+            dy = dy.contiguous()        # a broadcast gradient, as of a sum
+        dx, dw, db = layernorm_bwd(x, weight, dy.to(x.dtype), mean, rstd, rms=ctx.rms, bias=need_b,
+                                   need_dweight=need_w)
+        return (dx if need_x else None, dw.to(weight.dtype) if need_w else None,
+                db.to(ctx.bias_dtype) if need_b else None, None, None)
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, rms: bool = False) -> torch.Tensor:
+    """Autograd entry of the norm over the last dimension of ``x`` (RMS norm
+    with ``rms``, which takes no bias): gradients for x, weight and bias. Capture
+    ``layernorm_fwd`` and ``layernorm_bwd`` into a CUDA graph rather than this."""
+    return _LayerNormFn.apply(x.reshape(-1, x.shape[-1]), weight, bias, eps, rms).view(x.shape)
+
+
+class AdamW:
+    """AdamW over a list of CUDA tensors (float32 or bf16, contiguous), one call
+    for all of them; the arithmetic and the state formats are those of
+    grpo_adamw_step.
+
+    ``state_bits`` 32 keeps the two moments in float32, 8 as e4m3 codes with a
+    power of two for each 32 values. ``master=True`` keeps float32 masters of the
+    bf16 parameters; without one a bf16 parameter is rounded with the step's
+    dither, so that updates below half a bf16 step still count. ``weight_decay``
+    is one number or one for each tensor.
+
+    ``step(grads)`` applies the gradients (float32 or bf16, of the parameters'
+    shapes). With ``out``, an AdamW over other tensors of the same shapes and
+    types, the new parameters and states are written there and this object's stay
+    as they are.
+    """
+
+    def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas=(0.9, 0.999),
+                 eps: float = 1e-8, weight_decay=0.01, state_bits: int = 32, master: bool = False):
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32, got %r" % (state_bits,))
+        self.params = list(params)
+        self.lr, self.betas, self.eps, self.state_bits = lr, tuple(betas), eps, state_bits
+        n = len(self.params)
+        wd = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        if len(wd) != n:
+            raise ValueError("weight_decay must be one number or %d, got %d" % (n, len(wd)))
+        self.weight_decay = wd
+        self.step_count = 0
+        self.device = self.params[0].device if n else None
+        self.masters, self.exp_avg, self.exp_avg_sq = [], [], []
+        self.exp_avg_scale, self.exp_avg_sq_scale = [], []
+        eight = state_bits == 8
+        self._table = (_lib.AdamwTensor * max(n, 1))()
+        for i, p in enumerate(self.params):
+            code = _lib._plain_code(p.dtype, "params[%d]" % i)
+            _lib._ptr(p, "params[%d]" % i)
+            if p.device != self.device:
+                raise ValueError("params[%d] must be on %s, got %s" % (i, self.device, p.device))
+            self.masters.append(p.detach().float() if master and p.dtype == torch.bfloat16 else None)
+            st = dict(dtype=torch.uint8 if eight else torch.float32, device=p.device)
+            self.exp_avg.append(torch.zeros(p.shape, **st))
+            self.exp_avg_sq.append(torch.zeros(p.shape, **st))
+            for scales in (self.exp_avg_scale, self.exp_avg_sq_scale):
+                scales.append(torch.zeros((p.numel() + 31) // 32, **st) if eight else None)
+            t = self._table[i]
+            t.n, t.param_dtype, t.weight_decay = p.numel(), code, wd[i]
+            t.param, t.m, t.v = (x.data_ptr() for x in (p, self.exp_avg[i], self.exp_avg_sq[i]))
+            t.master = None if self.masters[i] is None else self.masters[i].data_ptr()
+            if eight:
+                t.m_scale, t.v_scale = self.exp_avg_scale[i].data_ptr(), self.exp_avg_sq_scale[i].data_ptr()
+
+    def _point(self, out: Optional["AdamW"]) -> None:
+        """Outputs into ``out``'s buffers, or in place."""
+        for i in range(len(self.params)):
+            t = self._table[i]
+            if out is None:
+                t.param_out = t.master_out = t.m_out = t.v_out = t.m_scale_out = t.v_scale_out = None
+            else:
+                o = out._table[i]
+                t.param_out, t.master_out, t.m_out, t.v_out = o.param, o.master, o.m, o.v
+                t.m_scale_out, t.v_scale_out = o.m_scale, o.v_scale
+
+    def step(self, grads: Sequence[torch.Tensor], grad_scale: float = 1.0, lr: Optional[float] = None,
+             step: Optional[int] = None, out: Optional["AdamW"] = None, stream=None) -> None:
+        """``step`` overrides the count of steps taken (1 for the first), ``lr``
+        this step's rate; ``grad_scale`` multiplies every gradient."""
+        if len(grads) != len(self.params):
+            raise ValueError("expected %d gradients, got %d" % (len(self.params), len(grads)))
+        if out is not None:
+            if out is self or out.state_bits != self.state_bits or \
+                    [(p.shape, p.dtype) for p in out.params] != [(p.shape, p.dtype) for p in self.params] or \
+                    [m is None for m in out.masters] != [m is None for m in self.masters]:
+                raise ValueError("out must be another AdamW of the same shapes, types and states")
+        if not self.params:
+            return
+        for i, (g, p) in enumerate(zip(grads, self.params)):
+            if g.shape != p.shape:
+                raise ValueError("grads[%d] must have shape %s, got %s" % (i, tuple(p.shape), tuple(g.shape)))
+            if g.device != self.device or not g.is_contiguous():
+                raise ValueError("grads[%d] must be contiguous and on %s" % (i, self.device))
+            t = self._table[i]
+            t.grad_dtype = _lib._plain_code(g.dtype, "grads[%d]" % i)
+            t.grad = g.data_ptr()
+        self._point(out)
+        count = self.step_count + 1 if step is None else step
+        config = _lib.AdamwConfig(self.lr if lr is None else lr, self.betas[0], self.betas[1],
+                                  self.eps, grad_scale, self.state_bits, count)
+        with torch.cuda.device(self.device):
+            _lib.adamw_step(config, self._table, len(self.params), stream)
+        torch.autograd.graph.increment_version((self if out is None else out).params)
+        if out is not None:
+            out.step_count = count
+        else:
+            self.step_count = count

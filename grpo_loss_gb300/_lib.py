@@ -45,6 +45,37 @@ class Problem(ctypes.Structure):
                 ("cluster_mode", ctypes.c_int32)]
 
 
+class SampleProblem(ctypes.Structure):
+    """Mirror of ``grpo_sample_problem``."""
+    _fields_ = [("rows", ctypes.c_int64), ("V", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
+class LayernormProblem(ctypes.Structure):
+    """Mirror of ``grpo_layernorm_problem``."""
+    _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int64), ("ld_x", ctypes.c_int64),
+                ("ld_y", ctypes.c_int64), ("ld_dy", ctypes.c_int64), ("ld_dx", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("rms", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32)]
+
+
+class AdamwTensor(ctypes.Structure):
+    """Mirror of ``grpo_adamw_tensor``."""
+    _fields_ = [("n", ctypes.c_int64)] + \
+        [(k, ctypes.c_void_p) for k in ("grad", "param", "master", "m", "v", "m_scale", "v_scale",
+                                        "param_out", "master_out", "m_out", "v_out",
+                                        "m_scale_out", "v_scale_out")] + \
+        [("weight_decay", ctypes.c_float), ("param_dtype", ctypes.c_int32),
+         ("grad_dtype", ctypes.c_int32)]
+
+
+class AdamwConfig(ctypes.Structure):
+    """Mirror of ``grpo_adamw_config``."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("grad_scale", ctypes.c_float),
+                ("state_bits", ctypes.c_int32), ("step", ctypes.c_int64)]
+
+
 def make_problem(num_seqs: int, seq_len: int, d: int, V: int, group_size: int,
                  beta: float = 0.04, eps: float = 1e-4, std_unbiased: int = 1,
                  chunk_rows: int = 0, dtype=torch.bfloat16, compute_dW: int = 0,
@@ -96,6 +127,14 @@ _SIGNATURES = {
                            [ctypes.c_float, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
     "grpo_quantize_e4m3_rows": (ctypes.c_int, [_VP, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
                                                _VP, _VP, _VP]),
+    "grpo_sample": (ctypes.c_int, [ctypes.POINTER(SampleProblem)] + [_VP] * 9),
+    "grpo_layernorm_workspace_size": (ctypes.c_int, [ctypes.POINTER(LayernormProblem),
+                                                     ctypes.POINTER(ctypes.c_size_t)]),
+    "grpo_layernorm_fwd": (ctypes.c_int, [ctypes.POINTER(LayernormProblem)] + [_VP] * 7),
+    "grpo_layernorm_bwd": (ctypes.c_int, [ctypes.POINTER(LayernormProblem)] + [_VP] * 9 +
+                           [ctypes.c_size_t, _VP]),
+    "grpo_adamw_step": (ctypes.c_int, [ctypes.POINTER(AdamwConfig), ctypes.POINTER(AdamwTensor),
+                                       ctypes.c_int32, _VP]),
     "grpo_get_device_status": (ctypes.c_int, [_VP, _VP]),
     "grpo_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "grpo_profile_enable": (ctypes.c_int, [ctypes.c_int32]),
@@ -269,6 +308,156 @@ def loss_bwd_e4m3(problem: Problem, H_pol, s_pol, W, s_W, ids, mask, adv, logp_p
         _ptr(dW, "dW", torch.float32, Vd),
         _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
         _stream(stream)), "grpo_loss_bwd_e4m3")
+
+
+def _plain_code(dtype, name: str) -> int:
+    """grpo_dtype of float32 or bfloat16."""
+    if dtype == torch.float32:
+        return GRPO_F32
+    if dtype == torch.bfloat16:
+        return GRPO_BF16
+    raise ValueError("%s must be float32 or bfloat16, got %s" % (name, dtype))
+
+
+def _rows_ptr(t: torch.Tensor, name: str, dtype, rows: int, cols: int):
+    """(pointer, row stride) of a [rows, cols] CUDA matrix whose columns are
+    contiguous; the rows may be strided."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError("%s must have shape (%d, %d), got %s" % (name, rows, cols, tuple(t.shape)))
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError("%s must be contiguous along its last dimension" % name)
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
+        raise ValueError("%s must have a row stride of at least %d, got %d" % (name, cols, ld))
+    return t.data_ptr(), ld
+
+
+def _on(device, **tensors) -> None:
+    """Raise unless every tensor given is on ``device``."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None,
+           min_p=None, tokens=None, logp=None, stream=None):
+    """One token a row of ``logits`` (float32 or bf16 [rows, V], rows may be
+    strided) from the uniforms ``u`` (float32 [rows]): (tokens int32 [rows],
+    logp float32 [rows]). ``temperature``, ``top_p``, ``min_p`` (float32 [rows])
+    and ``top_k`` (int32 [rows]) are optional; see grpo_sample for the
+    definition. logp is the token's log-probability under the full softmax at
+    its temperature, what a GRPOLoss with that temperature calls logp_pol."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D")
+    rows, V = logits.shape
+    code = _plain_code(logits.dtype, "logits")
+    ptr, ld = _rows_ptr(logits, "logits", logits.dtype, rows, V)
+    dev = logits.device
+    if tokens is None:
+        tokens = torch.empty(rows, dtype=torch.int32, device=dev)
+    if logp is None:
+        logp = torch.empty(rows, dtype=torch.float32, device=dev)
+    _on(dev, u=u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, tokens=tokens,
+        logp=logp)
+    f32 = torch.float32
+    problem = SampleProblem(rows, V, ld, code)
+    with torch.cuda.device(dev):
+        _check(lib().grpo_sample(
+            ctypes.byref(problem), ptr, _ptr(u, "u", f32, rows),
+            _ptr(temperature, "temperature", f32, rows), _ptr(top_k, "top_k", torch.int32, rows),
+            _ptr(top_p, "top_p", f32, rows), _ptr(min_p, "min_p", f32, rows),
+            _ptr(tokens, "tokens", torch.int32, rows), _ptr(logp, "logp", f32, rows),
+            _stream(stream)), "grpo_sample")
+    return tokens, logp
+
+
+def layernorm_workspace_size(problem: LayernormProblem) -> int:
+    """Bytes of grpo_layernorm_bwd's workspace on the current device."""
+    b = ctypes.c_size_t(0)
+    _check(lib().grpo_layernorm_workspace_size(ctypes.byref(problem), ctypes.byref(b)),
+           "grpo_layernorm_workspace_size")
+    return b.value
+
+
+def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float = 1e-5,
+                  rms: bool = False, y=None, mean=None, rstd=None, stream=None):
+    """Layer norm (RMS norm with ``rms``) of the rows of ``x`` (float32 or bf16
+    [rows, d], rows may be strided): (y, mean, rstd), mean None with ``rms``.
+    ``weight`` and ``bias`` are float32 or bf16 [d], of one type."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    rows, d = x.shape
+    dev, f32 = x.device, torch.float32
+    code = _plain_code(x.dtype, "x")
+    xp, ld_x = _rows_ptr(x, "x", x.dtype, rows, d)
+    if y is None:
+        y = torch.empty(rows, d, dtype=x.dtype, device=dev)
+    yp, ld_y = _rows_ptr(y, "y", x.dtype, rows, d)
+    if mean is None and not rms:
+        mean = torch.empty(rows, dtype=f32, device=dev)
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=f32, device=dev)
+    _on(dev, weight=weight, bias=bias, y=y, mean=mean, rstd=rstd)
+    problem = LayernormProblem(rows, d, ld_x, ld_y, 0, 0, eps, 1 if rms else 0, code,
+                               _plain_code(weight.dtype, "weight"))
+    with torch.cuda.device(dev):
+        _check(lib().grpo_layernorm_fwd(
+            ctypes.byref(problem), xp, _ptr(weight, "weight", weight.dtype, d),
+            _ptr(bias, "bias", weight.dtype, d), yp, None if rms else _ptr(mean, "mean", f32, rows),
+            _ptr(rstd, "rstd", f32, rows), _stream(stream)), "grpo_layernorm_fwd")
+    return y, None if rms else mean, rstd
+
+
+def layernorm_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, mean, rstd,
+                  rms: bool = False, bias: bool = True, dx=None, dweight=None, dbias=None,
+                  need_dweight: bool = True, workspace=None, stream=None):
+    """Gradients of ``layernorm_fwd`` from its inputs and statistics: (dx,
+    dweight, dbias), dx of x's type, the column sums float32 [d]; dweight is None
+    without ``need_dweight``, dbias without ``bias`` or with ``rms``."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    rows, d = x.shape
+    dev, f32 = x.device, torch.float32
+    code = _plain_code(x.dtype, "x")
+    xp, ld_x = _rows_ptr(x, "x", x.dtype, rows, d)
+    gp, ld_dy = _rows_ptr(dy, "dy", x.dtype, rows, d)
+    if dx is None:
+        dx = torch.empty(rows, d, dtype=x.dtype, device=dev)
+    dxp, ld_dx = _rows_ptr(dx, "dx", x.dtype, rows, d)
+    if dweight is None and need_dweight:
+        dweight = torch.empty(d, dtype=f32, device=dev)
+    if dbias is None and bias and not rms:
+        dbias = torch.empty(d, dtype=f32, device=dev)
+    if mean is None and not rms:
+        raise ValueError("mean is needed unless rms")
+    problem = LayernormProblem(rows, d, ld_x, 0, ld_dy, ld_dx, 0.0, 1 if rms else 0, code,
+                               _plain_code(weight.dtype, "weight"))
+    with torch.cuda.device(dev):
+        if workspace is None and (dweight is not None or dbias is not None):
+            workspace = torch.empty(layernorm_workspace_size(problem), dtype=torch.uint8, device=dev)
+        _on(dev, weight=weight, dy=dy, mean=mean, rstd=rstd, dx=dx, dweight=dweight, dbias=dbias,
+            workspace=workspace)
+        _check(lib().grpo_layernorm_bwd(
+            ctypes.byref(problem), xp, _ptr(weight, "weight", weight.dtype, d), gp,
+            None if rms else _ptr(mean, "mean", f32, rows), _ptr(rstd, "rstd", f32, rows), dxp,
+            _ptr(dweight, "dweight", f32, d), _ptr(dbias, "dbias", f32, d),
+            _ptr(workspace, "workspace"),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _stream(stream)), "grpo_layernorm_bwd")
+    return dx, dweight, dbias
+
+
+def adamw_step(config: AdamwConfig, tensors, n: int, stream=None) -> None:
+    """One grpo_adamw_step over a ctypes array of AdamwTensor (on the current
+    device); the AdamW class checks the tensors and fills the array."""
+    _check(lib().grpo_adamw_step(ctypes.byref(config), tensors, n, _stream(stream)),
+           "grpo_adamw_step")
 
 
 def device_status(workspace: torch.Tensor, stream=None) -> int:

@@ -20,8 +20,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgrpo_gb300.so")
-SOURCES = ["gemm_tc.cu", "rows.cu", "grpo_api.cu", "noalloc.cu"]
-HEADERS = ["ptx.cuh", "internal.h"]
+SOURCES = ["gemm_tc.cu", "rows.cu", "grpo_api.cu", "noalloc.cu", "sample.cu", "norm.cu", "adamw.cu",
+           "ops_api.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "api_common.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "-I" + os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]

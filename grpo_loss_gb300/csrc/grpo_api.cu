@@ -8,12 +8,11 @@
 #include <math.h>
 #include <string.h>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include <mutex>
 #include <vector>
 
 #include "../../include/grpo.h"
+#include "api_common.h"
 #include "internal.h"
 
 using namespace grpo;
@@ -27,7 +26,6 @@ constexpr int kMaxSlices = 8;                      // vocab slices per block in 
 constexpr double kL2ABudget = 40e6;                // bytes of A blocks kept resident in L2
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ------------------------------------------------------------ profiling
 struct Profiler {
@@ -43,7 +41,12 @@ constexpr size_t kMaxProfiled = 65536;
 const char* kKindNames[K_NUM_KINDS] = {
     "advantages", "convert_bf16", "seq_count",  "block_plan",  "fwd_gemm_lse", "fwd_finish",
     "fwd_reduce", "bwd_coef",     "transpose_w", "zero_rows",  "bwd_dz_gemm",  "bwd_dh_gemm",
-    "bwd_dw_gemm", "transpose_h",  "quantize_e4m3"};
+    "bwd_dw_gemm", "transpose_h",  "quantize_e4m3", "sample", "norm_fwd", "norm_bwd",
+    "norm_colsum", "adamw"};
+
+}  // namespace
+
+namespace grpo {
 
 void prof_begin(int k, cudaStream_t s) {
   if (!g_prof.on || g_prof.used >= kMaxProfiled) return;
@@ -66,20 +69,9 @@ void prof_end(cudaStream_t s) {
   g_prof.used++;
 }
 
-#define LAUNCH(kind, stream, call)         \
-  do {                                     \
-    prof_begin(kind, stream);              \
-    cudaError_t e_ = (call);               \
-    prof_end(stream);                      \
-    if (e_ != cudaSuccess) return GRPO_ERR_CUDA; \
-  } while (0)
+}  // namespace grpo
 
-// NVTX range around one library call (visible in Nsight Systems timelines;
-// a no-op when no tool is attached).
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-};
+namespace {
 
 // ------------------------------------------------------- device properties
 struct DeviceInfo {
@@ -90,7 +82,9 @@ struct DeviceInfo {
 std::mutex g_dev_mu;
 DeviceInfo g_dev[64];
 
-grpo_status device_info(int* sms) {
+}  // namespace
+
+grpo_status grpo::device_info(int* sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GRPO_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_dev_mu);
@@ -104,6 +98,8 @@ grpo_status device_info(int* sms) {
   *sms = di.sms;
   return GRPO_OK;
 }
+
+namespace {
 
 // Sets the kernels' shared-memory limits once per device and returns how
 // many CTA pairs of the cta_group::2 kernels can be resident at once.
@@ -386,8 +382,6 @@ grpo_status make_plan(const grpo_problem* p, Plan* pl) {
   P.b_total = o;
   return GRPO_OK;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Logit transform parameters of a problem (0 in a field means "off").
 void set_xform(const grpo_problem* p, GemmArgs* g) {

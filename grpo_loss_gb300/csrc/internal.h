@@ -97,6 +97,11 @@ enum KernelKind : int {
   K_BWD_DW_GEMM,
   K_TRANSPOSE_H,
   K_QUANTIZE,
+  K_SAMPLE,
+  K_NORM_FWD,
+  K_NORM_BWD,
+  K_NORM_COLSUM,
+  K_ADAMW,
   K_NUM_KINDS
 };
 
@@ -143,5 +148,77 @@ cudaError_t launch_quantize_e4m3_rows(const void* x, int x_f32, int64_t rows, in
                                       uint8_t* q, float* scale, cudaStream_t s);
 cudaError_t launch_zero_invalid_rows(const int* inv, int64_t N, int64_t d, void* out,
                                      int out_f32, cudaStream_t s);
+
+// --------------------------------------------------------------- sample.cu
+struct SampleArgs {
+  const void* logits;
+  int64_t rows, V, ld;
+  int bf16;
+  const float* u;
+  const float* temperature;  // the four parameter arrays may be null
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t* tokens;
+  float* logp;
+};
+cudaError_t launch_sample(const SampleArgs& a, int sms, cudaStream_t s);
+
+// ----------------------------------------------------------------- norm.cu
+struct NormArgs {
+  int64_t rows, d;
+  int64_t ld_x, ld_y, ld_dy, ld_dx;
+  float eps;
+  int rms;
+  int bf16;        // x, y, dy, dx are bf16 (else float32)
+  int param_bf16;  // weight and bias are bf16 (else float32)
+  const void* x;
+  const void* weight;
+  const void* bias;
+  void* y;
+  const void* dy;
+  void* dx;
+  float* mean;
+  float* rstd;
+  float* dweight;
+  float* dbias;
+  float* partial;  // [parts][2][d] partial column sums
+};
+int norm_parts(const NormArgs& a, int sms);  // row groups of the backward's partial column sums
+cudaError_t launch_norm_fwd(const NormArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_norm_colsum(const NormArgs& a, int sms, cudaStream_t s);
+
+// ---------------------------------------------------------------- adamw.cu
+struct AdamTensor {
+  const void* g;
+  const void* p;
+  const float* w;  // master, or null
+  const void* m;
+  const void* v;
+  const uint8_t* ms;
+  const uint8_t* vs;
+  void* p_out;
+  float* w_out;
+  void* m_out;
+  void* v_out;
+  uint8_t* ms_out;
+  uint8_t* vs_out;
+  int64_t n;
+  float keep;       // 1 - lr * weight_decay
+  uint32_t chunk0;  // first work chunk of this tensor
+};
+struct AdamConst {
+  float beta1, one_m_beta1, beta2, one_m_beta2;
+  float lr_t;       // lr / (1 - beta1^t)
+  float rsqrt_c2;   // 1 / sqrt(1 - beta2^t)
+  float eps, grad_scale;
+  uint32_t dither;  // t * 0xC13FA9A9 mod 2^32
+};
+enum AdamKind : int { ADAM_P_BF16 = 1, ADAM_G_BF16 = 2, ADAM_MASTER = 4, ADAM_BITS8 = 8 };
+constexpr int kAdamMaxTensors = 256;  // of one launch (its table is a kernel parameter)
+// `t[0..n)` share `kind`; chunk0 is filled in here.
+cudaError_t launch_adamw(AdamTensor* t, int n, int kind, const AdamConst& c, int sms,
+                         cudaStream_t s);
 
 }  // namespace grpo

@@ -307,6 +307,166 @@ grpo_status grpo_loss_bwd_e4m3(const grpo_problem *problem, const uint8_t *H_pol
                                void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The operators around the loss head. One GRPO iteration draws completions
+ * from the head's logits (grpo_sample), forms the hidden states the head reads
+ * with a norm (grpo_layernorm_fwd), takes the loss and its gradients (above),
+ * carries dH back through the norm (grpo_layernorm_bwd) and applies dW and the
+ * other gradients (grpo_adamw_step). The conventions above hold, except that
+ * pointers need only their element's alignment and rows may be strided; the
+ * kernels take 16-byte accesses where addresses allow them.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Token sampling from given random numbers, one token a row.
+ *
+ * Row z[0..V), its temperature T, top_k k, top_p p, min_p q and uniform u in
+ * [0, 1). A NaN logit counts as -inf. With zmax = max z,
+ *   w_i = exp((z_i - zmax) / T), 0 where that is below 2^-40;
+ *   1. of the tokens with w_i >= q, the first k in the order (logit descending,
+ *      index ascending), stay;
+ *   2. of these, in that order, each token stays before which the mass is
+ *      below p times the mass of step 1's tokens (the first always stays);
+ *   token = the smallest index i with sum_{j <= i, kept} w_j > u * sum_kept w_j;
+ *   logp  = (z_token - zmax) / T - ln sum_all w: the log-probability under the
+ *           full softmax at temperature T, the quantity grpo_loss_fwd calls q.
+ * Weights and their sums are integers of fixed point (2^-44 of the largest
+ * weight, fewer bits for V above 2^18), so the token does not depend on how a
+ * row is split or on any order of summation.
+ * T <= 0 or NaN: the token of the largest logit (lowest index), logp at T = 1.
+ * k <= 0, p >= 1, q <= 0 and NaN p or q switch a cut-off off; q > 1 counts as 1;
+ * p <= 0 keeps the first token only. u is clamped to [0, 1 - 2^-24], NaN to 0.
+ * A row of -inf has no token: token -1, logp -inf.
+ *
+ *   logits  [rows, V] of dtype (GRPO_F32 or GRPO_BF16), row stride ld elements
+ *   u       float32 [rows]
+ *   temperature, top_p, min_p  float32 [rows], top_k int32 [rows]; each may be
+ *           NULL (1, off, off, off)
+ *   tokens  int32 [rows], written     logp  float32 [rows], written
+ * INVALID_ARG for null pointers, rows < 0, V < 1, ld below V or another dtype;
+ * UNSUPPORTED for pointers off their element's alignment and V or rows of 2^31
+ * or more. rows = 0 launches nothing.
+ */
+typedef struct grpo_sample_problem {
+  int64_t rows;
+  int64_t V;
+  int64_t ld;        /* row stride of logits in elements; 0 = V */
+  grpo_dtype dtype;
+} grpo_sample_problem;
+
+grpo_status grpo_sample(const grpo_sample_problem *problem, const void *logits, const float *u,
+                        const float *temperature, const int32_t *top_k, const float *top_p,
+                        const float *min_p, int32_t *tokens, float *logp, cudaStream_t stream);
+
+/*
+ * Layer norm over rows of d values, and its RMS form (rms = 1: no mean, no
+ * bias):
+ *   mean = sum x / d, rstd = 1 / sqrt(sum (x - mean)^2 / d + eps),
+ *   y = (x - mean) * rstd * weight + bias
+ * and with g = dy * weight, h = (x - mean) * rstd
+ *   dx = rstd * (g - sum g / d - h * sum(g h) / d)    (rms: without sum g / d)
+ *   dweight = sum over rows of dy * h,   dbias = sum over rows of dy.
+ * Statistics and every sum are float32 or wider; y and dx are rounded once.
+ * The column sums run in a fixed order: results do not vary between calls.
+ *
+ *   x, y, dy, dx  [rows, d] of dtype (GRPO_F32 or GRPO_BF16), row strides ld_*
+ *   weight, bias  [d] of param_dtype (GRPO_F32 or GRPO_BF16); bias may be NULL
+ *   mean, rstd    float32 [rows], written by the forward and read by the
+ *                 backward; in the forward either may be NULL; mean is not used
+ *                 with rms
+ *   dweight, dbias  float32 [d], written, each may be NULL (a frozen norm, a
+ *                 norm with no bias); dbias must be NULL with rms
+ * y may be x and dx may be dy or x (same stride). The backward's workspace
+ * (grpo_layernorm_workspace_size, for the current device) holds the partial
+ * column sums; it may be NULL when both column outputs are. rows = 0 writes
+ * zeros to dweight and dbias. INVALID_ARG for null pointers, rows < 0, d < 1,
+ * a stride below d, eps that is negative or not finite, another dtype;
+ * UNSUPPORTED for d > 65536, rows of 2^31 or more and pointers off their
+ * element's alignment.
+ */
+typedef struct grpo_layernorm_problem {
+  int64_t rows;
+  int64_t d;
+  int64_t ld_x, ld_y, ld_dy, ld_dx; /* row strides in elements; 0 = d */
+  float eps;
+  int32_t rms;
+  grpo_dtype dtype;
+  grpo_dtype param_dtype;
+} grpo_layernorm_problem;
+
+grpo_status grpo_layernorm_workspace_size(const grpo_layernorm_problem *problem,
+                                          size_t *bwd_bytes);
+grpo_status grpo_layernorm_fwd(const grpo_layernorm_problem *problem, const void *x,
+                               const void *weight, const void *bias, void *y, float *mean,
+                               float *rstd, cudaStream_t stream);
+grpo_status grpo_layernorm_bwd(const grpo_layernorm_problem *problem, const void *x,
+                               const void *weight, const void *dy, const float *mean,
+                               const float *rstd, void *dx, float *dweight, float *dbias,
+                               void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * One AdamW step over many tensors at once, step number t = config->step >= 1:
+ *   g = grad_scale * grad,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   x = x (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in float32. x is the float32 master where the tensor has one (the parameter
+ * is then only written: x in its own type, to nearest), else the parameter.
+ *
+ * state_bits = 32: m and v are float32 [n]. state_bits = 8: m and v are e4m3
+ * codes [n] with one power of two for each 32 consecutive values (the last
+ * block may be short): value = code * 2^(scale - 127), scale byte [ceil(n/32)].
+ * The power is the smallest that brings the block to 448 or less; byte 255
+ * marks a block that held an infinity or a NaN and reads as NaN. Zeroed bytes
+ * are zero states. v of a block that is not all zero is at least its smallest
+ * code step, so that no update divides by a v that was rounded away.
+ *
+ * 8-bit codes, and bf16 parameters with no master, are not rounded to nearest:
+ * a state moves by (1 - beta) of its distance a step, which to nearest is less
+ * than half a code and would be lost at every step (v then settles at a quarter
+ * of the mean square gradient). Each magnitude is rounded up by the dither
+ *   ((i * 0x91E10DA5 + t * 0xC13FA9A9 + salt) mod 2^32) div 2^16, in 2^-16 of a
+ * code, i the element's index in its tensor, salt 0 for m, 0x55555555 for v
+ * and 0xAAAAAAAA for parameters: an additive recurrence over index and step,
+ * so that over the steps a value is rounded up its share of the times.
+ *
+ * Every *_out pointer may be NULL (in place) or name another buffer of the same
+ * kind, which leaves the old state as it was (for a step that may be rolled
+ * back, or a generator that still reads the old weights). Buffers of different
+ * kinds or tensors must not overlap, nor may an output overlap its own input
+ * except as a whole. `tensors` is host memory, read before the call returns.
+ * Tensors with n = 0 are skipped.
+ * INVALID_ARG for null pointers, n < 0, step < 1, betas outside [0, 1), eps or
+ * lr or weight_decay that is negative or not finite, a grad_scale that is not
+ * finite, state_bits other than 8 and 32, dtypes other than GRPO_F32 and
+ * GRPO_BF16, a master beside a float32 parameter; UNSUPPORTED for pointers off
+ * their element's alignment.
+ */
+typedef struct grpo_adamw_tensor {
+  int64_t n;
+  const void *grad;       /* [n] of grad_dtype */
+  void *param;            /* [n] of param_dtype */
+  float *master;          /* [n], or NULL */
+  void *m, *v;            /* [n] float32, or [n] e4m3 codes */
+  uint8_t *m_scale, *v_scale; /* [ceil(n/32)] with state_bits = 8, else NULL */
+  void *param_out;
+  float *master_out;
+  void *m_out, *v_out;
+  uint8_t *m_scale_out, *v_scale_out;
+  float weight_decay;
+  grpo_dtype param_dtype, grad_dtype;
+} grpo_adamw_tensor;
+
+typedef struct grpo_adamw_config {
+  double lr, beta1, beta2, eps;
+  float grad_scale;       /* multiplies every gradient (a clip factor, 1 / loss scale) */
+  int32_t state_bits;     /* 32 or 8 */
+  int64_t step;           /* 1 for the first step */
+} grpo_adamw_config;
+
+grpo_status grpo_adamw_step(const grpo_adamw_config *config, const grpo_adamw_tensor *tensors,
+                            int32_t n_tensors, cudaStream_t stream);
+
+/*
  * Synchronises `stream`, reads and clears the error word of a workspace
  * used by grpo_loss_fwd or grpo_loss_bwd, and returns GRPO_OK,
  * GRPO_ERR_TIMEOUT or GRPO_ERR_BAD_TOKEN (timeout wins if both occurred).
