@@ -81,6 +81,19 @@ def test_flat_and_peaked_rows(spread):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("par", [dict(p=0.9), dict(p=0.5, q=1e-4), dict(k=5000), dict(k=900, p=0.97), dict(k=20000, p=0.6, T=1.5),
+                                 dict(p=0.99999), dict(p=1e-3), dict(k=1024), dict(k=1025)], ids=str)
+@pytest.mark.parametrize("V", [30011, 128256])
+def test_cuts_that_keep_many_tokens(V, par):
+    """Cuts among thousands of tokens: of one value each (float32) and of many
+    ties (bf16); spread-out rows and almost flat ones."""
+    for dtype, spread in ((torch.float32, 1.0), (torch.bfloat16, 1.0), (torch.float32, 0.05), (torch.bfloat16, 0.05),
+                          (torch.bfloat16, 4.0)):
+        z, u = logits_of(2, V, dtype, 31, spread)
+        check(z, u, **par)
+
+
+@pytest.mark.gpu
 def test_borders_of_u():
     z = torch.zeros(8, 4096, device="cuda")
     u = torch.tensor([0.0, 2.0 ** -12, 0.5, 0.5 - 2.0 ** -25, 1 - 2.0 ** -24, 1.0, 2.0, float("nan")], device="cuda")
