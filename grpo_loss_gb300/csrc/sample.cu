@@ -38,7 +38,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;                 // the portable cluster size
 constexpr int kBins = 1280;                    // 1/32 of a binary order each, down to 2^-40
-constexpr int kCap = 1024;                     // candidates that one CTA sorts
+constexpr int kCap = 2048;                     // candidates that one CTA sorts
 constexpr int kMaxSliceBytes = 184 * 1024;     // of a row's slice kept in shared memory
 constexpr float kCut = -40.f;                  // binary orders below the top that weigh nothing
 
@@ -93,50 +93,84 @@ __device__ __forceinline__ float Vec<__nv_bfloat16>::get(int e) const {
   return clean(__uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16)));
 }
 
-// What turns a logit into its weight: y = (z - zmax) log2(e) / T as a pair of
-// floats, scaled by 2^B.
+// log2(e) and ln(2) as pairs of floats
+constexpr float kLog2e = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0cp-26f;
+constexpr float kLn2 = 0x1.62e430p-1f, kLn2Lo = -0x1.05c610p-29f;
+
+// 2^(p + pl) = 2^n (h + hl) to about 2^-46, for |pl| far below |p|, -41 < p <= 0
+__device__ __forceinline__ void exp2_pair(const float2* tab, float p, float pl, int& n, float& h,
+                                          float& hl) {
+  // p = k / 32 + r, |r| <= 1/64
+  const float kf = rintf(p * 32.f);
+  const int k = static_cast<int>(kf);
+  const float r0 = __fmaf_rn(kf, -0.03125f, p);
+  const float r = __fadd_rn(r0, pl), rl = __fsub_rn(pl, __fsub_rn(r, r0));
+  // s = 2^r - 1 = x + x^2/2 + x^3/6 + ..., x = r ln 2, the first two terms in pairs
+  const float x = __fmul_rn(r, kLn2);
+  const float xl = __fmaf_rn(r, kLn2, -x) + __fmaf_rn(r, kLn2Lo, rl * kLn2);
+  const float xx = __fmul_rn(x, x);
+  const float xxl = __fmaf_rn(x, x, -xx) + 2.f * x * xl;
+  const float cubic = xx * x * __fmaf_rn(x, __fmaf_rn(x, __fmaf_rn(x, 1.f / 720.f, 1.f / 120.f), 1.f / 24.f), 1.f / 6.f);
+  const float s = __fmaf_rn(xx, 0.5f, x);
+  const float sl = __fmaf_rn(xx, 0.5f, __fsub_rn(x, s)) + (xl + 0.5f * xxl + cubic);
+  // 2^(k/32) (1 + s)
+  const float2 t = tab[k & 31];
+  const float q = __fmul_rn(t.x, s);
+  const float ql = __fmaf_rn(t.x, s, -q) + __fmaf_rn(t.x, sl, t.y * s);
+  h = __fadd_rn(t.x, q);
+  hl = __fsub_rn(q, __fsub_rn(h, t.x)) + (ql + t.y);
+  n = k >> 5;
+}
+
+// What turns a logit into its weight: y = (z - zmax) log2(e) / T, log2(e) / T
+// as a pair of floats, and the fixed point's scale.
 struct Weigher {
   float zmax, c_hi, c_lo, one;  // one = 2^B
   const float2* tab;
 };
 
 // W = round(2^(y + B)), 0 below y = -40. The argument error is 2^-46 |y|.
-__device__ __forceinline__ uint64_t weight(const Weigher& w, float z) {
+__device__ __noinline__ uint64_t weight(Weigher w, float z) {
   if (z == w.zmax) return static_cast<uint64_t>(__float2ll_rn(w.one));
   // z - zmax without loss: the difference and what its rounding left
-  const float d = z - w.zmax;
-  const float bb = d - z;
-  const float dl = (z - (d - bb)) + (-w.zmax - bb);
-  const float p = d * w.c_hi;
+  const float d = __fsub_rn(z, w.zmax);
+  const float b = __fsub_rn(d, z);
+  const float dl = __fsub_rn(z, __fsub_rn(d, b)) + __fsub_rn(-w.zmax, b);
+  const float p = __fmul_rn(d, w.c_hi);
   if (!(p >= -40.5f)) return 0;
   const float pl = __fmaf_rn(d, w.c_hi, -p) + __fmaf_rn(d, w.c_lo, dl * w.c_hi);
-  if (p + pl < -40.f || (p == -40.f && pl < 0.f)) return 0;
-  // y = k / 32 + r, |r| <= 1/64
-  const float kf = rintf(p * 32.f);
-  const int k = static_cast<int>(kf);
-  const float r0 = __fmaf_rn(kf, -0.03125f, p);
-  const float r = r0 + pl, rl = pl - (r - r0);
-  // s = 2^r - 1 = x + x^2/2 + x^3/6 + ..., x = r ln 2, the first two terms in pairs
-  const float kLn2 = 0x1.62e4300000000p-1f, kLn2Lo = -0x1.05c6100000000p-29f;
-  const float x = r * kLn2;
-  const float xl = __fmaf_rn(r, kLn2, -x) + __fmaf_rn(r, kLn2Lo, rl * kLn2);
-  const float xx = x * x;
-  const float xxl = __fmaf_rn(x, x, -xx) + 2.f * x * xl;
-  const float cubic =
-      xx * x * __fmaf_rn(x, __fmaf_rn(x, __fmaf_rn(x, 1.f / 720.f, 1.f / 120.f), 1.f / 24.f), 1.f / 6.f);
-  const float s = __fmaf_rn(xx, 0.5f, x);
-  const float sl = __fmaf_rn(xx, 0.5f, x - s) + (xl + 0.5f * xxl + cubic);
-  // 2^(k/32) (1 + s)
-  const float2 t = w.tab[k & 31];
-  const float q = t.x * s;
-  const float ql = __fmaf_rn(t.x, s, -q) + __fmaf_rn(t.x, sl, t.y * s);
-  const float h = t.x + q;
-  const float hl = (q - (h - t.x)) + (ql + t.y);
-  const float scale = w.one * __uint_as_float(static_cast<uint32_t>(127 + (k >> 5)) << 23);
+  if (p + pl < kCut || (p == kCut && pl < 0.f)) return 0;
+  int n;
+  float h, hl;
+  exp2_pair(w.tab, p, pl, n, h, hl);
+  const float scale = w.one * __uint_as_float(static_cast<uint32_t>(127 + n) << 23);
   return static_cast<uint64_t>(__float2ll_rn(h * scale) +
                                static_cast<long long>(__float2int_rn(hl * scale)));
 }
 
+// floor and ceiling of f x for 0 <= f < 1: exact
+__device__ __forceinline__ uint64_t mul_floor(float f, uint64_t x, bool& rest) {
+  const uint32_t b = __float_as_uint(f), e = b >> 23;
+  const uint64_t m = e ? (b & 0x7FFFFFu) | 0x800000u : b;
+  const int sh = 150 - static_cast<int>(e ? e : 1);  // f = m 2^-sh, sh >= 24
+  const uint64_t lo = m * x, hi = __umul64hi(m, x);
+  if (sh < 64) {
+    rest = (lo & ((1ull << sh) - 1)) != 0;
+    return (lo >> sh) | (hi << (64 - sh));
+  }
+  if (sh < 128) {
+    rest = lo != 0 || (hi & ((1ull << (sh - 64)) - 1)) != 0;
+    return hi >> (sh - 64);
+  }
+  rest = (lo | hi) != 0;
+  return 0;
+}
+__device__ __forceinline__ uint64_t mul_ceil(float f, uint64_t x) {
+  bool rest;
+  const uint64_t r = mul_floor(f, x, rest);
+  return r + rest;
+}
+__device__ __forceinline__ uint64_t distance(uint64_t a, uint64_t b) { return a > b ? a - b : b - a; }
 
 // The fast weight's y = (z - zmax) log2(e) / T (zmax finite). Its error is
 // 3 * 2^-24 |y| (three roundings), that of 2^y 2^-22: together
@@ -179,35 +213,38 @@ struct PairSum {
   }
 };
 
-// What one warp tells the cluster.
+// What the parts of a row add up to.
 struct Part {
-  uint64_t mass;
-  uint64_t mass2;
-  uint32_t count;
-  uint32_t lo, hi;
-  float err;
+  uint64_t mass = 0;
+  uint64_t mass2 = 0;
+  uint32_t count = 0;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0;
+  float err = 0.f;
 };
+enum : int { P_MASS = 1, P_MASS2 = 2, P_COUNT = 4, P_LO = 8, P_HI = 16, P_ERR = 32 };
 
 struct Shared {
   float2 tab[32];
-  Part part[2][kWarps];          // alternating between joins
-  uint32_t cnt[kBins];
-  uint32_t mass[kBins];
-  uint64_t cand[kCap];
-  uint64_t wts[kCap];
+  Part warps[kWarps];               // of this CTA
+  Part ctas[2][kMaxCluster];        // of the cluster, alternating between joins
+  uint64_t cand[kCap];              // the leader's list: key, then ~index
+  union {
+    uint64_t wts[kCap];             // its weights
+    uint2 hist[kBins];              // count and mass of a bin (read before the list is made)
+  };
   uint32_t n_cand;
-  // leader's answers to the cluster
+  // the leader's answers to the cluster
   uint32_t t, ties;
-  int again, bad;
+  int bad;
   // this CTA's scratch
   float scan_f[kWarps];
   uint32_t scan_u[kWarps];
-  int b1, b2;
+  int b;
   uint32_t upto;
+  // the row's parameters
   Weigher w;
-  float floor_z, top_p, u;
+  float floor_z, top_p, u, temp;
   int top_k, warm, use_p, use_q;
-  double temp;
 };
 
 // One row, seen from one CTA.
@@ -261,50 +298,72 @@ struct Row {
     }
   }
 
-  // Joins one Part of each warp over the cluster; every thread gets the whole.
-  __device__ __forceinline__ Part join(Part p) {
-    p.mass = warp_sum(p.mass);
-    p.mass2 = warp_sum(p.mass2);
-    p.count = __reduce_add_sync(0xffffffffu, p.count);
-    p.lo = __reduce_min_sync(0xffffffffu, p.lo);
-    p.hi = __reduce_max_sync(0xffffffffu, p.hi);
+  // The fields of F of a Part over LANES lanes, in every one of them.
+  template <int F, int LANES>
+  __device__ __forceinline__ static void lanes(Part& p) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) p.err += __shfl_xor_sync(0xffffffffu, p.err, o);
-    Part* mine = sh.part[turn];
-    if (lane == 0) mine[warp] = p;
-    cl.sync();
-    Part q = {0, 0, 0, 0xFFFFFFFFu, 0, 0.f};
-    for (int i = lane; i < C * kWarps; i += 32) {
-      const Part o = cl.map_shared_rank(mine, i / kWarps)[i % kWarps];
-      q.mass += o.mass;
-      q.mass2 += o.mass2;
-      q.count += o.count;
-      q.lo = min(q.lo, o.lo);
-      q.hi = max(q.hi, o.hi);
-      q.err += o.err;
+    for (int o = LANES / 2; o >= 1; o >>= 1) {
+      if (F & P_MASS) p.mass += __shfl_xor_sync(0xffffffffu, p.mass, o);
+      if (F & P_MASS2) p.mass2 += __shfl_xor_sync(0xffffffffu, p.mass2, o);
+      if (F & P_ERR) p.err += __shfl_xor_sync(0xffffffffu, p.err, o);
+      if (F & P_COUNT) p.count += __shfl_xor_sync(0xffffffffu, p.count, o);
+      if (F & P_LO) p.lo = min(p.lo, __shfl_xor_sync(0xffffffffu, p.lo, o));
+      if (F & P_HI) p.hi = max(p.hi, __shfl_xor_sync(0xffffffffu, p.hi, o));
     }
-    q.mass = warp_sum(q.mass);
-    q.mass2 = warp_sum(q.mass2);
-    q.count = __reduce_add_sync(0xffffffffu, q.count);
-    q.lo = __reduce_min_sync(0xffffffffu, q.lo);
-    q.hi = __reduce_max_sync(0xffffffffu, q.hi);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) q.err += __shfl_xor_sync(0xffffffffu, q.err, o);
+  }
+  template <int F>
+  __device__ __forceinline__ static void put(Part& to, const Part& p) {
+    if (F & P_MASS) to.mass = p.mass;
+    if (F & P_MASS2) to.mass2 = p.mass2;
+    if (F & P_ERR) to.err = p.err;
+    if (F & P_COUNT) to.count = p.count;
+    if (F & P_LO) to.lo = p.lo;
+    if (F & P_HI) to.hi = p.hi;
+  }
+
+  // Joins the fields F of every thread's Part over the cluster; each thread gets
+  // the whole. The CTA's own sum is pushed to the others (remote shared memory
+  // is slow to read: 128 parts read by every warp took 16,000 cycles), so that
+  // after one barrier everything is read at home. `before` gets the sum over the
+  // CTAs ahead of this one; sh.warps keeps the warps'.
+  template <int F>
+  __device__ __forceinline__ Part join(Part p, Part* before = nullptr) {
+    lanes<F, 32>(p);
+    if (lane == 0) put<F>(sh.warps[warp], p);
+    __syncthreads();
+    if (warp == 0) {
+      Part q;
+      if (lane < kWarps) put<F>(q, sh.warps[lane]);
+      lanes<F, kWarps>(q);  // (kWarps lanes hold the warps' sums; the others are not used)
+      if (lane < C) put<F>(*cl.map_shared_rank(&sh.ctas[turn][rank], lane), q);
+    }
+    cl.sync();
+    Part all;
+    for (int c = 0; c < C; ++c) {
+      if (before && c == rank) *before = all;
+      const Part& o = sh.ctas[turn][c];
+      if (F & P_MASS) all.mass += o.mass;
+      if (F & P_MASS2) all.mass2 += o.mass2;
+      if (F & P_ERR) all.err += o.err;
+      if (F & P_COUNT) all.count += o.count;
+      if (F & P_LO) all.lo = min(all.lo, o.lo);
+      if (F & P_HI) all.hi = max(all.hi, o.hi);
+    }
     turn ^= 1;
-    return q;
+    return all;
   }
 
   // Number of tokens with key above k, and their mass.
   template <bool MASS>
   __device__ Part above(const Weigher& w, uint32_t k) {
-    Part p = {0, 0, 0, 0xFFFFFFFFu, 0, 0.f};
+    Part p;
     each([&](float z) {
       if (key_of(z) > k) {
         ++p.count;
         if (MASS) p.mass += weight(w, z);
       }
     });
-    return join(p);
+    return join<MASS ? P_MASS | P_COUNT : P_COUNT>(p);
   }
 
   // Bin of a logit in steps of 1/32 of a binary order below the top.
@@ -370,16 +429,46 @@ struct Row {
   }
 };
 
-// Threshold and ties that a cut keeps, or the token itself.
+// Threshold and ties that the cut-offs keep.
 struct Kept {
   uint32_t t = 0, ties = 0xFFFFFFFFu;
 };
 
+// The first of `bins` bins of hist whose running count reaches k, kBins - 1 if
+// none does; one CTA.
+__device__ __forceinline__ int local_bin(Shared& sh, uint32_t k, int lane, int warp) {
+  uint32_t n[3], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int b = threadIdx.x * 3 + i;
+    n[i] = b < kBins ? sh.hist[b].x : 0;
+    sum += n[i];
+  }
+  uint32_t at = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += x;
+  }
+  if (lane == 31) sh.scan_u[warp] = at;
+  if (threadIdx.x == 0) sh.b = kBins - 1;
+  __syncthreads();
+  at -= sum;
+  for (int i = 0; i < warp; ++i) at += sh.scan_u[i];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (at < k && at + n[i] >= k) sh.b = threadIdx.x * 3 + i;  // one thread's at most
+    at += n[i];
+  }
+  __syncthreads();
+  return sh.b;
+}
+
 // One row with one way of weighing. Returns whether the token is decided; with
 // EXACT it always is. Every thread of the cluster returns the same.
 template <typename T, bool EXACT>
-__device__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kmax, float my_max,
-                       bool hist) {
+__device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kmax,
+                                    float my_max, bool hist) {
   constexpr int VE = Vec<T>::N;
   Shared& sh = r.sh;
   const Weigher w = sh.w;
@@ -388,7 +477,7 @@ __device__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kma
   const bool warm = sh.warm != 0, use_k = sh.top_k > 0, use_p = sh.use_p != 0;
 
   // ---- the mass of all tokens, and of those that min-p keeps
-  Part p = {0, 0, 0, 0xFFFFFFFFu, 0, 0.f};
+  Part p;
   if (EXACT) {
     r.each([&](float z) {
       const uint64_t x = weight(w, z);
@@ -424,123 +513,133 @@ __device__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kma
     // the slack of this bound's own sums
     p.err = (7.5f * all.hi + 2.2f * e) * 5.9604645e-8f;
   }
-  // the warps' masses stay where they are for a draw without cut-offs
-  const uint64_t warp_all = warp_sum(p.mass);
-  const Part S = r.join(p);
+  Part before;
+  const Part S = r.template join<P_MASS | P_MASS2 | P_ERR>(p, &before);
   // bound on the error of any sum of weights, in units of W
-  const double E = EXACT || !warm ? 0.0
-                                  : static_cast<double>(S.err) * w.one * 1.01 + static_cast<double>(r.V) + 1024.0;
+  const uint64_t E = EXACT || !warm ? 0
+                                    : static_cast<uint64_t>(__float2ll_ru(S.err * 1.01f * w.one)) +
+                                          static_cast<uint64_t>(r.V) + 1024;
+  const float mass2 = static_cast<float>(S.mass2) / w.one;
 
   Kept keep;
-  int token = -1;         // decided by the leader alone
+  uint32_t token = 0;  // decided by the leader alone
   bool leader_draws = false;
   if (!warm) {
     keep.t = kmax;
     keep.ties = 1;
   } else if (use_k || use_p) {
-    // ---- candidates: every token that can stay has a bin of at most b_cut
-    int b_cut = kBins - 1;
     bool listed = false;
+    auto in_bins = [&](float z, int lo, int hi) {
+      const float y = fast_y(w, z);
+      if (!(y >= kCut) || !(z >= floor_z)) return false;
+      const int b = min(Row<T>::bin_of(y), kBins - 1);
+      return b >= lo && b <= hi;
+    };
     if (hist) {
-      for (int i = threadIdx.x; i < kBins; i += kThreads) sh.cnt[i] = sh.mass[i] = 0;
+      for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = make_uint2(0, 0);
       if (threadIdx.x == 0) sh.n_cand = 0;
       __syncthreads();
-      const bool fits = w.zmax < INFINITY;
+      int b1 = 0, b2 = kBins - 1;
+      uint32_t upto = 0;  // tokens in bins up to b2
       if (use_k) {
-        // The k-th largest of the threads' maxima is at most the k-th largest
-        // logit: bins up to its own hold at least k tokens, and few more.
+        // Each slice holds k / C tokens down to the bin where the maxima of its
+        // threads number k / C; the lowest of these bins over the slices is down
+        // to k tokens in all, and not many more.
         const float y = fast_y(w, my_max);
-        if (fits && y >= kCut) atomicAdd(&sh.cnt[min(Row<T>::bin_of(y), kBins - 1)], 1u);
+        if (y >= kCut) atomicAdd(&sh.hist[min(Row<T>::bin_of(y), kBins - 1)].x, 1u);
+        __syncthreads();
+        Part q;
+        q.hi = local_bin(sh, (sh.top_k + r.C - 1) / r.C, lane, warp);
+        b2 = static_cast<int>(r.template join<P_HI>(q).hi);
       } else {
         // Tokens lighter than (1 - p) mass / V sum to less than (1 - p) mass.
-        const float y = log2f(fmaxf(0.5f * (1.f - sh.top_p) * (static_cast<float>(S.mass2) / w.one) /
-                                        static_cast<float>(r.V), 1e-30f));
-        b_cut = y > kCut ? max(0, Row<T>::bin_of(fminf(y, 0.f))) : kBins - 1;
-        b_cut = min(b_cut + 1, kBins - 1);
+        const float y = log2f(fmaxf(0.5f * (1.f - sh.top_p) * mass2 / static_cast<float>(r.V), 1e-30f));
+        const int b_cut = y > kCut ? min(Row<T>::bin_of(fminf(y, 0.f)) + 1, kBins - 1) : kBins - 1;
         r.each([&](float z) {
           const float yy = fast_y(w, z);
           if (yy >= kCut && z >= floor_z) {
             const int b = min(Row<T>::bin_of(yy), kBins - 1);
             if (b <= b_cut) {
-              atomicAdd(&sh.cnt[b], 1u);
+              atomicAdd(&sh.hist[b].x, 1u);
               // the weight over the bin's own: 15 bits
-              atomicAdd(&sh.mass[b], __float2uint_rn(32768.f * ex2_approx(yy + 0.03125f * b)));
+              atomicAdd(&sh.hist[b].y, __float2uint_rn(32768.f * ex2_approx(yy + 0.03125f * b)));
             }
           }
         });
-      }
-      r.cl.sync();
-      // running sums over the bins of all slices; each thread takes three bins
-      uint32_t n[3];
-      float m[3], n_m = 0.f;
-      uint32_t n_c = 0;
+        r.cl.sync();
+        // Running sums: this CTA adds up its share of the bins over the slices,
+        // three bins or fewer a thread.
+        const int share = (b_cut + r.C) / r.C, per = (share + kThreads - 1) / kThreads;
+        const int first = r.rank * share;
+        uint32_t n[3], n_c = 0;
+        float m[3], n_m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const int b = threadIdx.x * 3 + i;
-        n[i] = 0;
-        uint64_t mm = 0;
-        if (b <= b_cut)
-          for (int c = 0; c < r.C; ++c) {
-            n[i] += r.cl.map_shared_rank(sh.cnt, c)[b];
-            if (!use_k) mm += r.cl.map_shared_rank(sh.mass, c)[b];
-          }
-        m[i] = static_cast<float>(mm) * ex2_approx(-15.f - 0.03125f * b);
-        n_c += n[i];
-        n_m += m[i];
-      }
-      uint32_t n_in = n_c;
-      float m_in = n_m;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xffffffffu, n_in, o);
-        const float y = __shfl_up_sync(0xffffffffu, m_in, o);
-        if (lane >= o) {
-          n_in += x;
-          m_in += y;
+        for (int i = 0; i < 3; ++i) {
+          const int j = static_cast<int>(threadIdx.x) * per + i, b = first + j;
+          n[i] = 0;
+          uint64_t mm = 0;
+          if (i < per && j < share && b <= b_cut)
+            for (int c = 0; c < r.C; ++c) {
+              const uint2 h = r.cl.map_shared_rank(sh.hist, c)[b];
+              n[i] += h.x;
+              mm += h.y;
+            }
+          m[i] = static_cast<float>(mm) * ex2_approx(-15.f - 0.03125f * b);
+          n_c += n[i];
+          n_m += m[i];
         }
-      }
-      if (lane == 31) {
-        sh.scan_u[warp] = n_in;
-        sh.scan_f[warp] = m_in;
-      }
-      if (threadIdx.x == 0) {
-        sh.b1 = sh.b2 = kBins - 1;
-        sh.upto = 0xFFFFFFFFu;
-      }
-      __syncthreads();
-      uint32_t n_at = n_in - n_c;
-      float m_at = m_in - n_m;
-      for (int i = 0; i < warp; ++i) {
-        n_at += sh.scan_u[i];
-        m_at += sh.scan_f[i];
-      }
-      // the masses here are 2^-16 off for their 15 bits, and 2^-20 for the rest
-      const float need = sh.top_p * (static_cast<float>(S.mass2) / w.one);
+        uint32_t n_in = n_c;
+        float m_in = n_m;
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const int b = threadIdx.x * 3 + i;
-        n_at += n[i];
-        m_at += m[i];
-        if (b >= kBins) continue;
-        if (use_k) {
-          if (n_at >= static_cast<uint32_t>(sh.top_k)) atomicMin(&sh.b2, b);
-        } else {
-          if (m_at * (1.f + 6e-5f) >= need) atomicMin(&sh.b1, b);
-          if (m_at * (1.f - 6e-5f) > need) {  // (running counts ascend with b)
-            atomicMin(&sh.b2, b);
-            atomicMin(&sh.upto, n_at);
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t x = __shfl_up_sync(0xffffffffu, n_in, o);
+          const float z = __shfl_up_sync(0xffffffffu, m_in, o);
+          if (lane >= o) {
+            n_in += x;
+            m_in += z;
           }
         }
+        if (lane == 31) {
+          sh.scan_u[warp] = n_in;
+          sh.scan_f[warp] = m_in;
+        }
+        Part q, ahead;
+        q.count = n_c;
+        q.err = n_m;
+        r.template join<P_COUNT | P_ERR>(q, &ahead);
+        uint32_t n_at = ahead.count + n_in - n_c;
+        float m_at = ahead.err + m_in - n_m;
+        for (int i = 0; i < warp; ++i) {
+          n_at += sh.scan_u[i];
+          m_at += sh.scan_f[i];
+        }
+        // the masses here are 2^-16 off for their 15 bits, and 2^-20 for the rest
+        const float need = sh.top_p * mass2;
+        // the first bins that may, and that must, reach the mass
+        uint32_t must = kBins - 1, must_n = 0xFFFFFFFFu;
+        q.lo = kBins - 1;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int j = static_cast<int>(threadIdx.x) * per + i;
+          n_at += n[i];
+          m_at += m[i];
+          if (i >= per || j >= share || first + j > b_cut) continue;
+          if (m_at * (1.f + 6e-5f) >= need) q.lo = min(q.lo, static_cast<uint32_t>(first + j));
+          if (m_at * (1.f - 6e-5f) > need && static_cast<uint32_t>(first + j) < must) {
+            must = first + j;
+            must_n = n_at;
+          }
+        }
+        // the smallest bin that must, and the count up to it, through one maximum
+        q.hi = kBins - 1 - must;
+        const Part f = r.template join<P_LO | P_HI>(q);
+        b1 = static_cast<int>(f.lo);
+        b2 = static_cast<int>(kBins - 1 - f.hi);
+        Part g;
+        g.lo = must == static_cast<uint32_t>(b2) ? must_n : 0xFFFFFFFFu;
+        upto = r.template join<P_LO>(g).lo;
       }
-      __syncthreads();
-      const int b1 = sh.b1, b2 = sh.b2;
-      auto in_bins = [&](float z, int lo, int hi) {
-        const float y = fast_y(w, z);
-        if (!(y >= kCut) || !(z >= floor_z)) return false;
-        const int b = min(Row<T>::bin_of(y), kBins - 1);
-        return b >= lo && b <= hi;
-      };
-      if (fits && (use_k || sh.upto <= kCap)) {
+      if (use_k || upto <= kCap) {
         // ---- few candidates: the leader finishes the row with exact weights
         const uint32_t n_all = r.gather([&](float z) { return in_bins(z, 0, b2); });
         if (n_all <= kCap) {
@@ -553,28 +652,28 @@ __device__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kma
             __syncthreads();
             if (warp == 0) {
               if (use_k) n_l = min(n_l, static_cast<uint32_t>(sh.top_k));
-              uint64_t total = 0;
-              for (uint32_t i = lane; i < n_l; i += 32) total += sh.wts[i];
-              total = warp_sum(total);
               bool bad = false;
               if (use_p) {
                 // with top-k the mass is this list's; else everything's, within E
-                const double base = static_cast<double>(use_k ? total : S.mass2);
-                const double want = static_cast<double>(sh.top_p) * base;
-                const double slack = use_k ? 0.0 : 2.0 * E;
+                uint64_t base = S.mass2;
+                if (use_k) {
+                  base = 0;
+                  for (uint32_t i = lane; i < n_l; i += 32) base += sh.wts[i];
+                  base = warp_sum(base);
+                }
+                const uint64_t want = mul_ceil(sh.top_p, base);
+                const uint64_t slack = use_k ? 0 : 2 * E;
                 uint64_t run = 0;
                 uint32_t stay = 0;
                 for (uint32_t i0 = 0; i0 < n_l; i0 += 32) {
                   const uint32_t i = i0 + lane;
                   const uint64_t x = i < n_l ? sh.wts[i] : 0;
-                  const uint64_t before = run + warp_scan(x, lane) - x;
-                  const double off = static_cast<double>(before) - want;
-                  stay += __popc(__ballot_sync(0xffffffffu, i < n_l && off < 0.0));
-                  bad |= __any_sync(0xffffffffu, slack > 0.0 && i < n_l && i > 0 && fabs(off) <= slack);
+                  const uint64_t ahead = run + warp_scan(x, lane) - x;
+                  stay += __popc(__ballot_sync(0xffffffffu, i < n_l && ahead < want));
+                  bad |= __any_sync(0xffffffffu, slack && i < n_l && i > 0 && distance(ahead, want) <= slack);
                   run += warp_sum(x);
                 }
-                // the last one's far side, where the cut may fall behind the list
-                bad |= slack > 0.0 && static_cast<double>(run) - want <= slack;
+                bad |= slack && run <= want + slack;  // the cut may fall behind the list
                 n_l = max(1u, stay);
               }
               if (lane == 0) {
@@ -592,18 +691,16 @@ __device__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kma
             if (warp == 0) {
               uint64_t total = 0;
               for (uint32_t i = lane; i < n_l; i += 32) total += sh.wts[i];
-              total = warp_sum(total);
-              const double target = static_cast<double>(sh.u) * static_cast<double>(total);
+              bool rest;
+              const uint64_t target = mul_floor(sh.u, warp_sum(total), rest);
               uint64_t run = 0;
               for (uint32_t i0 = 0; i0 < n_l; i0 += 32) {
                 const uint32_t i = i0 + lane;
                 const uint64_t c = i < n_l ? sh.cand[i] : 0;
                 const uint64_t x = i < n_l ? sh.wts[static_cast<uint32_t>(c)] : 0;
-                const uint64_t upto = run + warp_scan(x, lane);
-                const uint32_t hit = __ballot_sync(0xffffffffu, static_cast<double>(upto) > target);
+                const uint32_t hit = __ballot_sync(0xffffffffu, run + warp_scan(x, lane) > target);
                 if (hit) {
-                  token = static_cast<int>(~static_cast<uint32_t>(
-                      __shfl_sync(0xffffffffu, c, __ffs(hit) - 1) >> 32));
+                  token = ~static_cast<uint32_t>(__shfl_sync(0xffffffffu, c, __ffs(hit) - 1) >> 32);
                   break;
                 }
                 run += warp_sum(x);
@@ -611,10 +708,10 @@ __device__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kma
             }
           }
         }
-      } else if (fits && !use_k) {
+      } else {
         // ---- many tokens stay: the cut falls in bins b1 to b2, whose tokens are
         // of one value (they tie) or few enough to be sorted
-        Part q = {0, 0, 0, 0xFFFFFFFFu, 0, 0.f};
+        Part q;
         r.each([&](float z) {
           const float y = fast_y(w, z);
           if (!(y >= kCut) || !(z >= floor_z)) return;
@@ -628,17 +725,17 @@ __device__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kma
             q.hi = max(q.hi, key);
           }
         });
-        q = r.join(q);
-        const double want = static_cast<double>(sh.top_p) * static_cast<double>(S.mass2);
-        const double rest = want - static_cast<double>(q.mass);
+        q = r.template join<P_MASS | P_COUNT | P_LO | P_HI>(q);
+        const uint64_t want = mul_ceil(sh.top_p, S.mass2);
+        const uint64_t rest = want > q.mass ? want - q.mass : 0;
         if (q.count > 0 && q.lo == q.hi) {
-          const double each = static_cast<double>(weight(w, float_of(q.lo)));
-          const double m = rest / each, up = ceil(m);
+          const uint64_t each = max(static_cast<uint64_t>(1), weight(w, float_of(q.lo)));
+          const uint64_t ties = (rest + each - 1) / each, over = ties * each - rest;
           // the cut is the interval's own only if it falls inside it
-          if (rest > 0.0 && up <= static_cast<double>(q.count)) {
-            if (!EXACT && ((up - m) * each <= 2.0 * E || (m - (up - 1.0)) * each <= 2.0 * E)) return false;
+          if (rest > 0 && ties <= q.count) {
+            if (!EXACT && (over <= 2 * E || each - over <= 2 * E)) return false;
             keep.t = q.lo;
-            keep.ties = static_cast<uint32_t>(up);
+            keep.ties = static_cast<uint32_t>(ties);
             listed = true;
           }
         } else if (q.count > 0 && q.count <= kCap) {
@@ -651,17 +748,16 @@ __device__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kma
             if (warp == 0) {
               uint64_t run = 0;
               uint32_t stay = 0;
-              bool bad = false;
+              bool bad = rest == 0;
               for (uint32_t i0 = 0; i0 < q.count; i0 += 32) {
                 const uint32_t i = i0 + lane;
                 const uint64_t x = i < q.count ? sh.wts[i] : 0;
-                const double off = static_cast<double>(run + warp_scan(x, lane) - x) - rest;
-                stay += __popc(__ballot_sync(0xffffffffu, i < q.count && off < 0.0));
-                bad |= !EXACT && __any_sync(0xffffffffu, i < q.count && fabs(off) <= 2.0 * E);
+                const uint64_t ahead = run + warp_scan(x, lane) - x;
+                stay += __popc(__ballot_sync(0xffffffffu, i < q.count && ahead < rest));
+                bad |= !EXACT && __any_sync(0xffffffffu, i < q.count && distance(ahead, rest) <= 2 * E);
                 run += warp_sum(x);
               }
-              bad |= !EXACT && fabs(static_cast<double>(run) - rest) <= 2.0 * E;
-              bad |= stay == 0 || (stay == q.count && static_cast<double>(run) < rest);
+              bad |= run < rest || (!EXACT && run - rest <= 2 * E);
               const uint32_t t = stay ? static_cast<uint32_t>(sh.cand[stay - 1] >> 32) : 0;
               uint32_t ties = 0;
               for (uint32_t i = lane; i < stay; i += 32)
@@ -706,20 +802,19 @@ __device__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kma
         // t = 0 has no ties: no logit has key 0
         const uint32_t from = t == 0 ? over.count : r.template above<false>(w, t - 1).count;
         const uint64_t at = min(keep.ties, from - over.count);
-        const uint64_t kept = over.mass + (t == 0 ? 0 : at * weight(w, float_of(t)));
-        const double need = static_cast<double>(sh.top_p) * static_cast<double>(kept);
+        const uint64_t need =
+            mul_ceil(sh.top_p, over.mass + (t == 0 ? 0 : at * weight(w, float_of(t))));
         uint32_t lo = t, hi = kmax;  // smallest key with less than `need` above it
         while (lo < hi) {
           const uint32_t mid = lo + (hi - lo) / 2;
-          if (static_cast<double>(r.template above<true>(w, mid).mass) < need) hi = mid;
+          if (r.template above<true>(w, mid).mass < need) hi = mid;
           else lo = mid + 1;
         }
-        const double rest = need - static_cast<double>(r.template above<true>(w, lo).mass);
-        const double each = static_cast<double>(weight(w, float_of(lo)));
-        uint32_t more = 0xFFFFFFFFu;  // ties before which there is less than `need`
-        if (rest <= 0.0) more = 1;    // p <= 0: the first token alone
-        else if (each > 0.0 && rest / each < 4294967295.0)
-          more = static_cast<uint32_t>(ceil(rest / each));
+        const uint64_t ahead = r.template above<true>(w, lo).mass;
+        const uint64_t each = weight(w, float_of(lo));
+        uint32_t more = 0xFFFFFFFFu;        // ties before which there is less than `need`
+        if (ahead >= need) more = 1;        // p <= 0: the first token alone
+        else if (each > 0) more = static_cast<uint32_t>(min((need - ahead + each - 1) / each, static_cast<uint64_t>(0xFFFFFFFFu)));
         keep.ties = lo > t ? more : min(keep.ties, more);
         keep.t = lo;
       }
@@ -729,63 +824,48 @@ __device__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kma
   }
 
   if (leader_draws) {
-    if (threadIdx.x == 0 && r.rank == 0 && !sh.bad) sh.t = static_cast<uint32_t>(token);
+    if (threadIdx.x == 0 && r.rank == 0 && !sh.bad) sh.t = token;
   } else {
-    // ---- the draw: the warps' masses and ties, then the one warp that holds u
-    uint64_t my_mass = warp_all;
-    uint32_t my_eq = 0;
+    // ---- the draw: the mass and ties ahead of each warp, then the one that holds u
+    Part all = S;
     if (keep.t != 0) {
-      uint64_t m = 0;
+      Part q;
       PairSum f;
-      uint32_t eq = 0;
       r.each([&](float z) {
         const uint32_t key = key_of(z);
         if (key > keep.t) {
-          if (EXACT) m += weight(w, z);
+          if (EXACT) q.mass += weight(w, z);
           else f.add(fast_weight(fast_y(w, z)));
         }
-        eq += key == keep.t;
+        q.count += key == keep.t;
       });
-      my_mass = warp_sum(EXACT ? m : f.fixed(w.one));
-      my_eq = __reduce_add_sync(0xffffffffu, eq);
+      if (!EXACT) q.mass = f.fixed(w.one);
+      all = r.template join<P_MASS | P_COUNT>(q, &before);
+    } else {
+      all.count = before.count = 0;
+      if (lane == 0) sh.warps[warp].count = 0;
     }
-    Part* mine = sh.part[r.turn];
-    if (lane == 0) {
-      mine[warp].mass = my_mass;
-      mine[warp].count = my_eq;
-    }
+    Shared* lead = r.cl.map_shared_rank(&sh, 0);
     if (threadIdx.x == 0) sh.bad = 0;
     r.cl.sync();
-    r.turn ^= 1;
-    // before this warp, and in all: ranks and warps are in index order
-    uint64_t m_before = 0, m_all = 0, e_before = 0, e_all = 0;
-    for (int i = lane; i < r.C * kWarps; i += 32) {
-      const Part& o = r.cl.map_shared_rank(mine, i / kWarps)[i % kWarps];
-      const uint64_t m = o.mass, e = o.count;
-      m_all += m;
-      e_all += e;
-      if (i < r.rank * kWarps + warp) {
-        m_before += m;
-        e_before += e;
-      }
+    // ranks and warps are in index order
+    uint64_t m = before.mass;
+    uint32_t e = before.count;
+    for (int i = 0; i < warp; ++i) {
+      m += sh.warps[i].mass;
+      e += sh.warps[i].count;
     }
-    m_all = warp_sum(m_all);
-    e_all = warp_sum(e_all);
-    m_before = warp_sum(m_before);
-    e_before = warp_sum(e_before);
-    const uint64_t lim = keep.ties;
+    const Part mine = sh.warps[warp];
+    const uint32_t lim = keep.ties;
     const uint64_t wt = keep.t == 0 ? 0 : weigh<EXACT>(w, float_of(keep.t));
-    const uint64_t total = m_all + min(e_all, lim) * wt;
-    const double target = static_cast<double>(sh.u) * static_cast<double>(total);
-    const uint64_t before = m_before + min(e_before, lim) * wt;
-    const uint64_t after = m_before + my_mass + min(e_before + my_eq, lim) * wt;
-    Shared* lead = r.cl.map_shared_rank(&sh, 0);
-    if (static_cast<double>(before) <= target && static_cast<double>(after) > target) {
-      uint64_t m = m_before, e = e_before;
+    bool rest;
+    const uint64_t target = mul_floor(sh.u, all.mass + min(all.count, lim) * wt, rest);
+    if (m + min(e, lim) * wt <= target && m + mine.mass + min(e + mine.count, lim) * wt > target) {
       bool done = false;
       for (int vb = r.v0; vb < r.v1 && !done; vb += 32) {
         const int v = vb + lane;
-        uint64_t s = 0, eq = 0;
+        uint64_t s = 0;
+        uint32_t eq = 0;
         Vec<T> x;
         if (v < r.v1) {
           x = r.load(v);
@@ -797,23 +877,30 @@ __device__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kma
             eq += key == keep.t;
           }
         }
-        const uint64_t s_in = m + warp_scan(s, lane), e_in = e + warp_scan(eq, lane);
-        const uint32_t hit = __ballot_sync(
-            0xffffffffu, static_cast<double>(s_in + min(e_in, lim) * wt) > target);
+        const uint64_t s_in = m + warp_scan(s, lane);
+        uint32_t e_in = eq;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, e_in, o);
+          if (lane >= o) e_in += y;
+        }
+        e_in += e;
+        const uint32_t hit = __ballot_sync(0xffffffffu, s_in + min(e_in, lim) * wt > target);
         if (hit) {
           done = true;
           if (lane == __ffs(hit) - 1) {
-            uint64_t sm = s_in - s, se = e_in - eq;
+            uint64_t sm = s_in - s;
+            uint32_t se = e_in - eq;
             for (int i = 0; i < VE; ++i) {
               const float z = x.get(i);
               const uint32_t key = key_of(z);
-              const double was = static_cast<double>(sm + min(se, lim) * wt);
+              const uint64_t was = sm + min(se, lim) * wt;
               if (key > keep.t) sm += weigh<EXACT>(w, z);
               se += key == keep.t;
-              const double now = static_cast<double>(sm + min(se, lim) * wt);
+              const uint64_t now = sm + min(se, lim) * wt;
               if (now > target) {
                 // a border within E of u: left to the exact weights
-                if (!EXACT && (now - target <= 2.0 * E || target - was <= 2.0 * E)) lead->bad = 1;
+                if (E && (now - target <= 2 * E || distance(target, was) <= 2 * E)) lead->bad = 1;
                 lead->t = static_cast<uint32_t>(r.pos0 + static_cast<int64_t>(v) * VE + i);
                 break;
               }
@@ -829,17 +916,47 @@ __device__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kma
   r.cl.sync();
   if (!EXACT && r.cl.map_shared_rank(&sh, 0)->bad) return false;
   if (r.rank == 0 && threadIdx.x == 0) {
-    const int at = static_cast<int>(sh.t);
-    const float z = clean(to_f(static_cast<const T*>(a.logits)[row * a.ld + at]));
-    const double d = z == w.zmax ? 0.0 : (static_cast<double>(z) - w.zmax) / sh.temp;
-    a.tokens[row] = at;
-    a.logp[row] = static_cast<float>(d - log(static_cast<double>(S.mass) / w.one));
+    const int64_t at = sh.t;
+    const float z = clean(to_f(r.row[at]));
+    const float d = z == w.zmax ? 0.f : (z - w.zmax) / sh.temp;
+    // ln(mass): the sum as two floats
+    const float hi = static_cast<float>(S.mass);
+    const float lo = static_cast<float>(static_cast<int64_t>(S.mass - static_cast<uint64_t>(hi)));
+    a.tokens[row] = static_cast<int32_t>(at);
+    a.logp[row] = d - (logf(hi / w.one) + lo / hi);
   }
   return true;
 }
 
+// The smallest float z with exp((z - zmax) / T) >= q, for 2^-40 <= q < 1.
+__device__ __noinline__ float min_logit(Weigher w, float temp, float q) {
+  // log2(q) = y + yl: what 2^y misses of q, relative to q, times log2(e)
+  const float y = fminf(log2f(q), 0.f);
+  int n;
+  float h, hl;
+  exp2_pair(w.tab, y, 0.f, n, h, hl);
+  const float qs = q * __uint_as_float(static_cast<uint32_t>(127 - n) << 23);
+  const float yl = __fsub_rn(__fsub_rn(qs, h), hl) / h * kLog2e;
+  // zmax + (y + yl) T ln 2, rounded up
+  const float t = __fmul_rn(temp, kLn2), tl = __fmaf_rn(temp, kLn2, -t) + temp * kLn2Lo;
+  const float p = __fmul_rn(y, t), pl = __fmaf_rn(y, t, -p) + __fmaf_rn(y, tl, yl * t);
+  const float s = __fadd_rn(w.zmax, p), b = __fsub_rn(s, w.zmax);
+  const float sl = __fadd_rn(__fadd_rn(__fsub_rn(w.zmax, __fsub_rn(s, b)), __fsub_rn(p, b)), pl);
+  if (!(fabsf(s) < INFINITY) || !(fabsf(sl) < INFINITY)) return s;
+  const float f = __fadd_rn(s, sl);
+  return __fsub_rn(sl, __fsub_rn(f, s)) > 0.f ? nextafterf(f, INFINITY) : f;
+}
+
+// The rare way, apart from the common one's registers.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int slice_vecs, int resident) {
+__device__ __noinline__ int decide_exact(Row<T> r, const SampleArgs& a, int64_t row, uint32_t kmax,
+                                         float my_max, bool hist) {
+  decide<T, true>(r, a, row, kmax, my_max, hist);
+  return r.turn;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ SampleArgs a, int slice_vecs, int resident) {
   extern __shared__ uint4 s_slice[];
   __shared__ Shared sh;
   constexpr int VE = Vec<T>::N;
@@ -875,9 +992,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
       for (int e = 0; e < VE; ++e) mx = fmaxf(mx, x.get(e));
     }
     __syncwarp();
-    Part p = {0, 0, 0, 0xFFFFFFFFu, key_of(mx), 0.f};
-    p = r.join(p);
-    const uint32_t kmax = p.hi;
+    Part p;
+    p.hi = key_of(mx);
+    const uint32_t kmax = r.template join<P_HI>(p).hi;
     const float zmax = float_of(kmax);
     if (zmax == -INFINITY) {  // nothing to choose from
       if (r.rank == 0 && threadIdx.x == 0) {
@@ -889,13 +1006,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
     if (threadIdx.x == 0) {
       const float T_in = a.temperature ? a.temperature[row] : 1.f;
       sh.warm = T_in > 0.f;
-      const double temp = sh.warm ? static_cast<double>(T_in) : 1.0;
+      const float temp = sh.warm ? T_in : 1.f;
       sh.temp = temp;
-      const double c = 1.4426950408889634074 / temp;
       sh.w.zmax = zmax;
-      // within float range: a T of 0 or infinity up to rounding
-      sh.w.c_hi = fminf(fmaxf(static_cast<float>(c), 1.4e-45f), 3.4e38f);
-      sh.w.c_lo = c < 3.4e38 && c > 1e-30 ? static_cast<float>(c - static_cast<double>(sh.w.c_hi)) : 0.f;
+      // log2(e) / T, kept within float's range (a T near 0, an infinite one)
+      const float c = fminf(fmaxf(kLog2e / temp, 1.4e-45f), 3.4e38f);
+      sh.w.c_hi = c;
+      sh.w.c_lo = c > 1e-30f && c < 1e30f ? (__fmaf_rn(-c, temp, kLog2e) + kLog2eLo) / temp : 0.f;
       // V 2^B < 2^62
       const int bits = min(44, 62 - (32 - __clz(static_cast<int>(a.V))));
       sh.w.one = __uint_as_float(static_cast<uint32_t>(127 + bits) << 23);
@@ -903,11 +1020,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
       const int k = a.top_k ? a.top_k[row] : 0;
       sh.top_k = k > 0 && k < a.V ? k : 0;
       const float q = a.min_p ? a.min_p[row] : 0.f;
-      sh.use_q = q > 0.f && sh.warm;
-      // the smallest float z with exp((z - zmax) / T) >= q
-      sh.floor_z = !sh.use_q ? -INFINITY
-                   : q >= 1.f ? zmax
-                              : fminf(zmax, __double2float_ru(zmax + temp * log(static_cast<double>(q))));
+      // weights below 2^-40 are 0: a lower q keeps every token that counts
+      sh.use_q = q >= 9.094947e-13f && sh.warm;
+      sh.floor_z = !sh.use_q ? -INFINITY : q >= 1.f ? zmax : min_logit(sh.w, temp, q);
       sh.top_p = a.top_p ? a.top_p[row] : 1.f;
       sh.use_p = sh.top_p < 1.f;
       sh.top_p = fmaxf(sh.top_p, 0.f);
@@ -917,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
     if (!resident || zmax == INFINITY || !decide<T, false>(r, a, row, kmax, mx, true)) {
       // (the cluster's CTAs leave a row that was not decided at the same point)
       r.cl.sync();
-      decide<T, true>(r, a, row, kmax, mx, resident && zmax < INFINITY);
+      r.turn = decide_exact<T>(r, a, row, kmax, mx, resident && zmax < INFINITY);
     }
     r.cl.sync();
   }
