@@ -34,11 +34,11 @@ namespace grpo {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxThreads = 512;               // a CTA has 512 threads or 256
+constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 8;                 // the portable cluster size
-constexpr int kBins = 1280;                    // 1/32 of a binary order each, down to 2^-40
-constexpr int kCap = 2048;                     // candidates that one CTA sorts
+constexpr int kBins = 1280;                    // (five a thread at most) 1/32 of a binary order each, down to 2^-40
+constexpr int kCap = 1024;                     // candidates that one CTA sorts
 constexpr int kMaxSliceBytes = 184 * 1024;     // of a row's slice kept in shared memory
 constexpr float kCut = -40.f;                  // binary orders below the top that weigh nothing
 
@@ -82,6 +82,7 @@ struct Vec {
   static constexpr int N = 16 / sizeof(T);
   uint4 raw;
   __device__ __forceinline__ float get(int e) const;
+  __device__ __forceinline__ float max() const;  // NaN counts as -inf
 };
 template <>
 __device__ __forceinline__ float Vec<float>::get(int e) const {
@@ -91,6 +92,18 @@ template <>
 __device__ __forceinline__ float Vec<__nv_bfloat16>::get(int e) const {
   const uint32_t w = e < 2 ? raw.x : e < 4 ? raw.y : e < 6 ? raw.z : raw.w;
   return clean(__uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16)));
+}
+
+template <>
+__device__ __forceinline__ float Vec<float>::max() const {
+  return fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3)));
+}
+template <>
+__device__ __forceinline__ float Vec<__nv_bfloat16>::max() const {
+  auto h = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); };
+  // of a number and a NaN this maximum is the number
+  const __nv_bfloat162 m = __hmax2(__hmax2(h(raw.x), h(raw.y)), __hmax2(h(raw.z), h(raw.w)));
+  return fmaxf(clean(__low2float(m)), __high2float(m));
 }
 
 // log2(e) and ln(2) as pairs of floats
@@ -130,7 +143,7 @@ struct Weigher {
 };
 
 // W = round(2^(y + B)), 0 below y = -40. The argument error is 2^-46 |y|.
-__device__ __noinline__ uint64_t weight(Weigher w, float z) {
+__device__ __forceinline__ uint64_t weight_inline(const Weigher& w, float z) {
   if (z == w.zmax) return static_cast<uint64_t>(__float2ll_rn(w.one));
   // z - zmax without loss: the difference and what its rounding left
   const float d = __fsub_rn(z, w.zmax);
@@ -147,6 +160,8 @@ __device__ __noinline__ uint64_t weight(Weigher w, float z) {
   return static_cast<uint64_t>(__float2ll_rn(h * scale) +
                                static_cast<long long>(__float2int_rn(hl * scale)));
 }
+
+__device__ __noinline__ uint64_t weight(Weigher w, float z) { return weight_inline(w, z); }
 
 // floor and ceiling of f x for 0 <= f < 1: exact
 __device__ __forceinline__ uint64_t mul_floor(float f, uint64_t x, bool& rest) {
@@ -174,9 +189,10 @@ __device__ __forceinline__ uint64_t distance(uint64_t a, uint64_t b) { return a 
 
 // The fast weight's y = (z - zmax) log2(e) / T (zmax finite). Its error is
 // 3 * 2^-24 |y| (three roundings), that of 2^y 2^-22: together
-// w (4 + 2.1 |y|) 2^-24.
+// w (4 + 2.1 |y|) 2^-24. It has no cut at 2^-40; what it has below is V 2^-40 at
+// most.
 __device__ __forceinline__ float fast_y(const Weigher& w, float z) { return (z - w.zmax) * w.c_hi; }
-__device__ __forceinline__ float fast_weight(float y) { return y < kCut ? 0.f : ex2_approx(y); }
+__device__ __forceinline__ float fast_weight(float y) { return ex2_approx(fmaxf(y, -200.f)); }
 
 // Element weight as an integer.
 template <bool EXACT>
@@ -225,7 +241,7 @@ enum : int { P_MASS = 1, P_MASS2 = 2, P_COUNT = 4, P_LO = 8, P_HI = 16, P_ERR = 
 
 struct Shared {
   float2 tab[32];
-  Part warps[kWarps];               // of this CTA
+  Part warps[kMaxWarps];            // of this CTA
   Part ctas[2][kMaxCluster];        // of the cluster, alternating between joins
   uint64_t cand[kCap];              // the leader's list: key, then ~index
   union {
@@ -233,12 +249,14 @@ struct Shared {
     uint2 hist[kBins];              // count and mass of a bin (read before the list is made)
   };
   uint32_t n_cand;
-  // the leader's answers to the cluster
-  uint32_t t, ties;
-  int bad;
+  // the leader's answers to the cluster, alternating between rows
+  struct {
+    uint32_t t, ties;
+    int bad;
+  } ans[2];
   // this CTA's scratch
-  float scan_f[kWarps];
-  uint32_t scan_u[kWarps];
+  float scan_f[kMaxWarps];
+  uint32_t scan_u[kMaxWarps];
   int b;
   uint32_t upto;
   // the row's parameters
@@ -259,7 +277,7 @@ struct Row {
   int n_vec;           // 16-byte pieces of the slice
   int64_t pos0;        // row index of the slice's first element (may be below 0)
   int64_t V;
-  int lane, warp, C, rank, turn = 0;
+  int lane, warp, nt, nw, C, rank, turn = 0, par = 0;  // nt threads, nw warps
   int v0, v1;          // this warp's pieces
 
   __device__ __forceinline__ Row(Shared& s) : sh(s) {}
@@ -333,8 +351,8 @@ struct Row {
     __syncthreads();
     if (warp == 0) {
       Part q;
-      if (lane < kWarps) put<F>(q, sh.warps[lane]);
-      lanes<F, kWarps>(q);  // (kWarps lanes hold the warps' sums; the others are not used)
+      if (lane < nw) put<F>(q, sh.warps[lane]);
+      lanes<F, kMaxWarps>(q);
       if (lane < C) put<F>(*cl.map_shared_rank(&sh.ctas[turn][rank], lane), q);
     }
     cl.sync();
@@ -353,6 +371,17 @@ struct Row {
     return all;
   }
 
+  // f(z) for the pieces whose largest element passes `some`.
+  template <typename P, typename F>
+  __device__ __forceinline__ void each_if(P some, F f) const {
+    for (int v = v0 + lane; v < v1; v += 32) {
+      const Vec<T> x = load(v);
+      if (!some(x.max())) continue;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) f(x.get(e));
+    }
+  }
+
   // Number of tokens with key above k, and their mass.
   template <bool MASS>
   __device__ Part above(const Weigher& w, uint32_t k) {
@@ -369,10 +398,11 @@ struct Row {
   // Bin of a logit in steps of 1/32 of a binary order below the top.
   __device__ __forceinline__ static int bin_of(float y) { return static_cast<int>(-32.f * y); }
 
-  // Copies the elements f accepts to the leader's list; returns their number
+  // Copies the elements that both functions accept to the leader's list (the
+  // first accepts from some logit on, so that a piece's maximum can be asked); returns their number
   // over the cluster (the list is cut at kCap).
-  template <typename F>
-  __device__ uint32_t gather(F accept) {
+  template <typename F, typename G>
+  __device__ uint32_t gather(F accept, G also) {
     uint32_t* n = cl.map_shared_rank(&sh.n_cand, 0);
     uint64_t* to = cl.map_shared_rank(sh.cand, 0);
     for (int vb = v0; vb < v1; vb += 32) {
@@ -381,8 +411,10 @@ struct Row {
       uint32_t want = 0;
       if (v < v1) {
         x = load(v);
+        if (accept(x.max())) {  // (what it accepts it accepts above, too)
 #pragma unroll
-        for (int e = 0; e < VE; ++e) want |= accept(x.get(e)) ? (1u << e) : 0u;
+          for (int e = 0; e < VE; ++e) want |= accept(x.get(e)) && also(x.get(e)) ? (1u << e) : 0u;
+        }
       }
       if (!__any_sync(0xffffffffu, want != 0)) continue;
       const uint32_t mine = __popc(want);
@@ -412,11 +444,11 @@ struct Row {
   __device__ void sort_desc(uint64_t* a, uint32_t n) {
     uint32_t n2 = 2;
     while (n2 < n) n2 <<= 1;
-    for (uint32_t i = n + threadIdx.x; i < n2; i += kThreads) a[i] = 0;
+    for (uint32_t i = n + threadIdx.x; i < n2; i += nt) a[i] = 0;
     __syncthreads();
     for (uint32_t k = 2; k <= n2; k <<= 1)
       for (uint32_t j = k >> 1; j > 0; j >>= 1) {
-        for (uint32_t i = threadIdx.x; i < n2 / 2; i += kThreads) {
+        for (uint32_t i = threadIdx.x; i < n2 / 2; i += nt) {
           const uint32_t lo = 2 * i - (i & (j - 1)), hi = lo + j;
           const uint64_t x = a[lo], y = a[hi];
           if ((x < y) == ((lo & k) == 0)) {
@@ -434,16 +466,12 @@ struct Kept {
   uint32_t t = 0, ties = 0xFFFFFFFFu;
 };
 
-// The first of `bins` bins of hist whose running count reaches k, kBins - 1 if
-// none does; one CTA.
-__device__ __forceinline__ int local_bin(Shared& sh, uint32_t k, int lane, int warp) {
-  uint32_t n[3], sum = 0;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int b = threadIdx.x * 3 + i;
-    n[i] = b < kBins ? sh.hist[b].x : 0;
-    sum += n[i];
-  }
+// The first bin of hist whose running count reaches k, kBins - 1 if none does;
+// one CTA of nt threads, five bins a thread or three.
+__device__ __forceinline__ int local_bin(Shared& sh, uint32_t k, int lane, int warp, int nt) {
+  const int per = (kBins + nt - 1) / nt, first = static_cast<int>(threadIdx.x) * per;
+  uint32_t sum = 0;
+  for (int i = 0; i < per; ++i) sum += first + i < kBins ? sh.hist[first + i].x : 0;
   uint32_t at = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -455,10 +483,10 @@ __device__ __forceinline__ int local_bin(Shared& sh, uint32_t k, int lane, int w
   __syncthreads();
   at -= sum;
   for (int i = 0; i < warp; ++i) at += sh.scan_u[i];
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    if (at < k && at + n[i] >= k) sh.b = threadIdx.x * 3 + i;  // one thread's at most
-    at += n[i];
+  if (at < k && at + sum >= k) {  // one thread at most
+    int i = 0;
+    for (; at + sh.hist[first + i].x < k; ++i) at += sh.hist[first + i].x;
+    sh.b = first + i;
   }
   __syncthreads();
   return sh.b;
@@ -471,55 +499,58 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
                                     float my_max, bool hist) {
   constexpr int VE = Vec<T>::N;
   Shared& sh = r.sh;
+  if (EXACT && threadIdx.x == 0) sh.ans[r.par].bad = 0;
   const Weigher w = sh.w;
   const int lane = r.lane, warp = r.warp;
   const float floor_z = sh.floor_z;  // min-p keeps logits from here on (-inf: off)
   const bool warm = sh.warm != 0, use_k = sh.top_k > 0, use_p = sh.use_p != 0;
 
-  // ---- the mass of all tokens, and of those that min-p keeps
+  // ---- the mass of all tokens
   Part p;
   if (EXACT) {
-    r.each([&](float z) {
-      const uint64_t x = weight(w, z);
-      p.mass += x;
-      if (z >= floor_z) p.mass2 += x;
-    });
+    r.each([&](float z) { p.mass += weight_inline(w, z); });
   } else {
-    PairSum all, kept;
-    float e = 0.f;
+    PairSum all;
+#pragma unroll 2
     for (int v = r.v0 + lane; v < r.v1; v += 32) {
       const Vec<T> x = r.load(v);
-      float s[VE], k[VE];
+      float s[VE];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float z = x.get(i), y = fast_y(w, z);
-        s[i] = fast_weight(y);
-        e = fmaf(s[i], -fmaxf(y, kCut), e);
-        k[i] = z >= floor_z ? s[i] : 0.f;
-      }
+      for (int i = 0; i < VE; ++i) s[i] = fast_weight(fast_y(w, x.get(i)));
 #pragma unroll
       for (int o = 1; o < VE; o <<= 1)
 #pragma unroll
-        for (int i = 0; i + o < VE; i += 2 * o) {
-          s[i] += s[i + o];
-          k[i] += k[i + o];
-        }
+        for (int i = 0; i + o < VE; i += 2 * o) s[i] += s[i + o];
       all.add(s[0]);
-      if (sh.use_q) kept.add(k[0]);
     }
     p.mass = all.fixed(w.one);
-    p.mass2 = sh.use_q ? kept.fixed(w.one) : p.mass;
-    // w (4 + 2.1 |y|) 2^-24, three more roundings in the sum of a piece, and
-    // the slack of this bound's own sums
-    p.err = (7.5f * all.hi + 2.2f * e) * 5.9604645e-8f;
   }
   Part before;
-  const Part S = r.template join<P_MASS | P_MASS2 | P_ERR>(p, &before);
-  // bound on the error of any sum of weights, in units of W
-  const uint64_t E = EXACT || !warm ? 0
-                                    : static_cast<uint64_t>(__float2ll_ru(S.err * 1.01f * w.one)) +
-                                          static_cast<uint64_t>(r.V) + 1024;
-  const float mass2 = static_cast<float>(S.mass2) / w.one;
+  const Part S = r.template join<P_MASS>(p, &before);
+  // Bound on the error of any sum of weights, in units of W: 2^-24 sum w
+  // (4 + 2.1 |y|), three more roundings in the sum of a piece; and since the
+  // entropy of w / S is at most log2 V, sum w |y| <= S log2(V / S).
+  uint64_t E = 0;
+  if (!EXACT && warm) {
+    const float s = static_cast<float>(S.mass) / w.one;
+    E = static_cast<uint64_t>(__float2ll_ru(
+            s * (8.f + 2.2f * fmaxf(0.f, log2f(static_cast<float>(r.V) / s))) * 6.0e-8f * w.one)) +
+        static_cast<uint64_t>(__float2ll_ru(static_cast<float>(r.V) * 1e-12f * w.one)) + 2 * r.V + 1024;
+  }
+  // and of those that min-p keeps, where the top-p cut is taken of these
+  uint64_t mass_q = S.mass;
+  if (use_p && sh.use_q && !use_k) {
+    Part q;
+    PairSum kept;
+    r.each_if([&](float z) { return z >= floor_z; }, [&](float z) {
+      if (!(z >= floor_z)) return;
+      if (EXACT) q.mass += weight(w, z);
+      else kept.add(fast_weight(fast_y(w, z)));
+    });
+    if (!EXACT) q.mass = kept.fixed(w.one);
+    mass_q = r.template join<P_MASS>(q).mass;
+  }
+  const float mass2 = static_cast<float>(mass_q) / w.one;
 
   Kept keep;
   uint32_t token = 0;  // decided by the leader alone
@@ -529,18 +560,18 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
     keep.ties = 1;
   } else if (use_k || use_p) {
     bool listed = false;
-    auto in_bins = [&](float z, int lo, int hi) {
+    // the tokens of bins up to b that min-p keeps
+    auto in_bin = [&](float z, int b) {
       const float y = fast_y(w, z);
-      if (!(y >= kCut) || !(z >= floor_z)) return false;
-      const int b = min(Row<T>::bin_of(y), kBins - 1);
-      return b >= lo && b <= hi;
+      return y >= kCut && z >= floor_z && min(Row<T>::bin_of(y), kBins - 1) <= b;
     };
     if (hist) {
-      for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = make_uint2(0, 0);
+      for (int i = threadIdx.x; i < kBins; i += r.nt) sh.hist[i] = make_uint2(0, 0);
       if (threadIdx.x == 0) sh.n_cand = 0;
       __syncthreads();
       int b1 = 0, b2 = kBins - 1;
       uint32_t upto = 0;  // tokens in bins up to b2
+      int b_cut = kBins - 1;  // candidates have bins up to this one
       if (use_k) {
         // Each slice holds k / C tokens down to the bin where the maxima of its
         // threads number k / C; the lowest of these bins over the slices is down
@@ -549,42 +580,49 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         if (y >= kCut) atomicAdd(&sh.hist[min(Row<T>::bin_of(y), kBins - 1)].x, 1u);
         __syncthreads();
         Part q;
-        q.hi = local_bin(sh, (sh.top_k + r.C - 1) / r.C, lane, warp);
-        b2 = static_cast<int>(r.template join<P_HI>(q).hi);
+        q.hi = local_bin(sh, (sh.top_k + r.C - 1) / r.C, lane, warp, r.nt);
+        b_cut = b2 = static_cast<int>(r.template join<P_HI>(q).hi);
       } else {
         // Tokens lighter than (1 - p) mass / V sum to less than (1 - p) mass.
         const float y = log2f(fmaxf(0.5f * (1.f - sh.top_p) * mass2 / static_cast<float>(r.V), 1e-30f));
-        const int b_cut = y > kCut ? min(Row<T>::bin_of(fminf(y, 0.f)) + 1, kBins - 1) : kBins - 1;
-        r.each([&](float z) {
-          const float yy = fast_y(w, z);
-          if (yy >= kCut && z >= floor_z) {
-            const int b = min(Row<T>::bin_of(yy), kBins - 1);
-            if (b <= b_cut) {
-              atomicAdd(&sh.hist[b].x, 1u);
-              // the weight over the bin's own: 15 bits
-              atomicAdd(&sh.hist[b].y, __float2uint_rn(32768.f * ex2_approx(yy + 0.03125f * b)));
-            }
-          }
+        b_cut = y > kCut ? min(Row<T>::bin_of(fminf(y, 0.f)) + 1, kBins - 1) : kBins - 1;
+      }
+      // With a small k these candidates are few enough to be sorted; else they
+      // are counted and weighed by bins.
+      if (!use_k || sh.top_k > kCap / 2) {
+        if (use_k) {
+          for (int i = threadIdx.x; i < kBins; i += r.nt) sh.hist[i] = make_uint2(0, 0);
+          __syncthreads();
+        }
+        r.each_if([&](float z) { return in_bin(z, b_cut); }, [&](float z) {
+          if (!in_bin(z, b_cut)) return;
+          const float y = fast_y(w, z);
+          const int b = min(Row<T>::bin_of(y), kBins - 1);
+          atomicAdd(&sh.hist[b].x, 1u);
+          // the weight over the bin's own: 15 bits
+          if (!use_k) atomicAdd(&sh.hist[b].y, __float2uint_rn(32768.f * ex2_approx(y + 0.03125f * b)));
         });
         r.cl.sync();
         // Running sums: this CTA adds up its share of the bins over the slices,
-        // three bins or fewer a thread.
-        const int share = (b_cut + r.C) / r.C, per = (share + kThreads - 1) / kThreads;
+        // five bins a thread or fewer.
+        const int share = (b_cut + r.C) / r.C, per = (share + r.nt - 1) / r.nt;
         const int first = r.rank * share;
-        uint32_t n[3], n_c = 0;
-        float m[3], n_m = 0.f;
+        uint32_t n[5], n_c = 0;
+        float m[5], n_m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 5; ++i) {
           const int j = static_cast<int>(threadIdx.x) * per + i, b = first + j;
           n[i] = 0;
-          uint64_t mm = 0;
-          if (i < per && j < share && b <= b_cut)
+          m[i] = 0.f;
+          if (i < per && j < share && b <= b_cut) {
+            uint64_t mm = 0;
             for (int c = 0; c < r.C; ++c) {
               const uint2 h = r.cl.map_shared_rank(sh.hist, c)[b];
               n[i] += h.x;
               mm += h.y;
             }
-          m[i] = static_cast<float>(mm) * ex2_approx(-15.f - 0.03125f * b);
+            m[i] = static_cast<float>(mm) * ex2_approx(-15.f - 0.03125f * b);
+          }
           n_c += n[i];
           n_m += m[i];
         }
@@ -619,13 +657,15 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         uint32_t must = kBins - 1, must_n = 0xFFFFFFFFu;
         q.lo = kBins - 1;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 5; ++i) {
           const int j = static_cast<int>(threadIdx.x) * per + i;
           n_at += n[i];
           m_at += m[i];
           if (i >= per || j >= share || first + j > b_cut) continue;
-          if (m_at * (1.f + 6e-5f) >= need) q.lo = min(q.lo, static_cast<uint32_t>(first + j));
-          if (m_at * (1.f - 6e-5f) > need && static_cast<uint32_t>(first + j) < must) {
+          const bool may = use_k ? n_at >= static_cast<uint32_t>(sh.top_k) : m_at * (1.f + 6e-5f) >= need;
+          const bool does = use_k ? may : m_at * (1.f - 6e-5f) > need;
+          if (may) q.lo = min(q.lo, static_cast<uint32_t>(first + j));
+          if (does && static_cast<uint32_t>(first + j) < must) {
             must = first + j;
             must_n = n_at;
           }
@@ -641,13 +681,13 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
       }
       if (use_k || upto <= kCap) {
         // ---- few candidates: the leader finishes the row with exact weights
-        const uint32_t n_all = r.gather([&](float z) { return in_bins(z, 0, b2); });
+        const uint32_t n_all = r.gather([&](float z) { return in_bin(z, b2); }, [](float) { return true; });
         if (n_all <= kCap) {
           listed = leader_draws = true;
           if (r.rank == 0) {
             uint32_t n_l = n_all;
             r.sort_desc(sh.cand, n_l);
-            for (uint32_t i = threadIdx.x; i < n_l; i += kThreads)
+            for (uint32_t i = threadIdx.x; i < n_l; i += r.nt)
               sh.wts[i] = weight(w, float_of(static_cast<uint32_t>(sh.cand[i] >> 32)));
             __syncthreads();
             if (warp == 0) {
@@ -655,7 +695,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
               bool bad = false;
               if (use_p) {
                 // with top-k the mass is this list's; else everything's, within E
-                uint64_t base = S.mass2;
+                uint64_t base = mass_q;
                 if (use_k) {
                   base = 0;
                   for (uint32_t i = lane; i < n_l; i += 32) base += sh.wts[i];
@@ -678,13 +718,13 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
               }
               if (lane == 0) {
                 sh.upto = n_l;
-                sh.bad = bad ? 1 : 0;
+                sh.ans[r.par].bad = bad ? 1 : 0;
               }
             }
             __syncthreads();
             n_l = sh.upto;
             // by index: the draw runs in the row's own order
-            for (uint32_t i = threadIdx.x; i < n_l; i += kThreads)
+            for (uint32_t i = threadIdx.x; i < n_l; i += r.nt)
               sh.cand[i] = (sh.cand[i] << 32) | i;  // ~index descends as the index ascends
             __syncthreads();
             r.sort_desc(sh.cand, n_l);
@@ -712,13 +752,11 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         // ---- many tokens stay: the cut falls in bins b1 to b2, whose tokens are
         // of one value (they tie) or few enough to be sorted
         Part q;
-        r.each([&](float z) {
-          const float y = fast_y(w, z);
-          if (!(y >= kCut) || !(z >= floor_z)) return;
-          const int b = min(Row<T>::bin_of(y), kBins - 1);
-          if (b < b1) {
+        r.each_if([&](float z) { return in_bin(z, b2); }, [&](float z) {
+          if (!in_bin(z, b2)) return;
+          if (in_bin(z, b1 - 1)) {
             q.mass += weigh<EXACT>(w, z);
-          } else if (b <= b2) {
+          } else {
             const uint32_t key = key_of(z);
             ++q.count;
             q.lo = min(q.lo, key);
@@ -726,7 +764,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
           }
         });
         q = r.template join<P_MASS | P_COUNT | P_LO | P_HI>(q);
-        const uint64_t want = mul_ceil(sh.top_p, S.mass2);
+        const uint64_t want = mul_ceil(sh.top_p, mass_q);
         const uint64_t rest = want > q.mass ? want - q.mass : 0;
         if (q.count > 0 && q.lo == q.hi) {
           const uint64_t each = max(static_cast<uint64_t>(1), weight(w, float_of(q.lo)));
@@ -739,10 +777,10 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
             listed = true;
           }
         } else if (q.count > 0 && q.count <= kCap) {
-          r.gather([&](float z) { return in_bins(z, b1, b2); });
+          r.gather([&](float z) { return in_bin(z, b2); }, [&](float z) { return !in_bin(z, b1 - 1); });
           if (r.rank == 0) {
             r.sort_desc(sh.cand, q.count);
-            for (uint32_t i = threadIdx.x; i < q.count; i += kThreads)
+            for (uint32_t i = threadIdx.x; i < q.count; i += r.nt)
               sh.wts[i] = weight(w, float_of(static_cast<uint32_t>(sh.cand[i] >> 32)));
             __syncthreads();
             if (warp == 0) {
@@ -764,14 +802,14 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
                 ties += static_cast<uint32_t>(sh.cand[i] >> 32) == t;
               ties = __reduce_add_sync(0xffffffffu, ties);
               if (lane == 0) {
-                sh.t = t;
-                sh.ties = ties;
-                sh.bad = bad ? 1 : 0;
+                sh.ans[r.par].t = t;
+                sh.ans[r.par].ties = ties;
+                sh.ans[r.par].bad = bad ? 1 : 0;
               }
             }
           }
           r.cl.sync();
-          const Shared& lead = *r.cl.map_shared_rank(&sh, 0);
+          const auto& lead = r.cl.map_shared_rank(&sh, 0)->ans[r.par];
           keep.t = lead.t;
           keep.ties = lead.ties;
           listed = lead.bad == 0;
@@ -824,14 +862,14 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
   }
 
   if (leader_draws) {
-    if (threadIdx.x == 0 && r.rank == 0 && !sh.bad) sh.t = token;
+    if (threadIdx.x == 0 && r.rank == 0) sh.ans[r.par].t = token;
   } else {
     // ---- the draw: the mass and ties ahead of each warp, then the one that holds u
     Part all = S;
     if (keep.t != 0) {
       Part q;
       PairSum f;
-      r.each([&](float z) {
+      r.each_if([&](float z) { return key_of(z) >= keep.t; }, [&](float z) {
         const uint32_t key = key_of(z);
         if (key > keep.t) {
           if (EXACT) q.mass += weight(w, z);
@@ -843,24 +881,22 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
       all = r.template join<P_MASS | P_COUNT>(q, &before);
     } else {
       all.count = before.count = 0;
-      if (lane == 0) sh.warps[warp].count = 0;
     }
-    Shared* lead = r.cl.map_shared_rank(&sh, 0);
-    if (threadIdx.x == 0) sh.bad = 0;
-    r.cl.sync();
+    auto* lead = &r.cl.map_shared_rank(&sh, 0)->ans[r.par];
     // ranks and warps are in index order
     uint64_t m = before.mass;
     uint32_t e = before.count;
     for (int i = 0; i < warp; ++i) {
       m += sh.warps[i].mass;
-      e += sh.warps[i].count;
+      if (keep.t != 0) e += sh.warps[i].count;
     }
-    const Part mine = sh.warps[warp];
+    const uint64_t my_mass = sh.warps[warp].mass;
+    const uint32_t my_eq = keep.t != 0 ? sh.warps[warp].count : 0;
     const uint32_t lim = keep.ties;
     const uint64_t wt = keep.t == 0 ? 0 : weigh<EXACT>(w, float_of(keep.t));
     bool rest;
     const uint64_t target = mul_floor(sh.u, all.mass + min(all.count, lim) * wt, rest);
-    if (m + min(e, lim) * wt <= target && m + mine.mass + min(e + mine.count, lim) * wt > target) {
+    if (m + min(e, lim) * wt <= target && m + my_mass + min(e + my_eq, lim) * wt > target) {
       bool done = false;
       for (int vb = r.v0; vb < r.v1 && !done; vb += 32) {
         const int v = vb + lane;
@@ -869,7 +905,6 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         Vec<T> x;
         if (v < r.v1) {
           x = r.load(v);
-#pragma unroll
           for (int i = 0; i < VE; ++i) {
             const float z = x.get(i);
             const uint32_t key = key_of(z);
@@ -914,9 +949,9 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
     }
   }
   r.cl.sync();
-  if (!EXACT && r.cl.map_shared_rank(&sh, 0)->bad) return false;
+  if (!EXACT && r.cl.map_shared_rank(&sh, 0)->ans[r.par].bad) return false;
   if (r.rank == 0 && threadIdx.x == 0) {
-    const int64_t at = sh.t;
+    const int64_t at = sh.ans[r.par].t;
     const float z = clean(to_f(r.row[at]));
     const float d = z == w.zmax ? 0.f : (z - w.zmax) / sh.temp;
     // ln(mass): the sum as two floats
@@ -956,13 +991,15 @@ __device__ __noinline__ int decide_exact(Row<T> r, const SampleArgs& a, int64_t 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ SampleArgs a, int slice_vecs, int resident) {
+__global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant__ SampleArgs a, int slice_vecs, int resident) {
   extern __shared__ uint4 s_slice[];
   __shared__ Shared sh;
   constexpr int VE = Vec<T>::N;
   Row<T> r(sh);
   r.lane = threadIdx.x & 31;
   r.warp = threadIdx.x >> 5;
+  r.nt = blockDim.x;
+  r.nw = blockDim.x >> 5;
   r.C = static_cast<int>(r.cl.num_blocks());
   r.rank = static_cast<int>(r.cl.block_rank());
   r.V = a.V;
@@ -976,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     const int64_t p0 = static_cast<int64_t>(r.rank) * slice_vecs;
     r.n_vec = static_cast<int>(p0 >= pieces ? 0 : min(static_cast<int64_t>(slice_vecs), pieces - p0));
     r.pos0 = p0 * VE - off;
-    const int per = (r.n_vec + kWarps - 1) / kWarps;
+    const int per = (r.n_vec + r.nw - 1) / r.nw;
     r.v0 = min(r.n_vec, r.warp * per);
     r.v1 = min(r.n_vec, r.v0 + per);
     r.row = z;
@@ -985,12 +1022,33 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
 
     // ---- copy the slice, taking the maximum on the way (a warp reads back its own)
     float mx = -INFINITY;
-    for (int v = r.v0 + r.lane; v < r.v1; v += 32) {
-      const Vec<T> x = r.fetch(v);
-      if (resident) s_slice[v] = x.raw;
+    {
+      // the pieces that lie inside the row, four loads in flight a thread
+      const int f0 = max(r.v0, r.pos0 < 0 ? 1 : 0);
+      const int64_t whole = a.V - r.pos0 >= 0 ? (a.V - r.pos0) / VE : 0;
+      const int f1 = static_cast<int>(min(static_cast<int64_t>(r.v1), whole));
+      for (int v = f0 + r.lane; v < f1; v += 128) {
+        Vec<T> x[4];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) mx = fmaxf(mx, x.get(e));
+        for (int i = 0; i < 4; ++i)
+          if (v + 32 * i < f1) x[i].raw = __ldg(r.global + v + 32 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (v + 32 * i < f1) {
+            if (resident) s_slice[v + 32 * i] = x[i].raw;
+            mx = fmaxf(mx, x[i].max());
+          }
+        }
+      }
+      // and the ones at its ends
+      for (int v = r.v0 + r.lane; v < r.v1; v += 32) {
+        if (v >= f0 && v < f1) continue;
+        const Vec<T> x = r.fetch(v);
+        if (resident) s_slice[v] = x.raw;
+        mx = fmaxf(mx, x.max());
+      }
     }
+    if (threadIdx.x == 0) sh.ans[r.par].bad = 0;
     __syncwarp();
     Part p;
     p.hi = key_of(mx);
@@ -1034,8 +1092,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       r.cl.sync();
       r.turn = decide_exact<T>(r, a, row, kmax, mx, resident && zmax < INFINITY);
     }
-    r.cl.sync();
+    r.par ^= 1;
   }
+  r.cl.sync();  // no CTA leaves while another may read its shared memory
 }
 
 template <typename T>
@@ -1064,7 +1123,9 @@ cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   const int64_t clusters = a.rows < 65536 ? a.rows : 65536;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * C));
-  cfg.blockDim = dim3(kThreads);
+  // 512 threads share a slice when there are few rows; with many, 256, three such
+  // CTAs on an SM: the fixed work of a row is a warp's
+  cfg.blockDim = dim3(a.rows * C <= sms ? 512 : 256);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
