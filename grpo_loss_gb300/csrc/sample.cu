@@ -39,7 +39,8 @@ constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 8;                 // the portable cluster size
 constexpr int kBins = 1280;                    // (five a thread at most) 1/32 of a binary order each, down to 2^-40
 constexpr int kCap = 1024;                     // candidates that one CTA sorts
-constexpr int kMaxSliceBytes = 184 * 1024;     // of a row's slice kept in shared memory
+constexpr int kCount = 256;                    // and those that it sorts by counting
+constexpr int kMaxSliceBytes = 192 * 1024;     // of a row's slice kept in shared memory
 constexpr float kCut = -40.f;                  // binary orders below the top that weigh nothing
 
 // 2^(j/32), j = 0..31, each as the sum of two floats.
@@ -139,6 +140,7 @@ __device__ __forceinline__ void exp2_pair(const float2* tab, float p, float pl, 
 // as a pair of floats, and the fixed point's scale.
 struct Weigher {
   float zmax, c_hi, c_lo, one;  // one = 2^B
+  int down;                     // 44 - B
   const float2* tab;
 };
 
@@ -156,9 +158,12 @@ __device__ __forceinline__ uint64_t weight_inline(const Weigher& w, float z) {
   int n;
   float h, hl;
   exp2_pair(w.tab, p, pl, n, h, hl);
-  const float scale = w.one * __uint_as_float(static_cast<uint32_t>(127 + n) << 23);
-  return static_cast<uint64_t>(__float2ll_rn(h * scale) +
-                               static_cast<long long>(__float2int_rn(hl * scale)));
+  // 2^44 (h + hl), h in [0.98, 2) with 24 bits behind the point at most; then
+  // down by 44 - B - n
+  const uint64_t w0 = (static_cast<uint64_t>(__float2uint_rn(h * 16777216.f)) << 20) +
+                      static_cast<int64_t>(__float2int_rn(hl * 17592186044416.f));
+  const int down = w.down - n;
+  return (w0 + ((1ull << down) >> 1)) >> down;
 }
 
 __device__ __noinline__ uint64_t weight(Weigher w, float z) { return weight_inline(w, z); }
@@ -232,21 +237,19 @@ struct PairSum {
 // What the parts of a row add up to.
 struct Part {
   uint64_t mass = 0;
-  uint64_t mass2 = 0;
+  uint64_t best = ~0ull;  // a minimum
   uint32_t count = 0;
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
-  float err = 0.f;
+  float sum = 0.f;
 };
-enum : int { P_MASS = 1, P_MASS2 = 2, P_COUNT = 4, P_LO = 8, P_HI = 16, P_ERR = 32 };
+enum : int { P_MASS = 1, P_BEST = 2, P_COUNT = 4, P_LO = 8, P_HI = 16, P_SUM = 32 };
 
 struct Shared {
   float2 tab[32];
-  Part warps[kMaxWarps];            // of this CTA
-  Part ctas[2][kMaxCluster];        // of the cluster, alternating between joins
-  uint64_t cand[kCap];              // the leader's list: key, then ~index
+  uint64_t cand[kCap];              // this CTA's candidates, the leader's list: key, then ~index
   union {
-    uint64_t wts[kCap];             // its weights
-    uint2 hist[kBins];              // count and mass of a bin (read before the list is made)
+    uint64_t wts[kCap];             // their weights
+    uint2 hist[kBins];              // count and mass of a bin (read before there are weights)
   };
   uint32_t n_cand;
   // the leader's answers to the cluster, alternating between rows
@@ -255,10 +258,10 @@ struct Shared {
     int bad;
   } ans[2];
   // this CTA's scratch
-  float scan_f[kMaxWarps];
   uint32_t scan_u[kMaxWarps];
-  int b;
-  uint32_t upto;
+  int b, b1, b2;                    // bins of the top-p cut, for both ways of weighing
+  uint32_t upto, n_kept;
+  int upto_valid;
   // the row's parameters
   Weigher w;
   float floor_z, top_p, u, temp;
@@ -271,6 +274,7 @@ struct Row {
   static constexpr int VE = Vec<T>::N;
   cg::cluster_group cl = cg::this_cluster();
   Shared& sh;
+  Part* parts;         // [2][C of at most 8][warps], alternating between joins
   const uint4* slice;  // this CTA's slice in shared memory, or null: the logits are read again
   const uint4* global; // its first piece among the logits
   const T* row;
@@ -316,56 +320,64 @@ struct Row {
     }
   }
 
-  // The fields of F of a Part over LANES lanes, in every one of them.
-  template <int F, int LANES>
-  __device__ __forceinline__ static void lanes(Part& p) {
-#pragma unroll
-    for (int o = LANES / 2; o >= 1; o >>= 1) {
-      if (F & P_MASS) p.mass += __shfl_xor_sync(0xffffffffu, p.mass, o);
-      if (F & P_MASS2) p.mass2 += __shfl_xor_sync(0xffffffffu, p.mass2, o);
-      if (F & P_ERR) p.err += __shfl_xor_sync(0xffffffffu, p.err, o);
-      if (F & P_COUNT) p.count += __shfl_xor_sync(0xffffffffu, p.count, o);
-      if (F & P_LO) p.lo = min(p.lo, __shfl_xor_sync(0xffffffffu, p.lo, o));
-      if (F & P_HI) p.hi = max(p.hi, __shfl_xor_sync(0xffffffffu, p.hi, o));
-    }
+  template <int F>
+  __device__ __forceinline__ static void add(Part& p, const Part& o) {
+    if (F & P_MASS) p.mass += o.mass;
+    if (F & P_BEST) p.best = min(p.best, o.best);
+    if (F & P_SUM) p.sum += o.sum;
+    if (F & P_COUNT) p.count += o.count;
+    if (F & P_LO) p.lo = min(p.lo, o.lo);
+    if (F & P_HI) p.hi = max(p.hi, o.hi);
   }
   template <int F>
   __device__ __forceinline__ static void put(Part& to, const Part& p) {
     if (F & P_MASS) to.mass = p.mass;
-    if (F & P_MASS2) to.mass2 = p.mass2;
-    if (F & P_ERR) to.err = p.err;
+    if (F & P_BEST) to.best = p.best;
+    if (F & P_SUM) to.sum = p.sum;
     if (F & P_COUNT) to.count = p.count;
     if (F & P_LO) to.lo = p.lo;
     if (F & P_HI) to.hi = p.hi;
   }
+  // The fields F of the warp's Parts, in every lane.
+  template <int F>
+  __device__ __forceinline__ static void lanes(Part& p) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      Part q;
+      if (F & P_MASS) q.mass = __shfl_xor_sync(0xffffffffu, p.mass, o);
+      if (F & P_BEST) q.best = __shfl_xor_sync(0xffffffffu, p.best, o);
+      if (F & P_SUM) q.sum = __shfl_xor_sync(0xffffffffu, p.sum, o);
+      if (F & P_COUNT) q.count = __shfl_xor_sync(0xffffffffu, p.count, o);
+      if (F & P_LO) q.lo = __shfl_xor_sync(0xffffffffu, p.lo, o);
+      if (F & P_HI) q.hi = __shfl_xor_sync(0xffffffffu, p.hi, o);
+      add<F>(p, q);
+    }
+  }
 
   // Joins the fields F of every thread's Part over the cluster; each thread gets
-  // the whole. The CTA's own sum is pushed to the others (remote shared memory
-  // is slow to read: 128 parts read by every warp took 16,000 cycles), so that
-  // after one barrier everything is read at home. `before` gets the sum over the
-  // CTAs ahead of this one; sh.warps keeps the warps'.
+  // the whole, `mine` its warp's and `before` what the warps ahead of its own
+  // have. A warp pushes its sum into every CTA's shared memory, so that after
+  // one barrier all is read at home (remote shared memory is slow to read: 128
+  // Parts read by every warp took 16,000 cycles).
   template <int F>
-  __device__ __forceinline__ Part join(Part p, Part* before = nullptr) {
-    lanes<F, 32>(p);
-    if (lane == 0) put<F>(sh.warps[warp], p);
-    __syncthreads();
-    if (warp == 0) {
-      Part q;
-      if (lane < nw) put<F>(q, sh.warps[lane]);
-      lanes<F, kMaxWarps>(q);
-      if (lane < C) put<F>(*cl.map_shared_rank(&sh.ctas[turn][rank], lane), q);
-    }
+  __device__ __forceinline__ Part join(Part p, Part* mine = nullptr, Part* before = nullptr) {
+    lanes<F>(p);
+    if (mine) *mine = p;
+    const int n = C * nw, me = rank * nw + warp;
+    Part* slots = parts + turn * kMaxCluster * nw;
+    if (lane < C) put<F>(*cl.map_shared_rank(slots + me, lane), p);
     cl.sync();
-    Part all;
-    for (int c = 0; c < C; ++c) {
-      if (before && c == rank) *before = all;
-      const Part& o = sh.ctas[turn][c];
-      if (F & P_MASS) all.mass += o.mass;
-      if (F & P_MASS2) all.mass2 += o.mass2;
-      if (F & P_ERR) all.err += o.err;
-      if (F & P_COUNT) all.count += o.count;
-      if (F & P_LO) all.lo = min(all.lo, o.lo);
-      if (F & P_HI) all.hi = max(all.hi, o.hi);
+    Part all, ahead;
+    for (int i = lane; i < n; i += 32) {
+      Part o;
+      put<F>(o, slots[i]);
+      add<F>(all, o);
+      if (before && i < me) add<F>(ahead, o);
+    }
+    lanes<F>(all);
+    if (before) {
+      lanes<F>(ahead);
+      *before = ahead;
     }
     turn ^= 1;
     return all;
@@ -398,46 +410,63 @@ struct Row {
   // Bin of a logit in steps of 1/32 of a binary order below the top.
   __device__ __forceinline__ static int bin_of(float y) { return static_cast<int>(-32.f * y); }
 
-  // Copies the elements that both functions accept to the leader's list (the
-  // first accepts from some logit on, so that a piece's maximum can be asked); returns their number
-  // over the cluster (the list is cut at kCap).
+  // Lists the elements that both functions accept (the first accepts from some
+  // logit on, so that a piece's maximum can be asked); returns their number over
+  // the cluster. If they are kCap or fewer, the leader gets all of them.
   template <typename F, typename G>
   __device__ uint32_t gather(F accept, G also) {
-    uint32_t* n = cl.map_shared_rank(&sh.n_cand, 0);
-    uint64_t* to = cl.map_shared_rank(sh.cand, 0);
-    for (int vb = v0; vb < v1; vb += 32) {
-      const int v = vb + lane;
-      Vec<T> x;
-      uint32_t want = 0;
-      if (v < v1) {
-        x = load(v);
-        if (accept(x.max())) {  // (what it accepts it accepts above, too)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) want |= accept(x.get(e)) && also(x.get(e)) ? (1u << e) : 0u;
-        }
-      }
-      if (!__any_sync(0xffffffffu, want != 0)) continue;
-      const uint32_t mine = __popc(want);
-      uint32_t at = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, at, o);
-        if (lane >= o) at += y;
-      }
-      uint32_t base = 0;
-      if (lane == 31) base = atomicAdd(n, at);
-      base = __shfl_sync(0xffffffffu, base, 31) + at - mine;
+    Part p;
+    for (int v = v0 + lane; v < v1; v += 32) {
+      const Vec<T> x = load(v);
+      if (!accept(x.max())) continue;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        if (want >> e & 1) {
+        const float z = x.get(e);
+        if (accept(z) && also(z)) {
+          const uint32_t at = atomicAdd(&sh.n_cand, 1u);
           const uint32_t idx = static_cast<uint32_t>(pos0 + static_cast<int64_t>(v) * VE + e);
-          if (base < kCap) to[base] = (static_cast<uint64_t>(key_of(x.get(e))) << 32) | ~idx;
-          ++base;
+          if (at < kCap) sh.cand[at] = (static_cast<uint64_t>(key_of(z)) << 32) | ~idx;
+          ++p.count;
         }
       }
     }
-    cl.sync();
-    return *n;
+    const uint32_t n = join<P_COUNT>(p).count;
+    if (rank == 0 && n <= kCap) {
+      if (static_cast<int>(threadIdx.x) < C) sh.scan_u[threadIdx.x] = *cl.map_shared_rank(&sh.n_cand, threadIdx.x);
+      __syncthreads();
+      for (uint32_t i = sh.scan_u[0] + threadIdx.x; i < n; i += nt) {
+        uint32_t j = i;
+        int c = 0;
+        while (j >= sh.scan_u[c]) j -= sh.scan_u[c++];
+        sh.cand[i] = cl.map_shared_rank(sh.cand, c)[j];
+      }
+      __syncthreads();
+    }
+    return n;
+  }
+
+  // Sorts the leader's n candidates, largest first, and weighs them. A few by
+  // counting the larger ones of each: a barrier of the CTA takes some 200 cycles
+  // and a sorting network of 128 elements has 28 of them.
+  __device__ void sort_and_weigh(uint32_t n) {
+    if (n <= kCount) {
+      uint64_t c = 0;
+      uint32_t at = 0;
+      if (threadIdx.x < n) {
+        c = sh.cand[threadIdx.x];
+        for (uint32_t j = 0; j < n; ++j) at += sh.cand[j] > c;
+      }
+      __syncthreads();
+      if (threadIdx.x < n) {
+        sh.cand[at] = c;
+        sh.wts[at] = weight(sh.w, float_of(static_cast<uint32_t>(c >> 32)));
+      }
+    } else {
+      sort_desc(sh.cand, n);
+      for (uint32_t i = threadIdx.x; i < n; i += nt)
+        sh.wts[i] = weight(sh.w, float_of(static_cast<uint32_t>(sh.cand[i] >> 32)));
+    }
+    __syncthreads();
   }
 
   // Sorts the first n of a list in shared memory, largest first (one CTA).
@@ -500,9 +529,9 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
   constexpr int VE = Vec<T>::N;
   Shared& sh = r.sh;
   if (EXACT && threadIdx.x == 0) sh.ans[r.par].bad = 0;
-  const Weigher w = sh.w;
+  Weigher w = sh.w;
+  w.zmax = float_of(kmax);
   const int lane = r.lane, warp = r.warp;
-  const float floor_z = sh.floor_z;  // min-p keeps logits from here on (-inf: off)
   const bool warm = sh.warm != 0, use_k = sh.top_k > 0, use_p = sh.use_p != 0;
 
   // ---- the mass of all tokens
@@ -525,8 +554,9 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
     }
     p.mass = all.fixed(w.one);
   }
-  Part before;
-  const Part S = r.template join<P_MASS>(p, &before);
+  Part mine, before;
+  const Part S = r.template join<P_MASS>(p, &mine, &before);
+  const float floor_z = sh.floor_z;  // min-p keeps logits from here on (-inf: off)
   // Bound on the error of any sum of weights, in units of W: 2^-24 sum w
   // (4 + 2.1 |y|), three more roundings in the sum of a piece; and since the
   // entropy of w / S is at most log2 V, sum w |y| <= S log2(V / S).
@@ -553,8 +583,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
   const float mass2 = static_cast<float>(mass_q) / w.one;
 
   Kept keep;
-  uint32_t token = 0;  // decided by the leader alone
-  bool leader_draws = false;
+  bool leader_draws = false;  // the token is decided by the leader alone
   if (!warm) {
     keep.t = kmax;
     keep.ties = 1;
@@ -571,6 +600,13 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
       __syncthreads();
       int b1 = 0, b2 = kBins - 1;
       uint32_t upto = 0;  // tokens in bins up to b2
+      // (the exact way takes over the bins that the fast one found)
+      const bool found = EXACT && !use_k && sh.upto_valid;
+      if (found) {
+        b1 = sh.b1;
+        b2 = sh.b2;
+        upto = sh.upto;
+      } else {
       int b_cut = kBins - 1;  // candidates have bins up to this one
       if (use_k) {
         // Each slice holds k / C tokens down to the bin where the maxima of its
@@ -626,58 +662,51 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
           n_c += n[i];
           n_m += m[i];
         }
-        uint32_t n_in = n_c;
-        float m_in = n_m;
+        uint32_t n_at = n_c;  // inclusive over the warp, then with what is ahead of it
+        float m_at = n_m;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t x = __shfl_up_sync(0xffffffffu, n_in, o);
-          const float z = __shfl_up_sync(0xffffffffu, m_in, o);
+          const uint32_t x = __shfl_up_sync(0xffffffffu, n_at, o);
+          const float z = __shfl_up_sync(0xffffffffu, m_at, o);
           if (lane >= o) {
-            n_in += x;
-            m_in += z;
+            n_at += x;
+            m_at += z;
           }
-        }
-        if (lane == 31) {
-          sh.scan_u[warp] = n_in;
-          sh.scan_f[warp] = m_in;
         }
         Part q, ahead;
         q.count = n_c;
-        q.err = n_m;
-        r.template join<P_COUNT | P_ERR>(q, &ahead);
-        uint32_t n_at = ahead.count + n_in - n_c;
-        float m_at = ahead.err + m_in - n_m;
-        for (int i = 0; i < warp; ++i) {
-          n_at += sh.scan_u[i];
-          m_at += sh.scan_f[i];
-        }
+        q.sum = n_m;
+        r.template join<P_COUNT | P_SUM>(q, nullptr, &ahead);
+        n_at += ahead.count - n_c;
+        m_at += ahead.sum - n_m;
         // the masses here are 2^-16 off for their 15 bits, and 2^-20 for the rest
         const float need = sh.top_p * mass2;
-        // the first bins that may, and that must, reach the mass
-        uint32_t must = kBins - 1, must_n = 0xFFFFFFFFu;
+        // the first bin that may reach the mass; the first that does, and the count up to it
         q.lo = kBins - 1;
+        q.best = (static_cast<uint64_t>(kBins - 1) << 32) | 0xFFFFFFFFu;
 #pragma unroll
         for (int i = 0; i < 5; ++i) {
           const int j = static_cast<int>(threadIdx.x) * per + i;
           n_at += n[i];
           m_at += m[i];
           if (i >= per || j >= share || first + j > b_cut) continue;
+          const uint32_t b = first + j;
           const bool may = use_k ? n_at >= static_cast<uint32_t>(sh.top_k) : m_at * (1.f + 6e-5f) >= need;
           const bool does = use_k ? may : m_at * (1.f - 6e-5f) > need;
-          if (may) q.lo = min(q.lo, static_cast<uint32_t>(first + j));
-          if (does && static_cast<uint32_t>(first + j) < must) {
-            must = first + j;
-            must_n = n_at;
-          }
+          if (may) q.lo = min(q.lo, b);
+          if (does) q.best = min(q.best, (static_cast<uint64_t>(b) << 32) | n_at);
         }
-        // the smallest bin that must, and the count up to it, through one maximum
-        q.hi = kBins - 1 - must;
-        const Part f = r.template join<P_LO | P_HI>(q);
-        b1 = static_cast<int>(f.lo);
-        b2 = static_cast<int>(kBins - 1 - f.hi);
-        Part g;
-        g.lo = must == static_cast<uint32_t>(b2) ? must_n : 0xFFFFFFFFu;
-        upto = r.template join<P_LO>(g).lo;
+        q = r.template join<P_LO | P_BEST>(q);
+        b1 = static_cast<int>(q.lo);
+        b2 = static_cast<int>(q.best >> 32);
+        upto = static_cast<uint32_t>(q.best);
+        if (threadIdx.x == 0) {
+          sh.b1 = b1;
+          sh.b2 = b2;
+          sh.upto = upto;
+          sh.upto_valid = 1;
+        }
+      }
       }
       if (use_k || upto <= kCap) {
         // ---- few candidates: the leader finishes the row with exact weights
@@ -686,10 +715,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
           listed = leader_draws = true;
           if (r.rank == 0) {
             uint32_t n_l = n_all;
-            r.sort_desc(sh.cand, n_l);
-            for (uint32_t i = threadIdx.x; i < n_l; i += r.nt)
-              sh.wts[i] = weight(w, float_of(static_cast<uint32_t>(sh.cand[i] >> 32)));
-            __syncthreads();
+            r.sort_and_weigh(n_l);
             if (warp == 0) {
               if (use_k) n_l = min(n_l, static_cast<uint32_t>(sh.top_k));
               bool bad = false;
@@ -717,13 +743,29 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
                 n_l = max(1u, stay);
               }
               if (lane == 0) {
-                sh.upto = n_l;
+                sh.n_kept = n_l;
                 sh.ans[r.par].bad = bad ? 1 : 0;
+                sh.ans[r.par].t = 0xFFFFFFFFu;
               }
             }
             __syncthreads();
-            n_l = sh.upto;
-            // by index: the draw runs in the row's own order
+            n_l = sh.n_kept;
+            // The draw runs in the row's own order. Of a few, each adds up the
+            // weights of the indexes up to its own.
+            if (n_l <= kCount) {
+              uint64_t total = 0, upto_me = 0;
+              const uint32_t mine_idx = threadIdx.x < n_l ? static_cast<uint32_t>(sh.cand[threadIdx.x]) : 0;
+              if (warp * 32 < static_cast<int>(n_l)) {
+                for (uint32_t j = 0; j < n_l; ++j) {
+                  const uint64_t x = sh.wts[j];
+                  total += x;
+                  if (static_cast<uint32_t>(sh.cand[j]) >= mine_idx) upto_me += x;  // (~index)
+                }
+              }
+              bool rest;
+              if (threadIdx.x < n_l && upto_me > mul_floor(sh.u, total, rest))
+                atomicMin(&sh.ans[r.par].t, ~mine_idx);
+            } else {
             for (uint32_t i = threadIdx.x; i < n_l; i += r.nt)
               sh.cand[i] = (sh.cand[i] << 32) | i;  // ~index descends as the index ascends
             __syncthreads();
@@ -740,11 +782,14 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
                 const uint64_t x = i < n_l ? sh.wts[static_cast<uint32_t>(c)] : 0;
                 const uint32_t hit = __ballot_sync(0xffffffffu, run + warp_scan(x, lane) > target);
                 if (hit) {
-                  token = ~static_cast<uint32_t>(__shfl_sync(0xffffffffu, c, __ffs(hit) - 1) >> 32);
+                  const uint32_t at = ~static_cast<uint32_t>(
+                      __shfl_sync(0xffffffffu, c, __ffs(hit) - 1) >> 32);
+                  if (lane == 0) sh.ans[r.par].t = at;
                   break;
                 }
                 run += warp_sum(x);
               }
+            }
             }
           }
         }
@@ -779,10 +824,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         } else if (q.count > 0 && q.count <= kCap) {
           r.gather([&](float z) { return in_bin(z, b2); }, [&](float z) { return !in_bin(z, b1 - 1); });
           if (r.rank == 0) {
-            r.sort_desc(sh.cand, q.count);
-            for (uint32_t i = threadIdx.x; i < q.count; i += r.nt)
-              sh.wts[i] = weight(w, float_of(static_cast<uint32_t>(sh.cand[i] >> 32)));
-            __syncthreads();
+            r.sort_and_weigh(q.count);
             if (warp == 0) {
               uint64_t run = 0;
               uint32_t stay = 0;
@@ -861,9 +903,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
     keep.t = key_of(floor_z);
   }
 
-  if (leader_draws) {
-    if (threadIdx.x == 0 && r.rank == 0) sh.ans[r.par].t = token;
-  } else {
+  if (!leader_draws) {
     // ---- the draw: the mass and ties ahead of each warp, then the one that holds u
     Part all = S;
     if (keep.t != 0) {
@@ -878,25 +918,17 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         q.count += key == keep.t;
       });
       if (!EXACT) q.mass = f.fixed(w.one);
-      all = r.template join<P_MASS | P_COUNT>(q, &before);
-    } else {
-      all.count = before.count = 0;
+      all = r.template join<P_MASS | P_COUNT>(q, &mine, &before);
     }
     auto* lead = &r.cl.map_shared_rank(&sh, 0)->ans[r.par];
-    // ranks and warps are in index order
+    // (CTAs and warps are in index order)
     uint64_t m = before.mass;
     uint32_t e = before.count;
-    for (int i = 0; i < warp; ++i) {
-      m += sh.warps[i].mass;
-      if (keep.t != 0) e += sh.warps[i].count;
-    }
-    const uint64_t my_mass = sh.warps[warp].mass;
-    const uint32_t my_eq = keep.t != 0 ? sh.warps[warp].count : 0;
     const uint32_t lim = keep.ties;
     const uint64_t wt = keep.t == 0 ? 0 : weigh<EXACT>(w, float_of(keep.t));
     bool rest;
     const uint64_t target = mul_floor(sh.u, all.mass + min(all.count, lim) * wt, rest);
-    if (m + min(e, lim) * wt <= target && m + my_mass + min(e + my_eq, lim) * wt > target) {
+    if (m + min(e, lim) * wt <= target && m + mine.mass + min(e + mine.count, lim) * wt > target) {
       bool done = false;
       for (int vb = r.v0; vb < r.v1 && !done; vb += 32) {
         const int v = vb + lane;
@@ -905,11 +937,17 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         Vec<T> x;
         if (v < r.v1) {
           x = r.load(v);
-          for (int i = 0; i < VE; ++i) {
-            const float z = x.get(i);
-            const uint32_t key = key_of(z);
-            if (key > keep.t) s += weigh<EXACT>(w, z);
-            eq += key == keep.t;
+          if (keep.t == 0 || key_of(x.max()) >= keep.t) {
+            float f = 0.f;
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+              const float z = x.get(i);
+              const uint32_t key = key_of(z);
+              if (EXACT) s += key > keep.t ? weight(w, z) : 0;
+              else f += key > keep.t ? fast_weight(fast_y(w, z)) : 0.f;
+              eq += key == keep.t;
+            }
+            if (!EXACT) s = static_cast<uint64_t>(__float2ll_rn(f * w.one));
           }
         }
         const uint64_t s_in = m + warp_scan(s, lane);
@@ -1003,6 +1041,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
   r.C = static_cast<int>(r.cl.num_blocks());
   r.rank = static_cast<int>(r.cl.block_rank());
   r.V = a.V;
+  r.parts = reinterpret_cast<Part*>(s_slice + (resident ? slice_vecs : 0));
   if (threadIdx.x < 32) sh.tab[threadIdx.x] = c_exp2_32[threadIdx.x];
   const int n_cl = gridDim.x / r.C;
   for (int64_t row = blockIdx.x / r.C; row < a.rows; row += n_cl) {
@@ -1019,6 +1058,16 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
     r.row = z;
     r.global = reinterpret_cast<const uint4*>(z - off) + p0;
     r.slice = resident ? s_slice : nullptr;
+
+    float prm_t = 1.f, prm_p = 1.f, prm_q = 0.f, prm_u = 0.f;
+    int prm_k = 0;
+    if (threadIdx.x == 0) {
+      if (a.temperature) prm_t = a.temperature[row];
+      if (a.top_k) prm_k = a.top_k[row];
+      if (a.top_p) prm_p = a.top_p[row];
+      if (a.min_p) prm_q = a.min_p[row];
+      prm_u = a.u[row];
+    }
 
     // ---- copy the slice, taking the maximum on the way (a warp reads back its own)
     float mx = -INFINITY;
@@ -1048,7 +1097,28 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
         mx = fmaxf(mx, x.max());
       }
     }
-    if (threadIdx.x == 0) sh.ans[r.par].bad = 0;
+    if (threadIdx.x == 0) {
+      sh.ans[r.par].bad = 0;
+      sh.upto_valid = 0;
+      sh.warm = prm_t > 0.f;
+      const float temp = sh.warm ? prm_t : 1.f;
+      sh.temp = temp;
+      // log2(e) / T, kept within float's range (a T near 0, an infinite one)
+      const float c = fminf(fmaxf(kLog2e / temp, 1.4e-45f), 3.4e38f);
+      sh.w.c_hi = c;
+      sh.w.c_lo = c > 1e-30f && c < 1e30f ? (__fmaf_rn(-c, temp, kLog2e) + kLog2eLo) / temp : 0.f;
+      // V 2^B < 2^62
+      const int bits = min(44, 62 - (32 - __clz(static_cast<int>(a.V))));
+      sh.w.one = __uint_as_float(static_cast<uint32_t>(127 + bits) << 23);
+      sh.w.down = 44 - bits;
+      sh.w.tab = sh.tab;
+      sh.top_k = prm_k > 0 && prm_k < a.V ? prm_k : 0;
+      // weights below 2^-40 are 0: a lower q keeps every token that counts
+      sh.use_q = prm_q >= 9.094947e-13f && sh.warm;
+      sh.use_p = prm_p < 1.f;
+      sh.top_p = fmaxf(prm_p, 0.f);
+      sh.u = fminf(fmaxf(prm_u, 0.f), 1.f - 5.9604645e-8f);
+    }
     __syncwarp();
     Part p;
     p.hi = key_of(mx);
@@ -1061,32 +1131,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
       }
       continue;
     }
-    if (threadIdx.x == 0) {
-      const float T_in = a.temperature ? a.temperature[row] : 1.f;
-      sh.warm = T_in > 0.f;
-      const float temp = sh.warm ? T_in : 1.f;
-      sh.temp = temp;
+    if (threadIdx.x == 0) {  // (read behind the next join)
       sh.w.zmax = zmax;
-      // log2(e) / T, kept within float's range (a T near 0, an infinite one)
-      const float c = fminf(fmaxf(kLog2e / temp, 1.4e-45f), 3.4e38f);
-      sh.w.c_hi = c;
-      sh.w.c_lo = c > 1e-30f && c < 1e30f ? (__fmaf_rn(-c, temp, kLog2e) + kLog2eLo) / temp : 0.f;
-      // V 2^B < 2^62
-      const int bits = min(44, 62 - (32 - __clz(static_cast<int>(a.V))));
-      sh.w.one = __uint_as_float(static_cast<uint32_t>(127 + bits) << 23);
-      sh.w.tab = sh.tab;
-      const int k = a.top_k ? a.top_k[row] : 0;
-      sh.top_k = k > 0 && k < a.V ? k : 0;
-      const float q = a.min_p ? a.min_p[row] : 0.f;
-      // weights below 2^-40 are 0: a lower q keeps every token that counts
-      sh.use_q = q >= 9.094947e-13f && sh.warm;
-      sh.floor_z = !sh.use_q ? -INFINITY : q >= 1.f ? zmax : min_logit(sh.w, temp, q);
-      sh.top_p = a.top_p ? a.top_p[row] : 1.f;
-      sh.use_p = sh.top_p < 1.f;
-      sh.top_p = fmaxf(sh.top_p, 0.f);
-      sh.u = fminf(fmaxf(a.u[row], 0.f), 1.f - 5.9604645e-8f);
+      sh.floor_z = !sh.use_q ? -INFINITY : prm_q >= 1.f ? zmax : min_logit(sh.w, sh.temp, prm_q);
     }
-    __syncthreads();
     if (!resident || zmax == INFINITY || !decide<T, false>(r, a, row, kmax, mx, true)) {
       // (the cluster's CTAs leave a row that was not decided at the same point)
       r.cl.sync();
@@ -1109,23 +1157,26 @@ cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t s) {
   const int64_t slice = (pieces + C - 1) / C;
   const bool resident = slice * 16 <= kMaxSliceBytes;
   if (slice > INT32_MAX / VE) return cudaErrorInvalidValue;
-  const size_t smem = resident ? static_cast<size_t>(slice) * 16 : 0;
+  // 512 threads share a slice when there are few rows; with many, 256, three such
+  // CTAs on an SM: the fixed work of a row is a warp's
+  const int threads = a.rows * C <= sms ? 512 : 256;
+  const size_t smem = (resident ? static_cast<size_t>(slice) * 16 : 0) +
+                      2 * kMaxCluster * (threads / 32) * sizeof(Part);
   static std::atomic<uint64_t> configured{0};  // one bit a device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(configured.load() & bit)) {
-    e = cudaFuncSetAttribute(k_sample<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSliceBytes);
+    e = cudaFuncSetAttribute(k_sample<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxSliceBytes + 2 * kMaxCluster * kMaxWarps * static_cast<int>(sizeof(Part)));
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
   cudaLaunchConfig_t cfg = {};
   const int64_t clusters = a.rows < 65536 ? a.rows : 65536;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * C));
-  // 512 threads share a slice when there are few rows; with many, 256, three such
-  // CTAs on an SM: the fixed work of a row is a warp's
-  cfg.blockDim = dim3(a.rows * C <= sms ? 512 : 256);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
