@@ -17,6 +17,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunk = 4096;  // elements a CTA takes at a time (a multiple of 32: whole blocks)
 
+// The table of one launch, a kernel parameter: no copy to the device goes before
+// the launch, and a captured launch holds its own.
 struct AdamTable {
   AdamConst c;
   int n;
@@ -24,10 +26,9 @@ struct AdamTable {
   AdamTensor t[kAdamMaxTensors];
 };
 
-// The dither of element i: 16 bits (see grpo_adamw_step in grpo.h).
-__device__ __forceinline__ uint32_t dither16(uint32_t i, uint32_t base) {
-  return (i * 0x91E10DA5u + base) >> 16;
-}
+// The dither of element i at step t: the high 16 bits of i * kDitherIndex + t *
+// 0xC13FA9A9 + salt (see grpo_adamw_step in grpo.h).
+constexpr uint32_t kDitherIndex = 0x91E10DA5u, kSaltV = 0x55555555u, kSaltP = 0xAAAAAAAAu;
 
 // Largest power-of-two byte E with amax * 2^(127 - E) <= 448 = 1.75 * 2^8:
 // adding 0x1FFFFF to the bits carries into the exponent when the significand
@@ -58,15 +59,6 @@ __device__ __forceinline__ float dither_e4m3(float y, uint32_t d) {
   return __uint_as_float(b & 0xFFF00000u) - base;
 }
 
-__device__ __forceinline__ float decode_e4m3(uint8_t c) {
-  __nv_fp8_e4m3 q;
-  q.__x = c;
-  return static_cast<float>(q);
-}
-__device__ __forceinline__ uint8_t encode_e4m3(float y) {
-  return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
-}
-
 // Maximum over the warp that keeps a NaN.
 __device__ __forceinline__ float warp_amax(float a) {
 #pragma unroll
@@ -89,13 +81,199 @@ __device__ __forceinline__ void update(const AdamConst& c, float keep, float g, 
   x = __fmaf_rn(-c.lr_t, __fdiv_rn(m, den), __fmul_rn(x, keep));
 }
 
-// A thread takes one element at a time; with 8-bit states a warp holds one
-// block of 32.
+// Eight consecutive elements of a buffer, as 16-byte accesses.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+  if (BF16) {
+    const uint4 r = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float((e & 1) ? (w[e / 2] & 0xFFFF0000u) : (w[e / 2] << 16));
+  } else {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = __ldcs(q), b = __ldcs(q + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store8(float* p, int64_t i, const float (&v)[8]) {
+  float4* q = reinterpret_cast<float4*>(p + i);
+  __stcs(q, make_float4(v[0], v[1], v[2], v[3]));
+  __stcs(q + 1, make_float4(v[4], v[5], v[6], v[7]));
+}
+// bf16 bit patterns in the low halves
+__device__ __forceinline__ void store8(__nv_bfloat16* p, int64_t i, const uint32_t (&v)[8]) {
+  __stcs(reinterpret_cast<uint4*>(p + i), make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16,
+                                                     v[4] | v[5] << 16, v[6] | v[7] << 16));
+}
+// Decodes or encodes a pair of e4m3 codes.
+__device__ __forceinline__ float2 decode2(uint32_t c) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ void decode8(const void* p, int64_t i, float scale, float (&v)[8]) {
+  const uint2 r = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + i));
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float2 f = decode2(((e < 4 ? r.x : r.y) >> (8 * (e & 3))) & 0xFFFFu);
+    v[e] = f.x * scale;
+    v[e + 1] = f.y * scale;
+  }
+}
+__device__ __forceinline__ void encode8(void* p, int64_t i, const float (&v)[8]) {
+  uint2 r;
+  r.x = encode2(v[0], v[1]) | encode2(v[2], v[3]) << 16;
+  r.y = encode2(v[4], v[5]) | encode2(v[6], v[7]) << 16;
+  __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + i), r);
+}
+// max(a, b) that keeps a NaN
+__device__ __forceinline__ float amax(float a, float b) { return (a != a || a > b) ? a : b; }
+// over the four threads of a block of 32
+__device__ __forceinline__ float quad_amax(float a) {
+  a = amax(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  return amax(a, __shfl_xor_sync(0xffffffffu, a, 2));
+}
+// bf16 bits of x: to nearest beside a master, else dithered
+template <bool NEAREST>
+__device__ __forceinline__ uint32_t param_bits(float x, uint32_t d) {
+  if (NEAREST || !(fabsf(x) < INFINITY)) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+  return (__float_as_uint(x) + d) >> 16;
+}
+
+// Whole pieces of eight elements of a chunk at element i0, `end` of them in all
+// (a multiple of 8; every buffer on a 16-byte boundary). With 8-bit states four
+// threads hold a block of 32.
 template <int KIND>
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamTable tab) {
+__device__ __forceinline__ void pieces(const AdamConst& c, const AdamTensor& t, int64_t i0, int end) {
   constexpr bool kPBf16 = (KIND & ADAM_P_BF16) != 0, kGBf16 = (KIND & ADAM_G_BF16) != 0;
   constexpr bool kMaster = (KIND & ADAM_MASTER) != 0, k8 = (KIND & ADAM_BITS8) != 0;
-  const AdamConst& c = tab.c;
+  for (int k = threadIdx.x * 8; k < kChunk; k += kThreads * 8) {
+    const bool in = k < end;
+    if (k8 ? !__any_sync(0xffffffffu, in) : !in) break;
+    const int64_t i = i0 + k, blk = i >> 5;
+    float g[8], x[8], m[8], v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = x[e] = m[e] = v[e] = 0.f;
+    if (in) {
+      load8<kGBf16>(t.g, i, g);
+      load8<kPBf16 && !kMaster>(kMaster ? t.w : t.p, i, x);
+      if (k8) {
+        decode8(t.m, i, scale_value(t.ms[blk]), m);
+        decode8(t.v, i, scale_value(t.vs[blk]), v);
+      } else {
+        load8<false>(t.m, i, m);
+        load8<false>(t.v, i, v);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) update(c, t.keep, g[e], x[e], m[e], v[e]);
+    const uint32_t d0 = static_cast<uint32_t>(i) * kDitherIndex + c.dither;  // of element i, unshifted
+    if (k8) {
+      float am = 0.f, av = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        am = amax(am, fabsf(m[e]));
+        av = amax(av, v[e]);
+      }
+      am = quad_amax(am);
+      av = quad_amax(av);
+      const uint32_t em = block_scale(am), ev = block_scale(av);
+      const float im = inv_scale_value(em), iv = inv_scale_value(ev);
+      const float least = av == 0.f ? 0.f : 0.001953125f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t d = d0 + e * kDitherIndex;
+        m[e] = copysignf(dither_e4m3(fabsf(m[e]) * im, d >> 16), m[e]);
+        v[e] = fmaxf(dither_e4m3(v[e] * iv, (d + kSaltV) >> 16), least);
+      }
+      if (in) {
+        encode8(t.m_out, i, m);
+        encode8(t.v_out, i, v);
+        if ((k & 31) == 0) {
+          t.ms_out[blk] = static_cast<uint8_t>(em);
+          t.vs_out[blk] = static_cast<uint8_t>(ev);
+        }
+      }
+    } else {
+      store8(static_cast<float*>(t.m_out), i, m);
+      store8(static_cast<float*>(t.v_out), i, v);
+    }
+    if (in) {
+      if (kMaster) store8(t.w_out, i, x);
+      if (kPBf16) {
+        uint32_t b[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[e] = param_bits<kMaster>(x[e], (d0 + e * kDitherIndex + kSaltP) >> 16);
+        store8(static_cast<__nv_bfloat16*>(t.p_out), i, b);
+      } else {
+        store8(static_cast<float*>(t.p_out), i, x);
+      }
+    }
+  }
+}
+
+// Elements first to end of a chunk one by one (a tensor's ragged end, buffers
+// off a 16-byte boundary); with 8-bit states a warp holds a block of 32.
+template <int KIND>
+__device__ __forceinline__ void singles(const AdamConst& c, const AdamTensor& t, int64_t i0, int first,
+                                        int end) {
+  constexpr bool kPBf16 = (KIND & ADAM_P_BF16) != 0, kGBf16 = (KIND & ADAM_G_BF16) != 0;
+  constexpr bool kMaster = (KIND & ADAM_MASTER) != 0, k8 = (KIND & ADAM_BITS8) != 0;
+  for (int k = first + threadIdx.x; k < kChunk; k += kThreads) {
+    const bool in = k < end;
+    if (!__any_sync(0xffffffffu, in)) break;
+    const int64_t i = i0 + k, blk = i >> 5;
+    float g = 0.f, x = 0.f, m = 0.f, v = 0.f;
+    if (in) {
+      g = kGBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.g)[i])
+                 : static_cast<const float*>(t.g)[i];
+      x = kMaster ? t.w[i]
+          : kPBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.p)[i])
+                   : static_cast<const float*>(t.p)[i];
+      if (k8) {
+        m = decode2(static_cast<const uint8_t*>(t.m)[i]).x * scale_value(t.ms[blk]);
+        v = decode2(static_cast<const uint8_t*>(t.v)[i]).x * scale_value(t.vs[blk]);
+      } else {
+        m = static_cast<const float*>(t.m)[i];
+        v = static_cast<const float*>(t.v)[i];
+      }
+      update(c, t.keep, g, x, m, v);
+    }
+    const uint32_t d = static_cast<uint32_t>(i) * kDitherIndex + c.dither;
+    if (k8) {
+      const float av = warp_amax(v);
+      const uint32_t em = block_scale(warp_amax(fabsf(m))), ev = block_scale(av);
+      const float ym = dither_e4m3(fabsf(m) * inv_scale_value(em), d >> 16);
+      const float yv = fmaxf(dither_e4m3(v * inv_scale_value(ev), (d + kSaltV) >> 16),
+                             av == 0.f ? 0.f : 0.001953125f);
+      if (in) {
+        static_cast<uint8_t*>(t.m_out)[i] = static_cast<uint8_t>(encode2(copysignf(ym, m), 0.f));
+        static_cast<uint8_t*>(t.v_out)[i] = static_cast<uint8_t>(encode2(yv, 0.f));
+        if ((k & 31) == 0) {
+          t.ms_out[blk] = static_cast<uint8_t>(em);
+          t.vs_out[blk] = static_cast<uint8_t>(ev);
+        }
+      }
+    } else if (in) {
+      static_cast<float*>(t.m_out)[i] = m;
+      static_cast<float*>(t.v_out)[i] = v;
+    }
+    if (in) {
+      if (kMaster) t.w_out[i] = x;
+      if (kPBf16)
+        static_cast<__nv_bfloat16*>(t.p_out)[i] =
+            __ushort_as_bfloat16(static_cast<unsigned short>(param_bits<kMaster>(x, (d + kSaltP) >> 16)));
+      else
+        static_cast<float*>(t.p_out)[i] = x;
+    }
+  }
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamTable tab) {
   for (uint32_t chunk = blockIdx.x; chunk < tab.chunks; chunk += gridDim.x) {
     int lo = 0, hi = tab.n - 1;  // the last tensor whose first chunk is not past this one
     while (lo < hi) {
@@ -105,61 +283,14 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
     }
     const AdamTensor& t = tab.t[lo];
     const int64_t i0 = static_cast<int64_t>(chunk - t.chunk0) * kChunk;
-    const int64_t end = t.n - i0 < kChunk ? t.n - i0 : kChunk;
-    for (int k = threadIdx.x; k < kChunk; k += kThreads) {
-      const bool in = k < end;
-      if (!__any_sync(0xffffffffu, in)) break;
-      const int64_t i = i0 + k, blk = i >> 5;
-      float g = 0.f, x = 0.f, m = 0.f, v = 0.f;
-      if (in) {
-        g = kGBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.g)[i])
-                   : static_cast<const float*>(t.g)[i];
-        x = kMaster ? t.w[i]
-            : kPBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.p)[i])
-                     : static_cast<const float*>(t.p)[i];
-        if (k8) {
-          m = decode_e4m3(static_cast<const uint8_t*>(t.m)[i]) * scale_value(t.ms[blk]);
-          v = decode_e4m3(static_cast<const uint8_t*>(t.v)[i]) * scale_value(t.vs[blk]);
-        } else {
-          m = static_cast<const float*>(t.m)[i];
-          v = static_cast<const float*>(t.v)[i];
-        }
-        update(c, t.keep, g, x, m, v);
-      }
-      const uint32_t i32 = static_cast<uint32_t>(i);
-      if (k8) {
-        const uint32_t em = block_scale(warp_amax(fabsf(m))), ev = block_scale(warp_amax(v));
-        const float ym = dither_e4m3(fabsf(m) * inv_scale_value(em), dither16(i32, c.dither));
-        float yv = dither_e4m3(v * inv_scale_value(ev), dither16(i32, c.dither + 0x55555555u));
-        const bool zero = warp_amax(v) == 0.f;
-        if (!zero) yv = fmaxf(yv, 0.001953125f);
-        if (in) {
-          static_cast<uint8_t*>(t.m_out)[i] = encode_e4m3(copysignf(ym, m));
-          static_cast<uint8_t*>(t.v_out)[i] = encode_e4m3(yv);
-          if ((k & 31) == 0) {
-            t.ms_out[blk] = static_cast<uint8_t>(em);
-            t.vs_out[blk] = static_cast<uint8_t>(ev);
-          }
-        }
-      } else if (in) {
-        static_cast<float*>(t.m_out)[i] = m;
-        static_cast<float*>(t.v_out)[i] = v;
-      }
-      if (in) {
-        if (kMaster) t.w_out[i] = x;
-        if (!kPBf16) {
-          static_cast<float*>(t.p_out)[i] = x;
-        } else if (kMaster || !(fabsf(x) < INFINITY)) {
-          static_cast<__nv_bfloat16*>(t.p_out)[i] = __float2bfloat16_rn(x);
-        } else {
-          const uint32_t b = __float_as_uint(x) + dither16(i32, c.dither + 0xAAAAAAAAu);
-          static_cast<__nv_bfloat16*>(t.p_out)[i] =
-              __ushort_as_bfloat16(static_cast<unsigned short>(b >> 16));
-        }
-      }
-    }
+    const int end = static_cast<int>(t.n - i0 < kChunk ? t.n - i0 : kChunk);
+    const int whole = t.on16 ? end & ~31 : 0;
+    pieces<KIND>(tab.c, t, i0, whole);
+    if (whole < end) singles<KIND>(tab.c, t, i0, whole, end);
   }
 }
+
+static_assert(sizeof(AdamTable) <= 32764, "kernel parameters");
 
 template <int KIND>
 cudaError_t launch_kind(const AdamTable& tab, int grid, cudaStream_t s) {
@@ -179,6 +310,12 @@ cudaError_t launch_adamw(AdamTensor* t, int n, int kind, const AdamConst& c, int
     tab.t[i] = t[i];
     tab.t[i].chunk0 = chunks;
     chunks += static_cast<uint32_t>((t[i].n + kChunk - 1) / kChunk);
+    uintptr_t low = 0;  // (codes are read by 8 bytes)
+    for (const void* p : {t[i].g, t[i].p, static_cast<const void*>(t[i].w), t[i].m, t[i].v,
+                          static_cast<const void*>(t[i].p_out), static_cast<const void*>(t[i].w_out),
+                          static_cast<const void*>(t[i].m_out), static_cast<const void*>(t[i].v_out)})
+      low |= reinterpret_cast<uintptr_t>(p);
+    tab.t[i].on16 = low % 16 == 0;
   }
   tab.chunks = chunks;
   const int grid = static_cast<int>(chunks < 8u * sms ? chunks : 8u * sms);

@@ -207,6 +207,7 @@ struct AdamTensor {
   int64_t n;
   float keep;       // 1 - lr * weight_decay
   uint32_t chunk0;  // first work chunk of this tensor
+  uint32_t on16;    // every buffer starts on a 16-byte boundary
 };
 struct AdamConst {
   float beta1, one_m_beta1, beta2, one_m_beta2;
@@ -216,8 +217,8 @@ struct AdamConst {
   uint32_t dither;  // t * 0xC13FA9A9 mod 2^32
 };
 enum AdamKind : int { ADAM_P_BF16 = 1, ADAM_G_BF16 = 2, ADAM_MASTER = 4, ADAM_BITS8 = 8 };
-constexpr int kAdamMaxTensors = 256;  // of one launch (its table is a kernel parameter)
-// `t[0..n)` share `kind`; chunk0 is filled in here.
+constexpr int kAdamMaxTensors = 248;  // of one launch (its table is a kernel parameter)
+// `t[0..n)` share `kind`; chunk0 and on16 are filled in here.
 cudaError_t launch_adamw(AdamTensor* t, int n, int kind, const AdamConst& c, int sms,
                          cudaStream_t s);
 

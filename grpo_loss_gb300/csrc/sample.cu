@@ -41,6 +41,7 @@ constexpr int kBins = 1280;                    // (five a thread at most) 1/32 o
 constexpr int kCap = 1024;                     // candidates that one CTA sorts
 constexpr int kCount = 256;                    // and those that it sorts by counting
 constexpr int kMaxSliceBytes = 192 * 1024;     // of a row's slice kept in shared memory
+constexpr int kMaxFast = 1 << 19;              // elements of a slice that the bins' sums can take
 constexpr float kCut = -40.f;                  // binary orders below the top that weigh nothing
 
 // 2^(j/32), j = 0..31, each as the sum of two floats.
@@ -283,6 +284,8 @@ struct Row {
   int64_t V;
   int lane, warp, nt, nw, C, rank, turn = 0, par = 0;  // nt threads, nw warps
   int v0, v1;          // this warp's pieces
+  float hist_bits;     // of a bin's mass: no sum of them passes 2^32
+  int full0, full1;    // pieces that lie inside the row
 
   __device__ __forceinline__ Row(Shared& s) : sh(s) {}
 
@@ -290,10 +293,10 @@ struct Row {
   // elements, or none: these are read one by one, with -inf in their place.
   __device__ __forceinline__ Vec<T> fetch(int v) const {
     Vec<T> x;
-    const int64_t i0 = pos0 + static_cast<int64_t>(v) * VE;
-    if (i0 >= 0 && i0 + VE <= V) {
+    if (v >= full0 && v < full1) {
       x.raw = __ldg(global + v);
     } else {
+      const int64_t i0 = pos0 + static_cast<int64_t>(v) * VE;
       uint32_t w[4];
       T* e = reinterpret_cast<T*>(w);
 #pragma unroll
@@ -635,8 +638,8 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
           const float y = fast_y(w, z);
           const int b = min(Row<T>::bin_of(y), kBins - 1);
           atomicAdd(&sh.hist[b].x, 1u);
-          // the weight over the bin's own: 15 bits
-          if (!use_k) atomicAdd(&sh.hist[b].y, __float2uint_rn(32768.f * ex2_approx(y + 0.03125f * b)));
+          // the weight over the bin's own: 13 bits or more
+          if (!use_k) atomicAdd(&sh.hist[b].y, __float2uint_rn(ex2_approx(y + 0.03125f * b + r.hist_bits)));
         });
         r.cl.sync();
         // Running sums: this CTA adds up its share of the bins over the slices,
@@ -657,7 +660,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
               n[i] += h.x;
               mm += h.y;
             }
-            m[i] = static_cast<float>(mm) * ex2_approx(-15.f - 0.03125f * b);
+            m[i] = static_cast<float>(mm) * ex2_approx(-r.hist_bits - 0.03125f * b);
           }
           n_c += n[i];
           n_m += m[i];
@@ -679,7 +682,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         r.template join<P_COUNT | P_SUM>(q, nullptr, &ahead);
         n_at += ahead.count - n_c;
         m_at += ahead.sum - n_m;
-        // the masses here are 2^-16 off for their 15 bits, and 2^-20 for the rest
+        // the masses here are 2^-14 off for their 13 bits, and 2^-20 for the rest
         const float need = sh.top_p * mass2;
         // the first bin that may reach the mass; the first that does, and the count up to it
         q.lo = kBins - 1;
@@ -691,8 +694,8 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
           m_at += m[i];
           if (i >= per || j >= share || first + j > b_cut) continue;
           const uint32_t b = first + j;
-          const bool may = use_k ? n_at >= static_cast<uint32_t>(sh.top_k) : m_at * (1.f + 6e-5f) >= need;
-          const bool does = use_k ? may : m_at * (1.f - 6e-5f) > need;
+          const bool may = use_k ? n_at >= static_cast<uint32_t>(sh.top_k) : m_at * (1.f + 8e-5f) >= need;
+          const bool does = use_k ? may : m_at * (1.f - 8e-5f) > need;
           if (may) q.lo = min(q.lo, b);
           if (does) q.best = min(q.best, (static_cast<uint64_t>(b) << 32) | n_at);
         }
@@ -1041,6 +1044,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
   r.C = static_cast<int>(r.cl.num_blocks());
   r.rank = static_cast<int>(r.cl.block_rank());
   r.V = a.V;
+  r.hist_bits = slice_vecs * VE <= 131072 ? 15.f : 13.f;
   r.parts = reinterpret_cast<Part*>(s_slice + (resident ? slice_vecs : 0));
   if (threadIdx.x < 32) sh.tab[threadIdx.x] = c_exp2_32[threadIdx.x];
   const int n_cl = gridDim.x / r.C;
@@ -1055,6 +1059,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
     const int per = (r.n_vec + r.nw - 1) / r.nw;
     r.v0 = min(r.n_vec, r.warp * per);
     r.v1 = min(r.n_vec, r.v0 + per);
+    r.full0 = r.pos0 < 0 ? 1 : 0;
+    r.full1 = static_cast<int>(min(static_cast<int64_t>(r.n_vec), a.V > r.pos0 ? (a.V - r.pos0) / VE : 0));
     r.row = z;
     r.global = reinterpret_cast<const uint4*>(z - off) + p0;
     r.slice = resident ? s_slice : nullptr;
@@ -1073,9 +1079,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
     float mx = -INFINITY;
     {
       // the pieces that lie inside the row, four loads in flight a thread
-      const int f0 = max(r.v0, r.pos0 < 0 ? 1 : 0);
-      const int64_t whole = a.V - r.pos0 >= 0 ? (a.V - r.pos0) / VE : 0;
-      const int f1 = static_cast<int>(min(static_cast<int64_t>(r.v1), whole));
+      const int f0 = max(r.v0, r.full0), f1 = min(r.v1, r.full1);
       for (int v = f0 + r.lane; v < f1; v += 128) {
         Vec<T> x[4];
 #pragma unroll
@@ -1135,10 +1139,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
       sh.w.zmax = zmax;
       sh.floor_z = !sh.use_q ? -INFINITY : prm_q >= 1.f ? zmax : min_logit(sh.w, sh.temp, prm_q);
     }
-    if (!resident || zmax == INFINITY || !decide<T, false>(r, a, row, kmax, mx, true)) {
+    const bool fast = zmax < INFINITY && slice_vecs * VE <= kMaxFast;
+    if (!fast || !decide<T, false>(r, a, row, kmax, mx, true)) {
       // (the cluster's CTAs leave a row that was not decided at the same point)
       r.cl.sync();
-      r.turn = decide_exact<T>(r, a, row, kmax, mx, resident && zmax < INFINITY);
+      r.turn = decide_exact<T>(r, a, row, kmax, mx, fast);
     }
     r.par ^= 1;
   }
@@ -1149,8 +1154,6 @@ template <typename T>
 cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t s) {
   constexpr int VE = 16 / static_cast<int>(sizeof(T));
   const int64_t bytes = a.V * static_cast<int64_t>(sizeof(T)) + 15;
-  // The smallest cluster whose slices leave room for three CTAs on an SM, and
-  // with few rows a larger one, down to 8 KB a CTA, until every SM has one.
   int C = 1;
   while (C < kMaxCluster && (bytes / C > 52 * 1024 || (a.rows * C < sms && bytes / C > 16 * 1024))) C *= 2;
   const int64_t pieces = (a.V + VE - 1) / VE + 1;  // a row may start inside its first piece
