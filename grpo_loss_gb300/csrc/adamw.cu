@@ -7,6 +7,7 @@
 // gradients and states; 10 with bf16 gradients and 8-bit states).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+#include <stdlib.h>
 
 #include "internal.h"
 
@@ -33,8 +34,7 @@ constexpr uint32_t kDitherIndex = 0x91E10DA5u, kSaltV = 0x55555555u, kSaltP = 0x
 // Largest power-of-two byte E with amax * 2^(127 - E) <= 448 = 1.75 * 2^8:
 // adding 0x1FFFFF to the bits carries into the exponent when the significand
 // is above 1.75. 255 marks infinities and NaN.
-__device__ __forceinline__ uint32_t block_scale(float amax) {
-  const uint32_t b = __float_as_uint(amax);
+__device__ __forceinline__ uint32_t block_scale(uint32_t b) {
   if (b >= 0x7F800000u) return 255u;
   const int e = static_cast<int>((b + 0x1FFFFFu) >> 23) - 8;
   return e < 0 ? 0u : static_cast<uint32_t>(e);
@@ -53,58 +53,46 @@ __device__ __forceinline__ float inv_scale_value(uint32_t e) {
 // bits, so the dither is added to the 20 bits below it; under 2^-6, where the
 // step is 2^-9 throughout, y is first moved to [2^-6, 2^-5), whose significand
 // step is the same.
-__device__ __forceinline__ float dither_e4m3(float y, uint32_t d) {
+__device__ __forceinline__ float dither_e4m3(float y, uint32_t d) {  // the dither: d's high 16 bits
   const float base = y < 0.015625f ? 0.015625f : 0.f;
-  const uint32_t b = __float_as_uint(y + base) + (d << 4);
+  const uint32_t b = __float_as_uint(y + base) + ((d >> 12) & 0xFFFF0u);
   return __uint_as_float(b & 0xFFF00000u) - base;
-}
-
-// Maximum over the warp that keeps a NaN.
-__device__ __forceinline__ float warp_amax(float a) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    const float b = __shfl_xor_sync(0xffffffffu, a, o);
-    a = (a != a || a > b) ? a : b;
-  }
-  return a;
 }
 
 // The update of one element. Roundings are spelled out, so that every inlined
 // copy gives the same bits and a tensor's result does not depend on its place
-// in a table.
+// in a table. The root and the quotient are the special-function unit's, some
+// 2^-22 off together: of the update, not of the parameter.
 __device__ __forceinline__ void update(const AdamConst& c, float keep, float g, float& x, float& m,
                                        float& v) {
   g = __fmul_rn(g, c.grad_scale);
   m = __fmaf_rn(c.beta1, m, __fmul_rn(c.one_m_beta1, g));
   v = __fmaf_rn(c.beta2, v, __fmul_rn(__fmul_rn(c.one_m_beta2, g), g));
-  const float den = __fmaf_rn(__fsqrt_rn(v), c.rsqrt_c2, c.eps);
-  x = __fmaf_rn(-c.lr_t, __fdiv_rn(m, den), __fmul_rn(x, keep));
+  float root;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
+  const float den = __fmaf_rn(root, c.rsqrt_c2, c.eps);
+  x = __fmaf_rn(-c.lr_t, __fdividef(m, den), __fmul_rn(x, keep));
 }
 
-// Eight consecutive elements of a buffer, as 16-byte accesses.
+// Four consecutive elements of a buffer in one access: a warp's accesses are
+// whole 128-byte lines for every type. (Eight a thread, as two 16-byte loads for
+// float32, reach each line twice: 1179 instead of 1050 us on 233 M elements
+// with masters.)
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+__device__ __forceinline__ void load4(const void* p, int64_t i, float (&v)[4]) {
   if (BF16) {
-    const uint4 r = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float((e & 1) ? (w[e / 2] & 0xFFFF0000u) : (w[e / 2] << 16));
+    const uint2 r = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i));
+    v[0] = __uint_as_float(r.x << 16);
+    v[1] = __uint_as_float(r.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(r.y << 16);
+    v[3] = __uint_as_float(r.y & 0xFFFF0000u);
   } else {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = __ldcs(q), b = __ldcs(q + 1);
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
 }
-__device__ __forceinline__ void store8(float* p, int64_t i, const float (&v)[8]) {
-  float4* q = reinterpret_cast<float4*>(p + i);
-  __stcs(q, make_float4(v[0], v[1], v[2], v[3]));
-  __stcs(q + 1, make_float4(v[4], v[5], v[6], v[7]));
-}
-// bf16 bit patterns in the low halves
-__device__ __forceinline__ void store8(__nv_bfloat16* p, int64_t i, const uint32_t (&v)[8]) {
-  __stcs(reinterpret_cast<uint4*>(p + i), make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16,
-                                                     v[4] | v[5] << 16, v[6] | v[7] << 16));
+__device__ __forceinline__ void store4(float* p, int64_t i, const float (&v)[4]) {
+  __stcs(reinterpret_cast<float4*>(p + i), make_float4(v[0], v[1], v[2], v[3]));
 }
 // Decodes or encodes a pair of e4m3 codes.
 __device__ __forceinline__ float2 decode2(uint32_t c) {
@@ -114,102 +102,113 @@ __device__ __forceinline__ float2 decode2(uint32_t c) {
 __device__ __forceinline__ uint32_t encode2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ void decode8(const void* p, int64_t i, float scale, float (&v)[8]) {
-  const uint2 r = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + i));
-#pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    const float2 f = decode2(((e < 4 ? r.x : r.y) >> (8 * (e & 3))) & 0xFFFFu);
-    v[e] = f.x * scale;
-    v[e + 1] = f.y * scale;
-  }
-}
-__device__ __forceinline__ void encode8(void* p, int64_t i, const float (&v)[8]) {
-  uint2 r;
-  r.x = encode2(v[0], v[1]) | encode2(v[2], v[3]) << 16;
-  r.y = encode2(v[4], v[5]) | encode2(v[6], v[7]) << 16;
-  __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + i), r);
-}
-// max(a, b) that keeps a NaN
-__device__ __forceinline__ float amax(float a, float b) { return (a != a || a > b) ? a : b; }
-// over the four threads of a block of 32
-__device__ __forceinline__ float quad_amax(float a) {
-  a = amax(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  return amax(a, __shfl_xor_sync(0xffffffffu, a, 2));
-}
 // bf16 bits of x: to nearest beside a master, else dithered
 template <bool NEAREST>
 __device__ __forceinline__ uint32_t param_bits(float x, uint32_t d) {
   if (NEAREST || !(fabsf(x) < INFINITY)) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
   return (__float_as_uint(x) + d) >> 16;
 }
+// Magnitude bits: they order like the magnitudes, infinities and NaN above all.
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// Whole pieces of eight elements of a chunk at element i0, `end` of them in all
-// (a multiple of 8; every buffer on a 16-byte boundary). With 8-bit states four
-// threads hold a block of 32.
+// Whole pieces of four elements of a chunk at element i0, `end` of them in all
+// (a multiple of 32; every buffer on a 16-byte boundary). With 8-bit states
+// eight threads hold a block of 32.
 template <int KIND>
 __device__ __forceinline__ void pieces(const AdamConst& c, const AdamTensor& t, int64_t i0, int end) {
   constexpr bool kPBf16 = (KIND & ADAM_P_BF16) != 0, kGBf16 = (KIND & ADAM_G_BF16) != 0;
   constexpr bool kMaster = (KIND & ADAM_MASTER) != 0, k8 = (KIND & ADAM_BITS8) != 0;
-  for (int k = threadIdx.x * 8; k < kChunk; k += kThreads * 8) {
-    const bool in = k < end;
-    if (k8 ? !__any_sync(0xffffffffu, in) : !in) break;
-    const int64_t i = i0 + k, blk = i >> 5;
-    float g[8], x[8], m[8], v[8];
+  constexpr int U = 2;  // pieces whose loads are in flight together
+  for (int k0 = threadIdx.x * 4; k0 < kChunk; k0 += kThreads * 4 * U) {
+    float g[U][4], x[U][4], m[U][4], v[U][4];
+    uint32_t cm[U], cv[U], sm[U], sv[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = x[e] = m[e] = v[e] = 0.f;
-    if (in) {
-      load8<kGBf16>(t.g, i, g);
-      load8<kPBf16 && !kMaster>(kMaster ? t.w : t.p, i, x);
-      if (k8) {
-        decode8(t.m, i, scale_value(t.ms[blk]), m);
-        decode8(t.v, i, scale_value(t.vs[blk]), v);
+    for (int j = 0; j < U; ++j) {
+      const int k = k0 + j * kThreads * 4;
+      const int64_t i = i0 + k;
+      cm[j] = cv[j] = sm[j] = sv[j] = 0;
+      if (k < end) {
+        load4<kGBf16>(t.g, i, g[j]);
+        load4<kPBf16 && !kMaster>(kMaster ? t.w : t.p, i, x[j]);
+        if (k8) {
+          cm[j] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i));
+          cv[j] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i));
+          sm[j] = t.ms[i >> 5];
+          sv[j] = t.vs[i >> 5];
+        } else {
+          load4<false>(t.m, i, m[j]);
+          load4<false>(t.v, i, v[j]);
+        }
       } else {
-        load8<false>(t.m, i, m);
-        load8<false>(t.v, i, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[j][e] = x[j][e] = m[j][e] = v[j][e] = 0.f;
       }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) update(c, t.keep, g[e], x[e], m[e], v[e]);
-    const uint32_t d0 = static_cast<uint32_t>(i) * kDitherIndex + c.dither;  // of element i, unshifted
-    if (k8) {
-      float am = 0.f, av = 0.f;
+    for (int j = 0; j < U; ++j) {
+      const int k = k0 + j * kThreads * 4;
+      const int64_t i = i0 + k;
+      const bool in = k < end;
+      // (a block's eight threads are in or out together)
+      if (!in) continue;
+      if (k8) {
+        const float a = scale_value(sm[j]), b = scale_value(sv[j]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        am = amax(am, fabsf(m[e]));
-        av = amax(av, v[e]);
-      }
-      am = quad_amax(am);
-      av = quad_amax(av);
-      const uint32_t em = block_scale(am), ev = block_scale(av);
-      const float im = inv_scale_value(em), iv = inv_scale_value(ev);
-      const float least = av == 0.f ? 0.f : 0.001953125f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t d = d0 + e * kDitherIndex;
-        m[e] = copysignf(dither_e4m3(fabsf(m[e]) * im, d >> 16), m[e]);
-        v[e] = fmaxf(dither_e4m3(v[e] * iv, (d + kSaltV) >> 16), least);
-      }
-      if (in) {
-        encode8(t.m_out, i, m);
-        encode8(t.v_out, i, v);
-        if ((k & 31) == 0) {
-          t.ms_out[blk] = static_cast<uint8_t>(em);
-          t.vs_out[blk] = static_cast<uint8_t>(ev);
+        for (int e = 0; e < 4; e += 2) {
+          const float2 p = decode2(cm[j] >> (8 * e)), q = decode2(cv[j] >> (8 * e));
+          m[j][e] = p.x * a;
+          m[j][e + 1] = p.y * a;
+          v[j][e] = q.x * b;
+          v[j][e + 1] = q.y * b;
         }
       }
-    } else {
-      store8(static_cast<float*>(t.m_out), i, m);
-      store8(static_cast<float*>(t.v_out), i, v);
-    }
-    if (in) {
-      if (kMaster) store8(t.w_out, i, x);
-      if (kPBf16) {
-        uint32_t b[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) b[e] = param_bits<kMaster>(x[e], (d0 + e * kDitherIndex + kSaltP) >> 16);
-        store8(static_cast<__nv_bfloat16*>(t.p_out), i, b);
+      for (int e = 0; e < 4; ++e) update(c, t.keep, g[j][e], x[j][e], m[j][e], v[j][e]);
+      const uint32_t d0 = static_cast<uint32_t>(i) * kDitherIndex + c.dither;  // of element i, unshifted
+      if (k8) {
+        uint32_t am = 0, av = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          am = max(am, magnitude(m[j][e]));
+          av = max(av, magnitude(v[j][e]));
+        }
+        const uint32_t who = 0xFFu << (threadIdx.x & 24);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          am = max(am, __shfl_xor_sync(who, am, o));
+          av = max(av, __shfl_xor_sync(who, av, o));
+        }
+        const uint32_t em = block_scale(am), ev = block_scale(av);
+        const float im = inv_scale_value(em), iv = inv_scale_value(ev);
+        const float least = av == 0 ? 0.f : 0.001953125f;
+        float ym[4], yv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t d = d0 + e * kDitherIndex;
+          ym[e] = copysignf(dither_e4m3(fabsf(m[j][e]) * im, d), m[j][e]);
+          yv[e] = fmaxf(dither_e4m3(v[j][e] * iv, d + kSaltV), least);
+        }
+        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m_out) + i),
+               encode2(ym[0], ym[1]) | encode2(ym[2], ym[3]) << 16);
+        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v_out) + i),
+               encode2(yv[0], yv[1]) | encode2(yv[2], yv[3]) << 16);
+        if ((k & 31) == 0) {
+          t.ms_out[i >> 5] = static_cast<uint8_t>(em);
+          t.vs_out[i >> 5] = static_cast<uint8_t>(ev);
+        }
       } else {
-        store8(static_cast<float*>(t.p_out), i, x);
+        store4(static_cast<float*>(t.m_out), i, m[j]);
+        store4(static_cast<float*>(t.v_out), i, v[j]);
+      }
+      if (kMaster) store4(t.w_out, i, x[j]);
+      if (kPBf16) {
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = param_bits<kMaster>(x[j][e], (d0 + e * kDitherIndex + kSaltP) >> 16);
+        __stcs(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(t.p_out) + i),
+               make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16));
+      } else {
+        store4(static_cast<float*>(t.p_out), i, x[j]);
       }
     }
   }
@@ -222,7 +221,7 @@ __device__ __forceinline__ void singles(const AdamConst& c, const AdamTensor& t,
                                         int end) {
   constexpr bool kPBf16 = (KIND & ADAM_P_BF16) != 0, kGBf16 = (KIND & ADAM_G_BF16) != 0;
   constexpr bool kMaster = (KIND & ADAM_MASTER) != 0, k8 = (KIND & ADAM_BITS8) != 0;
-  for (int k = first + threadIdx.x; k < kChunk; k += kThreads) {
+  for (int k = first + threadIdx.x; k < kChunk; k += kThreads) {  // (first is a multiple of 32)
     const bool in = k < end;
     if (!__any_sync(0xffffffffu, in)) break;
     const int64_t i = i0 + k, blk = i >> 5;
@@ -244,11 +243,10 @@ __device__ __forceinline__ void singles(const AdamConst& c, const AdamTensor& t,
     }
     const uint32_t d = static_cast<uint32_t>(i) * kDitherIndex + c.dither;
     if (k8) {
-      const float av = warp_amax(v);
-      const uint32_t em = block_scale(warp_amax(fabsf(m))), ev = block_scale(av);
-      const float ym = dither_e4m3(fabsf(m) * inv_scale_value(em), d >> 16);
-      const float yv = fmaxf(dither_e4m3(v * inv_scale_value(ev), (d + kSaltV) >> 16),
-                             av == 0.f ? 0.f : 0.001953125f);
+      const uint32_t av = __reduce_max_sync(0xffffffffu, magnitude(v));
+      const uint32_t em = block_scale(__reduce_max_sync(0xffffffffu, magnitude(m))), ev = block_scale(av);
+      const float ym = dither_e4m3(fabsf(m) * inv_scale_value(em), d);
+      const float yv = fmaxf(dither_e4m3(v * inv_scale_value(ev), d + kSaltV), av == 0 ? 0.f : 0.001953125f);
       if (in) {
         static_cast<uint8_t*>(t.m_out)[i] = static_cast<uint8_t>(encode2(copysignf(ym, m), 0.f));
         static_cast<uint8_t*>(t.v_out)[i] = static_cast<uint8_t>(encode2(yv, 0.f));
@@ -310,7 +308,7 @@ cudaError_t launch_adamw(AdamTensor* t, int n, int kind, const AdamConst& c, int
     tab.t[i] = t[i];
     tab.t[i].chunk0 = chunks;
     chunks += static_cast<uint32_t>((t[i].n + kChunk - 1) / kChunk);
-    uintptr_t low = 0;  // (codes are read by 8 bytes)
+    uintptr_t low = 0;  // (narrower types need less)
     for (const void* p : {t[i].g, t[i].p, static_cast<const void*>(t[i].w), t[i].m, t[i].v,
                           static_cast<const void*>(t[i].p_out), static_cast<const void*>(t[i].w_out),
                           static_cast<const void*>(t[i].m_out), static_cast<const void*>(t[i].v_out)})
@@ -318,7 +316,8 @@ cudaError_t launch_adamw(AdamTensor* t, int n, int kind, const AdamConst& c, int
     tab.t[i].on16 = low % 16 == 0;
   }
   tab.chunks = chunks;
-  const int grid = static_cast<int>(chunks < 8u * sms ? chunks : 8u * sms);
+  const char* ev = getenv("AG"); const unsigned gm = ev ? atoi(ev) : 0;
+  const int grid = static_cast<int>(!gm || chunks < gm * sms ? chunks : gm * sms);
   switch (kind) {
 #define ADAM_CASE(k) case k: return launch_kind<k>(tab, grid, s);
     ADAM_CASE(0)

@@ -184,7 +184,7 @@ struct NormArgs {
   float* dbias;
   float* partial;  // [parts][2][d] partial column sums
 };
-int norm_parts(const NormArgs& a, int sms);  // row groups of the backward's partial column sums
+int norm_parts(const NormArgs& a, int sms);  // rows of partial column sums in the workspace
 cudaError_t launch_norm_fwd(const NormArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_norm_colsum(const NormArgs& a, int sms, cudaStream_t s);
