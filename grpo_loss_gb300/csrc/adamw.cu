@@ -70,29 +70,46 @@ __device__ __forceinline__ void update(const AdamConst& c, float keep, float g, 
   v = __fmaf_rn(c.beta2, v, __fmul_rn(__fmul_rn(c.one_m_beta2, g), g));
   float root;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
+  // (the root of a float is at least 2^-75: with eps = 0, too, den is normal or 0)
   const float den = __fmaf_rn(root, c.rsqrt_c2, c.eps);
-  x = __fmaf_rn(-c.lr_t, __fdividef(m, den), __fmul_rn(x, keep));
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(den));
+  x = __fmaf_rn(-c.lr_t, __fmul_rn(m, inv), __fmul_rn(x, keep));
 }
 
-// Four consecutive elements of a buffer in one access: a warp's accesses are
-// whole 128-byte lines for every type. (Eight a thread, as two 16-byte loads for
-// float32, reach each line twice: 1179 instead of 1050 us on 233 M elements
-// with masters.)
-template <bool BF16>
-__device__ __forceinline__ void load4(const void* p, int64_t i, float (&v)[4]) {
-  if (BF16) {
-    const uint2 r = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i));
-    v[0] = __uint_as_float(r.x << 16);
-    v[1] = __uint_as_float(r.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(r.y << 16);
-    v[3] = __uint_as_float(r.y & 0xFFFF0000u);
+// W consecutive elements of a buffer, W = 4 or 8. With float32 states a thread
+// takes four: a warp's accesses are then whole 128-byte lines for every type.
+// (Eight, as two 16-byte accesses, reach each line twice: 1179 instead of 998 us
+// on 233 M elements with masters.) With 8-bit states, where the instructions of
+// a piece weigh more than its bytes, it takes eight.
+template <bool BF16, int W>
+__device__ __forceinline__ void load(const void* p, int k, float (&v)[W]) {
+  if constexpr (BF16) {
+    uint32_t w[W / 2];
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p) + k;
+    if constexpr (W == 8) {
+      const uint4 r = __ldcs(reinterpret_cast<const uint4*>(q));
+      w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
+    } else {
+      const uint2 r = __ldcs(reinterpret_cast<const uint2*>(q));
+      w[0] = r.x, w[1] = r.y;
+    }
+#pragma unroll
+    for (int e = 0; e < W; ++e) v[e] = __uint_as_float((e & 1) ? (w[e / 2] & 0xFFFF0000u) : (w[e / 2] << 16));
   } else {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + k);
+#pragma unroll
+    for (int f = 0; f < W / 4; ++f) {
+      const float4 a = W == 4 ? __ldcs(q) : __ldg(q + f);
+      v[4 * f] = a.x, v[4 * f + 1] = a.y, v[4 * f + 2] = a.z, v[4 * f + 3] = a.w;
+    }
   }
 }
-__device__ __forceinline__ void store4(float* p, int64_t i, const float (&v)[4]) {
-  __stcs(reinterpret_cast<float4*>(p + i), make_float4(v[0], v[1], v[2], v[3]));
+template <int W>
+__device__ __forceinline__ void store(void* p, int k, const float (&v)[W]) {
+  float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + k);
+#pragma unroll
+  for (int f = 0; f < W / 4; ++f) __stcs(q + f, make_float4(v[4 * f], v[4 * f + 1], v[4 * f + 2], v[4 * f + 3]));
 }
 // Decodes or encodes a pair of e4m3 codes.
 __device__ __forceinline__ float2 decode2(uint32_t c) {
@@ -111,51 +128,57 @@ __device__ __forceinline__ uint32_t param_bits(float x, uint32_t d) {
 // Magnitude bits: they order like the magnitudes, infinities and NaN above all.
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// Whole pieces of four elements of a chunk at element i0, `end` of them in all
-// (a multiple of 32; every buffer on a 16-byte boundary). With 8-bit states
-// eight threads hold a block of 32.
+// Whole pieces of W elements of a chunk that starts at element i0, `end` elements
+// in all (a multiple of 32; every buffer on a 16-byte boundary). With 8-bit
+// states four threads hold a block of 32.
 template <int KIND>
 __device__ __forceinline__ void pieces(const AdamConst& c, const AdamTensor& t, int64_t i0, int end) {
   constexpr bool kPBf16 = (KIND & ADAM_P_BF16) != 0, kGBf16 = (KIND & ADAM_G_BF16) != 0;
   constexpr bool kMaster = (KIND & ADAM_MASTER) != 0, k8 = (KIND & ADAM_BITS8) != 0;
-  constexpr int U = 2;  // pieces whose loads are in flight together
-  for (int k0 = threadIdx.x * 4; k0 < kChunk; k0 += kThreads * 4 * U) {
-    float g[U][4], x[U][4], m[U][4], v[U][4];
-    uint32_t cm[U], cv[U], sm[U], sv[U];
+  constexpr int W = k8 ? 8 : 4, U = k8 ? 1 : 2;  // U pieces' loads are in flight together
+  // the chunk's own pointers: elements of it have 32-bit offsets
+  auto at = [&](const void* p, int size) { return static_cast<const char*>(p) + i0 * size; };
+  auto to = [&](void* p, int size) { return static_cast<char*>(p) + i0 * size; };
+  constexpr int kSS = k8 ? 1 : 4;
+  const char* const g_in = at(t.g, kGBf16 ? 2 : 4);
+  const char* const x_in = kMaster ? at(t.w, 4) : at(t.p, kPBf16 ? 2 : 4);
+  const char* const m_in = at(t.m, kSS);
+  const char* const v_in = at(t.v, kSS);
+  char* const m_to = to(t.m_out, kSS);
+  char* const v_to = to(t.v_out, kSS);
+  char* const p_to = to(t.p_out, kPBf16 ? 2 : 4);
+  const float keep = t.keep;
+  for (int k0 = threadIdx.x * W; k0 < end; k0 += kThreads * W * U) {
+    float g[U][W], x[U][W], m[U][W], v[U][W];
+    uint2 cm, cv;
+    uint32_t sm = 0, sv = 0;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int k = k0 + j * kThreads * 4;
-      const int64_t i = i0 + k;
-      cm[j] = cv[j] = sm[j] = sv[j] = 0;
+      const int k = k0 + j * kThreads * W;
       if (k < end) {
-        load4<kGBf16>(t.g, i, g[j]);
-        load4<kPBf16 && !kMaster>(kMaster ? t.w : t.p, i, x[j]);
-        if (k8) {
-          cm[j] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i));
-          cv[j] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i));
-          sm[j] = t.ms[i >> 5];
-          sv[j] = t.vs[i >> 5];
+        load<kGBf16, W>(g_in, k, g[j]);
+        load<kPBf16 && !kMaster, W>(x_in, k, x[j]);
+        if constexpr (k8) {
+          cm = __ldcs(reinterpret_cast<const uint2*>(m_in + k));
+          cv = __ldcs(reinterpret_cast<const uint2*>(v_in + k));
+          sm = t.ms[(i0 + k) >> 5];
+          sv = t.vs[(i0 + k) >> 5];
         } else {
-          load4<false>(t.m, i, m[j]);
-          load4<false>(t.v, i, v[j]);
+          load<false, W>(m_in, k, m[j]);
+          load<false, W>(v_in, k, v[j]);
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) g[j][e] = x[j][e] = m[j][e] = v[j][e] = 0.f;
       }
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int k = k0 + j * kThreads * 4;
-      const int64_t i = i0 + k;
-      const bool in = k < end;
-      // (a block's eight threads are in or out together)
-      if (!in) continue;
-      if (k8) {
-        const float a = scale_value(sm[j]), b = scale_value(sv[j]);
+      const int k = k0 + j * kThreads * W;
+      if (k >= end) break;  // (a block's threads are in or out together)
+      if constexpr (k8) {
+        const float a = scale_value(sm), b = scale_value(sv);
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const float2 p = decode2(cm[j] >> (8 * e)), q = decode2(cv[j] >> (8 * e));
+        for (int e = 0; e < W; e += 2) {
+          const float2 p = decode2((e < 4 ? cm.x : cm.y) >> (8 * (e & 3)));
+          const float2 q = decode2((e < 4 ? cv.x : cv.y) >> (8 * (e & 3)));
           m[j][e] = p.x * a;
           m[j][e + 1] = p.y * a;
           v[j][e] = q.x * b;
@@ -163,52 +186,57 @@ __device__ __forceinline__ void pieces(const AdamConst& c, const AdamTensor& t, 
         }
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) update(c, t.keep, g[j][e], x[j][e], m[j][e], v[j][e]);
-      const uint32_t d0 = static_cast<uint32_t>(i) * kDitherIndex + c.dither;  // of element i, unshifted
-      if (k8) {
-        uint32_t am = 0, av = 0;
+      for (int e = 0; e < W; ++e) update(c, keep, g[j][e], x[j][e], m[j][e], v[j][e]);
+      const uint32_t d0 = static_cast<uint32_t>(i0 + k) * kDitherIndex + c.dither;  // of the first element
+      if constexpr (k8) {
+        uint32_t am = 0, av = 0;  // (v has no sign; a NaN's would leave it the largest)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < W; ++e) {
           am = max(am, magnitude(m[j][e]));
-          av = max(av, magnitude(v[j][e]));
+          av = max(av, __float_as_uint(v[j][e]));
         }
-        const uint32_t who = 0xFFu << (threadIdx.x & 24);
+        const uint32_t who = 0xFu << (threadIdx.x & 28);
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
+        for (int o = 1; o < 4; o <<= 1) {
           am = max(am, __shfl_xor_sync(who, am, o));
           av = max(av, __shfl_xor_sync(who, av, o));
         }
         const uint32_t em = block_scale(am), ev = block_scale(av);
         const float im = inv_scale_value(em), iv = inv_scale_value(ev);
         const float least = av == 0 ? 0.f : 0.001953125f;
-        float ym[4], yv[4];
+        float ym[W], yv[W];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < W; ++e) {
           const uint32_t d = d0 + e * kDitherIndex;
           ym[e] = copysignf(dither_e4m3(fabsf(m[j][e]) * im, d), m[j][e]);
           yv[e] = fmaxf(dither_e4m3(v[j][e] * iv, d + kSaltV), least);
         }
-        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m_out) + i),
-               encode2(ym[0], ym[1]) | encode2(ym[2], ym[3]) << 16);
-        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v_out) + i),
-               encode2(yv[0], yv[1]) | encode2(yv[2], yv[3]) << 16);
+        __stcs(reinterpret_cast<uint2*>(m_to + k), make_uint2(encode2(ym[0], ym[1]) | encode2(ym[2], ym[3]) << 16,
+                                                              encode2(ym[4], ym[5]) | encode2(ym[6], ym[7]) << 16));
+        __stcs(reinterpret_cast<uint2*>(v_to + k), make_uint2(encode2(yv[0], yv[1]) | encode2(yv[2], yv[3]) << 16,
+                                                              encode2(yv[4], yv[5]) | encode2(yv[6], yv[7]) << 16));
         if ((k & 31) == 0) {
-          t.ms_out[i >> 5] = static_cast<uint8_t>(em);
-          t.vs_out[i >> 5] = static_cast<uint8_t>(ev);
+          t.ms_out[(i0 + k) >> 5] = static_cast<uint8_t>(em);
+          t.vs_out[(i0 + k) >> 5] = static_cast<uint8_t>(ev);
         }
       } else {
-        store4(static_cast<float*>(t.m_out), i, m[j]);
-        store4(static_cast<float*>(t.v_out), i, v[j]);
+        store<W>(m_to, k, m[j]);
+        store<W>(v_to, k, v[j]);
       }
-      if (kMaster) store4(t.w_out, i, x[j]);
-      if (kPBf16) {
-        uint32_t b[4];
+      if constexpr (kMaster) store<W>(to(t.w_out, 4), k, x[j]);
+      if constexpr (kPBf16) {
+        uint32_t b[W / 2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = param_bits<kMaster>(x[j][e], (d0 + e * kDitherIndex + kSaltP) >> 16);
-        __stcs(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(t.p_out) + i),
-               make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16));
+        for (int e = 0; e < W; e += 2) {
+          const uint32_t d = d0 + e * kDitherIndex + kSaltP;
+          b[e / 2] = param_bits<kMaster>(x[j][e], d >> 16) |
+                     param_bits<kMaster>(x[j][e + 1], (d + kDitherIndex) >> 16) << 16;
+        }
+        __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(p_to) + k;
+        if constexpr (W == 8) __stcs(reinterpret_cast<uint4*>(q), make_uint4(b[0], b[1], b[2], b[3]));
+        else __stcs(reinterpret_cast<uint2*>(q), make_uint2(b[0], b[1]));
       } else {
-        store4(static_cast<float*>(t.p_out), i, x[j]);
+        store<W>(p_to, k, x[j]);
       }
     }
   }

@@ -111,6 +111,33 @@ template <typename T, int N>
 __device__ __forceinline__ void store_piece(T* p, const Piece<T, N>& v) {
   *reinterpret_cast<Piece<T, N>*>(p) = v;
 }
+// Pairs of floats in one register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 of_pair(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // N weights (or biases) from element i on; their type is the same for a launch.
 template <int N>
 __device__ __forceinline__ void load_params(const void* p, int bf16, int i, float* v) {
@@ -146,14 +173,18 @@ __device__ __forceinline__ float2 group_sum(float a, float b, float2* part, int 
   if (G == 32) return make_float2(a, b);
   const int warp = threadIdx.x >> 5, first = warp / (G / 32) * (G / 32);
   float2* mine = part + slot * 32;
-  if ((threadIdx.x & 31) == 0) mine[warp] = make_float2(a, b);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) mine[warp] = make_float2(a, b);
   __syncthreads();
-  a = b = 0.f;
+  // each lane takes one warp's sums
+  constexpr int W = G / 32, P = W <= 2 ? 2 : W <= 4 ? 4 : W <= 8 ? 8 : W <= 16 ? 16 : 32;
+  const float2 p = (lane & (P - 1)) < W ? mine[first + (lane & (P - 1))] : make_float2(0.f, 0.f);
+  a = p.x;
+  b = p.y;
 #pragma unroll
-  for (int w = 0; w < G / 32; ++w) {
-    const float2 p = mine[first + w];
-    a += p.x;
-    if (BOTH) b += p.y;
+  for (int o = P / 2; o >= 1; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (BOTH) b += __shfl_xor_sync(0xffffffffu, b, o);
   }
   return make_float2(a, b);
 }
@@ -252,13 +283,19 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
   const T* x = static_cast<const T*>(a.x);
   const T* dy = static_cast<const T*>(a.dy);
-  float dw[NV][N], db[NV][N], w[NV][N];
+  // columns in pairs (a column alone has a pair of its own)
+  constexpr int H = (N + 1) / 2;
+  uint64_t dw[NV][H], db[NV][H], w[NV][H];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = (k * G + tid) * N;
+    float ww[2 * H] = {};
+    if (i < d) load_params<N>(a.weight, a.param_bf16, i, ww);
 #pragma unroll
-    for (int e = 0; e < N; ++e) dw[k][e] = db[k][e] = w[k][e] = 0.f;
-    if (i < d) load_params<N>(a.weight, a.param_bf16, i, w[k]);
+    for (int e = 0; e < H; ++e) {
+      dw[k][e] = db[k][e] = pair_of(0.f, 0.f);
+      w[k][e] = pair_of(ww[2 * e], ww[2 * e + 1]);
+    }
   }
   auto slot_of = [&](int s, int which, int k) -> V& {
     return ring[((s * 2 + which) * NV + k) * (G * R)];
@@ -304,38 +341,48 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
       mean_next = a.rms ? 0.f : a.mean[row + groups];
       rstd_next = a.rstd[row + groups];
     }
-    float gw[NV][N], h[NV][N], sg = 0.f, sgh = 0.f;
+    uint64_t gw[NV][H], h[NV][H], sg = pair_of(0.f, 0.f), sgh = sg;
     if (live) {
+      // (x - mean) r, the difference first: x and mean may be large and close
+      const uint64_t rr = pair_of(r, r), shift = pair_of(-mean, -mean);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         if ((k * G + tid) * N < d) {
           const V xv = slot_of(at, 0, k), gv = slot_of(at, 1, k);
 #pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const float g = gv.get(e);
-            h[k][e] = (xv.get(e) - mean) * r;
-            dw[k][e] = fmaf(g, h[k][e], dw[k][e]);
-            db[k][e] += g;
-            gw[k][e] = g * w[k][e];
-            sg += gw[k][e];
-            sgh = fmaf(gw[k][e], h[k][e], sgh);
+          for (int e = 0; e < H; ++e) {
+            const bool two = 2 * e + 1 < N;
+            const uint64_t g = pair_of(gv.get(2 * e), two ? gv.get(2 * e + 1) : 0.f);
+            const uint64_t x2 = pair_of(xv.get(2 * e), two ? xv.get(2 * e + 1) : 0.f);
+            h[k][e] = mul2(add2(x2, shift), rr);
+            dw[k][e] = fma2(g, h[k][e], dw[k][e]);
+            db[k][e] = add2(db[k][e], g);
+            gw[k][e] = mul2(g, w[k][e]);
+            sg = add2(sg, gw[k][e]);
+            sgh = fma2(gw[k][e], h[k][e], sgh);
           }
         }
       }
     }
-    float2 s = group_sum<G, true>(sg, sgh, part, parity);
+    const float2 pg = of_pair(sg), ph = of_pair(sgh);
+    float2 s = group_sum<G, true>(pg.x + pg.y, ph.x + ph.y, part, parity);
     parity ^= 1;
     s.x = a.rms ? 0.f : s.x * inv_d;
     s.y *= inv_d;
     if (live) {
+      const uint64_t rr = pair_of(r, r), c1 = pair_of(-s.x, -s.x), c2 = pair_of(-s.y, -s.y);
       T* dx = static_cast<T*>(a.dx) + row * a.ld_dx;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int i = (k * G + tid) * N;
         if (i < d) {
-          float o[N];
+          float o[2 * H];
 #pragma unroll
-          for (int e = 0; e < N; ++e) o[e] = r * (gw[k][e] - s.x - h[k][e] * s.y);
+          for (int e = 0; e < H; ++e) {
+            const float2 q = of_pair(mul2(fma2(h[k][e], c2, add2(gw[k][e], c1)), rr));
+            o[2 * e] = q.x;
+            o[2 * e + 1] = q.y;
+          }
           V p;
           p.set(o);
           store_piece<T, N>(dx + i, p);
@@ -351,9 +398,14 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
     const int i = (k * G + tid) * N;
     if (i < d) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        pw[i + e] = dw[k][e];
-        pw[d + i + e] = db[k][e];
+      for (int e = 0; e < H; ++e) {
+        const float2 p = of_pair(dw[k][e]), q = of_pair(db[k][e]);
+        pw[i + 2 * e] = p.x;
+        pw[d + i + 2 * e] = q.x;
+        if (2 * e + 1 < N) {
+          pw[i + 2 * e + 1] = p.y;
+          pw[d + i + 2 * e + 1] = q.y;
+        }
       }
     }
   }
