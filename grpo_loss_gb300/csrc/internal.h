@@ -186,8 +186,9 @@ struct NormArgs {
 };
 int norm_parts(const NormArgs& a, int sms);  // rows of partial column sums in the workspace
 cudaError_t launch_norm_fwd(const NormArgs& a, int sms, cudaStream_t s);
-cudaError_t launch_norm_bwd(const NormArgs& a, int sms, cudaStream_t s);
-cudaError_t launch_norm_colsum(const NormArgs& a, int sms, cudaStream_t s);
+// *groups: the rows of partial column sums that it writes
+cudaError_t launch_norm_bwd(const NormArgs& a, int sms, int* groups, cudaStream_t s);
+cudaError_t launch_norm_colsum(const NormArgs& a, int groups, cudaStream_t s);
 
 // ---------------------------------------------------------------- adamw.cu
 struct AdamTensor {
@@ -219,7 +220,6 @@ struct AdamConst {
 enum AdamKind : int { ADAM_P_BF16 = 1, ADAM_G_BF16 = 2, ADAM_MASTER = 4, ADAM_BITS8 = 8 };
 constexpr int kAdamMaxTensors = 248;  // of one launch (its table is a kernel parameter)
 // `t[0..n)` share `kind`; chunk0 and on16 are filled in here.
-cudaError_t launch_adamw(AdamTensor* t, int n, int kind, const AdamConst& c, int sms,
-                         cudaStream_t s);
+cudaError_t launch_adamw(AdamTensor* t, int n, int kind, const AdamConst& c, cudaStream_t s);
 
 }  // namespace grpo

@@ -160,33 +160,60 @@ __device__ __forceinline__ float param(const void* p, int bf16, int i) {
   return bf16 ? ldf(static_cast<const __nv_bfloat16*>(p), i) : ldf(static_cast<const float*>(p), i);
 }
 
-// Sum of (a, b) over a group of G threads (a power of two from 32 on that
-// divides the CTA), returned to each of them. `slot` alternates between calls,
-// so that one barrier a call is enough.
-template <int G, bool BOTH>
-__device__ __forceinline__ float2 group_sum(float a, float b, float2* part, int slot) {
+// Sums over a group of G threads (a multiple of 32 that divides the CTA or is
+// it), returned to each of them. `slot` alternates between calls, so that one
+// barrier a call is enough.
+template <int G>
+__device__ __forceinline__ float group_sum(float a, float* part, int slot) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    if (BOTH) b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  if (G == 32) return make_float2(a, b);
-  const int warp = threadIdx.x >> 5, first = warp / (G / 32) * (G / 32);
-  float2* mine = part + slot * 32;
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) mine[warp] = make_float2(a, b);
-  __syncthreads();
-  // each lane takes one warp's sums
+  for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if (G == 32) return a;
   constexpr int W = G / 32, P = W <= 2 ? 2 : W <= 4 ? 4 : W <= 8 ? 8 : W <= 16 ? 16 : 32;
-  const float2 p = (lane & (P - 1)) < W ? mine[first + (lane & (P - 1))] : make_float2(0.f, 0.f);
-  a = p.x;
-  b = p.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* mine = part + slot * 128;
+  if (lane == 0) mine[warp] = a;
+  __syncthreads();
+  // each lane takes one warp's sum
+  const int w = lane & (P - 1);
+  a = w < W ? mine[warp / W * W + w] : 0.f;
 #pragma unroll
-  for (int o = P / 2; o >= 1; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    if (BOTH) b += __shfl_xor_sync(0xffffffffu, b, o);
+  for (int o = P / 2; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  return a;
+}
+// 2 or 4 sums at once. While the lanes are halved, so are the sums that a lane
+// carries: first the lanes of either half take half of the sums each, and so on.
+template <int G, int M>
+__device__ __forceinline__ void group_sums(float (&v)[M], float* part, int slot) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int m = M / 2; m >= 1; m /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < m; ++i) {
+      const float give = up ? v[i] : v[i + m], keep = up ? v[i + m] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
   }
-  return make_float2(a, b);
+  // each of M runs of `run` lanes holds one sum, in the order of the runs
+  constexpr int run = 32 / M;
+  float a = v[0];
+#pragma unroll
+  for (int p = run / 2; p >= 1; p /= 2) a += __shfl_xor_sync(0xffffffffu, a, p);
+  if (G > 32) {
+    constexpr int W = G / 32;
+    float* mine = part + slot * 128 + lane / run * 32;  // the run's sum of every warp
+    if (lane % run == 0) mine[warp] = a;
+    __syncthreads();
+    a = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; w += run)
+      if (w + lane % run < W) a += mine[warp / W * W + w + lane % run];
+#pragma unroll
+    for (int p = run / 2; p >= 1; p /= 2) a += __shfl_xor_sync(0xffffffffu, a, p);
+  }
+#pragma unroll
+  for (int i = 0; i < M; ++i) v[i] = __shfl_sync(0xffffffffu, a, i * run);
 }
 
 // ---------------------------------------------------------------- forward
@@ -194,7 +221,7 @@ __device__ __forceinline__ float2 group_sum(float a, float b, float2* part, int 
 // N values of it (G N NV >= d).
 template <typename T, int N, int NV, int G, int R>
 __global__ void __launch_bounds__(G * R) k_norm_fwd(NormArgs a) {
-  __shared__ float2 part[2 * 32];
+  __shared__ float part[2 * 128];
   const int tid = threadIdx.x % G;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
   const bool live = row < a.rows;  // every thread takes part in the barriers
@@ -215,7 +242,7 @@ __global__ void __launch_bounds__(G * R) k_norm_fwd(NormArgs a) {
       if ((k * G + tid) * N < d)
 #pragma unroll
         for (int e = 0; e < N; ++e) s += v[k].get(e);
-    mean = group_sum<G, false>(s, 0.f, part, 0).x * inv_d;
+    mean = group_sum<G>(s, part, 0) * inv_d;
   }
   float q = 0.f;
 #pragma unroll
@@ -226,7 +253,7 @@ __global__ void __launch_bounds__(G * R) k_norm_fwd(NormArgs a) {
         const float c = v[k].get(e) - mean;
         q = fmaf(c, c, q);
       }
-  const float r = rsqrtf(group_sum<G, false>(q, 0.f, part, 1).x * inv_d + a.eps);
+  const float r = rsqrtf(group_sum<G>(q, part, 1) * inv_d + a.eps);
   if (!live) return;
   T* y = static_cast<T*>(a.y) + row * a.ld_y;
 #pragma unroll
@@ -266,23 +293,22 @@ __device__ __forceinline__ void copy_async(void* to, const void* from) {
 
 // A group of G threads walks over the rows group, + groups, ... (R groups a CTA);
 // each thread holds NV pieces of N columns: their values of a row and their column
-// sums. Its pieces of the next S - 1 rows are on their way into shared memory:
-// S 16-byte pieces of x and of dy a thread keep HBM busy where registers for them
-// would halve the threads (1075 us for 163840 x 4096 bf16 with one row ahead in
-// registers). A thread reads back what it copied itself, so no barrier is needed
-// for them.
-template <typename T, int N, int NV, int G, int R, int S>
+// sums. It takes Q rows a turn, so that the joining of the row sums over the CTA
+// (a barrier, and the shuffles before and behind it) is waited for once in Q rows;
+// meanwhile its pieces of the next turn's rows are on their way into shared
+// memory, whence they are read twice, for the sums and for dx. A thread reads back
+// what it copied itself, so no barrier is needed for that. (163840 x 4096 bf16: 2
+// rows ahead or 4 make no difference, one row a turn takes 936 us.)
+template <typename T, int N, int NV, int G, int R, int Q>
 __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
   constexpr int B = N * static_cast<int>(sizeof(T));
   using V = Piece<T, N>;
   extern __shared__ __align__(16) unsigned char ring_raw[];
-  __shared__ float2 part[2 * 32];
-  V* ring = reinterpret_cast<V*>(ring_raw) + threadIdx.x;  // [S][2][NV][threads]
+  __shared__ float part[2 * 128];
+  V* ring = reinterpret_cast<V*>(ring_raw) + threadIdx.x;  // [2 turns][Q][2][NV][threads]
   const int tid = threadIdx.x % G, d = static_cast<int>(a.d);
   const int64_t groups = static_cast<int64_t>(gridDim.x) * R;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
-  const T* x = static_cast<const T*>(a.x);
-  const T* dy = static_cast<const T*>(a.dy);
   // columns in pairs (a column alone has a pair of its own)
   constexpr int H = (N + 1) / 2;
   uint64_t dw[NV][H], db[NV][H], w[NV][H];
@@ -300,20 +326,35 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
   auto slot_of = [&](int s, int which, int k) -> V& {
     return ring[((s * 2 + which) * NV + k) * (G * R)];
   };
-  auto fetch = [&](int64_t row, int s) {
-    if (row < a.rows) {
+  // this thread's first piece of the row that is fetched next, and of the row that
+  // is written; `left` rows of the group are still to be fetched
+  const int64_t step = groups, mine = row0 < a.rows ? (a.rows - row0 + groups - 1) / groups : 0;
+  const T* xp = static_cast<const T*>(a.x) + row0 * a.ld_x + tid * N;
+  const T* gp = static_cast<const T*>(a.dy) + row0 * a.ld_dy + tid * N;
+  T* dp = static_cast<T*>(a.dx) + row0 * a.ld_dx + tid * N;
+  const float* mp = a.mean + (a.rms ? 0 : row0);
+  const float* rp = a.rstd + row0;
+  int left = static_cast<int>(mine);
+  auto fetch = [&](int half) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int i = (k * G + tid) * N;
-        if (i < d) {
-          if constexpr (B >= 4) {
-            copy_async<B>(&slot_of(s, 0, k), x + row * a.ld_x + i);
-            copy_async<B>(&slot_of(s, 1, k), dy + row * a.ld_dy + i);
-          } else {
-            slot_of(s, 0, k) = load_piece<T, N>(x + row * a.ld_x + i);
-            slot_of(s, 1, k) = load_piece<T, N>(dy + row * a.ld_dy + i);
+    for (int q = 0; q < Q; ++q) {
+      if (left > 0) {
+        const int s = half * Q + q;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          if ((k * G + tid) * N < d) {
+            if constexpr (B >= 4) {
+              copy_async<B>(&slot_of(s, 0, k), xp + k * G * N);
+              copy_async<B>(&slot_of(s, 1, k), gp + k * G * N);
+            } else {
+              slot_of(s, 0, k) = load_piece<T, N>(xp + k * G * N);
+              slot_of(s, 1, k) = load_piece<T, N>(gp + k * G * N);
+            }
           }
         }
+        xp += step * a.ld_x;
+        gp += step * a.ld_dy;
+        --left;
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -321,75 +362,94 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
   const float inv_d = 1.f / d;
   // every group of a CTA makes the same number of turns: barriers are the CTA's
   const int64_t first = static_cast<int64_t>(blockIdx.x) * R;
-  const int64_t turns = first < a.rows ? (a.rows - first + groups - 1) / groups : 0;
+  const int rows = static_cast<int>(first < a.rows ? (a.rows - first + groups - 1) / groups : 0);
+  float mean_next[Q], rstd_next[Q];
+  auto fetch_stats = [&](int n) {  // of the group's rows from n on
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) fetch(row0 + s * groups, s);
-  float mean_next = 0.f, rstd_next = 0.f;
-  if (row0 < a.rows) {
-    mean_next = a.rms ? 0.f : a.mean[row0];
-    rstd_next = a.rstd[row0];
-  }
-  int at = 0, parity = 0;
-  int64_t row = row0;
-  for (int64_t n = 0; n < turns; ++n, row += groups) {
-    const bool live = row < a.rows;
-    const int to = at == 0 ? S - 1 : at - 1;  // the slot read last
-    fetch(row + (S - 1) * groups, to);
-    asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-    const float mean = mean_next, r = rstd_next;
-    if (row + groups < a.rows) {
-      mean_next = a.rms ? 0.f : a.mean[row + groups];
-      rstd_next = a.rstd[row + groups];
+    for (int q = 0; q < Q; ++q) {
+      mean_next[q] = rstd_next[q] = 0.f;
+      if (n + q < static_cast<int>(mine)) {
+        if (!a.rms) {
+          mean_next[q] = *mp;
+          mp += step;
+        }
+        rstd_next[q] = *rp;
+        rp += step;
+      }
     }
-    uint64_t gw[NV][H], h[NV][H], sg = pair_of(0.f, 0.f), sgh = sg;
-    if (live) {
-      // (x - mean) r, the difference first: x and mean may be large and close
-      const uint64_t rr = pair_of(r, r), shift = pair_of(-mean, -mean);
+  };
+  fetch(0);
+  fetch_stats(0);
+  int half = 0;
+  for (int n = 0; n < rows; n += Q, half ^= 1) {
+    fetch(half ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    float mean[Q], r[Q], sums[2 * Q];
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        if ((k * G + tid) * N < d) {
-          const V xv = slot_of(at, 0, k), gv = slot_of(at, 1, k);
+    for (int q = 0; q < Q; ++q) {
+      mean[q] = mean_next[q];
+      r[q] = rstd_next[q];
+    }
+    fetch_stats(n + Q);
+    // (x - mean) r, the difference first: x and mean may be large and close
+    auto columns = [&](int q, int k, int e, const V& xv, const V& gv, uint64_t& g, uint64_t& h) {
+      const bool two = 2 * e + 1 < N;
+      g = pair_of(gv.get(2 * e), two ? gv.get(2 * e + 1) : 0.f);
+      const uint64_t x2 = pair_of(xv.get(2 * e), two ? xv.get(2 * e + 1) : 0.f);
+      h = mul2(add2(x2, pair_of(-mean[q], -mean[q])), pair_of(r[q], r[q]));
+    };
 #pragma unroll
-          for (int e = 0; e < H; ++e) {
-            const bool two = 2 * e + 1 < N;
-            const uint64_t g = pair_of(gv.get(2 * e), two ? gv.get(2 * e + 1) : 0.f);
-            const uint64_t x2 = pair_of(xv.get(2 * e), two ? xv.get(2 * e + 1) : 0.f);
-            h[k][e] = mul2(add2(x2, shift), rr);
-            dw[k][e] = fma2(g, h[k][e], dw[k][e]);
-            db[k][e] = add2(db[k][e], g);
-            gw[k][e] = mul2(g, w[k][e]);
-            sg = add2(sg, gw[k][e]);
-            sgh = fma2(gw[k][e], h[k][e], sgh);
+    for (int q = 0; q < Q; ++q) {
+      uint64_t sg = pair_of(0.f, 0.f), sgh = sg;
+      if (n + q < static_cast<int>(mine)) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          if ((k * G + tid) * N < d) {
+            const V xv = slot_of(half * Q + q, 0, k), gv = slot_of(half * Q + q, 1, k);
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+              uint64_t g, h;
+              columns(q, k, e, xv, gv, g, h);
+              dw[k][e] = fma2(g, h, dw[k][e]);
+              db[k][e] = add2(db[k][e], g);
+              const uint64_t gw = mul2(g, w[k][e]);
+              sg = add2(sg, gw);
+              sgh = fma2(gw, h, sgh);
+            }
           }
         }
       }
+      const float2 pg = of_pair(sg), ph = of_pair(sgh);
+      sums[2 * q] = pg.x + pg.y;
+      sums[2 * q + 1] = ph.x + ph.y;
     }
-    const float2 pg = of_pair(sg), ph = of_pair(sgh);
-    float2 s = group_sum<G, true>(pg.x + pg.y, ph.x + ph.y, part, parity);
-    parity ^= 1;
-    s.x = a.rms ? 0.f : s.x * inv_d;
-    s.y *= inv_d;
-    if (live) {
-      const uint64_t rr = pair_of(r, r), c1 = pair_of(-s.x, -s.x), c2 = pair_of(-s.y, -s.y);
-      T* dx = static_cast<T*>(a.dx) + row * a.ld_dx;
+    group_sums<G, 2 * Q>(sums, part, half);
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int i = (k * G + tid) * N;
-        if (i < d) {
-          float o[2 * H];
+    for (int q = 0; q < Q; ++q) {
+      if (n + q < static_cast<int>(mine)) {
+        const float m1 = a.rms ? 0.f : -sums[2 * q] * inv_d, m2 = -sums[2 * q + 1] * inv_d;
+        const uint64_t c1 = pair_of(m1, m1), c2 = pair_of(m2, m2), rr = pair_of(r[q], r[q]);
 #pragma unroll
-          for (int e = 0; e < H; ++e) {
-            const float2 q = of_pair(mul2(fma2(h[k][e], c2, add2(gw[k][e], c1)), rr));
-            o[2 * e] = q.x;
-            o[2 * e + 1] = q.y;
+        for (int k = 0; k < NV; ++k) {
+          if ((k * G + tid) * N < d) {
+            const V xv = slot_of(half * Q + q, 0, k), gv = slot_of(half * Q + q, 1, k);
+            float o[2 * H];
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+              uint64_t g, h;
+              columns(q, k, e, xv, gv, g, h);
+              const float2 t = of_pair(mul2(fma2(h, c2, fma2(g, w[k][e], c1)), rr));
+              o[2 * e] = t.x;
+              o[2 * e + 1] = t.y;
+            }
+            V p;
+            p.set(o);
+            store_piece<T, N>(dp + k * G * N, p);
           }
-          V p;
-          p.set(o);
-          store_piece<T, N>(dx + i, p);
         }
+        dp += step * a.ld_dx;
       }
     }
-    at = at == S - 1 ? 0 : at + 1;
   }
   if (!a.partial) return;
   float* pw = a.partial + 2 * row0 * d;  // one pair of rows a group
@@ -415,7 +475,7 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
 constexpr int kLong = 1024;
 template <typename T>
 __global__ void __launch_bounds__(kLong) k_norm_fwd_long(NormArgs a) {
-  __shared__ float2 part[2 * 32];
+  __shared__ float part[2 * 128];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
   T* y = static_cast<T*>(a.y) + row * a.ld_y;
@@ -424,14 +484,14 @@ __global__ void __launch_bounds__(kLong) k_norm_fwd_long(NormArgs a) {
   if (!a.rms) {
     float s = 0.f;
     for (int i = threadIdx.x; i < d; i += kLong) s += ldf(x, i);
-    mean = group_sum<kLong, false>(s, 0.f, part, 0).x / d;
+    mean = group_sum<kLong>(s, part, 0) / d;
   }
   float q = 0.f;
   for (int i = threadIdx.x; i < d; i += kLong) {
     const float c = ldf(x, i) - mean;
     q = fmaf(c, c, q);
   }
-  const float r = rsqrtf(group_sum<kLong, false>(q, 0.f, part, 1).x / d + a.eps);
+  const float r = rsqrtf(group_sum<kLong>(q, part, 1) / d + a.eps);
   for (int i = threadIdx.x; i < d; i += kLong) {
     float v = (ldf(x, i) - mean) * r * param(a.weight, a.param_bf16, i);
     if (a.bias) v += param(a.bias, a.param_bf16, i);
@@ -447,7 +507,7 @@ __global__ void __launch_bounds__(kLong) k_norm_fwd_long(NormArgs a) {
 // from its first row on.
 template <typename T>
 __global__ void __launch_bounds__(kLong) k_norm_bwd_long(NormArgs a) {
-  __shared__ float2 part[2 * 32];
+  __shared__ float part[2 * 128];
   const int d = static_cast<int>(a.d);
   float* pw = a.partial ? a.partial + 2 * static_cast<int64_t>(blockIdx.x) * d : nullptr;
   int slot = 0;
@@ -467,7 +527,9 @@ __global__ void __launch_bounds__(kLong) k_norm_bwd_long(NormArgs a) {
         pw[d + i] = g + (first ? 0.f : pw[d + i]);
       }
     }
-    float2 s = group_sum<kLong, true>(sg, sgh, part, slot);
+    float sums[2] = {sg, sgh};
+    group_sums<kLong, 2>(sums, part, slot);
+    float2 s = make_float2(sums[0], sums[1]);
     slot ^= 1;
     s.x = a.rms ? 0.f : s.x / d;
     s.y /= d;
@@ -531,31 +593,6 @@ int piece_of(const NormArgs& a, bool fwd) {
   return n;
 }
 
-// The backward's threads: G a row, R rows a CTA at a time, NV pieces a thread; 0
-// where a row does not fit.
-struct BwdShape {
-  int n, g, r, nv;
-};
-BwdShape bwd_shape(const NormArgs& a) {
-  BwdShape s;
-  s.n = piece_of(a, false);
-  const int pieces = static_cast<int>((a.d + s.n - 1) / s.n);
-  s.nv = 1;
-  s.r = 1;
-  if (pieces <= 32) s.g = 32, s.r = 8;
-  else if (pieces <= 64) s.g = 32, s.r = 8, s.nv = 2;
-  else if (pieces <= 128) s.g = 128, s.r = 2;
-  else if (pieces <= 256) s.g = 256;
-  else if (pieces <= 384) s.g = 384;
-  else if (pieces <= 512) s.g = 512;
-  else if (pieces <= 768) s.g = 384, s.nv = 2;
-  else if (pieces <= 1024) s.g = 512, s.nv = 2;
-  else if (pieces <= 2048) s.g = 1024, s.nv = 2;
-  else if (s.n <= 2 && pieces <= 4096) s.g = 1024, s.nv = 4;
-  else s.g = 0;
-  return s;
-}
-
 template <typename T, int N, int NV, int G, int R>
 cudaError_t fwd(const NormArgs& a, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>((a.rows + R - 1) / R);
@@ -578,54 +615,61 @@ cudaError_t fwd_n(const NormArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// CTAs of the backward: what the SMs hold at a time (by threads and the ring's
-// shared memory), so that each walks over its share of the rows once.
-int bwd_ctas_per_sm(const BwdShape& b) {
-  if (b.g == 0) return 2;
-  const int by_threads = 1024 / (b.g * b.r);
-  return by_threads < 1 ? 1 : by_threads;
-}
-int bwd_grid(const NormArgs& a, const BwdShape& b, int sms) {
-  const int64_t need = (a.rows + (b.g ? b.r : 1) - 1) / (b.g ? b.r : 1);
-  const int64_t most = static_cast<int64_t>(bwd_ctas_per_sm(b)) * sms;
-  return static_cast<int>(need < 1 ? 1 : need < most ? need : most);
-}
-
+// One backward launch: as many CTAs as the SMs hold at a time, so that each walks
+// over its share of the rows once. *groups: rows of partial sums it writes.
 template <typename T, int N, int NV, int G, int R>
-cudaError_t bwd(const NormArgs& a, int grid, cudaStream_t s) {
+cudaError_t bwd(const NormArgs& a, int sms, int* groups, cudaStream_t s) {
   constexpr int slot = 2 * NV * N * static_cast<int>(sizeof(T)) * G * R;
-  constexpr int S = 4 * slot <= 200 * 1024 ? 4 : 3;
-  constexpr int smem = S * slot;
-  if constexpr (smem > 40 * 1024) {  // (48 KB with the static part need no attribute)
-    static std::atomic<uint64_t> configured{0};  // one bit a device
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+  constexpr int Q = 4 * slot <= 200 * 1024 ? 2 : 1;
+  constexpr int smem = 2 * Q * slot;
+  auto kernel = k_norm_bwd<T, N, NV, G, R, Q>;
+  static std::atomic<uint64_t> configured{0};  // one bit a device
+  static std::atomic<int> per_sm{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    int n = 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, G * R, smem);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (!(configured.load() & bit)) {
-      e = cudaFuncSetAttribute(k_norm_bwd<T, N, NV, G, R, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return e;
-      configured.fetch_or(bit);
-    }
+    per_sm.store(n < 1 ? 1 : n);
+    configured.fetch_or(bit);
   }
-  k_norm_bwd<T, N, NV, G, R, S><<<grid, G * R, smem, s>>>(a);
+  // four rows a group at least, where that leaves the SMs at work: a group's
+  // partial sums are written and read again
+  int64_t grid = (a.rows + R - 1) / R;
+  if (grid > sms / 2) grid = grid / 4 > sms / 2 ? grid / 4 : sms / 2;
+  const int64_t most = static_cast<int64_t>(per_sm.load()) * sms, room = norm_parts(a, sms) / R;
+  grid = grid < most ? grid : most;
+  grid = grid < room ? grid : room;
+  *groups = static_cast<int>(grid) * R;
+  kernel<<<static_cast<unsigned>(grid), G * R, smem, s>>>(a);
   return cudaGetLastError();
 }
+
+// A row is given to few threads with several pieces each: the fewer warps join
+// their sums, the more rows an SM has under way (163840 x 4096 bf16: 512 threads
+// a row 811 us, 256 with two pieces 679 us).
 template <typename T, int N>
-cudaError_t bwd_n(const NormArgs& a, const BwdShape& b, int grid, cudaStream_t s) {
-  if (b.g == 32 && b.nv == 1) return bwd<T, N, 1, 32, 8>(a, grid, s);
-  if (b.g == 32) return bwd<T, N, 2, 32, 8>(a, grid, s);
-  if (b.g == 128) return bwd<T, N, 1, 128, 2>(a, grid, s);
-  if (b.g == 256) return bwd<T, N, 1, 256, 1>(a, grid, s);
-  if (b.g == 384 && b.nv == 1) return bwd<T, N, 1, 384, 1>(a, grid, s);
-  if (b.g == 512 && b.nv == 1) return bwd<T, N, 1, 512, 1>(a, grid, s);
-  if (b.g == 384) return bwd<T, N, 2, 384, 1>(a, grid, s);
-  if (b.g == 512) return bwd<T, N, 2, 512, 1>(a, grid, s);
-  if (b.g == 1024 && b.nv == 2) return bwd<T, N, 2, 1024, 1>(a, grid, s);
+cudaError_t bwd_n(const NormArgs& a, int sms, int* groups, cudaStream_t s) {
+  const int64_t pieces = (a.d + N - 1) / N;
+  if (pieces <= 32) return bwd<T, N, 1, 32, 8>(a, sms, groups, s);
+  if (pieces <= 64) return bwd<T, N, 2, 32, 8>(a, sms, groups, s);
+  if (pieces <= 128) return bwd<T, N, 2, 64, 4>(a, sms, groups, s);
+  if (pieces <= 256) return bwd<T, N, 2, 128, 1>(a, sms, groups, s);
+  if (pieces <= 384) return bwd<T, N, 3, 128, 1>(a, sms, groups, s);
+  if (pieces <= 512) return bwd<T, N, 2, 256, 1>(a, sms, groups, s);
+  if (pieces <= 768) return bwd<T, N, 3, 256, 1>(a, sms, groups, s);
+  if (pieces <= 1024) return bwd<T, N, 2, 512, 1>(a, sms, groups, s);
+  if (pieces <= 2048) return bwd<T, N, 4, 512, 1>(a, sms, groups, s);
   if constexpr (N <= 2) {
-    if (b.g == 1024) return bwd<T, N, 4, 1024, 1>(a, grid, s);
+    if (pieces <= 4096) return bwd<T, N, 4, 1024, 1>(a, sms, groups, s);
   }
-  k_norm_bwd_long<T><<<grid, kLong, 0, s>>>(a);
+  const int64_t most = 2ll * sms;
+  *groups = static_cast<int>(a.rows < most ? a.rows : most);
+  k_norm_bwd_long<T><<<*groups, kLong, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -649,22 +693,20 @@ cudaError_t launch_norm_fwd(const NormArgs& a, int, cudaStream_t s) {
   return n == 4 ? fwd_n<float, 4>(a, s) : n == 2 ? fwd_n<float, 2>(a, s) : fwd_n<float, 1>(a, s);
 }
 
-cudaError_t launch_norm_bwd(const NormArgs& a, int sms, cudaStream_t s) {
-  const BwdShape b = bwd_shape(a);
-  const int grid = bwd_grid(a, b, sms);
+cudaError_t launch_norm_bwd(const NormArgs& a, int sms, int* groups, cudaStream_t s) {
+  const int n = piece_of(a, false);
   if (a.bf16)
-    return b.n == 8   ? bwd_n<__nv_bfloat16, 8>(a, b, grid, s)
-           : b.n == 4 ? bwd_n<__nv_bfloat16, 4>(a, b, grid, s)
-           : b.n == 2 ? bwd_n<__nv_bfloat16, 2>(a, b, grid, s)
-                      : bwd_n<__nv_bfloat16, 1>(a, b, grid, s);
-  return b.n == 4 ? bwd_n<float, 4>(a, b, grid, s)
-         : b.n == 2 ? bwd_n<float, 2>(a, b, grid, s)
-                    : bwd_n<float, 1>(a, b, grid, s);
+    return n == 8   ? bwd_n<__nv_bfloat16, 8>(a, sms, groups, s)
+           : n == 4 ? bwd_n<__nv_bfloat16, 4>(a, sms, groups, s)
+           : n == 2 ? bwd_n<__nv_bfloat16, 2>(a, sms, groups, s)
+                    : bwd_n<__nv_bfloat16, 1>(a, sms, groups, s);
+  return n == 4   ? bwd_n<float, 4>(a, sms, groups, s)
+         : n == 2 ? bwd_n<float, 2>(a, sms, groups, s)
+                  : bwd_n<float, 1>(a, sms, groups, s);
 }
 
-cudaError_t launch_norm_colsum(const NormArgs& a, int sms, cudaStream_t s) {
-  k_norm_colsum<<<static_cast<unsigned>((a.d + 31) / 32), 1024, 0, s>>>(
-      a, bwd_grid(a, bwd_shape(a), sms) * (bwd_shape(a).g ? bwd_shape(a).r : 1));
+cudaError_t launch_norm_colsum(const NormArgs& a, int groups, cudaStream_t s) {
+  k_norm_colsum<<<static_cast<unsigned>((a.d + 31) / 32), 1024, 0, s>>>(a, groups);
   return cudaGetLastError();
 }
 

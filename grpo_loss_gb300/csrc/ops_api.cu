@@ -154,8 +154,9 @@ grpo_status grpo_layernorm_bwd(const grpo_layernorm_problem* p, const void* x,
   a.dweight = dweight;
   a.dbias = dbias;
   a.partial = sums ? static_cast<float*>(workspace) : nullptr;
-  LAUNCH(K_NORM_BWD, stream, launch_norm_bwd(a, sms, stream));
-  if (sums) LAUNCH(K_NORM_COLSUM, stream, launch_norm_colsum(a, sms, stream));
+  int groups = 0;
+  LAUNCH(K_NORM_BWD, stream, launch_norm_bwd(a, sms, &groups, stream));
+  if (sums) LAUNCH(K_NORM_COLSUM, stream, launch_norm_colsum(a, groups, stream));
   return GRPO_OK;
 }
 
@@ -192,10 +193,6 @@ grpo_status grpo_adamw_step(const grpo_adamw_config* c, const grpo_adamw_tensor*
         !aligned_to(t.v, ss) || !aligned_to(t.m_out, ss) || !aligned_to(t.v_out, ss))
       return GRPO_ERR_UNSUPPORTED;
   }
-  int sms = 0;
-  const grpo_status st = device_info(&sms);
-  if (st != GRPO_OK) return st;
-
   // The scalars are formed in float64 and rounded once.
   AdamConst k;
   const double b1 = c->beta1, b2 = c->beta2, t = static_cast<double>(c->step);
@@ -217,7 +214,7 @@ grpo_status grpo_adamw_step(const grpo_adamw_config* c, const grpo_adamw_tensor*
     for (int32_t i = 0; i <= n_tensors; ++i) {
       if (used == kAdamMaxTensors || (i == n_tensors && used > 0)) {
         LAUNCH(K_ADAMW, stream,
-               launch_adamw(table, used, kind | (eight ? ADAM_BITS8 : 0), k, sms, stream));
+               launch_adamw(table, used, kind | (eight ? ADAM_BITS8 : 0), k, stream));
         used = 0;
       }
       if (i == n_tensors) break;
