@@ -39,6 +39,7 @@ constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 8;                 // the portable cluster size
 constexpr int kBins = 1280;                    // (five a thread at most) 1/32 of a binary order each, down to 2^-40
 constexpr int kCap = 1024;                     // candidates that one CTA sorts
+constexpr int kGuess = 96;                      // candidates asked for with top-p alone
 constexpr int kCount = 256;                    // and those that it sorts by counting
 constexpr int kMaxSliceBytes = 192 * 1024;     // of a row's slice kept in shared memory
 constexpr int kMaxFast = 1 << 19;              // elements of a slice that the bins' sums can take
@@ -85,7 +86,40 @@ struct Vec {
   uint4 raw;
   __device__ __forceinline__ float get(int e) const;
   __device__ __forceinline__ float max() const;  // NaN counts as -inf
+  // elements 2 e and 2 e + 1 as they are
+  __device__ __forceinline__ uint64_t pair(int e) const;
 };
+// Two floats in one register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_of(float v) { return pair_of(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ float2 of_pair(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint64_t Vec<float>::pair(int e) const {
+  return e == 0 ? pair_of(raw.x, raw.y) : pair_of(raw.z, raw.w);
+}
+template <>
+__device__ __forceinline__ uint64_t Vec<__nv_bfloat16>::pair(int e) const {
+  const uint32_t w = e == 0 ? raw.x : e == 1 ? raw.y : e == 2 ? raw.z : raw.w;
+  return pair_of(w << 16, w & 0xFFFF0000u);
+}
 template <>
 __device__ __forceinline__ float Vec<float>::get(int e) const {
   return clean(__uint_as_float(e == 0 ? raw.x : e == 1 ? raw.y : e == 2 ? raw.z : raw.w));
@@ -413,9 +447,16 @@ struct Row {
   // Bin of a logit in steps of 1/32 of a binary order below the top.
   __device__ __forceinline__ static int bin_of(float y) { return static_cast<int>(-32.f * y); }
 
+  // Adds an element to this CTA's list.
+  __device__ __forceinline__ void list(float z, int v, int e) {
+    const uint32_t at = atomicAdd(&sh.n_cand, 1u);
+    const uint32_t idx = static_cast<uint32_t>(pos0 + static_cast<int64_t>(v) * VE + e);
+    if (at < kCap) sh.cand[at] = (static_cast<uint64_t>(key_of(z)) << 32) | ~idx;
+  }
+
   // Lists the elements that both functions accept (the first accepts from some
   // logit on, so that a piece's maximum can be asked); returns their number over
-  // the cluster. If they are kCap or fewer, the leader gets all of them.
+  // the cluster.
   template <typename F, typename G>
   __device__ uint32_t gather(F accept, G also) {
     Part p;
@@ -426,26 +467,25 @@ struct Row {
       for (int e = 0; e < VE; ++e) {
         const float z = x.get(e);
         if (accept(z) && also(z)) {
-          const uint32_t at = atomicAdd(&sh.n_cand, 1u);
-          const uint32_t idx = static_cast<uint32_t>(pos0 + static_cast<int64_t>(v) * VE + e);
-          if (at < kCap) sh.cand[at] = (static_cast<uint64_t>(key_of(z)) << 32) | ~idx;
+          list(z, v, e);
           ++p.count;
         }
       }
     }
-    const uint32_t n = join<P_COUNT>(p).count;
-    if (rank == 0 && n <= kCap) {
-      if (static_cast<int>(threadIdx.x) < C) sh.scan_u[threadIdx.x] = *cl.map_shared_rank(&sh.n_cand, threadIdx.x);
-      __syncthreads();
-      for (uint32_t i = sh.scan_u[0] + threadIdx.x; i < n; i += nt) {
-        uint32_t j = i;
-        int c = 0;
-        while (j >= sh.scan_u[c]) j -= sh.scan_u[c++];
-        sh.cand[i] = cl.map_shared_rank(sh.cand, c)[j];
-      }
-      __syncthreads();
+    return join<P_COUNT>(p).count;
+  }
+
+  // The leader fetches the other CTAs' lists, n <= kCap candidates in all.
+  __device__ void fetch_lists(uint32_t n) {
+    if (static_cast<int>(threadIdx.x) < C) sh.scan_u[threadIdx.x] = *cl.map_shared_rank(&sh.n_cand, threadIdx.x);
+    __syncthreads();
+    for (uint32_t i = sh.scan_u[0] + threadIdx.x; i < n; i += nt) {
+      uint32_t j = i;
+      int c = 0;
+      while (j >= sh.scan_u[c]) j -= sh.scan_u[c++];
+      sh.cand[i] = cl.map_shared_rank(sh.cand, c)[j];
     }
-    return n;
+    __syncthreads();
   }
 
   // Sorts the leader's n candidates, largest first, and weighs them. A few by
@@ -524,41 +564,191 @@ __device__ __forceinline__ int local_bin(Shared& sh, uint32_t k, int lane, int w
   return sh.b;
 }
 
-// One row with one way of weighing. Returns whether the token is decided; with
-// EXACT it always is. Every thread of the cluster returns the same.
+// The largest value of 16 leading bits that at least k of the warp's keys reach
+// (N a lane); 0 if fewer do.
+template <int N>
+__device__ __forceinline__ uint32_t kth_from_below(const uint32_t (&key)[N], uint32_t k) {
+  uint32_t prefix = 0;
+#pragma unroll
+  for (int bit = 31; bit >= 16; --bit) {
+    const uint32_t t = prefix | (1u << bit);
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += __popc(__ballot_sync(0xffffffffu, key[i] >= t));
+    if (n >= k) prefix = t;
+  }
+  return prefix;
+}
+
+// How the leader's list served: the token is in ans.t; or u or the top-p cut is
+// within the error of a border; or the top-p cut is behind the list's end.
+enum : int { L_DONE = 0, L_CLOSE = 1, L_SHORT = 2 };
+
+// The leader alone draws from its list of n candidates, exactly. top_k > 0: the
+// list holds the k first tokens. Else with use_p: `base` is the mass that the
+// top-p cut is taken of, off by slack at most, and `whole` says whether the list
+// holds every token that the cut can keep.
+template <typename T>
+__device__ __noinline__ void draw_from_list(Row<T> r, uint32_t n, bool warm, uint64_t base,
+                                            uint64_t slack, bool whole) {
+  Shared& sh = r.sh;
+  const int lane = r.lane, warp = r.warp;
+  const bool use_k = !warm || sh.top_k > 0, use_p = warm && sh.use_p;
+  r.fetch_lists(n);
+  r.sort_and_weigh(n);
+  if (warp == 0) {
+    const uint32_t floor_key = sh.use_q ? key_of(sh.floor_z) : 0;
+    uint32_t n_l = n;
+    if (use_k) n_l = min(n_l, warm ? static_cast<uint32_t>(sh.top_k) : 1u);
+    if (sh.use_q) {  // those from the min-p floor on are the first of the order
+      uint32_t m = 0;
+      for (uint32_t i = lane; i < n_l; i += 32) m += static_cast<uint32_t>(sh.cand[i] >> 32) >= floor_key;
+      m = __reduce_add_sync(0xffffffffu, m);
+      whole |= m < n_l;
+      n_l = m;
+    }
+    int state = L_DONE;
+    if (use_p) {
+      if (use_k) {  // the mass is this list's
+        base = 0;
+        for (uint32_t i = lane; i < n_l; i += 32) base += sh.wts[i];
+        base = warp_sum(base);
+        slack = 0;
+        whole = true;
+      }
+      const uint64_t want = mul_ceil(sh.top_p, base);
+      uint64_t run = 0;
+      uint32_t stay = 0;
+      for (uint32_t i0 = 0; i0 < n_l; i0 += 32) {
+        const uint32_t i = i0 + lane;
+        const uint64_t x = i < n_l ? sh.wts[i] : 0;
+        const uint64_t ahead = run + warp_scan(x, lane) - x;
+        stay += __popc(__ballot_sync(0xffffffffu, i < n_l && ahead < want));
+        if (__any_sync(0xffffffffu, slack && i < n_l && i > 0 && distance(ahead, want) <= slack)) state = L_CLOSE;
+        run += warp_sum(x);
+      }
+      if (!whole && run <= want + slack) state = L_SHORT;
+      else if (slack && run <= want + slack) state = L_CLOSE;
+      n_l = max(1u, stay);
+    }
+    if (lane == 0) {
+      sh.n_kept = n_l;
+      sh.ans[r.par].bad = state;
+      sh.ans[r.par].t = 0xFFFFFFFFu;
+    }
+  }
+  __syncthreads();
+  const uint32_t n_l = sh.n_kept;
+  if (sh.ans[r.par].bad != L_DONE) return;
+  // The draw runs in the row's own order. Of a few, each adds up the weights of
+  // the indexes up to its own.
+  if (n_l <= kCount) {
+    if (warp * 32 < static_cast<int>(n_l)) {
+      uint64_t total = 0, upto_me = 0;
+      const bool in = threadIdx.x < n_l;
+      const uint32_t me = in ? static_cast<uint32_t>(sh.cand[threadIdx.x]) : 0;
+      for (uint32_t j = 0; j < n_l; ++j) {
+        const uint64_t x = sh.wts[j];
+        total += x;
+        if (static_cast<uint32_t>(sh.cand[j]) >= me) upto_me += x;  // (~index)
+      }
+      bool rest;
+      if (in && upto_me > mul_floor(sh.u, total, rest)) atomicMin(&sh.ans[r.par].t, ~me);
+    }
+  } else {
+    for (uint32_t i = threadIdx.x; i < n_l; i += r.nt)
+      sh.cand[i] = (sh.cand[i] << 32) | i;  // ~index descends as the index ascends
+    __syncthreads();
+    r.sort_desc(sh.cand, n_l);
+    if (warp == 0) {
+      uint64_t total = 0;
+      for (uint32_t i = lane; i < n_l; i += 32) total += sh.wts[i];
+      bool rest;
+      const uint64_t target = mul_floor(sh.u, warp_sum(total), rest);
+      uint64_t run = 0;
+      for (uint32_t i0 = 0; i0 < n_l; i0 += 32) {
+        const uint32_t i = i0 + lane;
+        const uint64_t c = i < n_l ? sh.cand[i] : 0;
+        const uint64_t x = i < n_l ? sh.wts[static_cast<uint32_t>(c)] : 0;
+        const uint32_t hit = __ballot_sync(0xffffffffu, run + warp_scan(x, lane) > target);
+        if (hit) {
+          const uint32_t at =
+              ~static_cast<uint32_t>(__shfl_sync(0xffffffffu, c, __ffs(hit) - 1) >> 32);
+          if (lane == 0) sh.ans[r.par].t = at;
+          break;
+        }
+        run += warp_sum(x);
+      }
+    }
+  }
+}
+
+// One row with one way of weighing. `from`: with a list to be made, the logit
+// from which on tokens are candidates. Returns whether the token is decided;
+// with EXACT it always is. Every thread of the cluster returns the same.
 template <typename T, bool EXACT>
 __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kmax,
-                                    float my_max, bool hist) {
+                                    float my_max, bool hist, bool listing, float from) {
   constexpr int VE = Vec<T>::N;
   Shared& sh = r.sh;
-  if (EXACT && threadIdx.x == 0) sh.ans[r.par].bad = 0;
+  if (EXACT) {
+    if (threadIdx.x == 0) {
+      sh.ans[r.par].bad = 0;
+      sh.n_cand = 0;
+    }
+    __syncthreads();
+  }
   Weigher w = sh.w;
   w.zmax = float_of(kmax);
   const int lane = r.lane, warp = r.warp;
   const bool warm = sh.warm != 0, use_k = sh.top_k > 0, use_p = sh.use_p != 0;
 
-  // ---- the mass of all tokens
+  // ---- the mass of all tokens, and the list
   Part p;
+  auto list = [&](const Vec<T>& x, int v) {
+    if (listing && x.max() >= from) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float z = x.get(e);
+        if (z >= from && z > -INFINITY) {
+          r.list(z, v, e);
+          ++p.count;
+        }
+      }
+    }
+  };
   if (EXACT) {
-    r.each([&](float z) { p.mass += weight_inline(w, z); });
+    for (int v = r.v0 + lane; v < r.v1; v += 32) {
+      const Vec<T> x = r.load(v);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) p.mass += weight_inline(w, x.get(e));
+      list(x, v);
+    }
   } else {
     PairSum all;
+    const uint64_t top = pair_of(-w.zmax), scale = pair_of(w.c_hi);
 #pragma unroll 2
     for (int v = r.v0 + lane; v < r.v1; v += 32) {
       const Vec<T> x = r.load(v);
-      float s[VE];
+      uint64_t s[VE / 2];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) s[i] = fast_weight(fast_y(w, x.get(i)));
+      for (int i = 0; i < VE / 2; ++i) {
+        const float2 y = of_pair(mul2(add2(x.pair(i), top), scale));  // as fast_y
+        s[i] = pair_of(__float_as_uint(fast_weight(y.x)), __float_as_uint(fast_weight(y.y)));
+      }
 #pragma unroll
-      for (int o = 1; o < VE; o <<= 1)
+      for (int o = 1; o < VE / 2; o <<= 1)
 #pragma unroll
-        for (int i = 0; i + o < VE; i += 2 * o) s[i] += s[i + o];
-      all.add(s[0]);
+        for (int i = 0; i + o < VE / 2; i += 2 * o) s[i] = add2(s[i], s[i + o]);
+      const float2 t = of_pair(s[0]);
+      all.add(t.x + t.y);
+      list(x, v);
     }
     p.mass = all.fixed(w.one);
   }
   Part mine, before;
-  const Part S = r.template join<P_MASS>(p, &mine, &before);
+  const Part S = r.template join<P_MASS | P_COUNT>(p, &mine, &before);
+  const uint32_t n_list = S.count;
   const float floor_z = sh.floor_z;  // min-p keeps logits from here on (-inf: off)
   // Bound on the error of any sum of weights, in units of W: 2^-24 sum w
   // (4 + 2.1 |y|), three more roundings in the sum of a piece; and since the
@@ -572,7 +762,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
   }
   // and of those that min-p keeps, where the top-p cut is taken of these
   uint64_t mass_q = S.mass;
-  if (use_p && sh.use_q && !use_k) {
+  if (use_p && sh.use_q && !use_k && warm) {
     Part q;
     PairSum kept;
     r.each_if([&](float z) { return z >= floor_z; }, [&](float z) {
@@ -586,8 +776,24 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
   const float mass2 = static_cast<float>(mass_q) / w.one;
 
   Kept keep;
-  bool leader_draws = false;  // the token is decided by the leader alone
-  if (!warm) {
+  bool drawn = false, synced = false;  // the leader has the token; and all know it
+  if (listing && n_list <= kCap) {
+    // ---- few candidates: the leader finishes the row with exact weights
+    if (r.rank == 0) draw_from_list<T>(r, n_list, warm, mass_q, 2 * E, false);
+    drawn = true;
+    if (warm && !use_k) {  // (the top-p cut may fall behind the list)
+      r.cl.sync();
+      const int state = r.cl.map_shared_rank(&sh, 0)->ans[r.par].bad;
+      if (state == L_CLOSE) return false;
+      drawn = synced = state == L_DONE;
+      if (!drawn) {
+        r.cl.sync();  // all have read it
+        if (threadIdx.x == 0) sh.ans[r.par].bad = 0;
+      }
+    }
+  }
+  if (drawn) {
+  } else if (!warm) {
     keep.t = kmax;
     keep.ties = 1;
   } else if (use_k || use_p) {
@@ -715,86 +921,8 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         // ---- few candidates: the leader finishes the row with exact weights
         const uint32_t n_all = r.gather([&](float z) { return in_bin(z, b2); }, [](float) { return true; });
         if (n_all <= kCap) {
-          listed = leader_draws = true;
-          if (r.rank == 0) {
-            uint32_t n_l = n_all;
-            r.sort_and_weigh(n_l);
-            if (warp == 0) {
-              if (use_k) n_l = min(n_l, static_cast<uint32_t>(sh.top_k));
-              bool bad = false;
-              if (use_p) {
-                // with top-k the mass is this list's; else everything's, within E
-                uint64_t base = mass_q;
-                if (use_k) {
-                  base = 0;
-                  for (uint32_t i = lane; i < n_l; i += 32) base += sh.wts[i];
-                  base = warp_sum(base);
-                }
-                const uint64_t want = mul_ceil(sh.top_p, base);
-                const uint64_t slack = use_k ? 0 : 2 * E;
-                uint64_t run = 0;
-                uint32_t stay = 0;
-                for (uint32_t i0 = 0; i0 < n_l; i0 += 32) {
-                  const uint32_t i = i0 + lane;
-                  const uint64_t x = i < n_l ? sh.wts[i] : 0;
-                  const uint64_t ahead = run + warp_scan(x, lane) - x;
-                  stay += __popc(__ballot_sync(0xffffffffu, i < n_l && ahead < want));
-                  bad |= __any_sync(0xffffffffu, slack && i < n_l && i > 0 && distance(ahead, want) <= slack);
-                  run += warp_sum(x);
-                }
-                bad |= slack && run <= want + slack;  // the cut may fall behind the list
-                n_l = max(1u, stay);
-              }
-              if (lane == 0) {
-                sh.n_kept = n_l;
-                sh.ans[r.par].bad = bad ? 1 : 0;
-                sh.ans[r.par].t = 0xFFFFFFFFu;
-              }
-            }
-            __syncthreads();
-            n_l = sh.n_kept;
-            // The draw runs in the row's own order. Of a few, each adds up the
-            // weights of the indexes up to its own.
-            if (n_l <= kCount) {
-              uint64_t total = 0, upto_me = 0;
-              const uint32_t mine_idx = threadIdx.x < n_l ? static_cast<uint32_t>(sh.cand[threadIdx.x]) : 0;
-              if (warp * 32 < static_cast<int>(n_l)) {
-                for (uint32_t j = 0; j < n_l; ++j) {
-                  const uint64_t x = sh.wts[j];
-                  total += x;
-                  if (static_cast<uint32_t>(sh.cand[j]) >= mine_idx) upto_me += x;  // (~index)
-                }
-              }
-              bool rest;
-              if (threadIdx.x < n_l && upto_me > mul_floor(sh.u, total, rest))
-                atomicMin(&sh.ans[r.par].t, ~mine_idx);
-            } else {
-            for (uint32_t i = threadIdx.x; i < n_l; i += r.nt)
-              sh.cand[i] = (sh.cand[i] << 32) | i;  // ~index descends as the index ascends
-            __syncthreads();
-            r.sort_desc(sh.cand, n_l);
-            if (warp == 0) {
-              uint64_t total = 0;
-              for (uint32_t i = lane; i < n_l; i += 32) total += sh.wts[i];
-              bool rest;
-              const uint64_t target = mul_floor(sh.u, warp_sum(total), rest);
-              uint64_t run = 0;
-              for (uint32_t i0 = 0; i0 < n_l; i0 += 32) {
-                const uint32_t i = i0 + lane;
-                const uint64_t c = i < n_l ? sh.cand[i] : 0;
-                const uint64_t x = i < n_l ? sh.wts[static_cast<uint32_t>(c)] : 0;
-                const uint32_t hit = __ballot_sync(0xffffffffu, run + warp_scan(x, lane) > target);
-                if (hit) {
-                  const uint32_t at = ~static_cast<uint32_t>(
-                      __shfl_sync(0xffffffffu, c, __ffs(hit) - 1) >> 32);
-                  if (lane == 0) sh.ans[r.par].t = at;
-                  break;
-                }
-                run += warp_sum(x);
-              }
-            }
-            }
-          }
+          listed = drawn = true;
+          if (r.rank == 0) draw_from_list<T>(r, n_all, true, mass_q, 2 * E, true);
         }
       } else {
         // ---- many tokens stay: the cut falls in bins b1 to b2, whose tokens are
@@ -827,6 +955,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         } else if (q.count > 0 && q.count <= kCap) {
           r.gather([&](float z) { return in_bin(z, b2); }, [&](float z) { return !in_bin(z, b1 - 1); });
           if (r.rank == 0) {
+            r.fetch_lists(q.count);
             r.sort_and_weigh(q.count);
             if (warp == 0) {
               uint64_t run = 0;
@@ -906,7 +1035,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
     keep.t = key_of(floor_z);
   }
 
-  if (!leader_draws) {
+  if (!drawn) {
     // ---- the draw: the mass and ties ahead of each warp, then the one that holds u
     Part all = S;
     if (keep.t != 0) {
@@ -932,27 +1061,62 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
     bool rest;
     const uint64_t target = mul_floor(sh.u, all.mass + min(all.count, lim) * wt, rest);
     if (m + min(e, lim) * wt <= target && m + mine.mass + min(e + mine.count, lim) * wt > target) {
+      // the mass and ties of a lane's piece
+      auto piece = [&](int v, const Vec<T>& x, uint64_t& s, uint32_t& eq) {
+        s = 0;
+        eq = 0;
+        if (v >= r.v1 || !(keep.t == 0 || key_of(x.max()) >= keep.t)) return;
+        float f = 0.f;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          const float z = x.get(i);
+          const uint32_t key = key_of(z);
+          if (EXACT) s += key > keep.t ? weight(w, z) : 0;
+          else f += key > keep.t ? fast_weight(fast_y(w, z)) : 0.f;
+          eq += key == keep.t;
+        }
+        if (!EXACT) s = static_cast<uint64_t>(__float2ll_rn(f * w.one));
+      };
+      // four steps of the warp at a time, until one holds the target
+      int vb = r.v0;
       bool done = false;
-      for (int vb = r.v0; vb < r.v1 && !done; vb += 32) {
+      for (; vb < r.v1 && !done; ) {
+        uint64_t s4[4];
+        uint32_t e4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int v = vb + 32 * i + lane;
+          Vec<T> x;
+          if (v < r.v1) x = r.load(v);
+          piece(v, x, s4[i], e4[i]);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s4[i] += __shfl_xor_sync(0xffffffffu, s4[i], o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e4[i] = __reduce_add_sync(0xffffffffu, e4[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!done) {
+            if (m + s4[i] + min(e + e4[i], lim) * wt > target) {
+              done = true;
+            } else {
+              m += s4[i];
+              e += e4[i];
+              vb += 32;
+            }
+          }
+        }
+      }
+      if (done) {
+        done = false;
         const int v = vb + lane;
         uint64_t s = 0;
         uint32_t eq = 0;
         Vec<T> x;
-        if (v < r.v1) {
-          x = r.load(v);
-          if (keep.t == 0 || key_of(x.max()) >= keep.t) {
-            float f = 0.f;
-#pragma unroll
-            for (int i = 0; i < VE; ++i) {
-              const float z = x.get(i);
-              const uint32_t key = key_of(z);
-              if (EXACT) s += key > keep.t ? weight(w, z) : 0;
-              else f += key > keep.t ? fast_weight(fast_y(w, z)) : 0.f;
-              eq += key == keep.t;
-            }
-            if (!EXACT) s = static_cast<uint64_t>(__float2ll_rn(f * w.one));
-          }
-        }
+        if (v < r.v1) x = r.load(v);
+        piece(v, x, s, eq);
         const uint64_t s_in = m + warp_scan(s, lane);
         uint32_t e_in = eq;
 #pragma unroll
@@ -967,6 +1131,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
           if (lane == __ffs(hit) - 1) {
             uint64_t sm = s_in - s;
             uint32_t se = e_in - eq;
+            bool found = false;
             for (int i = 0; i < VE; ++i) {
               const float z = x.get(i);
               const uint32_t key = key_of(z);
@@ -978,19 +1143,21 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
                 // a border within E of u: left to the exact weights
                 if (E && (now - target <= 2 * E || distance(target, was) <= 2 * E)) lead->bad = 1;
                 lead->t = static_cast<uint32_t>(r.pos0 + static_cast<int64_t>(v) * VE + i);
+                found = true;
                 break;
               }
             }
+            if (!found) lead->bad = 1;  // (float sums: a piece's and its elements' differ)
           }
         }
-        m = __shfl_sync(0xffffffffu, s_in, 31);
-        e = __shfl_sync(0xffffffffu, e_in, 31);
       }
       if (!EXACT && !done && lane == 0) lead->bad = 1;  // the float sums disagree by their rounding
     }
   }
-  r.cl.sync();
-  if (!EXACT && r.cl.map_shared_rank(&sh, 0)->ans[r.par].bad) return false;
+  if (!synced) {
+    r.cl.sync();
+    if (!EXACT && r.cl.map_shared_rank(&sh, 0)->ans[r.par].bad) return false;
+  }
   if (r.rank == 0 && threadIdx.x == 0) {
     const int64_t at = sh.ans[r.par].t;
     const float z = clean(to_f(r.row[at]));
@@ -1026,8 +1193,8 @@ __device__ __noinline__ float min_logit(Weigher w, float temp, float q) {
 // The rare way, apart from the common one's registers.
 template <typename T>
 __device__ __noinline__ int decide_exact(Row<T> r, const SampleArgs& a, int64_t row, uint32_t kmax,
-                                         float my_max, bool hist) {
-  decide<T, true>(r, a, row, kmax, my_max, hist);
+                                         float my_max, bool hist, bool listing, float from) {
+  decide<T, true>(r, a, row, kmax, my_max, hist, listing, from);
   return r.turn;
 }
 
@@ -1065,12 +1232,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
     r.global = reinterpret_cast<const uint4*>(z - off) + p0;
     r.slice = resident ? s_slice : nullptr;
 
-    float prm_t = 1.f, prm_p = 1.f, prm_q = 0.f, prm_u = 0.f;
-    int prm_k = 0;
+    const float prm_t = a.temperature ? __ldg(a.temperature + row) : 1.f;
+    const float prm_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
+    const int prm_k = a.top_k ? __ldg(a.top_k + row) : 0;
+    float prm_q = 0.f, prm_u = 0.f;
     if (threadIdx.x == 0) {
-      if (a.temperature) prm_t = a.temperature[row];
-      if (a.top_k) prm_k = a.top_k[row];
-      if (a.top_p) prm_p = a.top_p[row];
       if (a.min_p) prm_q = a.min_p[row];
       prm_u = a.u[row];
     }
@@ -1078,20 +1244,21 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
     // ---- copy the slice, taking the maximum on the way (a warp reads back its own)
     float mx = -INFINITY;
     {
-      // the pieces that lie inside the row, four loads in flight a thread
+      // the pieces that lie inside the row, all on their way at once
       const int f0 = max(r.v0, r.full0), f1 = min(r.v1, r.full1);
-      for (int v = f0 + r.lane; v < f1; v += 128) {
-        Vec<T> x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (v + 32 * i < f1) x[i].raw = __ldg(r.global + v + 32 * i);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (v + 32 * i < f1) {
-            if (resident) s_slice[v + 32 * i] = x[i].raw;
-            mx = fmaxf(mx, x[i].max());
-          }
-        }
+      if (resident) {
+        for (int v = f0 + r.lane; v < f1; v += 32)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           static_cast<uint32_t>(__cvta_generic_to_shared(s_slice + v))),
+                       "l"(r.global + v)
+                       : "memory");
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+      }
+#pragma unroll 4
+      for (int v = f0 + r.lane; v < f1; v += 32) {  // (each lane reads its own copies)
+        Vec<T> x;
+        x.raw = resident ? s_slice[v] : __ldg(r.global + v);
+        mx = fmaxf(mx, x.max());
       }
       // and the ones at its ends
       for (int v = r.v0 + r.lane; v < r.v1; v += 32) {
@@ -1104,6 +1271,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
     if (threadIdx.x == 0) {
       sh.ans[r.par].bad = 0;
       sh.upto_valid = 0;
+      sh.n_cand = 0;
       sh.warm = prm_t > 0.f;
       const float temp = sh.warm ? prm_t : 1.f;
       sh.temp = temp;
@@ -1124,9 +1292,33 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
       sh.u = fminf(fmaxf(prm_u, 0.f), 1.f - 5.9604645e-8f);
     }
     __syncwarp();
+    // A list of candidates is made where few tokens can stay: the one of a greedy
+    // row, top-k's, and with top-p alone a first guess. The k largest of the warps'
+    // maxima, or with larger k the warps' own j-th largest lane maxima, are k logits
+    // of the row at least: candidates lie from the smallest of them on.
+    const int kk = !(prm_t > 0.f) ? 1 : prm_k > 0 && prm_k < a.V ? prm_k : prm_p < 1.f ? kGuess : 0;
+    const int n_warps = r.C * r.nw, j = (kk + n_warps - 1) / n_warps;
+    const bool listing = kk > 0 && kk <= kCap / 2 && j <= 32;
     Part p;
     p.hi = key_of(mx);
-    const uint32_t kmax = r.template join<P_HI>(p).hi;
+    if (listing && j > 1) {
+      const uint32_t mine[1] = {p.hi};
+      p.lo = kth_from_below<1>(mine, j);
+    }
+    const Part tops = r.template join<P_HI | P_LO>(p);
+    const uint32_t kmax = tops.hi;
+    float from = 0.f;
+    if (listing) {
+      uint32_t key = kk == 1 ? kmax : tops.lo;
+      if (kk > 1 && j == 1) {
+        const Part* slots = r.parts + (r.turn ^ 1) * kMaxCluster * r.nw;  // that join's
+        uint32_t top[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = r.lane + 32 * i < n_warps ? slots[r.lane + 32 * i].hi : 0;
+        key = kth_from_below<4>(top, kk);
+      }
+      from = float_of(max(key, key_of(-INFINITY)));
+    }
     const float zmax = float_of(kmax);
     if (zmax == -INFINITY) {  // nothing to choose from
       if (r.rank == 0 && threadIdx.x == 0) {
@@ -1140,10 +1332,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
       sh.floor_z = !sh.use_q ? -INFINITY : prm_q >= 1.f ? zmax : min_logit(sh.w, sh.temp, prm_q);
     }
     const bool fast = zmax < INFINITY && slice_vecs * VE <= kMaxFast;
-    if (!fast || !decide<T, false>(r, a, row, kmax, mx, true)) {
+    if (!fast || !decide<T, false>(r, a, row, kmax, mx, true, listing, from)) {
       // (the cluster's CTAs leave a row that was not decided at the same point)
       r.cl.sync();
-      r.turn = decide_exact<T>(r, a, row, kmax, mx, fast);
+      r.turn = decide_exact<T>(r, a, row, kmax, mx, fast, listing, from);
     }
     r.par ^= 1;
   }
