@@ -111,6 +111,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 template <>
 __device__ __forceinline__ uint64_t Vec<float>::pair(int e) const {
   return e == 0 ? pair_of(raw.x, raw.y) : pair_of(raw.z, raw.w);
@@ -175,33 +180,63 @@ __device__ __forceinline__ void exp2_pair(const float2* tab, float p, float pl, 
 // as a pair of floats, and the fixed point's scale.
 struct Weigher {
   float zmax, c_hi, c_lo, one;  // one = 2^B
+  float d_min;                  // z - zmax where y = -120
   int down;                     // 44 - B
   const float2* tab;
 };
 
-// W = round(2^(y + B)), 0 below y = -40. The argument error is 2^-46 |y|.
-__device__ __forceinline__ uint64_t weight_inline(const Weigher& w, float z) {
-  if (z == w.zmax) return static_cast<uint64_t>(__float2ll_rn(w.one));
+// W = round(2^(y + B)) of two logits, 0 below y = -40 and for NaN. The steps are
+// those of exp2_pair, for both at once; the argument error is 2^-46 |y|.
+__device__ __forceinline__ void weight2(const Weigher& w, uint64_t z, uint64_t& w0, uint64_t& w1) {
+  const uint64_t neg = pair_of(-1.f), c = pair_of(w.c_hi), top = pair_of(-w.zmax);
   // z - zmax without loss: the difference and what its rounding left
-  const float d = __fsub_rn(z, w.zmax);
-  const float b = __fsub_rn(d, z);
-  const float dl = __fsub_rn(z, __fsub_rn(d, b)) + __fsub_rn(-w.zmax, b);
-  const float p = __fmul_rn(d, w.c_hi);
-  if (!(p >= -40.5f)) return 0;
-  const float pl = __fmaf_rn(d, w.c_hi, -p) + __fmaf_rn(d, w.c_lo, dl * w.c_hi);
-  if (p + pl < kCut || (p == kCut && pl < 0.f)) return 0;
-  int n;
-  float h, hl;
-  exp2_pair(w.tab, p, pl, n, h, hl);
+  const uint64_t d = add2(z, top), b = fma2(z, neg, d);
+  const uint64_t dl = add2(fma2(fma2(b, neg, d), neg, z), fma2(b, neg, top));
+  const uint64_t p = mul2(d, c);
+  const uint64_t pl = add2(fma2(d, c, mul2(p, neg)), fma2(d, pair_of(w.c_lo), mul2(dl, c)));
+  const float2 pf = of_pair(p);
+  const uint64_t y = pair_of(__float_as_uint(fmaxf(pf.x, -41.f)), __float_as_uint(fmaxf(pf.y, -41.f)));
+  // y = k / 32 + r, |r| <= 1/64
+  const uint64_t kt = fma2(y, pair_of(32.f), pair_of(12582912.f));
+  const uint64_t r0 = fma2(add2(kt, pair_of(-12582912.f)), pair_of(-0.03125f), y);
+  const uint64_t r = add2(r0, pl), rl = fma2(fma2(r0, neg, r), neg, pl);
+  const uint64_t ln2 = pair_of(kLn2), half = pair_of(0.5f);
+  const uint64_t x = mul2(r, ln2);
+  const uint64_t xl = add2(fma2(r, ln2, mul2(x, neg)), fma2(r, pair_of(kLn2Lo), mul2(rl, ln2)));
+  const uint64_t xx = mul2(x, x);
+  const uint64_t xxl = fma2(x, add2(xl, xl), fma2(x, x, mul2(xx, neg)));
+  const uint64_t q3 = fma2(x, fma2(x, fma2(x, pair_of(1.f / 720.f), pair_of(1.f / 120.f)), pair_of(1.f / 24.f)),
+                           pair_of(1.f / 6.f));
+  const uint64_t cubic = mul2(mul2(xx, x), q3);
+  const uint64_t s = fma2(xx, half, x);
+  const uint64_t sl = add2(fma2(xx, half, fma2(s, neg, x)), fma2(xxl, half, add2(xl, cubic)));
+  const float2 ktf = of_pair(kt);
+  const uint32_t k0 = __float_as_uint(ktf.x), k1 = __float_as_uint(ktf.y);  // 0x4B400000 + k
+  const float2 t0 = w.tab[k0 & 31], t1 = w.tab[k1 & 31];
+  const uint64_t tx = pair_of(__float_as_uint(t0.x), __float_as_uint(t1.x));
+  const uint64_t ty = pair_of(__float_as_uint(t0.y), __float_as_uint(t1.y));
+  const uint64_t q = mul2(tx, s);
+  const uint64_t ql = add2(fma2(tx, s, mul2(q, neg)), fma2(tx, sl, mul2(ty, s)));
+  const uint64_t h = add2(tx, q);
+  const uint64_t hl = add2(fma2(fma2(tx, neg, h), neg, q), add2(ql, ty));
   // 2^44 (h + hl), h in [0.98, 2) with 24 bits behind the point at most; then
   // down by 44 - B - n
-  const uint64_t w0 = (static_cast<uint64_t>(__float2uint_rn(h * 16777216.f)) << 20) +
-                      static_cast<int64_t>(__float2int_rn(hl * 17592186044416.f));
-  const int down = w.down - n;
-  return (w0 + ((1ull << down) >> 1)) >> down;
+  const float2 hf = of_pair(mul2(h, pair_of(16777216.f))), lf = of_pair(mul2(hl, pair_of(17592186044416.f)));
+  auto fixed = [&](float hi, float lo, uint32_t k, float pp, float zz) {
+    const uint64_t v = (static_cast<uint64_t>(__float2uint_rn(hi)) << 20) + static_cast<int64_t>(__float2int_rn(lo));
+    const int down = w.down - (static_cast<int>(k - 0x4B400000u) >> 5);
+    const uint64_t r = (v + ((1ull << down) >> 1)) >> down;
+    return zz == w.zmax ? static_cast<uint64_t>(__float2ll_rn(w.one)) : pp >= kCut ? r : 0;
+  };
+  const float2 zf = of_pair(z);
+  w0 = fixed(hf.x, lf.x, k0, pf.x, zf.x);
+  w1 = fixed(hf.y, lf.y, k1, pf.y, zf.y);
 }
-
-__device__ __noinline__ uint64_t weight(Weigher w, float z) { return weight_inline(w, z); }
+__device__ __noinline__ uint64_t weight(Weigher w, float z) {
+  uint64_t a, b;
+  weight2(w, pair_of(z), a, b);
+  return a;
+}
 
 // floor and ceiling of f x for 0 <= f < 1: exact
 __device__ __forceinline__ uint64_t mul_floor(float f, uint64_t x, bool& rest) {
@@ -227,18 +262,50 @@ __device__ __forceinline__ uint64_t mul_ceil(float f, uint64_t x) {
 }
 __device__ __forceinline__ uint64_t distance(uint64_t a, uint64_t b) { return a > b ? a - b : b - a; }
 
-// The fast weight's y = (z - zmax) log2(e) / T (zmax finite). Its error is
-// 3 * 2^-24 |y| (three roundings), that of 2^y 2^-22: together
-// w (4 + 2.1 |y|) 2^-24. It has no cut at 2^-40; what it has below is V 2^-40 at
-// most.
+// y in single precision, for the bins.
 __device__ __forceinline__ float fast_y(const Weigher& w, float z) { return (z - w.zmax) * w.c_hi; }
-__device__ __forceinline__ float fast_weight(float y) { return ex2_approx(fmaxf(y, -200.f)); }
+
+// The fast weight, 2^(n + f): n = round(d log2(e) / T) by adding 1.5 * 2^23, f what
+// the product leaves, 2^f = 1 + f q(f) with q of degree 5, fitted to 2^-28.9. In
+// units of 2^-24 its error is 1.3 for 2^f, 0.4 for f and 0.7 |y| for d = z - zmax
+// (exact for bf16 logits, but for |z| below 2^-16 |zmax|). It has no cut at 2^-40;
+// what it has below is V 2^-40 at most. (The special-function unit's 2^y is four
+// times less exact: one row in seven of a spread-out softmax was left to the exact
+// weights.)
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+#define SAMPLE_Q {0x1.62e430p-1f, 0x1.ebfbdcp-3f, 0x1.c6aee8p-5f, 0x1.3b2d4cp-7f, 0x1.5f3e58p-10f, 0x1.41fbc8p-13f}
+__device__ __forceinline__ float fast_weight(const Weigher& w, float z) {
+  const float d = fmaxf(z - w.zmax, w.d_min);
+  const float t = __fmaf_rn(d, w.c_hi, kRound);
+  const float f = __fmaf_rn(d, w.c_lo, __fmaf_rn(d, w.c_hi, -__fsub_rn(t, kRound)));
+  const float k[6] = SAMPLE_Q;
+  float q = k[5];
+#pragma unroll
+  for (int i = 4; i >= 0; --i) q = __fmaf_rn(q, f, k[i]);
+  return __uint_as_float(__float_as_uint(__fmaf_rn(q, f, 1.f)) + (__float_as_uint(t) << 23));
+}
+// The same of two logits.
+__device__ __forceinline__ uint64_t fast_weight2(uint64_t z, uint64_t top, float d_min, uint64_t c_hi,
+                                                 uint64_t c_lo) {
+  const float2 d0 = of_pair(add2(z, top));
+  const uint64_t d = pair_of(__float_as_uint(fmaxf(d0.x, d_min)), __float_as_uint(fmaxf(d0.y, d_min)));
+  const uint64_t t = fma2(d, c_hi, pair_of(kRound));
+  const uint64_t n = add2(t, pair_of(-kRound));
+  const uint64_t f = fma2(d, c_lo, fma2(d, c_hi, mul2(n, pair_of(-1.f))));
+  const float k[6] = SAMPLE_Q;
+  uint64_t q = pair_of(k[5]);
+#pragma unroll
+  for (int i = 4; i >= 0; --i) q = fma2(q, f, pair_of(k[i]));
+  const float2 r = of_pair(fma2(q, f, pair_of(1.f))), e = of_pair(t);
+  return pair_of(__float_as_uint(r.x) + (__float_as_uint(e.x) << 23),
+                 __float_as_uint(r.y) + (__float_as_uint(e.y) << 23));
+}
 
 // Element weight as an integer.
 template <bool EXACT>
 __device__ __forceinline__ uint64_t weigh(const Weigher& w, float z) {
   if (EXACT) return weight(w, z);
-  return static_cast<uint64_t>(__float2ll_rn(fast_weight(fast_y(w, z)) * w.one));
+  return static_cast<uint64_t>(__float2ll_rn(fast_weight(w, z) * w.one));
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
@@ -302,6 +369,11 @@ struct Shared {
   float floor_z, top_p, u, temp;
   int top_k, warm, use_p, use_q;
 };
+
+template <typename T>
+struct Row;
+template <typename T, typename F>
+__device__ __noinline__ uint64_t exact_mass(const Row<T> r, const Weigher w, F some);
 
 // One row, seen from one CTA.
 template <typename T>
@@ -435,12 +507,8 @@ struct Row {
   template <bool MASS>
   __device__ Part above(const Weigher& w, uint32_t k) {
     Part p;
-    each([&](float z) {
-      if (key_of(z) > k) {
-        ++p.count;
-        if (MASS) p.mass += weight(w, z);
-      }
-    });
+    each_if([&](float z) { return key_of(z) > k; }, [&](float z) { p.count += key_of(z) > k; });
+    if (MASS) p.mass = exact_mass<T>(*this, w, [k](float z) { return key_of(z) > k; });
     return join<MASS ? P_MASS | P_COUNT : P_COUNT>(p);
   }
 
@@ -532,6 +600,27 @@ struct Row {
       }
   }
 };
+
+// The exact mass of this thread's elements that `some` accepts (from some logit
+// on: a piece's maximum is asked first); in a function of its own, whose
+// registers are the weights'.
+template <typename T, typename F>
+__device__ __noinline__ uint64_t exact_mass(const Row<T> r, const Weigher w, F some) {
+  uint64_t m = 0;
+  for (int v = r.v0 + r.lane; v < r.v1; v += 32) {
+    const Vec<T> x = r.load(v);
+    if (!some(x.max())) continue;
+#pragma unroll 2
+    for (int e = 0; e < Vec<T>::N / 2; ++e) {
+      const uint64_t z = x.pair(e);
+      uint64_t a, b;
+      weight2(w, z, a, b);
+      const float2 f = of_pair(z);
+      m += (some(clean(f.x)) ? a : 0) + (some(clean(f.y)) ? b : 0);
+    }
+  }
+  return m;
+}
 
 // Threshold and ties that the cut-offs keep.
 struct Kept {
@@ -718,24 +807,18 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
     }
   };
   if (EXACT) {
-    for (int v = r.v0 + lane; v < r.v1; v += 32) {
-      const Vec<T> x = r.load(v);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) p.mass += weight_inline(w, x.get(e));
-      list(x, v);
-    }
+    p.mass = exact_mass<T>(r, w, [](float) { return true; });
+    if (listing)
+      for (int v = r.v0 + lane; v < r.v1; v += 32) list(r.load(v), v);
   } else {
     PairSum all;
-    const uint64_t top = pair_of(-w.zmax), scale = pair_of(w.c_hi);
+    const uint64_t top = pair_of(-w.zmax), c_hi = pair_of(w.c_hi), c_lo = pair_of(w.c_lo);
 #pragma unroll 2
     for (int v = r.v0 + lane; v < r.v1; v += 32) {
       const Vec<T> x = r.load(v);
       uint64_t s[VE / 2];
 #pragma unroll
-      for (int i = 0; i < VE / 2; ++i) {
-        const float2 y = of_pair(mul2(add2(x.pair(i), top), scale));  // as fast_y
-        s[i] = pair_of(__float_as_uint(fast_weight(y.x)), __float_as_uint(fast_weight(y.y)));
-      }
+      for (int i = 0; i < VE / 2; ++i) s[i] = fast_weight2(x.pair(i), top, w.d_min, c_hi, c_lo);
 #pragma unroll
       for (int o = 1; o < VE / 2; o <<= 1)
 #pragma unroll
@@ -750,27 +833,31 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
   const Part S = r.template join<P_MASS | P_COUNT>(p, &mine, &before);
   const uint32_t n_list = S.count;
   const float floor_z = sh.floor_z;  // min-p keeps logits from here on (-inf: off)
-  // Bound on the error of any sum of weights, in units of W: 2^-24 sum w
-  // (4 + 2.1 |y|), three more roundings in the sum of a piece; and since the
-  // entropy of w / S is at most log2 V, sum w |y| <= S log2(V / S).
+  // Bound on the error of any sum of weights, in units of W: 2^-24 sum w (1.7 +
+  // 0.7 |y|), and three roundings in the sum of a piece. The entropy of w / S is at
+  // most log2 V, so sum w |y| <= S log2(V / S); for bf16 the term with |y| is left
+  // only for logits around 0, whose weights are 2^(-zmax log2(e) / T).
   uint64_t E = 0;
   if (!EXACT && warm) {
-    const float s = static_cast<float>(S.mass) / w.one;
-    E = static_cast<uint64_t>(__float2ll_ru(
-            s * (8.f + 2.2f * fmaxf(0.f, log2f(static_cast<float>(r.V) / s))) * 6.0e-8f * w.one)) +
-        static_cast<uint64_t>(__float2ll_ru(static_cast<float>(r.V) * 1e-12f * w.one)) + 2 * r.V + 1024;
+    const float s = static_cast<float>(S.mass) / w.one, V = static_cast<float>(r.V);
+    const float y0 = fmaxf(0.f, w.zmax * w.c_hi);
+    const float terms = sizeof(T) == 4 ? s * (5.5f + 0.8f * fmaxf(0.f, log2f(V / s)))
+                                       : s * 5.5f + V * ex2_approx(-y0) * fminf(y0, 200.f);
+    E = static_cast<uint64_t>(__float2ll_ru((terms * 6.0e-8f + V * 1e-12f) * w.one)) + 2 * r.V + 1024;
   }
   // and of those that min-p keeps, where the top-p cut is taken of these
   uint64_t mass_q = S.mass;
   if (use_p && sh.use_q && !use_k && warm) {
     Part q;
-    PairSum kept;
-    r.each_if([&](float z) { return z >= floor_z; }, [&](float z) {
-      if (!(z >= floor_z)) return;
-      if (EXACT) q.mass += weight(w, z);
-      else kept.add(fast_weight(fast_y(w, z)));
-    });
-    if (!EXACT) q.mass = kept.fixed(w.one);
+    if (EXACT) {
+      q.mass = exact_mass<T>(r, w, [=](float z) { return z >= floor_z; });
+    } else {
+      PairSum kept;
+      r.each_if([&](float z) { return z >= floor_z; }, [&](float z) {
+        if (z >= floor_z) kept.add(fast_weight(w, z));
+      });
+      q.mass = kept.fixed(w.one);
+    }
     mass_q = r.template join<P_MASS>(q).mass;
   }
   const float mass2 = static_cast<float>(mass_q) / w.one;
@@ -799,7 +886,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
   } else if (use_k || use_p) {
     bool listed = false;
     // the tokens of bins up to b that min-p keeps
-    auto in_bin = [&](float z, int b) {
+    auto in_bin = [w, floor_z](float z, int b) {
       const float y = fast_y(w, z);
       return y >= kCut && z >= floor_z && min(Row<T>::bin_of(y), kBins - 1) <= b;
     };
@@ -931,7 +1018,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         r.each_if([&](float z) { return in_bin(z, b2); }, [&](float z) {
           if (!in_bin(z, b2)) return;
           if (in_bin(z, b1 - 1)) {
-            q.mass += weigh<EXACT>(w, z);
+            if (!EXACT) q.mass += weigh<EXACT>(w, z);
           } else {
             const uint32_t key = key_of(z);
             ++q.count;
@@ -939,6 +1026,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
             q.hi = max(q.hi, key);
           }
         });
+        if (EXACT) q.mass = exact_mass<T>(r, w, [=](float z) { return in_bin(z, b1 - 1); });
         q = r.template join<P_MASS | P_COUNT | P_LO | P_HI>(q);
         const uint64_t want = mul_ceil(sh.top_p, mass_q);
         const uint64_t rest = want > q.mass ? want - q.mass : 0;
@@ -1043,13 +1131,11 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
       PairSum f;
       r.each_if([&](float z) { return key_of(z) >= keep.t; }, [&](float z) {
         const uint32_t key = key_of(z);
-        if (key > keep.t) {
-          if (EXACT) q.mass += weight(w, z);
-          else f.add(fast_weight(fast_y(w, z)));
-        }
+        if (!EXACT && key > keep.t) f.add(fast_weight(w, z));
         q.count += key == keep.t;
       });
-      if (!EXACT) q.mass = f.fixed(w.one);
+      const uint32_t t = keep.t;
+      q.mass = EXACT ? exact_mass<T>(r, w, [t](float z) { return key_of(z) > t; }) : f.fixed(w.one);
       all = r.template join<P_MASS | P_COUNT>(q, &mine, &before);
     }
     auto* lead = &r.cl.map_shared_rank(&sh, 0)->ans[r.par];
@@ -1072,7 +1158,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
           const float z = x.get(i);
           const uint32_t key = key_of(z);
           if (EXACT) s += key > keep.t ? weight(w, z) : 0;
-          else f += key > keep.t ? fast_weight(fast_y(w, z)) : 0.f;
+          else f += key > keep.t ? fast_weight(w, z) : 0.f;
           eq += key == keep.t;
         }
         if (!EXACT) s = static_cast<uint64_t>(__float2ll_rn(f * w.one));
@@ -1198,8 +1284,9 @@ __device__ __noinline__ int decide_exact(Row<T> r, const SampleArgs& a, int64_t 
   return r.turn;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant__ SampleArgs a, int slice_vecs, int resident) {
+// (three CTAs of 256 threads on an SM, or one of 512)
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_sample(const __grid_constant__ SampleArgs a, int slice_vecs, int resident) {
   extern __shared__ uint4 s_slice[];
   __shared__ Shared sh;
   constexpr int VE = Vec<T>::N;
@@ -1279,6 +1366,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
       const float c = fminf(fmaxf(kLog2e / temp, 1.4e-45f), 3.4e38f);
       sh.w.c_hi = c;
       sh.w.c_lo = c > 1e-30f && c < 1e30f ? (__fmaf_rn(-c, temp, kLog2e) + kLog2eLo) / temp : 0.f;
+      sh.w.d_min = -120.f / c;
       // V 2^B < 2^62
       const int bits = min(44, 62 - (32 - __clz(static_cast<int>(a.V))));
       sh.w.one = __uint_as_float(static_cast<uint32_t>(127 + bits) << 23);
@@ -1331,7 +1419,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_sample(const __grid_constant
       sh.w.zmax = zmax;
       sh.floor_z = !sh.use_q ? -INFINITY : prm_q >= 1.f ? zmax : min_logit(sh.w, sh.temp, prm_q);
     }
-    const bool fast = zmax < INFINITY && slice_vecs * VE <= kMaxFast;
+    // (a T near 0 or infinity is the exact way's)
+    const bool fast = zmax < INFINITY && slice_vecs * VE <= kMaxFast && sh.w.c_hi > 1e-30f && sh.w.c_hi < 1e30f;
     if (!fast || !decide<T, false>(r, a, row, kmax, mx, true, listing, from)) {
       // (the cluster's CTAs leave a row that was not decided at the same point)
       r.cl.sync();
@@ -1357,15 +1446,18 @@ cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t s) {
   const int threads = a.rows * C <= sms ? 512 : 256;
   const size_t smem = (resident ? static_cast<size_t>(slice) * 16 : 0) +
                       2 * kMaxCluster * (threads / 32) * sizeof(Part);
+  auto kernel = threads == 512 ? k_sample<T, 512> : k_sample<T, 256>;
   static std::atomic<uint64_t> configured{0};  // one bit a device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(configured.load() & bit)) {
-    e = cudaFuncSetAttribute(k_sample<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxSliceBytes + 2 * kMaxCluster * kMaxWarps * static_cast<int>(sizeof(Part)));
-    if (e != cudaSuccess) return e;
+    for (auto k : {k_sample<T, 512>, k_sample<T, 256>}) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kMaxSliceBytes + 2 * kMaxCluster * kMaxWarps * static_cast<int>(sizeof(Part)));
+      if (e != cudaSuccess) return e;
+    }
     configured.fetch_or(bit);
   }
   cudaLaunchConfig_t cfg = {};
@@ -1381,7 +1473,7 @@ cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t s) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_sample<T>, a, static_cast<int>(slice), resident ? 1 : 0);
+  return cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(slice), resident ? 1 : 0);
 }
 
 }  // namespace
