@@ -24,6 +24,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <stdlib.h>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -34,15 +35,16 @@ namespace grpo {
 
 namespace {
 
-constexpr int kMaxThreads = 512;               // a CTA has 512 threads or 256
+constexpr int kMaxThreads = 512;               // of a CTA: 256 or 512
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 8;                 // the portable cluster size
 constexpr int kBins = 1280;                    // (five a thread at most) 1/32 of a binary order each, down to 2^-40
 constexpr int kCap = 1024;                     // candidates that one CTA sorts
 constexpr int kGuess = 96;                      // candidates asked for with top-p alone
 constexpr int kCount = 256;                    // and those that it sorts by counting
+constexpr int kSliceBytes = 33 * 1024;
 constexpr int kMaxSliceBytes = 192 * 1024;     // of a row's slice kept in shared memory
-constexpr int kMaxFast = 1 << 19;              // elements of a slice that the bins' sums can take
+constexpr int kMaxFast = 500000;              // elements of a slice that the bins' sums can take
 constexpr float kCut = -40.f;                  // binary orders below the top that weigh nothing
 
 // 2^(j/32), j = 0..31, each as the sum of two floats.
@@ -361,6 +363,7 @@ struct Shared {
   } ans[2];
   // this CTA's scratch
   uint32_t scan_u[kMaxWarps];
+  uint64_t base;
   int b, b1, b2;                    // bins of the top-p cut, for both ways of weighing
   uint32_t upto, n_kept;
   int upto_valid;
@@ -370,13 +373,13 @@ struct Shared {
   int top_k, warm, use_p, use_q;
 };
 
-template <typename T>
+template <typename T, bool ONE>
 struct Row;
-template <typename T, typename F>
-__device__ __noinline__ uint64_t exact_mass(const Row<T> r, const Weigher w, F some);
+template <typename T, bool ONE, typename F>
+__device__ __noinline__ uint64_t exact_mass(const Row<T, ONE> r, const Weigher w, F some);
 
-// One row, seen from one CTA.
-template <typename T>
+// One row, seen from one CTA. ONE: the row has one CTA and no cluster.
+template <typename T, bool ONE>
 struct Row {
   static constexpr int VE = Vec<T>::N;
   cg::cluster_group cl = cg::this_cluster();
@@ -419,14 +422,30 @@ struct Row {
     return x;
   }
 
-  // f(z) for this warp's elements; (step, lane, e) is their index order.
-  template <typename F>
-  __device__ __forceinline__ void each(F f) const {
-    for (int v = v0 + lane; v < v1; v += 32) {
-      const Vec<T> x = load(v);
+  // f(piece, its number) for this warp's pieces, U loads at a time; (step, lane,
+  // element) is their index order.
+  template <int U = 1, typename F>
+  __device__ __forceinline__ void pieces(F f) const {
+#pragma unroll 1
+    for (int vb = v0 + lane; vb < v1; vb += 32 * U) {
+      Vec<T> x[U];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) f(x.get(e));
+      for (int i = 0; i < U; ++i)
+        if (vb + 32 * i < v1) x[i] = load(vb + 32 * i);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (vb + 32 * i < v1) f(x[i], vb + 32 * i);
     }
+  }
+
+  // Waits for the row's CTAs, whose writes are then seen.
+  __device__ __forceinline__ void sync() {
+    if (ONE) __syncthreads();
+    else cl.sync();
+  }
+  template <typename U>
+  __device__ __forceinline__ U* of_rank(U* p, int k) {
+    return ONE ? p : cl.map_shared_rank(p, k);
   }
 
   template <int F>
@@ -473,9 +492,9 @@ struct Row {
     lanes<F>(p);
     if (mine) *mine = p;
     const int n = C * nw, me = rank * nw + warp;
-    Part* slots = parts + turn * kMaxCluster * nw;
-    if (lane < C) put<F>(*cl.map_shared_rank(slots + me, lane), p);
-    cl.sync();
+    Part* slots = parts + turn * (ONE ? 1 : kMaxCluster) * nw;
+    if (lane < C) put<F>(*of_rank(slots + me, lane), p);
+    sync();
     Part all, ahead;
     for (int i = lane; i < n; i += 32) {
       Part o;
@@ -495,12 +514,11 @@ struct Row {
   // f(z) for the pieces whose largest element passes `some`.
   template <typename P, typename F>
   __device__ __forceinline__ void each_if(P some, F f) const {
-    for (int v = v0 + lane; v < v1; v += 32) {
-      const Vec<T> x = load(v);
-      if (!some(x.max())) continue;
+    pieces([&](const Vec<T>& x, int) {
+      if (!some(x.max())) return;
 #pragma unroll
       for (int e = 0; e < VE; ++e) f(x.get(e));
-    }
+    });
   }
 
   // Number of tokens with key above k, and their mass.
@@ -508,7 +526,7 @@ struct Row {
   __device__ Part above(const Weigher& w, uint32_t k) {
     Part p;
     each_if([&](float z) { return key_of(z) > k; }, [&](float z) { p.count += key_of(z) > k; });
-    if (MASS) p.mass = exact_mass<T>(*this, w, [k](float z) { return key_of(z) > k; });
+    if (MASS) p.mass = exact_mass<T, ONE>(*this, w, [k](float z) { return key_of(z) > k; });
     return join<MASS ? P_MASS | P_COUNT : P_COUNT>(p);
   }
 
@@ -528,9 +546,8 @@ struct Row {
   template <typename F, typename G>
   __device__ uint32_t gather(F accept, G also) {
     Part p;
-    for (int v = v0 + lane; v < v1; v += 32) {
-      const Vec<T> x = load(v);
-      if (!accept(x.max())) continue;
+    pieces([&](const Vec<T>& x, int v) {
+      if (!accept(x.max())) return;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
         const float z = x.get(e);
@@ -539,19 +556,19 @@ struct Row {
           ++p.count;
         }
       }
-    }
+    });
     return join<P_COUNT>(p).count;
   }
 
   // The leader fetches the other CTAs' lists, n <= kCap candidates in all.
   __device__ void fetch_lists(uint32_t n) {
-    if (static_cast<int>(threadIdx.x) < C) sh.scan_u[threadIdx.x] = *cl.map_shared_rank(&sh.n_cand, threadIdx.x);
+    if (static_cast<int>(threadIdx.x) < C) sh.scan_u[threadIdx.x] = *of_rank(&sh.n_cand, threadIdx.x);
     __syncthreads();
     for (uint32_t i = sh.scan_u[0] + threadIdx.x; i < n; i += nt) {
       uint32_t j = i;
       int c = 0;
       while (j >= sh.scan_u[c]) j -= sh.scan_u[c++];
-      sh.cand[i] = cl.map_shared_rank(sh.cand, c)[j];
+      sh.cand[i] = of_rank(sh.cand, c)[j];
     }
     __syncthreads();
   }
@@ -604,11 +621,14 @@ struct Row {
 // The exact mass of this thread's elements that `some` accepts (from some logit
 // on: a piece's maximum is asked first); in a function of its own, whose
 // registers are the weights'.
-template <typename T, typename F>
-__device__ __noinline__ uint64_t exact_mass(const Row<T> r, const Weigher w, F some) {
+template <typename T, bool ONE, typename F>
+__device__ __noinline__ uint64_t exact_mass(const Row<T, ONE> r, const Weigher w, F some) {
   uint64_t m = 0;
+  Vec<T> next;
+  if (r.v0 + r.lane < r.v1) next = r.load(r.v0 + r.lane);
   for (int v = r.v0 + r.lane; v < r.v1; v += 32) {
-    const Vec<T> x = r.load(v);
+    const Vec<T> x = next;
+    if (v + 32 < r.v1) next = r.load(v + 32);
     if (!some(x.max())) continue;
 #pragma unroll 2
     for (int e = 0; e < Vec<T>::N / 2; ++e) {
@@ -669,17 +689,70 @@ __device__ __forceinline__ uint32_t kth_from_below(const uint32_t (&key)[N], uin
   return prefix;
 }
 
+// Bound on the error of any sum of fast weights, in units of W: 2^-24 sum w (1.7 +
+// 0.7 |y|), and three roundings in the sum of a piece. The entropy of w / S is at
+// most log2 V, so sum w |y| <= S log2(V / S); for bf16 the term with |y| is left
+// only for logits around 0, whose weights are 2^(-zmax log2(e) / T).
+template <typename T>
+__device__ __forceinline__ uint64_t error_bound(const Weigher& w, uint64_t mass, int64_t V) {
+  const float s = static_cast<float>(mass) / w.one, v = static_cast<float>(V);
+  const float y0 = fmaxf(0.f, w.zmax * w.c_hi);
+  const float terms = sizeof(T) == 4 ? s * (5.5f + 0.8f * fmaxf(0.f, log2f(v / s)))
+                                     : s * 5.5f + v * ex2_approx(-y0) * fminf(y0, 200.f);
+  return static_cast<uint64_t>(__float2ll_ru((terms * 6.0e-8f + v * 1e-12f) * w.one)) + 2 * V + 1024;
+}
+
+// The row's parameters (one thread; zmax and the min-p floor follow).
+__device__ __forceinline__ void set_row(Shared& sh, float t, int k, float p, bool use_q, float u,
+                                        int64_t V) {
+  sh.upto_valid = 0;
+  sh.n_cand = 0;
+  sh.warm = t > 0.f;
+  const float temp = sh.warm ? t : 1.f;
+  sh.temp = temp;
+  // log2(e) / T, kept within float's range (a T near 0, an infinite one)
+  const float c = fminf(fmaxf(kLog2e / temp, 1.4e-45f), 3.4e38f);
+  sh.w.c_hi = c;
+  sh.w.c_lo = c > 1e-30f && c < 1e30f ? (__fmaf_rn(-c, temp, kLog2e) + kLog2eLo) / temp : 0.f;
+  sh.w.d_min = -120.f / c;
+  // V 2^B < 2^62
+  const int bits = min(44, 62 - (32 - __clz(static_cast<int>(V))));
+  sh.w.one = __uint_as_float(static_cast<uint32_t>(127 + bits) << 23);
+  sh.w.down = 44 - bits;
+  sh.w.tab = sh.tab;
+  sh.top_k = k > 0 && k < V ? k : 0;
+  sh.use_q = use_q;
+  sh.use_p = p < 1.f;
+  sh.top_p = fmaxf(p, 0.f);
+  sh.u = fminf(fmaxf(u, 0.f), 1.f - 5.9604645e-8f);
+}
+
+// The token of a row and its log-probability (one thread).
+template <typename T>
+__device__ __forceinline__ void write_row(const SampleArgs& a, int64_t row, const T* logits, const Shared& sh,
+                                          const Weigher& w, uint64_t mass, int par = 0) {
+  const int64_t at = sh.ans[par].t;
+  const float z = clean(to_f(logits[at]));
+  const float d = z == w.zmax ? 0.f : (z - w.zmax) / sh.temp;
+  // ln(mass): the sum as two floats
+  const float hi = static_cast<float>(mass);
+  const float lo = static_cast<float>(static_cast<int64_t>(mass - static_cast<uint64_t>(hi)));
+  a.tokens[row] = static_cast<int32_t>(at);
+  a.logp[row] = d - (logf(hi / w.one) + lo / hi);
+}
+
+constexpr int32_t kUndecided = -2;  // marks a row that is left for a second launch
+
 // How the leader's list served: the token is in ans.t; or u or the top-p cut is
 // within the error of a border; or the top-p cut is behind the list's end.
 enum : int { L_DONE = 0, L_CLOSE = 1, L_SHORT = 2 };
 
-// The leader alone draws from its list of n candidates, exactly. top_k > 0: the
-// list holds the k first tokens. Else with use_p: `base` is the mass that the
-// top-p cut is taken of, off by slack at most, and `whole` says whether the list
-// holds every token that the cut can keep.
-template <typename T>
-__device__ __noinline__ void draw_from_list(Row<T> r, uint32_t n, bool warm, uint64_t base,
-                                            uint64_t slack, bool whole) {
+// The leader alone draws from its list of n candidates, exactly. With top-k the
+// list holds the k first tokens, with `whole` every token that can stay. `own`: the
+// top-p cut is taken of the list's mass; else of `base`, off by slack at most.
+template <typename T, bool ONE>
+__device__ __noinline__ void draw_from_list(Row<T, ONE> r, uint32_t n, bool warm, uint64_t base,
+                                            uint64_t slack, bool whole, bool own) {
   Shared& sh = r.sh;
   const int lane = r.lane, warp = r.warp;
   const bool use_k = !warm || sh.top_k > 0, use_p = warm && sh.use_p;
@@ -698,7 +771,7 @@ __device__ __noinline__ void draw_from_list(Row<T> r, uint32_t n, bool warm, uin
     }
     int state = L_DONE;
     if (use_p) {
-      if (use_k) {  // the mass is this list's
+      if (own || use_k) {
         base = 0;
         for (uint32_t i = lane; i < n_l; i += 32) base += sh.wts[i];
         base = warp_sum(base);
@@ -775,8 +848,8 @@ __device__ __noinline__ void draw_from_list(Row<T> r, uint32_t n, bool warm, uin
 // One row with one way of weighing. `from`: with a list to be made, the logit
 // from which on tokens are candidates. Returns whether the token is decided;
 // with EXACT it always is. Every thread of the cluster returns the same.
-template <typename T, bool EXACT>
-__device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t row, uint32_t kmax,
+template <typename T, bool ONE, bool EXACT>
+__device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int64_t row, uint32_t kmax,
                                     float my_max, bool hist, bool listing, float from) {
   constexpr int VE = Vec<T>::N;
   Shared& sh = r.sh;
@@ -807,15 +880,12 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
     }
   };
   if (EXACT) {
-    p.mass = exact_mass<T>(r, w, [](float) { return true; });
-    if (listing)
-      for (int v = r.v0 + lane; v < r.v1; v += 32) list(r.load(v), v);
+    p.mass = exact_mass<T, ONE>(r, w, [](float) { return true; });
+    if (listing) r.pieces(list);
   } else {
     PairSum all;
     const uint64_t top = pair_of(-w.zmax), c_hi = pair_of(w.c_hi), c_lo = pair_of(w.c_lo);
-#pragma unroll 2
-    for (int v = r.v0 + lane; v < r.v1; v += 32) {
-      const Vec<T> x = r.load(v);
+    r.pieces([&](const Vec<T>& x, int v) {
       uint64_t s[VE / 2];
 #pragma unroll
       for (int i = 0; i < VE / 2; ++i) s[i] = fast_weight2(x.pair(i), top, w.d_min, c_hi, c_lo);
@@ -826,31 +896,21 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
       const float2 t = of_pair(s[0]);
       all.add(t.x + t.y);
       list(x, v);
-    }
+    });
     p.mass = all.fixed(w.one);
   }
   Part mine, before;
   const Part S = r.template join<P_MASS | P_COUNT>(p, &mine, &before);
   const uint32_t n_list = S.count;
   const float floor_z = sh.floor_z;  // min-p keeps logits from here on (-inf: off)
-  // Bound on the error of any sum of weights, in units of W: 2^-24 sum w (1.7 +
-  // 0.7 |y|), and three roundings in the sum of a piece. The entropy of w / S is at
-  // most log2 V, so sum w |y| <= S log2(V / S); for bf16 the term with |y| is left
-  // only for logits around 0, whose weights are 2^(-zmax log2(e) / T).
-  uint64_t E = 0;
-  if (!EXACT && warm) {
-    const float s = static_cast<float>(S.mass) / w.one, V = static_cast<float>(r.V);
-    const float y0 = fmaxf(0.f, w.zmax * w.c_hi);
-    const float terms = sizeof(T) == 4 ? s * (5.5f + 0.8f * fmaxf(0.f, log2f(V / s)))
-                                       : s * 5.5f + V * ex2_approx(-y0) * fminf(y0, 200.f);
-    E = static_cast<uint64_t>(__float2ll_ru((terms * 6.0e-8f + V * 1e-12f) * w.one)) + 2 * r.V + 1024;
-  }
+  const uint64_t E = EXACT || !warm ? 0 : error_bound<T>(w, S.mass, r.V);
   // and of those that min-p keeps, where the top-p cut is taken of these
+  const bool floored = sh.use_q && !use_k;  // the list is of all logits from min-p's floor on
   uint64_t mass_q = S.mass;
-  if (use_p && sh.use_q && !use_k && warm) {
+  if (use_p && floored && !(listing && n_list <= kCap)) {
     Part q;
     if (EXACT) {
-      q.mass = exact_mass<T>(r, w, [=](float z) { return z >= floor_z; });
+      q.mass = exact_mass<T, ONE>(r, w, [=](float z) { return z >= floor_z; });
     } else {
       PairSum kept;
       r.each_if([&](float z) { return z >= floor_z; }, [&](float z) {
@@ -866,15 +926,15 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
   bool drawn = false, synced = false;  // the leader has the token; and all know it
   if (listing && n_list <= kCap) {
     // ---- few candidates: the leader finishes the row with exact weights
-    if (r.rank == 0) draw_from_list<T>(r, n_list, warm, mass_q, 2 * E, false);
+    if (r.rank == 0) draw_from_list<T, ONE>(r, n_list, warm, mass_q, 2 * E, floored, floored);
     drawn = true;
-    if (warm && !use_k) {  // (the top-p cut may fall behind the list)
-      r.cl.sync();
-      const int state = r.cl.map_shared_rank(&sh, 0)->ans[r.par].bad;
+    if (warm && !use_k && !floored) {  // (the top-p cut may fall behind the list)
+      r.sync();
+      const int state = r.of_rank(&sh, 0)->ans[r.par].bad;
       if (state == L_CLOSE) return false;
       drawn = synced = state == L_DONE;
       if (!drawn) {
-        r.cl.sync();  // all have read it
+        r.sync();  // all have read it
         if (threadIdx.x == 0) sh.ans[r.par].bad = 0;
       }
     }
@@ -888,7 +948,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
     // the tokens of bins up to b that min-p keeps
     auto in_bin = [w, floor_z](float z, int b) {
       const float y = fast_y(w, z);
-      return y >= kCut && z >= floor_z && min(Row<T>::bin_of(y), kBins - 1) <= b;
+      return y >= kCut && z >= floor_z && min(Row<T, ONE>::bin_of(y), kBins - 1) <= b;
     };
     if (hist) {
       for (int i = threadIdx.x; i < kBins; i += r.nt) sh.hist[i] = make_uint2(0, 0);
@@ -909,7 +969,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         // threads number k / C; the lowest of these bins over the slices is down
         // to k tokens in all, and not many more.
         const float y = fast_y(w, my_max);
-        if (y >= kCut) atomicAdd(&sh.hist[min(Row<T>::bin_of(y), kBins - 1)].x, 1u);
+        if (y >= kCut) atomicAdd(&sh.hist[min(Row<T, ONE>::bin_of(y), kBins - 1)].x, 1u);
         __syncthreads();
         Part q;
         q.hi = local_bin(sh, (sh.top_k + r.C - 1) / r.C, lane, warp, r.nt);
@@ -917,7 +977,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
       } else {
         // Tokens lighter than (1 - p) mass / V sum to less than (1 - p) mass.
         const float y = log2f(fmaxf(0.5f * (1.f - sh.top_p) * mass2 / static_cast<float>(r.V), 1e-30f));
-        b_cut = y > kCut ? min(Row<T>::bin_of(fminf(y, 0.f)) + 1, kBins - 1) : kBins - 1;
+        b_cut = y > kCut ? min(Row<T, ONE>::bin_of(fminf(y, 0.f)) + 1, kBins - 1) : kBins - 1;
       }
       // With a small k these candidates are few enough to be sorted; else they
       // are counted and weighed by bins.
@@ -929,12 +989,12 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         r.each_if([&](float z) { return in_bin(z, b_cut); }, [&](float z) {
           if (!in_bin(z, b_cut)) return;
           const float y = fast_y(w, z);
-          const int b = min(Row<T>::bin_of(y), kBins - 1);
+          const int b = min(Row<T, ONE>::bin_of(y), kBins - 1);
           atomicAdd(&sh.hist[b].x, 1u);
           // the weight over the bin's own: 13 bits or more
           if (!use_k) atomicAdd(&sh.hist[b].y, __float2uint_rn(ex2_approx(y + 0.03125f * b + r.hist_bits)));
         });
-        r.cl.sync();
+        r.sync();
         // Running sums: this CTA adds up its share of the bins over the slices,
         // five bins a thread or fewer.
         const int share = (b_cut + r.C) / r.C, per = (share + r.nt - 1) / r.nt;
@@ -949,7 +1009,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
           if (i < per && j < share && b <= b_cut) {
             uint64_t mm = 0;
             for (int c = 0; c < r.C; ++c) {
-              const uint2 h = r.cl.map_shared_rank(sh.hist, c)[b];
+              const uint2 h = r.of_rank(sh.hist, c)[b];
               n[i] += h.x;
               mm += h.y;
             }
@@ -1009,7 +1069,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         const uint32_t n_all = r.gather([&](float z) { return in_bin(z, b2); }, [](float) { return true; });
         if (n_all <= kCap) {
           listed = drawn = true;
-          if (r.rank == 0) draw_from_list<T>(r, n_all, true, mass_q, 2 * E, true);
+          if (r.rank == 0) draw_from_list<T, ONE>(r, n_all, true, mass_q, 2 * E, true, false);
         }
       } else {
         // ---- many tokens stay: the cut falls in bins b1 to b2, whose tokens are
@@ -1026,7 +1086,7 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
             q.hi = max(q.hi, key);
           }
         });
-        if (EXACT) q.mass = exact_mass<T>(r, w, [=](float z) { return in_bin(z, b1 - 1); });
+        if (EXACT) q.mass = exact_mass<T, ONE>(r, w, [=](float z) { return in_bin(z, b1 - 1); });
         q = r.template join<P_MASS | P_COUNT | P_LO | P_HI>(q);
         const uint64_t want = mul_ceil(sh.top_p, mass_q);
         const uint64_t rest = want > q.mass ? want - q.mass : 0;
@@ -1070,8 +1130,8 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
               }
             }
           }
-          r.cl.sync();
-          const auto& lead = r.cl.map_shared_rank(&sh, 0)->ans[r.par];
+          r.sync();
+          const auto& lead = r.of_rank(&sh, 0)->ans[r.par];
           keep.t = lead.t;
           keep.ties = lead.ties;
           listed = lead.bad == 0;
@@ -1135,10 +1195,10 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
         q.count += key == keep.t;
       });
       const uint32_t t = keep.t;
-      q.mass = EXACT ? exact_mass<T>(r, w, [t](float z) { return key_of(z) > t; }) : f.fixed(w.one);
+      q.mass = EXACT ? exact_mass<T, ONE>(r, w, [t](float z) { return key_of(z) > t; }) : f.fixed(w.one);
       all = r.template join<P_MASS | P_COUNT>(q, &mine, &before);
     }
-    auto* lead = &r.cl.map_shared_rank(&sh, 0)->ans[r.par];
+    auto* lead = &r.of_rank(&sh, 0)->ans[r.par];
     // (CTAs and warps are in index order)
     uint64_t m = before.mass;
     uint32_t e = before.count;
@@ -1241,19 +1301,10 @@ __device__ __forceinline__ bool decide(Row<T>& r, const SampleArgs& a, int64_t r
     }
   }
   if (!synced) {
-    r.cl.sync();
-    if (!EXACT && r.cl.map_shared_rank(&sh, 0)->ans[r.par].bad) return false;
+    r.sync();
+    if (!EXACT && r.of_rank(&sh, 0)->ans[r.par].bad) return false;
   }
-  if (r.rank == 0 && threadIdx.x == 0) {
-    const int64_t at = sh.ans[r.par].t;
-    const float z = clean(to_f(r.row[at]));
-    const float d = z == w.zmax ? 0.f : (z - w.zmax) / sh.temp;
-    // ln(mass): the sum as two floats
-    const float hi = static_cast<float>(S.mass);
-    const float lo = static_cast<float>(static_cast<int64_t>(S.mass - static_cast<uint64_t>(hi)));
-    a.tokens[row] = static_cast<int32_t>(at);
-    a.logp[row] = d - (logf(hi / w.one) + lo / hi);
-  }
+  if (r.rank == 0 && threadIdx.x == 0) write_row(a, row, r.row, sh, w, S.mass, r.par);
   return true;
 }
 
@@ -1277,32 +1328,33 @@ __device__ __noinline__ float min_logit(Weigher w, float temp, float q) {
 }
 
 // The rare way, apart from the common one's registers.
-template <typename T>
-__device__ __noinline__ int decide_exact(Row<T> r, const SampleArgs& a, int64_t row, uint32_t kmax,
+template <typename T, bool ONE>
+__device__ __noinline__ int decide_exact(Row<T, ONE> r, const SampleArgs& a, int64_t row, uint32_t kmax,
                                          float my_max, bool hist, bool listing, float from) {
-  decide<T, true>(r, a, row, kmax, my_max, hist, listing, from);
+  decide<T, ONE, true>(r, a, row, kmax, my_max, hist, listing, from);
   return r.turn;
 }
 
 // (three CTAs of 256 threads on an SM, or one of 512)
-template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_sample(const __grid_constant__ SampleArgs a, int slice_vecs, int resident) {
+template <typename T, int THREADS, bool ONE>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) k_sample(const __grid_constant__ SampleArgs a, int slice_vecs, int resident, int rest) {  // rest: the marked rows only
   extern __shared__ uint4 s_slice[];
   __shared__ Shared sh;
   constexpr int VE = Vec<T>::N;
-  Row<T> r(sh);
+  Row<T, ONE> r(sh);
   r.lane = threadIdx.x & 31;
   r.warp = threadIdx.x >> 5;
   r.nt = blockDim.x;
   r.nw = blockDim.x >> 5;
-  r.C = static_cast<int>(r.cl.num_blocks());
-  r.rank = static_cast<int>(r.cl.block_rank());
+  r.C = ONE ? 1 : static_cast<int>(r.cl.num_blocks());
+  r.rank = ONE ? 0 : static_cast<int>(r.cl.block_rank());
   r.V = a.V;
   r.hist_bits = slice_vecs * VE <= 131072 ? 15.f : 13.f;
   r.parts = reinterpret_cast<Part*>(s_slice + (resident ? slice_vecs : 0));
   if (threadIdx.x < 32) sh.tab[threadIdx.x] = c_exp2_32[threadIdx.x];
   const int n_cl = gridDim.x / r.C;
   for (int64_t row = blockIdx.x / r.C; row < a.rows; row += n_cl) {
+    if (rest && a.tokens[row] != kUndecided) continue;
     const T* z = static_cast<const T*>(a.logits) + row * a.ld;
     // 16-byte pieces from the one that holds the row's first element
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
@@ -1322,11 +1374,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_sample(cons
     const float prm_t = a.temperature ? __ldg(a.temperature + row) : 1.f;
     const float prm_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
     const int prm_k = a.top_k ? __ldg(a.top_k + row) : 0;
-    float prm_q = 0.f, prm_u = 0.f;
-    if (threadIdx.x == 0) {
-      if (a.min_p) prm_q = a.min_p[row];
-      prm_u = a.u[row];
-    }
+    const float prm_q = a.min_p ? __ldg(a.min_p + row) : 0.f;
+    const float prm_u = threadIdx.x == 0 ? a.u[row] : 0.f;
 
     // ---- copy the slice, taking the maximum on the way (a warp reads back its own)
     float mx = -INFINITY;
@@ -1341,11 +1390,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_sample(cons
                        : "memory");
         asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
       }
-#pragma unroll 4
-      for (int v = f0 + r.lane; v < f1; v += 32) {  // (each lane reads its own copies)
-        Vec<T> x;
-        x.raw = resident ? s_slice[v] : __ldg(r.global + v);
-        mx = fmaxf(mx, x.max());
+      for (int vb = f0 + r.lane; vb < f1; vb += 256) {  // (each lane reads its own copies)
+        Vec<T> x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (vb + 32 * i < f1) x[i].raw = resident ? s_slice[vb + 32 * i] : __ldg(r.global + vb + 32 * i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (vb + 32 * i < f1) mx = fmaxf(mx, x[i].max());
       }
       // and the ones at its ends
       for (int v = r.v0 + r.lane; v < r.v1; v += 32) {
@@ -1355,51 +1407,35 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_sample(cons
         mx = fmaxf(mx, x.max());
       }
     }
+    // weights below 2^-40 are 0: a lower q keeps every token that counts
+    const bool use_q = prm_q >= 9.094947e-13f && prm_t > 0.f;
     if (threadIdx.x == 0) {
       sh.ans[r.par].bad = 0;
-      sh.upto_valid = 0;
-      sh.n_cand = 0;
-      sh.warm = prm_t > 0.f;
-      const float temp = sh.warm ? prm_t : 1.f;
-      sh.temp = temp;
-      // log2(e) / T, kept within float's range (a T near 0, an infinite one)
-      const float c = fminf(fmaxf(kLog2e / temp, 1.4e-45f), 3.4e38f);
-      sh.w.c_hi = c;
-      sh.w.c_lo = c > 1e-30f && c < 1e30f ? (__fmaf_rn(-c, temp, kLog2e) + kLog2eLo) / temp : 0.f;
-      sh.w.d_min = -120.f / c;
-      // V 2^B < 2^62
-      const int bits = min(44, 62 - (32 - __clz(static_cast<int>(a.V))));
-      sh.w.one = __uint_as_float(static_cast<uint32_t>(127 + bits) << 23);
-      sh.w.down = 44 - bits;
-      sh.w.tab = sh.tab;
-      sh.top_k = prm_k > 0 && prm_k < a.V ? prm_k : 0;
-      // weights below 2^-40 are 0: a lower q keeps every token that counts
-      sh.use_q = prm_q >= 9.094947e-13f && sh.warm;
-      sh.use_p = prm_p < 1.f;
-      sh.top_p = fmaxf(prm_p, 0.f);
-      sh.u = fminf(fmaxf(prm_u, 0.f), 1.f - 5.9604645e-8f);
+      set_row(sh, prm_t, prm_k, prm_p, use_q, prm_u, a.V);
     }
     __syncwarp();
     // A list of candidates is made where few tokens can stay: the one of a greedy
-    // row, top-k's, and with top-p alone a first guess. The k largest of the warps'
-    // maxima, or with larger k the warps' own j-th largest lane maxima, are k logits
-    // of the row at least: candidates lie from the smallest of them on.
-    const int kk = !(prm_t > 0.f) ? 1 : prm_k > 0 && prm_k < a.V ? prm_k : prm_p < 1.f ? kGuess : 0;
+    // row, top-k's, those from min-p's floor on, and with top-p alone a first guess.
+    // The k largest of the warps' maxima, or with larger k the warps' own j-th largest
+    // lane maxima, are k logits of the row at least: candidates lie from the smallest
+    // of them on.
+    const bool has_k = prm_k > 0 && prm_k < a.V, floored = use_q && !has_k;
+    const int kk = !(prm_t > 0.f) ? 1 : has_k ? prm_k : prm_p < 1.f ? kGuess : 0;
     const int n_warps = r.C * r.nw, j = (kk + n_warps - 1) / n_warps;
-    const bool listing = kk > 0 && kk <= kCap / 2 && j <= 32;
+    const bool listing = floored || (kk > 0 && kk <= kCap / 2 && j <= 32);
     Part p;
     p.hi = key_of(mx);
-    if (listing && j > 1) {
+    if (listing && !floored && j > 1) {
       const uint32_t mine[1] = {p.hi};
       p.lo = kth_from_below<1>(mine, j);
     }
     const Part tops = r.template join<P_HI | P_LO>(p);
     const uint32_t kmax = tops.hi;
     float from = 0.f;
-    if (listing) {
+    if (listing && !floored) {
       uint32_t key = kk == 1 ? kmax : tops.lo;
       if (kk > 1 && j == 1) {
-        const Part* slots = r.parts + (r.turn ^ 1) * kMaxCluster * r.nw;  // that join's
+        const Part* slots = r.parts + (r.turn ^ 1) * (ONE ? 1 : kMaxCluster) * r.nw;  // that join's
         uint32_t top[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) top[i] = r.lane + 32 * i < n_warps ? slots[r.lane + 32 * i].hi : 0;
@@ -1417,54 +1453,295 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_sample(cons
     }
     if (threadIdx.x == 0) {  // (read behind the next join)
       sh.w.zmax = zmax;
-      sh.floor_z = !sh.use_q ? -INFINITY : prm_q >= 1.f ? zmax : min_logit(sh.w, sh.temp, prm_q);
+      sh.floor_z = !use_q ? -INFINITY : prm_q >= 1.f ? zmax : min_logit(sh.w, sh.temp, prm_q);
+    }
+    if (floored) {
+      __syncthreads();
+      from = sh.floor_z;
     }
     // (a T near 0 or infinity is the exact way's)
     const bool fast = zmax < INFINITY && slice_vecs * VE <= kMaxFast && sh.w.c_hi > 1e-30f && sh.w.c_hi < 1e30f;
-    if (!fast || !decide<T, false>(r, a, row, kmax, mx, true, listing, from)) {
-      // (the cluster's CTAs leave a row that was not decided at the same point)
-      r.cl.sync();
-      r.turn = decide_exact<T>(r, a, row, kmax, mx, fast, listing, from);
+    if (!fast || !decide<T, ONE, false>(r, a, row, kmax, mx, true, listing, from)) {
+      r.sync();  // (a row's CTAs leave it at the same point where it was not decided)
+      r.turn = decide_exact<T, ONE>(r, a, row, kmax, mx, fast, listing, from);
     }
     r.par ^= 1;
   }
-  r.cl.sync();  // no CTA leaves while another may read its shared memory
+  r.sync();  // no CTA leaves while another may read its shared memory
 }
 
+// Many rows: a CTA takes a row and reads it once for the maximum and the mass (each
+// lane weighs against the largest logit it has seen, and scales its sum down when a
+// larger one comes), and, as a rule from L2, once more for the candidates. Greedy, top-k,
+// min-p and plain softmax rows end here, and top-p rows whose cut is within the
+// list; what is left is marked for k_sample, whose clusters take it row by row.
+constexpr int kRowThreads = 256;
 template <typename T>
-cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t s) {
+__global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows(const __grid_constant__ SampleArgs a) {
+  __shared__ Shared sh;
+  __shared__ Part s_parts[2 * (kRowThreads / 32)];
+  __shared__ uint64_t s_chunk[kRowThreads / 32];
+  __shared__ uint32_t s_hits;
+  __shared__ int s_hit[kCap];
+  constexpr int VE = Vec<T>::N;
+  Row<T, true> r(sh);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  r.lane = lane;
+  r.warp = warp;
+  r.nt = kRowThreads;
+  r.nw = kRowThreads / 32;
+  r.C = 1;
+  r.rank = 0;
+  r.V = a.V;
+  r.parts = s_parts;
+  r.slice = nullptr;
+  r.hist_bits = 13.f;
+  const int64_t row = blockIdx.x;
+  const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
+  r.n_vec = static_cast<int>((off + a.V + VE - 1) / VE);
+  r.pos0 = -off;
+  const int per = (r.n_vec + r.nw - 1) / r.nw;
+  r.v0 = min(r.n_vec, warp * per);
+  r.v1 = min(r.n_vec, r.v0 + per);
+  r.full0 = off ? 1 : 0;
+  r.full1 = static_cast<int>((a.V + off) / VE);
+  r.row = z;
+  r.global = reinterpret_cast<const uint4*>(z - off);
+
+  const float prm_t = a.temperature ? __ldg(a.temperature + row) : 1.f;
+  const float prm_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
+  const float prm_q = a.min_p ? __ldg(a.min_p + row) : 0.f;
+  const int prm_k = a.top_k ? __ldg(a.top_k + row) : 0;
+  const bool warm = prm_t > 0.f, use_q = prm_q >= 9.094947e-13f && warm, has_k = prm_k > 0 && prm_k < a.V;
+  const bool floored = use_q && !has_k;
+  const int kk = !warm ? 1 : has_k ? prm_k : prm_p < 1.f ? kGuess : 0;
+  const int j = (kk + r.nw - 1) / r.nw;
+  const bool listing = floored || (kk > 0 && kk <= kCap / 2 && j <= 32);
+  if (threadIdx.x < 32) sh.tab[threadIdx.x] = c_exp2_32[threadIdx.x];
+  if (threadIdx.x == 0) s_hits = 0;
+  if (threadIdx.x == 0) set_row(sh, prm_t, prm_k, prm_p, use_q, a.u[row], a.V);
+
+  __syncthreads();
+  // ---- the maximum and the mass
+  Weigher w = sh.w;
+  float mx = -INFINITY, err = 0.f;  // err: what the scalings rounded, in units of 2^-24
+  PairSum all;
+  {
+    const uint64_t c_hi = pair_of(w.c_hi), c_lo = pair_of(w.c_lo);
+    for (int vb = r.v0 + lane; vb < r.v1; vb += 128) {
+      Vec<T> x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i].raw = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (vb + 32 * i < r.v1) x[i] = r.fetch(vb + 32 * i);
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (vb + 32 * i < r.v1) m = fmaxf(m, x[i].max());
+      if (m > mx) {
+        w.zmax = m;
+        const float f = mx > -INFINITY ? fast_weight(w, mx) : 0.f;
+        err = (err + 4.f * all.hi) * f;
+        all.hi *= f;
+        all.lo *= f;
+        mx = m;
+      }
+      const uint64_t top = pair_of(-mx);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (vb + 32 * i < r.v1 && mx > -INFINITY) {
+          uint64_t s[VE / 2];
+#pragma unroll
+          for (int k = 0; k < VE / 2; ++k) s[k] = fast_weight2(x[i].pair(k), top, w.d_min, c_hi, c_lo);
+#pragma unroll
+          for (int o = 1; o < VE / 2; o <<= 1)
+#pragma unroll
+            for (int k = 0; k + o < VE / 2; k += 2 * o) s[k] = add2(s[k], s[k + o]);
+          const float2 u = of_pair(s[0]);
+          all.add(u.x + u.y);
+        }
+      }
+    }
+  }
+  Part p;
+  p.hi = key_of(mx);
+  if (listing && !floored && j > 1) {
+    const uint32_t mine[1] = {p.hi};
+    p.lo = kth_from_below<1>(mine, j);
+  }
+  const Part tops = r.template join<P_HI | P_LO>(p);
+  const uint32_t kmax = tops.hi;
+  const float zmax = float_of(kmax);
+  if (zmax == -INFINITY) {  // nothing to choose from
+    if (threadIdx.x == 0) {
+      a.tokens[row] = -1;
+      a.logp[row] = -INFINITY;
+    }
+    return;
+  }
+  float from = INFINITY;
+  if (listing && !floored) {
+    uint32_t key = kk == 1 ? kmax : tops.lo;
+    if (kk > 1 && j == 1) {
+      const uint32_t top[1] = {lane < r.nw ? s_parts[(r.turn ^ 1) * r.nw + lane].hi : 0};
+      key = kth_from_below<1>(top, kk);
+    }
+    from = float_of(max(key, key_of(-INFINITY)));
+  }
+  if (threadIdx.x == 0) {  // (read behind the next barrier)
+    sh.w.zmax = zmax;
+    sh.floor_z = !use_q ? -INFINITY : prm_q >= 1.f ? zmax : min_logit(sh.w, sh.temp, prm_q);
+  }
+  if (floored) {
+    __syncthreads();
+    from = sh.floor_z;
+  }
+  bool decided = false;
+  w.zmax = zmax;
+  uint64_t mass = 0;
+  if (zmax < INFINITY && w.c_hi > 1e-30f && w.c_hi < 1e30f) {
+    Part q;
+    if (mx > -INFINITY) {  // from the lane's largest logit to the row's
+      const float f = fast_weight(w, mx);
+      q.sum = (err + 4.f * all.hi) * f;
+      all.hi *= f;
+      all.lo *= f;
+      q.mass = all.fixed(w.one);
+    }
+    // ---- the list: the pieces that hold candidates, their tokens below
+    if (listing) {
+      for (int vb = r.v0 + lane; vb < r.v1; vb += 256) {
+        Vec<T> x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (vb + 32 * i < r.v1) x[i] = r.fetch(vb + 32 * i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (vb + 32 * i < r.v1 && x[i].max() >= from) {
+            const uint32_t at = atomicAdd(&s_hits, 1u);
+            if (at < kCap) s_hit[at] = vb + 32 * i;
+          }
+      }
+    }
+    Part mine, before;
+    const Part S = r.template join<P_MASS | P_SUM>(q, &mine, &before);
+    mass = S.mass;
+    bool fits = false;
+    if (listing) {
+      fits = s_hits <= kCap;
+      for (uint32_t i = threadIdx.x; fits && i < s_hits; i += kRowThreads) {
+        const int v = s_hit[i];
+        const Vec<T> x = r.load(v);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const float f = x.get(e);
+          if (f >= from && f > -INFINITY) r.list(f, v, e);
+        }
+      }
+      __syncthreads();
+      fits = fits && sh.n_cand <= kCap;
+    }
+    const uint64_t E =
+        warm ? error_bound<T>(w, S.mass, a.V) + static_cast<uint64_t>(__float2ll_ru(S.sum * 6.0e-8f * w.one)) : 0;
+    if (listing) {
+      if (fits) {
+        draw_from_list<T, true>(r, sh.n_cand, warm, S.mass, 2 * E, floored, floored);
+        __syncthreads();
+        decided = sh.ans[0].bad == L_DONE;
+      }
+    } else if (kk == 0) {
+      // ---- the draw from all tokens: the warp that holds u, then the chunk of it
+      // (every warp takes one), then the piece and the token
+      bool rest;
+      const uint64_t target = mul_floor(sh.u, S.mass, rest);
+      if (threadIdx.x == 0) sh.ans[0].bad = L_CLOSE;
+      if (before.mass <= target && before.mass + mine.mass > target && lane == 0) {
+        sh.b = warp;
+        sh.base = before.mass;
+      }
+      __syncthreads();
+      const int v0 = min(r.n_vec, sh.b * per), v1 = min(r.n_vec, v0 + per);
+      const int chunk = (per + 32 * r.nw - 1) / (32 * r.nw) * 32;  // pieces of a chunk: whole steps
+      const int c0 = min(v1, v0 + warp * chunk), c1 = min(v1, c0 + chunk);
+      auto piece = [&](int v) {
+        const Vec<T> x = r.load(v);
+        float f = 0.f;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f += fast_weight(w, x.get(e));
+        return static_cast<uint64_t>(__float2ll_rn(f * w.one));
+      };
+      uint64_t m = 0;
+      for (int v = c0 + lane; v < c1; v += 32) m += piece(v);
+      m = warp_sum(m);
+      if (lane == 0) s_chunk[warp] = m;
+      __syncthreads();
+      uint64_t ahead = sh.base;
+      for (int i = 0; i < warp; ++i) ahead += s_chunk[i];
+      if (ahead <= target && ahead + m > target) {
+        for (int vb = c0; vb < c1; vb += 32) {
+          const int v = vb + lane;
+          const uint64_t s = v < c1 ? piece(v) : 0;
+          const uint64_t upto = ahead + warp_scan(s, lane);
+          const uint32_t hit = __ballot_sync(0xffffffffu, upto > target);
+          if (hit) {
+            if (lane == __ffs(hit) - 1) {
+              const Vec<T> x = r.load(v);
+              uint64_t at = upto - s;
+              for (int e = 0; e < VE; ++e) {
+                const uint64_t was = at;
+                at += weigh<false>(w, x.get(e));
+                if (at > target) {  // a border within E of u is left to the exact weights
+                  if (at - target > 2 * E && distance(target, was) > 2 * E) {
+                    sh.ans[0].t = static_cast<uint32_t>(r.pos0 + static_cast<int64_t>(v) * VE + e);
+                    sh.ans[0].bad = L_DONE;
+                  }
+                  break;
+                }
+              }
+            }
+            break;
+          }
+          ahead = __shfl_sync(0xffffffffu, upto, 31);
+        }
+      }
+      __syncthreads();
+      decided = sh.ans[0].bad == L_DONE;
+    }
+  }
+  if (threadIdx.x == 0) {
+    if (decided) write_row(a, row, z, sh, w, mass);
+    else a.tokens[row] = kUndecided;
+  }
+}
+
+template <typename T, int THREADS, bool ONE>
+cudaError_t launch_with(const SampleArgs& a, int C, int most_clusters, int rest, cudaStream_t s) {
   constexpr int VE = 16 / static_cast<int>(sizeof(T));
-  const int64_t bytes = a.V * static_cast<int64_t>(sizeof(T)) + 15;
-  int C = 1;
-  while (C < kMaxCluster && (bytes / C > 52 * 1024 || (a.rows * C < sms && bytes / C > 16 * 1024))) C *= 2;
-  const int64_t pieces = (a.V + VE - 1) / VE + 1;  // a row may start inside its first piece
-  const int64_t slice = (pieces + C - 1) / C;
-  const bool resident = slice * 16 <= kMaxSliceBytes;
-  if (slice > INT32_MAX / VE) return cudaErrorInvalidValue;
-  // 512 threads share a slice when there are few rows; with many, 256, three such
-  // CTAs on an SM: the fixed work of a row is a warp's
-  const int threads = a.rows * C <= sms ? 512 : 256;
-  const size_t smem = (resident ? static_cast<size_t>(slice) * 16 : 0) +
-                      2 * kMaxCluster * (threads / 32) * sizeof(Part);
-  auto kernel = threads == 512 ? k_sample<T, 512> : k_sample<T, 256>;
+  auto kernel = k_sample<T, THREADS, ONE>;
+  constexpr int parts = 2 * (ONE ? 1 : kMaxCluster) * (THREADS / 32) * static_cast<int>(sizeof(Part));
   static std::atomic<uint64_t> configured{0};  // one bit a device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(configured.load() & bit)) {
-    for (auto k : {k_sample<T, 512>, k_sample<T, 256>}) {
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kMaxSliceBytes + 2 * kMaxCluster * kMaxWarps * static_cast<int>(sizeof(Part)));
-      if (e != cudaSuccess) return e;
-    }
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSliceBytes + parts);
+    if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
+  const int64_t pieces = (a.V + VE - 1) / VE + 1;  // a row may start inside its first piece
+  const int64_t slice = (pieces + C - 1) / C;
+  if (slice > INT32_MAX / VE) return cudaErrorInvalidValue;
+  // A slice stays in shared memory where four CTAs of 256 threads, or one of 512,
+  // have room for theirs; else it is read again from L2.
+  const bool resident = !ONE && slice * 16 <= (THREADS == 512 ? kMaxSliceBytes : kSliceBytes);
   cudaLaunchConfig_t cfg = {};
-  const int64_t clusters = a.rows < 65536 ? a.rows : 65536;
+  const int64_t clusters = a.rows < most_clusters ? a.rows : most_clusters;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * C));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(resident ? slice * 16 : 0) + parts;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1472,8 +1749,28 @@ cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t s) {
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(slice), resident ? 1 : 0);
+  cfg.numAttrs = ONE ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(slice), resident ? 1 : 0, rest);
+}
+
+template <typename T>
+cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t s) {
+  const int64_t bytes = a.V * static_cast<int64_t>(sizeof(T));
+  // Short rows, and rows enough for every SM: a CTA a row, which needs no cluster's
+  // barriers. What the fast weights leave of long ones is done by a second launch,
+  // many SMs a row.
+  if (bytes <= 16 * 1024) return launch_with<T, 256, true>(a, 1, 1 << 30, 0, s);
+  const char* em = getenv("SM1");
+  if (a.rows >= (em ? atoi(em) : sms) && a.V <= kMaxFast) {
+    k_sample_rows<T><<<static_cast<unsigned>(a.rows), kRowThreads, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_with<T, 256, false>(a, kMaxCluster, 4 * sms / kMaxCluster, 1, s);
+  }
+  int C = 2;
+  while (C < kMaxCluster && a.rows * C < sms && bytes / C > 16 * 1024) C *= 2;
+  if (a.rows * C <= sms) return launch_with<T, 512, false>(a, C, 65536, 0, s);
+  return launch_with<T, 256, false>(a, C, 65536, 0, s);
 }
 
 }  // namespace
