@@ -81,6 +81,12 @@ __device__ __forceinline__ float float_of(uint32_t key) {
   return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+// The float z such that a logit is above it if and only if its key is above k.
+// (Key 0x7FFFFFFF is that of -0, which no logit has: both zeros are above it.)
+__device__ __forceinline__ float above_key(uint32_t k) {
+  return k <= 0x007FFFFFu ? -INFINITY : float_of(k == 0x7FFFFFFFu ? 0x7FFFFFFEu : k);
+}
+
 // A 16-byte piece of a row.
 template <typename T>
 struct Vec {
@@ -341,19 +347,18 @@ struct PairSum {
 // What the parts of a row add up to.
 struct Part {
   uint64_t mass = 0;
-  uint64_t best = ~0ull;  // a minimum
   uint32_t count = 0;
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
   float sum = 0.f;
 };
-enum : int { P_MASS = 1, P_BEST = 2, P_COUNT = 4, P_LO = 8, P_HI = 16, P_SUM = 32 };
+enum : int { P_MASS = 1, P_COUNT = 4, P_LO = 8, P_HI = 16, P_SUM = 32 };
 
 struct Shared {
   float2 tab[32];
   uint64_t cand[kCap];              // this CTA's candidates, the leader's list: key, then ~index
   union {
     uint64_t wts[kCap];             // their weights
-    uint2 hist[kBins];              // count and mass of a bin (read before there are weights)
+    uint32_t hist[kBins];           // masses of the bins (read before there are weights)
   };
   uint32_t n_cand;
   // the leader's answers to the cluster, alternating between rows
@@ -364,9 +369,12 @@ struct Shared {
   // this CTA's scratch
   uint32_t scan_u[kMaxWarps];
   uint64_t base;
-  int b, b1, b2;                    // bins of the top-p cut, for both ways of weighing
-  uint32_t upto, n_kept;
-  int upto_valid;
+  int b;
+  uint32_t n_kept;
+  // what the fast way leaves to the exact one: the top-p cut is behind the list;
+  // it lies among the logits from z2 to z1
+  int behind, found;
+  float z1, z2;
   // the row's parameters
   Weigher w;
   float floor_z, top_p, u, temp;
@@ -375,8 +383,8 @@ struct Shared {
 
 template <typename T, bool ONE>
 struct Row;
-template <typename T, bool ONE, typename F>
-__device__ __noinline__ uint64_t exact_mass(const Row<T, ONE> r, const Weigher w, F some);
+template <typename T, bool ONE>
+__device__ __noinline__ ulonglong2 exact_mass(const Row<T, ONE> r, const Weigher w, float lo, float hi);
 
 // One row, seen from one CTA. ONE: the row has one CTA and no cluster.
 template <typename T, bool ONE>
@@ -451,7 +459,6 @@ struct Row {
   template <int F>
   __device__ __forceinline__ static void add(Part& p, const Part& o) {
     if (F & P_MASS) p.mass += o.mass;
-    if (F & P_BEST) p.best = min(p.best, o.best);
     if (F & P_SUM) p.sum += o.sum;
     if (F & P_COUNT) p.count += o.count;
     if (F & P_LO) p.lo = min(p.lo, o.lo);
@@ -460,7 +467,6 @@ struct Row {
   template <int F>
   __device__ __forceinline__ static void put(Part& to, const Part& p) {
     if (F & P_MASS) to.mass = p.mass;
-    if (F & P_BEST) to.best = p.best;
     if (F & P_SUM) to.sum = p.sum;
     if (F & P_COUNT) to.count = p.count;
     if (F & P_LO) to.lo = p.lo;
@@ -473,8 +479,7 @@ struct Row {
     for (int o = 16; o >= 1; o >>= 1) {
       Part q;
       if (F & P_MASS) q.mass = __shfl_xor_sync(0xffffffffu, p.mass, o);
-      if (F & P_BEST) q.best = __shfl_xor_sync(0xffffffffu, p.best, o);
-      if (F & P_SUM) q.sum = __shfl_xor_sync(0xffffffffu, p.sum, o);
+        if (F & P_SUM) q.sum = __shfl_xor_sync(0xffffffffu, p.sum, o);
       if (F & P_COUNT) q.count = __shfl_xor_sync(0xffffffffu, p.count, o);
       if (F & P_LO) q.lo = __shfl_xor_sync(0xffffffffu, p.lo, o);
       if (F & P_HI) q.hi = __shfl_xor_sync(0xffffffffu, p.hi, o);
@@ -521,12 +526,14 @@ struct Row {
     });
   }
 
-  // Number of tokens with key above k, and their mass.
+  // Number of tokens above key k, and their exact mass.
   template <bool MASS>
   __device__ Part above(const Weigher& w, uint32_t k) {
     Part p;
     each_if([&](float z) { return key_of(z) > k; }, [&](float z) { p.count += key_of(z) > k; });
-    if (MASS) p.mass = exact_mass<T, ONE>(*this, w, [k](float z) { return key_of(z) > k; });
+    if (MASS) {
+      p.mass = exact_mass(*this, w, above_key(k), INFINITY).x;
+    }
     return join<MASS ? P_MASS | P_COUNT : P_COUNT>(p);
   }
 
@@ -540,18 +547,15 @@ struct Row {
     if (at < kCap) sh.cand[at] = (static_cast<uint64_t>(key_of(z)) << 32) | ~idx;
   }
 
-  // Lists the elements that both functions accept (the first accepts from some
-  // logit on, so that a piece's maximum can be asked); returns their number over
-  // the cluster.
-  template <typename F, typename G>
-  __device__ uint32_t gather(F accept, G also) {
+  // Lists the elements from lo to hi; returns their number over the cluster.
+  __device__ uint32_t gather(float lo, float hi) {
     Part p;
     pieces([&](const Vec<T>& x, int v) {
-      if (!accept(x.max())) return;
+      if (!(x.max() >= lo)) return;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
         const float z = x.get(e);
-        if (accept(z) && also(z)) {
+        if (z >= lo && z <= hi) {
           list(z, v, e);
           ++p.count;
         }
@@ -618,60 +622,32 @@ struct Row {
   }
 };
 
-// The exact mass of this thread's elements that `some` accepts (from some logit
-// on: a piece's maximum is asked first); in a function of its own, whose
-// registers are the weights'.
-template <typename T, bool ONE, typename F>
-__device__ __noinline__ uint64_t exact_mass(const Row<T, ONE> r, const Weigher w, F some) {
-  uint64_t m = 0;
-  Vec<T> next;
-  if (r.v0 + r.lane < r.v1) next = r.load(r.v0 + r.lane);
+// The exact mass of this thread's elements above `lo`, and of those above `hi`; in
+// a function of its own, whose registers are the weights'.
+template <typename T, bool ONE>
+__device__ __noinline__ ulonglong2 exact_mass(const Row<T, ONE> r, const Weigher w, float lo, float hi) {
+  uint64_t m = 0, n = 0;
+#pragma unroll 1
   for (int v = r.v0 + r.lane; v < r.v1; v += 32) {
-    const Vec<T> x = next;
-    if (v + 32 < r.v1) next = r.load(v + 32);
-    if (!some(x.max())) continue;
-#pragma unroll 2
+    const Vec<T> x = r.load(v);
+    if (!(x.max() > lo)) continue;
+#pragma unroll
     for (int e = 0; e < Vec<T>::N / 2; ++e) {
       const uint64_t z = x.pair(e);
       uint64_t a, b;
       weight2(w, z, a, b);
       const float2 f = of_pair(z);
-      m += (some(clean(f.x)) ? a : 0) + (some(clean(f.y)) ? b : 0);
+      m += (f.x > lo ? a : 0) + (f.y > lo ? b : 0);
+      n += (f.x > hi ? a : 0) + (f.y > hi ? b : 0);
     }
   }
-  return m;
+  return make_ulonglong2(m, n);
 }
 
 // Threshold and ties that the cut-offs keep.
 struct Kept {
   uint32_t t = 0, ties = 0xFFFFFFFFu;
 };
-
-// The first bin of hist whose running count reaches k, kBins - 1 if none does;
-// one CTA of nt threads, five bins a thread or three.
-__device__ __forceinline__ int local_bin(Shared& sh, uint32_t k, int lane, int warp, int nt) {
-  const int per = (kBins + nt - 1) / nt, first = static_cast<int>(threadIdx.x) * per;
-  uint32_t sum = 0;
-  for (int i = 0; i < per; ++i) sum += first + i < kBins ? sh.hist[first + i].x : 0;
-  uint32_t at = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t x = __shfl_up_sync(0xffffffffu, at, o);
-    if (lane >= o) at += x;
-  }
-  if (lane == 31) sh.scan_u[warp] = at;
-  if (threadIdx.x == 0) sh.b = kBins - 1;
-  __syncthreads();
-  at -= sum;
-  for (int i = 0; i < warp; ++i) at += sh.scan_u[i];
-  if (at < k && at + sum >= k) {  // one thread at most
-    int i = 0;
-    for (; at + sh.hist[first + i].x < k; ++i) at += sh.hist[first + i].x;
-    sh.b = first + i;
-  }
-  __syncthreads();
-  return sh.b;
-}
 
 // The largest value of 16 leading bits that at least k of the warp's keys reach
 // (N a lane); 0 if fewer do.
@@ -705,7 +681,7 @@ __device__ __forceinline__ uint64_t error_bound(const Weigher& w, uint64_t mass,
 // The row's parameters (one thread; zmax and the min-p floor follow).
 __device__ __forceinline__ void set_row(Shared& sh, float t, int k, float p, bool use_q, float u,
                                         int64_t V) {
-  sh.upto_valid = 0;
+  sh.behind = sh.found = 0;
   sh.n_cand = 0;
   sh.warm = t > 0.f;
   const float temp = sh.warm ? t : 1.f;
@@ -845,12 +821,211 @@ __device__ __noinline__ void draw_from_list(Row<T, ONE> r, uint32_t n, bool warm
   }
 }
 
-// One row with one way of weighing. `from`: with a list to be made, the logit
-// from which on tokens are candidates. Returns whether the token is decided;
-// with EXACT it always is. Every thread of the cluster returns the same.
+// The smallest key t from lo to hi that `enough` holds for (it holds for hi, and
+// from some key on). bf16 logits differ in a key's upper half only.
+template <typename T, typename F>
+__device__ __forceinline__ uint32_t first_key(uint32_t lo, uint32_t hi, F enough) {
+  constexpr int SH = sizeof(T) == 2 ? 16 : 0;
+  auto whole = [](uint32_t k) { return SH == 0 ? k : k >= 0x8000u ? k << SH : (k << SH) | 0xFFFFu; };
+  uint32_t a = lo >> SH, b = hi >> SH;
+  while (a < b) {
+    const uint32_t mid = a + (b - a) / 2;
+    if (enough(whole(mid))) b = mid;
+    else a = mid + 1;
+  }
+  return whole(a);
+}
+
+// Where the top-p cut falls, when `want` is to be kept: a threshold and its ties,
+// from the mass ahead of the logits z2 to z1 and a look at these. Returns 1 where
+// that is found, 0 where it is not among them, -1 within E of a border. *mine_a:
+// this warp's mass above z1.
+template <typename T, bool ONE, bool EXACT>
+__device__ __noinline__ int cut_between(Row<T, ONE> r, int* turn, uint32_t* t, uint32_t* ties,
+                                        uint64_t* mine_a, uint64_t above, uint64_t want, uint64_t E) {
+  Shared& sh = r.sh;
+  const Weigher w = sh.w;
+  const float z1 = sh.z1, z2 = sh.z2;
+  Part q;
+  PairSum f;
+  const uint64_t top = pair_of(-w.zmax), c_hi = pair_of(w.c_hi), c_lo = pair_of(w.c_lo);
+  r.pieces([&](const Vec<T>& x, int) {
+    if (!(x.max() >= z2)) return;
+#pragma unroll
+    for (int e = 0; e < Vec<T>::N / 2; ++e) {
+      const uint64_t z = x.pair(e);
+      const float2 v = of_pair(z);
+      if (!EXACT) {
+        const float2 m = of_pair(fast_weight2(z, top, w.d_min, c_hi, c_lo));
+        f.add((v.x > z1 ? m.x : 0.f) + (v.y > z1 ? m.y : 0.f));
+      }
+      for (float y : {v.x, v.y}) {
+        if (y >= z2 && y <= z1) {
+          const uint32_t key = key_of(y);
+          ++q.count;
+          q.lo = min(q.lo, key);
+          q.hi = max(q.hi, key);
+        }
+      }
+    }
+  });
+  q.mass = EXACT ? above : f.fixed(w.one);
+  Part mine;
+  q = r.template join<P_MASS | P_COUNT | P_LO | P_HI>(q, &mine);
+  *mine_a = mine.mass;
+  int state = 0;
+  if (q.count > 0 && want > q.mass) {
+    const uint64_t rest = want - q.mass;
+    if (q.lo != q.hi && q.count <= kCap) {
+      // few enough to be sorted by the leader
+      if (threadIdx.x == 0) sh.n_cand = 0;
+      __syncthreads();
+      r.gather(z2, z1);
+      if (r.rank == 0) {
+        r.fetch_lists(q.count);
+        r.sort_and_weigh(q.count);
+        if (r.warp == 0) {
+          uint64_t run = 0;
+          uint32_t stay = 0;
+          bool close = false;
+          for (uint32_t i0 = 0; i0 < q.count; i0 += 32) {
+            const uint32_t i = i0 + r.lane;
+            const uint64_t x = i < q.count ? sh.wts[i] : 0;
+            const uint64_t ahead = run + warp_scan(x, r.lane) - x;
+            stay += __popc(__ballot_sync(0xffffffffu, i < q.count && ahead < rest));
+            close |= E && __any_sync(0xffffffffu, i < q.count && distance(ahead, rest) <= 2 * E);
+            run += warp_sum(x);
+          }
+          close |= E && distance(run, rest) <= 2 * E;
+          const uint32_t key = stay ? static_cast<uint32_t>(sh.cand[stay - 1] >> 32) : 0;
+          uint32_t n = 0;
+          for (uint32_t i = r.lane; i < stay; i += 32) n += static_cast<uint32_t>(sh.cand[i] >> 32) == key;
+          n = __reduce_add_sync(0xffffffffu, n);
+          if (r.lane == 0) {
+            sh.ans[r.par].t = key;
+            sh.ans[r.par].ties = n;
+            sh.ans[r.par].bad = close ? -1 : stay == 0 || run < rest ? 0 : 1;
+          }
+        }
+      }
+      r.sync();
+      const auto& lead = r.of_rank(&sh, 0)->ans[r.par];
+      *t = lead.t;
+      *ties = lead.ties;
+      state = lead.bad;
+      r.sync();  // all have read it
+      if (threadIdx.x == 0) sh.ans[r.par].bad = 0;
+    } else {
+      // one value, or many: by halves of the keys between
+      auto inside = [&](uint32_t k) {
+        Part p;
+        r.each_if([&](float z) { return z >= z2 && key_of(z) > k; }, [&](float z) {
+          if (z >= z2 && z <= z1 && key_of(z) > k) p.mass += weight(w, z);
+        });
+        return r.template join<P_MASS>(p).mass;
+      };
+      uint32_t key = q.hi;
+      uint64_t ahead = 0;
+      if (q.lo != q.hi) {
+        key = first_key<T>(q.lo, q.hi, [&](uint32_t k) { return inside(k) < rest; });
+        ahead = inside(key);
+      }
+      const uint64_t each = max(static_cast<uint64_t>(1), weight(w, float_of(key)));
+      const uint64_t n = (rest - ahead + each - 1) / each, over = n * each - (rest - ahead);
+      *t = key;
+      *ties = static_cast<uint32_t>(n);
+      state = n > q.count ? 0 : E && (over <= 2 * E || each - over <= 2 * E) ? -1 : 1;
+    }
+  }
+  *turn = r.turn;
+  return state;
+}
+
+// The logits among which the top-p cut falls, from a histogram of the masses by
+// bins of 1/32 of a binary order, into sh.z1 and sh.z2.
+template <typename T, bool ONE>
+__device__ __noinline__ int find_cut(Row<T, ONE> r, float mass) {
+  Shared& sh = r.sh;
+  const Weigher w = sh.w;
+  const int lane = r.lane;
+  const float floor_z = sh.floor_z;
+  for (int i = threadIdx.x; i < kBins; i += r.nt) sh.hist[i] = 0;
+  __syncthreads();
+  // Tokens lighter than (1 - p) mass / V sum to less than (1 - p) mass.
+  const float least = log2f(fmaxf(0.5f * (1.f - sh.top_p) * mass / static_cast<float>(r.V), 1e-30f));
+  const float y_cut = fmaxf(least - 0.0625f, kCut);
+  const int b_cut = min(Row<T, ONE>::bin_of(fminf(y_cut, 0.f)), kBins - 1);
+  r.each_if([&](float z) { return fast_y(w, z) >= y_cut && z >= floor_z; }, [&](float z) {
+    const float y = fast_y(w, z);
+    if (y >= y_cut && z >= floor_z) {
+      const int b = min(Row<T, ONE>::bin_of(y), kBins - 1);
+      // the weight over the bin's own: 13 bits or more
+      atomicAdd(&sh.hist[b], __float2uint_rn(ex2_approx(y + 0.03125f * b + r.hist_bits)));
+    }
+  });
+  r.sync();
+  // Running sums: this CTA adds up its share of the bins over the slices, five bins
+  // a thread or fewer.
+  const int share = (b_cut + r.C) / r.C, per = (share + r.nt - 1) / r.nt;
+  const int first = r.rank * share;
+  float m[5], n_m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const int j = static_cast<int>(threadIdx.x) * per + i, b = first + j;
+    m[i] = 0.f;
+    if (i < per && j < share && b <= b_cut) {
+      uint64_t mm = 0;
+      for (int c = 0; c < r.C; ++c) mm += r.of_rank(sh.hist, c)[b];
+      m[i] = static_cast<float>(mm) * ex2_approx(-r.hist_bits - 0.03125f * b);
+    }
+    n_m += m[i];
+  }
+  float m_at = n_m;  // inclusive over the warp, then with what is ahead of it
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float x = __shfl_up_sync(0xffffffffu, m_at, o);
+    if (lane >= o) m_at += x;
+  }
+  Part q, ahead;
+  q.sum = n_m;
+  r.template join<P_SUM>(q, nullptr, &ahead);
+  m_at += ahead.sum - n_m;
+  // the masses here are 2^-14 off for their 13 bits, and 2^-20 for the rest
+  const float need = sh.top_p * mass;
+  q.lo = kBins - 1;  // the first bin that may reach the mass, and that does
+  uint32_t does = kBins - 1;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const int j = static_cast<int>(threadIdx.x) * per + i;
+    m_at += m[i];
+    if (i >= per || j >= share || first + j > b_cut) continue;
+    const uint32_t b = first + j;
+    if (m_at * (1.f + 8e-5f) >= need) q.lo = min(q.lo, b);
+    if (m_at * (1.f - 8e-5f) > need) does = min(does, b);
+  }
+  q.hi = kBins - 1 - does;  // (a minimum as a maximum)
+  q = r.template join<P_LO | P_HI>(q);
+  const int b1 = static_cast<int>(q.lo), b2 = static_cast<int>(kBins - 1 - q.hi);
+  if (threadIdx.x == 0) {
+    // the bins' edges, a little apart for their rounding
+    const float step = 0.03125f * kLn2 * sh.temp;
+    const float e1 = w.zmax - b1 * step, e2 = w.zmax - (b2 + 1) * step;
+    sh.z1 = e1 + (fabsf(e1) + fabsf(w.zmax)) * 4e-7f;
+    sh.z2 = b2 == kBins - 1 ? -3.4e38f : e2 - (fabsf(e2) + fabsf(w.zmax)) * 4e-7f;
+    sh.z2 = fmaxf(sh.z2, floor_z);
+    sh.found = 1;
+  }
+  __syncthreads();
+  return r.turn;
+}
+
+// One row with one way of weighing. `from`: at least the k first tokens (a first
+// guess of them, with top-p alone; all, with min-p and no top-k) are logits from it
+// on; `listing`: they are few. Returns whether the token is decided; with EXACT it
+// always is. Every thread of the cluster returns the same.
 template <typename T, bool ONE, bool EXACT>
 __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int64_t row, uint32_t kmax,
-                                    float my_max, bool hist, bool listing, float from) {
+                                    bool bins, bool listing, float from) {
   constexpr int VE = Vec<T>::N;
   Shared& sh = r.sh;
   if (EXACT) {
@@ -859,14 +1034,16 @@ __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int6
       sh.n_cand = 0;
     }
     __syncthreads();
+    listing = listing && !sh.behind;
   }
   Weigher w = sh.w;
   w.zmax = float_of(kmax);
-  const int lane = r.lane, warp = r.warp;
+  const int lane = r.lane;
   const bool warm = sh.warm != 0, use_k = sh.top_k > 0, use_p = sh.use_p != 0;
 
   // ---- the mass of all tokens, and the list
   Part p;
+  uint64_t my_above = 0;
   auto list = [&](const Vec<T>& x, int v) {
     if (listing && x.max() >= from) {
 #pragma unroll
@@ -875,12 +1052,15 @@ __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int6
         if (z >= from && z > -INFINITY) {
           r.list(z, v, e);
           ++p.count;
+          p.sum += ex2_approx(fast_y(w, z));
         }
       }
     }
   };
   if (EXACT) {
-    p.mass = exact_mass<T, ONE>(r, w, [](float) { return true; });
+    const ulonglong2 m = exact_mass(r, w, -INFINITY, sh.found ? sh.z1 : INFINITY);
+    p.mass = m.x;
+    my_above = m.y;
     if (listing) r.pieces(list);
   } else {
     PairSum all;
@@ -900,17 +1080,17 @@ __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int6
     p.mass = all.fixed(w.one);
   }
   Part mine, before;
-  const Part S = r.template join<P_MASS | P_COUNT>(p, &mine, &before);
-  const uint32_t n_list = S.count;
+  const Part S = r.template join<P_MASS | P_COUNT | P_SUM>(p, &mine, &before);
   const float floor_z = sh.floor_z;  // min-p keeps logits from here on (-inf: off)
   const uint64_t E = EXACT || !warm ? 0 : error_bound<T>(w, S.mass, r.V);
-  // and of those that min-p keeps, where the top-p cut is taken of these
   const bool floored = sh.use_q && !use_k;  // the list is of all logits from min-p's floor on
+  const bool listed = listing && S.count <= kCap;
+  // the mass that the top-p cut is taken of
   uint64_t mass_q = S.mass;
-  if (use_p && floored && !(listing && n_list <= kCap)) {
+  if (use_p && floored && !listed) {
     Part q;
     if (EXACT) {
-      q.mass = exact_mass<T, ONE>(r, w, [=](float z) { return z >= floor_z; });
+      q.mass = exact_mass(r, w, nextafterf(floor_z, -INFINITY), INFINITY).x;
     } else {
       PairSum kept;
       r.each_if([&](float z) { return z >= floor_z; }, [&](float z) {
@@ -920,13 +1100,13 @@ __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int6
     }
     mass_q = r.template join<P_MASS>(q).mass;
   }
-  const float mass2 = static_cast<float>(mass_q) / w.one;
+  const float mass_f = static_cast<float>(mass_q) / w.one;
 
   Kept keep;
   bool drawn = false, synced = false;  // the leader has the token; and all know it
-  if (listing && n_list <= kCap) {
-    // ---- few candidates: the leader finishes the row with exact weights
-    if (r.rank == 0) draw_from_list<T, ONE>(r, n_list, warm, mass_q, 2 * E, floored, floored);
+  // ---- few candidates: the leader finishes the row with exact weights
+  if (listed && (!warm || use_k || floored || S.sum > 0.9999f * sh.top_p * mass_f)) {
+    if (r.rank == 0) draw_from_list<T, ONE>(r, S.count, warm, mass_q, 2 * E, floored, floored);
     drawn = true;
     if (warm && !use_k && !floored) {  // (the top-p cut may fall behind the list)
       r.sync();
@@ -939,245 +1119,55 @@ __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int6
       }
     }
   }
+  bool between = false;  // mine_a is this warp's mass above sh.z1, and the cut is below
+  uint64_t mine_a = 0;
   if (drawn) {
   } else if (!warm) {
     keep.t = kmax;
     keep.ties = 1;
   } else if (use_k || use_p) {
-    bool listed = false;
-    // the tokens of bins up to b that min-p keeps
-    auto in_bin = [w, floor_z](float z, int b) {
-      const float y = fast_y(w, z);
-      return y >= kCut && z >= floor_z && min(Row<T, ONE>::bin_of(y), kBins - 1) <= b;
-    };
-    if (hist) {
-      for (int i = threadIdx.x; i < kBins; i += r.nt) sh.hist[i] = make_uint2(0, 0);
-      if (threadIdx.x == 0) sh.n_cand = 0;
-      __syncthreads();
-      int b1 = 0, b2 = kBins - 1;
-      uint32_t upto = 0;  // tokens in bins up to b2
-      // (the exact way takes over the bins that the fast one found)
-      const bool found = EXACT && !use_k && sh.upto_valid;
-      if (found) {
-        b1 = sh.b1;
-        b2 = sh.b2;
-        upto = sh.upto;
-      } else {
-      int b_cut = kBins - 1;  // candidates have bins up to this one
-      if (use_k) {
-        // Each slice holds k / C tokens down to the bin where the maxima of its
-        // threads number k / C; the lowest of these bins over the slices is down
-        // to k tokens in all, and not many more.
-        const float y = fast_y(w, my_max);
-        if (y >= kCut) atomicAdd(&sh.hist[min(Row<T, ONE>::bin_of(y), kBins - 1)].x, 1u);
-        __syncthreads();
-        Part q;
-        q.hi = local_bin(sh, (sh.top_k + r.C - 1) / r.C, lane, warp, r.nt);
-        b_cut = b2 = static_cast<int>(r.template join<P_HI>(q).hi);
-      } else {
-        // Tokens lighter than (1 - p) mass / V sum to less than (1 - p) mass.
-        const float y = log2f(fmaxf(0.5f * (1.f - sh.top_p) * mass2 / static_cast<float>(r.V), 1e-30f));
-        b_cut = y > kCut ? min(Row<T, ONE>::bin_of(fminf(y, 0.f)) + 1, kBins - 1) : kBins - 1;
-      }
-      // With a small k these candidates are few enough to be sorted; else they
-      // are counted and weighed by bins.
-      if (!use_k || sh.top_k > kCap / 2) {
-        if (use_k) {
-          for (int i = threadIdx.x; i < kBins; i += r.nt) sh.hist[i] = make_uint2(0, 0);
-          __syncthreads();
-        }
-        r.each_if([&](float z) { return in_bin(z, b_cut); }, [&](float z) {
-          if (!in_bin(z, b_cut)) return;
-          const float y = fast_y(w, z);
-          const int b = min(Row<T, ONE>::bin_of(y), kBins - 1);
-          atomicAdd(&sh.hist[b].x, 1u);
-          // the weight over the bin's own: 13 bits or more
-          if (!use_k) atomicAdd(&sh.hist[b].y, __float2uint_rn(ex2_approx(y + 0.03125f * b + r.hist_bits)));
-        });
-        r.sync();
-        // Running sums: this CTA adds up its share of the bins over the slices,
-        // five bins a thread or fewer.
-        const int share = (b_cut + r.C) / r.C, per = (share + r.nt - 1) / r.nt;
-        const int first = r.rank * share;
-        uint32_t n[5], n_c = 0;
-        float m[5], n_m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 5; ++i) {
-          const int j = static_cast<int>(threadIdx.x) * per + i, b = first + j;
-          n[i] = 0;
-          m[i] = 0.f;
-          if (i < per && j < share && b <= b_cut) {
-            uint64_t mm = 0;
-            for (int c = 0; c < r.C; ++c) {
-              const uint2 h = r.of_rank(sh.hist, c)[b];
-              n[i] += h.x;
-              mm += h.y;
-            }
-            m[i] = static_cast<float>(mm) * ex2_approx(-r.hist_bits - 0.03125f * b);
-          }
-          n_c += n[i];
-          n_m += m[i];
-        }
-        uint32_t n_at = n_c;  // inclusive over the warp, then with what is ahead of it
-        float m_at = n_m;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t x = __shfl_up_sync(0xffffffffu, n_at, o);
-          const float z = __shfl_up_sync(0xffffffffu, m_at, o);
-          if (lane >= o) {
-            n_at += x;
-            m_at += z;
-          }
-        }
-        Part q, ahead;
-        q.count = n_c;
-        q.sum = n_m;
-        r.template join<P_COUNT | P_SUM>(q, nullptr, &ahead);
-        n_at += ahead.count - n_c;
-        m_at += ahead.sum - n_m;
-        // the masses here are 2^-14 off for their 13 bits, and 2^-20 for the rest
-        const float need = sh.top_p * mass2;
-        // the first bin that may reach the mass; the first that does, and the count up to it
-        q.lo = kBins - 1;
-        q.best = (static_cast<uint64_t>(kBins - 1) << 32) | 0xFFFFFFFFu;
-#pragma unroll
-        for (int i = 0; i < 5; ++i) {
-          const int j = static_cast<int>(threadIdx.x) * per + i;
-          n_at += n[i];
-          m_at += m[i];
-          if (i >= per || j >= share || first + j > b_cut) continue;
-          const uint32_t b = first + j;
-          const bool may = use_k ? n_at >= static_cast<uint32_t>(sh.top_k) : m_at * (1.f + 8e-5f) >= need;
-          const bool does = use_k ? may : m_at * (1.f - 8e-5f) > need;
-          if (may) q.lo = min(q.lo, b);
-          if (does) q.best = min(q.best, (static_cast<uint64_t>(b) << 32) | n_at);
-        }
-        q = r.template join<P_LO | P_BEST>(q);
-        b1 = static_cast<int>(q.lo);
-        b2 = static_cast<int>(q.best >> 32);
-        upto = static_cast<uint32_t>(q.best);
-        if (threadIdx.x == 0) {
-          sh.b1 = b1;
-          sh.b2 = b2;
-          sh.upto = upto;
-          sh.upto_valid = 1;
-        }
-      }
-      }
-      if (use_k || upto <= kCap) {
-        // ---- few candidates: the leader finishes the row with exact weights
-        const uint32_t n_all = r.gather([&](float z) { return in_bin(z, b2); }, [](float) { return true; });
-        if (n_all <= kCap) {
-          listed = drawn = true;
-          if (r.rank == 0) draw_from_list<T, ONE>(r, n_all, true, mass_q, 2 * E, true, false);
-        }
-      } else {
-        // ---- many tokens stay: the cut falls in bins b1 to b2, whose tokens are
-        // of one value (they tie) or few enough to be sorted
-        Part q;
-        r.each_if([&](float z) { return in_bin(z, b2); }, [&](float z) {
-          if (!in_bin(z, b2)) return;
-          if (in_bin(z, b1 - 1)) {
-            if (!EXACT) q.mass += weigh<EXACT>(w, z);
-          } else {
-            const uint32_t key = key_of(z);
-            ++q.count;
-            q.lo = min(q.lo, key);
-            q.hi = max(q.hi, key);
-          }
-        });
-        if (EXACT) q.mass = exact_mass<T, ONE>(r, w, [=](float z) { return in_bin(z, b1 - 1); });
-        q = r.template join<P_MASS | P_COUNT | P_LO | P_HI>(q);
-        const uint64_t want = mul_ceil(sh.top_p, mass_q);
-        const uint64_t rest = want > q.mass ? want - q.mass : 0;
-        if (q.count > 0 && q.lo == q.hi) {
-          const uint64_t each = max(static_cast<uint64_t>(1), weight(w, float_of(q.lo)));
-          const uint64_t ties = (rest + each - 1) / each, over = ties * each - rest;
-          // the cut is the interval's own only if it falls inside it
-          if (rest > 0 && ties <= q.count) {
-            if (!EXACT && (over <= 2 * E || each - over <= 2 * E)) return false;
-            keep.t = q.lo;
-            keep.ties = static_cast<uint32_t>(ties);
-            listed = true;
-          }
-        } else if (q.count > 0 && q.count <= kCap) {
-          r.gather([&](float z) { return in_bin(z, b2); }, [&](float z) { return !in_bin(z, b1 - 1); });
-          if (r.rank == 0) {
-            r.fetch_lists(q.count);
-            r.sort_and_weigh(q.count);
-            if (warp == 0) {
-              uint64_t run = 0;
-              uint32_t stay = 0;
-              bool bad = rest == 0;
-              for (uint32_t i0 = 0; i0 < q.count; i0 += 32) {
-                const uint32_t i = i0 + lane;
-                const uint64_t x = i < q.count ? sh.wts[i] : 0;
-                const uint64_t ahead = run + warp_scan(x, lane) - x;
-                stay += __popc(__ballot_sync(0xffffffffu, i < q.count && ahead < rest));
-                bad |= !EXACT && __any_sync(0xffffffffu, i < q.count && distance(ahead, rest) <= 2 * E);
-                run += warp_sum(x);
-              }
-              bad |= run < rest || (!EXACT && run - rest <= 2 * E);
-              const uint32_t t = stay ? static_cast<uint32_t>(sh.cand[stay - 1] >> 32) : 0;
-              uint32_t ties = 0;
-              for (uint32_t i = lane; i < stay; i += 32)
-                ties += static_cast<uint32_t>(sh.cand[i] >> 32) == t;
-              ties = __reduce_add_sync(0xffffffffu, ties);
-              if (lane == 0) {
-                sh.ans[r.par].t = t;
-                sh.ans[r.par].ties = ties;
-                sh.ans[r.par].bad = bad ? 1 : 0;
-              }
-            }
-          }
-          r.sync();
-          const auto& lead = r.of_rank(&sh, 0)->ans[r.par];
-          keep.t = lead.t;
-          keep.ties = lead.ties;
-          listed = lead.bad == 0;
-        }
-      }
-    }
-    if (!listed) {
-      // ---- by halves of the key's range: any row, any number of ties
-      if (!EXACT) return false;
-      if (use_k) {  // smallest t with fewer than k keys above it
-        const uint32_t k = static_cast<uint32_t>(sh.top_k);
-        uint32_t lo = 0, hi = kmax;
-        while (lo < hi) {
-          const uint32_t mid = lo + (hi - lo) / 2;
-          if (r.template above<false>(w, mid).count < k) hi = mid;
-          else lo = mid + 1;
-        }
-        keep.t = lo;
-        keep.ties = k - r.template above<false>(w, lo).count;
-      }
+    int state = 0;
+    if (use_k) {
+      // ---- many of top-k's: the smallest t with fewer than k keys above it
+      if (!EXACT && (use_p || sh.use_q)) return false;
+      const uint32_t k = static_cast<uint32_t>(sh.top_k);
+      keep.t = first_key<T>(key_of(from), kmax, [&](uint32_t t) { return r.template above<false>(w, t).count < k; });
+      keep.ties = k - r.template above<false>(w, keep.t).count;
       if (sh.use_q && key_of(floor_z) > keep.t) {
         keep.t = key_of(floor_z);
         keep.ties = 0xFFFFFFFFu;
       }
-      if (use_p) {
-        const uint32_t t = keep.t;
-        const Part over = r.template above<true>(w, t);
-        // t = 0 has no ties: no logit has key 0
-        const uint32_t from = t == 0 ? over.count : r.template above<false>(w, t - 1).count;
-        const uint64_t at = min(keep.ties, from - over.count);
-        const uint64_t need =
-            mul_ceil(sh.top_p, over.mass + (t == 0 ? 0 : at * weight(w, float_of(t))));
-        uint32_t lo = t, hi = kmax;  // smallest key with less than `need` above it
-        while (lo < hi) {
-          const uint32_t mid = lo + (hi - lo) / 2;
-          if (r.template above<true>(w, mid).mass < need) hi = mid;
-          else lo = mid + 1;
-        }
-        const uint64_t ahead = r.template above<true>(w, lo).mass;
-        const uint64_t each = weight(w, float_of(lo));
-        uint32_t more = 0xFFFFFFFFu;        // ties before which there is less than `need`
-        if (ahead >= need) more = 1;        // p <= 0: the first token alone
-        else if (each > 0) more = static_cast<uint32_t>(min((need - ahead + each - 1) / each, static_cast<uint64_t>(0xFFFFFFFFu)));
-        keep.ties = lo > t ? more : min(keep.ties, more);
-        keep.t = lo;
-      }
+      state = !use_p;
+    } else if (bins) {
+      // ---- many of top-p's: the cut falls among the logits of a bin or two
+      if (threadIdx.x == 0) sh.behind = 1;
+      if (!EXACT) r.turn = find_cut<T, ONE>(r, mass_f);
+      if (!EXACT || sh.found)
+        state = cut_between<T, ONE, EXACT>(r, &r.turn, &keep.t, &keep.ties, &mine_a, my_above,
+                                           mul_ceil(sh.top_p, mass_q), E);
+      between = state == 1;
+    }
+    if (state != 1) {
+      // ---- by halves of the key's range: any row, any number of ties
+      if (!EXACT) return false;
+      if (!use_k) keep = Kept();
+      if (floored && key_of(floor_z) > keep.t) keep.t = key_of(floor_z);
+      const uint32_t t = keep.t;
+      const Part over = r.template above<true>(w, t);
+      // t = 0 has no ties: no logit has key 0
+      const uint32_t from_t = t == 0 ? over.count : r.template above<false>(w, t - 1).count;
+      const uint64_t at = min(keep.ties, from_t - over.count);
+      const uint64_t need = mul_ceil(sh.top_p, over.mass + (t == 0 ? 0 : at * weight(w, float_of(t))));
+      // the smallest key with less than `need` above it
+      const uint32_t key = first_key<T>(t, kmax, [&](uint32_t k) { return r.template above<true>(w, k).mass < need; });
+      const uint64_t ahead = r.template above<true>(w, key).mass;
+      const uint64_t each = weight(w, float_of(key));
+      uint32_t more = 0xFFFFFFFFu;  // ties before which there is less than `need`
+      if (ahead >= need) more = 1;  // p <= 0: the first token alone
+      else if (each > 0)
+        more = static_cast<uint32_t>(min((need - ahead + each - 1) / each, static_cast<uint64_t>(0xFFFFFFFFu)));
+      keep.ties = key > t ? more : min(keep.ties, more);
+      keep.t = key;
     }
   } else if (sh.use_q) {
     keep.t = key_of(floor_z);
@@ -1188,15 +1178,26 @@ __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int6
     Part all = S;
     if (keep.t != 0) {
       Part q;
-      PairSum f;
-      r.each_if([&](float z) { return key_of(z) >= keep.t; }, [&](float z) {
-        const uint32_t key = key_of(z);
-        if (!EXACT && key > keep.t) f.add(fast_weight(w, z));
-        q.count += key == keep.t;
-      });
-      const uint32_t t = keep.t;
-      q.mass = EXACT ? exact_mass<T, ONE>(r, w, [t](float z) { return key_of(z) > t; }) : f.fixed(w.one);
+      if (between) {  // the warp's mass above z1 is known
+        const float z1 = sh.z1;
+        r.each_if([&](float z) { return key_of(z) >= keep.t; }, [&](float z) {
+          const uint32_t key = key_of(z);
+          if (key > keep.t && z <= z1) q.mass += weight(w, z);
+          q.count += key == keep.t;
+        });
+        if (lane == 0) q.mass += mine_a;
+      } else {
+        PairSum f;
+        r.each_if([&](float z) { return key_of(z) >= keep.t; }, [&](float z) {
+          const uint32_t key = key_of(z);
+          if (!EXACT && key > keep.t) f.add(fast_weight(w, z));
+          q.count += key == keep.t;
+        });
+        q.mass = EXACT ? exact_mass(r, w, above_key(keep.t), INFINITY).x : f.fixed(w.one);
+      }
       all = r.template join<P_MASS | P_COUNT>(q, &mine, &before);
+    } else {
+      all.count = mine.count = before.count = 0;
     }
     auto* lead = &r.of_rank(&sh, 0)->ans[r.par];
     // (CTAs and warps are in index order)
@@ -1208,40 +1209,47 @@ __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int6
     const uint64_t target = mul_floor(sh.u, all.mass + min(all.count, lim) * wt, rest);
     if (m + min(e, lim) * wt <= target && m + mine.mass + min(e + mine.count, lim) * wt > target) {
       // the mass and ties of a lane's piece
-      auto piece = [&](int v, const Vec<T>& x, uint64_t& s, uint32_t& eq) {
+      auto piece = [&](int v, uint64_t& s, uint32_t& eq) {
         s = 0;
         eq = 0;
-        if (v >= r.v1 || !(keep.t == 0 || key_of(x.max()) >= keep.t)) return;
+        if (v >= r.v1) return;
+        const Vec<T> x = r.load(v);
+        if (keep.t != 0 && !(key_of(x.max()) >= keep.t)) return;
         float f = 0.f;
 #pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          const float z = x.get(i);
-          const uint32_t key = key_of(z);
-          if (EXACT) s += key > keep.t ? weight(w, z) : 0;
-          else f += key > keep.t ? fast_weight(w, z) : 0.f;
-          eq += key == keep.t;
+        for (int i = 0; i < VE / 2; ++i) {
+          const float z0 = x.get(2 * i), z1 = x.get(2 * i + 1);
+          const uint32_t k0 = key_of(z0), k1 = key_of(z1);
+          if (EXACT) {
+            uint64_t w0, w1;
+            weight2(w, x.pair(i), w0, w1);
+            s += (k0 > keep.t ? w0 : 0) + (k1 > keep.t ? w1 : 0);
+          } else {
+            f += (k0 > keep.t ? fast_weight(w, z0) : 0.f) + (k1 > keep.t ? fast_weight(w, z1) : 0.f);
+          }
+          eq += (k0 == keep.t) + (k1 == keep.t);
         }
         if (!EXACT) s = static_cast<uint64_t>(__float2ll_rn(f * w.one));
       };
       // four steps of the warp at a time, until one holds the target
       int vb = r.v0;
       bool done = false;
-      for (; vb < r.v1 && !done; ) {
+#pragma unroll 1
+      while (vb < r.v1 && !done) {
         uint64_t s4[4];
         uint32_t e4[4];
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-          const int v = vb + 32 * i + lane;
-          Vec<T> x;
-          if (v < r.v1) x = r.load(v);
-          piece(v, x, s4[i], e4[i]);
+          uint64_t s;
+          uint32_t eq;
+          piece(vb + 32 * i + lane, s, eq);
+          s = warp_sum(s);
+          eq = __reduce_add_sync(0xffffffffu, eq);
+          if (i == 0) s4[0] = s, e4[0] = eq;
+          else if (i == 1) s4[1] = s, e4[1] = eq;
+          else if (i == 2) s4[2] = s, e4[2] = eq;
+          else s4[3] = s, e4[3] = eq;
         }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s4[i] += __shfl_xor_sync(0xffffffffu, s4[i], o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e4[i] = __reduce_add_sync(0xffffffffu, e4[i]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (!done) {
@@ -1258,11 +1266,9 @@ __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int6
       if (done) {
         done = false;
         const int v = vb + lane;
-        uint64_t s = 0;
-        uint32_t eq = 0;
-        Vec<T> x;
-        if (v < r.v1) x = r.load(v);
-        piece(v, x, s, eq);
+        uint64_t s;
+        uint32_t eq;
+        piece(v, s, eq);
         const uint64_t s_in = m + warp_scan(s, lane);
         uint32_t e_in = eq;
 #pragma unroll
@@ -1275,9 +1281,11 @@ __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int6
         if (hit) {
           done = true;
           if (lane == __ffs(hit) - 1) {
+            const Vec<T> x = r.load(v);
             uint64_t sm = s_in - s;
             uint32_t se = e_in - eq;
             bool found = false;
+#pragma unroll 1
             for (int i = 0; i < VE; ++i) {
               const float z = x.get(i);
               const uint32_t key = key_of(z);
@@ -1330,8 +1338,8 @@ __device__ __noinline__ float min_logit(Weigher w, float temp, float q) {
 // The rare way, apart from the common one's registers.
 template <typename T, bool ONE>
 __device__ __noinline__ int decide_exact(Row<T, ONE> r, const SampleArgs& a, int64_t row, uint32_t kmax,
-                                         float my_max, bool hist, bool listing, float from) {
-  decide<T, ONE, true>(r, a, row, kmax, my_max, hist, listing, from);
+                                         bool bins, bool listing, float from) {
+  decide<T, ONE, true>(r, a, row, kmax, bins, listing, from);
   return r.turn;
 }
 
@@ -1425,14 +1433,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) k_sample(cons
     const bool listing = floored || (kk > 0 && kk <= kCap / 2 && j <= 32);
     Part p;
     p.hi = key_of(mx);
-    if (listing && !floored && j > 1) {
+    if (!floored && j > 1 && j <= 32) {
       const uint32_t mine[1] = {p.hi};
       p.lo = kth_from_below<1>(mine, j);
     }
     const Part tops = r.template join<P_HI | P_LO>(p);
     const uint32_t kmax = tops.hi;
-    float from = 0.f;
-    if (listing && !floored) {
+    float from = -INFINITY;
+    if (kk > 0 && !floored && j <= 32) {
       uint32_t key = kk == 1 ? kmax : tops.lo;
       if (kk > 1 && j == 1) {
         const Part* slots = r.parts + (r.turn ^ 1) * (ONE ? 1 : kMaxCluster) * r.nw;  // that join's
@@ -1461,9 +1469,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) k_sample(cons
     }
     // (a T near 0 or infinity is the exact way's)
     const bool fast = zmax < INFINITY && slice_vecs * VE <= kMaxFast && sh.w.c_hi > 1e-30f && sh.w.c_hi < 1e30f;
-    if (!fast || !decide<T, ONE, false>(r, a, row, kmax, mx, true, listing, from)) {
+    if (!fast || !decide<T, ONE, false>(r, a, row, kmax, true, listing, from)) {
       r.sync();  // (a row's CTAs leave it at the same point where it was not decided)
-      r.turn = decide_exact<T, ONE>(r, a, row, kmax, mx, fast, listing, from);
+      r.turn = decide_exact<T, ONE>(r, a, row, kmax, fast, listing, from);
     }
     r.par ^= 1;
   }
@@ -1642,6 +1650,13 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
       }
       __syncthreads();
       fits = fits && sh.n_cand <= kCap;
+      if (fits && warm && !has_k && !floored) {  // the top-p cut may fall behind the list
+        Part l;
+        for (uint32_t i = threadIdx.x; i < sh.n_cand; i += kRowThreads)
+          l.sum += ex2_approx(fast_y(w, float_of(static_cast<uint32_t>(sh.cand[i] >> 32))));
+        const float s = r.template join<P_SUM>(l).sum;
+        fits = s > 0.9999f * sh.top_p * (static_cast<float>(mass) / w.one);
+      }
     }
     const uint64_t E =
         warm ? error_bound<T>(w, S.mass, a.V) + static_cast<uint64_t>(__float2ll_ru(S.sum * 6.0e-8f * w.one)) : 0;
