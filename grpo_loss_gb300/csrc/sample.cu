@@ -368,8 +368,11 @@ struct Shared {
   } ans[2];
   // this CTA's scratch
   uint32_t scan_u[kMaxWarps];
-  uint64_t base;
+  // the draw: the warp that holds u, what is ahead of it, and its chunks
   int b;
+  uint32_t base_ties;
+  uint64_t base, chunk[kMaxWarps];
+  uint32_t chunk_ties[kMaxWarps];
   uint32_t n_kept;
   // what the fast way leaves to the exact one: the top-p cut is behind the list;
   // it lies among the logits from z2 to z1
@@ -631,7 +634,7 @@ __device__ __noinline__ ulonglong2 exact_mass(const Row<T, ONE> r, const Weigher
   for (int v = r.v0 + r.lane; v < r.v1; v += 32) {
     const Vec<T> x = r.load(v);
     if (!(x.max() > lo)) continue;
-#pragma unroll
+#pragma unroll 2
     for (int e = 0; e < Vec<T>::N / 2; ++e) {
       const uint64_t z = x.pair(e);
       uint64_t a, b;
@@ -717,7 +720,7 @@ __device__ __forceinline__ void write_row(const SampleArgs& a, int64_t row, cons
   a.logp[row] = d - (logf(hi / w.one) + lo / hi);
 }
 
-constexpr int32_t kUndecided = -2;  // marks a row that is left for a second launch
+constexpr int32_t kUndecided = -2, kClose = -3;  // mark rows that are left for a second launch
 
 // How the leader's list served: the token is in ans.t; or u or the top-p cut is
 // within the error of a border; or the top-p cut is behind the list's end.
@@ -1200,112 +1203,108 @@ __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int6
       all.count = mine.count = before.count = 0;
     }
     auto* lead = &r.of_rank(&sh, 0)->ans[r.par];
-    // (CTAs and warps are in index order)
-    uint64_t m = before.mass;
-    uint32_t e = before.count;
     const uint32_t lim = keep.ties;
     const uint64_t wt = keep.t == 0 ? 0 : weigh<EXACT>(w, float_of(keep.t));
     bool rest;
     const uint64_t target = mul_floor(sh.u, all.mass + min(all.count, lim) * wt, rest);
-    if (m + min(e, lim) * wt <= target && m + mine.mass + min(e + mine.count, lim) * wt > target) {
+    auto holds = [&](uint64_t m, uint32_t e, uint64_t dm, uint32_t de) {
+      return m + min(e, lim) * wt <= target && m + dm + min(e + de, lim) * wt > target;
+    };
+    // the warp that holds u (CTAs and warps are in index order), then the chunk of its
+    // pieces: every warp of its CTA takes one
+    if (threadIdx.x == 0) sh.b = -1;
+    __syncthreads();
+    if (holds(before.mass, before.count, mine.mass, mine.count) && lane == 0) {
+      sh.b = r.warp;
+      sh.base = before.mass;
+      sh.base_ties = before.count;
+      if (!EXACT) lead->bad = 1;  // until the token is found
+    }
+    __syncthreads();
+    if (sh.b >= 0) {
       // the mass and ties of a lane's piece
       auto piece = [&](int v, uint64_t& s, uint32_t& eq) {
-        s = 0;
-        eq = 0;
-        if (v >= r.v1) return;
         const Vec<T> x = r.load(v);
         if (keep.t != 0 && !(key_of(x.max()) >= keep.t)) return;
         float f = 0.f;
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < VE / 2; ++i) {
-          const float z0 = x.get(2 * i), z1 = x.get(2 * i + 1);
-          const uint32_t k0 = key_of(z0), k1 = key_of(z1);
+          const float2 z = of_pair(x.pair(i));
+          const uint32_t k0 = key_of(clean(z.x)), k1 = key_of(clean(z.y));
           if (EXACT) {
             uint64_t w0, w1;
             weight2(w, x.pair(i), w0, w1);
             s += (k0 > keep.t ? w0 : 0) + (k1 > keep.t ? w1 : 0);
           } else {
-            f += (k0 > keep.t ? fast_weight(w, z0) : 0.f) + (k1 > keep.t ? fast_weight(w, z1) : 0.f);
+            f += (k0 > keep.t ? fast_weight(w, z.x) : 0.f) + (k1 > keep.t ? fast_weight(w, z.y) : 0.f);
           }
           eq += (k0 == keep.t) + (k1 == keep.t);
         }
-        if (!EXACT) s = static_cast<uint64_t>(__float2ll_rn(f * w.one));
+        if (!EXACT) s += static_cast<uint64_t>(__float2ll_rn(f * w.one));
       };
-      // four steps of the warp at a time, until one holds the target
-      int vb = r.v0;
-      bool done = false;
+      const int per = (r.n_vec + r.nw - 1) / r.nw, v0 = min(r.n_vec, sh.b * per), v1 = min(r.n_vec, v0 + per);
+      const int chunk = (per + r.nw - 1) / r.nw;
+      const int c0 = min(v1, v0 + r.warp * chunk), c1 = min(v1, c0 + chunk);
+      uint64_t s = 0;
+      uint32_t eq = 0;
 #pragma unroll 1
-      while (vb < r.v1 && !done) {
-        uint64_t s4[4];
-        uint32_t e4[4];
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          uint64_t s;
-          uint32_t eq;
-          piece(vb + 32 * i + lane, s, eq);
-          s = warp_sum(s);
-          eq = __reduce_add_sync(0xffffffffu, eq);
-          if (i == 0) s4[0] = s, e4[0] = eq;
-          else if (i == 1) s4[1] = s, e4[1] = eq;
-          else if (i == 2) s4[2] = s, e4[2] = eq;
-          else s4[3] = s, e4[3] = eq;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!done) {
-            if (m + s4[i] + min(e + e4[i], lim) * wt > target) {
-              done = true;
-            } else {
-              m += s4[i];
-              e += e4[i];
-              vb += 32;
-            }
-          }
-        }
+      for (int v = c0 + lane; v < c1; v += 32) piece(v, s, eq);
+      s = warp_sum(s);
+      eq = __reduce_add_sync(0xffffffffu, eq);
+      if (lane == 0) {
+        sh.chunk[r.warp] = s;
+        sh.chunk_ties[r.warp] = eq;
       }
-      if (done) {
-        done = false;
-        const int v = vb + lane;
-        uint64_t s;
-        uint32_t eq;
-        piece(v, s, eq);
-        const uint64_t s_in = m + warp_scan(s, lane);
-        uint32_t e_in = eq;
+      __syncthreads();
+      uint64_t m = sh.base;
+      uint32_t e = sh.base_ties;
+      for (int i = 0; i < r.warp; ++i) {
+        m += sh.chunk[i];
+        e += sh.chunk_ties[i];
+      }
+      if (holds(m, e, s, eq)) {
+        for (int vb = c0; vb < c1; vb += 32) {
+          const int v = vb + lane;
+          uint64_t s1 = 0;
+          uint32_t e1 = 0;
+          if (v < c1) piece(v, s1, e1);
+          const uint64_t s_in = m + warp_scan(s1, lane);
+          uint32_t e_in = e1;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t y = __shfl_up_sync(0xffffffffu, e_in, o);
-          if (lane >= o) e_in += y;
-        }
-        e_in += e;
-        const uint32_t hit = __ballot_sync(0xffffffffu, s_in + min(e_in, lim) * wt > target);
-        if (hit) {
-          done = true;
-          if (lane == __ffs(hit) - 1) {
-            const Vec<T> x = r.load(v);
-            uint64_t sm = s_in - s;
-            uint32_t se = e_in - eq;
-            bool found = false;
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, e_in, o);
+            if (lane >= o) e_in += y;
+          }
+          e_in += e;
+          const uint32_t hit = __ballot_sync(0xffffffffu, s_in + min(e_in, lim) * wt > target);
+          if (hit) {
+            if (lane == __ffs(hit) - 1) {
+              const Vec<T> x = r.load(v);
+              uint64_t sm = s_in - s1;
+              uint32_t se = e_in - e1;
 #pragma unroll 1
-            for (int i = 0; i < VE; ++i) {
-              const float z = x.get(i);
-              const uint32_t key = key_of(z);
-              const uint64_t was = sm + min(se, lim) * wt;
-              if (key > keep.t) sm += weigh<EXACT>(w, z);
-              se += key == keep.t;
-              const uint64_t now = sm + min(se, lim) * wt;
-              if (now > target) {
-                // a border within E of u: left to the exact weights
-                if (E && (now - target <= 2 * E || distance(target, was) <= 2 * E)) lead->bad = 1;
-                lead->t = static_cast<uint32_t>(r.pos0 + static_cast<int64_t>(v) * VE + i);
-                found = true;
-                break;
+              for (int i = 0; i < VE; ++i) {
+                const float z = x.get(i);
+                const uint32_t key = key_of(z);
+                const uint64_t was = sm + min(se, lim) * wt;
+                if (key > keep.t) sm += weigh<EXACT>(w, z);
+                se += key == keep.t;
+                const uint64_t now = sm + min(se, lim) * wt;
+                if (now > target) {
+                  // a border within E of u is left to the exact weights (as is a
+                  // token that the float sums of pieces and of elements disagree on)
+                  lead->t = static_cast<uint32_t>(r.pos0 + static_cast<int64_t>(v) * VE + i);
+                  if (!EXACT && (!E || (now - target > 2 * E && distance(target, was) > 2 * E))) lead->bad = 0;
+                  break;
+                }
               }
             }
-            if (!found) lead->bad = 1;  // (float sums: a piece's and its elements' differ)
+            break;
           }
+          m = __shfl_sync(0xffffffffu, s_in, 31);
+          e = __shfl_sync(0xffffffffu, e_in, 31);
         }
       }
-      if (!EXACT && !done && lane == 0) lead->bad = 1;  // the float sums disagree by their rounding
     }
   }
   if (!synced) {
@@ -1362,7 +1361,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) k_sample(cons
   if (threadIdx.x < 32) sh.tab[threadIdx.x] = c_exp2_32[threadIdx.x];
   const int n_cl = gridDim.x / r.C;
   for (int64_t row = blockIdx.x / r.C; row < a.rows; row += n_cl) {
-    if (rest && a.tokens[row] != kUndecided) continue;
+    const int32_t mark = rest ? a.tokens[row] : kUndecided;
+    if (mark > kUndecided) continue;
     const T* z = static_cast<const T*>(a.logits) + row * a.ld;
     // 16-byte pieces from the one that holds the row's first element
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
@@ -1469,7 +1469,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) k_sample(cons
     }
     // (a T near 0 or infinity is the exact way's)
     const bool fast = zmax < INFINITY && slice_vecs * VE <= kMaxFast && sh.w.c_hi > 1e-30f && sh.w.c_hi < 1e30f;
-    if (!fast || !decide<T, ONE, false>(r, a, row, kmax, true, listing, from)) {
+    if (mark == kClose || !fast || !decide<T, ONE, false>(r, a, row, kmax, true, listing, from)) {
       r.sync();  // (a row's CTAs leave it at the same point where it was not decided)
       r.turn = decide_exact<T, ONE>(r, a, row, kmax, fast, listing, from);
     }
@@ -1488,7 +1488,6 @@ template <typename T>
 __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows(const __grid_constant__ SampleArgs a) {
   __shared__ Shared sh;
   __shared__ Part s_parts[2 * (kRowThreads / 32)];
-  __shared__ uint64_t s_chunk[kRowThreads / 32];
   __shared__ uint32_t s_hits;
   __shared__ int s_hit[kCap];
   constexpr int VE = Vec<T>::N;
@@ -1690,10 +1689,10 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
       uint64_t m = 0;
       for (int v = c0 + lane; v < c1; v += 32) m += piece(v);
       m = warp_sum(m);
-      if (lane == 0) s_chunk[warp] = m;
+      if (lane == 0) sh.chunk[warp] = m;
       __syncthreads();
       uint64_t ahead = sh.base;
-      for (int i = 0; i < warp; ++i) ahead += s_chunk[i];
+      for (int i = 0; i < warp; ++i) ahead += sh.chunk[i];
       if (ahead <= target && ahead + m > target) {
         for (int vb = c0; vb < c1; vb += 32) {
           const int v = vb + lane;
@@ -1727,7 +1726,7 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
   }
   if (threadIdx.x == 0) {
     if (decided) write_row(a, row, z, sh, w, mass);
-    else a.tokens[row] = kUndecided;
+    else a.tokens[row] = kk == 0 ? kClose : kUndecided;
   }
 }
 
@@ -1780,7 +1779,9 @@ cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t s) {
     k_sample_rows<T><<<static_cast<unsigned>(a.rows), kRowThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_with<T, 256, false>(a, kMaxCluster, 4 * sms / kMaxCluster, 1, s);
+    const int rc = getenv("RC") ? atoi(getenv("RC")) : 8;
+    if (getenv("RT")) return launch_with<T, 512, false>(a, rc, sms / rc, 1, s);
+    return launch_with<T, 256, false>(a, rc, 4 * sms / rc, 1, s);
   }
   int C = 2;
   while (C < kMaxCluster && a.rows * C < sms && bytes / C > 16 * 1024) C *= 2;
