@@ -4,27 +4,35 @@
 // point, W = w 2^B, so that sums do not depend on their order, and the token is
 // the one that real numbers give: the draw compares u sum W with the running sum,
 // and with 10^5 tokens of similar weight, sums of float32 weights (2^-22 off, or
-// so) would pick a neighbour in one draw of ten. Two ways of weighing share one
-// body. The fast one takes 2^y from the special-function unit and carries a bound
-// E on the error of its sums; where the draw or the top-p cut falls within E of a
-// border, the row is done again with weights from pairs of floats (2^-43), whose
-// integer sums decide. A trained model's rows (a few likely tokens) seldom need
-// that; flat rows always do.
+// so) would pick a neighbour in one draw of ten. All three cut-offs keep a prefix
+// of the order (logit descending, index ascending): what is kept is a threshold t
+// on the logit's sort key and a number of ties at t, the first in index order.
 //
-// All three cut-offs keep a prefix of the order (logit descending, index
-// ascending): what is kept is a threshold t on the logit's sort key and a number
-// of ties at t, the first in index order.
+// The bytes of a row are read in well under a microsecond's share of the memory's
+// rate; what bounds a call is the work on each logit, some eight cycles of an SM for
+// 32 of them and a pass, and for few rows the barriers between the questions that a
+// row is asked. Three kernels share the parts below:
 //
-// A cluster of CTAs takes a row, each CTA one slice of it that it copies into
-// shared memory once (a row of 128K bf16 logits is 250 KB: more than one SM
-// holds). Every later question (maximum, sums, histogram, draw) reads shared
-// memory and is joined over the cluster through distributed shared memory, so
-// the logits cross HBM once and a row needs one launch.
+// - k_sample_counts (bf16 rows): the row as counts of its few distinct values, in
+//   which every sum is exact and every cut-off is a search; a cluster of CTAs a row.
+//   One row of 128256: 15 us; 64 rows: 23 to 32.
+// - k_sample (float32 rows, and short ones): two ways of weighing share one body. The
+//   fast one takes 2^y from a polynomial and carries a bound E on the error of its
+//   sums; where the draw or the top-p cut falls within E of a border, the row is
+//   done again with weights from pairs of floats (2^-43), whose integer sums decide.
+//   A trained model's rows (a few likely tokens) seldom need that. A cluster takes a
+//   row, each CTA one slice of it that it copies into shared memory once, and every
+//   question (maximum, sums, histogram, draw) reads that and is joined through
+//   distributed shared memory. 8 rows of 128256: 17 to 32 us with few candidates or
+//   none, 22 to 108 with top-p alone.
+// - k_sample_rows (rows enough for every SM): a CTA a row in two passes, for what a list
+//   of a few candidates or the plain softmax decides; the others are left to a second
+//   launch of the kernels above. 512 rows of 201088 in bf16: greedy and small top-k
+//   118 to 124 us, all rows left to the second launch (wide top-p) 346 to 368.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include <atomic>
-#include <stdlib.h>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -35,15 +43,15 @@ namespace grpo {
 
 namespace {
 
-constexpr int kMaxThreads = 512;               // of a CTA: 256 or 512
+constexpr int kMaxThreads = 1024;              // of a CTA
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 8;                 // the portable cluster size
 constexpr int kBins = 1280;                    // (five a thread at most) 1/32 of a binary order each, down to 2^-40
 constexpr int kCap = 1024;                     // candidates that one CTA sorts
 constexpr int kGuess = 96;                      // candidates asked for with top-p alone
 constexpr int kCount = 256;                    // and those that it sorts by counting
-constexpr int kSliceBytes = 33 * 1024;
-constexpr int kMaxSliceBytes = 192 * 1024;     // of a row's slice kept in shared memory
+constexpr int kSliceBytes = 33 * 1024;         // of a row's slice kept in shared memory, with 256 threads
+constexpr int kMaxSliceBytes = 192 * 1024;     // and with 512
 constexpr int kMaxFast = 500000;              // elements of a slice that the bins' sums can take
 constexpr float kCut = -40.f;                  // binary orders below the top that weigh nothing
 
@@ -426,6 +434,59 @@ struct Row {
     }
     return x;
   }
+  // This CTA's slice of a row: 16-byte pieces from the one that holds the row's
+  // first element. `to`: shared memory for it, or null (it is read again from L2).
+  __device__ __forceinline__ void place(const SampleArgs& a, int64_t which, int slice_vecs, uint4* to) {
+    const T* z = static_cast<const T*>(a.logits) + which * a.ld;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
+    const int64_t all = (off + a.V + VE - 1) / VE;
+    const int64_t p0 = static_cast<int64_t>(rank) * slice_vecs;
+    n_vec = static_cast<int>(p0 >= all ? 0 : min(static_cast<int64_t>(slice_vecs), all - p0));
+    pos0 = p0 * VE - off;
+    const int per = (n_vec + nw - 1) / nw;
+    v0 = min(n_vec, warp * per);
+    v1 = min(n_vec, v0 + per);
+    full0 = pos0 < 0 ? 1 : 0;
+    full1 = static_cast<int>(min(static_cast<int64_t>(n_vec), a.V > pos0 ? (a.V - pos0) / VE : 0));
+    V = a.V;
+    row = z;
+    global = reinterpret_cast<const uint4*>(z - off) + p0;
+    slice = to;
+  }
+
+  // Copies the slice, taking this thread's maximum on the way (a warp reads back its own).
+  __device__ __forceinline__ float copy_in() {
+    uint4* to = const_cast<uint4*>(slice);
+    float mx = -INFINITY;
+    // the pieces that lie inside the row, all on their way at once
+    const int f0 = max(v0, full0), f1 = min(v1, full1);
+    if (to) {
+      for (int v = f0 + lane; v < f1; v += 32)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         static_cast<uint32_t>(__cvta_generic_to_shared(to + v))),
+                     "l"(global + v)
+                     : "memory");
+      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+    }
+    for (int vb = f0 + lane; vb < f1; vb += 256) {  // (each lane reads its own copies)
+      Vec<T> x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (vb + 32 * i < f1) x[i].raw = to ? to[vb + 32 * i] : __ldg(global + vb + 32 * i);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (vb + 32 * i < f1) mx = fmaxf(mx, x[i].max());
+    }
+    // and the ones at its ends
+    for (int v = v0 + lane; v < v1; v += 32) {
+      if (v >= f0 && v < f1) continue;
+      const Vec<T> x = fetch(v);
+      if (to) to[v] = x.raw;
+      mx = fmaxf(mx, x.max());
+    }
+    return mx;
+  }
+
   __device__ __forceinline__ Vec<T> load(int v) const {
     if (slice == nullptr) return fetch(v);
     Vec<T> x;
@@ -475,19 +536,23 @@ struct Row {
     if (F & P_LO) to.lo = p.lo;
     if (F & P_HI) to.hi = p.hi;
   }
-  // The fields F of the warp's Parts, in every lane.
+  // The fields F of the warp's Parts, in every lane. (A mass below 2^62 is added up
+  // as three limbs: a reduction of 32 bits is one instruction, one of 64 ten shuffles.)
   template <int F>
   __device__ __forceinline__ static void lanes(Part& p) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      Part q;
-      if (F & P_MASS) q.mass = __shfl_xor_sync(0xffffffffu, p.mass, o);
-        if (F & P_SUM) q.sum = __shfl_xor_sync(0xffffffffu, p.sum, o);
-      if (F & P_COUNT) q.count = __shfl_xor_sync(0xffffffffu, p.count, o);
-      if (F & P_LO) q.lo = __shfl_xor_sync(0xffffffffu, p.lo, o);
-      if (F & P_HI) q.hi = __shfl_xor_sync(0xffffffffu, p.hi, o);
-      add<F>(p, q);
+    constexpr uint32_t all = 0xffffffffu, limb = (1u << 27) - 1;
+    if (F & P_MASS) {
+      const uint32_t a = __reduce_add_sync(all, static_cast<uint32_t>(p.mass) & limb);
+      const uint32_t b = __reduce_add_sync(all, static_cast<uint32_t>(p.mass >> 27) & limb);
+      const uint32_t c = __reduce_add_sync(all, static_cast<uint32_t>(p.mass >> 54));
+      p.mass = a + (static_cast<uint64_t>(b) << 27) + (static_cast<uint64_t>(c) << 54);
     }
+    if (F & P_COUNT) p.count = __reduce_add_sync(all, p.count);
+    if (F & P_LO) p.lo = __reduce_min_sync(all, p.lo);
+    if (F & P_HI) p.hi = __reduce_max_sync(all, p.hi);
+    if (F & P_SUM)
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) p.sum += __shfl_xor_sync(all, p.sum, o);
   }
 
   // Joins the fields F of every thread's Part over the cluster; each thread gets
@@ -500,7 +565,7 @@ struct Row {
     lanes<F>(p);
     if (mine) *mine = p;
     const int n = C * nw, me = rank * nw + warp;
-    Part* slots = parts + turn * (ONE ? 1 : kMaxCluster) * nw;
+    Part* slots = parts + turn * C * nw;
     if (lane < C) put<F>(*of_rank(slots + me, lane), p);
     sync();
     Part all, ahead;
@@ -1342,9 +1407,10 @@ __device__ __noinline__ int decide_exact(Row<T, ONE> r, const SampleArgs& a, int
   return r.turn;
 }
 
-// (three CTAs of 256 threads on an SM, or one of 512)
+// (four CTAs of 256 threads on an SM, or one of 512; rest: the marked rows only)
 template <typename T, int THREADS, bool ONE>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) k_sample(const __grid_constant__ SampleArgs a, int slice_vecs, int resident, int rest) {  // rest: the marked rows only
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1)
+    k_sample(const __grid_constant__ SampleArgs a, int slice_vecs, int resident, int rest) {
   extern __shared__ uint4 s_slice[];
   __shared__ Shared sh;
   constexpr int VE = Vec<T>::N;
@@ -1363,58 +1429,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) k_sample(cons
   for (int64_t row = blockIdx.x / r.C; row < a.rows; row += n_cl) {
     const int32_t mark = rest ? a.tokens[row] : kUndecided;
     if (mark > kUndecided) continue;
-    const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-    // 16-byte pieces from the one that holds the row's first element
-    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
-    const int64_t pieces = (off + a.V + VE - 1) / VE;
-    const int64_t p0 = static_cast<int64_t>(r.rank) * slice_vecs;
-    r.n_vec = static_cast<int>(p0 >= pieces ? 0 : min(static_cast<int64_t>(slice_vecs), pieces - p0));
-    r.pos0 = p0 * VE - off;
-    const int per = (r.n_vec + r.nw - 1) / r.nw;
-    r.v0 = min(r.n_vec, r.warp * per);
-    r.v1 = min(r.n_vec, r.v0 + per);
-    r.full0 = r.pos0 < 0 ? 1 : 0;
-    r.full1 = static_cast<int>(min(static_cast<int64_t>(r.n_vec), a.V > r.pos0 ? (a.V - r.pos0) / VE : 0));
-    r.row = z;
-    r.global = reinterpret_cast<const uint4*>(z - off) + p0;
-    r.slice = resident ? s_slice : nullptr;
-
+    r.place(a, row, slice_vecs, resident ? s_slice : nullptr);
     const float prm_t = a.temperature ? __ldg(a.temperature + row) : 1.f;
     const float prm_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
     const int prm_k = a.top_k ? __ldg(a.top_k + row) : 0;
     const float prm_q = a.min_p ? __ldg(a.min_p + row) : 0.f;
     const float prm_u = threadIdx.x == 0 ? a.u[row] : 0.f;
 
-    // ---- copy the slice, taking the maximum on the way (a warp reads back its own)
-    float mx = -INFINITY;
-    {
-      // the pieces that lie inside the row, all on their way at once
-      const int f0 = max(r.v0, r.full0), f1 = min(r.v1, r.full1);
-      if (resident) {
-        for (int v = f0 + r.lane; v < f1; v += 32)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                           static_cast<uint32_t>(__cvta_generic_to_shared(s_slice + v))),
-                       "l"(r.global + v)
-                       : "memory");
-        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-      }
-      for (int vb = f0 + r.lane; vb < f1; vb += 256) {  // (each lane reads its own copies)
-        Vec<T> x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (vb + 32 * i < f1) x[i].raw = resident ? s_slice[vb + 32 * i] : __ldg(r.global + vb + 32 * i);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (vb + 32 * i < f1) mx = fmaxf(mx, x[i].max());
-      }
-      // and the ones at its ends
-      for (int v = r.v0 + r.lane; v < r.v1; v += 32) {
-        if (v >= f0 && v < f1) continue;
-        const Vec<T> x = r.fetch(v);
-        if (resident) s_slice[v] = x.raw;
-        mx = fmaxf(mx, x.max());
-      }
-    }
+    const float mx = r.copy_in();
     // weights below 2^-40 are 0: a lower q keeps every token that counts
     const bool use_q = prm_q >= 9.094947e-13f && prm_t > 0.f;
     if (threadIdx.x == 0) {
@@ -1443,7 +1465,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) k_sample(cons
     if (kk > 0 && !floored && j <= 32) {
       uint32_t key = kk == 1 ? kmax : tops.lo;
       if (kk > 1 && j == 1) {
-        const Part* slots = r.parts + (r.turn ^ 1) * (ONE ? 1 : kMaxCluster) * r.nw;  // that join's
+        const Part* slots = r.parts + (r.turn ^ 1) * r.C * r.nw;  // that join's
         uint32_t top[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) top[i] = r.lane + 32 * i < n_warps ? slots[r.lane + 32 * i].hi : 0;
@@ -1482,7 +1504,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) k_sample(cons
 // lane weighs against the largest logit it has seen, and scales its sum down when a
 // larger one comes), and, as a rule from L2, once more for the candidates. Greedy, top-k,
 // min-p and plain softmax rows end here, and top-p rows whose cut is within the
-// list; what is left is marked for k_sample, whose clusters take it row by row.
+// list; what is left is marked for a second launch.
 constexpr int kRowThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows(const __grid_constant__ SampleArgs a) {
@@ -1525,6 +1547,10 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
   const int kk = !warm ? 1 : has_k ? prm_k : prm_p < 1.f ? kGuess : 0;
   const int j = (kk + r.nw - 1) / r.nw;
   const bool listing = floored || (kk > 0 && kk <= kCap / 2 && j <= 32);
+  if (kk > 0 && !listing) {  // too many candidates for a list
+    if (threadIdx.x == 0) a.tokens[row] = kUndecided;
+    return;
+  }
   if (threadIdx.x < 32) sh.tab[threadIdx.x] = c_exp2_32[threadIdx.x];
   if (threadIdx.x == 0) s_hits = 0;
   if (threadIdx.x == 0) set_row(sh, prm_t, prm_k, prm_p, use_q, a.u[row], a.V);
@@ -1730,6 +1756,398 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
   }
 }
 
+// bf16 logits have few values: those of 30 binary orders below the largest magnitude
+// that weighs are 7679, and a row is its counts of them. From the counts every sum
+// is exact (a count times a weight), so that a cut-off is a search in them and no
+// draw has to be done again. A cluster takes a row: each CTA counts its slice in
+// shared memory, and adds up a share of the counters over the cluster. The draw
+// weighs each token that stays by its counter's place in a table of exact weights.
+// A row that does not fit the counters (nonzero values more than 30 binary orders
+// below) and T near 0 or infinity go through decide().
+//
+// One row of 128256 on 8 CTAs takes 28,000 cycles: 3,000 until the first logits are
+// there, 5,000 for their counts, 8,000 for the weights, some 3,000 for each join, 5,000
+// for the draw's pass. With one CTA a row the two passes are most of it, 7 and 10
+// cycles for 32 logits: the banks of shared memory, on which 32 values fall in 3 or
+// 4 turns. (The draw's pass with the fast weights took as long: their 12
+// instructions a logit.) Against lists, histograms of masses and the two ways of
+// weighing, as float32 rows have them, one row with top-p took 15 us for 61, 61 rows
+// with all cut-offs 33 for 37, and the rows that 512 mixed ones leave 75 for 330.
+constexpr int kSide = 3840;           // values of one sign, 128 a binary order
+constexpr int kCounts = 2 * kSide;    // in the order of descending logits; the last is for what weighs nothing
+constexpr int kMostCounted = 200 * 1024;  // dynamic shared memory
+constexpr int kUsual = 0x4300 - kSide;  // m0 for magnitudes below 2^7
+
+// Magnitudes up to m0 share the counter of 0.
+__device__ __forceinline__ uint32_t count_at(uint32_t bits, int m0) {
+  const int m = max(static_cast<int>(bits & 0x7FFFu) - m0, 0);
+  return min(static_cast<uint32_t>(kSide - 1 + ((bits & 0x8000u) ? m : -m)), static_cast<uint32_t>(kCounts - 1));
+}
+__device__ __forceinline__ float count_value(int i, int m0) {
+  const int s = i - (kSide - 1);
+  const uint32_t bits = s > 0 ? 0x8000u | static_cast<uint32_t>(s + m0) : static_cast<uint32_t>(m0 - s);
+  return i == kCounts - 1 ? -INFINITY : s == 0 ? 0.f : __uint_as_float(bits << 16);
+}
+
+// The token that u falls on, of the counters ahead of `cut` and `ties` of its own,
+// which weigh `kept`.
+__device__ __forceinline__ void draw_counted(Row<__nv_bfloat16, false>& r, const SampleArgs& a, int64_t row, const Weigher& w,
+                             uint32_t cut, uint32_t ties, uint64_t kept, uint64_t mass, int m0,
+                             const uint64_t* table) {
+  using T = __nv_bfloat16;
+  constexpr int VE = Vec<T>::N;
+  Shared& sh = r.sh;
+  const int lane = r.lane;
+  const float z_cut = count_value(cut, m0);
+  const uint64_t w_cut = ties ? weight(w, z_cut) : 0;
+  auto piece = [&](const Vec<T>& x, uint64_t& s, uint32_t& eq) {
+    if (!(x.max() >= z_cut)) return;
+#pragma unroll
+    for (uint32_t b : {x.raw.x, x.raw.y, x.raw.z, x.raw.w}) {
+      const uint32_t i = count_at(b, m0), j = count_at(b >> 16, m0);
+      if (i < cut) s += table[i];
+      if (j < cut) s += table[j];
+      eq += (i == cut) + (j == cut);
+    }
+  };
+  if (threadIdx.x == 0) sh.b = -1;
+  // the mass and ties ahead of each warp, then the warp that holds u
+  Part q, mine, before;
+  r.template pieces<4>([&](const Vec<T>& x, int) { piece(x, q.mass, q.count); });
+  r.template join<P_MASS | P_COUNT>(q, &mine, &before);
+  bool left;
+  const uint64_t target = mul_floor(sh.u, kept, left);
+  auto upto = [&](uint64_t m, uint32_t e) { return m + min(e, ties) * w_cut; };
+  auto holds = [&](uint64_t m, uint32_t e, uint64_t dm, uint32_t de) {
+    return upto(m, e) <= target && upto(m + dm, e + de) > target;
+  };
+  if (holds(before.mass, before.count, mine.mass, mine.count) && lane == 0) {
+    sh.b = r.warp;
+    sh.base = before.mass;
+    sh.base_ties = before.count;
+  }
+  __syncthreads();
+  if (sh.b < 0) return;
+  // the chunk of its pieces (every warp takes one), the piece and the token
+  const int per = (r.n_vec + r.nw - 1) / r.nw, v0 = min(r.n_vec, sh.b * per), v1 = min(r.n_vec, v0 + per);
+  const int chunk = (per + r.nw - 1) / r.nw;
+  const int c0 = min(v1, v0 + r.warp * chunk), c1 = min(v1, c0 + chunk);
+  Part c;
+#pragma unroll 1
+  for (int v = c0 + lane; v < c1; v += 32) piece(r.load(v), c.mass, c.count);
+  r.template lanes<P_MASS | P_COUNT>(c);
+  const uint64_t s = c.mass;
+  const uint32_t eq = c.count;
+  if (lane == 0) {
+    sh.chunk[r.warp] = s;
+    sh.chunk_ties[r.warp] = eq;
+  }
+  __syncthreads();
+  uint64_t m = sh.base;
+  uint32_t e = sh.base_ties;
+  for (int i = 0; i < r.warp; ++i) {
+    m += sh.chunk[i];
+    e += sh.chunk_ties[i];
+  }
+  if (holds(m, e, s, eq)) {
+    for (int vb = c0; vb < c1; vb += 32) {
+      const int v = vb + lane;
+      uint64_t s1 = 0;
+      uint32_t e1 = 0;
+      if (v < c1) piece(r.load(v), s1, e1);
+      const uint64_t s_in = m + warp_scan(s1, lane);
+      uint32_t e_in = e1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, e_in, o);
+        if (lane >= o) e_in += y;
+      }
+      e_in += e;
+      const uint32_t hit = __ballot_sync(0xffffffffu, upto(s_in, e_in) > target);
+      if (hit) {
+        if (lane == __ffs(hit) - 1) {
+          const Vec<T> x = r.load(v);
+          uint64_t sm = s_in - s1;
+          uint32_t se = e_in - e1;
+#pragma unroll 1
+          for (int i = 0; i < VE; ++i) {
+            const uint32_t at = count_at(__float_as_uint(x.get(i)) >> 16, m0);
+            if (at < cut) sm += table[at];
+            se += at == cut;
+            if (upto(sm, se) > target) {
+              sh.ans[0].t = static_cast<uint32_t>(r.pos0 + static_cast<int64_t>(v) * VE + i);
+              break;
+            }
+          }
+          write_row(a, row, r.row, sh, w, mass);
+        }
+        break;
+      }
+      m = __shfl_sync(0xffffffffu, s_in, 31);
+      e = __shfl_sync(0xffffffffu, e_in, 31);
+    }
+  }
+}
+
+// (rest: the marked rows only)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_sample_counts(const __grid_constant__ SampleArgs a, int slice_vecs, int resident, int rest) {
+  using T = __nv_bfloat16;
+  extern __shared__ uint4 s_slice[];
+  __shared__ Shared sh;
+  Row<T, false> r(sh);
+  r.lane = threadIdx.x & 31;
+  r.warp = threadIdx.x >> 5;
+  r.nt = THREADS;
+  r.nw = THREADS / 32;
+  r.C = static_cast<int>(r.cl.num_blocks());
+  r.rank = static_cast<int>(r.cl.block_rank());
+  r.hist_bits = 13.f;
+  uint32_t* counts = reinterpret_cast<uint32_t*>(s_slice + (resident ? slice_vecs : 0));
+  uint64_t* table = reinterpret_cast<uint64_t*>(counts + kCounts);
+  uint32_t* joined = r.C == 1 ? counts : reinterpret_cast<uint32_t*>(table + kCounts);
+  r.parts = reinterpret_cast<Part*>(reinterpret_cast<uint32_t*>(table + kCounts) + (r.C == 1 ? 0 : kSide));
+  const int64_t row = blockIdx.x / r.C;
+  if (rest && a.tokens[row] > kUndecided) return;
+  if (threadIdx.x < 32) sh.tab[threadIdx.x] = c_exp2_32[threadIdx.x];
+  r.place(a, row, slice_vecs, resident ? s_slice : nullptr);
+  const int lane = r.lane;
+
+  if (threadIdx.x == 0) {
+    const float t = a.temperature ? __ldg(a.temperature + row) : 1.f, q = a.min_p ? __ldg(a.min_p + row) : 0.f;
+    // weights below 2^-40 are 0: a lower q keeps every token that counts
+    set_row(sh, t, a.top_k ? __ldg(a.top_k + row) : 0, a.top_p ? __ldg(a.top_p + row) : 1.f,
+            q >= 9.094947e-13f && t > 0.f, a.u[row], a.V);
+    sh.floor_z = q;
+    sh.ans[0].bad = 0;
+  }
+  // ---- the counts, with the maximum, while the slice comes in: for the magnitudes
+  // that logits have as a rule, and where these do not fit, once more for the row's own
+  Part p;
+  Weigher w;
+  int m0 = kUsual;
+  uint32_t kmax;
+  bool good;
+  for (int again = 0;; ++again) {
+    for (int i = threadIdx.x; i < kCounts / 4; i += THREADS) reinterpret_cast<uint4*>(counts)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    float mx = -INFINITY;
+    for (int vb = r.v0 + lane; vb < r.v1; vb += 32 * 8) {
+      Vec<T> x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (vb + 32 * i < r.v1) x[i] = r.fetch(vb + 32 * i);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (vb + 32 * i >= r.v1) continue;
+        if (resident) s_slice[vb + 32 * i] = x[i].raw;
+        mx = fmaxf(mx, x[i].max());
+#pragma unroll
+        for (uint32_t b : {x[i].raw.x, x[i].raw.y, x[i].raw.z, x[i].raw.w}) {
+          const uint32_t j = count_at(b, m0), k = count_at(b >> 16, m0);
+          if (j < kCounts - 1) atomicAdd(counts + j, 1u);
+          if (k < kCounts - 1) atomicAdd(counts + k, 1u);
+        }
+      }
+    }
+    __syncthreads();
+    p = Part();
+    p.hi = key_of(mx);
+    p.lo = 1;
+    if (m0 > 0 && counts[kSide - 1]) {  // zeros, or values too small for a counter of their own?
+      r.pieces([&](const Vec<T>& x, int) {
+#pragma unroll
+        for (uint32_t b : {x.raw.x, x.raw.y, x.raw.z, x.raw.w})
+          for (int m : {static_cast<int>(b & 0x7FFFu), static_cast<int>((b >> 16) & 0x7FFFu)})
+            if (m > 0 && m <= m0) p.lo = 0;
+      });
+    }
+    p = r.template join<P_HI | P_LO>(p);
+    kmax = p.hi;
+    const float zmax = float_of(kmax);
+    if (zmax == -INFINITY) {  // nothing to choose from
+      if (r.rank == 0 && threadIdx.x == 0) {
+        a.tokens[row] = -1;
+        a.logp[row] = -INFINITY;
+      }
+      return;
+    }
+    w = sh.w;
+    w.zmax = zmax;
+    // (a T near 0 or infinity, and an infinite logit, are the other way's)
+    good = zmax < INFINITY && w.c_hi > 1e-30f && w.c_hi < 1e30f;
+    if (!good) break;
+    const float z_lo = zmax - 41.f / w.c_hi;  // what lies below weighs nothing
+    const int most = max(__float_as_uint(fabsf(zmax)) >> 16, (__float_as_uint(fabsf(z_lo)) >> 16) + 1);
+    good = p.lo == 1 && most < m0 + kSide;
+    if (good || again) break;
+    m0 = max(min(most, 0x7F7F) - (kSide - 1), 0);
+  }
+  if (threadIdx.x == 0) {  // (read behind the next barrier)
+    sh.w.zmax = w.zmax;
+    const float q = sh.floor_z;
+    sh.floor_z = !sh.use_q ? -INFINITY : q >= 1.f ? w.zmax : min_logit(sh.w, sh.temp, q);
+  }
+  p = Part();
+  Part S, mine, before;
+  if (good) {
+    // ---- this CTA's share of the counters over the cluster, a warp a run of them
+    const int share = kCounts / r.C, run = share / r.nw, first = r.rank * share + r.warp * run;
+    for (int i = 2 * lane; i < run; i += 64) {
+      const int b = first + i;
+      uint2 c = *reinterpret_cast<const uint2*>(counts + b), o[kMaxCluster];
+#pragma unroll
+      for (int k = 1; k < kMaxCluster; ++k)
+        o[k] = k < r.C ? *reinterpret_cast<const uint2*>(r.of_rank(counts, r.rank ^ k) + b) : make_uint2(0, 0);
+#pragma unroll
+      for (int k = 1; k < kMaxCluster; ++k) {
+        c.x += o[k].x;
+        c.y += o[k].y;
+      }
+      if (r.C > 1) *reinterpret_cast<uint2*>(joined + r.warp * run + i) = c;
+      if (c.x | c.y) {
+        uint64_t w0, w1;
+        weight2(w, pair_of(__float_as_uint(count_value(b, m0)), __float_as_uint(count_value(b + 1, m0))), w0, w1);
+        table[b] = w0;
+        table[b + 1] = w1;
+        p.mass += c.x * w0 + c.y * w1;
+        p.count += c.x + c.y;
+      }
+    }
+    // and the weights of the slice's own values
+    for (int i = 2 * threadIdx.x; i < kCounts; i += 2 * THREADS) {
+      const uint2 c = *reinterpret_cast<const uint2*>(counts + i);
+      if ((c.x | c.y) && (i < r.rank * share || i >= (r.rank + 1) * share)) {
+        uint64_t w0, w1;
+        weight2(w, pair_of(__float_as_uint(count_value(i, m0)), __float_as_uint(count_value(i + 1, m0))), w0, w1);
+        table[i] = w0;
+        table[i + 1] = w1;
+      }
+    }
+    S = r.template join<P_MASS | P_COUNT>(p, &mine, &before);
+    {
+      // f(counter, its count, its weight, tokens and mass ahead of it), for this warp's counters
+      auto each = [&](auto f) {
+        uint32_t n = before.count;
+        uint64_t m = before.mass;
+        for (int i0 = 0; i0 < run; i0 += 32) {
+          const int b = first + i0 + lane;
+          const bool in = i0 + lane < run;
+          const uint32_t c = in ? joined[b - (r.C > 1 ? r.rank * share : 0)] : 0;
+          const uint64_t wt = c ? table[b] : 0;
+          if (!__any_sync(0xffffffffu, c != 0)) {
+            if (in) f(b, c, wt, n, m);
+            continue;
+          }
+          uint32_t n_in = c;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, n_in, o);
+            if (lane >= o) n_in += y;
+          }
+          const uint64_t m_in = warp_scan(c * wt, lane);
+          if (in) f(b, c, wt, n + n_in - c, m + m_in - c * wt);
+          n += __shfl_sync(0xffffffffu, n_in, 31);
+          m += __shfl_sync(0xffffffffu, m_in, 31);
+        }
+      };
+      // ---- what stays: the counters ahead of `cut` and `ties` of its own, `kept` in all
+      const bool warm = sh.warm != 0;
+      uint32_t cut = kCounts - 1, ties = 0;
+      uint64_t kept = S.mass;
+      uint32_t stay = S.count;
+      if (warm && sh.use_q) {
+        const float floor_z = sh.floor_z;
+        Part q;
+        each([&](int b, uint32_t, uint64_t, uint32_t n, uint64_t m) {
+          if (count_value(b, m0) < floor_z && (b == 0 || count_value(b - 1, m0) >= floor_z)) {
+            q.lo = b;
+            q.count = n;
+            q.mass = m;
+          }
+        });
+        q = r.template join<P_MASS | P_COUNT | P_LO>(q);
+        if (q.lo < cut) {
+          cut = q.lo;
+          stay = q.count;
+          kept = q.mass;
+        }
+      }
+      const uint32_t k = !warm ? 1 : sh.top_k > 0 ? sh.top_k : 0xFFFFFFFFu;
+      if (k < stay) {
+        Part q;
+        if (before.count <= k && before.count + mine.count > k)
+          each([&](int b, uint32_t c, uint64_t wt, uint32_t n, uint64_t m) {
+            if (n <= k && n + c > k) {
+              q.lo = b;
+              q.count = k - n;
+              q.mass = m + (k - n) * wt;
+            }
+          });
+        q = r.template join<P_MASS | P_COUNT | P_LO>(q);
+        cut = q.lo;
+        ties = q.count;
+        kept = q.mass;
+      }
+      if (warm && sh.use_p) {
+        const uint64_t want = max(mul_ceil(sh.top_p, kept), static_cast<uint64_t>(1));
+        Part q;
+        if (before.mass < want && before.mass + mine.mass >= want)
+          each([&](int b, uint32_t c, uint64_t wt, uint32_t, uint64_t m) {
+            if (m < want && m + c * wt >= want) {
+              const uint32_t n = static_cast<uint32_t>((want - m + wt - 1) / wt);
+              q.lo = b;
+              q.count = n;
+              q.mass = m + n * wt;
+            }
+          });
+        q = r.template join<P_MASS | P_COUNT | P_LO>(q);
+        cut = q.lo;
+        ties = q.count;
+        kept = q.mass;
+      }
+      draw_counted(r, a, row, w, cut, ties, kept, S.mass, m0, table);
+      return;  // (none reads or writes another's shared memory any more)
+    }
+  }
+  decide_exact<T, false>(r, a, row, kmax, false, false, -INFINITY);
+  r.sync();  // no CTA leaves while another may read its shared memory
+}
+
+template <int THREADS>
+cudaError_t launch_counts(const SampleArgs& a, int C, int rest, cudaStream_t s) {
+  auto kernel = k_sample_counts<THREADS>;
+  // counts, weights, joined counts, and what is joined
+  const int words = kCounts * 12 + (C == 1 ? 0 : kSide * 4) + 2 * C * (THREADS / 32) * static_cast<int>(sizeof(Part));
+  static std::atomic<uint64_t> configured{0};  // one bit a device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostCounted);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  const int64_t slice = ((a.V + 7) / 8 + 1 + C - 1) / C;  // a row may start inside its first piece
+  if (slice > INT32_MAX / 8) return cudaErrorInvalidValue;
+  const bool resident = C > 1 && slice * 16 + words <= kMostCounted;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows * C));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = static_cast<size_t>((resident ? slice * 16 : 0) + words);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(slice), resident ? 1 : 0, rest);
+}
+
 template <typename T, int THREADS, bool ONE>
 cudaError_t launch_with(const SampleArgs& a, int C, int most_clusters, int rest, cudaStream_t s) {
   constexpr int VE = 16 / static_cast<int>(sizeof(T));
@@ -1770,23 +2188,28 @@ cudaError_t launch_with(const SampleArgs& a, int C, int most_clusters, int rest,
 template <typename T>
 cudaError_t launch(const SampleArgs& a, int sms, cudaStream_t s) {
   const int64_t bytes = a.V * static_cast<int64_t>(sizeof(T));
-  // Short rows, and rows enough for every SM: a CTA a row, which needs no cluster's
-  // barriers. What the fast weights leave of long ones is done by a second launch,
-  // many SMs a row.
+  // Short rows: a CTA a row, which needs no cluster's barriers.
   if (bytes <= 16 * 1024) return launch_with<T, 256, true>(a, 1, 1 << 30, 0, s);
-  const char* em = getenv("SM1");
-  if (a.rows >= (em ? atoi(em) : sms) && a.V <= kMaxFast) {
+  // Rows enough for every SM: one CTA a row as well, and what that leaves, as a rule
+  // top-p rows whose cut is behind the list, a second launch does.
+  const bool many = a.rows >= sms && a.V <= kMaxFast;
+  if (many) {
     k_sample_rows<T><<<static_cast<unsigned>(a.rows), kRowThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int rc = getenv("RC") ? atoi(getenv("RC")) : 8;
-    if (getenv("RT")) return launch_with<T, 512, false>(a, rc, sms / rc, 1, s);
-    return launch_with<T, 256, false>(a, rc, 4 * sms / rc, 1, s);
   }
-  int C = 2;
-  while (C < kMaxCluster && a.rows * C < sms && bytes / C > 16 * 1024) C *= 2;
-  if (a.rows * C <= sms) return launch_with<T, 512, false>(a, C, 65536, 0, s);
-  return launch_with<T, 256, false>(a, C, 65536, 0, s);
+  // Else as many CTAs a row as there are SMs for, each with 16 KB of it at least.
+  if constexpr (sizeof(T) == 2) {
+    int C = 1;
+    while (!many && C < kMaxCluster && a.rows * C * 2 <= sms && bytes / C > 16 * 1024) C *= 2;
+    return C == 1 ? launch_counts<1024>(a, C, many, s) : launch_counts<512>(a, C, many, s);
+  } else {
+    if (many) return launch_with<T, 256, false>(a, kMaxCluster, 4 * sms / kMaxCluster, 1, s);
+    int C = 2;
+    while (C < kMaxCluster && a.rows * C < sms && bytes / C > 16 * 1024) C *= 2;
+    if (a.rows * C <= sms) return launch_with<T, 512, false>(a, C, 65536, 0, s);
+    return launch_with<T, 256, false>(a, C, 65536, 0, s);
+  }
 }
 
 }  // namespace

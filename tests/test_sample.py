@@ -94,6 +94,59 @@ def test_cuts_that_keep_many_tokens(V, par):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("par", [{}, dict(p=0.9), dict(k=40, p=0.8, q=0.01, T=0.7), dict(T=0.0), dict(k=3000), dict(q=0.02)],
+                         ids=str)
+def test_bf16_values_of_every_magnitude(par):
+    """Logits far from 1 in either direction, orders apart within a row, zeros of
+    both signs, subnormals, masked ones, and rows of one value."""
+    V = 30011
+    z, u = logits_of(20, V, torch.float32, 41)
+    z[0] *= 1e-6
+    z[1] *= 100.0                                   # beyond 2^7
+    z[2] = z[2] * 100.0 - 2000.0
+    z[3] = z[3].abs() * -1e-3
+    z[4] *= 1e-36
+    z[5, ::2] *= 1e-30                              # too far below the others, and not 0
+    z[6, ::2] = 0.0
+    z[7, ::2], z[7, 1::4] = 0.0, -0.0
+    z[8] = 0.0
+    z[9] = -1e-39
+    z[10, 1:] = torch.finfo(torch.bfloat16).min
+    z[11] = torch.where(z[11] > 0, z[11], -math.inf)
+    z[12, :29000] = -math.inf
+    z[13] = math.nan
+    z[13, ::3] = -math.inf
+    z[14, 5::3] = math.nan
+    z[15, ::2] = math.inf
+    z[16] = -math.inf
+    z[16, 30010] = 3e38
+    z[17] += 1000.0
+    z[18] = 150.0
+    z[18, 7] = 1e-30
+    check(z.to(torch.bfloat16), u, **par)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("spread", [1.0, 4.0])
+def test_many_rows_with_parameters_of_their_own(dtype, spread):
+    """More rows than SMs, each with other cut-offs, masks among them: rows that
+    need one CTA's passes and rows that need more."""
+    rows, V = 200, 20011
+    z, u = logits_of(rows, V, dtype, 43, spread)
+    g = torch.Generator().manual_seed(5)
+    pick = lambda *v: torch.tensor(v)[torch.randint(len(v), (rows,), generator=g)]
+    z[::9, ::2] = -math.inf
+    z[5] = -math.inf
+    z[6] = math.nan
+    z[7, 11] = math.inf
+    z[8] = 0.0
+    z[9] *= 1e-8
+    check(z, u, T=pick(0.0, 0.3, 0.7, 1.0, 1.0, 1.5), k=pick(0, 0, 0, 1, 20, 256, 257, 3000), p=pick(1.0, 1.0, 0.3, 0.9, 0.95),
+          q=pick(0.0, 0.0, 0.05, 1e-4))
+
+
+@pytest.mark.gpu
 def test_borders_of_u():
     z = torch.zeros(8, 4096, device="cuda")
     u = torch.tensor([0.0, 2.0 ** -12, 0.5, 0.5 - 2.0 ** -25, 1 - 2.0 ** -24, 1.0, 2.0, float("nan")], device="cuda")
