@@ -13,6 +13,7 @@ from __future__ import annotations
 
 from typing import Optional, Sequence
 
+import numpy as np
 import torch
 
 from . import _lib
@@ -232,65 +233,78 @@ class AdamW:
         self.masters, self.exp_avg, self.exp_avg_sq = [], [], []
         self.exp_avg_scale, self.exp_avg_sq_scale = [], []
         eight = state_bits == 8
-        self._table = (_lib.AdamwTensor * max(n, 1))()
         for i, p in enumerate(self.params):
-            code = _lib._plain_code(p.dtype, "params[%d]" % i)
+            _lib._plain_code(p.dtype, "params[%d]" % i)
             _lib._ptr(p, "params[%d]" % i)
-            if p.device != self.device:
-                raise ValueError("params[%d] must be on %s, got %s" % (i, self.device, p.device))
             self.masters.append(p.detach().float() if master and p.dtype == torch.bfloat16 else None)
             st = dict(dtype=torch.uint8 if eight else torch.float32, device=p.device)
             self.exp_avg.append(torch.zeros(p.shape, **st))
             self.exp_avg_sq.append(torch.zeros(p.shape, **st))
             for scales in (self.exp_avg_scale, self.exp_avg_sq_scale):
                 scales.append(torch.zeros((p.numel() + 31) // 32, **st) if eight else None)
-            t = self._table[i]
-            t.n, t.param_dtype, t.weight_decay = p.numel(), code, wd[i]
-            t.param, t.m, t.v = (x.data_ptr() for x in (p, self.exp_avg[i], self.exp_avg_sq[i]))
-            t.master = None if self.masters[i] is None else self.masters[i].data_ptr()
-            if eight:
-                t.m_scale, t.v_scale = self.exp_avg_scale[i].data_ptr(), self.exp_avg_sq_scale[i].data_ptr()
+        self._bind()
 
-    def _point(self, out: Optional["AdamW"]) -> None:
-        """Outputs into ``out``'s buffers, or in place."""
-        for i in range(len(self.params)):
-            t = self._table[i]
-            if out is None:
-                t.param_out = t.master_out = t.m_out = t.v_out = t.m_scale_out = t.v_scale_out = None
-            else:
-                o = out._table[i]
-                t.param_out, t.master_out, t.m_out, t.v_out = o.param, o.master, o.m, o.v
-                t.m_scale_out, t.v_scale_out = o.m_scale, o.v_scale
+    def _pointers(self):
+        return [None if t is None else t.data_ptr() for ts in (
+            self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale,
+            self.exp_avg_sq_scale) for t in ts]
+
+    def _bind(self) -> None:
+        """Fill the table of the tensors that a step is given (again, when a tensor
+        of the lists was replaced or moved)."""
+        n, state = len(self.params), torch.uint8 if self.state_bits == 8 else torch.float32
+        self._table = (_lib.AdamwTensor * max(n, 1))()
+        for i, p in enumerate(self.params):
+            t, dev, many = self._table[i], self.device, p.numel()
+            t.n, t.weight_decay = many, self.weight_decay[i]
+            t.param_dtype = _lib._plain_code(p.dtype, "params[%d]" % i)
+            t.param = _lib._vec_ptr(p, "params[%d]" % i, p.dtype, many, dev)
+            t.master = _lib._vec_ptr(self.masters[i], "masters[%d]" % i, torch.float32, many, dev)
+            t.m = _lib._vec_ptr(self.exp_avg[i], "exp_avg[%d]" % i, state, many, dev)
+            t.v = _lib._vec_ptr(self.exp_avg_sq[i], "exp_avg_sq[%d]" % i, state, many, dev)
+            scales = (many + 31) // 32
+            t.m_scale = _lib._vec_ptr(self.exp_avg_scale[i], "exp_avg_scale[%d]" % i, state, scales, dev)
+            t.v_scale = _lib._vec_ptr(self.exp_avg_sq_scale[i], "exp_avg_sq_scale[%d]" % i, state, scales, dev)
+        self._columns = np.frombuffer(self._table, dtype=_lib.ADAMW_COLUMNS)[:n]   # the same memory
+        self._kinds = [(self.state_bits, p.shape, p.dtype, m is None)
+                       for p, m in zip(self.params, self.masters)]
+        self._bound = self._pointers()
 
     def step(self, grads: Sequence[torch.Tensor], grad_scale: float = 1.0, lr: Optional[float] = None,
              step: Optional[int] = None, out: Optional["AdamW"] = None, stream=None) -> None:
         """``step`` overrides the count of steps taken (1 for the first), ``lr``
         this step's rate; ``grad_scale`` multiplies every gradient."""
-        if len(grads) != len(self.params):
-            raise ValueError("expected %d gradients, got %d" % (len(self.params), len(grads)))
-        if out is not None:
-            if out is self or out.state_bits != self.state_bits or \
-                    [(p.shape, p.dtype) for p in out.params] != [(p.shape, p.dtype) for p in self.params] or \
-                    [m is None for m in out.masters] != [m is None for m in self.masters]:
-                raise ValueError("out must be another AdamW of the same shapes, types and states")
-        if not self.params:
+        n = len(self.params)
+        if len(grads) != n:
+            raise ValueError("expected %d gradients, got %d" % (n, len(grads)))
+        for o in (self,) if out is None else (self, out):
+            if o._pointers() != o._bound:
+                o._bind()
+        if out is not None and (out is self or out._kinds != self._kinds or out.device != self.device):
+            raise ValueError("out must be another AdamW of the same shapes, types and states")
+        if not n:
             return
-        for i, (g, p) in enumerate(zip(grads, self.params)):
-            if g.shape != p.shape:
-                raise ValueError("grads[%d] must have shape %s, got %s" % (i, tuple(p.shape), tuple(g.shape)))
-            if g.device != self.device or not g.is_contiguous():
-                raise ValueError("grads[%d] must be contiguous and on %s" % (i, self.device))
-            t = self._table[i]
-            t.grad_dtype = _lib._plain_code(g.dtype, "grads[%d]" % i)
-            t.grad = g.data_ptr()
-        self._point(out)
+        dev, table, f32 = self.device, self._columns, torch.float32
+        for g, p in zip(grads, self.params):
+            if g.shape != p.shape or g.device != dev or not g.is_contiguous() or \
+                    (g.dtype != f32 and g.dtype != torch.bfloat16):
+                self._refuse(grads)
+        table["grad"] = [g.data_ptr() for g in grads]
+        table["grad_dtype"] = [_lib.GRPO_F32 if g.dtype == f32 else _lib.GRPO_BF16 for g in grads]
         count = self.step_count + 1 if step is None else step
         config = _lib.AdamwConfig(self.lr if lr is None else lr, self.betas[0], self.betas[1],
                                   self.eps, grad_scale, self.state_bits, count)
-        with torch.cuda.device(self.device):
-            _lib.adamw_step(config, self._table, len(self.params), stream)
+        _lib.adamw_step(config, self._table, None if out is None else out._table, n, dev, stream)
         torch.autograd.graph.increment_version((self if out is None else out).params)
         if out is not None:
             out.step_count = count
         else:
             self.step_count = count
+
+    def _refuse(self, grads) -> None:
+        for i, (g, p) in enumerate(zip(grads, self.params)):
+            if g.shape != p.shape:
+                raise ValueError("grads[%d] must have shape %s, got %s" % (i, tuple(p.shape), tuple(g.shape)))
+            if g.device != self.device or not g.is_contiguous():
+                raise ValueError("grads[%d] must be contiguous and on %s" % (i, self.device))
+            _lib._plain_code(g.dtype, "grads[%d]" % i)

@@ -11,6 +11,7 @@ import os
 import threading
 from typing import Optional
 
+import numpy as np
 import torch
 
 # The in-tree build; GRPO_GB300_LIB may name another build of the same library.
@@ -62,11 +63,15 @@ class LayernormProblem(ctypes.Structure):
 class AdamwTensor(ctypes.Structure):
     """Mirror of ``grpo_adamw_tensor``."""
     _fields_ = [("n", ctypes.c_int64)] + \
-        [(k, ctypes.c_void_p) for k in ("grad", "param", "master", "m", "v", "m_scale", "v_scale",
-                                        "param_out", "master_out", "m_out", "v_out",
-                                        "m_scale_out", "v_scale_out")] + \
+        [(k, ctypes.c_void_p) for k in ("grad", "param", "master", "m", "v", "m_scale", "v_scale")] + \
         [("weight_decay", ctypes.c_float), ("param_dtype", ctypes.c_int32),
          ("grad_dtype", ctypes.c_int32)]
+
+
+# The fields of AdamwTensor that a step fills, as columns of an array of them.
+ADAMW_COLUMNS = np.dtype({"names": ["grad", "grad_dtype"], "formats": [np.uint64, np.int32],
+                          "offsets": [AdamwTensor.grad.offset, AdamwTensor.grad_dtype.offset],
+                          "itemsize": ctypes.sizeof(AdamwTensor)})
 
 
 class AdamwConfig(ctypes.Structure):
@@ -134,7 +139,7 @@ _SIGNATURES = {
     "grpo_layernorm_bwd": (ctypes.c_int, [ctypes.POINTER(LayernormProblem)] + [_VP] * 9 +
                            [ctypes.c_size_t, _VP]),
     "grpo_adamw_step": (ctypes.c_int, [ctypes.POINTER(AdamwConfig), ctypes.POINTER(AdamwTensor),
-                                       ctypes.c_int32, _VP]),
+                                       ctypes.POINTER(AdamwTensor), ctypes.c_int32, _VP]),
     "grpo_get_device_status": (ctypes.c_int, [_VP, _VP]),
     "grpo_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "grpo_profile_enable": (ctypes.c_int, [ctypes.c_int32]),
@@ -319,14 +324,20 @@ def _plain_code(dtype, name: str) -> int:
     raise ValueError("%s must be float32 or bfloat16, got %s" % (name, dtype))
 
 
-def _rows_ptr(t: torch.Tensor, name: str, dtype, rows: int, cols: int):
-    """(pointer, row stride) of a [rows, cols] CUDA matrix whose columns are
-    contiguous; the rows may be strided."""
+def _device_of(t: torch.Tensor, name: str):
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
+    return t.device
+
+
+def _rows_ptr(t: torch.Tensor, name: str, dtype, rows: int, cols: int, device):
+    """(pointer, row stride) of a [rows, cols] matrix on ``device`` whose columns
+    are contiguous; the rows may be strided."""
     if t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if t.shape != (rows, cols):
         raise ValueError("%s must have shape (%d, %d), got %s" % (name, rows, cols, tuple(t.shape)))
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
@@ -338,11 +349,34 @@ def _rows_ptr(t: torch.Tensor, name: str, dtype, rows: int, cols: int):
     return t.data_ptr(), ld
 
 
-def _on(device, **tensors) -> None:
-    """Raise unless every tensor given is on ``device``."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+def _vec_ptr(t, name: str, dtype, numel: int, device):
+    """Pointer of an optional contiguous tensor of ``numel`` elements on ``device``."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if t.numel() != numel:
+        raise ValueError("%s must have %d elements, got %d" % (name, numel, t.numel()))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _call(fn, where: str, device, stream, *args) -> None:
+    """fn(*args, stream) with ``device`` current, on ``stream`` or the device's
+    current one. The launches of small operators are bound by the host: torch's
+    own stream and device objects are not made where their numbers will do."""
+    at = device.index
+    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(at)
+    if torch._C._cuda_getDevice() == at:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status != GRPO_OK:
+        raise GrpoError(status, where)
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None,
@@ -356,24 +390,19 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D")
     rows, V = logits.shape
+    i32, f32 = torch.int32, torch.float32
     code = _plain_code(logits.dtype, "logits")
-    ptr, ld = _rows_ptr(logits, "logits", logits.dtype, rows, V)
-    dev = logits.device
+    dev = _device_of(logits, "logits")
+    ptr, ld = _rows_ptr(logits, "logits", logits.dtype, rows, V, dev)
     if tokens is None:
-        tokens = torch.empty(rows, dtype=torch.int32, device=dev)
+        tokens = logits.new_empty(rows, dtype=i32)
     if logp is None:
-        logp = torch.empty(rows, dtype=torch.float32, device=dev)
-    _on(dev, u=u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, tokens=tokens,
-        logp=logp)
-    f32 = torch.float32
-    problem = SampleProblem(rows, V, ld, code)
-    with torch.cuda.device(dev):
-        _check(lib().grpo_sample(
-            ctypes.byref(problem), ptr, _ptr(u, "u", f32, rows),
-            _ptr(temperature, "temperature", f32, rows), _ptr(top_k, "top_k", torch.int32, rows),
-            _ptr(top_p, "top_p", f32, rows), _ptr(min_p, "min_p", f32, rows),
-            _ptr(tokens, "tokens", torch.int32, rows), _ptr(logp, "logp", f32, rows),
-            _stream(stream)), "grpo_sample")
+        logp = logits.new_empty(rows, dtype=f32)
+    _call(lib().grpo_sample, "grpo_sample", dev, stream, SampleProblem(rows, V, ld, code), ptr,
+          _vec_ptr(u, "u", f32, rows, dev), _vec_ptr(temperature, "temperature", f32, rows, dev),
+          _vec_ptr(top_k, "top_k", i32, rows, dev), _vec_ptr(top_p, "top_p", f32, rows, dev),
+          _vec_ptr(min_p, "min_p", f32, rows, dev), _vec_ptr(tokens, "tokens", i32, rows, dev),
+          _vec_ptr(logp, "logp", f32, rows, dev))
     return tokens, logp
 
 
@@ -393,25 +422,24 @@ def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float =
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     rows, d = x.shape
-    dev, f32 = x.device, torch.float32
-    code = _plain_code(x.dtype, "x")
-    xp, ld_x = _rows_ptr(x, "x", x.dtype, rows, d)
+    f32, dt, pt = torch.float32, x.dtype, weight.dtype
+    code, pcode = _plain_code(dt, "x"), _plain_code(pt, "weight")
+    dev = _device_of(x, "x")
+    xp, ld_x = _rows_ptr(x, "x", dt, rows, d, dev)
     if y is None:
-        y = torch.empty(rows, d, dtype=x.dtype, device=dev)
-    yp, ld_y = _rows_ptr(y, "y", x.dtype, rows, d)
-    if mean is None and not rms:
-        mean = torch.empty(rows, dtype=f32, device=dev)
+        y = x.new_empty((rows, d))
+    yp, ld_y = _rows_ptr(y, "y", dt, rows, d, dev)
+    if rms:
+        mean = None
+    elif mean is None:
+        mean = x.new_empty(rows, dtype=f32)
     if rstd is None:
-        rstd = torch.empty(rows, dtype=f32, device=dev)
-    _on(dev, weight=weight, bias=bias, y=y, mean=mean, rstd=rstd)
-    problem = LayernormProblem(rows, d, ld_x, ld_y, 0, 0, eps, 1 if rms else 0, code,
-                               _plain_code(weight.dtype, "weight"))
-    with torch.cuda.device(dev):
-        _check(lib().grpo_layernorm_fwd(
-            ctypes.byref(problem), xp, _ptr(weight, "weight", weight.dtype, d),
-            _ptr(bias, "bias", weight.dtype, d), yp, None if rms else _ptr(mean, "mean", f32, rows),
-            _ptr(rstd, "rstd", f32, rows), _stream(stream)), "grpo_layernorm_fwd")
-    return y, None if rms else mean, rstd
+        rstd = x.new_empty(rows, dtype=f32)
+    problem = LayernormProblem(rows, d, ld_x, ld_y, 0, 0, eps, 1 if rms else 0, code, pcode)
+    _call(lib().grpo_layernorm_fwd, "grpo_layernorm_fwd", dev, stream, problem, xp,
+          _vec_ptr(weight, "weight", pt, d, dev), _vec_ptr(bias, "bias", pt, d, dev), yp,
+          _vec_ptr(mean, "mean", f32, rows, dev), _vec_ptr(rstd, "rstd", f32, rows, dev))
+    return y, mean, rstd
 
 
 def layernorm_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, mean, rstd,
@@ -423,41 +451,42 @@ def layernorm_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, mean,
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     rows, d = x.shape
-    dev, f32 = x.device, torch.float32
-    code = _plain_code(x.dtype, "x")
-    xp, ld_x = _rows_ptr(x, "x", x.dtype, rows, d)
-    gp, ld_dy = _rows_ptr(dy, "dy", x.dtype, rows, d)
-    if dx is None:
-        dx = torch.empty(rows, d, dtype=x.dtype, device=dev)
-    dxp, ld_dx = _rows_ptr(dx, "dx", x.dtype, rows, d)
-    if dweight is None and need_dweight:
-        dweight = torch.empty(d, dtype=f32, device=dev)
-    if dbias is None and bias and not rms:
-        dbias = torch.empty(d, dtype=f32, device=dev)
+    f32, dt, pt = torch.float32, x.dtype, weight.dtype
+    code, pcode = _plain_code(dt, "x"), _plain_code(pt, "weight")
+    dev = _device_of(x, "x")
     if mean is None and not rms:
         raise ValueError("mean is needed unless rms")
-    problem = LayernormProblem(rows, d, ld_x, 0, ld_dy, ld_dx, 0.0, 1 if rms else 0, code,
-                               _plain_code(weight.dtype, "weight"))
-    with torch.cuda.device(dev):
-        if workspace is None and (dweight is not None or dbias is not None):
-            workspace = torch.empty(layernorm_workspace_size(problem), dtype=torch.uint8, device=dev)
-        _on(dev, weight=weight, dy=dy, mean=mean, rstd=rstd, dx=dx, dweight=dweight, dbias=dbias,
-            workspace=workspace)
-        _check(lib().grpo_layernorm_bwd(
-            ctypes.byref(problem), xp, _ptr(weight, "weight", weight.dtype, d), gp,
-            None if rms else _ptr(mean, "mean", f32, rows), _ptr(rstd, "rstd", f32, rows), dxp,
-            _ptr(dweight, "dweight", f32, d), _ptr(dbias, "dbias", f32, d),
-            _ptr(workspace, "workspace"),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _stream(stream)), "grpo_layernorm_bwd")
+    xp, ld_x = _rows_ptr(x, "x", dt, rows, d, dev)
+    gp, ld_dy = _rows_ptr(dy, "dy", dt, rows, d, dev)
+    if dx is None:
+        dx = x.new_empty((rows, d))
+    dxp, ld_dx = _rows_ptr(dx, "dx", dt, rows, d, dev)
+    if dweight is None and need_dweight:
+        dweight = x.new_empty(d, dtype=f32)
+    if dbias is None and bias and not rms:
+        dbias = x.new_empty(d, dtype=f32)
+    problem = LayernormProblem(rows, d, ld_x, 0, ld_dy, ld_dx, 0.0, 1 if rms else 0, code, pcode)
+    size = 0
+    if workspace is None and (dweight is not None or dbias is not None):
+        with torch.cuda.device(dev):
+            size = layernorm_workspace_size(problem)
+        workspace = x.new_empty(size, dtype=torch.uint8)
+    elif workspace is not None:
+        size = workspace.numel() * workspace.element_size()
+    _call(lib().grpo_layernorm_bwd, "grpo_layernorm_bwd", dev, stream, problem, xp,
+          _vec_ptr(weight, "weight", pt, d, dev), gp,
+          None if rms else _vec_ptr(mean, "mean", f32, rows, dev),
+          _vec_ptr(rstd, "rstd", f32, rows, dev), dxp, _vec_ptr(dweight, "dweight", f32, d, dev),
+          _vec_ptr(dbias, "dbias", f32, d, dev),
+          None if workspace is None else _vec_ptr(workspace, "workspace", workspace.dtype,
+                                                  workspace.numel(), dev), size)
     return dx, dweight, dbias
 
 
-def adamw_step(config: AdamwConfig, tensors, n: int, stream=None) -> None:
-    """One grpo_adamw_step over a ctypes array of AdamwTensor (on the current
-    device); the AdamW class checks the tensors and fills the array."""
-    _check(lib().grpo_adamw_step(ctypes.byref(config), tensors, n, _stream(stream)),
-           "grpo_adamw_step")
+def adamw_step(config: AdamwConfig, tensors, out, n: int, device, stream=None) -> None:
+    """One grpo_adamw_step over ctypes arrays of AdamwTensor (``out`` may be None);
+    the AdamW class checks the tensors and fills the arrays."""
+    _call(lib().grpo_adamw_step, "grpo_adamw_step", device, stream, config, tensors, out, n)
 
 
 def device_status(workspace: torch.Tensor, stream=None) -> int:

@@ -40,6 +40,18 @@ grpo_status norm_args(const grpo_layernorm_problem* p, NormArgs* a) {
   return GRPO_OK;
 }
 
+// The parameter and state buffers of one tensor.
+grpo_status adamw_buffers(const grpo_adamw_tensor& t, bool eight) {
+  if (!t.param || !t.m || !t.v) return GRPO_ERR_INVALID_ARG;
+  if (eight != (t.m_scale != nullptr) || eight != (t.v_scale != nullptr))
+    return GRPO_ERR_INVALID_ARG;
+  const size_t ss = eight ? 1 : 4;
+  if (!aligned_to(t.param, elem_size(t.param_dtype)) || !aligned_to(t.master, 4) ||
+      !aligned_to(t.m, ss) || !aligned_to(t.v, ss))
+    return GRPO_ERR_UNSUPPORTED;
+  return GRPO_OK;
+}
+
 size_t norm_bwd_bytes(const NormArgs& a, int sms) {
   return sizeof(float) * 2 * static_cast<size_t>(norm_parts(a, sms)) * static_cast<size_t>(a.d);
 }
@@ -161,7 +173,8 @@ grpo_status grpo_layernorm_bwd(const grpo_layernorm_problem* p, const void* x,
 }
 
 grpo_status grpo_adamw_step(const grpo_adamw_config* c, const grpo_adamw_tensor* tensors,
-                            int32_t n_tensors, cudaStream_t stream) {
+                            const grpo_adamw_tensor* out, int32_t n_tensors,
+                            cudaStream_t stream) {
   NvtxRange nvtx_range("grpo_adamw_step");
   if (!c || n_tensors < 0 || (n_tensors > 0 && !tensors) || c->step < 1)
     return GRPO_ERR_INVALID_ARG;
@@ -172,25 +185,23 @@ grpo_status grpo_adamw_step(const grpo_adamw_config* c, const grpo_adamw_tensor*
   if (!isfinite(c->grad_scale)) return GRPO_ERR_INVALID_ARG;
   if (c->state_bits != 32 && c->state_bits != 8) return GRPO_ERR_INVALID_ARG;
   const bool eight = c->state_bits == 8;
-  const size_t ss = eight ? 1 : 4;
   // every tensor is checked before the first launch
   for (int32_t i = 0; i < n_tensors; ++i) {
     const grpo_adamw_tensor& t = tensors[i];
     if (t.n < 0 || !isfinite(t.weight_decay) || t.weight_decay < 0.f) return GRPO_ERR_INVALID_ARG;
     if (!is_f32_or_bf16(t.param_dtype) || !is_f32_or_bf16(t.grad_dtype))
       return GRPO_ERR_INVALID_ARG;
-    if (t.n == 0) continue;
-    if (!t.grad || !t.param || !t.m || !t.v) return GRPO_ERR_INVALID_ARG;
-    if (eight != (t.m_scale != nullptr) || eight != (t.v_scale != nullptr))
+    if (out && (out[i].n != t.n || out[i].param_dtype != t.param_dtype ||
+                (out[i].master != nullptr) != (t.master != nullptr)))
       return GRPO_ERR_INVALID_ARG;
-    if (!eight && (t.m_scale_out || t.v_scale_out)) return GRPO_ERR_INVALID_ARG;
+    if (t.n == 0) continue;
+    if (!t.grad) return GRPO_ERR_INVALID_ARG;
     if (t.master && t.param_dtype == GRPO_F32) return GRPO_ERR_INVALID_ARG;
-    if (!t.master && t.master_out) return GRPO_ERR_INVALID_ARG;
-    if (t.n > (static_cast<int64_t>(1) << 40)) return GRPO_ERR_UNSUPPORTED;
-    const size_t es = elem_size(t.param_dtype), gs = elem_size(t.grad_dtype);
-    if (!aligned_to(t.grad, gs) || !aligned_to(t.param, es) || !aligned_to(t.param_out, es) ||
-        !aligned_to(t.master, 4) || !aligned_to(t.master_out, 4) || !aligned_to(t.m, ss) ||
-        !aligned_to(t.v, ss) || !aligned_to(t.m_out, ss) || !aligned_to(t.v_out, ss))
+    for (const grpo_adamw_tensor* u : {&t, out ? out + i : &t}) {
+      const grpo_status st = adamw_buffers(*u, eight);
+      if (st != GRPO_OK) return st;
+    }
+    if (!aligned_to(t.grad, elem_size(t.grad_dtype)) || t.n > (static_cast<int64_t>(1) << 40))
       return GRPO_ERR_UNSUPPORTED;
   }
   // The scalars are formed in float64 and rounded once.
@@ -231,12 +242,13 @@ grpo_status grpo_adamw_step(const grpo_adamw_config* c, const grpo_adamw_tensor*
       d.v = s.v;
       d.ms = s.m_scale;
       d.vs = s.v_scale;
-      d.p_out = s.param_out ? s.param_out : s.param;
-      d.w_out = s.master_out ? s.master_out : s.master;
-      d.m_out = s.m_out ? s.m_out : s.m;
-      d.v_out = s.v_out ? s.v_out : s.v;
-      d.ms_out = s.m_scale_out ? s.m_scale_out : s.m_scale;
-      d.vs_out = s.v_scale_out ? s.v_scale_out : s.v_scale;
+      const grpo_adamw_tensor& o = out ? out[i] : s;
+      d.p_out = o.param;
+      d.w_out = o.master;
+      d.m_out = o.m;
+      d.v_out = o.v;
+      d.ms_out = o.m_scale;
+      d.vs_out = o.v_scale;
       d.n = s.n;
       d.keep = static_cast<float>(1.0 - c->lr * s.weight_decay);
       d.chunk0 = 0;

@@ -429,17 +429,19 @@ grpo_status grpo_layernorm_bwd(const grpo_layernorm_problem *problem, const void
  * and 0xAAAAAAAA for parameters: an additive recurrence over index and step,
  * so that over the steps a value is rounded up its share of the times.
  *
- * Every *_out pointer may be NULL (in place) or name another buffer of the same
- * kind, which leaves the old state as it was (for a step that may be rolled
- * back, or a generator that still reads the old weights). Buffers of different
- * kinds or tensors must not overlap, nor may an output overlap its own input
- * except as a whole. `tensors` is host memory, read before the call returns.
- * Tensors with n = 0 are skipped.
+ * `out` may be NULL: parameters, masters and states are updated in place. Else
+ * out[i] names the buffers that the new ones of tensors[i] go to (its param,
+ * master, m, v, m_scale and v_scale, of the same n and types; its grad is not
+ * used), and the old ones stay as they are (for a step that may be rolled back, or
+ * a generator that still reads the old weights).
+ * Buffers of different kinds or tensors must not overlap, nor may an output
+ * overlap its own input except as a whole. `tensors` and `out` are host memory,
+ * read before the call returns. Tensors with n = 0 are skipped.
  * INVALID_ARG for null pointers, n < 0, step < 1, betas outside [0, 1), eps or
  * lr or weight_decay that is negative or not finite, a grad_scale that is not
  * finite, state_bits other than 8 and 32, dtypes other than GRPO_F32 and
- * GRPO_BF16, a master beside a float32 parameter; UNSUPPORTED for pointers off
- * their element's alignment.
+ * GRPO_BF16, a master beside a float32 parameter, an out[i] of another n, type or set of
+ * buffers than tensors[i]; UNSUPPORTED for pointers off their element's alignment.
  */
 typedef struct grpo_adamw_tensor {
   int64_t n;
@@ -448,10 +450,6 @@ typedef struct grpo_adamw_tensor {
   float *master;          /* [n], or NULL */
   void *m, *v;            /* [n] float32, or [n] e4m3 codes */
   uint8_t *m_scale, *v_scale; /* [ceil(n/32)] with state_bits = 8, else NULL */
-  void *param_out;
-  float *master_out;
-  void *m_out, *v_out;
-  uint8_t *m_scale_out, *v_scale_out;
   float weight_decay;
   grpo_dtype param_dtype, grad_dtype;
 } grpo_adamw_tensor;
@@ -464,7 +462,8 @@ typedef struct grpo_adamw_config {
 } grpo_adamw_config;
 
 grpo_status grpo_adamw_step(const grpo_adamw_config *config, const grpo_adamw_tensor *tensors,
-                            int32_t n_tensors, cudaStream_t stream);
+                            const grpo_adamw_tensor *out, int32_t n_tensors,
+                            cudaStream_t stream);
 
 /*
  * Synchronises `stream`, reads and clears the error word of a workspace

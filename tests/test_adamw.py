@@ -264,7 +264,7 @@ def lib():
     return L.lib()
 
 
-def _call(lib, config=None, tensor=None, n=1):
+def _call(lib, config=None, tensor=None, n=1, out=None):
     c = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=1.0, state_bits=8, step=1)
     c.update(config or {})
     at = 4096
@@ -272,7 +272,8 @@ def _call(lib, config=None, tensor=None, n=1):
              param_dtype=L.GRPO_BF16, grad_dtype=L.GRPO_F32)
     t.update(tensor or {})
     arr = (L.AdamwTensor * 1)(L.AdamwTensor(**t))
-    return lib.grpo_adamw_step(ctypes.byref(L.AdamwConfig(**c)), arr, n, None)
+    to = None if out is None else (L.AdamwTensor * 1)(L.AdamwTensor(**{**t, **out}))
+    return lib.grpo_adamw_step(ctypes.byref(L.AdamwConfig(**c)), arr, to, n, None)
 
 
 @pytest.mark.parametrize("config", [dict(lr=-1.0), dict(lr=math.nan), dict(beta1=1.0), dict(beta2=-0.1),
@@ -286,7 +287,7 @@ def test_refuses_bad_settings_on_the_host(lib, config):
     (dict(n=-1), 1), (dict(grad=None), 1), (dict(param=None), 1), (dict(m=None), 1), (dict(v=None), 1),
     (dict(m_scale=None), 1), (dict(v_scale=None), 1), (dict(weight_decay=-0.1), 1), (dict(weight_decay=math.inf), 1),
     (dict(param_dtype=2), 1), (dict(grad_dtype=5), 1), (dict(master=4096, param_dtype=0), 1),
-    (dict(master_out=4096), 1), (dict(grad=4098), 2), (dict(param=4097), 2), (dict(param_out=4097), 2),
+    (dict(grad=4098), 2), (dict(param=4097), 2),
     (dict(master=4098), 2), (dict(n=(1 << 40) + 1), 2)], ids=str)
 def test_refuses_bad_tensors_on_the_host(lib, tensor, status):
     assert _call(lib, tensor=tensor) == status
@@ -294,10 +295,16 @@ def test_refuses_bad_tensors_on_the_host(lib, tensor, status):
 
 def test_refuses_states_of_the_other_width(lib):
     assert _call(lib, dict(state_bits=32)) == 1                          # scales beside float32 states
-    assert _call(lib, dict(state_bits=32), dict(m_scale=None, v_scale=None, m_scale_out=4096)) == 1
     assert _call(lib, dict(state_bits=32), dict(m_scale=None, v_scale=None, m=4098)) == 2
     assert _call(lib, n=-1) == 1
-    assert lib.grpo_adamw_step(None, None, 0, None) == 1
+    assert lib.grpo_adamw_step(None, None, None, 0, None) == 1
+
+
+@pytest.mark.parametrize("out,status", [
+    (dict(n=63), 1), (dict(param_dtype=0), 1), (dict(master=4096), 1), (dict(param=None), 1), (dict(m=None), 1),
+    (dict(m_scale=None), 1), (dict(param=4097), 2)], ids=str)
+def test_refuses_outputs_of_another_kind(lib, out, status):
+    assert _call(lib, out=out) == status
 
 
 def test_binding_refuses_wrong_tensors():
