@@ -28,11 +28,12 @@
 // - k_sample_rows (rows enough for every SM): a CTA a row in two passes, for what a list
 //   of a few candidates or the plain softmax decides; the others are left to a second
 //   launch of the kernels above. 512 rows of 201088 in bf16: greedy and small top-k
-//   118 to 124 us, all rows left to the second launch (wide top-p) 346 to 368.
+//   85 to 91 us, all rows left to the second launch (wide top-p) 298 to 330.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -315,6 +316,13 @@ __device__ __forceinline__ uint64_t fast_weight2(uint64_t z, uint64_t top, float
   const float2 r = of_pair(fma2(q, f, pair_of(1.f))), e = of_pair(t);
   return pair_of(__float_as_uint(r.x) + (__float_as_uint(e.x) << 23),
                  __float_as_uint(r.y) + (__float_as_uint(e.y) << 23));
+}
+
+// The rough weights, from the special-function unit: 2^y to 2^-22.4, y off by its own
+// rounding and c_hi's, 2^-24 |y|. (NaN weighs nothing.)
+__device__ __forceinline__ uint64_t rough_weight2(uint64_t z, uint64_t top, uint64_t c_hi) {
+  const float2 y = of_pair(mul2(add2(z, top), c_hi));
+  return pair_of(__float_as_uint(ex2_approx(clean(y.x))), __float_as_uint(ex2_approx(clean(y.y))));
 }
 
 // Element weight as an integer.
@@ -737,12 +745,14 @@ __device__ __forceinline__ uint32_t kth_from_below(const uint32_t (&key)[N], uin
 // 0.7 |y|), and three roundings in the sum of a piece. The entropy of w / S is at
 // most log2 V, so sum w |y| <= S log2(V / S); for bf16 the term with |y| is left
 // only for logits around 0, whose weights are 2^(-zmax log2(e) / T).
+// The rough weights' sums are off by 2^-24 sum w (3 + 0.7 |y|) for every type, where d
+// is exact, and the same three roundings.
 template <typename T>
-__device__ __forceinline__ uint64_t error_bound(const Weigher& w, uint64_t mass, int64_t V) {
+__device__ __forceinline__ uint64_t error_bound(const Weigher& w, uint64_t mass, int64_t V, bool rough = false) {
   const float s = static_cast<float>(mass) / w.one, v = static_cast<float>(V);
-  const float y0 = fmaxf(0.f, w.zmax * w.c_hi);
-  const float terms = sizeof(T) == 4 ? s * (5.5f + 0.8f * fmaxf(0.f, log2f(v / s)))
-                                     : s * 5.5f + v * ex2_approx(-y0) * fminf(y0, 200.f);
+  const float y0 = fmaxf(0.f, w.zmax * w.c_hi), per_y = 0.8f * s * fmaxf(0.f, log2f(v / s));
+  float terms = s * 5.5f + (sizeof(T) == 4 ? per_y : v * ex2_approx(-y0) * fminf(y0, 200.f));
+  if (rough) terms += 1.5f * s + per_y;
   return static_cast<uint64_t>(__float2ll_ru((terms * 6.0e-8f + v * 1e-12f) * w.one)) + 2 * V + 1024;
 }
 
@@ -1504,7 +1514,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1)
 // lane weighs against the largest logit it has seen, and scales its sum down when a
 // larger one comes), and, as a rule from L2, once more for the candidates. Greedy, top-k,
 // min-p and plain softmax rows end here, and top-p rows whose cut is within the
-// list; what is left is marked for a second launch.
+// list; what is left is marked for a second launch. The masses are of rough weights:
+// with the fast ones, which leave fewer rows, 512 greedy rows of 201088 took 118 us
+// for 85, and as many plain ones 163 for 128 (spread-out logits) and 244 for 238 (flat).
 constexpr int kRowThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows(const __grid_constant__ SampleArgs a) {
@@ -1560,7 +1572,10 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
   Weigher w = sh.w;
   float mx = -INFINITY, err = 0.f;  // err: what the scalings rounded, in units of 2^-24
   PairSum all;
-  {
+  // (what needs the better weights to end here: float32 rows without a cut-off)
+  const bool rough = sizeof(T) == 2 || kk > 0;
+  auto pass = [&](auto is_rough) {
+    constexpr bool ROUGH = decltype(is_rough)::value;
     const uint64_t c_hi = pair_of(w.c_hi), c_lo = pair_of(w.c_lo);
     for (int vb = r.v0 + lane; vb < r.v1; vb += 128) {
       Vec<T> x[4];
@@ -1587,7 +1602,8 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
         if (vb + 32 * i < r.v1 && mx > -INFINITY) {
           uint64_t s[VE / 2];
 #pragma unroll
-          for (int k = 0; k < VE / 2; ++k) s[k] = fast_weight2(x[i].pair(k), top, w.d_min, c_hi, c_lo);
+          for (int k = 0; k < VE / 2; ++k)
+            s[k] = ROUGH ? rough_weight2(x[i].pair(k), top, c_hi) : fast_weight2(x[i].pair(k), top, w.d_min, c_hi, c_lo);
 #pragma unroll
           for (int o = 1; o < VE / 2; o <<= 1)
 #pragma unroll
@@ -1597,7 +1613,9 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
         }
       }
     }
-  }
+  };
+  if (rough) pass(std::true_type());
+  else if constexpr (sizeof(T) == 4) pass(std::false_type());
   Part p;
   p.hi = key_of(mx);
   if (listing && !floored && j > 1) {
@@ -1684,7 +1702,7 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
       }
     }
     const uint64_t E =
-        warm ? error_bound<T>(w, S.mass, a.V) + static_cast<uint64_t>(__float2ll_ru(S.sum * 6.0e-8f * w.one)) : 0;
+        warm ? error_bound<T>(w, S.mass, a.V, rough) + static_cast<uint64_t>(__float2ll_ru(S.sum * 6.0e-8f * w.one)) : 0;
     if (listing) {
       if (fits) {
         draw_from_list<T, true>(r, sh.n_cand, warm, S.mass, 2 * E, floored, floored);
@@ -1772,7 +1790,7 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
 // 4 turns. (The draw's pass with the fast weights took as long: their 12
 // instructions a logit.) Against lists, histograms of masses and the two ways of
 // weighing, as float32 rows have them, one row with top-p took 15 us for 61, 61 rows
-// with all cut-offs 33 for 37, and the rows that 512 mixed ones leave 75 for 330.
+// with all cut-offs 33 for 37, and the rows that 512 mixed ones leave 50 for 330.
 constexpr int kSide = 3840;           // values of one sign, 128 a binary order
 constexpr int kCounts = 2 * kSide;    // in the order of descending logits; the last is for what weighs nothing
 constexpr int kMostCounted = 200 * 1024;  // dynamic shared memory
