@@ -468,8 +468,11 @@ def layernorm_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, mean,
     problem = LayernormProblem(rows, d, ld_x, 0, ld_dy, ld_dx, 0.0, 1 if rms else 0, code, pcode)
     size = 0
     if workspace is None and (dweight is not None or dbias is not None):
-        with torch.cuda.device(dev):
+        if torch._C._cuda_getDevice() == dev.index:
             size = layernorm_workspace_size(problem)
+        else:
+            with torch.cuda.device(dev):
+                size = layernorm_workspace_size(problem)
         workspace = x.new_empty(size, dtype=torch.uint8)
     elif workspace is not None:
         size = workspace.numel() * workspace.element_size()

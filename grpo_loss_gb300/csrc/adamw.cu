@@ -60,13 +60,14 @@ __device__ __forceinline__ float dither_e4m3(float y, uint32_t d) {  // the dith
 
 // The update of one element. Roundings are spelled out, so that every inlined
 // copy gives the same bits and a tensor's result does not depend on its place
-// in a table. The root and the quotient are the special-function unit's, some
+// in a table; those of the moments are the formula's own, operation by operation,
+// so that 8-bit states are the same as those of any float32 code. The root and the quotient are the special-function unit's, some
 // 2^-22 off together: of the update, not of the parameter.
 __device__ __forceinline__ void update(const AdamConst& c, float keep, float g, float& x, float& m,
                                        float& v) {
   g = __fmul_rn(g, c.grad_scale);
-  m = __fmaf_rn(c.beta1, m, __fmul_rn(c.one_m_beta1, g));
-  v = __fmaf_rn(c.beta2, v, __fmul_rn(__fmul_rn(c.one_m_beta2, g), g));
+  m = __fadd_rn(__fmul_rn(c.beta1, m), __fmul_rn(c.one_m_beta1, g));
+  v = __fadd_rn(__fmul_rn(c.beta2, v), __fmul_rn(__fmul_rn(c.one_m_beta2, g), g));
   float root;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
   // (the root of a float is at least 2^-75: with eps = 0, too, den is normal or 0)

@@ -1518,12 +1518,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1)
 // with the fast ones, which leave fewer rows, 512 greedy rows of 201088 took 118 us
 // for 85, and as many plain ones 163 for 128 (spread-out logits) and 244 for 238 (flat).
 constexpr int kRowThreads = 256;
+constexpr int kFirstSteps = 4;  // a power of two
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows(const __grid_constant__ SampleArgs a) {
   __shared__ Shared sh;
   __shared__ Part s_parts[2 * (kRowThreads / 32)];
   __shared__ uint32_t s_hits;
   __shared__ int s_hit[kCap];
+  __shared__ volatile uint32_t s_low[kRowThreads / 32];
   constexpr int VE = Vec<T>::N;
   Row<T, true> r(sh);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1574,10 +1576,32 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
   PairSum all;
   // (what needs the better weights to end here: float32 rows without a cut-off)
   const bool rough = sizeof(T) == 2 || kk > 0;
+  // What the list will be taken from is known at the end only, but a bound from below is
+  // known on the way: of the pieces from the fifth step on, those that reach it are noted.
+  float low = INFINITY;
+  const float to_floor = floored ? fminf(log2f(prm_q), 0.f) * kLn2 * prm_t : 0.f;
   auto pass = [&](auto is_rough) {
     constexpr bool ROUGH = decltype(is_rough)::value;
     const uint64_t c_hi = pair_of(w.c_hi), c_lo = pair_of(w.c_lo);
-    for (int vb = r.v0 + lane; vb < r.v1; vb += 128) {
+    const int steps = (per + 127) / 128;  // the same for every warp
+    for (int step = 0; step < steps; ++step) {
+      const int vb = r.v0 + 128 * step + lane;
+      if (listing && step >= kFirstSteps && (step & (step - 1)) == 0) {
+        if (floored) {
+          const float top = float_of(__reduce_max_sync(0xffffffffu, key_of(mx)));
+          low = top + to_floor - (fabsf(top) + fabsf(to_floor)) * 1e-5f;
+          if (!(low > -INFINITY)) low = -INFINITY;
+        } else {
+          const uint32_t mine[1] = {key_of(mx)};
+          uint32_t key = kth_from_below<1>(mine, j);
+          if (kk > 1) {  // the least of the warps' bounds (later, of what they had when this one looks)
+            if (lane == 0) s_low[warp] = key;
+            if (step == kFirstSteps) __syncthreads();
+            key = __reduce_min_sync(0xffffffffu, s_low[lane % (kRowThreads / 32)]);
+          }
+          low = float_of(max(key, key_of(-INFINITY)));
+        }
+      }
       Vec<T> x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i].raw = make_uint4(0, 0, 0, 0);
@@ -1588,6 +1612,14 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (vb + 32 * i < r.v1) m = fmaxf(m, x[i].max());
+      if (m >= low) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (vb + 32 * i < r.v1 && x[i].max() >= low) {
+            const uint32_t at = atomicAdd(&s_hits, 1u);
+            if (at < kCap) s_hit[at] = vb + 32 * i;
+          }
+      }
       if (m > mx) {
         w.zmax = m;
         const float f = mx > -INFINITY ? fast_weight(w, mx) : 0.f;
@@ -1661,16 +1693,24 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
       all.lo *= f;
       q.mass = all.fixed(w.one);
     }
-    // ---- the list: the pieces that hold candidates, their tokens below
+    // ---- the list: the pieces that may hold candidates, their tokens below; if too many
+    // were noted, those that do
     if (listing) {
-      for (int vb = r.v0 + lane; vb < r.v1; vb += 256) {
+      const bool again = s_hits > kCap;
+      __syncthreads();
+      if (again) {
+        if (threadIdx.x == 0) s_hits = 0;
+        __syncthreads();
+      }
+      const int v1 = again ? r.v1 : min(r.v1, r.v0 + 128 * kFirstSteps);
+      for (int vb = r.v0 + lane; vb < v1; vb += 256) {
         Vec<T> x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (vb + 32 * i < r.v1) x[i] = r.fetch(vb + 32 * i);
+          if (vb + 32 * i < v1) x[i] = r.fetch(vb + 32 * i);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (vb + 32 * i < r.v1 && x[i].max() >= from) {
+          if (vb + 32 * i < v1 && x[i].max() >= from) {
             const uint32_t at = atomicAdd(&s_hits, 1u);
             if (at < kCap) s_hit[at] = vb + 32 * i;
           }
