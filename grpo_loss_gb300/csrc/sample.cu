@@ -1847,8 +1847,25 @@ __device__ __forceinline__ float count_value(int i, int m0) {
   return i == kCounts - 1 ? -INFINITY : s == 0 ? 0.f : __uint_as_float(bits << 16);
 }
 
+// The weights of the slice's own values in the counters ahead of `end` (this CTA's
+// share of the counters has them).
+__device__ __forceinline__ void fill_table(const Row<__nv_bfloat16, false>& r, const Weigher& w, int m0, int end,
+                                           const uint32_t* counts, uint64_t* table) {
+  const int share = kCounts / r.C;
+  for (int i = 2 * threadIdx.x; i < end; i += 2 * r.nt) {
+    const uint2 c = *reinterpret_cast<const uint2*>(counts + i);
+    if ((c.x | c.y) && (i < r.rank * share || i >= (r.rank + 1) * share)) {
+      uint64_t w0, w1;
+      weight2(w, pair_of(__float_as_uint(count_value(i, m0)), __float_as_uint(count_value(i + 1, m0))), w0, w1);
+      table[i] = w0;
+      table[i + 1] = w1;
+    }
+  }
+}
+
 // The token that u falls on, of the counters ahead of `cut` and `ties` of its own,
 // which weigh `kept`.
+template <int U>
 __device__ __forceinline__ void draw_counted(Row<__nv_bfloat16, false>& r, const SampleArgs& a, int64_t row, const Weigher& w,
                              uint32_t cut, uint32_t ties, uint64_t kept, uint64_t mass, int m0,
                              const uint64_t* table) {
@@ -1871,7 +1888,7 @@ __device__ __forceinline__ void draw_counted(Row<__nv_bfloat16, false>& r, const
   if (threadIdx.x == 0) sh.b = -1;
   // the mass and ties ahead of each warp, then the warp that holds u
   Part q, mine, before;
-  r.template pieces<4>([&](const Vec<T>& x, int) { piece(x, q.mass, q.count); });
+  r.template pieces<U>([&](const Vec<T>& x, int) { piece(x, q.mass, q.count); });
   r.template join<P_MASS | P_COUNT>(q, &mine, &before);
   bool left;
   const uint64_t target = mul_floor(sh.u, kept, left);
@@ -2073,16 +2090,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         p.count += c.x + c.y;
       }
     }
-    // and the weights of the slice's own values
-    for (int i = 2 * threadIdx.x; i < kCounts; i += 2 * THREADS) {
-      const uint2 c = *reinterpret_cast<const uint2*>(counts + i);
-      if ((c.x | c.y) && (i < r.rank * share || i >= (r.rank + 1) * share)) {
-        uint64_t w0, w1;
-        weight2(w, pair_of(__float_as_uint(count_value(i, m0)), __float_as_uint(count_value(i + 1, m0))), w0, w1);
-        table[i] = w0;
-        table[i + 1] = w1;
-      }
-    }
+    // with a narrow cut to come, few of the table's weights are needed
+    const bool narrow = sh.warm == 0 || sh.top_k > 0 || sh.use_q;
+    if (!narrow) fill_table(r, w, m0, kCounts, counts, table);
     S = r.template join<P_MASS | P_COUNT>(p, &mine, &before);
     {
       // f(counter, its count, its weight, tokens and mass ahead of it), for this warp's counters
@@ -2165,7 +2175,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         ties = q.count;
         kept = q.mass;
       }
-      draw_counted(r, a, row, w, cut, ties, kept, S.mass, m0, table);
+      if (narrow) {
+        fill_table(r, w, m0, cut, counts, table);
+        __syncthreads();
+      }
+      draw_counted<THREADS == 512 ? 8 : 4>(r, a, row, w, cut, ties, kept, S.mass, m0, table);
       return;  // (none reads or writes another's shared memory any more)
     }
   }
