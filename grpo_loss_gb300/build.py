@@ -22,7 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgrpo_gb300.so")
 SOURCES = ["gemm_tc.cu", "rows.cu", "grpo_api.cu", "noalloc.cu", "sample.cu", "norm.cu", "adamw.cu",
            "ops_api.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "api_common.h"]
+HEADERS = ["ptx.cuh", "f32x2.cuh", "internal.h", "api_common.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "-I" + os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]

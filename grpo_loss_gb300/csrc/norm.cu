@@ -7,10 +7,13 @@
 // its output. The backward's CTAs walk over the rows and keep dw and db of
 // their columns in registers, so that x and dy are not read again for the
 // column sums: those leave one partial row pair a CTA, joined in a fixed order.
+// 262144 rows of 2880 in bf16, RMS: forward 443 us (6.8 TB/s); 163840 of 4096: backward
+// 677 us (6.0 TB/s; two rows' sums, barriers and column sums a turn beside the bytes).
 #include <cuda_bf16.h>
 
 #include <atomic>
 
+#include "f32x2.cuh"
 #include "internal.h"
 
 namespace grpo {
@@ -111,33 +114,6 @@ template <typename T, int N>
 __device__ __forceinline__ void store_piece(T* p, const Piece<T, N>& v) {
   *reinterpret_cast<Piece<T, N>*>(p) = v;
 }
-// Pairs of floats in one register pair: one instruction for both.
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 of_pair(uint64_t p) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // N weights (or biases) from element i on; their type is the same for a launch.
 template <int N>
 __device__ __forceinline__ void load_params(const void* p, int bf16, int i, float* v) {
