@@ -183,6 +183,8 @@ struct NormArgs {
   float* dweight;
   float* dbias;
   float* partial;  // [parts][2][d] partial column sums
+  // set by the launch: rows on 16-byte boundaries, outputs alike
+  int rows16, out16;
 };
 int norm_parts(const NormArgs& a, int sms);  // rows of partial column sums in the workspace
 cudaError_t launch_norm_fwd(const NormArgs& a, int sms, cudaStream_t s);

@@ -90,22 +90,6 @@ struct Piece<__nv_bfloat16, 1> {
     raw = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
   }
 };
-template <>
-struct Piece<float, 2> {
-  uint2 raw;
-  __device__ __forceinline__ float get(int e) const { return __uint_as_float(e == 0 ? raw.x : raw.y); }
-  __device__ __forceinline__ void set(const float* v) {
-    raw = make_uint2(__float_as_uint(v[0]), __float_as_uint(v[1]));
-  }
-};
-template <>
-struct Piece<__nv_bfloat16, 2> {
-  uint32_t raw;
-  __device__ __forceinline__ float get(int e) const {
-    return __uint_as_float(e ? raw & 0xFFFF0000u : raw << 16);
-  }
-  __device__ __forceinline__ void set(const float* v) { raw = pack_bf16(v[0], v[1]); }
-};
 template <typename T, int N>
 __device__ __forceinline__ Piece<T, N> load_piece(const T* p) {
   return *reinterpret_cast<const Piece<T, N>*>(p);
@@ -136,24 +120,25 @@ __device__ __forceinline__ float param(const void* p, int bf16, int i) {
   return bf16 ? ldf(static_cast<const __nv_bfloat16*>(p), i) : ldf(static_cast<const float*>(p), i);
 }
 
-// Sums over a group of G threads (a multiple of 32 that divides the CTA or is
-// it), returned to each of them. `slot` alternates between calls, so that one
+// Sums over a group of G threads (a part of a warp, or a multiple of 32 that
+// divides the CTA or is it), returned to each of them. `slot` alternates between calls, so that one
 // barrier a call is enough.
 template <int G>
 __device__ __forceinline__ float group_sum(float a, float* part, int slot) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  if (G == 32) return a;
-  constexpr int W = G / 32, P = W <= 2 ? 2 : W <= 4 ? 4 : W <= 8 ? 8 : W <= 16 ? 16 : 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* mine = part + slot * 128;
-  if (lane == 0) mine[warp] = a;
-  __syncthreads();
-  // each lane takes one warp's sum
-  const int w = lane & (P - 1);
-  a = w < W ? mine[warp / W * W + w] : 0.f;
+  for (int o = G < 32 ? G / 2 : 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if constexpr (G > 32) {
+    constexpr int W = G / 32, P = W <= 2 ? 2 : W <= 4 ? 4 : W <= 8 ? 8 : W <= 16 ? 16 : 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* mine = part + slot * 128;
+    if (lane == 0) mine[warp] = a;
+    __syncthreads();
+    // each lane takes one warp's sum
+    const int w = lane & (P - 1);
+    a = w < W ? mine[warp / W * W + w] : 0.f;
 #pragma unroll
-  for (int o = P / 2; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    for (int o = P / 2; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  }
   return a;
 }
 // 2 or 4 sums at once. While the lanes are halved, so are the sums that a lane
@@ -256,7 +241,6 @@ __global__ void __launch_bounds__(G * R) k_norm_fwd(NormArgs a) {
   }
 }
 
-// --------------------------------------------------------------- backward
 // Copies a piece into shared memory while the thread goes on.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* to, const void* from) {
@@ -267,6 +251,176 @@ __device__ __forceinline__ void copy_async(void* to, const void* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
 }
 
+// The same of the first `bytes` bytes; the others are 0.
+__device__ __forceinline__ void copy_async_zero(void* to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+               "l"(from), "r"(bytes)
+               : "memory");
+}
+// Clears the first n elements of a 16-byte piece.
+template <typename T, int N>
+__device__ __forceinline__ void clear_first(Piece<T, N>& p, int n) {
+  if constexpr (N * sizeof(T) == 16) {
+    const int bits = n * 8 * static_cast<int>(sizeof(T));  // below 128
+    auto keep = [&](int word) {
+      const int b = min(max(bits - 32 * word, 0), 32);
+      return b == 32 ? 0u : 0xFFFFFFFFu << b;
+    };
+    p.raw.x &= keep(0);
+    p.raw.y &= keep(1);
+    p.raw.z &= keep(2);
+    p.raw.w &= keep(3);
+  }
+}
+
+// Rows that are not on 16-byte boundaries, or not a multiple of 16 bytes long: a
+// row's pieces are those of the 16-byte granules it lies in. A group walks over rows
+// a multiple of 8 apart, which all start `off` elements inside a granule, so that the
+// weights of its pieces stay the same; they are in shared memory, each thread's own in
+// the order it reads them, and the next row is on its way there meanwhile. What a
+// granule holds beside the row is cleared, and not written. (99900 rows of 1001 in
+// bf16: 99 us; single elements 183, granules without the copies ahead 134.)
+template <typename T, int NV, int G, int R>
+__global__ void __launch_bounds__(G * R) k_norm_fwd_ragged(NormArgs a) {
+  constexpr int N = 16 / static_cast<int>(sizeof(T)), THREADS = G * R;
+  using V = Piece<T, N>;
+  extern __shared__ __align__(16) unsigned char ring_raw[];
+  __shared__ float part[2 * 128];
+  V* const ring = reinterpret_cast<V*>(ring_raw) + threadIdx.x;  // [2 rows][NV][threads]
+  // [w, b][NV][threads] pieces of bf16, or [w, b][NV][N / 4][threads] of four floats
+  unsigned char* const params = ring_raw + 2 * NV * THREADS * 16;
+  using P16 = Piece<__nv_bfloat16, N>;
+  auto par16 = [&](int which, int k) -> P16& { return reinterpret_cast<P16*>(params)[(which * NV + k) * THREADS + threadIdx.x]; };
+  auto par32 = [&](int which, int k, int f) -> float4& {
+    return reinterpret_cast<float4*>(params)[((which * NV + k) * (N / 4) + f) * THREADS + threadIdx.x];
+  };
+  const int tid = threadIdx.x % G, d = static_cast<int>(a.d);
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * R, row0 = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x) + row0 * a.ld_x) & 15) / sizeof(T));
+  auto column = [&](int k) { return (k * G + tid) * N - off; };  // of a piece's first element
+  auto inside = [&](int i) { return i >= 0 && i < d; };
+  for (int which = 0; which < (a.bias ? 2 : 1); ++which) {
+    const void* const from = which ? a.bias : a.weight;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float v[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = inside(column(k) + e) ? param(from, a.param_bf16, column(k) + e) : 0.f;
+      if (a.param_bf16) par16(which, k).set(v);  // (exact)
+      else
+#pragma unroll
+        for (int f = 0; f < N / 4; ++f) par32(which, k, f) = make_float4(v[4 * f], v[4 * f + 1], v[4 * f + 2], v[4 * f + 3]);
+    }
+  }
+  auto load_par = [&](int which, int k, float (&v)[N]) {
+    if (a.param_bf16) {
+      const P16 q = par16(which, k);
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = q.get(e);
+    } else {
+#pragma unroll
+      for (int f = 0; f < N / 4; ++f) {
+        const float4 q = par32(which, k, f);
+        v[4 * f] = q.x, v[4 * f + 1] = q.y, v[4 * f + 2] = q.z, v[4 * f + 3] = q.w;
+      }
+    }
+  };
+  auto fetch = [&](int64_t row, int half) {
+    if (row < a.rows) {
+      const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int i = column(k);
+        V& to = ring[(half * NV + k) * THREADS];
+        if (i < 0 && row < off) {  // the granule begins before the matrix (a row is an element long at least)
+#pragma unroll
+          for (int e = 0; e < N; ++e) reinterpret_cast<T*>(&to)[e] = inside(i + e) ? x[i + e] : static_cast<T>(0.f);
+        } else if (i < d) {
+          copy_async_zero(&to, x + i, min(N, d - i) * static_cast<int>(sizeof(T)));
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const float inv_d = 1.f / d;
+  int slot = 1, half = 0;
+  fetch(row0, 0);
+  // every group of a CTA makes the same number of turns: barriers are the CTA's
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * R; first < a.rows; first += groups, half ^= 1) {
+    const int64_t row = first + threadIdx.x / G;
+    const bool live = row < a.rows;
+    fetch(row + groups, half ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    V v[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      v[k].raw = make_uint4(0, 0, 0, 0);
+      if (live && column(k) < d) v[k] = ring[(half * NV + k) * THREADS];
+    }
+    if (tid == 0 && off > 0) clear_first(v[0], off);
+    float mean = 0.f;
+    if (!a.rms) {
+      float t = 0.f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < N; ++e) t += v[k].get(e);
+      mean = group_sum<G>(t, part, 0) * inv_d;
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = column(k);
+      if (i >= 0 && i + N <= d) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float c = v[k].get(e) - mean;
+          q = fmaf(c, c, q);
+        }
+      } else if (i < d) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float c = inside(i + e) ? v[k].get(e) - mean : 0.f;
+          q = fmaf(c, c, q);
+        }
+      }
+    }
+    const float r = rsqrtf(group_sum<G>(q, part, slot) * inv_d + a.eps);
+    if (a.rms) slot ^= 1;  // (else the mean's sum has the other)
+    if (!live) continue;
+    T* y = static_cast<T*>(a.y) + row * a.ld_y;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = column(k);
+      if (i >= d) continue;
+      float o[N], w[N];
+      load_par(0, k, w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[e] = (v[k].get(e) - mean) * r * w[e];
+      if (a.bias) {
+        load_par(1, k, w);
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] += w[e];
+      }
+      if (i >= 0 && i + N <= d && a.out16) {
+        V p;
+        p.set(o);
+        store_piece<T, N>(y + i, p);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (inside(i + e)) stf(y, i + e, o[e]);
+      }
+    }
+    if (tid == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = r;
+    }
+  }
+}
+
+// --------------------------------------------------------------- backward
 // A group of G threads walks over the rows group, + groups, ... (R groups a CTA);
 // each thread holds NV pieces of N columns: their values of a row and their column
 // sums. It takes Q rows a turn, so that the joining of the row sums over the CTA
@@ -275,7 +429,10 @@ __device__ __forceinline__ void copy_async(void* to, const void* from) {
 // memory, whence they are read twice, for the sums and for dx. A thread reads back
 // what it copied itself, so no barrier is needed for that. (163840 x 4096 bf16: 2
 // rows ahead or 4 make no difference, one row a turn takes 936 us.)
-template <typename T, int N, int NV, int G, int R, int Q>
+// RAGGED: the pieces of a row are those of the 16-byte granules that it lies in, as in
+// k_norm_fwd_ragged, `off` elements before its first. (99900 rows of 1001 in bf16: 150
+// us, 60 % of the bytes' time; single elements 436.)
+template <typename T, int N, int NV, int G, int R, int Q, bool RAGGED>
 __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
   constexpr int B = N * static_cast<int>(sizeof(T));
   using V = Piece<T, N>;
@@ -285,14 +442,23 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
   const int tid = threadIdx.x % G, d = static_cast<int>(a.d);
   const int64_t groups = static_cast<int64_t>(gridDim.x) * R;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
+  const int off = RAGGED ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x) + row0 * a.ld_x) & 15) / sizeof(T)) : 0;
+  const int end = d + off;  // the pieces are those from 0 on that begin before it
+  auto inside = [&](int i) { return i >= 0 && i < d; };
+  auto whole = [&](int i) { return !RAGGED || (i >= 0 && i + N <= d && a.out16); };
   // columns in pairs (a column alone has a pair of its own)
   constexpr int H = (N + 1) / 2;
   uint64_t dw[NV][H], db[NV][H], w[NV][H];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int i = (k * G + tid) * N;
+    const int i = (k * G + tid) * N - off;
     float ww[2 * H] = {};
-    if (i < d) load_params<N>(a.weight, a.param_bf16, i, ww);
+    if constexpr (RAGGED) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) ww[e] = inside(i + e) ? param(a.weight, a.param_bf16, i + e) : 0.f;
+    } else if (i < d) {
+      load_params<N>(a.weight, a.param_bf16, i, ww);
+    }
 #pragma unroll
     for (int e = 0; e < H; ++e) {
       dw[k][e] = db[k][e] = pair_of(0.f, 0.f);
@@ -305,12 +471,13 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
   // this thread's first piece of the row that is fetched next, and of the row that
   // is written; `left` rows of the group are still to be fetched
   const int64_t step = groups, mine = row0 < a.rows ? (a.rows - row0 + groups - 1) / groups : 0;
-  const T* xp = static_cast<const T*>(a.x) + row0 * a.ld_x + tid * N;
-  const T* gp = static_cast<const T*>(a.dy) + row0 * a.ld_dy + tid * N;
-  T* dp = static_cast<T*>(a.dx) + row0 * a.ld_dx + tid * N;
+  const T* xp = static_cast<const T*>(a.x) + row0 * a.ld_x + tid * N - off;
+  const T* gp = static_cast<const T*>(a.dy) + row0 * a.ld_dy + tid * N - off;
+  T* dp = static_cast<T*>(a.dx) + row0 * a.ld_dx + tid * N - off;
   const float* mp = a.mean + (a.rms ? 0 : row0);
   const float* rp = a.rstd + row0;
   int left = static_cast<int>(mine);
+  int64_t from = row0;  // the row that is fetched next (a row is an element long at least)
   auto fetch = [&](int half) {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -318,8 +485,20 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
         const int s = half * Q + q;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-          if ((k * G + tid) * N < d) {
-            if constexpr (B >= 4) {
+          if ((k * G + tid) * N < end) {
+            const int i = (k * G + tid) * N - off;
+            if (RAGGED && i < 0 && from < off) {
+              // the granule begins before the matrix
+#pragma unroll
+              for (int e = 0; e < N; ++e) {
+                const bool in = inside(i + e);
+                reinterpret_cast<T*>(&slot_of(s, 0, k))[e] = in ? xp[k * G * N + e] : static_cast<T>(0.f);
+                reinterpret_cast<T*>(&slot_of(s, 1, k))[e] = in ? gp[k * G * N + e] : static_cast<T>(0.f);
+              }
+            } else if (RAGGED && i + N > d) {
+              copy_async_zero(&slot_of(s, 0, k), xp + k * G * N, (d - i) * static_cast<int>(sizeof(T)));
+              copy_async_zero(&slot_of(s, 1, k), gp + k * G * N, (d - i) * static_cast<int>(sizeof(T)));
+            } else if constexpr (B >= 4) {
               copy_async<B>(&slot_of(s, 0, k), xp + k * G * N);
               copy_async<B>(&slot_of(s, 1, k), gp + k * G * N);
             } else {
@@ -330,6 +509,7 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
         }
         xp += step * a.ld_x;
         gp += step * a.ld_dy;
+        from += step;
         --left;
       }
     }
@@ -380,8 +560,12 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
       if (n + q < static_cast<int>(mine)) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-          if ((k * G + tid) * N < d) {
-            const V xv = slot_of(half * Q + q, 0, k), gv = slot_of(half * Q + q, 1, k);
+          if ((k * G + tid) * N < end) {
+            V xv = slot_of(half * Q + q, 0, k), gv = slot_of(half * Q + q, 1, k);
+            if (RAGGED && k == 0 && tid == 0 && off > 0) {  // what is before the row counts for nothing
+              clear_first(xv, off);
+              clear_first(gv, off);
+            }
 #pragma unroll
             for (int e = 0; e < H; ++e) {
               uint64_t g, h;
@@ -407,7 +591,7 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
         const uint64_t c1 = pair_of(m1, m1), c2 = pair_of(m2, m2), rr = pair_of(r[q], r[q]);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-          if ((k * G + tid) * N < d) {
+          if ((k * G + tid) * N < end) {
             const V xv = slot_of(half * Q + q, 0, k), gv = slot_of(half * Q + q, 1, k);
             float o[2 * H];
 #pragma unroll
@@ -418,9 +602,16 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
               o[2 * e] = t.x;
               o[2 * e + 1] = t.y;
             }
-            V p;
-            p.set(o);
-            store_piece<T, N>(dp + k * G * N, p);
+            const int i = (k * G + tid) * N - off;
+            if (whole(i)) {
+              V p;
+              p.set(o);
+              store_piece<T, N>(dp + k * G * N, p);
+            } else {
+#pragma unroll
+              for (int e = 0; e < N; ++e)
+                if (inside(i + e)) stf(dp, k * G * N + e, o[e]);
+            }
           }
         }
         dp += step * a.ld_dx;
@@ -431,14 +622,16 @@ __global__ void __launch_bounds__(G * R) k_norm_bwd(NormArgs a) {
   float* pw = a.partial + 2 * row0 * d;  // one pair of rows a group
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int i = (k * G + tid) * N;
+    const int i = (k * G + tid) * N - off;
     if (i < d) {
 #pragma unroll
       for (int e = 0; e < H; ++e) {
         const float2 p = of_pair(dw[k][e]), q = of_pair(db[k][e]);
-        pw[i + 2 * e] = p.x;
-        pw[d + i + 2 * e] = q.x;
-        if (2 * e + 1 < N) {
+        if (!RAGGED || inside(i + 2 * e)) {
+          pw[i + 2 * e] = p.x;
+          pw[d + i + 2 * e] = q.x;
+        }
+        if (2 * e + 1 < N && (!RAGGED || inside(i + 2 * e + 1))) {
           pw[i + 2 * e + 1] = p.y;
           pw[d + i + 2 * e + 1] = q.y;
         }
@@ -548,25 +741,53 @@ __global__ void __launch_bounds__(1024) k_norm_colsum(NormArgs a, int parts) {
   }
 }
 
-// Values a piece: as many of 8, 4, 2 and 1 (up to 16 bytes) as divide d and find
-// every row of every operand on a boundary of their size.
-int piece_of(const NormArgs& a, bool fwd) {
-  const int es = a.bf16 ? 2 : 4, ps = a.param_bf16 ? 2 : 4;
-  uint64_t rows = 0, params = reinterpret_cast<uintptr_t>(a.weight);  // low bits of all addresses
-  auto add = [&](const void* p, int64_t ld) {
-    rows |= reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(ld) * es;
+// How a call's rows are taken: in 16-byte pieces where every row of every operand,
+// and the weights, are on 16-byte boundaries and d is whole pieces; else by 16-byte
+// granules, where the rows of the inputs lie alike in these; else element by element.
+// An output that lies otherwise is written element by element, and the order of the
+// sums, so the result, does not depend on it.
+enum : int { WHOLE, GRANULES, SINGLES };
+int pieces_of(NormArgs& a, bool fwd) {
+  const int es = a.bf16 ? 2 : 4;
+  auto at = [&](const void* p, int64_t ld) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) | static_cast<int>(ld * es & 15) << 4;
   };
-  add(a.x, a.ld_x);
-  if (fwd) {
-    add(a.y, a.ld_y);
-    params |= reinterpret_cast<uintptr_t>(a.bias);
-  } else {
-    add(a.dy, a.ld_dy);
-    add(a.dx, a.ld_dx);
+  const int x = at(a.x, a.ld_x);
+  a.out16 = x == (fwd ? at(a.y, a.ld_y) : at(a.dx, a.ld_dx));
+  a.rows16 = x == 0;
+  if (!fwd && x != at(a.dy, a.ld_dy)) return SINGLES;
+  return a.rows16 && a.out16 && a.d * es % 16 == 0 && at(a.weight, 0) == 0 && (!fwd || at(a.bias, 0) == 0) ? WHOLE
+                                                                                                           : GRANULES;
+}
+// 16-byte pieces of a row, at most.
+template <int N>
+int64_t granules(const NormArgs& a) {
+  return (a.d + (a.rows16 ? 1 : 2) * (N - 1)) / N;
+}
+// CTAs whose groups, R a CTA, are a multiple of 8: rows so far apart lie alike in the
+// granules. (No more than one row a group: any number.)
+template <int R>
+int64_t whole_eights(int64_t grid, int64_t rows) {
+  constexpr int unit = R >= 8 ? 1 : 8 / R;
+  return grid * R >= rows || grid < unit ? grid : grid / unit * unit;
+}
+// CTAs of a kernel that an SM holds, asked once a device; -1 where that fails. `most`:
+// the largest shared memory that it is launched with.
+template <typename K>
+int ctas_of(K kernel, int threads, int smem, int most, std::atomic<uint64_t>& configured, std::atomic<int>& per_sm, cudaError_t* e) {
+  int dev = 0;
+  *e = cudaGetDevice(&dev);
+  if (*e != cudaSuccess) return -1;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    int n = 0;
+    if (*e == cudaSuccess) *e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+    if (*e != cudaSuccess) return -1;
+    per_sm.store(n < 1 ? 1 : n);
+    configured.fetch_or(bit);
   }
-  int n = 16 / es;
-  while (n > 1 && (a.d % n || rows % (n * es) || params % (n * ps < 16 ? n * ps : 16))) n /= 2;
-  return n;
+  return per_sm.load();
 }
 
 template <typename T, int N, int NV, int G, int R>
@@ -575,10 +796,28 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t s) {
   k_norm_fwd<T, N, NV, G, R><<<grid, G * R, 0, s>>>(a);
   return cudaGetLastError();
 }
+template <typename T, int NV, int G, int R>
+cudaError_t fwd_ragged(const NormArgs& a, int sms, cudaStream_t s) {
+  constexpr int N = 16 / static_cast<int>(sizeof(T)), ring = 2 * NV * 16 * G * R, par = NV * N * 4 * G * R;
+  const int smem = ring + (a.bias ? 2 : 1) * (a.param_bf16 ? par / 2 : par);
+  auto kernel = k_norm_fwd_ragged<T, NV, G, R>;
+  static std::atomic<uint64_t> configured[4];
+  static std::atomic<int> per_sm[4];
+  cudaError_t e;
+  const int which = (a.bias ? 2 : 0) + (a.param_bf16 ? 1 : 0);
+  const int n = ctas_of(kernel, G * R, smem, ring + 2 * par, configured[which], per_sm[which], &e);
+  if (n < 0) return e;
+  const int64_t all = (a.rows + R - 1) / R, most = static_cast<int64_t>(n) * sms;
+  const int64_t grid = whole_eights<R>(all < most ? all : most, a.rows);
+  kernel<<<static_cast<unsigned>(grid), G * R, smem, s>>>(a);
+  return cudaGetLastError();
+}
 template <typename T, int N>
 cudaError_t fwd_n(const NormArgs& a, cudaStream_t s) {
   const int64_t pieces = (a.d + N - 1) / N;
-  if (pieces <= 32) return fwd<T, N, 1, 32, 4>(a, s);
+  if (N > 1 && pieces <= 8) return fwd<T, N, 1, 8, 32>(a, s);
+  if (N > 1 && pieces <= 16) return fwd<T, N, 1, 16, 16>(a, s);
+  if (pieces <= 32) return fwd<T, N, 1, 32, 8>(a, s);
   if (pieces <= 64) return fwd<T, N, 2, 32, 4>(a, s);
   if (pieces <= 128) return fwd<T, N, 4, 32, 4>(a, s);
   if (pieces <= 256) return fwd<T, N, 2, 128, 1>(a, s);
@@ -590,36 +829,45 @@ cudaError_t fwd_n(const NormArgs& a, cudaStream_t s) {
   k_norm_fwd_long<T><<<static_cast<unsigned>(a.rows), kLong, 0, s>>>(a);
   return cudaGetLastError();
 }
+template <typename T>
+cudaError_t fwd_granules(const NormArgs& a, int sms, cudaStream_t s) {
+  constexpr int N = 16 / static_cast<int>(sizeof(T));
+  const int64_t pieces = granules<N>(a);
+  if (pieces <= 8) return fwd_ragged<T, 1, 8, 32>(a, sms, s);
+  if (pieces <= 16) return fwd_ragged<T, 1, 16, 16>(a, sms, s);
+  if (pieces <= 32) return fwd_ragged<T, 1, 32, 8>(a, sms, s);
+  if (pieces <= 64) return fwd_ragged<T, 2, 32, 4>(a, sms, s);
+  if (pieces <= 128) return fwd_ragged<T, 4, 32, 4>(a, sms, s);
+  if (pieces <= 256) return fwd_ragged<T, 2, 128, 1>(a, sms, s);
+  if (pieces <= 512) return fwd_ragged<T, 4, 128, 1>(a, sms, s);
+  if (pieces <= 768) return fwd_ragged<T, 3, 256, 1>(a, sms, s);
+  if (pieces <= 1024) return fwd_ragged<T, 4, 256, 1>(a, sms, s);
+  if (pieces <= 1536) return fwd_ragged<T, 3, 512, 1>(a, sms, s);
+  if (pieces <= 2048) return fwd_ragged<T, 4, 512, 1>(a, sms, s);
+  return fwd_n<T, 1>(a, s);
+}
 
 // One backward launch: as many CTAs as the SMs hold at a time, so that each walks
 // over its share of the rows once. *groups: rows of partial sums it writes.
-template <typename T, int N, int NV, int G, int R>
+template <typename T, int N, int NV, int G, int R, bool RAGGED>
 cudaError_t bwd(const NormArgs& a, int sms, int* groups, cudaStream_t s) {
   constexpr int slot = 2 * NV * N * static_cast<int>(sizeof(T)) * G * R;
   constexpr int Q = 4 * slot <= 200 * 1024 ? 2 : 1;
   constexpr int smem = 2 * Q * slot;
-  auto kernel = k_norm_bwd<T, N, NV, G, R, Q>;
-  static std::atomic<uint64_t> configured{0};  // one bit a device
+  auto kernel = k_norm_bwd<T, N, NV, G, R, Q, RAGGED>;
+  static std::atomic<uint64_t> configured{0};
   static std::atomic<int> per_sm{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(configured.load() & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    int n = 0;
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, G * R, smem);
-    if (e != cudaSuccess) return e;
-    per_sm.store(n < 1 ? 1 : n);
-    configured.fetch_or(bit);
-  }
+  cudaError_t e;
+  const int n = ctas_of(kernel, G * R, smem, smem, configured, per_sm, &e);
+  if (n < 0) return e;
   // four rows a group at least, where that leaves the SMs at work: a group's
   // partial sums are written and read again
   int64_t grid = (a.rows + R - 1) / R;
   if (grid > sms / 2) grid = grid / 4 > sms / 2 ? grid / 4 : sms / 2;
-  const int64_t most = static_cast<int64_t>(per_sm.load()) * sms, room = norm_parts(a, sms) / R;
+  const int64_t most = static_cast<int64_t>(n) * sms, room = norm_parts(a, sms) / R;
   grid = grid < most ? grid : most;
   grid = grid < room ? grid : room;
+  if (RAGGED) grid = whole_eights<R>(grid, a.rows);
   *groups = static_cast<int>(grid) * R;
   kernel<<<static_cast<unsigned>(grid), G * R, smem, s>>>(a);
   return cudaGetLastError();
@@ -628,20 +876,23 @@ cudaError_t bwd(const NormArgs& a, int sms, int* groups, cudaStream_t s) {
 // A row is given to few threads with several pieces each: the fewer warps join
 // their sums, the more rows an SM has under way (163840 x 4096 bf16: 512 threads
 // a row 811 us, 256 with two pieces 679 us).
-template <typename T, int N>
+template <typename T, int N, bool RAGGED>
 cudaError_t bwd_n(const NormArgs& a, int sms, int* groups, cudaStream_t s) {
-  const int64_t pieces = (a.d + N - 1) / N;
-  if (pieces <= 32) return bwd<T, N, 1, 32, 8>(a, sms, groups, s);
-  if (pieces <= 64) return bwd<T, N, 2, 32, 8>(a, sms, groups, s);
-  if (pieces <= 128) return bwd<T, N, 2, 64, 4>(a, sms, groups, s);
-  if (pieces <= 256) return bwd<T, N, 2, 128, 1>(a, sms, groups, s);
-  if (pieces <= 384) return bwd<T, N, 3, 128, 1>(a, sms, groups, s);
-  if (pieces <= 512) return bwd<T, N, 2, 256, 1>(a, sms, groups, s);
-  if (pieces <= 768) return bwd<T, N, 3, 256, 1>(a, sms, groups, s);
-  if (pieces <= 1024) return bwd<T, N, 2, 512, 1>(a, sms, groups, s);
-  if (pieces <= 2048) return bwd<T, N, 4, 512, 1>(a, sms, groups, s);
-  if constexpr (N <= 2) {
-    if (pieces <= 4096) return bwd<T, N, 4, 1024, 1>(a, sms, groups, s);
+  const int64_t pieces = RAGGED ? granules<N>(a) : (a.d + N - 1) / N;
+  if (pieces <= 32) return bwd<T, N, 1, 32, 8, RAGGED>(a, sms, groups, s);
+  if (pieces <= 64) return bwd<T, N, 2, 32, 8, RAGGED>(a, sms, groups, s);
+  if (pieces <= 128) return bwd<T, N, 2, 64, 4, RAGGED>(a, sms, groups, s);
+  if (pieces <= 256) return bwd<T, N, 2, 128, 1, RAGGED>(a, sms, groups, s);
+  if (pieces <= 384) return bwd<T, N, 3, 128, 1, RAGGED>(a, sms, groups, s);
+  if (pieces <= 512) return bwd<T, N, 2, 256, 1, RAGGED>(a, sms, groups, s);
+  if (pieces <= 768) return bwd<T, N, 3, 256, 1, RAGGED>(a, sms, groups, s);
+  if (pieces <= 1024) return bwd<T, N, 2, 512, 1, RAGGED>(a, sms, groups, s);
+  if (pieces <= 1536) return bwd<T, N, 3, 512, 1, RAGGED>(a, sms, groups, s);
+  if (pieces <= 2048) return bwd<T, N, 4, 512, 1, RAGGED>(a, sms, groups, s);
+  if constexpr (N > 1) {
+    if (pieces <= 3072) return bwd<T, N, 3, 1024, 1, RAGGED>(a, sms, groups, s);
+  } else {
+    if (pieces <= 4096) return bwd<T, N, 4, 1024, 1, RAGGED>(a, sms, groups, s);
   }
   const int64_t most = 2ll * sms;
   *groups = static_cast<int>(a.rows < most ? a.rows : most);
@@ -659,26 +910,26 @@ int norm_parts(const NormArgs& a, int sms) {
   return static_cast<int>(need < 8 ? 8 : need < most ? need : most);
 }
 
-cudaError_t launch_norm_fwd(const NormArgs& a, int, cudaStream_t s) {
-  const int n = piece_of(a, true);
+cudaError_t launch_norm_fwd(const NormArgs& args, int sms, cudaStream_t s) {
+  NormArgs a = args;
+  const int how = pieces_of(a, true);
   if (a.bf16)
-    return n == 8   ? fwd_n<__nv_bfloat16, 8>(a, s)
-           : n == 4 ? fwd_n<__nv_bfloat16, 4>(a, s)
-           : n == 2 ? fwd_n<__nv_bfloat16, 2>(a, s)
-                    : fwd_n<__nv_bfloat16, 1>(a, s);
-  return n == 4 ? fwd_n<float, 4>(a, s) : n == 2 ? fwd_n<float, 2>(a, s) : fwd_n<float, 1>(a, s);
+    return how == WHOLE      ? fwd_n<__nv_bfloat16, 8>(a, s)
+           : how == GRANULES ? fwd_granules<__nv_bfloat16>(a, sms, s)
+                             : fwd_n<__nv_bfloat16, 1>(a, s);
+  return how == WHOLE ? fwd_n<float, 4>(a, s) : how == GRANULES ? fwd_granules<float>(a, sms, s) : fwd_n<float, 1>(a, s);
 }
 
-cudaError_t launch_norm_bwd(const NormArgs& a, int sms, int* groups, cudaStream_t s) {
-  const int n = piece_of(a, false);
+cudaError_t launch_norm_bwd(const NormArgs& args, int sms, int* groups, cudaStream_t s) {
+  NormArgs a = args;
+  const int how = pieces_of(a, false);
   if (a.bf16)
-    return n == 8   ? bwd_n<__nv_bfloat16, 8>(a, sms, groups, s)
-           : n == 4 ? bwd_n<__nv_bfloat16, 4>(a, sms, groups, s)
-           : n == 2 ? bwd_n<__nv_bfloat16, 2>(a, sms, groups, s)
-                    : bwd_n<__nv_bfloat16, 1>(a, sms, groups, s);
-  return n == 4   ? bwd_n<float, 4>(a, sms, groups, s)
-         : n == 2 ? bwd_n<float, 2>(a, sms, groups, s)
-                  : bwd_n<float, 1>(a, sms, groups, s);
+    return how == WHOLE      ? bwd_n<__nv_bfloat16, 8, false>(a, sms, groups, s)
+           : how == GRANULES ? bwd_n<__nv_bfloat16, 8, true>(a, sms, groups, s)
+                             : bwd_n<__nv_bfloat16, 1, false>(a, sms, groups, s);
+  return how == WHOLE      ? bwd_n<float, 4, false>(a, sms, groups, s)
+         : how == GRANULES ? bwd_n<float, 4, true>(a, sms, groups, s)
+                           : bwd_n<float, 1, false>(a, sms, groups, s);
 }
 
 cudaError_t launch_norm_colsum(const NormArgs& a, int groups, cudaStream_t s) {

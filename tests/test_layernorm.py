@@ -115,6 +115,40 @@ def test_strided_and_unaligned_rows(dtype, offset, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,d", [(4000, 3), (5000, 67), (3000, 129), (2000, 513), (1700, 1001), (1300, 2881), (700, 5003),
+                                    (400, 9999), (330, 16383), (90, 1001), (77, 67)])
+def test_odd_widths_over_many_rows(rows, d):
+    """Rows that begin anywhere in a 16-byte granule, several of them a CTA."""
+    for dtype, pdtype, rms in ((BF16, BF16, False), (F32, F32, False), (BF16, F32, True)):
+        x, w, b, dy = inputs(rows, d, dtype, pdtype, bias=not rms)
+        x[0] *= 3.0
+        check(x, w, b, dy, rms)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_and_operands_that_lie_differently(dtype):
+    """Bases off a 16-byte boundary, odd strides, operands that differ in both;
+    NaN beside the rows stays out of them."""
+    import grpo_loss_gb300 as G
+    rows, d = 900, 257
+    x, w, b, dy = inputs(rows, d, dtype, dtype)
+
+    def laid(t, base, ld):
+        flat = torch.full((base + rows * ld,), float("nan"), dtype=dtype, device="cuda")
+        view = flat[base:].view(rows, ld)[:, :d]
+        view.copy_(t)
+        return view
+
+    for bases, lds in (((1, 1), (261, 261)), ((5, 5), (257, 257)), ((0, 3), (264, 264)), ((2, 2), (259, 275)), ((8, 0), (264, 257))):
+        xs, gs = laid(x, bases[0], lds[0]), laid(dy, bases[1], lds[1])
+        y, mean, rstd, dx, dw, db = check(xs, w, b, gs)
+        out = laid(torch.zeros_like(x), bases[0], lds[0])
+        assert torch.equal(G.layernorm_bwd(xs, w, gs, mean, rstd, dx=out)[0], dx)
+        assert torch.equal(G.layernorm_fwd(xs, w, b, y=out)[0], y)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,d", [(50, 1024), (50, 1021), (3, 65536)])
 def test_in_place(rows, d):
     import grpo_loss_gb300 as G
