@@ -5,9 +5,10 @@
 // power of two a block of 32. Bound by memory: every buffer is read and written
 // once (30 bytes an element with bf16 parameters, masters and float32
 // gradients and states; 10 with bf16 gradients and 8-bit states). 233 M elements
-// with masters: 994 us (7.0 TB/s); with 8-bit states and float32 gradients 513 us
-// (5.5 TB/s): there some 60 instructions an element come near to what the SMs issue
-// (with the update's arithmetic one element at a time, 71 of them, 557 us).
+// with masters: 994 us (7.0 TB/s); with 8-bit states and float32 gradients 462 us
+// (6.1 TB/s): there some 60 instructions an element weigh as much as the bytes (with
+// the update's arithmetic one element at a time, 71 of them, 557 us; with pairs 513;
+// the rest is the second step's bytes asked for ahead).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -150,6 +151,11 @@ __device__ __forceinline__ uint32_t param_bits(float x, uint32_t d) {
 // Magnitude bits: they order like the magnitudes, infinities and NaN above all.
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
+// Asks L2 for n elements from `from` on.
+__device__ __forceinline__ void prefetch(const char* p, int size, int from, int n) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p + from * size), "r"(n * size) : "memory");
+}
+
 // Whole pieces of W elements of a chunk that starts at element i0, `end` elements
 // in all (a multiple of 32; every buffer on a 16-byte boundary). With 8-bit
 // states four threads hold a block of 32.
@@ -170,6 +176,16 @@ __device__ __forceinline__ void pieces(const AdamConst& c, const AdamTensor& t, 
   char* const v_to = to(t.v_out, kSS);
   char* const p_to = to(t.p_out, kPBf16 ? 2 : 4);
   const float keep = t.keep;
+  if (k8 && threadIdx.x == 0 && end > kThreads * W) {
+    // the second step's bytes, asked for while the first's are waited for (registers for
+    // them there are none: two steps' loads at a time spill, 647 us); with float32
+    // states two steps' loads are in flight as it is
+    const int from = kThreads * W, n = end - from;
+    prefetch(g_in, kGBf16 ? 2 : 4, from, n);
+    prefetch(x_in, kMaster || !kPBf16 ? 4 : 2, from, n);
+    prefetch(m_in, 1, from, n);
+    prefetch(v_in, 1, from, n);
+  }
   for (int k0 = threadIdx.x * W; k0 < end; k0 += kThreads * W * U) {
     float g[U][W], x[U][W], m[U][W], v[U][W];
     uint2 cm, cv;
