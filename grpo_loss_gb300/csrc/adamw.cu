@@ -5,8 +5,8 @@
 // power of two a block of 32. Bound by memory: every buffer is read and written
 // once (30 bytes an element with bf16 parameters, masters and float32
 // gradients and states; 10 with bf16 gradients and 8-bit states). 233 M elements
-// with masters: 994 us (7.0 TB/s); with 8-bit states and float32 gradients 462 us
-// (6.1 TB/s): there some 60 instructions an element weigh as much as the bytes (with
+// with masters: 994 us (7.0 TB/s); with 8-bit states and float32 gradients 475 us
+// (6.0 TB/s): there some 60 instructions an element weigh as much as the bytes (with
 // the update's arithmetic one element at a time, 71 of them, 557 us; with pairs 513;
 // the rest is the second step's bytes asked for ahead).
 #include <cuda_bf16.h>
@@ -84,19 +84,22 @@ __device__ __forceinline__ void update(const AdamConst& c, float keep, float g, 
   x = __fmaf_rn(-c.lr_t, __fmul_rn(m, inv), __fmul_rn(x, keep));
 }
 
-// The same of two elements, bit by bit.
+// The same of two elements, bit by bit. (The sums are one at a time: the assembler
+// fuses a product and a sum of pairs into one rounding.)
 __device__ __forceinline__ void update2(const AdamConst& c, float keep, float* g, float* x, float* m, float* v) {
   const uint64_t g2 = mul2(pair_of(g[0], g[1]), pair_of(c.grad_scale));
-  const uint64_t m2 = add2(mul2(pair_of(c.beta1), pair_of(m[0], m[1])), mul2(pair_of(c.one_m_beta1), g2));
-  const uint64_t v2 = add2(mul2(pair_of(c.beta2), pair_of(v[0], v[1])), mul2(mul2(pair_of(c.one_m_beta2), g2), g2));
-  const float2 mm = of_pair(m2), vv = of_pair(v2);
+  const float2 m0 = of_pair(mul2(pair_of(c.beta1), pair_of(m[0], m[1]))), m1 = of_pair(mul2(pair_of(c.one_m_beta1), g2));
+  const float2 v0 = of_pair(mul2(pair_of(c.beta2), pair_of(v[0], v[1])));
+  const float2 v1 = of_pair(mul2(mul2(pair_of(c.one_m_beta2), g2), g2));
+  const float2 mm = make_float2(__fadd_rn(m0.x, m1.x), __fadd_rn(m0.y, m1.y));
+  const float2 vv = make_float2(__fadd_rn(v0.x, v1.x), __fadd_rn(v0.y, v1.y));
   float2 root, inv;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(root.x) : "f"(vv.x));
   asm("sqrt.approx.f32 %0, %1;" : "=f"(root.y) : "f"(vv.y));
   const float2 den = of_pair(fma2(pair_of(root.x, root.y), pair_of(c.rsqrt_c2), pair_of(c.eps)));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.x) : "f"(den.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.y) : "f"(den.y));
-  const float2 xx = of_pair(fma2(pair_of(-c.lr_t), mul2(m2, pair_of(inv.x, inv.y)), mul2(pair_of(x[0], x[1]), pair_of(keep))));
+  const float2 xx = of_pair(fma2(pair_of(-c.lr_t), mul2(pair_of(mm.x, mm.y), pair_of(inv.x, inv.y)), mul2(pair_of(x[0], x[1]), pair_of(keep))));
   m[0] = mm.x, m[1] = mm.y, v[0] = vv.x, v[1] = vv.y, x[0] = xx.x, x[1] = xx.y;
 }
 

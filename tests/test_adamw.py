@@ -255,7 +255,37 @@ def test_repeats_streams_and_graphs():
                     assert (t is None and k is None) or torch.equal(t, k)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_same_bits_on_and_off_a_boundary(dtype, bits):
+    """Elements that are taken in pieces and one by one, and moments that are those
+    of float32 operations one after the other."""
+    import grpo_loss_gb300 as G
+    n = 20000
+    g = torch.Generator(device="cuda").manual_seed(7)
+    rand = lambda: torch.randn(n, generator=g, device="cuda")  # noqa: E731
+    p, grads = rand().to(dtype), [rand() * 1e-3 for _ in range(4)]
+    shifted = torch.empty(n + 1, dtype=dtype, device="cuda")[1:].copy_(p)
+    a, b = (G.AdamW([t], state_bits=bits, lr=1e-2) for t in (p, shifted))
+    m, v = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    for x in grads:
+        off = torch.empty(n + 1, device="cuda")[1:].copy_(x)
+        a.step([x])
+        b.step([off])
+        m, v = 0.9 * m + (1 - 0.9) * x, 0.999 * v + (1 - 0.999) * x * x
+        for s, t in zip((a.params, a.exp_avg, a.exp_avg_sq), (b.params, b.exp_avg, b.exp_avg_sq)):
+            assert torch.equal(s[0], t[0])
+        if bits == 32:
+            assert torch.equal(a.exp_avg[0], m) and torch.equal(a.exp_avg_sq[0], v)
+        else:
+            assert torch.equal(a.exp_avg_scale[0], b.exp_avg_scale[0])
+            assert torch.equal(a.exp_avg_sq_scale[0], b.exp_avg_sq_scale[0])
+
+
 # ---------------------------------------------------------------- refusals
+
+
 @pytest.fixture(scope="module")
 def lib():
     import os
