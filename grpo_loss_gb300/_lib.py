@@ -364,10 +364,27 @@ def _vec_ptr(t, name: str, dtype, numel: int, device):
     return t.data_ptr()
 
 
+def _rows_out(t, name: str, dtype, rows: int, cols: int, device):
+    """(tensor, pointer, row stride) of an output that is given or made."""
+    if t is None:
+        t = torch.empty(rows, cols, dtype=dtype, device=device)
+        return t, t.data_ptr(), cols
+    return (t,) + _rows_ptr(t, name, dtype, rows, cols, device)
+
+
+def _vec_out(t, name: str, dtype, numel: int, device):
+    """(tensor, pointer) of an output that is given or made."""
+    if t is None:
+        t = torch.empty(numel, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _vec_ptr(t, name, dtype, numel, device)
+
+
 def _call(fn, where: str, device, stream, *args) -> None:
     """fn(*args, stream) with ``device`` current, on ``stream`` or the device's
     current one. The launches of small operators are bound by the host: torch's
-    own stream and device objects are not made where their numbers will do."""
+    own stream and device objects are not made where their numbers will do (nor is
+    new_empty used for outputs: torch.empty takes 2 us less of a tensor)."""
     at = device.index
     raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(at)
     if torch._C._cuda_getDevice() == at:
@@ -386,7 +403,11 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     logp float32 [rows]). ``temperature``, ``top_p``, ``min_p`` (float32 [rows])
     and ``top_k`` (int32 [rows]) are optional; see grpo_sample for the
     definition. logp is the token's log-probability under the full softmax at
-    its temperature, what a GRPOLoss with that temperature calls logp_pol."""
+    its temperature, what a GRPOLoss with that temperature calls logp_pol.
+    Outputs that are not given belong to ``stream``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return sample(logits, u, temperature, top_k, top_p, min_p, tokens, logp)
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D")
     rows, V = logits.shape
@@ -394,15 +415,12 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     code = _plain_code(logits.dtype, "logits")
     dev = _device_of(logits, "logits")
     ptr, ld = _rows_ptr(logits, "logits", logits.dtype, rows, V, dev)
-    if tokens is None:
-        tokens = logits.new_empty(rows, dtype=i32)
-    if logp is None:
-        logp = logits.new_empty(rows, dtype=f32)
-    _call(lib().grpo_sample, "grpo_sample", dev, stream, SampleProblem(rows, V, ld, code), ptr,
+    tokens, tp = _vec_out(tokens, "tokens", i32, rows, dev)
+    logp, lp = _vec_out(logp, "logp", f32, rows, dev)
+    _call(lib().grpo_sample, "grpo_sample", dev, None, SampleProblem(rows, V, ld, code), ptr,
           _vec_ptr(u, "u", f32, rows, dev), _vec_ptr(temperature, "temperature", f32, rows, dev),
           _vec_ptr(top_k, "top_k", i32, rows, dev), _vec_ptr(top_p, "top_p", f32, rows, dev),
-          _vec_ptr(min_p, "min_p", f32, rows, dev), _vec_ptr(tokens, "tokens", i32, rows, dev),
-          _vec_ptr(logp, "logp", f32, rows, dev))
+          _vec_ptr(min_p, "min_p", f32, rows, dev), tp, lp)
     return tokens, logp
 
 
@@ -418,7 +436,11 @@ def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float =
                   rms: bool = False, y=None, mean=None, rstd=None, stream=None):
     """Layer norm (RMS norm with ``rms``) of the rows of ``x`` (float32 or bf16
     [rows, d], rows may be strided): (y, mean, rstd), mean None with ``rms``.
-    ``weight`` and ``bias`` are float32 or bf16 [d], of one type."""
+    ``weight`` and ``bias`` are float32 or bf16 [d], of one type. Outputs that are
+    not given belong to ``stream``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layernorm_fwd(x, weight, bias, eps, rms, y, mean, rstd)
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     rows, d = x.shape
@@ -426,19 +448,12 @@ def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float =
     code, pcode = _plain_code(dt, "x"), _plain_code(pt, "weight")
     dev = _device_of(x, "x")
     xp, ld_x = _rows_ptr(x, "x", dt, rows, d, dev)
-    if y is None:
-        y = x.new_empty((rows, d))
-    yp, ld_y = _rows_ptr(y, "y", dt, rows, d, dev)
-    if rms:
-        mean = None
-    elif mean is None:
-        mean = x.new_empty(rows, dtype=f32)
-    if rstd is None:
-        rstd = x.new_empty(rows, dtype=f32)
+    y, yp, ld_y = _rows_out(y, "y", dt, rows, d, dev)
+    mean, mp = (None, None) if rms else _vec_out(mean, "mean", f32, rows, dev)
+    rstd, rp = _vec_out(rstd, "rstd", f32, rows, dev)
     problem = LayernormProblem(rows, d, ld_x, ld_y, 0, 0, eps, 1 if rms else 0, code, pcode)
-    _call(lib().grpo_layernorm_fwd, "grpo_layernorm_fwd", dev, stream, problem, xp,
-          _vec_ptr(weight, "weight", pt, d, dev), _vec_ptr(bias, "bias", pt, d, dev), yp,
-          _vec_ptr(mean, "mean", f32, rows, dev), _vec_ptr(rstd, "rstd", f32, rows, dev))
+    _call(lib().grpo_layernorm_fwd, "grpo_layernorm_fwd", dev, None, problem, xp,
+          _vec_ptr(weight, "weight", pt, d, dev), _vec_ptr(bias, "bias", pt, d, dev), yp, mp, rp)
     return y, mean, rstd
 
 
@@ -447,7 +462,12 @@ def layernorm_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, mean,
                   need_dweight: bool = True, workspace=None, stream=None):
     """Gradients of ``layernorm_fwd`` from its inputs and statistics: (dx,
     dweight, dbias), dx of x's type, the column sums float32 [d]; dweight is None
-    without ``need_dweight``, dbias without ``bias`` or with ``rms``."""
+    without ``need_dweight``, dbias without ``bias`` or with ``rms``. Outputs and a
+    workspace that are not given belong to ``stream``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layernorm_bwd(x, weight, dy, mean, rstd, rms, bias, dx, dweight, dbias,
+                                 need_dweight, workspace)
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     rows, d = x.shape
@@ -458,13 +478,12 @@ def layernorm_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, mean,
         raise ValueError("mean is needed unless rms")
     xp, ld_x = _rows_ptr(x, "x", dt, rows, d, dev)
     gp, ld_dy = _rows_ptr(dy, "dy", dt, rows, d, dev)
-    if dx is None:
-        dx = x.new_empty((rows, d))
-    dxp, ld_dx = _rows_ptr(dx, "dx", dt, rows, d, dev)
-    if dweight is None and need_dweight:
-        dweight = x.new_empty(d, dtype=f32)
-    if dbias is None and bias and not rms:
-        dbias = x.new_empty(d, dtype=f32)
+    dx, dxp, ld_dx = _rows_out(dx, "dx", dt, rows, d, dev)
+    wp = bp = None
+    if dweight is not None or need_dweight:
+        dweight, wp = _vec_out(dweight, "dweight", f32, d, dev)
+    if dbias is not None or (bias and not rms):
+        dbias, bp = _vec_out(dbias, "dbias", f32, d, dev)
     problem = LayernormProblem(rows, d, ld_x, 0, ld_dy, ld_dx, 0.0, 1 if rms else 0, code, pcode)
     size = 0
     if workspace is None and (dweight is not None or dbias is not None):
@@ -473,14 +492,13 @@ def layernorm_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, mean,
         else:
             with torch.cuda.device(dev):
                 size = layernorm_workspace_size(problem)
-        workspace = x.new_empty(size, dtype=torch.uint8)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     elif workspace is not None:
         size = workspace.numel() * workspace.element_size()
-    _call(lib().grpo_layernorm_bwd, "grpo_layernorm_bwd", dev, stream, problem, xp,
+    _call(lib().grpo_layernorm_bwd, "grpo_layernorm_bwd", dev, None, problem, xp,
           _vec_ptr(weight, "weight", pt, d, dev), gp,
           None if rms else _vec_ptr(mean, "mean", f32, rows, dev),
-          _vec_ptr(rstd, "rstd", f32, rows, dev), dxp, _vec_ptr(dweight, "dweight", f32, d, dev),
-          _vec_ptr(dbias, "dbias", f32, d, dev),
+          _vec_ptr(rstd, "rstd", f32, rows, dev), dxp, wp, bp,
           None if workspace is None else _vec_ptr(workspace, "workspace", workspace.dtype,
                                                   workspace.numel(), dev), size)
     return dx, dweight, dbias

@@ -149,6 +149,26 @@ def test_rows_and_operands_that_lie_differently(dtype):
 
 
 @pytest.mark.gpu
+def test_another_stream_owns_what_it_makes():
+    """A workspace made by a call on a side stream is not handed to the current
+    stream's next tensors while the call runs."""
+    import grpo_loss_gb300 as G
+    x, w, b, dy = inputs(20000, 1024, BF16, BF16)
+    y, mean, rstd = G.layernorm_fwd(x, w, b)
+    want = G.layernorm_bwd(x, w, dy, mean, rstd)
+    size = G._lib.layernorm_workspace_size(G._lib.LayernormProblem(20000, 1024, 1024, 0, 1024, 1024, 0.0, 0, 1, 1))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        ys, ms, rs = G.layernorm_fwd(x, w, b, stream=side)
+        got = G.layernorm_bwd(x, w, dy, ms, rs, stream=side)
+        junk = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(ys, y) and all(torch.equal(s, t) for s, t in zip(got, want))
+        del junk
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("d", [64, 512, 1000, 4096, 8192])
 def test_outputs_off_a_boundary_have_the_same_bits(d, dtype):
