@@ -890,7 +890,7 @@ cudaError_t bwd_n(const NormArgs& a, int sms, int* groups, cudaStream_t s) {
   if (pieces <= 1536) return bwd<T, N, 3, 512, 1, RAGGED>(a, sms, groups, s);
   if (pieces <= 2048) return bwd<T, N, 4, 512, 1, RAGGED>(a, sms, groups, s);
   if constexpr (N > 1) {
-    if (pieces <= 3072) return bwd<T, N, 3, 1024, 1, RAGGED>(a, sms, groups, s);
+    if (pieces <= 3 * 1024) return bwd<T, N, 3, 1024, 1, RAGGED>(a, sms, groups, s);
   } else {
     if (pieces <= 4096) return bwd<T, N, 4, 1024, 1, RAGGED>(a, sms, groups, s);
   }

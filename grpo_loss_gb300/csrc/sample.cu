@@ -8,14 +8,14 @@
 // of the order (logit descending, index ascending): what is kept is a threshold t
 // on the logit's sort key and a number of ties at t, the first in index order.
 //
-// The bytes of a row are read in well under a microsecond's share of the memory's
-// rate; what bounds a call is the work on each logit, some eight cycles of an SM for
-// 32 of them and a pass, and for few rows the barriers between the questions that a
-// row is asked. Three kernels share the parts below:
+// What bounds a call is not the bytes of a row (31 us of the 135 that 512 mixed rows of
+// 201088 take) but the work on each logit, two to ten cycles of an SM for 32 of them and
+// a pass, and for few rows the barriers between the questions that a row is asked.
+// Three kernels share the parts below:
 //
 // - k_sample_counts (bf16 rows): the row as counts of its few distinct values, in
 //   which every sum is exact and every cut-off is a search; a cluster of CTAs a row.
-//   One row of 128256: 15 us; 64 rows: 23 to 32.
+//   One row of 128256: 14 to 17 us; 64 rows: 22 to 31.
 // - k_sample (float32 rows, and short ones): two ways of weighing share one body. The
 //   fast one takes 2^y from a polynomial and carries a bound E on the error of its
 //   sums; where the draw or the top-p cut falls within E of a border, the row is
@@ -23,12 +23,12 @@
 //   A trained model's rows (a few likely tokens) seldom need that. A cluster takes a
 //   row, each CTA one slice of it that it copies into shared memory once, and every
 //   question (maximum, sums, histogram, draw) reads that and is joined through
-//   distributed shared memory. 8 rows of 128256: 17 to 32 us with few candidates or
-//   none, 22 to 108 with top-p alone.
-// - k_sample_rows (rows enough for every SM): a CTA a row in two passes, for what a list
-//   of a few candidates or the plain softmax decides; the others are left to a second
-//   launch of the kernels above. 512 rows of 201088 in bf16: greedy and small top-k
-//   85 to 91 us, all rows left to the second launch (wide top-p) 298 to 330.
+//   distributed shared memory. 8 rows of 128256: 16 to 35 us with few candidates or
+//   no cut-off, 21 to 105 with top-p alone.
+// - k_sample_rows (rows enough for every SM): a CTA a row in little more than a pass, for
+//   what a list of a few candidates or the plain softmax decides; the others are left to
+//   a second launch of the kernels above. 512 rows of 201088 in bf16: greedy and small
+//   top-k 66 to 78 us, all rows left to the second launch (wide top-p) 302 to 348.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -1486,11 +1486,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1)
 
 // Many rows: a CTA takes a row and reads it once for the maximum and the mass (each
 // lane weighs against the largest logit it has seen, and scales its sum down when a
-// larger one comes), and, as a rule from L2, once more for the candidates. Greedy, top-k,
-// min-p and plain softmax rows end here, and top-p rows whose cut is within the
-// list; what is left is marked for a second launch. The masses are of rough weights:
-// with the fast ones, which leave fewer rows, 512 greedy rows of 201088 took 118 us
-// for 85, and as many plain ones 163 for 128 (spread-out logits) and 244 for 238 (flat).
+// larger one comes). On the way it notes the pieces that may hold candidates, from a
+// bound that rises as the row is read; only the row's first steps are read again. Greedy,
+// top-k, min-p and plain softmax rows end here, and top-p rows whose cut is within the
+// list; what is left is marked for a second launch. 512 greedy rows of 201088 take 66 us,
+// with a second pass for the candidates 85. The masses are of rough weights: with the
+// fast ones, which leave fewer rows, that was 118, and as many plain rows took 163 for
+// 133 (spread-out logits) and 244 for 238 (flat).
 constexpr int kRowThreads = 256;
 constexpr int kFirstSteps = 4;  // a power of two
 template <typename T>
@@ -1797,9 +1799,9 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
 // A row that does not fit the counters (nonzero values more than 30 binary orders
 // below) and T near 0 or infinity go through decide().
 //
-// One row of 128256 on 8 CTAs takes 28,000 cycles: 3,000 until the first logits are
-// there, 5,000 for their counts, 8,000 for the weights, some 3,000 for each join, 5,000
-// for the draw's pass. With one CTA a row the two passes are most of it, 7 and 10
+// One row of 128256 on 8 CTAs takes 30,000 cycles: 2,000 until the loads are out, 4,000
+// for the counts, 6,000 for the weights, 2,000 to 2,600 for each join, 5,000 for the cut,
+// 8,000 for the draw. With one CTA a row the two passes are most of it, 7 and 10
 // cycles for 32 logits: the banks of shared memory, on which 32 values fall in 3 or
 // 4 turns. (The draw's pass with the fast weights took as long: their 12
 // instructions a logit.) Against lists, histograms of masses and the two ways of
