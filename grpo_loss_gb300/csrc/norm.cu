@@ -745,7 +745,8 @@ __global__ void __launch_bounds__(1024) k_norm_colsum(NormArgs a, int parts) {
 // and the weights, are on 16-byte boundaries and d is whole pieces; else by 16-byte
 // granules, where the rows of the inputs lie alike in these; else element by element.
 // An output that lies otherwise is written element by element: the order of a row's
-// sums, so y, dx and the statistics, do not depend on it.
+// sums, so y, dx and the statistics, do not depend on it, in rows of up to 2048 pieces
+// (longer ones are taken element by element then).
 enum : int { WHOLE, GRANULES, SINGLES };
 int pieces_of(NormArgs& a, bool fwd) {
   const int es = a.bf16 ? 2 : 4;
