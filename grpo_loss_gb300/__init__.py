@@ -11,6 +11,7 @@ not been built.
 """
 from __future__ import annotations
 
+import operator
 from typing import Optional, Sequence
 
 import numpy as np
@@ -200,6 +201,11 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     return _LayerNormFn.apply(x.reshape(-1, x.shape[-1]), weight, bias, eps, rms).view(x.shape)
 
 
+_DATA_PTR, _CONTIGUOUS, _GET_DEVICE = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
+_NBYTES, _DTYPE, _SHAPE = operator.attrgetter("nbytes"), operator.attrgetter("dtype"), operator.attrgetter("shape")
+_PLAIN_CODES = {torch.float32: _lib.GRPO_F32, torch.bfloat16: _lib.GRPO_BF16}
+
+
 class AdamW:
     """AdamW over a list of CUDA tensors (float32 or bf16, contiguous), one call
     for all of them; the arithmetic and the state formats are those of
@@ -242,20 +248,24 @@ class AdamW:
             self.exp_avg_sq.append(torch.zeros(p.shape, **st))
             for scales in (self.exp_avg_scale, self.exp_avg_sq_scale):
                 scales.append(torch.zeros((p.numel() + 31) // 32, **st) if eight else None)
-        self._bind()
+        self._bind(self._key())
 
-    def _pointers(self):
-        return [None if t is None else t.data_ptr() for ts in (
-            self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale,
-            self.exp_avg_sq_scale) for t in ts]
+    def _key(self):
+        """What the table was made of: the place and bytes of every tensor, and of the
+        parameters, which are the caller's, type, shape and layout as well. (Methods of
+        the class, mapped: a step's host time is these walks.)"""
+        given = [*self.masters, *self.exp_avg_scale, *self.exp_avg_sq_scale]
+        ts = [*self.params, *self.exp_avg, *self.exp_avg_sq, *[t for t in given if t is not None]]
+        return (list(map(_DATA_PTR, ts)), list(map(_NBYTES, ts)), list(map(_DTYPE, self.params)),
+                list(map(_SHAPE, self.params)), all(map(_CONTIGUOUS, self.params)), [t is None for t in given])
 
-    def _bind(self) -> None:
-        """Fill the table of the tensors that a step is given (again, when a tensor
-        of the lists was replaced or moved)."""
+    def _bind(self, key) -> None:
+        """Make the table of the tensors that a step is given (again, when a tensor of
+        the lists was replaced, moved or resized). A refusal leaves the old one."""
         n, state = len(self.params), torch.uint8 if self.state_bits == 8 else torch.float32
-        self._table = (_lib.AdamwTensor * max(n, 1))()
+        table = (_lib.AdamwTensor * max(n, 1))()
         for i, p in enumerate(self.params):
-            t, dev, many = self._table[i], self.device, p.numel()
+            t, dev, many = table[i], self.device, p.numel()
             t.n, t.weight_decay = many, self.weight_decay[i]
             t.param_dtype = _lib._plain_code(p.dtype, "params[%d]" % i)
             t.param = _lib._vec_ptr(p, "params[%d]" % i, p.dtype, many, dev)
@@ -265,10 +275,13 @@ class AdamW:
             scales = (many + 31) // 32
             t.m_scale = _lib._vec_ptr(self.exp_avg_scale[i], "exp_avg_scale[%d]" % i, state, scales, dev)
             t.v_scale = _lib._vec_ptr(self.exp_avg_sq_scale[i], "exp_avg_sq_scale[%d]" % i, state, scales, dev)
-        self._columns = np.frombuffer(self._table, dtype=_lib.ADAMW_COLUMNS)[:n]   # the same memory
+        self._table = table
+        self._columns = np.frombuffer(table, dtype=_lib.ADAMW_COLUMNS)[:n]   # the same memory
+        self._shapes = [p.shape for p in self.params]
+        self._at = self.params[0].get_device() if n else -1
         self._kinds = [(self.state_bits, p.shape, p.dtype, m is None)
                        for p, m in zip(self.params, self.masters)]
-        self._bound = self._pointers()
+        self._bound = key
 
     def step(self, grads: Sequence[torch.Tensor], grad_scale: float = 1.0, lr: Optional[float] = None,
              step: Optional[int] = None, out: Optional["AdamW"] = None, stream=None) -> None:
@@ -278,19 +291,19 @@ class AdamW:
         if len(grads) != n:
             raise ValueError("expected %d gradients, got %d" % (n, len(grads)))
         for o in (self,) if out is None else (self, out):
-            if o._pointers() != o._bound:
-                o._bind()
+            key = o._key()
+            if key != o._bound:
+                o._bind(key)
         if out is not None and (out is self or out._kinds != self._kinds or out.device != self.device):
             raise ValueError("out must be another AdamW of the same shapes, types and states")
         if not n:
             return
-        dev, table, f32 = self.device, self._columns, torch.float32
-        for g, p in zip(grads, self.params):
-            if g.shape != p.shape or g.device != dev or not g.is_contiguous() or \
-                    (g.dtype != f32 and g.dtype != torch.bfloat16):
-                self._refuse(grads)
-        table["grad"] = [g.data_ptr() for g in grads]
-        table["grad_dtype"] = [_lib.GRPO_F32 if g.dtype == f32 else _lib.GRPO_BF16 for g in grads]
+        dev, table, codes = self.device, self._columns, list(map(_PLAIN_CODES.get, map(_DTYPE, grads)))
+        if list(map(_SHAPE, grads)) != self._shapes or None in codes or not all(map(_CONTIGUOUS, grads)) or \
+                any(map(self._at.__ne__, map(_GET_DEVICE, grads))):
+            self._refuse(grads)
+        table["grad"] = list(map(_DATA_PTR, grads))
+        table["grad_dtype"] = codes
         count = self.step_count + 1 if step is None else step
         config = _lib.AdamwConfig(self.lr if lr is None else lr, self.betas[0], self.betas[1],
                                   self.eps, grad_scale, self.state_bits, count)

@@ -350,6 +350,73 @@ def test_binding_refuses_wrong_tensors():
         G.AdamW([]).step([torch.zeros(3)])
 
 
+@pytest.fixture
+def calls(monkeypatch):
+    """Steps on the host alone: what each would have launched, tensor by tensor."""
+    got = []
+    monkeypatch.setattr(L, "_ptr", lambda t, name: t.data_ptr())
+    monkeypatch.setattr(L, "adamw_step", lambda config, tensors, out, n, device, stream=None: got.append(
+        [{f: getattr(t[i], f) for f, _ in L.AdamwTensor._fields_} for t in (tensors, out) if t is not None for i in range(n)]))
+    return got
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_that_shrank_where_it_is(calls, bits):
+    """The same address with fewer elements: refused while the states are longer,
+    and taken with its own size once they are not."""
+    import grpo_loss_gb300 as G
+    p, q = torch.zeros(1000, 64), torch.zeros(5)
+    opt = G.AdamW([p, q], state_bits=bits)
+    p.data = p.data[:10]
+    with pytest.raises(ValueError, match="elements"):
+        opt.step([torch.zeros(10, 64), torch.zeros(5)])
+    with pytest.raises(ValueError, match="elements"):        # and again: nothing was half bound
+        opt.step([torch.zeros(10, 64), torch.zeros(5)])
+    assert not calls and opt.step_count == 0
+    for ts in (opt.exp_avg, opt.exp_avg_sq):
+        ts[0] = ts[0][:10]
+    for ts in (opt.exp_avg_scale, opt.exp_avg_sq_scale):
+        ts[0] = None if bits == 32 else ts[0][:20]
+    opt.step([torch.zeros(10, 64), torch.zeros(5)])
+    assert [t["n"] for t in calls[0]] == [640, 5]
+
+
+def test_a_parameter_that_changed_where_it_is(calls):
+    import grpo_loss_gb300 as G
+    p = torch.zeros(8, 8)
+    opt, out = G.AdamW([p]), G.AdamW([torch.zeros(8, 8)])
+    opt.step([torch.zeros(8, 8)], out=out)
+    p.data = p.data.t()                                       # a square: shape and size stay
+    with pytest.raises(ValueError, match="contiguous"):
+        opt.step([torch.zeros(8, 8)])
+    p.data = p.data.t().view(4, 16)
+    opt.step([torch.zeros(4, 16)])
+    with pytest.raises(ValueError, match="out must be"):      # which has the old shape
+        opt.step([torch.zeros(4, 16)], out=out)
+    whole = torch.zeros(64)
+    opt, out = G.AdamW([whole]), G.AdamW([torch.zeros(64)])
+    opt.step([whole], out=out)
+    out.params[0].data = out.params[0].data[:32]
+    with pytest.raises(ValueError, match="elements"):
+        opt.step([whole], out=out)
+    opt.params[0] = whole.view(BF16)[:64]                     # the same address and length, another type
+    opt.step([torch.zeros(64)])
+    assert calls[-1][0]["param_dtype"] == L.GRPO_BF16
+
+
+def test_a_state_that_shrank_where_it_is(calls):
+    import grpo_loss_gb300 as G
+    opt = G.AdamW([torch.zeros(64, dtype=BF16)], master=True)
+    for ts in (opt.exp_avg, opt.exp_avg_sq, opt.masters):
+        keep = ts[0]
+        ts[0] = keep[:32]
+        with pytest.raises(ValueError, match="elements"):
+            opt.step([torch.zeros(64)])
+        ts[0] = keep
+    opt.step([torch.zeros(64)])
+    assert len(calls) == 1
+
+
 @pytest.mark.gpu
 def test_binding_refuses_wrong_gpu_tensors():
     import grpo_loss_gb300 as G
