@@ -215,7 +215,8 @@ class AdamW:
     power of two for each 32 values. ``master=True`` keeps float32 masters of the
     bf16 parameters; without one a bf16 parameter is rounded with the step's
     dither, so that updates below half a bf16 step still count. ``weight_decay``
-    is one number or one for each tensor.
+    is one number or one for each tensor. ``lr``, ``betas``, ``eps`` and
+    ``weight_decay`` are read at every step.
 
     ``step(grads)`` applies the gradients (float32 or bf16, of the parameters'
     shapes). With ``out``, an AdamW over other tensors of the same shapes and
@@ -230,10 +231,8 @@ class AdamW:
         self.params = list(params)
         self.lr, self.betas, self.eps, self.state_bits = lr, tuple(betas), eps, state_bits
         n = len(self.params)
-        wd = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
-        if len(wd) != n:
-            raise ValueError("weight_decay must be one number or %d, got %d" % (n, len(wd)))
-        self.weight_decay = wd
+        self.weight_decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        self._check_decays(n)
         self.step_count = 0
         self.device = self.params[0].device if n else None
         self.masters, self.exp_avg, self.exp_avg_sq = [], [], []
@@ -249,6 +248,10 @@ class AdamW:
             for scales in (self.exp_avg_scale, self.exp_avg_sq_scale):
                 scales.append(torch.zeros((p.numel() + 31) // 32, **st) if eight else None)
         self._bind(self._key())
+
+    def _check_decays(self, n: int) -> None:
+        if isinstance(self.weight_decay, (list, tuple)) and len(self.weight_decay) != n:
+            raise ValueError("weight_decay must be one number or %d, got %d" % (n, len(self.weight_decay)))
 
     def _key(self):
         """What the table was made of: the place and bytes of every tensor, and of the
@@ -266,7 +269,7 @@ class AdamW:
         table = (_lib.AdamwTensor * max(n, 1))()
         for i, p in enumerate(self.params):
             t, dev, many = table[i], self.device, p.numel()
-            t.n, t.weight_decay = many, self.weight_decay[i]
+            t.n = many
             t.param_dtype = _lib._plain_code(p.dtype, "params[%d]" % i)
             t.param = _lib._vec_ptr(p, "params[%d]" % i, p.dtype, many, dev)
             t.master = _lib._vec_ptr(self.masters[i], "masters[%d]" % i, torch.float32, many, dev)
@@ -302,6 +305,8 @@ class AdamW:
         if list(map(_SHAPE, grads)) != self._shapes or None in codes or not all(map(_CONTIGUOUS, grads)) or \
                 any(map(self._at.__ne__, map(_GET_DEVICE, grads))):
             self._refuse(grads)
+        self._check_decays(n)
+        table["weight_decay"] = self.weight_decay
         table["grad"] = list(map(_DATA_PTR, grads))
         table["grad_dtype"] = codes
         count = self.step_count + 1 if step is None else step

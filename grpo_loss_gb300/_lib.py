@@ -69,8 +69,9 @@ class AdamwTensor(ctypes.Structure):
 
 
 # The fields of AdamwTensor that a step fills, as columns of an array of them.
-ADAMW_COLUMNS = np.dtype({"names": ["grad", "grad_dtype"], "formats": [np.uint64, np.int32],
-                          "offsets": [AdamwTensor.grad.offset, AdamwTensor.grad_dtype.offset],
+ADAMW_COLUMNS = np.dtype({"names": ["grad", "grad_dtype", "weight_decay"], "formats": [np.uint64, np.int32, np.float32],
+                          "offsets": [AdamwTensor.grad.offset, AdamwTensor.grad_dtype.offset,
+                                      AdamwTensor.weight_decay.offset],
                           "itemsize": ctypes.sizeof(AdamwTensor)})
 
 

@@ -417,6 +417,26 @@ def test_a_state_that_shrank_where_it_is(calls):
     assert len(calls) == 1
 
 
+def test_weight_decay_acts_when_it_is_changed(calls):
+    """As lr, betas and eps do; with another AdamW's buffers, too."""
+    import grpo_loss_gb300 as G
+    ps, gs = [torch.zeros(8), torch.zeros(8)], [torch.zeros(8), torch.zeros(8)]
+    opt = G.AdamW(ps, weight_decay=0.5)
+    opt.step(gs)
+    opt.weight_decay[0] = 0.25
+    opt.step(gs)
+    opt.weight_decay = [0.0, 0.125]
+    opt.step(gs, out=G.AdamW([p.clone() for p in ps]))
+    opt.weight_decay = 0.75
+    opt.step(gs)
+    assert [[t["weight_decay"] for t in c[:2]] for c in calls] == [[0.5, 0.5], [0.25, 0.5], [0.0, 0.125], [0.75, 0.75]]
+    for bad in ([0.1], [0.1] * 3, ["a", 0.1]):
+        opt.weight_decay = bad
+        with pytest.raises(ValueError):
+            opt.step(gs)
+    assert len(calls) == 4
+
+
 @pytest.mark.gpu
 def test_binding_refuses_wrong_gpu_tensors():
     import grpo_loss_gb300 as G
