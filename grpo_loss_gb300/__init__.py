@@ -301,9 +301,14 @@ class AdamW:
             raise ValueError("out must be another AdamW of the same shapes, types and states")
         if not n:
             return
-        dev, table, codes = self.device, self._columns, list(map(_PLAIN_CODES.get, map(_DTYPE, grads)))
-        if list(map(_SHAPE, grads)) != self._shapes or None in codes or not all(map(_CONTIGUOUS, grads)) or \
-                any(map(self._at.__ne__, map(_GET_DEVICE, grads))):
+        dev, table = self.device, self._columns
+        try:
+            codes = list(map(_PLAIN_CODES.get, map(_DTYPE, grads)))
+            good = list(map(_SHAPE, grads)) == self._shapes and None not in codes and \
+                all(map(_CONTIGUOUS, grads)) and not any(map(self._at.__ne__, map(_GET_DEVICE, grads)))
+        except (AttributeError, TypeError):     # not tensors
+            good = False
+        if not good:
             self._refuse(grads)
         self._check_decays(n)
         table["weight_decay"] = self.weight_decay
@@ -321,6 +326,9 @@ class AdamW:
 
     def _refuse(self, grads) -> None:
         for i, (g, p) in enumerate(zip(grads, self.params)):
+            if not torch.is_tensor(g):
+                raise ValueError("grads[%d] must be a tensor, got %r (give a parameter without a gradient zeros, "
+                                 "or leave it out of the optimizer)" % (i, type(g)))
             if g.shape != p.shape:
                 raise ValueError("grads[%d] must have shape %s, got %s" % (i, tuple(p.shape), tuple(g.shape)))
             if g.device != self.device or not g.is_contiguous():

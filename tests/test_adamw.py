@@ -437,6 +437,15 @@ def test_weight_decay_acts_when_it_is_changed(calls):
     assert len(calls) == 4
 
 
+@pytest.mark.parametrize("bad", [None, 1.0, np.zeros(8, np.float32)], ids=["none", "number", "array"])
+def test_refuses_gradients_that_are_not_tensors(calls, bad):
+    import grpo_loss_gb300 as G
+    opt = G.AdamW([torch.zeros(8), torch.zeros(8)])
+    with pytest.raises(ValueError, match=r"grads\[1\] must be a tensor"):
+        opt.step([torch.zeros(8), bad])
+    assert not calls and opt.step_count == 0
+
+
 @pytest.mark.gpu
 def test_binding_refuses_wrong_gpu_tensors():
     import grpo_loss_gb300 as G
