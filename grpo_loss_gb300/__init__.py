@@ -185,19 +185,34 @@ class _LayerNormFn(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
-        if dy.stride(-1) != 1 or (dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]):
-            dy = dy.contiguous()        # a broadcast gradient, as of a sum
-        dx, dw, db = layernorm_bwd(x, weight, dy.to(x.dtype), mean, rstd, rms=ctx.rms, bias=need_b,
-                                   need_dweight=need_w)
-        return (dx if need_x else None, dw.to(weight.dtype) if need_w else None,
-                db.to(ctx.bias_dtype) if need_b else None, None, None)
+        # with a graph to be made of it, the gradient is a node that refuses its own
+        grads = _LayerNormGradFn.apply if torch.is_grad_enabled() else _layer_norm_grads
+        dx, dw, db = grads(dy, x, weight, mean, rstd, ctx.rms, need_w, need_b, ctx.bias_dtype)
+        return dx if need_x else None, dw, db, None, None, None
+
+
+def _layer_norm_grads(dy, x, weight, mean, rstd, rms, need_w, need_b, bias_dtype):
+    if dy.stride(-1) != 1 or (dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]):
+        dy = dy.contiguous()        # a broadcast gradient, as of a sum
+    dx, dw, db = layernorm_bwd(x, weight, dy.to(x.dtype), mean, rstd, rms=rms, bias=need_b, need_dweight=need_w)
+    return dx, dw.to(weight.dtype) if need_w else None, db.to(bias_dtype) if need_b else None
+
+
+class _LayerNormGradFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, *args):
+        return _layer_norm_grads(*args)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("layer_norm is once differentiable: its gradients have no gradients of their own")
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
                eps: float = 1e-5, rms: bool = False) -> torch.Tensor:
     """Autograd entry of the norm over the last dimension of ``x`` (RMS norm
-    with ``rms``, which takes no bias): gradients for x, weight and bias. Capture
-    ``layernorm_fwd`` and ``layernorm_bwd`` into a CUDA graph rather than this."""
+    with ``rms``, which takes no bias): gradients for x, weight and bias, which have
+    none of their own (asking for them is an error). Capture ``layernorm_fwd`` and ``layernorm_bwd`` into a CUDA graph rather than this."""
     return _LayerNormFn.apply(x.reshape(-1, x.shape[-1]), weight, bias, eps, rms).view(x.shape)
 
 

@@ -239,6 +239,38 @@ def test_autograd(rms):
     assert torch.equal(z.grad, ones[0])
 
 
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+def test_second_derivatives_are_refused(monkeypatch, rms):
+    """Gradients that come from kernels have no graph of their own: a penalty on them
+    would silently add nothing. (The kernels are stood in for by their formulas.)"""
+    import grpo_loss_gb300 as G
+
+    def fwd(x, w, b, eps=1e-5, rms=False):
+        mean = None if rms else x.mean(1)
+        c = x if rms else x - mean[:, None]
+        rstd = ((c * c).mean(1) + eps).rsqrt()
+        return c * rstd[:, None] * w, mean, rstd
+
+    def bwd(x, w, dy, mean, rstd, rms=False, bias=True, need_dweight=True):
+        h = (x if rms else x - mean[:, None]) * rstd[:, None]
+        g = dy * w
+        dx = rstd[:, None] * (g - (0 if rms else g.mean(1, keepdim=True)) - h * (g * h).mean(1, keepdim=True))
+        return dx, (dy * h).sum(0), None
+    monkeypatch.setattr(G, "layernorm_fwd", fwd)
+    monkeypatch.setattr(G, "layernorm_bwd", bwd)
+    x = torch.randn(4, 8, dtype=torch.float64, requires_grad=True)
+    w = torch.ones(8, dtype=torch.float64, requires_grad=True)
+    (want,) = torch.autograd.grad(torch.nn.functional.rms_norm(x, (8,), w, 1e-5).pow(2).sum() if rms else
+                                  torch.nn.functional.layer_norm(x, (8,), w, None).pow(2).sum(), x)
+    (got,) = torch.autograd.grad(G.layer_norm(x, w, rms=rms).pow(2).sum(), x)
+    assert torch.allclose(got, want)
+    for loss in (lambda y: y.pow(2).sum(), lambda y: y.sum()):      # dy with a graph, and without
+        gx, gw = torch.autograd.grad(loss(G.layer_norm(x, w, rms=rms)), (x, w), create_graph=True)
+        for g in (gx, gw):
+            with pytest.raises(RuntimeError, match="once differentiable"):
+                torch.autograd.grad(g.pow(2).sum() + x.pow(2).sum(), x, retain_graph=True)
+
+
 @pytest.mark.gpu
 def test_no_rows():
     import grpo_loss_gb300 as G
