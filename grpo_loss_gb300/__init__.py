@@ -154,22 +154,36 @@ class _GRPOLossFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, g_loss, g_kl):
-        H_pol, W, ids, mask, adv = ctx.saved_tensors
-        # the upstream gradient is read on the host: one scalar per backward
-        eng = ctx.engine
-        dH = eng.backward(H_pol, W, ids, mask, adv, float(g_loss),
-                          dH=torch.empty(H_pol.shape, dtype=torch.bfloat16, device=H_pol.device)
-                          if eng.e4m3 else torch.empty_like(H_pol))
-        dH = dH.to(H_pol.dtype)
-        dW = ctx.engine.dW.to(W.dtype) if ctx.engine.dW is not None else None
+        # with a graph to be made of it, the gradient is a node that refuses its own
+        grads = _GRPOLossGradFn.apply if torch.is_grad_enabled() else _grpo_loss_grads
+        dH, dW = grads(g_loss, *ctx.saved_tensors, ctx.engine)
         return dH, None, dW, None, None, None, None
+
+
+def _grpo_loss_grads(g_loss, H_pol, W, ids, mask, adv, eng):
+    # the upstream gradient is read on the host: one scalar per backward
+    dH = eng.backward(H_pol, W, ids, mask, adv, g_loss.item(),
+                      dH=torch.empty(H_pol.shape, dtype=torch.bfloat16, device=H_pol.device)
+                      if eng.e4m3 else torch.empty_like(H_pol))
+    return dH.to(H_pol.dtype), eng.dW.detach().to(W.dtype) if eng.dW is not None else None
+
+
+class _GRPOLossGradFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, *args):
+        return _grpo_loss_grads(*args)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("grpo_loss is once differentiable: its gradients have no gradients of their own")
 
 
 def grpo_loss(H_pol, H_ref, W, ids, mask, adv, engine: GRPOLoss):
     """Autograd entry: returns (loss, kl_mean); backward gives the gradient
     of the loss with respect to H_pol, and with respect to W when the engine
     was built with ``compute_dW`` (the reference model is frozen; kl_mean is a
-    metric and carries no gradient)."""
+    metric and carries no gradient). The gradients have none of their own: asking
+    for them is an error."""
     return _GRPOLossFn.apply(H_pol, H_ref, W, ids, mask, adv, engine)
 
 
@@ -212,7 +226,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
                eps: float = 1e-5, rms: bool = False) -> torch.Tensor:
     """Autograd entry of the norm over the last dimension of ``x`` (RMS norm
     with ``rms``, which takes no bias): gradients for x, weight and bias, which have
-    none of their own (asking for them is an error). Capture ``layernorm_fwd`` and ``layernorm_bwd`` into a CUDA graph rather than this."""
+    none of their own (asking for them is an error). Capture ``layernorm_fwd`` and
+    ``layernorm_bwd`` into a CUDA graph rather than this."""
     return _LayerNormFn.apply(x.reshape(-1, x.shape[-1]), weight, bias, eps, rms).view(x.shape)
 
 
