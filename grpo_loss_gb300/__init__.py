@@ -348,7 +348,8 @@ class AdamW:
         config = _lib.AdamwConfig(self.lr if lr is None else lr, self.betas[0], self.betas[1],
                                   self.eps, grad_scale, self.state_bits, count)
         _lib.adamw_step(config, self._table, None if out is None else out._table, n, dev, stream)
-        torch.autograd.graph.increment_version((self if out is None else out).params)
+        to = self if out is None else out
+        _lib._written(*to.params, *to.masters)
         if out is not None:
             out.step_count = count
         else:

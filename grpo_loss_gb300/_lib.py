@@ -397,6 +397,14 @@ def _call(fn, where: str, device, stream, *args) -> None:
         raise GrpoError(status, where)
 
 
+def _written(*tensors) -> None:
+    """Autograd learns that a call wrote these (None for one that was not given): what
+    it saved of them is gone."""
+    given = [t for t in tensors if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None,
            min_p=None, tokens=None, logp=None, stream=None):
     """One token a row of ``logits`` (float32 or bf16 [rows, V], rows may be
@@ -416,12 +424,14 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     code = _plain_code(logits.dtype, "logits")
     dev = _device_of(logits, "logits")
     ptr, ld = _rows_ptr(logits, "logits", logits.dtype, rows, V, dev)
+    given = tokens, logp
     tokens, tp = _vec_out(tokens, "tokens", i32, rows, dev)
     logp, lp = _vec_out(logp, "logp", f32, rows, dev)
     _call(lib().grpo_sample, "grpo_sample", dev, None, SampleProblem(rows, V, ld, code), ptr,
           _vec_ptr(u, "u", f32, rows, dev), _vec_ptr(temperature, "temperature", f32, rows, dev),
           _vec_ptr(top_k, "top_k", i32, rows, dev), _vec_ptr(top_p, "top_p", f32, rows, dev),
           _vec_ptr(min_p, "min_p", f32, rows, dev), tp, lp)
+    _written(*given)
     return tokens, logp
 
 
@@ -449,12 +459,14 @@ def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float =
     code, pcode = _plain_code(dt, "x"), _plain_code(pt, "weight")
     dev = _device_of(x, "x")
     xp, ld_x = _rows_ptr(x, "x", dt, rows, d, dev)
+    given = y, None if rms else mean, rstd
     y, yp, ld_y = _rows_out(y, "y", dt, rows, d, dev)
     mean, mp = (None, None) if rms else _vec_out(mean, "mean", f32, rows, dev)
     rstd, rp = _vec_out(rstd, "rstd", f32, rows, dev)
     problem = LayernormProblem(rows, d, ld_x, ld_y, 0, 0, eps, 1 if rms else 0, code, pcode)
     _call(lib().grpo_layernorm_fwd, "grpo_layernorm_fwd", dev, None, problem, xp,
           _vec_ptr(weight, "weight", pt, d, dev), _vec_ptr(bias, "bias", pt, d, dev), yp, mp, rp)
+    _written(*given)
     return y, mean, rstd
 
 
@@ -479,6 +491,7 @@ def layernorm_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, mean,
         raise ValueError("mean is needed unless rms")
     xp, ld_x = _rows_ptr(x, "x", dt, rows, d, dev)
     gp, ld_dy = _rows_ptr(dy, "dy", dt, rows, d, dev)
+    given = dx, dweight, dbias
     dx, dxp, ld_dx = _rows_out(dx, "dx", dt, rows, d, dev)
     wp = bp = None
     if dweight is not None or need_dweight:
@@ -502,6 +515,7 @@ def layernorm_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, mean,
           _vec_ptr(rstd, "rstd", f32, rows, dev), dxp, wp, bp,
           None if workspace is None else _vec_ptr(workspace, "workspace", workspace.dtype,
                                                   workspace.numel(), dev), size)
+    _written(*given)
     return dx, dweight, dbias
 
 
