@@ -1,6 +1,7 @@
 // C entry points of the operators around the loss head: token sampling, layer
 // norm and AdamW. Argument checks and launches only; the mathematics and the
 // layouts stand at the kernels (sample.cu, norm.cu, adamw.cu).
+#include <float.h>
 #include <math.h>
 
 #include "../../include/grpo.h"
@@ -213,7 +214,8 @@ grpo_status grpo_adamw_step(const grpo_adamw_config* c, const grpo_adamw_tensor*
   k.one_m_beta2 = static_cast<float>(1.0 - b2);
   k.lr_t = static_cast<float>(c->lr / (1.0 - pow(b1, t)));
   k.rsqrt_c2 = static_cast<float>(1.0 / sqrt(1.0 - pow(b2, t)));
-  k.eps = static_cast<float>(c->eps);
+  // (the kernel's reciprocal takes a denominator below 2^-126 for 0, and 0 / eps is 0)
+  k.eps = c->eps > 0.0 ? fmaxf(static_cast<float>(c->eps), FLT_MIN) : 0.f;
   k.grad_scale = c->grad_scale;
   k.dither = static_cast<uint32_t>(static_cast<uint64_t>(c->step) * 0xC13FA9A9ull);
 

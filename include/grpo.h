@@ -409,8 +409,9 @@ grpo_status grpo_layernorm_bwd(const grpo_layernorm_problem *problem, const void
  * One AdamW step over many tensors at once, step number t = config->step >= 1:
  *   g = grad_scale * grad,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
  *   x = x (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in float32. x is the float32 master where the tensor has one (the parameter
- * is then only written: x in its own type, to nearest), else the parameter.
+ * in float32; an eps above 0 counts as 2^-126 at least. x is the float32 master
+ * where the tensor has one (the parameter is then only written: x in its own type,
+ * to nearest), else the parameter.
  *
  * state_bits = 32: m and v are float32 [n]. state_bits = 8: m and v are e4m3
  * codes [n] with one power of two for each 32 consecutive values (the last

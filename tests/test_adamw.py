@@ -282,6 +282,30 @@ def test_the_same_bits_on_and_off_a_boundary(dtype, bits):
             assert torch.equal(a.exp_avg_scale[0], b.exp_avg_scale[0])
             assert torch.equal(a.exp_avg_sq_scale[0], b.exp_avg_sq_scale[0])
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-40, 1e-50, 1.17e-38])
+def test_a_tiny_eps_is_not_none(eps, bits):
+    """Below float32's normal range, too, an element with no moments stays: 0 / eps."""
+    import grpo_loss_gb300 as G
+    for n in (7, 4096):                                      # one by one, and in pieces
+        g = torch.Generator(device="cuda").manual_seed(n)
+        p = torch.randn(n, generator=g, device="cuda")
+        grad = torch.randn(n, generator=g, device="cuda")
+        grad[::2] = 0.0
+        grad[n // 2: n // 2 + 64] = 0.0                      # whole blocks, too
+        still = grad == 0
+        before = p.clone()
+        G.AdamW([p], lr=1e-3, eps=eps, weight_decay=0.0, state_bits=bits).step([grad])
+        torch.cuda.synchronize()
+        assert torch.isfinite(p).all()
+        assert torch.equal(p[still], before[still])
+        moved = grad != 0                                    # the first step moves by lr: m / sqrt(v) is a sign
+        off = (p.double() - (before.double() - 1e-3 * grad.sign().double()))[moved].abs()
+        # the update to 2^-20 (roundings of m, v and the constants 2^-24 each, root and quotient 2^-22), p to 2^-24
+        assert bool((off <= 1e-3 * 2.0 ** -20 + 2.0 ** -24 * (before[moved].abs().double() + 1e-3)).all())
+
+
 
 # ---------------------------------------------------------------- refusals
 
