@@ -126,7 +126,7 @@ __device__ __forceinline__ void load(const void* p, int k, float (&v)[W]) {
     const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + k);
 #pragma unroll
     for (int f = 0; f < W / 4; ++f) {
-      const float4 a = W == 4 ? __ldcs(q) : __ldg(q + f);
+      const float4 a = W == 4 ? __ldcs(q) : q[f];  // (of eight, the second half is in the same line)
       v[4 * f] = a.x, v[4 * f + 1] = a.y, v[4 * f + 2] = a.z, v[4 * f + 3] = a.w;
     }
   }
