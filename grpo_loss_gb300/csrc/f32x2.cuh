@@ -1,4 +1,7 @@
 // Pairs of floats in one register pair: one instruction, rounded to nearest, for both.
+// The assembler may fuse a product of pairs and a sum that takes it into one instruction
+// with one rounding, in one inlined copy of a function and not in another. Where bits
+// matter, the sum is written as fma2, or taken of single floats.
 #pragma once
 #include <stdint.h>
 

@@ -177,7 +177,10 @@ struct Weigher {
 };
 
 // W = round(2^(y + B)) of two logits, 0 below y = -40 and for NaN. The steps are
-// those of exp2_pair, for both at once; the argument error is 2^-46 |y|.
+// those of exp2_pair, for both at once; the argument error is 2^-46 |y|. Every copy of
+// this gives the same bits, so that the parts of a row add up to its sum wherever they
+// are weighed: no sum here takes a product, which might be rounded together with it
+// (see f32x2.cuh).
 __device__ __forceinline__ void weight2(const Weigher& w, uint64_t z, uint64_t& w0, uint64_t& w1) {
   const uint64_t neg = pair_of(-1.f), c = pair_of(w.c_hi), top = pair_of(-w.zmax);
   // z - zmax without loss: the difference and what its rounding left
@@ -198,9 +201,8 @@ __device__ __forceinline__ void weight2(const Weigher& w, uint64_t z, uint64_t& 
   const uint64_t xxl = fma2(x, add2(xl, xl), fma2(x, x, mul2(xx, neg)));
   const uint64_t q3 = fma2(x, fma2(x, fma2(x, pair_of(1.f / 720.f), pair_of(1.f / 120.f)), pair_of(1.f / 24.f)),
                            pair_of(1.f / 6.f));
-  const uint64_t cubic = mul2(mul2(xx, x), q3);
   const uint64_t s = fma2(xx, half, x);
-  const uint64_t sl = add2(fma2(xx, half, fma2(s, neg, x)), fma2(xxl, half, add2(xl, cubic)));
+  const uint64_t sl = add2(fma2(xx, half, fma2(s, neg, x)), fma2(xxl, half, fma2(mul2(xx, x), q3, xl)));
   const float2 ktf = of_pair(kt);
   const uint32_t k0 = __float_as_uint(ktf.x), k1 = __float_as_uint(ktf.y);  // 0x4B400000 + k
   const float2 t0 = w.tab[k0 & 31], t1 = w.tab[k1 & 31];
@@ -208,7 +210,7 @@ __device__ __forceinline__ void weight2(const Weigher& w, uint64_t z, uint64_t& 
   const uint64_t ty = pair_of(__float_as_uint(t0.y), __float_as_uint(t1.y));
   const uint64_t q = mul2(tx, s);
   const uint64_t ql = add2(fma2(tx, s, mul2(q, neg)), fma2(tx, sl, mul2(ty, s)));
-  const uint64_t h = add2(tx, q);
+  const uint64_t h = fma2(tx, s, tx);
   const uint64_t hl = add2(fma2(fma2(tx, neg, h), neg, q), add2(ql, ty));
   // 2^44 (h + hl), h in [0.98, 2) with 24 bits behind the point at most; then
   // down by 44 - B - n
@@ -759,7 +761,8 @@ __device__ __forceinline__ void set_row(Shared& sh, float t, int k, float p, boo
 template <typename T>
 __device__ __forceinline__ void write_row(const SampleArgs& a, int64_t row, const T* logits, const Shared& sh,
                                           const Weigher& w, uint64_t mass, int par = 0) {
-  const int64_t at = sh.ans[par].t;
+  // (an index that no draw has set stays in the row)
+  const int64_t at = min(static_cast<int64_t>(sh.ans[par].t), a.V - 1);
   const float z = clean(to_f(logits[at]));
   const float d = z == w.zmax ? 0.f : (z - w.zmax) / sh.temp;
   // ln(mass): the sum as two floats
@@ -1331,6 +1334,7 @@ __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int6
               const Vec<T> x = r.load(v);
               uint64_t sm = s_in - s1;
               uint32_t se = e_in - e1;
+              int at = 0;  // the piece's last token that stays, up to the one that passes u
 #pragma unroll 1
               for (int i = 0; i < VE; ++i) {
                 const float z = x.get(i);
@@ -1339,14 +1343,15 @@ __device__ __forceinline__ bool decide(Row<T, ONE>& r, const SampleArgs& a, int6
                 if (key > keep.t) sm += weigh<EXACT>(w, z);
                 se += key == keep.t;
                 const uint64_t now = sm + min(se, lim) * wt;
+                if (now > was) at = i;
                 if (now > target) {
                   // a border within E of u is left to the exact weights (as is a
                   // token that the float sums of pieces and of elements disagree on)
-                  lead->t = static_cast<uint32_t>(r.pos0 + static_cast<int64_t>(v) * VE + i);
                   if (!EXACT && (!E || (now - target > 2 * E && distance(target, was) > 2 * E))) lead->bad = 0;
                   break;
                 }
               }
+              lead->t = static_cast<uint32_t>(r.pos0 + static_cast<int64_t>(v) * VE + at);
             }
             break;
           }
