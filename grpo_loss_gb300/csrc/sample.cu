@@ -1411,7 +1411,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1)
   r.C = ONE ? 1 : static_cast<int>(r.cl.num_blocks());
   r.rank = ONE ? 0 : static_cast<int>(r.cl.block_rank());
   r.V = a.V;
-  r.hist_bits = slice_vecs * VE <= 131072 ? 15.f : 13.f;
+  r.hist_bits = slice_vecs * VE < 131072 ? 15.f : 13.f;  // (kMaxFast of 2^13 pass 2^32 no more than that)
   r.parts = reinterpret_cast<Part*>(s_slice + (resident ? slice_vecs : 0));
   if (threadIdx.x < 32) sh.tab[threadIdx.x] = c_exp2_32[threadIdx.x];
   const int n_cl = gridDim.x / r.C;

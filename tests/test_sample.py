@@ -81,6 +81,25 @@ def test_flat_and_peaked_rows(spread):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("V,row_of", [(1048572, 1), (524284, 4), (262140, 2)])
+def test_flat_rows_that_fill_a_slice(V, row_of):
+    """Slices of 131072 equal logits: the most that a bin's 32-bit sum may meet in
+    its finer units. (Clusters of 8, 4 and 2 CTAs a row, as few rows as take those.)"""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = 1 if row_of == 1 else sms // row_of
+    z = torch.full((rows, V), 1.5, device="cuda")
+    u = torch.rand(rows, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    import grpo_loss_gb300 as G
+    p = torch.full((rows,), 0.9, device="cuda")
+    tokens, logp = G.sample(z, u, top_p=p)
+    torch.cuda.synchronize()
+    # of n = ceil(0.9 V) equal weights the first whose running sum exceeds u n
+    n = math.ceil(float(np.float32(0.9)) * V)
+    assert tokens.tolist() == [math.floor(float(x) * n) for x in u.tolist()]
+    assert np.all(np.abs(f64(logp) + math.log(V)) <= LOGP_ABS)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("par", [dict(p=0.9), dict(p=0.5, q=1e-4), dict(k=5000), dict(k=900, p=0.97), dict(k=20000, p=0.6, T=1.5),
                                  dict(p=0.99999), dict(p=1e-3), dict(k=1024), dict(k=1025)], ids=str)
 @pytest.mark.parametrize("V", [30011, 128256])
