@@ -284,13 +284,16 @@ class AdamW:
             raise ValueError("weight_decay must be one number or %d, got %d" % (n, len(self.weight_decay)))
 
     def _key(self):
-        """What the table was made of: the place and bytes of every tensor, and of the
-        parameters, which are the caller's, type, shape and layout as well. (Methods of
-        the class, mapped: a step's host time is these walks.)"""
-        given = [*self.masters, *self.exp_avg_scale, *self.exp_avg_sq_scale]
-        ts = [*self.params, *self.exp_avg, *self.exp_avg_sq, *[t for t in given if t is not None]]
-        return (list(map(_DATA_PTR, ts)), list(map(_NBYTES, ts)), list(map(_DTYPE, self.params)),
-                list(map(_SHAPE, self.params)), all(map(_CONTIGUOUS, self.params)), [t is None for t in given])
+        """What the table was made of: the place of every tensor, the bytes of the states
+        and masters, and of the parameters, which are the caller's, type, shape and
+        layout. (Methods of the class, mapped: a step's host time is these walks.)"""
+        params = self.params
+        given = [[t for t in ts if t is not None] for ts in (self.masters, self.exp_avg_scale, self.exp_avg_sq_scale)]
+        states = [*self.exp_avg, *self.exp_avg_sq, *given[0], *given[1], *given[2]]
+        some = 0 < len(given[0]) < len(params)
+        return (list(map(_DATA_PTR, [*params, *states])), list(map(_NBYTES, states)), list(map(_DTYPE, params)),
+                list(map(_SHAPE, params)), all(map(_CONTIGUOUS, params)), self.state_bits,
+                [t is None for t in self.masters] if some else None)
 
     def _bind(self, key) -> None:
         """Make the table of the tensors that a step is given (again, when a tensor of
@@ -310,10 +313,7 @@ class AdamW:
             t.v_scale = _lib._vec_ptr(self.exp_avg_sq_scale[i], "exp_avg_sq_scale[%d]" % i, state, scales, dev)
         self._table = table
         self._columns = np.frombuffer(table, dtype=_lib.ADAMW_COLUMNS)[:n]   # the same memory
-        self._shapes = [p.shape for p in self.params]
         self._at = self.params[0].get_device() if n else -1
-        self._kinds = [(self.state_bits, p.shape, p.dtype, m is None)
-                       for p, m in zip(self.params, self.masters)]
         self._bound = key
 
     def step(self, grads: Sequence[torch.Tensor], grad_scale: float = 1.0, lr: Optional[float] = None,
@@ -323,18 +323,22 @@ class AdamW:
         n = len(self.params)
         if len(grads) != n:
             raise ValueError("expected %d gradients, got %d" % (n, len(grads)))
-        for o in (self,) if out is None else (self, out):
-            key = o._key()
-            if key != o._bound:
-                o._bind(key)
-        if out is not None and (out is self or out._kinds != self._kinds or out.device != self.device):
-            raise ValueError("out must be another AdamW of the same shapes, types and states")
+        key = self._key()
+        if key != self._bound:
+            self._bind(key)
+        to = self
+        if out is not None:
+            to, to_key = out, out._key()
+            if to_key != out._bound:
+                out._bind(to_key)
+            if out is self or to_key[1:] != key[1:] or out._at != self._at:
+                raise ValueError("out must be another AdamW of the same shapes, types and states")
         if not n:
             return
         dev, table = self.device, self._columns
         try:
             codes = list(map(_PLAIN_CODES.get, map(_DTYPE, grads)))
-            good = list(map(_SHAPE, grads)) == self._shapes and None not in codes and \
+            good = list(map(_SHAPE, grads)) == key[3] and None not in codes and \
                 all(map(_CONTIGUOUS, grads)) and not any(map(self._at.__ne__, map(_GET_DEVICE, grads)))
         except (AttributeError, TypeError):     # not tensors
             good = False
@@ -348,12 +352,8 @@ class AdamW:
         config = _lib.AdamwConfig(self.lr if lr is None else lr, self.betas[0], self.betas[1],
                                   self.eps, grad_scale, self.state_bits, count)
         _lib.adamw_step(config, self._table, None if out is None else out._table, n, dev, stream)
-        to = self if out is None else out
-        _lib._written(*to.params, *to.masters)
-        if out is not None:
-            out.step_count = count
-        else:
-            self.step_count = count
+        _lib._written(to.params, to.masters)
+        to.step_count = count
 
     def _refuse(self, grads) -> None:
         for i, (g, p) in enumerate(zip(grads, self.params)):

@@ -397,10 +397,10 @@ def _call(fn, where: str, device, stream, *args) -> None:
         raise GrpoError(status, where)
 
 
-def _written(*tensors) -> None:
-    """Autograd learns that a call wrote these (None for one that was not given): what
-    it saved of them is gone."""
-    given = [t for t in tensors if t is not None]
+def _written(*lists) -> None:
+    """Autograd learns that a call wrote the tensors of these (None for one that was not
+    given): what it saved of them is gone."""
+    given = [t for ts in lists for t in ts if t is not None]
     if given:
         torch.autograd.graph.increment_version(given)
 
@@ -431,7 +431,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
           _vec_ptr(u, "u", f32, rows, dev), _vec_ptr(temperature, "temperature", f32, rows, dev),
           _vec_ptr(top_k, "top_k", i32, rows, dev), _vec_ptr(top_p, "top_p", f32, rows, dev),
           _vec_ptr(min_p, "min_p", f32, rows, dev), tp, lp)
-    _written(*given)
+    _written(given)
     return tokens, logp
 
 
@@ -466,7 +466,7 @@ def layernorm_fwd(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float =
     problem = LayernormProblem(rows, d, ld_x, ld_y, 0, 0, eps, 1 if rms else 0, code, pcode)
     _call(lib().grpo_layernorm_fwd, "grpo_layernorm_fwd", dev, None, problem, xp,
           _vec_ptr(weight, "weight", pt, d, dev), _vec_ptr(bias, "bias", pt, d, dev), yp, mp, rp)
-    _written(*given)
+    _written(given)
     return y, mean, rstd
 
 
@@ -515,7 +515,7 @@ def layernorm_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, mean,
           _vec_ptr(rstd, "rstd", f32, rows, dev), dxp, wp, bp,
           None if workspace is None else _vec_ptr(workspace, "workspace", workspace.dtype,
                                                   workspace.numel(), dev), size)
-    _written(*given)
+    _written(given)
     return dx, dweight, dbias
 
 
