@@ -721,14 +721,15 @@ __device__ __forceinline__ uint32_t kth_from_below(const uint32_t (&key)[N], uin
 // 0.7 |y|), and three roundings in the sum of a piece. The entropy of w / S is at
 // most log2 V, so sum w |y| <= S log2(V / S); for bf16 the term with |y| is left
 // only for logits around 0, whose weights are 2^(-zmax log2(e) / T).
-// The rough weights' sums are off by 2^-24 sum w (3 + 0.7 |y|) for every type, where d
-// is exact, and the same three roundings.
+// The rough weights' sums are off by 2^-24 sum w (3 + 0.7 |y| (1 + e)) beside what the
+// difference's rounding leaves, for every type, and the same three roundings: y is
+// rounded once, and its factor c_hi is e 2^-24 off, what c_lo holds.
 template <typename T>
 __device__ __forceinline__ uint64_t error_bound(const Weigher& w, uint64_t mass, int64_t V, bool rough = false) {
   const float s = static_cast<float>(mass) / w.one, v = static_cast<float>(V);
-  const float y0 = fmaxf(0.f, w.zmax * w.c_hi), per_y = 0.8f * s * fmaxf(0.f, log2f(v / s));
-  float terms = s * 5.5f + (sizeof(T) == 4 ? per_y : v * ex2_approx(-y0) * fminf(y0, 200.f));
-  if (rough) terms += 1.5f * s + per_y;
+  const float y0 = fmaxf(0.f, w.zmax * w.c_hi), sum_y = s * fmaxf(0.f, log2f(v / s));
+  float terms = s * 5.5f + (sizeof(T) == 4 ? 0.8f * sum_y : v * ex2_approx(-y0) * fminf(y0, 200.f));
+  if (rough) terms += 0.7f * s + 0.7f * sum_y * (1.f + fabsf(w.c_lo) / w.c_hi * 16777216.f);
   return static_cast<uint64_t>(__float2ll_ru((terms * 6.0e-8f + v * 1e-12f) * w.one)) + 2 * V + 1024;
 }
 

@@ -166,6 +166,20 @@ def test_many_rows_with_parameters_of_their_own(dtype, spread):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("par", [{}, dict(p=0.9), dict(p=0.9, k=200), dict(q=0.004)], ids=str)
+def test_many_rows_whose_weights_err_alike(par):
+    """One likely token and a floor of equal ones, whose float32 weights are all off in
+    the same direction, as far as a product and its factor can be."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows, V = sms + 8, 131072
+    for dtype in (torch.bfloat16, torch.float32):
+        z = torch.full((rows, V), -7.96875, device="cuda", dtype=dtype)
+        z[:, 777] = 0.0
+        u = (torch.arange(rows, device="cuda") + 0.5) / rows
+        check(z, u, T=1.4333123, **par)
+
+
+@pytest.mark.gpu
 def test_borders_of_u():
     z = torch.zeros(8, 4096, device="cuda")
     u = torch.tensor([0.0, 2.0 ** -12, 0.5, 0.5 - 2.0 ** -25, 1 - 2.0 ** -24, 1.0, 2.0, float("nan")], device="cuda")
