@@ -57,7 +57,8 @@ constexpr int kMaxSliceBytes = 192 * 1024;     // and with 512
 constexpr int kMaxFast = 500000;              // elements of a slice that the bins' sums can take
 constexpr float kCut = -40.f;                  // binary orders below the top that weigh nothing
 
-// 2^(j/32), j = 0..31, each as the sum of two floats.
+// 2^(j/32), j = 0..31, each as the sum of two floats (2^x from a table and a short series
+// on the remainder: Tang's method).
 __constant__ float2 c_exp2_32[32] = {
     {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f},
     {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f}, {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f},
@@ -259,7 +260,7 @@ __device__ __forceinline__ uint64_t distance(uint64_t a, uint64_t b) { return a 
 __device__ __forceinline__ float fast_y(const Weigher& w, float z) { return (z - w.zmax) * w.c_hi; }
 
 // The fast weight, 2^(n + f): n = round(d log2(e) / T) by adding 1.5 * 2^23, f what
-// the product leaves, 2^f = 1 + f q(f) with q of degree 5, fitted to 2^-28.9. In
+// the product leaves, 2^f = 1 + f q(f) with q of degree 5, within 2^-25.9. In
 // units of 2^-24 its error is 1.3 for 2^f, 0.4 for f and 0.7 |y| for d = z - zmax
 // (exact for bf16 logits, but for |z| below 2^-16 |zmax|). It has no cut at 2^-40;
 // what it has below is V 2^-40 at most. (The special-function unit's 2^y is four
@@ -396,7 +397,7 @@ struct Row {
   int64_t V;
   int lane, warp, nt, nw, C, rank, turn = 0, par = 0;  // nt threads, nw warps
   int v0, v1;          // this warp's pieces
-  float hist_bits;     // of a bin's mass: no sum of them passes 2^32
+  float hist_bits = 13.f;  // of a bin's mass: no sum of them passes 2^32
   int full0, full1;    // pieces that lie inside the row
 
   __device__ __forceinline__ Row(Shared& s) : sh(s) {}
@@ -1412,7 +1413,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1)
   r.C = ONE ? 1 : static_cast<int>(r.cl.num_blocks());
   r.rank = ONE ? 0 : static_cast<int>(r.cl.block_rank());
   r.V = a.V;
-  r.hist_bits = slice_vecs * VE < 131072 ? 15.f : 13.f;  // (kMaxFast of 2^13 pass 2^32 no more than that)
+  if (slice_vecs * VE < 131072) r.hist_bits = 15.f;  // (of 2^13, kMaxFast stay below 2^32)
   r.parts = reinterpret_cast<Part*>(s_slice + (resident ? slice_vecs : 0));
   if (threadIdx.x < 32) sh.tab[threadIdx.x] = c_exp2_32[threadIdx.x];
   const int n_cl = gridDim.x / r.C;
@@ -1520,7 +1521,6 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_sample_rows
   r.V = a.V;
   r.parts = s_parts;
   r.slice = nullptr;
-  r.hist_bits = 13.f;
   const int64_t row = blockIdx.x;
   const T* z = static_cast<const T*>(a.logits) + row * a.ld;
   const int off = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
@@ -1960,7 +1960,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   r.nw = THREADS / 32;
   r.C = static_cast<int>(r.cl.num_blocks());
   r.rank = static_cast<int>(r.cl.block_rank());
-  r.hist_bits = 13.f;
   uint32_t* counts = reinterpret_cast<uint32_t*>(s_slice + (resident ? slice_vecs : 0));
   uint64_t* table = reinterpret_cast<uint64_t*>(counts + kCounts);
   uint32_t* joined = r.C == 1 ? counts : reinterpret_cast<uint32_t*>(table + kCounts);

@@ -179,6 +179,81 @@ def test_many_rows_whose_weights_err_alike(par):
         check(z, u, T=1.4333123, **par)
 
 
+def wanted(z, u, T=1.0, k=0, p=1.0, q=0.0):
+    """The definition for all rows at once, in float64 on the GPU (parameters of the
+    whole call; no masked rows)."""
+    z = z.double()
+    w = ((z - z.max(1, keepdim=True).values) / float(np.float32(T))).exp()
+    w[w < 2.0 ** -40] = 0.0
+    ws, order = torch.sort(z, dim=1, descending=True, stable=True)
+    ws = w.gather(1, order)
+    ws[ws < float(np.float32(q))] = 0.0
+    if k:
+        ws[:, k:] = 0.0
+    upto = ws.cumsum(1)
+    ws[:, 1:][(upto - ws)[:, 1:] >= float(np.float32(p)) * upto[:, -1:]] = 0.0
+    upto = torch.zeros_like(w).scatter_(1, order, ws).cumsum(1)
+    tokens = (upto <= u.double()[:, None] * upto[:, -1:]).sum(1)
+    return tokens.int(), w.gather(1, tokens[:, None])[:, 0].log() - w.sum(1).log()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("par", [{}, dict(p=0.9), dict(p=0.95, q=1e-3), dict(k=50, p=0.9), dict(k=3000, p=0.9, T=0.7)], ids=str)
+@pytest.mark.parametrize("V", [40001, 128256])
+@pytest.mark.parametrize("rows", [(1, 20), (1, 6), (2, 5), (4, 5), (21, 20)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_every_number_of_ctas_a_row(dtype, rows, V, par):
+    """From rows that take a cluster each to rows for every SM, in shares of the SMs:
+    clusters of 8, 4 and 2 CTAs, large ones and small, slices kept and read again."""
+    import grpo_loss_gb300 as G
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = sms * rows[0] // rows[1]
+    z, u = logits_of(n, V, dtype, n + V, 1.0)
+    names = dict(T="temperature", k="top_k", p="top_p", q="min_p")
+    tokens, logp = G.sample(z, u, **{names[a]: torch.full((n,), v, device="cuda", dtype=torch.int32 if a == "k" else torch.float32)
+                                     for a, v in par.items()})
+    want, lp = wanted(z, u, **par)
+    assert torch.equal(tokens, want)
+    assert bool(((logp.double() - lp).abs() <= LOGP_ABS + 2.0 ** -24 * lp.abs()).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [500009, 1000009])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_rows_too_long_for_one_cta_each(dtype, V):
+    """Float32 slices of up to, and of more than, the 500000 that are weighed fast."""
+    import grpo_loss_gb300 as G
+    n = torch.cuda.get_device_properties(0).multi_processor_count + 3
+    z, u = logits_of(n, V, dtype, V, 1.0)
+    for par in ({}, dict(p=0.9)):
+        kw = {"top_p": torch.full((n,), v, device="cuda") for v in par.values()}
+        tokens, logp = G.sample(z, u, **kw)
+        want, lp = wanted(z, u, **par)
+        assert torch.equal(tokens, want)
+        assert bool(((logp.double() - lp).abs() <= LOGP_ABS + 2.0 ** -24 * lp.abs()).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("spread", [1.0, 4.0])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_logp_of_few_rows_loses_no_more_than_float32(dtype, spread):
+    """In units of 2^-24, with S = sum w, d = (z - zmax) / T: the sum S itself (bf16
+    rows: integers of exact weights; float32 rows 5.5 + 0.8 log2(V / S)); its logarithm
+    2 ln S and their sum 1; d's difference and quotient 2 |d|; the result |logp|."""
+    import grpo_loss_gb300 as G
+    rows, V = 5, 128256
+    z, u = logits_of(rows, V, dtype, 77, spread)
+    temp = torch.full((rows,), 0.7, device="cuda")
+    tokens, logp = G.sample(z, u, temperature=temp)
+    y = z.double() / float(np.float32(0.7))
+    top = y.max(1).values
+    ln_s = (y - top[:, None]).exp().sum(1).log()
+    d = y.gather(1, tokens.long()[:, None])[:, 0] - top
+    mass = 0.01 if dtype == torch.bfloat16 else 5.5 + 0.8 * (math.log2(V) - ln_s / math.log(2))
+    units = mass + 3 * ln_s + 2 * d.abs() + (d - ln_s).abs()
+    assert bool(((logp.double() - (d - ln_s)).abs() <= 1.001 * units * 2.0 ** -24).all())
+
+
 @pytest.mark.gpu
 def test_borders_of_u():
     z = torch.zeros(8, 4096, device="cuda")
