@@ -233,6 +233,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
 
 _DATA_PTR, _CONTIGUOUS, _GET_DEVICE = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
 _NBYTES, _DTYPE, _SHAPE = operator.attrgetter("nbytes"), operator.attrgetter("dtype"), operator.attrgetter("shape")
+_LISTS = ("params", "masters", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale")
 _PLAIN_CODES = {torch.float32: _lib.GRPO_F32, torch.bfloat16: _lib.GRPO_BF16}
 
 
@@ -311,6 +312,11 @@ class AdamW:
             scales = (many + 31) // 32
             t.m_scale = _lib._vec_ptr(self.exp_avg_scale[i], "exp_avg_scale[%d]" % i, state, scales, dev)
             t.v_scale = _lib._vec_ptr(self.exp_avg_sq_scale[i], "exp_avg_sq_scale[%d]" % i, state, scales, dev)
+        spans = sorted((t.data_ptr(), t.nbytes, "%s[%d]" % (name, i)) for name in _LISTS
+                       for i, t in enumerate(getattr(self, name)) if t is not None and t.nbytes)
+        for (at, size, one), (after, _, other) in zip(spans, spans[1:]):
+            if at + size > after:
+                raise ValueError("%s overlaps %s: every buffer is one tensor's own" % (one, other))
         self._table = table
         self._columns = np.frombuffer(table, dtype=_lib.ADAMW_COLUMNS)[:n]   # the same memory
         self._at = self.params[0].get_device() if n else -1

@@ -470,6 +470,22 @@ def test_refuses_gradients_that_are_not_tensors(calls, bad):
     assert not calls and opt.step_count == 0
 
 
+def test_refuses_buffers_that_overlap(calls):
+    """A tensor given twice (tied weights) would be updated by two parts of one launch
+    at a time; neighbours in one buffer are no overlap, and empty ones never are."""
+    import grpo_loss_gb300 as G
+    flat = torch.zeros(100)
+    for params in ([flat, torch.zeros(3), flat], [flat[:60], flat[50:]], [flat, flat[10:20]], [flat.view(10, 10), flat]):
+        with pytest.raises(ValueError, match=r"overlaps"):
+            G.AdamW(params)
+    opt = G.AdamW([flat[:50], flat[50:], torch.zeros(0), flat[:0], torch.zeros(0)])
+    opt.step([torch.zeros(50), torch.zeros(50)] + [torch.zeros(0)] * 3)
+    opt.exp_avg[1] = opt.exp_avg[0]
+    with pytest.raises(ValueError, match="overlaps"):
+        opt.step([torch.zeros(50), torch.zeros(50)] + [torch.zeros(0)] * 3)
+    assert len(calls) == 1
+
+
 @pytest.mark.gpu
 def test_binding_refuses_wrong_gpu_tensors():
     import grpo_loss_gb300 as G
