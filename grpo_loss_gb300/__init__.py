@@ -252,7 +252,8 @@ class AdamW:
     ``step(grads)`` applies the gradients (float32 or bf16, of the parameters'
     shapes). With ``out``, an AdamW over other tensors of the same shapes and
     types, the new parameters and states are written there and this object's stay
-    as they are.
+    as they are. A step that is captured into a CUDA graph holds its number, rates and
+    dither: each replay is that same step, and 8-bit states replayed many times stall.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas=(0.9, 0.999),

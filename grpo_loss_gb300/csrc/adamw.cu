@@ -35,7 +35,7 @@ struct AdamTable {
 // 0xC13FA9A9 + salt (see grpo_adamw_step in grpo.h).
 constexpr uint32_t kDitherIndex = 0x91E10DA5u, kSaltV = 0x55555555u, kSaltP = 0xAAAAAAAAu;
 
-// Largest power-of-two byte E with amax * 2^(127 - E) <= 448 = 1.75 * 2^8:
+// Smallest power-of-two byte E with amax * 2^(127 - E) <= 448 = 1.75 * 2^8:
 // adding 0x1FFFFF to the bits carries into the exponent when the significand
 // is above 1.75. 255 marks infinities and NaN.
 __device__ __forceinline__ uint32_t block_scale(uint32_t b) {

@@ -331,6 +331,9 @@ grpo_status grpo_loss_bwd_e4m3(const grpo_problem *problem, const uint8_t *H_pol
  *   token = the smallest index i with sum_{j <= i, kept} w_j > u * sum_kept w_j;
  *   logp  = (z_token - zmax) / T - ln sum_all w: the log-probability under the
  *           full softmax at temperature T, the quantity grpo_loss_fwd calls q.
+ *           The sum is to float32's precision, from weights of that precision or
+ *           better: with rows for every SM it may be some 1e-7 from what the same
+ *           row gives alone.
  * Weights and their sums are integers of fixed point (2^-44 of the largest
  * weight, fewer bits for V above 2^18), so the token does not depend on how a
  * row is split or on any order of summation.
@@ -437,7 +440,9 @@ grpo_status grpo_layernorm_bwd(const grpo_layernorm_problem *problem, const void
  * a generator that still reads the old weights).
  * Buffers of different kinds or tensors must not overlap, nor may an output
  * overlap its own input except as a whole. `tensors` and `out` are host memory,
- * read before the call returns. Tensors with n = 0 are skipped.
+ * read before the call returns. Tensors with n = 0 are skipped. A captured step
+ * holds its config: each replay has the same bias corrections and the same dither,
+ * so that 8-bit states replayed many times stall as with rounding to nearest.
  * INVALID_ARG for null pointers, n < 0, step < 1, betas outside [0, 1), eps or
  * lr or weight_decay that is negative or not finite, a grad_scale that is not
  * finite, state_bits other than 8 and 32, dtypes other than GRPO_F32 and
