@@ -11,6 +11,7 @@ not been built.
 """
 from __future__ import annotations
 
+import copy
 import operator
 from typing import Optional, Sequence
 
@@ -279,23 +280,44 @@ class AdamW:
             self.exp_avg_sq.append(torch.zeros(p.shape, **st))
             for scales in (self.exp_avg_scale, self.exp_avg_sq_scale):
                 scales.append(torch.zeros((p.numel() + 31) // 32, **st) if eight else None)
+        self._none, self._mastered = [None] * n, any(m is not None for m in self.masters)
         self._bind(self._key())
 
     def _check_decays(self, n: int) -> None:
         if isinstance(self.weight_decay, (list, tuple)) and len(self.weight_decay) != n:
             raise ValueError("weight_decay must be one number or %d, got %d" % (n, len(self.weight_decay)))
 
-    def _key(self):
-        """What the table was made of: the place of every tensor, the bytes of the states
-        and masters, and of the parameters, which are the caller's, type, shape and
-        layout. (Methods of the class, mapped: a step's host time is these walks.)"""
-        params = self.params
-        given = [[t for t in ts if t is not None] for ts in (self.masters, self.exp_avg_scale, self.exp_avg_sq_scale)]
-        states = [*self.exp_avg, *self.exp_avg_sq, *given[0], *given[1], *given[2]]
-        some = 0 < len(given[0]) < len(params)
-        return (list(map(_DATA_PTR, [*params, *states])), list(map(_NBYTES, states)), list(map(_DTYPE, params)),
-                list(map(_SHAPE, params)), all(map(_CONTIGUOUS, params)), self.state_bits,
-                [t is None for t in self.masters] if some else None)
+    def _key(self, *others):
+        """What the tables were made of (this object's, and others' behind it): the place
+        of every tensor, the bytes of the states and masters, and of the parameters,
+        which are the caller's, type, shape and layout. (Methods of the class, mapped: a
+        step's host time is these walks.)"""
+        params, states, some = [], [], []
+        for o in (self, *others):
+            none = o._none
+            params += o.params
+            states += o.exp_avg
+            states += o.exp_avg_sq
+            if o.state_bits == 8 or o.exp_avg_scale != none or o.exp_avg_sq_scale != none:
+                states += [t for ts in (o.exp_avg_scale, o.exp_avg_sq_scale) for t in ts if t is not None]
+            if o._mastered or o.masters != none:
+                states += [t for t in o.masters if t is not None]
+                some += [t is None for t in o.masters]
+        return (list(map(_DATA_PTR, params + states)), list(map(_NBYTES, states)), list(map(_DTYPE, params)),
+                list(map(_SHAPE, params)), all(map(_CONTIGUOUS, params)), self.state_bits, some)
+
+    def _check_tables(self, out) -> None:
+        """Make the tables of this object, and of ``out`` if it is given, again where they
+        are not those of its tensors any more."""
+        of = (self,) if out is None else (self, out)
+        for o in of:
+            key = o._key()
+            if key != o._bound:
+                o._bind(key)
+        if out is not None:
+            if out is self or out._bound[1:] != self._bound[1:] or out._at != self._at:
+                raise ValueError("out must be another AdamW of the same shapes, types and states")
+            self._pair = self._bound, out._bound, self._key(out)
 
     def _bind(self, key) -> None:
         """Make the table of the tensors that a step is given (again, when a tensor of
@@ -321,6 +343,8 @@ class AdamW:
         self._table = table
         self._columns = np.frombuffer(table, dtype=_lib.ADAMW_COLUMNS)[:n]   # the same memory
         self._at = self.params[0].get_device() if n else -1
+        self._mastered = bool(key[-1])
+        self._filled, self._pair = None, (None, None, None)
         self._bound = key
 
     def step(self, grads: Sequence[torch.Tensor], grad_scale: float = 1.0, lr: Optional[float] = None,
@@ -330,36 +354,39 @@ class AdamW:
         n = len(self.params)
         if len(grads) != n:
             raise ValueError("expected %d gradients, got %d" % (n, len(grads)))
-        key = self._key()
-        if key != self._bound:
-            self._bind(key)
-        to = self
-        if out is not None:
-            to, to_key = out, out._key()
-            if to_key != out._bound:
-                out._bind(to_key)
-            if out is self or to_key[1:] != key[1:] or out._at != self._at:
-                raise ValueError("out must be another AdamW of the same shapes, types and states")
+        if out is None:
+            to, good = self, self._key() == self._bound
+        else:
+            mine, its, both = self._pair
+            to, good = out, mine is self._bound and its is out._bound and self._key(out) == both
+        if not good:
+            self._check_tables(out)
         if not n:
             return
         dev, table = self.device, self._columns
         try:
-            codes = list(map(_PLAIN_CODES.get, map(_DTYPE, grads)))
-            good = list(map(_SHAPE, grads)) == key[3] and None not in codes and \
-                all(map(_CONTIGUOUS, grads)) and not any(map(self._at.__ne__, map(_GET_DEVICE, grads)))
+            dtypes = list(map(_DTYPE, grads))
+            good = list(map(_SHAPE, grads)) == self._bound[3] and all(map(_CONTIGUOUS, grads)) and \
+                not any(map(self._at.__ne__, map(_GET_DEVICE, grads))) and not set(dtypes) - _PLAIN_CODES.keys()
         except (AttributeError, TypeError):     # not tensors
             good = False
         if not good:
             self._refuse(grads)
-        self._check_decays(n)
-        table["weight_decay"] = self.weight_decay
         table["grad"] = list(map(_DATA_PTR, grads))
-        table["grad_dtype"] = codes
+        filled = dtypes, self.weight_decay
+        if filled != self._filled:
+            self._check_decays(n)
+            table["grad_dtype"] = list(map(_PLAIN_CODES.get, dtypes))
+            table["weight_decay"] = self.weight_decay
+            self._filled = dtypes, copy.copy(self.weight_decay)
         count = self.step_count + 1 if step is None else step
         config = _lib.AdamwConfig(self.lr if lr is None else lr, self.betas[0], self.betas[1],
                                   self.eps, grad_scale, self.state_bits, count)
         _lib.adamw_step(config, self._table, None if out is None else out._table, n, dev, stream)
-        _lib._written(to.params, to.masters)
+        if to._mastered:
+            _lib._written(to.params, to.masters)
+        else:
+            torch.autograd.graph.increment_version(to.params)
         to.step_count = count
 
     def _refuse(self, grads) -> None:
