@@ -15,7 +15,8 @@
 //
 // - k_sample_counts (bf16 rows): the row as counts of its few distinct values, in
 //   which every sum is exact and every cut-off is a search; a cluster of CTAs a row.
-//   One row of 128256: 14 to 17 us; 64 rows: 22 to 31.
+//   One row of 128256: 15 to 19 us; 64 rows: 24 to 31, but 68 to 780 where the logits
+//   are almost equal (a spread of 0.05), whose counts meet in few counters.
 // - k_sample (float32 rows, and short ones): two ways of weighing share one body. The
 //   fast one takes 2^y from a polynomial and carries a bound E on the error of its
 //   sums; where the draw or the top-p cut falls within E of a border, the row is
@@ -23,12 +24,15 @@
 //   A trained model's rows (a few likely tokens) seldom need that. A cluster takes a
 //   row, each CTA one slice of it that it copies into shared memory once, and every
 //   question (maximum, sums, histogram, draw) reads that and is joined through
-//   distributed shared memory. 8 rows of 128256: 16 to 35 us with few candidates or
-//   no cut-off, 21 to 105 with top-p alone.
+//   distributed shared memory. 8 rows of 128256: 15 us with no cut-off, 33 where a draw
+//   falls near a border in one of them, 19 with few candidates; with top-p alone 74 (a
+//   spread of 3) to 650 (0.05).
 // - k_sample_rows (rows enough for every SM): a CTA a row in little more than a pass, for
 //   what a list of a few candidates or the plain softmax decides; the others are left to
 //   a second launch of the kernels above. 512 rows of 201088 in bf16: greedy and small
-//   top-k 66 to 78 us, all rows left to the second launch (wide top-p) 302 to 348.
+//   top-k 65 to 78 us, all rows left to the second launch (wide top-p) 295 to 321, or 2280
+//   of almost equal logits. In float32: 95 and 110; left to the second launch 2150 (a
+//   spread of 3) to 20000 (0.05).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
