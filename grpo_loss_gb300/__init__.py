@@ -255,6 +255,10 @@ class AdamW:
     types, the new parameters and states are written there and this object's stay
     as they are. A step that is captured into a CUDA graph holds its number, rates and
     dither: each replay is that same step, and 8-bit states replayed many times stall.
+
+    The state of a run is ``step_count`` and the lists ``masters``, ``exp_avg``,
+    ``exp_avg_sq``, ``exp_avg_scale`` and ``exp_avg_sq_scale``, beside the parameters:
+    save those, and copy into or replace their tensors to restore it.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas=(0.9, 0.999),

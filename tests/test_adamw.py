@@ -306,6 +306,37 @@ def test_a_tiny_eps_is_not_none(eps, bits):
         assert bool((off <= 1e-3 * 2.0 ** -20 + 2.0 ** -24 * (before[moved].abs().double() + 1e-3)).all())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_run_goes_on_from_its_lists(bits):
+    """Saved and restored, by copies into the tensors or by other tensors in the lists."""
+    import grpo_loss_gb300 as G
+    sizes = [5000, 77]
+    params, _ = tensors(sizes, BF16, F32, 2)
+    steps = [tensors(sizes, BF16, F32, 20 + i)[1] for i in range(3)]
+    opt = G.AdamW(params, state_bits=bits, master=True, **HYPER)
+    for g in steps[:2]:
+        opt.step(g)
+    saved, count = copies(opt), opt.step_count
+    opt.step(steps[2])
+    for replace in (False, True):
+        again = G.AdamW([torch.zeros_like(p) for p in params], state_bits=bits, master=True, **HYPER)
+        again.step([torch.zeros_like(g) for g in steps[0]])          # its table is made
+        for mine, theirs in zip((again.params, again.masters, again.exp_avg, again.exp_avg_sq, again.exp_avg_scale,
+                                 again.exp_avg_sq_scale), saved):
+            for i, t in enumerate(theirs):
+                if t is not None and replace:
+                    mine[i] = t.clone()
+                elif t is not None:
+                    mine[i].copy_(t)
+        again.step_count = count
+        again.step(steps[2])
+        torch.cuda.synchronize()
+        for ts, ks in zip(copies(again), copies(opt)):
+            for t, k in zip(ts, ks):
+                assert (t is None and k is None) or torch.equal(t, k)
+
+
 
 # ---------------------------------------------------------------- refusals
 
