@@ -400,7 +400,7 @@ def _plain_block_bwd(s, case):
         if len(gate) < len(g):
             dgate = dgate.view(len(gate), -1, dgate.shape[1]).sum(1)
         else:
-            dgate = dgate.to(gate.dtype if case["gate"] == "element" else torch.float32)
+            dgate = dgate.to(gate.dtype)            # a gate for every row is an activation
         g = g * _gate_rows(gate, len(g))
     if case["post"]:
         g, dpost_weight, dpost_bias = _plain_norm_bwd(g, x, s["post_weight"], s["post_mean"], s["post_rstd"],
