@@ -5,7 +5,11 @@ estimator plus the exp(q - q.detach()) * A advantage term) over the
 flattened token axis, in hand-written sm_103a CUDA kernels behind the C ABI
 of include/grpo.h; and the operators around that loss in a GRPO iteration: the
 draw of completion tokens (``sample``), the norm before the head with its
-gradients (``layer_norm``) and the optimizer step (``AdamW``). Importing the
+gradients (``layer_norm``) and the optimizer step (``AdamW``); and those of a
+rollout's further updates: the clipped policy loss (``policy_loss``,
+``clipped_policy_loss``), the norms around a block with its gate
+(``residual_norm``) and the clipping of the gradients (``grad_norm``,
+``clip_grad_norm``). Importing the
 package does not load the library; the first call does, and raises if it has
 not been built.
 """
@@ -19,14 +23,18 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import (GrpoError, Problem, advantages, device_status, layernorm_bwd, layernorm_fwd,
-                   loss_bwd, loss_bwd_e4m3, loss_fwd, loss_fwd_e4m3, make_problem,
-                   profile_collect, profile_enable, quantize_e4m3_rows, sample, workspace_size)
+from ._lib import (GrpoError, Problem, advantages, clip_grad_norm, device_status, grad_norm,
+                   layernorm_bwd, layernorm_fwd, loss_bwd, loss_bwd_dlogp, loss_bwd_dlogp_e4m3,
+                   loss_bwd_e4m3, loss_fwd, loss_fwd_e4m3, make_problem, policy_loss,
+                   profile_collect, profile_enable, quantize_e4m3_rows, residual_norm_bwd,
+                   residual_norm_fwd, sample, workspace_size)
 
-__all__ = ["GrpoError", "Problem", "advantages", "device_status", "layernorm_bwd",
-           "layernorm_fwd", "loss_bwd", "loss_bwd_e4m3", "loss_fwd", "loss_fwd_e4m3",
-           "make_problem", "profile_collect", "profile_enable", "quantize_e4m3_rows", "sample",
-           "workspace_size", "GRPOLoss", "grpo_loss", "layer_norm", "AdamW"]
+__all__ = ["GrpoError", "Problem", "advantages", "clip_grad_norm", "device_status", "grad_norm",
+           "layernorm_bwd", "layernorm_fwd", "loss_bwd", "loss_bwd_dlogp", "loss_bwd_dlogp_e4m3",
+           "loss_bwd_e4m3", "loss_fwd", "loss_fwd_e4m3", "make_problem", "policy_loss",
+           "profile_collect", "profile_enable", "quantize_e4m3_rows", "residual_norm_bwd",
+           "residual_norm_fwd", "sample", "workspace_size", "GRPOLoss", "grpo_loss", "layer_norm",
+           "clipped_policy_loss", "residual_norm", "AdamW"]
 
 
 _CTRL_BYTES = 256  # control block at the start of every workspace (error word, counts)
@@ -120,7 +128,9 @@ class GRPOLoss:
                      self.lse_pol, self.loss, self.kl_mean, self.ws_fwd)
         return self.loss, self.kl_mean, self.logp_pol, self.logp_ref
 
-    def backward(self, H_pol, W, ids, mask, adv, grad_loss: float = 1.0, dH=None):
+    def backward(self, H_pol, W, ids, mask, adv, grad_loss: float = 1.0, dH=None, dlogp=None):
+        """With ``dlogp`` (float32 [N], ``policy_loss``'s or any other objective's gradient by
+        ``logp_pol``) the gradient of that objective, and ``adv`` may be None."""
         if dH is None:
             if self.dH is None:
                 self.dH = (torch.empty(H_pol.shape, dtype=torch.bfloat16, device=H_pol.device)
@@ -129,9 +139,16 @@ class GRPOLoss:
         if self.e4m3:
             if self._quantized != (self._ident(H_pol), self._ident(W)):
                 self._quantize(H_pol, W)
+            if dlogp is not None:
+                loss_bwd_dlogp_e4m3(self.problem, self.q_pol, self.s_pol, self.q_W, self.s_W, ids, mask, dlogp,
+                                    self.lse_pol, grad_loss, dH, self.ws_bwd, dW=self.dW)
+                return dH
             loss_bwd_e4m3(self.problem, self.q_pol, self.s_pol, self.q_W, self.s_W, ids, mask,
                           adv, self.logp_pol, self.logp_ref, self.lse_pol, grad_loss, dH,
                           self.ws_bwd, dW=self.dW)
+        elif dlogp is not None:
+            loss_bwd_dlogp(self.problem, H_pol, W, ids, mask, dlogp, self.lse_pol, grad_loss, dH, self.ws_bwd,
+                           dW=self.dW)
         else:
             loss_bwd(self.problem, H_pol, W, ids, mask, adv, self.logp_pol, self.logp_ref,
                      self.lse_pol, grad_loss, dH, self.ws_bwd, dW=self.dW)
@@ -230,6 +247,106 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     none of their own (asking for them is an error). Capture ``layernorm_fwd`` and
     ``layernorm_bwd`` into a CUDA graph rather than this."""
     return _LayerNormFn.apply(x.reshape(-1, x.shape[-1]), weight, bias, eps, rms).view(x.shape)
+
+
+class _OnceDifferentiableFn(torch.autograd.Function):
+    """Gradients as a node that refuses its own, with a graph to be made of them."""
+
+    @staticmethod
+    def forward(ctx, name, fn, *args):
+        ctx.name = name
+        return fn(*args)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("%s is once differentiable: its gradients have no gradients of their own" % ctx.name)
+
+
+def _rows_of(t, shape):
+    """A gradient as rows that a kernel takes: one that is broadcast, or transposed, is laid out."""
+    t = t.reshape(shape)
+    return t.contiguous() if t.stride(-1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]) else t
+
+
+class _PolicyLossFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logp, advantages, mask, kw):
+        loss, dlogp, stats = policy_loss(logp, advantages, mask, need_dlogp=ctx.needs_input_grad[0], **kw)
+        if dlogp is not None:
+            ctx.save_for_backward(dlogp, logp)      # (logp: what the gradient would depend on)
+        ctx.mark_non_differentiable(stats)
+        return loss.reshape(()), stats
+
+    @staticmethod
+    def backward(ctx, g_loss, g_stats):
+        dlogp, logp = ctx.saved_tensors
+        if torch.is_grad_enabled():
+            times = lambda d, g, q: d * g  # noqa: E731
+            return _OnceDifferentiableFn.apply("clipped_policy_loss", times, dlogp, g_loss, logp), None, None, None
+        return dlogp * g_loss, None, None, None
+
+
+def clipped_policy_loss(logp: torch.Tensor, advantages: torch.Tensor, mask: torch.Tensor, logp_old=None,
+                        logp_ref=None, clip=(0.2, 0.2), dual_clip: Optional[float] = None, beta: float = 0.0,
+                        ratio: str = "token", reduce: str = "sequence", divisor: Optional[float] = None):
+    """Autograd entry of ``policy_loss``: (loss, stats), the loss with a gradient for
+    ``logp``. The gradient is formed with the loss, and has none of its own (asking for it is
+    an error). Capture ``policy_loss`` into a CUDA graph rather than this."""
+    kw = dict(logp_old=logp_old, logp_ref=logp_ref, clip=clip, dual_clip=dual_clip, beta=beta, ratio=ratio,
+              reduce=reduce, divisor=divisor)
+    return _PolicyLossFn.apply(logp, advantages, mask, kw)
+
+
+class _ResidualNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, bias, post_weight, post_bias, gate, scale, eps, rms):
+        h, y, mean, rstd, post_mean, post_rstd = residual_norm_fwd(x, residual, weight, bias, post_weight, post_bias,
+                                                                   gate, scale, eps, rms)
+        inner = post_weight is not None or gate is not None
+        ctx.save_for_backward(h, weight, mean, rstd, x if inner else None, post_weight, post_bias, post_mean, post_rstd,
+                              gate)
+        ctx.scale, ctx.rms, ctx.bias_dtype = scale, rms, None if bias is None else bias.dtype
+        ctx.set_materialize_grads(False)
+        return h, y
+
+    @staticmethod
+    def backward(ctx, dh, dy):
+        args = (dh, dy) + ctx.saved_tensors + (ctx.scale, ctx.rms, ctx.bias_dtype, ctx.needs_input_grad)
+        if torch.is_grad_enabled():
+            return _OnceDifferentiableFn.apply("residual_norm", _residual_norm_grads, *args) + (None,) * 3
+        return _residual_norm_grads(*args) + (None,) * 3
+
+
+def _residual_norm_grads(dh, dy, h, weight, mean, rstd, x, post_weight, post_bias, post_mean, post_rstd, gate, scale,
+                         rms, bias_dtype, need):
+    need_w, need_b, need_pw, need_pb, need_gate = need[2:7]
+    dy = torch.zeros_like(h) if dy is None else _rows_of(dy, h.shape).to(h.dtype)
+    dh = None if dh is None else _rows_of(dh, h.shape).to(h.dtype)
+    some = need_w or need_b or need_pw or need_pb
+    dx, dres, dw, db, dpw, dpb, dg = residual_norm_bwd(dy, dh, h, weight, mean, rstd, x, post_weight, post_bias,
+                                                       post_mean, post_rstd, gate, scale, rms,
+                                                       bias=bias_dtype is not None, need_params=some,
+                                                       need_dgate=need_gate)
+    return (dx if need[0] else None, dres if need[1] else None, dw.to(weight.dtype) if need_w else None,
+            db.to(bias_dtype) if need_b else None, dpw.to(post_weight.dtype) if need_pw else None,
+            dpb.to(post_bias.dtype) if need_pb else None, dg.to(gate.dtype) if need_gate else None)
+
+
+def residual_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
+                  bias: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+                  post_bias: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                  eps: float = 1e-5, rms: bool = False):
+    """Autograd entry of the norms around a block over the last dimension: (h, y) with
+    h = residual + scale * gate * post_norm(x) and y = norm(h), of x's shape; see
+    ``residual_norm_fwd``. The gate is one for each channel ([d]), or has the rows that
+    divide x's (of its leading dimensions: [sequences, d] for x [sequences, tokens, d]).
+    Gradients for every tensor, which have none of their own (asking for them is an error).
+    Capture ``residual_norm_fwd`` and ``residual_norm_bwd`` into a CUDA graph rather than
+    this."""
+    d = x.shape[-1]
+    h, y = _ResidualNormFn.apply(x.reshape(-1, d), residual.reshape(-1, d), weight, bias, post_weight, post_bias,
+                                 None if gate is None else gate.reshape(-1, d), scale, eps, rms)
+    return h.view(x.shape), y.view(x.shape)
 
 
 _DATA_PTR, _CONTIGUOUS, _GET_DEVICE = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
@@ -352,9 +469,11 @@ class AdamW:
         self._bound = key
 
     def step(self, grads: Sequence[torch.Tensor], grad_scale: float = 1.0, lr: Optional[float] = None,
-             step: Optional[int] = None, out: Optional["AdamW"] = None, stream=None) -> None:
+             step: Optional[int] = None, out: Optional["AdamW"] = None, stream=None, factor=None) -> None:
         """``step`` overrides the count of steps taken (1 for the first), ``lr``
-        this step's rate; ``grad_scale`` multiplies every gradient."""
+        this step's rate; ``grad_scale`` multiplies every gradient, and so does ``factor``, a
+        float32 tensor of one element on the device (``grad_norm``'s with ``max_norm``: the
+        gradients are clipped as the step reads them)."""
         n = len(self.params)
         if len(grads) != n:
             raise ValueError("expected %d gradients, got %d" % (n, len(grads)))
@@ -385,7 +504,8 @@ class AdamW:
             self._filled = dtypes, copy.copy(self.weight_decay)
         count = self.step_count + 1 if step is None else step
         config = _lib.AdamwConfig(self.lr if lr is None else lr, self.betas[0], self.betas[1],
-                                  self.eps, grad_scale, self.state_bits, count)
+                                  self.eps, grad_scale, self.state_bits, count,
+                                  None if factor is None else _lib._vec_ptr(factor, "factor", torch.float32, 1, dev))
         _lib.adamw_step(config, self._table, None if out is None else out._table, n, dev, stream)
         if to._mastered:
             _lib._written(to.params, to.masters)

@@ -79,7 +79,35 @@ class AdamwConfig(ctypes.Structure):
     """Mirror of ``grpo_adamw_config``."""
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("grad_scale", ctypes.c_float),
-                ("state_bits", ctypes.c_int32), ("step", ctypes.c_int64)]
+                ("state_bits", ctypes.c_int32), ("step", ctypes.c_int64), ("factor", ctypes.c_void_p)]
+
+
+class PolicyProblem(ctypes.Structure):
+    """Mirror of ``grpo_policy_problem``."""
+    _fields_ = [(k, ctypes.c_int64) for k in ("num_seqs", "seq_len", "ld_logp", "ld_old", "ld_ref", "ld_adv",
+                                              "ld_mask", "ld_dlogp")] + \
+        [(k, ctypes.c_double) for k in ("clip_low", "clip_high", "dual_clip", "beta", "divisor")] + \
+        [(k, ctypes.c_int32) for k in ("ratio", "reduce", "token_adv")]
+
+
+class ResidualNormProblem(ctypes.Structure):
+    """Mirror of ``grpo_residual_norm_problem``."""
+    _fields_ = [(k, ctypes.c_int64) for k in ("rows", "d", "ld_x", "ld_residual", "ld_h", "ld_y", "ld_gate", "ld_dy",
+                                              "ld_dh", "ld_dx", "ld_dresidual", "ld_dgate", "gate_rows")] + \
+        [("eps", ctypes.c_float), ("scale", ctypes.c_float)] + \
+        [(k, ctypes.c_int32) for k in ("rms", "dtype", "param_dtype", "gate_dtype")]
+
+
+class GradTensor(ctypes.Structure):
+    """Mirror of ``grpo_grad_tensor``."""
+    _fields_ = [("n", ctypes.c_int64), ("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("dtype", ctypes.c_int32)]
+
+
+# The same as columns of an array.
+GRAD_COLUMNS = np.dtype({"names": ["n", "grad", "out", "dtype"], "formats": [np.int64, np.uint64, np.uint64, np.int32],
+                         "offsets": [GradTensor.n.offset, GradTensor.grad.offset, GradTensor.out.offset,
+                                     GradTensor.dtype.offset],
+                         "itemsize": ctypes.sizeof(GradTensor)})
 
 
 def make_problem(num_seqs: int, seq_len: int, d: int, V: int, group_size: int,
@@ -141,6 +169,23 @@ _SIGNATURES = {
                            [ctypes.c_size_t, _VP]),
     "grpo_adamw_step": (ctypes.c_int, [ctypes.POINTER(AdamwConfig), ctypes.POINTER(AdamwTensor),
                                        ctypes.POINTER(AdamwTensor), ctypes.c_int32, _VP]),
+    "grpo_policy_loss_workspace_size": (ctypes.c_int, [ctypes.POINTER(PolicyProblem),
+                                                       ctypes.POINTER(ctypes.c_size_t)]),
+    "grpo_policy_loss": (ctypes.c_int, [ctypes.POINTER(PolicyProblem)] + [_VP] * 9 + [ctypes.c_size_t, _VP]),
+    "grpo_loss_bwd_dlogp": (ctypes.c_int, [ctypes.POINTER(Problem)] + [_VP] * 6 +
+                            [ctypes.c_float, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+    "grpo_loss_bwd_dlogp_e4m3": (ctypes.c_int, [ctypes.POINTER(Problem)] + [_VP] * 8 +
+                                 [ctypes.c_float, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+    "grpo_residual_norm_workspace_size": (ctypes.c_int, [ctypes.POINTER(ResidualNormProblem),
+                                                         ctypes.POINTER(ctypes.c_size_t)]),
+    "grpo_residual_norm_fwd": (ctypes.c_int, [ctypes.POINTER(ResidualNormProblem)] + [_VP] * 14),
+    "grpo_residual_norm_bwd": (ctypes.c_int, [ctypes.POINTER(ResidualNormProblem)] + [_VP] * 20 +
+                               [ctypes.c_size_t, _VP]),
+    "grpo_grad_norm_workspace_size": (ctypes.c_int, [ctypes.POINTER(ctypes.c_size_t)]),
+    "grpo_grad_norm": (ctypes.c_int, [_VP, ctypes.c_int32, ctypes.c_int32, ctypes.c_double, ctypes.c_double] +
+                       [_VP] * 3 + [ctypes.c_size_t, _VP]),
+    "grpo_clip_grad_norm": (ctypes.c_int, [_VP, ctypes.c_int32, ctypes.c_int32, ctypes.c_double, ctypes.c_double] +
+                            [_VP] * 3 + [ctypes.c_size_t, _VP]),
     "grpo_get_device_status": (ctypes.c_int, [_VP, _VP]),
     "grpo_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "grpo_profile_enable": (ctypes.c_int, [ctypes.c_int32]),
@@ -523,6 +568,379 @@ def adamw_step(config: AdamwConfig, tensors, out, n: int, device, stream=None) -
     """One grpo_adamw_step over ctypes arrays of AdamwTensor (``out`` may be None);
     the AdamW class checks the tensors and fills the arrays."""
     _call(lib().grpo_adamw_step, "grpo_adamw_step", device, stream, config, tensors, out, n)
+
+
+def _bytes(fn, where: str, dev, *args) -> int:
+    """A workspace's size, asked with ``dev`` current."""
+    b = ctypes.c_size_t(0)
+    if torch._C._cuda_getDevice() == dev.index:
+        status = fn(*args, ctypes.byref(b))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, ctypes.byref(b))
+    if status != GRPO_OK:
+        raise GrpoError(status, where)
+    return b.value
+
+
+def _workspace(workspace, size, dev):
+    """(tensor, pointer, bytes) of a workspace that is given or made of ``size()`` bytes."""
+    if workspace is None:
+        workspace = torch.empty(size(), dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), workspace.numel()
+    return workspace, _vec_ptr(workspace, "workspace", workspace.dtype, workspace.numel(), dev), workspace.nbytes
+
+
+_RATIOS, _REDUCES = {"token": 0, "sequence": 1}, {"sequence": 0, "token": 1, "constant": 2}
+
+
+def policy_workspace_size(problem: PolicyProblem) -> int:
+    """Bytes of grpo_policy_loss's workspace on the current device."""
+    b = ctypes.c_size_t(0)
+    _check(lib().grpo_policy_loss_workspace_size(ctypes.byref(problem), ctypes.byref(b)),
+           "grpo_policy_loss_workspace_size")
+    return b.value
+
+
+def policy_loss(logp: torch.Tensor, advantages: torch.Tensor, mask: torch.Tensor, logp_old=None, logp_ref=None,
+                clip=(0.2, 0.2), dual_clip: Optional[float] = None, beta: float = 0.0, ratio: str = "token",
+                reduce: str = "sequence", divisor: Optional[float] = None, need_dlogp: bool = True, loss=None,
+                dlogp=None, stats=None, workspace=None, stream=None):
+    """The clipped policy loss with its KL term over ``logp`` (float32 [B, T], rows may
+    be strided, as those of every [B, T] here): (loss float32 [1], dlogp float32 [B, T],
+    stats float32 [4]); see grpo_policy_loss for the definition. ``advantages`` is float32
+    [B] or [B, T]; ``mask`` bool or uint8 [B, T]; ``logp_old`` and ``logp_ref`` float32
+    [B, T], optional: ratio 1, and no KL term. ``clip`` is (low, high); ``ratio`` "token" or
+    "sequence"; ``reduce`` "sequence" (the mean over each sequence's tokens, then over
+    sequences), "token" (over all tokens) or "constant" (the sum over ``divisor``).
+    ``stats`` are means over valid tokens: the KL estimate, the shares of tokens whose
+    gradient the lower and the upper bound took away, the ratio. dlogp is None without
+    ``need_dlogp``. Outputs and a workspace that are not given belong to ``stream``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return policy_loss(logp, advantages, mask, logp_old, logp_ref, clip, dual_clip, beta, ratio, reduce,
+                               divisor, need_dlogp, loss, dlogp, stats, workspace)
+    if logp.dim() != 2:
+        raise ValueError("logp must be 2-D")
+    if ratio not in _RATIOS:
+        raise ValueError("ratio must be one of %s, got %r" % (sorted(_RATIOS), ratio))
+    if reduce not in _REDUCES:
+        raise ValueError("reduce must be one of %s, got %r" % (sorted(_REDUCES), reduce))
+    if (reduce == "constant") != (divisor is not None):
+        raise ValueError("divisor is needed with reduce=\"constant\", and only there")
+    B, T = logp.shape
+    f32 = torch.float32
+    dev = _device_of(logp, "logp")
+    lp, ld = _rows_ptr(logp, "logp", f32, B, T, dev)
+    if mask.dtype != torch.bool and mask.dtype != torch.uint8:
+        raise ValueError("mask must be bool or uint8, got %s" % (mask.dtype,))
+    mp, ld_mask = _rows_ptr(mask, "mask", mask.dtype, B, T, dev)
+    op, ld_old = (None, 0) if logp_old is None else _rows_ptr(logp_old, "logp_old", f32, B, T, dev)
+    rp, ld_ref = (None, 0) if logp_ref is None else _rows_ptr(logp_ref, "logp_ref", f32, B, T, dev)
+    per_token = advantages.dim() == 2
+    if per_token:
+        ap, ld_adv = _rows_ptr(advantages, "advantages", f32, B, T, dev)
+    else:
+        ap, ld_adv = _vec_ptr(advantages, "advantages", f32, B, dev), 0
+    given = loss, dlogp, stats
+    loss, out = _vec_out(loss, "loss", f32, 1, dev)
+    stats, sp = _vec_out(stats, "stats", f32, 4, dev)
+    dp, ld_d = None, 0
+    if dlogp is not None or need_dlogp:
+        dlogp, dp, ld_d = _rows_out(dlogp, "dlogp", f32, B, T, dev)
+    problem = PolicyProblem(B, T, ld, ld_old, ld_ref, ld_adv, ld_mask, ld_d, clip[0], clip[1], dual_clip or 0.0, beta,
+                            divisor or 0.0, _RATIOS[ratio], _REDUCES[reduce], 1 if per_token else 0)
+    L = lib()
+    _, wp, size = _workspace(workspace, lambda: _bytes(L.grpo_policy_loss_workspace_size,
+                                                       "grpo_policy_loss_workspace_size", dev, problem), dev)
+    _call(L.grpo_policy_loss, "grpo_policy_loss", dev, None, problem, lp, op, rp, ap, mp, out, sp, dp, wp, size)
+    _written(given)
+    return loss, dlogp, stats
+
+
+def loss_bwd_dlogp(problem: Problem, H_pol, W, ids, mask, dlogp, lse_pol, grad_loss: float, dH,
+                   workspace: torch.Tensor, stream=None, dW=None) -> None:
+    N = problem.N
+    _check(lib().grpo_loss_bwd_dlogp(
+        ctypes.byref(problem), _ptr(H_pol, "H_pol"), _ptr(W, "W"), _ptr(ids, "ids", torch.int32, N),
+        _ptr(mask, "mask", torch.uint8, N), _ptr(dlogp, "dlogp", torch.float32, N),
+        _ptr(lse_pol, "lse_pol", torch.float32, N), float(grad_loss), _ptr(dH, "dH"),
+        _ptr(dW, "dW", torch.float32, problem.V * problem.d), _ptr(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)), "grpo_loss_bwd_dlogp")
+
+
+def loss_bwd_dlogp_e4m3(problem: Problem, H_pol, s_pol, W, s_W, ids, mask, dlogp, lse_pol, grad_loss: float, dH,
+                        workspace: torch.Tensor, stream=None, dW=None) -> None:
+    N, Nd, Vd = problem.N, problem.N * problem.d, problem.V * problem.d
+    _check(lib().grpo_loss_bwd_dlogp_e4m3(
+        ctypes.byref(problem), _codes(H_pol, "H_pol", Nd), _ptr(s_pol, "s_pol", torch.float32, N),
+        _codes(W, "W", Vd), _ptr(s_W, "s_W", torch.float32, problem.V), _ptr(ids, "ids", torch.int32, N),
+        _ptr(mask, "mask", torch.uint8, N), _ptr(dlogp, "dlogp", torch.float32, N),
+        _ptr(lse_pol, "lse_pol", torch.float32, N), float(grad_loss), _ptr(dH, "dH", torch.bfloat16, Nd),
+        _ptr(dW, "dW", torch.float32, Vd), _ptr(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)), "grpo_loss_bwd_dlogp_e4m3")
+
+
+def residual_norm_workspace_size(problem: ResidualNormProblem) -> int:
+    """Bytes of grpo_residual_norm_bwd's workspace on the current device."""
+    b = ctypes.c_size_t(0)
+    _check(lib().grpo_residual_norm_workspace_size(ctypes.byref(problem), ctypes.byref(b)),
+           "grpo_residual_norm_workspace_size")
+    return b.value
+
+
+def _gate_ptr(gate, rows: int, d: int, device):
+    """(pointer, row stride, rows that share a gate's row, type) of an optional gate."""
+    if gate is None:
+        return None, 0, 0, GRPO_F32
+    if gate.dim() != 2:
+        raise ValueError("gate must be 2-D")
+    n = gate.shape[0]
+    if n < 1 and rows > 0 or n > 0 and rows % n != 0:
+        raise ValueError("gate must have a number of rows that divides %d, got %d" % (rows, n))
+    code = _plain_code(gate.dtype, "gate")
+    gp, ld = _rows_ptr(gate, "gate", gate.dtype, n, d, device)
+    return gp, ld, rows // n if n else 1, code
+
+
+def residual_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, bias=None, post_weight=None,
+                      post_bias=None, gate=None, scale: float = 1.0, eps: float = 1e-5, rms: bool = False, h=None,
+                      y=None, mean=None, rstd=None, post_mean=None, post_rstd=None, stream=None):
+    """h = residual + scale * gate * post_norm(x) and y = norm(h) over the rows of ``x``
+    and ``residual`` (float32 or bf16 [rows, d], rows may be strided): (h, y, mean, rstd,
+    post_mean, post_rstd). Without ``post_weight`` x is taken as it is, and the post_*
+    statistics are None; the means are with ``rms``. ``gate`` (float32 or bf16, rows may be
+    strided) has one row, or one for every row or for as many rows as divide them; the
+    parameters are float32 or bf16 [d], of one type. Outputs that are not given belong to
+    ``stream``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return residual_norm_fwd(x, residual, weight, bias, post_weight, post_bias, gate, scale, eps, rms, h, y,
+                                     mean, rstd, post_mean, post_rstd)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    rows, d = x.shape
+    f32, dt, pt, post = torch.float32, x.dtype, weight.dtype, post_weight is not None
+    code, pcode = _plain_code(dt, "x"), _plain_code(pt, "weight")
+    dev = _device_of(x, "x")
+    xp, ld_x = _rows_ptr(x, "x", dt, rows, d, dev)
+    sp, ld_res = _rows_ptr(residual, "residual", dt, rows, d, dev)
+    gp, ld_gate, gate_rows, gcode = _gate_ptr(gate, rows, d, dev)
+    given = h, y, None if rms else mean, rstd, post_mean if post and not rms else None, post_rstd if post else None
+    h, hp, ld_h = _rows_out(h, "h", dt, rows, d, dev)
+    y, yp, ld_y = _rows_out(y, "y", dt, rows, d, dev)
+    mean, mp = (None, None) if rms else _vec_out(mean, "mean", f32, rows, dev)
+    rstd, rp = _vec_out(rstd, "rstd", f32, rows, dev)
+    post_mean, pmp = (None, None) if rms or not post else _vec_out(post_mean, "post_mean", f32, rows, dev)
+    post_rstd, prp = _vec_out(post_rstd, "post_rstd", f32, rows, dev) if post else (None, None)
+    problem = ResidualNormProblem(rows, d, ld_x, ld_res, ld_h, ld_y, ld_gate, 0, 0, 0, 0, 0, gate_rows, eps, scale,
+                                  1 if rms else 0, code, pcode, gcode)
+    _call(lib().grpo_residual_norm_fwd, "grpo_residual_norm_fwd", dev, None, problem, xp, sp,
+          _vec_ptr(weight, "weight", pt, d, dev), _vec_ptr(bias, "bias", pt, d, dev),
+          _vec_ptr(post_weight, "post_weight", pt, d, dev), _vec_ptr(post_bias, "post_bias", pt, d, dev), gp, hp, yp,
+          mp, rp, pmp, prp)
+    _written(given)
+    return h, y, mean, rstd, post_mean, post_rstd
+
+
+def residual_norm_bwd(dy: torch.Tensor, dh, h: torch.Tensor, weight: torch.Tensor, mean, rstd, x=None,
+                      post_weight=None, post_bias=None, post_mean=None, post_rstd=None, gate=None, scale: float = 1.0,
+                      rms: bool = False, bias: bool = True, dx=None, dresidual=None, dweight=None, dbias=None,
+                      dpost_weight=None, dpost_bias=None, dgate=None, need_params: bool = True,
+                      need_dgate: bool = True, workspace=None, stream=None):
+    """Gradients of ``residual_norm_fwd`` from its inputs, statistics and h, from ``dy``
+    and ``dh`` (None: zero): (dx, dresidual, dweight, dbias, dpost_weight, dpost_bias,
+    dgate). dx and dresidual have h's type; where there is neither a gate nor a post norm
+    and ``scale`` is 1, dx is dresidual, the same tensor unless one is given. The column
+    sums are float32 [d]: None without ``need_params``, dbias also without ``bias`` or with
+    ``rms``, dpost_bias without ``post_bias``. dgate is float32 of the gate's shape, or of
+    its type where the gate has a row for every row. ``x`` is needed for a gate or a post norm. Outputs and a workspace that
+    are not given belong to ``stream``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return residual_norm_bwd(dy, dh, h, weight, mean, rstd, x, post_weight, post_bias, post_mean, post_rstd,
+                                     gate, scale, rms, bias, dx, dresidual, dweight, dbias, dpost_weight, dpost_bias,
+                                     dgate, need_params, need_dgate, workspace)
+    if h.dim() != 2:
+        raise ValueError("h must be 2-D")
+    rows, d = h.shape
+    f32, dt, pt, post = torch.float32, h.dtype, weight.dtype, post_weight is not None
+    code, pcode = _plain_code(dt, "h"), _plain_code(pt, "weight")
+    dev = _device_of(h, "h")
+    if mean is None and not rms:
+        raise ValueError("mean is needed unless rms")
+    if post and (post_rstd is None or (post_mean is None and not rms)):
+        raise ValueError("the post norm's statistics are needed")
+    inner = post or gate is not None
+    if inner and x is None:
+        raise ValueError("x is needed with a gate or a post norm")
+    yp, ld_dy = _rows_ptr(dy, "dy", dt, rows, d, dev)
+    zp, ld_dh = (None, 0) if dh is None else _rows_ptr(dh, "dh", dt, rows, d, dev)
+    hp, ld_h = _rows_ptr(h, "h", dt, rows, d, dev)
+    xp, ld_x = _rows_ptr(x, "x", dt, rows, d, dev) if inner else (None, 0)
+    gp, ld_gate, gate_rows, gcode = _gate_ptr(gate, rows, d, dev)
+    given = dx, dresidual, dweight, dbias, dpost_weight, dpost_bias, dgate
+    dresidual, sp, ld_s = _rows_out(dresidual, "dresidual", dt, rows, d, dev)
+    dxp, ld_dx, same = None, 0, not inner and scale == 1.0 and dx is None
+    if not same:
+        dx, dxp, ld_dx = _rows_out(dx, "dx", dt, rows, d, dev)
+    wp = bp = pwp = pbp = dgp = None
+    ld_dg = 0
+    if dweight is not None or need_params:
+        dweight, wp = _vec_out(dweight, "dweight", f32, d, dev)
+    if dbias is not None or (need_params and bias and not rms):
+        dbias, bp = _vec_out(dbias, "dbias", f32, d, dev)
+    if dpost_weight is not None or (need_params and post):
+        dpost_weight, pwp = _vec_out(dpost_weight, "dpost_weight", f32, d, dev)
+    if dpost_bias is not None or (need_params and post_bias is not None):
+        dpost_bias, pbp = _vec_out(dpost_bias, "dpost_bias", f32, d, dev)
+    if dgate is not None or (gate is not None and need_dgate):
+        if gate is None:
+            raise ValueError("dgate needs a gate")
+        n = gate.shape[0]
+        if gate_rows == 1:
+            dgate, dgp, ld_dg = _rows_out(dgate, "dgate", gate.dtype, n, d, dev)
+        else:
+            if dgate is None:
+                dgate = torch.empty(n, d, dtype=f32, device=dev)
+            dgp = _vec_ptr(dgate, "dgate", f32, n * d, dev)
+    problem = ResidualNormProblem(rows, d, ld_x, 0, ld_h, 0, ld_gate, ld_dy, ld_dh, ld_dx, ld_s, ld_dg, gate_rows, 0.0,
+                                  scale, 1 if rms else 0, code, pcode, gcode)
+    L = lib()
+    wsp, size = None, 0
+    if wp or bp or pwp or pbp or (dgp and gate_rows > 1):
+        workspace, wsp, size = _workspace(workspace, lambda: _bytes(
+            L.grpo_residual_norm_workspace_size, "grpo_residual_norm_workspace_size", dev, problem), dev)
+    _call(L.grpo_residual_norm_bwd, "grpo_residual_norm_bwd", dev, None, problem, yp, zp, hp,
+          _vec_ptr(weight, "weight", pt, d, dev), None if rms else _vec_ptr(mean, "mean", f32, rows, dev),
+          _vec_ptr(rstd, "rstd", f32, rows, dev), xp, _vec_ptr(post_weight, "post_weight", pt, d, dev),
+          _vec_ptr(post_bias, "post_bias", pt, d, dev),
+          _vec_ptr(post_mean, "post_mean", f32, rows, dev) if post and not rms else None,
+          _vec_ptr(post_rstd, "post_rstd", f32, rows, dev) if post else None, gp, dxp, sp, wp, bp, pwp, pbp, dgp, wsp,
+          size)
+    _written(given)
+    return dresidual if same else dx, dresidual, dweight, dbias, dpost_weight, dpost_bias, dgate
+
+
+_PLAIN = {torch.float32: GRPO_F32, torch.bfloat16: GRPO_BF16}
+_NORM_TYPES = {2: 2, float("inf"): 0}
+_get = torch.Tensor
+
+
+def _grad_table(grads, out, name: str):
+    """(columns of GradTensor, device) of a list of gradients."""
+    n = len(grads)
+    table = np.zeros(n, dtype=GRAD_COLUMNS)
+    if not n:
+        return table, None
+    try:
+        dev = grads[0].device
+        at = grads[0].get_device()
+        good = at >= 0 and all(map(_get.is_contiguous, grads)) and not any(map(at.__ne__, map(_get.get_device, grads)))
+        table["dtype"] = [_PLAIN[t.dtype] for t in grads]
+    except (AttributeError, TypeError, KeyError):
+        good = False
+    if not good:
+        for i, t in enumerate(grads):
+            if not torch.is_tensor(t):
+                raise ValueError("%s[%d] must be a tensor, got %r" % (name, i, type(t)))
+            _plain_code(t.dtype, "%s[%d]" % (name, i))
+            _device_of(t, "%s[%d]" % (name, i))
+            _vec_ptr(t, "%s[%d]" % (name, i), t.dtype, t.numel(), grads[0].device)
+    table["n"] = list(map(_get.numel, grads))
+    table["grad"] = list(map(_get.data_ptr, grads))
+    if out is None:
+        table["out"] = table["grad"]
+    else:
+        if len(out) != n:
+            raise ValueError("expected %d tensors in out, got %d" % (n, len(out)))
+        for i, (t, g) in enumerate(zip(out, grads)):
+            if not torch.is_tensor(t) or t.dtype != g.dtype or t.shape != g.shape or t.device != dev or \
+                    not t.is_contiguous():
+                raise ValueError("out[%d] must be contiguous, of %s[%d]'s shape %s and type %s, on %s" % (
+                    i, name, i, tuple(g.shape), g.dtype, dev))
+        table["out"] = list(map(_get.data_ptr, out))
+    return table, dev
+
+
+def _no_overlap(table, given: bool) -> None:
+    """A clipped tensor is written: no other may share its bytes."""
+    sizes = table["n"].astype(np.uint64) * np.where(table["dtype"] == GRPO_F32, 4, 2).astype(np.uint64)
+    some = sizes > 0
+    starts, sizes, index = table["out"][some], sizes[some], np.flatnonzero(some)
+    if given:           # the gradients too, but for those that are their own out
+        own = table["grad"][some] == starts
+        starts, sizes = np.concatenate([starts, table["grad"][some][~own]]), np.concatenate([sizes, sizes[~own]])
+        index = np.concatenate([index, index[~own]])
+        written = np.arange(len(starts)) < int(some.sum())
+    else:
+        written = np.ones(len(starts), dtype=bool)
+    order = np.argsort(starts, kind="stable")
+    ends = np.maximum.accumulate((starts + sizes)[order])
+    # two gradients that are only read may share theirs
+    if np.any(starts[order][1:] < ends[:-1]):
+        last_written = last_any = 0
+        for i in order:
+            if starts[i] < (last_any if written[i] else last_written):
+                raise ValueError("the gradient or out of number %d overlaps another: what is written is one tensor's own"
+                                 % index[i])
+            end = int(starts[i] + sizes[i])
+            last_any = max(last_any, end)
+            last_written = max(last_written, end) if written[i] else last_written
+
+
+def _grad_call(grads, clip: bool, max_norm, norm_type, eps, out, norm, factor, workspace):
+    grads = list(grads)
+    if norm_type not in _NORM_TYPES:
+        raise ValueError("norm_type must be 2 or inf, got %r" % (norm_type,))
+    if max_norm is not None and not max_norm >= 0.0:
+        raise ValueError("max_norm must not be negative, got %r" % (max_norm,))
+    table, dev = _grad_table(grads, out, "grads")
+    if dev is None:
+        given = norm if norm is not None else factor
+        dev = given.device if given is not None else torch.device("cuda", torch.cuda.current_device())
+    given = norm, factor
+    norm, np_ = _vec_out(norm, "norm", torch.float32, 1, dev)
+    fp = None
+    if factor is not None or max_norm is not None:
+        factor, fp = _vec_out(factor, "factor", torch.float32, 1, dev)
+    if clip:
+        _no_overlap(table, out is not None)
+    L = lib()
+    _, wp, size = _workspace(workspace, lambda: _bytes(L.grpo_grad_norm_workspace_size,
+                                                       "grpo_grad_norm_workspace_size", dev), dev)
+    name = "grpo_clip_grad_norm" if clip else "grpo_grad_norm"
+    _call(L.grpo_clip_grad_norm if clip else L.grpo_grad_norm, name, dev, None, table.ctypes.data, len(grads),
+          _NORM_TYPES[norm_type], float("inf") if max_norm is None else max_norm, eps, np_, fp, wp, size)
+    _written(given, (grads if out is None else out) if clip else ())
+    return norm, factor
+
+
+def grad_norm(grads, norm_type: float = 2.0, max_norm: Optional[float] = None, eps: float = 1e-6, norm=None,
+              factor=None, workspace=None, stream=None):
+    """The norm (float32 [1]) of ``grads`` (contiguous float32 or bf16 CUDA tensors) taken
+    as one vector, ``norm_type`` 2 or inf; see grpo_grad_norm. With ``max_norm``, (norm,
+    factor): factor = min(1, max_norm / (norm + eps)) stays on the device, where
+    ``AdamW.step(factor=...)`` takes it. Outputs and a workspace that are not given belong
+    to ``stream``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return grad_norm(grads, norm_type, max_norm, eps, norm, factor, workspace)
+    norm, factor = _grad_call(grads, False, max_norm, norm_type, eps, None, norm, factor, workspace)
+    return norm if max_norm is None else (norm, factor)
+
+
+def clip_grad_norm(grads, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, out=None, norm=None, factor=None,
+                   workspace=None, stream=None):
+    """Scales ``grads`` by min(1, max_norm / (norm + eps)), in place or into the tensors of
+    ``out`` (of the same shapes and types), and returns their norm before that (float32
+    [1]). Tensors that overlap are refused. Outputs and a workspace that are not given
+    belong to ``stream``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return clip_grad_norm(grads, max_norm, norm_type, eps, out, norm, factor, workspace)
+    return _grad_call(grads, True, max_norm, norm_type, eps, None if out is None else list(out), norm, factor,
+                      workspace)[0]
 
 
 def device_status(workspace: torch.Tensor, stream=None) -> int:

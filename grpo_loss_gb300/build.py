@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgrpo_gb300.so")
 SOURCES = ["gemm_tc.cu", "rows.cu", "grpo_api.cu", "noalloc.cu", "sample.cu", "norm.cu", "adamw.cu",
-           "ops_api.cu"]
+           "policy.cu", "residual_norm.cu", "grad_norm.cu", "ops_api.cu", "update_api.cu"]
 HEADERS = ["ptx.cuh", "f32x2.cuh", "internal.h", "api_common.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

@@ -71,9 +71,9 @@ __device__ __forceinline__ float dither_e4m3(float y, uint32_t d) {  // the dith
 // in a table; those of the moments are the formula's own, operation by operation,
 // so that 8-bit states are the same as those of any float32 code. The root and the quotient are the special-function unit's, some
 // 2^-22 off together: of the update, not of the parameter.
-__device__ __forceinline__ void update(const AdamConst& c, float keep, float g, float& x, float& m,
+__device__ __forceinline__ void update(const AdamConst& c, float gs, float keep, float g, float& x, float& m,
                                        float& v) {
-  g = __fmul_rn(g, c.grad_scale);
+  g = __fmul_rn(g, gs);
   m = __fadd_rn(__fmul_rn(c.beta1, m), __fmul_rn(c.one_m_beta1, g));
   v = __fadd_rn(__fmul_rn(c.beta2, v), __fmul_rn(__fmul_rn(c.one_m_beta2, g), g));
   float root;
@@ -87,8 +87,8 @@ __device__ __forceinline__ void update(const AdamConst& c, float keep, float g, 
 
 // The same of two elements, bit by bit. (The sums are one at a time: the assembler
 // fuses a product and a sum of pairs into one rounding.)
-__device__ __forceinline__ void update2(const AdamConst& c, float keep, float* g, float* x, float* m, float* v) {
-  const uint64_t g2 = mul2(pair_of(g[0], g[1]), pair_of(c.grad_scale));
+__device__ __forceinline__ void update2(const AdamConst& c, float gs, float keep, float* g, float* x, float* m, float* v) {
+  const uint64_t g2 = mul2(pair_of(g[0], g[1]), pair_of(gs));
   const float2 m0 = of_pair(mul2(pair_of(c.beta1), pair_of(m[0], m[1]))), m1 = of_pair(mul2(pair_of(c.one_m_beta1), g2));
   const float2 v0 = of_pair(mul2(pair_of(c.beta2), pair_of(v[0], v[1])));
   const float2 v1 = of_pair(mul2(mul2(pair_of(c.one_m_beta2), g2), g2));
@@ -164,7 +164,7 @@ __device__ __forceinline__ void prefetch(const char* p, int size, int from, int 
 // in all (a multiple of 32; every buffer on a 16-byte boundary). With 8-bit
 // states four threads hold a block of 32.
 template <int KIND>
-__device__ __forceinline__ void pieces(const AdamConst& c, const AdamTensor& t, int64_t i0, int end) {
+__device__ __forceinline__ void pieces(const AdamConst& c, float gs, const AdamTensor& t, int64_t i0, int end) {
   constexpr bool kPBf16 = (KIND & ADAM_P_BF16) != 0, kGBf16 = (KIND & ADAM_G_BF16) != 0;
   constexpr bool kMaster = (KIND & ADAM_MASTER) != 0, k8 = (KIND & ADAM_BITS8) != 0;
   constexpr int W = k8 ? 8 : 4, U = k8 ? 1 : 2;  // U pieces' loads are in flight together
@@ -227,7 +227,7 @@ __device__ __forceinline__ void pieces(const AdamConst& c, const AdamTensor& t, 
         }
       }
 #pragma unroll
-      for (int e = 0; e < W; e += 2) update2(c, keep, g[j] + e, x[j] + e, m[j] + e, v[j] + e);
+      for (int e = 0; e < W; e += 2) update2(c, gs, keep, g[j] + e, x[j] + e, m[j] + e, v[j] + e);
       const uint32_t d0 = static_cast<uint32_t>(i0 + k) * kDitherIndex + c.dither;  // of the first element
       if constexpr (k8) {
         uint32_t am = 0, av = 0;  // (v has no sign; a NaN's would leave it the largest)
@@ -287,7 +287,7 @@ __device__ __forceinline__ void pieces(const AdamConst& c, const AdamTensor& t, 
 // Elements first to end of a chunk one by one (a tensor's ragged end, buffers
 // off a 16-byte boundary); with 8-bit states a warp holds a block of 32.
 template <int KIND>
-__device__ __forceinline__ void singles(const AdamConst& c, const AdamTensor& t, int64_t i0, int first,
+__device__ __forceinline__ void singles(const AdamConst& c, float gs, const AdamTensor& t, int64_t i0, int first,
                                         int end) {
   constexpr bool kPBf16 = (KIND & ADAM_P_BF16) != 0, kGBf16 = (KIND & ADAM_G_BF16) != 0;
   constexpr bool kMaster = (KIND & ADAM_MASTER) != 0, k8 = (KIND & ADAM_BITS8) != 0;
@@ -309,7 +309,7 @@ __device__ __forceinline__ void singles(const AdamConst& c, const AdamTensor& t,
         m = static_cast<const float*>(t.m)[i];
         v = static_cast<const float*>(t.v)[i];
       }
-      update(c, t.keep, g, x, m, v);
+      update(c, gs, t.keep, g, x, m, v);
     }
     const uint32_t d = static_cast<uint32_t>(i) * kDitherIndex + c.dither;
     if (k8) {
@@ -342,6 +342,8 @@ __device__ __forceinline__ void singles(const AdamConst& c, const AdamTensor& t,
 
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, (KIND & ADAM_BITS8) ? 4 : 3) k_adamw(const __grid_constant__ AdamTable tab) {
+  // (a kernel of its own with the factor: without one the scale stays a constant)
+  const float gs = (KIND & ADAM_FACTOR) ? __fmul_rn(tab.c.grad_scale, *tab.c.factor) : tab.c.grad_scale;
   for (uint32_t chunk = blockIdx.x; chunk < tab.chunks; chunk += gridDim.x) {
     int lo = 0, hi = tab.n - 1;  // the last tensor whose first chunk is not past this one
     while (lo < hi) {
@@ -353,8 +355,8 @@ __global__ void __launch_bounds__(kThreads, (KIND & ADAM_BITS8) ? 4 : 3) k_adamw
     const int64_t i0 = static_cast<int64_t>(chunk - t.chunk0) * kChunk;
     const int end = static_cast<int>(t.n - i0 < kChunk ? t.n - i0 : kChunk);
     const int whole = t.on16 ? end & ~31 : 0;
-    pieces<KIND>(tab.c, t, i0, whole);
-    if (whole < end) singles<KIND>(tab.c, t, i0, whole, end);
+    pieces<KIND>(tab.c, gs, t, i0, whole);
+    if (whole < end) singles<KIND>(tab.c, gs, t, i0, whole, end);
   }
 }
 
@@ -390,7 +392,9 @@ cudaError_t launch_adamw(AdamTensor* t, int n, int kind, const AdamConst& c,
   // with masters; CTAs that walk over the chunks, 4 to 16 an SM, 1047 to 1078)
   const int64_t grid = chunks < (1u << 30) ? chunks : 1 << 30;
   switch (kind) {
-#define ADAM_CASE(k) case k: return launch_kind<k>(tab, grid, s);
+#define ADAM_CASE(k) \
+  case k: return launch_kind<k>(tab, grid, s); \
+  case (k) | ADAM_FACTOR: return launch_kind<(k) | ADAM_FACTOR>(tab, grid, s);
     ADAM_CASE(0)
     ADAM_CASE(ADAM_P_BF16)
     ADAM_CASE(ADAM_G_BF16)

@@ -42,7 +42,8 @@ const char* kKindNames[K_NUM_KINDS] = {
     "advantages", "convert_bf16", "seq_count",  "block_plan",  "fwd_gemm_lse", "fwd_finish",
     "fwd_reduce", "bwd_coef",     "transpose_w", "zero_rows",  "bwd_dz_gemm",  "bwd_dh_gemm",
     "bwd_dw_gemm", "transpose_h",  "quantize_e4m3", "sample", "norm_fwd", "norm_bwd",
-    "norm_colsum", "adamw"};
+    "norm_colsum", "adamw", "policy_count", "policy_loss", "resnorm_fwd", "resnorm_bwd",
+    "resnorm_join", "grad_norm", "grad_join", "grad_scale"};
 
 }  // namespace
 
@@ -419,9 +420,9 @@ grpo_status loss_fwd_impl(const grpo_problem* problem, const void* H_pol, const 
 grpo_status loss_bwd_impl(const grpo_problem* problem, const void* H_pol, const float* s_pol,
                           const void* W, const float* s_W, const int32_t* ids,
                           const uint8_t* mask, const float* adv, const float* logp_pol,
-                          const float* logp_ref, const float* lse_pol, float grad_loss, void* dH,
-                          float* dW, void* workspace, size_t workspace_bytes,
-                          cudaStream_t stream);
+                          const float* logp_ref, const float* lse_pol, const float* dlogp,
+                          float grad_loss, void* dH, float* dW, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
 
 }  // namespace
 
@@ -621,16 +622,17 @@ grpo_status loss_fwd_impl(const grpo_problem* problem, const void* H_pol, const 
 
 // The backward of every element type; the row scales are used (and
 // non-null) for e4m3 problems only.
+// The row coefficients come from the loss's own inputs, or from dlogp where it is given.
 grpo_status loss_bwd_impl(const grpo_problem* problem, const void* H_pol, const float* s_pol,
                           const void* W, const float* s_W, const int32_t* ids,
                           const uint8_t* mask, const float* adv, const float* logp_pol,
-                          const float* logp_ref, const float* lse_pol, float grad_loss, void* dH,
-                          float* dW, void* workspace, size_t workspace_bytes,
-                          cudaStream_t stream) {
+                          const float* logp_ref, const float* lse_pol, const float* dlogp,
+                          float grad_loss, void* dH, float* dW, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
   grpo_status st = validate_problem(problem);
   if (st != GRPO_OK) return st;
-  if (!H_pol || !W || !ids || !mask || !adv || !logp_pol || !logp_ref || !lse_pol || !dH)
-    return GRPO_ERR_INVALID_ARG;
+  if (!H_pol || !W || !ids || !mask || !lse_pol || !dH) return GRPO_ERR_INVALID_ARG;
+  if (!dlogp && (!adv || !logp_pol || !logp_ref)) return GRPO_ERR_INVALID_ARG;
   if ((dW != nullptr) != (problem->compute_dW != 0)) return GRPO_ERR_INVALID_ARG;
   if (dW && !aligned16(dW)) return GRPO_ERR_UNSUPPORTED;
   if (!isfinite(grad_loss)) return GRPO_ERR_INVALID_ARG;
@@ -705,9 +707,12 @@ grpo_status loss_bwd_impl(const grpo_problem* problem, const void* H_pol, const 
          launch_seq_count(mask, ids, P.B, P.T, P.V, cnt, &ctrl->err, stream));
   LAUNCH(K_BLOCK_PLAN, stream,
          launch_block_plan(mask, P.N, P.nblk_max, blk, inv, &ctrl->nblk, stream));
-  LAUNCH(K_BWD_COEF, stream,
-         launch_bwd_coef(mask, cnt, adv, logp_pol, logp_ref, P.N, P.B, P.T, problem->beta,
-                         grad_loss, problem->token_level, problem->kl_mode, coef, stream));
+  if (dlogp)
+    LAUNCH(K_BWD_COEF, stream, launch_bwd_coef_dlogp(mask, dlogp, P.N, grad_loss, coef, stream));
+  else
+    LAUNCH(K_BWD_COEF, stream,
+           launch_bwd_coef(mask, cnt, adv, logp_pol, logp_ref, P.N, P.B, P.T, problem->beta,
+                           grad_loss, problem->token_level, problem->kl_mode, coef, stream));
   const int w_type = P.f32 ? ELT_F32 : (P.e4m3 ? ELT_E4M3 : ELT_BF16);
   LAUNCH(K_TRANSPOSE_W, stream,
          launch_transpose_w(W, w_type, s_W, P.V, P.d, wt, P.ldv, stream));
@@ -800,7 +805,32 @@ grpo_status grpo_loss_bwd(const grpo_problem* problem, const void* H_pol, const 
   NvtxRange nvtx_range("grpo_loss_bwd");
   if (problem && problem->dtype == GRPO_E4M3) return GRPO_ERR_INVALID_ARG;
   return loss_bwd_impl(problem, H_pol, nullptr, W, nullptr, ids, mask, adv, logp_pol, logp_ref,
-                       lse_pol, grad_loss, dH, dW, workspace, workspace_bytes, stream);
+                       lse_pol, nullptr, grad_loss, dH, dW, workspace, workspace_bytes, stream);
+}
+
+grpo_status grpo_loss_bwd_dlogp(const grpo_problem* problem, const void* H_pol, const void* W,
+                                const int32_t* ids, const uint8_t* mask, const float* dlogp,
+                                const float* lse_pol, float grad_loss, void* dH, float* dW,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  NvtxRange nvtx_range("grpo_loss_bwd_dlogp");
+  if (problem && problem->dtype == GRPO_E4M3) return GRPO_ERR_INVALID_ARG;
+  if (!dlogp) return GRPO_ERR_INVALID_ARG;
+  return loss_bwd_impl(problem, H_pol, nullptr, W, nullptr, ids, mask, nullptr, nullptr, nullptr,
+                       lse_pol, dlogp, grad_loss, dH, dW, workspace, workspace_bytes, stream);
+}
+
+grpo_status grpo_loss_bwd_dlogp_e4m3(const grpo_problem* problem, const uint8_t* H_pol,
+                                     const float* s_pol, const uint8_t* W, const float* s_W,
+                                     const int32_t* ids, const uint8_t* mask, const float* dlogp,
+                                     const float* lse_pol, float grad_loss, void* dH, float* dW,
+                                     void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream) {
+  NvtxRange nvtx_range("grpo_loss_bwd_dlogp_e4m3");
+  if (!problem || problem->dtype != GRPO_E4M3) return GRPO_ERR_INVALID_ARG;
+  if (!s_pol || !s_W || !dlogp) return GRPO_ERR_INVALID_ARG;
+  if (!aligned16(s_W)) return GRPO_ERR_UNSUPPORTED;
+  return loss_bwd_impl(problem, H_pol, s_pol, W, s_W, ids, mask, nullptr, nullptr, nullptr,
+                       lse_pol, dlogp, grad_loss, dH, dW, workspace, workspace_bytes, stream);
 }
 
 grpo_status grpo_loss_bwd_e4m3(const grpo_problem* problem, const uint8_t* H_pol,
@@ -814,7 +844,7 @@ grpo_status grpo_loss_bwd_e4m3(const grpo_problem* problem, const uint8_t* H_pol
   if (!s_pol || !s_W) return GRPO_ERR_INVALID_ARG;
   if (!aligned16(s_W)) return GRPO_ERR_UNSUPPORTED;
   return loss_bwd_impl(problem, H_pol, s_pol, W, s_W, ids, mask, adv, logp_pol, logp_ref,
-                       lse_pol, grad_loss, dH, dW, workspace, workspace_bytes, stream);
+                       lse_pol, nullptr, grad_loss, dH, dW, workspace, workspace_bytes, stream);
 }
 
 grpo_status grpo_quantize_e4m3_rows(const void* x, grpo_dtype x_dtype, int64_t rows,

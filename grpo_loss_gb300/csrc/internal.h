@@ -102,6 +102,14 @@ enum KernelKind : int {
   K_NORM_BWD,
   K_NORM_COLSUM,
   K_ADAMW,
+  K_POLICY_COUNT,
+  K_POLICY_LOSS,
+  K_RESNORM_FWD,
+  K_RESNORM_BWD,
+  K_RESNORM_JOIN,
+  K_GRAD_NORM,
+  K_GRAD_JOIN,
+  K_GRAD_SCALE,
   K_NUM_KINDS
 };
 
@@ -132,6 +140,9 @@ cudaError_t launch_fwd_finish(const int* inv, const uint8_t* mask, const int* cn
 cudaError_t launch_fwd_reduce(const double* partials, int nparts, const int* cnt, int B,
                               float beta, int token_level, float* loss, float* kl_mean,
                               cudaStream_t s);
+// The same from gradients by the log-probabilities: c_n = -grad dlogp_n at valid rows.
+cudaError_t launch_bwd_coef_dlogp(const uint8_t* mask, const float* dlogp, int64_t N, float grad,
+                                  float* coef, cudaStream_t s);
 cudaError_t launch_bwd_coef(const uint8_t* mask, const int* cnt, const float* adv,
                             const float* logp_pol, const float* logp_ref, int64_t N, int B,
                             int T, float beta, float grad, int token_level, int kl_mode,
@@ -218,10 +229,98 @@ struct AdamConst {
   float rsqrt_c2;   // 1 / sqrt(1 - beta2^t)
   float eps, grad_scale;
   uint32_t dither;  // t * 0xC13FA9A9 mod 2^32
+  const float* factor;  // on the device, with ADAM_FACTOR: multiplies grad_scale
 };
-enum AdamKind : int { ADAM_P_BF16 = 1, ADAM_G_BF16 = 2, ADAM_MASTER = 4, ADAM_BITS8 = 8 };
+enum AdamKind : int { ADAM_P_BF16 = 1, ADAM_G_BF16 = 2, ADAM_MASTER = 4, ADAM_BITS8 = 8, ADAM_FACTOR = 16 };
 constexpr int kAdamMaxTensors = 248;  // of one launch (its table is a kernel parameter)
 // `t[0..n)` share `kind`; chunk0 and on16 are filled in here.
 cudaError_t launch_adamw(AdamTensor* t, int n, int kind, const AdamConst& c, cudaStream_t s);
+
+// --------------------------------------------------------------- policy.cu
+struct PolicyArgs {
+  int64_t B, T;
+  int64_t ld_logp, ld_old, ld_ref, ld_adv, ld_mask, ld_dlogp;
+  const float* logp;
+  const float* old;    // may be null (ratio 1)
+  const float* ref;    // may be null (no KL term)
+  const float* adv;    // [B], or [B, T] with token_adv
+  const uint8_t* mask;
+  float* loss;
+  float* stats;        // may be null
+  float* dlogp;        // may be null
+  int token_adv, sequence_ratio;
+  int reduce;          // 0 sequence, 1 token, 2 constant
+  double inv_divisor;
+  float beta;
+  // the bounds of the ratio, and their logs in two floats: 1 + clip_high, 1 - clip_low, dual_clip
+  float r_up, r_down, r_far;
+  float up_hi, up_lo, down_hi, down_lo, far_hi, far_lo;
+  // set by policy_plan: how the tokens are cut, and the workspace's parts
+  int64_t pieces, rows_per_chunk, chunks;
+  int count_ctas;
+  unsigned* ticket;
+  int64_t* cta_count;
+  double* partial;
+  int* seg_count;
+  double* seg_w;
+};
+// Bytes of the workspace; fills in the parts of a.
+size_t policy_plan(PolicyArgs& a, int sms, void* workspace);
+cudaError_t launch_policy_count(const PolicyArgs& a, cudaStream_t s);
+cudaError_t launch_policy_loss(const PolicyArgs& a, cudaStream_t s);
+
+// -------------------------------------------------------- residual_norm.cu
+constexpr int64_t kMaxResNormDim = 32768;
+struct ResNormArgs {
+  int64_t rows, d;
+  int64_t ld_x, ld_res, ld_h, ld_y, ld_gate;
+  int64_t ld_dy, ld_dh, ld_dx, ld_dres, ld_dgate;
+  float eps, scale;
+  int rms, bf16, param_bf16, gate_bf16;
+  int64_t gate_rows;  // rows that share a row of the gate
+  const void* x;
+  const void* residual;
+  const void* weight;
+  const void* bias;
+  const void* post_weight;  // null: no norm behind the block
+  const void* post_bias;
+  const void* gate;         // may be null
+  void* h_out;
+  void* y;
+  float *mean, *rstd, *post_mean, *post_rstd;
+  // backward
+  const void* h;
+  const void* dy;
+  const void* dh;           // may be null
+  void* dx;                 // may be null
+  void* dres;
+  float *dweight, *dbias, *dpost_weight, *dpost_bias;
+  void* dgate;              // float32 of a shared gate, else of the gate's type
+  float* partial;           // [arrays][walkers][d]
+  int at_dw, at_db, at_dpw, at_dpb, at_head, at_tail;  // their places among the arrays
+};
+int resnorm_walkers(const ResNormArgs& a, int sms);  // the most that a backward launch has
+cudaError_t launch_resnorm_fwd(const ResNormArgs& a, int sms, cudaStream_t s);
+// *walkers: how many share the rows out
+cudaError_t launch_resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s);
+cudaError_t launch_resnorm_join(const ResNormArgs& a, int walkers, cudaStream_t s);
+
+// ------------------------------------------------------------ grad_norm.cu
+struct GradTensor {
+  const void* grad;
+  void* out;
+  int64_t n;
+  uint32_t chunk0;  // first work chunk of this tensor
+  int bf16;
+};
+constexpr int kGradMaxTensors = 1000;  // of one launch (its table is a kernel parameter)
+int grad_parts(int sms);               // partial norms that a launch leaves, at most
+// `t[0..n)`, none of them empty; chunk0 is filled in here.
+cudaError_t launch_grad_norm(const GradTensor* t, int n, int inf, int sms, double* partial, int* parts, cudaStream_t s);
+cudaError_t launch_grad_join(const double* partial, int parts, int inf, double max_norm, double eps, float* norm, float* factor,
+                             cudaStream_t s);
+// Joins the first `parts` to one, in their place.
+cudaError_t launch_grad_fold(double* partial, int parts, int inf, cudaStream_t s);
+cudaError_t launch_grad_scale(const GradTensor* t, int n, const float* factor, int sms, cudaStream_t s);
 
 }  // namespace grpo

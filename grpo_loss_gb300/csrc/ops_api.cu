@@ -184,6 +184,7 @@ grpo_status grpo_adamw_step(const grpo_adamw_config* c, const grpo_adamw_tensor*
   for (double v : {c->lr, c->eps})
     if (!isfinite(v) || v < 0.0) return GRPO_ERR_INVALID_ARG;
   if (!isfinite(c->grad_scale)) return GRPO_ERR_INVALID_ARG;
+  if (!aligned_to(c->factor, 4)) return GRPO_ERR_UNSUPPORTED;
   if (c->state_bits != 32 && c->state_bits != 8) return GRPO_ERR_INVALID_ARG;
   const bool eight = c->state_bits == 8;
   // every tensor is checked before the first launch
@@ -218,6 +219,8 @@ grpo_status grpo_adamw_step(const grpo_adamw_config* c, const grpo_adamw_tensor*
   k.eps = c->eps > 0.0 ? fmaxf(static_cast<float>(c->eps), FLT_MIN) : 0.f;
   k.grad_scale = c->grad_scale;
   k.dither = static_cast<uint32_t>(static_cast<uint64_t>(c->step) * 0xC13FA9A9ull);
+  k.factor = c->factor;
+  const int every = (eight ? ADAM_BITS8 : 0) | (k.factor ? ADAM_FACTOR : 0);
 
   // One launch for each set of types that occurs (and each kAdamMaxTensors
   // tensors of it): the kernels are compiled for one set.
@@ -227,7 +230,7 @@ grpo_status grpo_adamw_step(const grpo_adamw_config* c, const grpo_adamw_tensor*
     for (int32_t i = 0; i <= n_tensors; ++i) {
       if (used == kAdamMaxTensors || (i == n_tensors && used > 0)) {
         LAUNCH(K_ADAMW, stream,
-               launch_adamw(table, used, kind | (eight ? ADAM_BITS8 : 0), k, stream));
+               launch_adamw(table, used, kind | every, k, stream));
         used = 0;
       }
       if (i == n_tensors) break;

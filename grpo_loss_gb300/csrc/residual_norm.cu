@@ -1,0 +1,245 @@
+// The norms behind and before a block of a model, with the block's gate and residual
+// scale:  p = post_norm(x) or x,  h = residual + scale gate p,  y = norm(h).
+// Backward, of dy and dh:
+//   g  = dh + norm'(dy)             the gradient of h, and of the residual
+//   q  = scale gate g               that of p;  dgate = sum over its rows of scale g p
+//   dx = post_norm'(q) or q
+// with norm'(v) = r (v w - mean(v w) - k mean(v w k)), k = (h - m) r.
+// A row takes a CTA; what its passes share is in shared memory.
+#include <cuda_bf16.h>
+
+#include "internal.h"
+
+namespace grpo {
+
+namespace {
+
+constexpr int kLong = 512;
+
+__device__ __forceinline__ float at(const void* p, int bf16, int64_t i) {
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+__device__ __forceinline__ void put(void* p, int bf16, int64_t i, float v) {
+  if (bf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<float*>(p)[i] = v;
+}
+
+template <int M>
+__device__ void cta_sums(float (&v)[M]) {
+  __shared__ float part[M][kLong / 32];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+    if ((threadIdx.x & 31) == 0) part[m][threadIdx.x >> 5] = v[m];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    v[m] = 0.f;
+    for (int w = 0; w < kLong / 32; ++w) v[m] += part[m][w];
+  }
+  __syncthreads();
+}
+
+__device__ float gate_of(const ResNormArgs& a, int64_t row, int i) {
+  return a.gate ? a.scale * at(a.gate, a.gate_bf16, row / a.gate_rows * a.ld_gate + i) : a.scale;
+}
+
+__global__ void __launch_bounds__(kLong) k_resnorm_fwd_long(ResNormArgs a) {
+  extern __shared__ float h[];
+  const int d = static_cast<int>(a.d);
+  const float inv_d = 1.f / d;
+  const int64_t row = blockIdx.x;
+  float pm = 0.f, pr = 1.f;
+  if (a.post_weight) {
+    float s[1] = {0.f};
+    if (!a.rms) {
+      for (int i = threadIdx.x; i < d; i += kLong) s[0] += at(a.x, a.bf16, row * a.ld_x + i);
+      cta_sums(s);
+      pm = s[0] * inv_d;
+    }
+    s[0] = 0.f;
+    for (int i = threadIdx.x; i < d; i += kLong) {
+      const float c = at(a.x, a.bf16, row * a.ld_x + i) - pm;
+      s[0] = fmaf(c, c, s[0]);
+    }
+    cta_sums(s);
+    pr = rsqrtf(s[0] * inv_d + a.eps);
+  }
+  float s[1] = {0.f};
+  for (int i = threadIdx.x; i < d; i += kLong) {
+    float p = at(a.x, a.bf16, row * a.ld_x + i);
+    if (a.post_weight) {
+      p = (p - pm) * pr * at(a.post_weight, a.param_bf16, i);
+      if (a.post_bias) p += at(a.post_bias, a.param_bf16, i);
+    }
+    h[i] = fmaf(gate_of(a, row, i), p, at(a.residual, a.bf16, row * a.ld_res + i));
+    put(a.h_out, a.bf16, row * a.ld_h + i, h[i]);
+    s[0] += h[i];
+  }
+  float m = 0.f;
+  if (!a.rms) {
+    cta_sums(s);
+    m = s[0] * inv_d;
+  }
+  s[0] = 0.f;
+  for (int i = threadIdx.x; i < d; i += kLong) s[0] = fmaf(h[i] - m, h[i] - m, s[0]);
+  cta_sums(s);
+  const float r = rsqrtf(s[0] * inv_d + a.eps);
+  for (int i = threadIdx.x; i < d; i += kLong) {
+    float v = (h[i] - m) * r * at(a.weight, a.param_bf16, i);
+    if (a.bias) v += at(a.bias, a.param_bf16, i);
+    put(a.y, a.bf16, row * a.ld_y + i, v);
+  }
+  if (threadIdx.x == 0) {
+    if (a.mean) a.mean[row] = m;
+    if (a.rstd) a.rstd[row] = r;
+    if (a.post_mean) a.post_mean[row] = pm;
+    if (a.post_rstd) a.post_rstd[row] = pr;
+  }
+}
+
+// The walker w of n takes rows [w rows / n, (w + 1) rows / n).
+__device__ __forceinline__ int64_t first_row(int64_t rows, int64_t w, int64_t n) { return w * rows / n; }
+__device__ __forceinline__ int64_t walker_of(int64_t rows, int64_t row, int64_t n) { return ((row + 1) * n - 1) / rows; }
+
+__global__ void __launch_bounds__(kLong) k_resnorm_bwd_long(ResNormArgs a, int walkers) {
+  extern __shared__ float g[];
+  const int d = static_cast<int>(a.d);
+  const float inv_d = 1.f / d;
+  const int64_t from = first_row(a.rows, blockIdx.x, walkers), to = first_row(a.rows, blockIdx.x + 1, walkers);
+  auto part = [&](int which) { return a.partial + (static_cast<int64_t>(which) * walkers + blockIdx.x) * d; };
+  float* const pw = a.dweight ? part(a.at_dw) : nullptr;
+  float* const pb = a.dbias ? part(a.at_db) : nullptr;
+  float* const ppw = a.dpost_weight ? part(a.at_dpw) : nullptr;
+  float* const ppb = a.dpost_bias ? part(a.at_dpb) : nullptr;
+  for (int64_t row = from; row < to; ++row) {
+    const bool first = row == from;
+    const float m = a.rms ? 0.f : a.mean[row], r = a.rstd[row];
+    float s[2] = {0.f, 0.f};
+    for (int i = threadIdx.x; i < d; i += kLong) {
+      const float v = at(a.dy, a.bf16, row * a.ld_dy + i), k = (at(a.h, a.bf16, row * a.ld_h + i) - m) * r;
+      const float vw = v * at(a.weight, a.param_bf16, i);
+      s[0] += vw;
+      s[1] = fmaf(vw, k, s[1]);
+      if (pw) pw[i] = fmaf(v, k, first ? 0.f : pw[i]);
+      if (pb) pb[i] = v + (first ? 0.f : pb[i]);
+    }
+    cta_sums(s);
+    const float c1 = a.rms ? 0.f : s[0] * inv_d, c2 = s[1] * inv_d;
+    for (int i = threadIdx.x; i < d; i += kLong) {
+      const float v = at(a.dy, a.bf16, row * a.ld_dy + i), k = (at(a.h, a.bf16, row * a.ld_h + i) - m) * r;
+      const float dz = r * (v * at(a.weight, a.param_bf16, i) - c1 - k * c2);
+      g[i] = a.dh ? dz + at(a.dh, a.bf16, row * a.ld_dh + i) : dz;
+      put(a.dres, a.bf16, row * a.ld_dres + i, g[i]);
+    }
+    if (!a.dx && !a.dgate && !a.dpost_weight && !a.dpost_bias) continue;
+    const float pm = a.post_weight && !a.rms ? a.post_mean[row] : 0.f, pr = a.post_weight ? a.post_rstd[row] : 1.f;
+    // the rows of a gate that lie in this walker: its first and its last may be shared
+    const int64_t q = a.gate ? row / a.gate_rows : 0, q0 = q * a.gate_rows, q1 = q0 + a.gate_rows;
+    float* dgate = nullptr;
+    if (a.dgate && a.gate_rows > 1)
+      dgate = q0 >= from && q1 <= to ? static_cast<float*>(a.dgate) + q * d : part(q0 <= from ? a.at_head : a.at_tail);
+    const bool first_of_gate = first || row == q0;
+    s[0] = s[1] = 0.f;
+    for (int i = threadIdx.x; i < d; i += kLong) {
+      const float x = a.x ? at(a.x, a.bf16, row * a.ld_x + i) : 0.f;
+      const float k = (x - pm) * pr, w = a.post_weight ? at(a.post_weight, a.param_bf16, i) : 1.f;
+      if (a.dgate) {
+        const float p = a.post_bias ? fmaf(k, w, at(a.post_bias, a.param_bf16, i)) : k * w;
+        const float v = a.scale * g[i] * p;
+        if (a.gate_rows > 1) dgate[i] = v + (first_of_gate ? 0.f : dgate[i]);
+        else put(a.dgate, a.gate_bf16, row * a.ld_dgate + i, v);
+      }
+      const float qv = g[i] * gate_of(a, row, i);
+      g[i] = qv;
+      if (a.post_weight) {
+        s[0] = fmaf(qv, w, s[0]);
+        s[1] = fmaf(qv * w, k, s[1]);
+        if (ppw) ppw[i] = fmaf(qv, k, first ? 0.f : ppw[i]);
+        if (ppb) ppb[i] = qv + (first ? 0.f : ppb[i]);
+      }
+    }
+    if (a.post_weight) {
+      cta_sums(s);
+      s[0] = a.rms ? 0.f : s[0] * inv_d;
+      s[1] *= inv_d;
+    }
+    if (a.dx)
+      for (int i = threadIdx.x; i < d; i += kLong) {
+        float v = g[i];
+        if (a.post_weight) {
+          const float k = (at(a.x, a.bf16, row * a.ld_x + i) - pm) * pr;
+          v = pr * (v * at(a.post_weight, a.param_bf16, i) - s[0] - k * s[1]);
+        }
+        put(a.dx, a.bf16, row * a.ld_dx + i, v);
+      }
+  }
+}
+
+// Joins the walkers' partial sums of a column: one after the other in a fixed order.
+// blockIdx.y: the parameters' sums, then the gates that several walkers share.
+__global__ void __launch_bounds__(1024) k_resnorm_join(ResNormArgs a, int walkers) {
+  __shared__ float s[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane, d = a.d;
+  int which = a.at_head, tail = -1;
+  int64_t w0 = 0, w1 = walkers - 1;
+  float* to;
+  if (static_cast<int>(blockIdx.y) < a.at_head) {
+    which = blockIdx.y;
+    to = which == a.at_dw ? a.dweight : which == a.at_db ? a.dbias : which == a.at_dpw ? a.dpost_weight : a.dpost_bias;
+  } else {
+    const int64_t q = blockIdx.y - a.at_head, q0 = q * a.gate_rows;
+    w0 = walker_of(a.rows, q0, walkers);
+    w1 = walker_of(a.rows, q0 + a.gate_rows - 1, walkers);
+    if (w0 == w1) return;  // written whole
+    if (q0 > first_row(a.rows, w0, walkers)) tail = static_cast<int>(w0);
+    to = static_cast<float*>(a.dgate) + q * d;
+  }
+  float sum = 0.f;
+  if (col < d)
+    for (int64_t w = w0 + warp; w <= w1; w += 32)
+      sum += a.partial[(static_cast<int64_t>(w == tail ? a.at_tail : which) * walkers + w) * d + col];
+  s[warp][lane] = sum;
+  __syncthreads();
+  sum = s[lane][warp];
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+  if (lane == 0 && at < d) to[at] = sum;
+}
+
+cudaError_t allow_row(const void* kernel, int64_t d) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(d * 4));
+}
+
+}  // namespace
+
+int resnorm_walkers(const ResNormArgs& a, int sms) {
+  const int64_t most = 4ll * sms;
+  return static_cast<int>(a.rows < most ? a.rows : most);
+}
+
+cudaError_t launch_resnorm_fwd(const ResNormArgs& a, int sms, cudaStream_t s) {
+  const cudaError_t e = allow_row(reinterpret_cast<const void*>(k_resnorm_fwd_long), kMaxResNormDim);
+  if (e != cudaSuccess) return e;
+  k_resnorm_fwd_long<<<static_cast<unsigned>(a.rows), kLong, a.d * 4, s>>>(a);
+  return cudaGetLastError();
+}
+cudaError_t launch_resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
+  const cudaError_t e = allow_row(reinterpret_cast<const void*>(k_resnorm_bwd_long), kMaxResNormDim);
+  if (e != cudaSuccess) return e;
+  *walkers = resnorm_walkers(a, sms);
+  k_resnorm_bwd_long<<<*walkers, kLong, a.d * 4, s>>>(a, *walkers);
+  return cudaGetLastError();
+}
+cudaError_t launch_resnorm_join(const ResNormArgs& a, int walkers, cudaStream_t s) {
+  const int64_t gates = a.dgate && a.gate_rows > 1 ? a.rows / a.gate_rows : 0;
+  const dim3 grid(static_cast<unsigned>((a.d + 31) / 32), static_cast<unsigned>(a.at_head + gates));
+  k_resnorm_join<<<grid, 1024, 0, s>>>(a, walkers);
+  return cudaGetLastError();
+}
+
+}  // namespace grpo

@@ -336,6 +336,15 @@ __global__ void k_bwd_coef(const uint8_t* __restrict__ mask, const int* __restri
   }
 }
 
+// The same where the objective is formed elsewhere: its gradient by every token's q is
+// given, and masked tokens' values are not looked at.
+__global__ void k_bwd_coef_dlogp(const uint8_t* __restrict__ mask, const float* __restrict__ dlogp,
+                                 int64_t N, float grad, float* __restrict__ coef) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t n = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; n < N; n += stride)
+    coef[n] = mask[n] ? -(grad * dlogp[n]) : 0.f;
+}
+
 // ------------------------------------------------------------- transpose
 // One element of a matrix of element type ELT as float: bf16 and float32 as
 // stored; e4m3 decoded exactly and multiplied by its row's scale.
@@ -639,6 +648,13 @@ cudaError_t launch_bwd_coef(const uint8_t* mask, const int* cnt, const float* ad
   const int blocks = static_cast<int>(std::min<int64_t>((N + 255) / 256, 4096));
   k_bwd_coef<<<blocks, 256, 0, s>>>(mask, cnt, adv, logp_pol, logp_ref, N, B, T, beta, grad,
                                     token_level, kl_mode, coef);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_bwd_coef_dlogp(const uint8_t* mask, const float* dlogp, int64_t N, float grad,
+                                  float* coef, cudaStream_t s) {
+  const int blocks = static_cast<int>(std::min<int64_t>((N + 255) / 256, 4096));
+  k_bwd_coef_dlogp<<<blocks, 256, 0, s>>>(mask, dlogp, N, grad, coef);
   return cudaGetLastError();
 }
 

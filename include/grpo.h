@@ -465,11 +465,194 @@ typedef struct grpo_adamw_config {
   float grad_scale;       /* multiplies every gradient (a clip factor, 1 / loss scale) */
   int32_t state_bits;     /* 32 or 8 */
   int64_t step;           /* 1 for the first step */
+  const float *factor;    /* device float32 [1], or NULL: multiplies grad_scale (the clip
+                             factor of grpo_grad_norm, which the host need not wait for) */
 } grpo_adamw_config;
 
 grpo_status grpo_adamw_step(const grpo_adamw_config *config, const grpo_adamw_tensor *tensors,
                             const grpo_adamw_tensor *out, int32_t n_tensors,
                             cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The operators of an update beyond a rollout's first. The policy has then moved away
+ * from the one that drew the tokens: the objective takes the ratio of the two
+ * (grpo_policy_loss), its gradient by the log-probabilities goes through the head
+ * (grpo_loss_bwd_dlogp) and through the norms of the model's blocks
+ * (grpo_residual_norm_*), and all gradients are clipped by their norm
+ * (grpo_grad_norm, whose factor grpo_adamw_step takes, or grpo_clip_grad_norm).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Clipped policy loss with a KL term, and its gradient by the log-probabilities, over
+ * num_seqs = B sequences of seq_len = T tokens. At a valid token (mask != 0) with the
+ * policy's log-probability q, the drawing policy's o, the reference's p and the
+ * advantage A:
+ *   w = q - o                 (ratio = 0), or the mean of q - o over the sequence's valid
+ *                             tokens (ratio = 1);  w = 0 without logp_old
+ *   r = exp(w)
+ *   l = -A min(r, 1 + clip_high)                        for A > 0
+ *       -A max(min(r, dual_clip), 1 - clip_low)         for A < 0;  0 for A = 0
+ *   x = p - q,  k = exp(x) - 1 - x                      (0 without logp_ref)
+ *   loss  = sum c (l + beta k)
+ *   dlogp = c (-A r [r within the bound that applies] - beta (exp(x) - 1))
+ * and 0 at masked tokens, of which nothing but the mask is read. The gradient of a mean
+ * ratio reaches a sequence's tokens alike, so that dlogp has the same form; where a token
+ * is on a bound, the gradient flows. A token's side of a bound is decided by the exact
+ * difference q - o and the bound's log to 48 bits. The weight c is
+ *   reduce = 0   1 / (B cnt_b), cnt_b the valid tokens of its sequence
+ *   reduce = 1   1 / (all valid tokens)
+ *   reduce = 2   1 / divisor
+ * clip_low, clip_high: >= 0, infinite for no bound. dual_clip: 0 (off) or >= 1.
+ *   logp, logp_old, logp_ref  float32 [B, T]; logp_old and logp_ref may be NULL
+ *   adv    float32 [B], or [B, T] with token_adv
+ *   mask   uint8 [B, T]
+ *   loss   float32 [1], written
+ *   stats  float32 [4], written, may be NULL: the means over valid tokens of k, of whether
+ *          the lower and the upper bound took the gradient away, and of r
+ *   dlogp  float32 [B, T], written, may be NULL
+ * Row strides ld_* in elements. dlogp may be logp, logp_old, logp_ref or adv [B, T] (same
+ * stride). Sums are float64 in a fixed order: results do not vary between calls. B = 0 or T = 0: loss and stats are 0. INVALID_ARG for null pointers,
+ * sizes below 0, a stride below T, bounds, beta or divisor outside the above or NaN;
+ * UNSUPPORTED for B or T of 2^31 or more, B T above 2^40, and pointers off their element's
+ * alignment.
+ */
+typedef struct grpo_policy_problem {
+  int64_t num_seqs, seq_len;
+  int64_t ld_logp, ld_old, ld_ref, ld_adv, ld_mask, ld_dlogp; /* 0 = seq_len */
+  double clip_low, clip_high, dual_clip;
+  double beta;       /* finite; may be 0 beside a logp_ref (k is then a statistic) */
+  double divisor;    /* > 0 and finite with reduce = 2 */
+  int32_t ratio;     /* 0 each token's, 1 its sequence's */
+  int32_t reduce;    /* 0 sequence, 1 token, 2 constant */
+  int32_t token_adv;
+} grpo_policy_problem;
+
+grpo_status grpo_policy_loss_workspace_size(const grpo_policy_problem *problem, size_t *bytes);
+grpo_status grpo_policy_loss(const grpo_policy_problem *problem, const float *logp,
+                             const float *logp_old, const float *logp_ref, const float *adv,
+                             const uint8_t *mask, float *loss, float *stats, float *dlogp,
+                             void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * grpo_loss_bwd and grpo_loss_bwd_e4m3 for an objective that is formed elsewhere: dlogp
+ * (float32 [N], read at valid rows) is its gradient by logp_pol, and the logit gradient
+ * is dZ_n = -grad_loss dlogp_n (softmax(z_n) - onehot(ids_n)). beta, kl_mode, token_level
+ * and group_size of the problem are not used. Every other argument as in those.
+ */
+grpo_status grpo_loss_bwd_dlogp(const grpo_problem *problem, const void *H_pol, const void *W,
+                                const int32_t *ids, const uint8_t *mask, const float *dlogp,
+                                const float *lse_pol, float grad_loss, void *dH, float *dW,
+                                void *workspace, size_t workspace_bytes, cudaStream_t stream);
+grpo_status grpo_loss_bwd_dlogp_e4m3(const grpo_problem *problem, const uint8_t *H_pol,
+                                     const float *s_pol, const uint8_t *W, const float *s_W,
+                                     const int32_t *ids, const uint8_t *mask, const float *dlogp,
+                                     const float *lse_pol, float grad_loss, void *dH, float *dW,
+                                     void *workspace, size_t workspace_bytes,
+                                     cudaStream_t stream);
+
+/*
+ * The norms behind and before a block, with its gate and its residual scale. x is the
+ * block's output, residual the stream beside it, all [rows, d]:
+ *   p = post_norm(x) with post_weight (and post_bias), else x
+ *   h = residual + scale * gate * p        (no gate: 1)
+ *   y = norm(h) with weight and bias       (both norms as in grpo_layernorm_fwd: layer
+ *                                           norm, or RMS norm with rms = 1)
+ * y and the statistics are those of h before its rounding to dtype. The gate has a row
+ * for every gate_rows rows (gate_rows = rows: one for each channel; 1: one for each
+ * element); gate_rows divides rows.
+ *
+ * Backward, from dy and dh (the gradient of h from where else the stream goes; may be
+ * NULL) and h as it was stored:
+ *   g = dh + norm'(dy)                     = dresidual
+ *   dgate = sum over the rows that share it of scale * g * p
+ *   dx = post_norm'(scale * gate * g), or scale * gate * g
+ * and the column sums of both norms' parameters as in grpo_layernorm_bwd. Sums are
+ * float32 or wider, in a fixed order.
+ *   x, residual, h, y, dy, dh, dx, dresidual  [rows, d] of dtype (GRPO_F32 or GRPO_BF16)
+ *   weight, bias, post_weight, post_bias      [d] of param_dtype; all but weight may be
+ *                                             NULL; no bias with rms, no post_bias
+ *                                             without post_weight
+ *   gate    [rows / gate_rows, d] of gate_dtype, may be NULL
+ *   mean, rstd, post_mean, post_rstd          float32 [rows]; written by the forward,
+ *           where each may be NULL, and read by the backward (mean and post_mean not with
+ *           rms, post_* not without post_weight)
+ *   dweight, dbias, dpost_weight, dpost_bias  float32 [d], written, each may be NULL, and
+ *           must be without the parameter's norm (dbias and dpost_bias: with rms)
+ *   dgate   written, may be NULL: float32 [rows / gate_rows, d] contiguous, or with
+ *           gate_rows = 1 of gate_dtype with row stride ld_dgate
+ *   dx      may be NULL where it is not needed (it is dresidual when there is no gate and
+ *           no post_weight, and scale = 1); x may be NULL when neither gate nor post_weight
+ *           is there
+ * h may be residual or x, y may be residual or x, and not each other; dresidual may be dy,
+ * dh or h; dx may be dy, dh, h or x, and not dresidual (same strides). The backward's
+ * workspace (grpo_residual_norm_workspace_size, for the current device) holds partial
+ * column sums; it may be NULL when there are none to take. rows = 0 writes zeros to the
+ * column sums. INVALID_ARG for null pointers, rows < 0, d < 1, a stride below d, a gate_rows
+ * that does not divide rows, eps that is negative or not finite, a scale that is not finite,
+ * another dtype; UNSUPPORTED for d > 32768, rows of 2^31 or more and pointers off their
+ * element's alignment.
+ */
+typedef struct grpo_residual_norm_problem {
+  int64_t rows, d;
+  int64_t ld_x, ld_residual, ld_h, ld_y, ld_gate;       /* row strides in elements; 0 = d */
+  int64_t ld_dy, ld_dh, ld_dx, ld_dresidual, ld_dgate;
+  int64_t gate_rows; /* not looked at without a gate */
+  float eps, scale;
+  int32_t rms;
+  grpo_dtype dtype, param_dtype, gate_dtype;
+} grpo_residual_norm_problem;
+
+grpo_status grpo_residual_norm_workspace_size(const grpo_residual_norm_problem *problem,
+                                              size_t *bwd_bytes);
+grpo_status grpo_residual_norm_fwd(const grpo_residual_norm_problem *problem, const void *x,
+                                   const void *residual, const void *weight, const void *bias,
+                                   const void *post_weight, const void *post_bias,
+                                   const void *gate, void *h, void *y, float *mean, float *rstd,
+                                   float *post_mean, float *post_rstd, cudaStream_t stream);
+grpo_status grpo_residual_norm_bwd(const grpo_residual_norm_problem *problem, const void *dy,
+                                   const void *dh, const void *h, const void *weight,
+                                   const float *mean, const float *rstd, const void *x,
+                                   const void *post_weight, const void *post_bias,
+                                   const float *post_mean, const float *post_rstd,
+                                   const void *gate, void *dx, void *dresidual, float *dweight,
+                                   float *dbias, float *dpost_weight, float *dpost_bias,
+                                   void *dgate, void *workspace, size_t workspace_bytes,
+                                   cudaStream_t stream);
+
+/*
+ * The norm of n_tensors gradients taken as one vector, and clipping by it:
+ *   norm   = sqrt(sum g^2) (norm_type = 2) or max |g| (norm_type = 0: infinity)
+ *   factor = min(1, max_norm / (norm + eps)), 1 for an infinite max_norm
+ *   out    = g * factor, rounded once (grpo_clip_grad_norm; out may be grad)
+ * An infinity makes the norm infinite, a NaN makes it and the factor NaN. Squares neither
+ * overflow nor underflow; sums run in a fixed order, so that the norm does not vary
+ * between calls. Where factor is 1, tensors that are their own out are not written.
+ * `tensors` is host memory, read before the call returns. Tensors with n = 0 are skipped;
+ * no tensor at all has norm 0. An out must not overlap another tensor's grad or out, nor
+ * its own grad except as a whole.
+ *   norm, factor  device float32 [1], written; factor may be NULL
+ * The workspace (grpo_grad_norm_workspace_size, for the current device) holds partial sums.
+ * INVALID_ARG for null pointers, n < 0, a max_norm or eps that is negative or NaN, an eps
+ * that is infinite, another norm_type or dtype; UNSUPPORTED for pointers off their element's
+ * alignment.
+ */
+typedef struct grpo_grad_tensor {
+  int64_t n;
+  const void *grad; /* [n] of dtype */
+  void *out;        /* [n] of dtype; not looked at by grpo_grad_norm */
+  grpo_dtype dtype; /* GRPO_F32 or GRPO_BF16 */
+} grpo_grad_tensor;
+
+grpo_status grpo_grad_norm_workspace_size(size_t *bytes);
+grpo_status grpo_grad_norm(const grpo_grad_tensor *tensors, int32_t n_tensors, int32_t norm_type,
+                           double max_norm, double eps, float *norm, float *factor,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream);
+grpo_status grpo_clip_grad_norm(const grpo_grad_tensor *tensors, int32_t n_tensors,
+                                int32_t norm_type, double max_norm, double eps, float *norm,
+                                float *factor, void *workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
 
 /*
  * Synchronises `stream`, reads and clears the error word of a workspace
