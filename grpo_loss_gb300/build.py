@@ -21,8 +21,10 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgrpo_gb300.so")
 SOURCES = ["gemm_tc.cu", "rows.cu", "grpo_api.cu", "noalloc.cu", "sample.cu", "norm.cu", "adamw.cu",
-           "policy.cu", "residual_norm.cu", "grad_norm.cu", "ops_api.cu", "update_api.cu"]
-HEADERS = ["ptx.cuh", "f32x2.cuh", "internal.h", "api_common.h"]
+           "policy.cu", "residual_norm.cu", "residual_norm_bwd_f32.cu", "residual_norm_bwd_f32_post.cu",
+           "residual_norm_bwd_bf16.cu", "residual_norm_bwd_bf16_post.cu", "grad_norm.cu", "ops_api.cu",
+           "update_api.cu"]
+HEADERS = ["ptx.cuh", "f32x2.cuh", "pieces.cuh", "residual_norm_bwd.cuh", "internal.h", "api_common.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "-I" + os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]

@@ -5,10 +5,14 @@
 //   q  = scale gate g               that of p;  dgate = sum over its rows of scale g p
 //   dx = post_norm'(q) or q
 // with norm'(v) = r (v w - mean(v w) - k mean(v w k)), k = (h - m) r.
-// A row takes a CTA; what its passes share is in shared memory.
+// Bound by memory: the forward reads x and the residual and writes h and y, the backward
+// (residual_norm_bwd.cuh) reads dy, dh, h and x and writes both gradients, each once. Here
+// stand the forward, what takes rows that do not come in whole 16-byte pieces or are too
+// long for them (a CTA a row, what its passes share in shared memory), and the join of
+// the walkers' column sums.
 #include <cuda_bf16.h>
 
-#include "internal.h"
+#include "residual_norm_bwd.cuh"
 
 namespace grpo {
 
@@ -44,6 +48,120 @@ __device__ void cta_sums(float (&v)[M]) {
 
 __device__ float gate_of(const ResNormArgs& a, int64_t row, int i) {
   return a.gate ? a.scale * at(a.gate, a.gate_bf16, row / a.gate_rows * a.ld_gate + i) : a.scale;
+}
+
+// A group of G threads takes a row, R rows a CTA; each thread holds NV pieces of N values
+// of it, in registers from the loads to y.
+template <typename T, int N, int NV, int G, int R, bool POST>
+__global__ void __launch_bounds__(G * R) k_resnorm_fwd(ResNormArgs a) {
+  __shared__ float part[2 * 128];
+  const int tid = threadIdx.x % G, d = static_cast<int>(a.d);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
+  const bool live = row < a.rows;  // every thread takes part in the barriers
+  const int64_t from = live ? row : 0;
+  const T* x = static_cast<const T*>(a.x) + from * a.ld_x;
+  const T* res = static_cast<const T*>(a.residual) + from * a.ld_res;
+  auto column = [&](int k) { return (k * G + tid) * N; };
+  Piece<T, N> vx[NV], vr[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (column(k) < d) {
+      vx[k] = load_piece<T, N>(x + column(k));
+      vr[k] = load_piece<T, N>(res + column(k));
+    }
+  const float inv_d = 1.f / d;
+  float pm = 0.f, pr = 1.f;
+  if constexpr (POST) {
+    if (!a.rms) {
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (column(k) < d)
+#pragma unroll
+          for (int e = 0; e < N; ++e) s += vx[k].get(e);
+      pm = group_sum<G>(s, part, 0) * inv_d;
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (column(k) < d)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float c = vx[k].get(e) - pm;
+          q = fmaf(c, c, q);
+        }
+    pr = rsqrtf(group_sum<G>(q, part, 1) * inv_d + a.eps);
+  }
+  float h[NV][N];
+  float s = 0.f;
+  const int64_t gate_at = a.gate ? from / a.gate_rows * a.ld_gate : 0;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (column(k) < d) {
+      float p[N], w[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) p[e] = vx[k].get(e);
+      if constexpr (POST) {
+        load_params<N>(a.post_weight, a.param_bf16, column(k), w);
+#pragma unroll
+        for (int e = 0; e < N; ++e) p[e] = (p[e] - pm) * pr * w[e];
+        if (a.post_bias) {
+          load_params<N>(a.post_bias, a.param_bf16, column(k), w);
+#pragma unroll
+          for (int e = 0; e < N; ++e) p[e] += w[e];
+        }
+      }
+      if (a.gate) {
+        const char* g = static_cast<const char*>(a.gate) + gate_at * (a.gate_bf16 ? 2 : 4);
+        load_params<N>(g, a.gate_bf16, column(k), w);
+#pragma unroll
+        for (int e = 0; e < N; ++e) p[e] *= w[e];
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        h[k][e] = fmaf(a.scale, p[e], vr[k].get(e));
+        s += h[k][e];
+      }
+      Piece<T, N> out;
+      out.set(h[k]);
+      if (live) store_piece<T, N>(static_cast<T*>(a.h_out) + row * a.ld_h + column(k), out);
+    }
+  float m = 0.f;
+  if (!a.rms) m = group_sum<G>(s, part, 0) * inv_d;
+  float q = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (column(k) < d)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float c = h[k][e] - m;
+        q = fmaf(c, c, q);
+      }
+  // (a slot is written again behind another slot's barrier)
+  const float r = rsqrtf(group_sum<G>(q, part, POST && a.rms ? 0 : 1) * inv_d + a.eps);
+  if (!live) return;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (column(k) < d) {
+      float w[N];
+      load_params<N>(a.weight, a.param_bf16, column(k), w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) h[k][e] = (h[k][e] - m) * r * w[e];
+      if (a.bias) {
+        load_params<N>(a.bias, a.param_bf16, column(k), w);
+#pragma unroll
+        for (int e = 0; e < N; ++e) h[k][e] += w[e];
+      }
+      Piece<T, N> out;
+      out.set(h[k]);
+      store_piece<T, N>(static_cast<T*>(a.y) + row * a.ld_y + column(k), out);
+    }
+  if (tid == 0) {
+    if (a.mean) a.mean[row] = m;
+    if (a.rstd) a.rstd[row] = r;
+    if (a.post_mean) a.post_mean[row] = pm;
+    if (a.post_rstd) a.post_rstd[row] = pr;
+  }
 }
 
 __global__ void __launch_bounds__(kLong) k_resnorm_fwd_long(ResNormArgs a) {
@@ -99,10 +217,6 @@ __global__ void __launch_bounds__(kLong) k_resnorm_fwd_long(ResNormArgs a) {
     if (a.post_rstd) a.post_rstd[row] = pr;
   }
 }
-
-// The walker w of n takes rows [w rows / n, (w + 1) rows / n).
-__device__ __forceinline__ int64_t first_row(int64_t rows, int64_t w, int64_t n) { return w * rows / n; }
-__device__ __forceinline__ int64_t walker_of(int64_t rows, int64_t row, int64_t n) { return ((row + 1) * n - 1) / rows; }
 
 __global__ void __launch_bounds__(kLong) k_resnorm_bwd_long(ResNormArgs a, int walkers) {
   extern __shared__ float g[];
@@ -211,6 +325,55 @@ __global__ void __launch_bounds__(1024) k_resnorm_join(ResNormArgs a, int walker
   if (lane == 0 && at < d) to[at] = sum;
 }
 
+// Whether every row of every operand, and the parameters, are on 16-byte boundaries and
+// the rows whole pieces.
+bool whole(const ResNormArgs& a, bool fwd) {
+  const int64_t es = a.bf16 ? 2 : 4, gs = a.gate_bf16 ? 2 : 4;
+  uintptr_t all = static_cast<uintptr_t>(a.d * es);
+  auto rows = [&](const void* p, int64_t ld, int64_t size) {
+    if (p) all |= reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * size);
+  };
+  rows(a.x, a.ld_x, es);
+  rows(a.gate, a.ld_gate, gs);
+  if (fwd) {
+    rows(a.residual, a.ld_res, es);
+    rows(a.h_out, a.ld_h, es);
+    rows(a.y, a.ld_y, es);
+  } else {
+    rows(a.h, a.ld_h, es);
+    rows(a.dy, a.ld_dy, es);
+    rows(a.dh, a.ld_dh, es);
+    rows(a.dx, a.ld_dx, es);
+    rows(a.dres, a.ld_dres, es);
+    if (a.gate_rows == 1) rows(a.dgate, a.ld_dgate, gs);
+  }
+  for (const void* p : {a.weight, a.bias, a.post_weight, a.post_bias}) rows(p, 0, 0);
+  return all % 16 == 0;
+}
+
+template <typename T, int N, int NV, int G, int R>
+cudaError_t fwd(const ResNormArgs& a, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>((a.rows + R - 1) / R);
+  if (a.post_weight) k_resnorm_fwd<T, N, NV, G, R, true><<<grid, G * R, 0, s>>>(a);
+  else k_resnorm_fwd<T, N, NV, G, R, false><<<grid, G * R, 0, s>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, int N>
+cudaError_t fwd_n(const ResNormArgs& a, cudaStream_t s) {
+  const int64_t pieces = (a.d + N - 1) / N;
+  if (N > 1 && pieces <= 8) return fwd<T, N, 1, 8, 32>(a, s);
+  if (N > 1 && pieces <= 16) return fwd<T, N, 1, 16, 16>(a, s);
+  if (pieces <= 32) return fwd<T, N, 1, 32, 8>(a, s);
+  if (pieces <= 64) return fwd<T, N, 2, 32, 4>(a, s);
+  if (pieces <= 128) return fwd<T, N, 2, 64, 2>(a, s);
+  if (pieces <= 256) return fwd<T, N, 2, 128, 1>(a, s);
+  if (pieces <= 512) return fwd<T, N, 2, 256, 1>(a, s);
+  if (pieces <= 1024) return fwd<T, N, 2, 512, 1>(a, s);
+  if (pieces <= 2048) return fwd<T, N, 4, 512, 1>(a, s);
+  if (pieces <= 4096) return fwd<T, N, 4, 1024, 1>(a, s);
+  return cudaErrorNotSupported;
+}
+
 cudaError_t allow_row(const void* kernel, int64_t d) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(d * 4));
 }
@@ -218,20 +381,33 @@ cudaError_t allow_row(const void* kernel, int64_t d) {
 }  // namespace
 
 int resnorm_walkers(const ResNormArgs& a, int sms) {
-  const int64_t most = 4ll * sms;
-  return static_cast<int>(a.rows < most ? a.rows : most);
+  // A bound that does not depend on addresses (the workspace is sized before they are
+  // known): up to 8 walkers a CTA, 32 an SM for short rows and 8 for others.
+  const int64_t most = 8ll * sms * (a.d <= 512 ? 4 : 1), need = (a.rows + 7) / 8 * 8;
+  return static_cast<int>(need < most ? need : most);
 }
 
 cudaError_t launch_resnorm_fwd(const ResNormArgs& a, int sms, cudaStream_t s) {
-  const cudaError_t e = allow_row(reinterpret_cast<const void*>(k_resnorm_fwd_long), kMaxResNormDim);
+  const bool pieces = whole(a, true);
+  cudaError_t e = a.bf16 ? (pieces ? fwd_n<__nv_bfloat16, 8>(a, s) : fwd_n<__nv_bfloat16, 1>(a, s))
+                         : (pieces ? fwd_n<float, 4>(a, s) : fwd_n<float, 1>(a, s));
+  if (e != cudaErrorNotSupported) return e;
+  e = allow_row(reinterpret_cast<const void*>(k_resnorm_fwd_long), kMaxResNormDim);
   if (e != cudaSuccess) return e;
   k_resnorm_fwd_long<<<static_cast<unsigned>(a.rows), kLong, a.d * 4, s>>>(a);
   return cudaGetLastError();
 }
 cudaError_t launch_resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
-  const cudaError_t e = allow_row(reinterpret_cast<const void*>(k_resnorm_bwd_long), kMaxResNormDim);
+  cudaError_t e = cudaErrorNotSupported;
+  if (whole(a, false) && !(a.gate && a.gate_rows == 1 && a.gate_bf16 != a.bf16)) {
+    if (a.bf16) e = a.post_weight ? resnorm_bwd_bf16_post(a, sms, walkers, s) : resnorm_bwd_bf16(a, sms, walkers, s);
+    else e = a.post_weight ? resnorm_bwd_f32_post(a, sms, walkers, s) : resnorm_bwd_f32(a, sms, walkers, s);
+  }
+  if (e != cudaErrorNotSupported) return e;
+  e = allow_row(reinterpret_cast<const void*>(k_resnorm_bwd_long), kMaxResNormDim);
   if (e != cudaSuccess) return e;
-  *walkers = resnorm_walkers(a, sms);
+  const int64_t most = 2ll * sms;
+  *walkers = static_cast<int>(a.rows < most ? a.rows : most);
   k_resnorm_bwd_long<<<*walkers, kLong, a.d * 4, s>>>(a, *walkers);
   return cudaGetLastError();
 }

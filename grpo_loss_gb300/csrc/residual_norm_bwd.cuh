@@ -1,0 +1,416 @@
+// Backward of the norms around a block, rows in whole pieces. With hat = (h - m) r,
+// e = dh + r dy w, k = (x - pm) pr and a = scale gate pw,
+//   g  = e - r (c1 + hat c2),   c1 = mean(dy w),  c2 = mean(dy w hat)
+//   dx = pr (a g - mean(a g) - k mean(a g k)),
+// where the two means over a g are sums over e less c1 and c2 times sums that need neither,
+//   sum a g   = sum a e   - r c1 sum a   - r c2 sum a hat
+//   sum a g k = sum a e k - r c1 sum a k - r c2 sum a hat k,
+// so that all sums of a row (8, or 3 of RMS norms) are taken in one pass and joined once.
+#pragma once
+
+#include <atomic>
+
+#include "f32x2.cuh"
+#include "internal.h"
+#include "pieces.cuh"
+
+namespace grpo {
+
+// The walker w of n takes rows [w rows / n, (w + 1) rows / n).
+__device__ __forceinline__ int64_t first_row(int64_t rows, int64_t w, int64_t n) { return w * rows / n; }
+__device__ __forceinline__ int64_t walker_of(int64_t rows, int64_t row, int64_t n) { return ((row + 1) * n - 1) / rows; }
+
+enum : int { GATE_NONE, GATE_SHARED, GATE_ROWS };
+constexpr int kResNormRing = 224 * 1024;  // of shared memory, beside the sums
+
+// CTAs of a kernel that an SM holds, asked once a device; -1 where that fails.
+inline int resident_ctas(const void* kernel, int threads, int smem, std::atomic<uint64_t>& configured, std::atomic<int>& per_sm,
+                         cudaError_t* e) {
+  int dev = 0;
+  *e = cudaGetDevice(&dev);
+  if (*e != cudaSuccess) return -1;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    int n = 0;
+    if (*e == cudaSuccess) *e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+    if (*e != cudaSuccess) return -1;
+    per_sm.store(n < 1 ? 1 : n);
+    configured.fetch_or(bit);
+  }
+  return per_sm.load();
+}
+
+// A group of G threads is a walker, R of them a CTA; each thread holds NV pieces of N
+// columns: their values of a row, and their column sums. The next row's pieces are on
+// their way into shared memory meanwhile, whence they are read twice, for the sums and for
+// the outputs. A thread reads back what it copied itself.
+// The gate's sums are e1 = sum scale g k and e0 = sum scale g over the rows that share it,
+// of which dgate = pw e1 + pb e0, and gate e1 and gate e0 are these rows' parts of the post
+// norm's dweight and dbias: taken when the gate changes, so that a row adds to two sums and
+// not to three.
+template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE>
+__global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walkers) {
+  constexpr int B = N * static_cast<int>(sizeof(T)), H = (N + 1) / 2;
+  constexpr bool INNER = POST || GATE != GATE_NONE;
+  constexpr int ARRAYS = 3 + INNER + (GATE == GATE_ROWS);  // dy, h, dh, x, gate
+  constexpr int SUMS = POST ? (RMS ? 4 : 8) : 2;
+  using V = Piece<T, N>;
+  extern __shared__ __align__(16) unsigned char ring_raw[];
+  __shared__ float part[2 * (SUMS < 4 ? 128 : 32 * SUMS)];
+  V* const ring = reinterpret_cast<V*>(ring_raw) + threadIdx.x;  // [2][ARRAYS][NV][threads]
+  const int tid = threadIdx.x % G, d = static_cast<int>(a.d);
+  const int64_t walker = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
+  const int64_t from = walker < walkers ? first_row(a.rows, walker, walkers) : 0;
+  const int mine = walker < walkers ? static_cast<int>(first_row(a.rows, walker + 1, walkers) - from) : 0;
+  // every group of a CTA makes the same number of turns: barriers are the CTA's
+  const int turns = static_cast<int>((a.rows + walkers - 1) / walkers);
+
+  uint64_t w[NV][H], f[NV][H], dw[NV][H], db[NV][H], e1[NV][H], e0[NV][H];  // f: a, or scale gate
+  auto load_pairs = [&](const void* p, int bf16, int64_t at, uint64_t (&v)[H]) {
+    float u[2 * H] = {};
+    if (bf16) load_params<N>(static_cast<const __nv_bfloat16*>(p) + at, 1, 0, u);
+    else load_params<N>(static_cast<const float*>(p) + at, 0, 0, u);
+#pragma unroll
+    for (int e = 0; e < H; ++e) v[e] = pair_of(u[2 * e], u[2 * e + 1]);
+  };
+  auto column = [&](int k) { return (k * G + tid) * N; };
+  const uint64_t zero = pair_of(0.f, 0.f), scale2 = pair_of(a.scale);
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+#pragma unroll
+    for (int e = 0; e < H; ++e) {
+      w[k][e] = dw[k][e] = db[k][e] = e1[k][e] = e0[k][e] = zero;
+      f[k][e] = scale2;
+    }
+    if (column(k) < d) {
+      load_pairs(a.weight, a.param_bf16, column(k), w[k]);
+      if constexpr (POST && GATE != GATE_SHARED) {
+        uint64_t pw[H];
+        load_pairs(a.post_weight, a.param_bf16, column(k), pw);
+#pragma unroll
+        for (int e = 0; e < H; ++e) f[k][e] = mul2(pw[e], scale2);
+      }
+    }
+  }
+
+  auto slot_of = [&](int half, int which, int k) -> V& { return ring[((half * ARRAYS + which) * NV + k) * (G * R)]; };
+  auto fetch = [&](int n, int half) {
+    if (n < mine) {
+      const int64_t row = from + n;
+      auto copy = [&](int which, const void* p, int64_t ld) {
+        const T* q = static_cast<const T*>(p) + row * ld;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          if (column(k) < d) {
+            if constexpr (B >= 4) copy_async<B>(&slot_of(half, which, k), q + column(k));
+            else slot_of(half, which, k) = load_piece<T, N>(q + column(k));
+          }
+      };
+      copy(0, a.dy, a.ld_dy);
+      copy(1, a.h, a.ld_h);
+      if (a.dh) copy(2, a.dh, a.ld_dh);
+      if constexpr (INNER) copy(3, a.x, a.ld_x);
+      if constexpr (GATE == GATE_ROWS) copy(4, a.gate, a.ld_gate);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto store_sums = [&](float* to, int k, const uint64_t (&v)[H]) {
+#pragma unroll
+    for (int e = 0; e < H; ++e) {
+      const float2 p = of_pair(v[e]);
+      to[column(k) + 2 * e] = p.x;
+      if (2 * e + 1 < N) to[column(k) + 2 * e + 1] = p.y;
+    }
+  };
+  auto part_of = [&](int which) { return a.partial + (static_cast<int64_t>(which) * walkers + walker) * d; };
+
+  // The rows of a gate that this walker has, from row `begin` on and before `end`, are done.
+  int flushed = 0;
+  auto flush = [&](int64_t begin, int64_t end) {
+    const int64_t q = begin / a.gate_rows, q0 = q * a.gate_rows;
+    // written whole, or left as a part: a gate's last rows, or its first ones
+    float* const to = !a.dgate ? nullptr
+                      : q0 == begin && q0 + a.gate_rows == end ? static_cast<float*>(a.dgate) + q * d
+                      : begin == from ? part_of(a.at_head)
+                                      : part_of(a.at_tail);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (column(k) < d) {
+        uint64_t pw[H], g[H], v[H];
+        if constexpr (POST) {
+          load_pairs(a.post_weight, a.param_bf16, column(k), pw);
+          load_pairs(a.gate, a.gate_bf16, q * a.ld_gate + column(k), g);
+        }
+        if (to) {
+#pragma unroll
+          for (int e = 0; e < H; ++e) v[e] = POST ? mul2(pw[e], e1[k][e]) : e1[k][e];
+          if (POST && !RMS && a.post_bias) {
+            uint64_t pb[H];
+            load_pairs(a.post_bias, a.param_bf16, column(k), pb);
+#pragma unroll
+            for (int e = 0; e < H; ++e) v[e] = fma2(pb[e], e0[k][e], v[e]);
+          }
+          store_sums(to, k, v);
+        }
+        if constexpr (POST) {
+          auto add = [&](float* p, const uint64_t (&s)[H]) {
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+              const int i = column(k) + 2 * e;
+              const uint64_t before = flushed ? pair_of(p[i], 2 * e + 1 < N ? p[i + 1] : 0.f) : zero;
+              v[e] = fma2(g[e], s[e], before);
+            }
+            store_sums(p, k, v);
+          };
+          if (a.dpost_weight) add(part_of(a.at_dpw), e1[k]);
+          if (!RMS && a.dpost_bias) add(part_of(a.at_dpb), e0[k]);
+        }
+#pragma unroll
+        for (int e = 0; e < H; ++e) e1[k][e] = e0[k][e] = zero;
+      }
+    flushed = 1;
+  };
+
+  const float inv_d = 1.f / d;
+  struct Stats {
+    float m, r, pm, pr;
+  };
+  auto stats_of = [&](int n) {
+    Stats s = {0.f, 0.f, 0.f, 1.f};
+    if (n < mine) {
+      if (!RMS) s.m = a.mean[from + n];
+      s.r = a.rstd[from + n];
+      if (POST) {
+        if (!RMS) s.pm = a.post_mean[from + n];
+        s.pr = a.post_rstd[from + n];
+      }
+    }
+    return s;
+  };
+  int64_t gate_from = from, gate_to = GATE == GATE_SHARED ? from : 0;  // the rows of the gate in f
+  Stats next = stats_of(0);
+  fetch(0, 0);
+  int half = 0;
+  for (int n = 0; n < turns; ++n, half ^= 1) {
+    fetch(n + 1, half ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const Stats s = next;
+    next = stats_of(n + 1);
+    const bool live = n < mine;
+    const int64_t row = from + n;
+    if constexpr (GATE == GATE_SHARED) {
+      if (live && row >= gate_to) {
+        if (n > 0) flush(gate_from, gate_to);
+        gate_from = row;
+        gate_to = (row / a.gate_rows + 1) * a.gate_rows;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          if (column(k) < d) {
+            load_pairs(a.gate, a.gate_bf16, row / a.gate_rows * a.ld_gate + column(k), f[k]);
+            uint64_t pw[H];
+            if constexpr (POST) load_pairs(a.post_weight, a.param_bf16, column(k), pw);
+#pragma unroll
+            for (int e = 0; e < H; ++e) f[k][e] = POST ? mul2(mul2(pw[e], scale2), f[k][e]) : mul2(f[k][e], scale2);
+          }
+      }
+    }
+    const uint64_t r2 = pair_of(s.r), pr2 = pair_of(s.pr), m2 = pair_of(-s.m), pm2 = pair_of(-s.pm);
+    auto pair = [&](const V& v, int e) { return pair_of(v.get(2 * e), 2 * e + 1 < N ? v.get(2 * e + 1) : 0.f); };
+    // (x - mean) r, the difference first: x and mean may be large and close
+    auto hat_of = [&](uint64_t v, uint64_t m, uint64_t r) { return mul2(RMS ? v : add2(v, m), r); };
+    uint64_t t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = zero;
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (column(k) < d) {
+          const V vy = slot_of(half, 0, k), vh = slot_of(half, 1, k);
+          V vd, vx, vg;
+          if constexpr (POST) {
+            if (a.dh) vd = slot_of(half, 2, k);
+            vx = slot_of(half, 3, k);
+            if constexpr (GATE == GATE_ROWS) vg = slot_of(half, 4, k);
+          }
+#pragma unroll
+          for (int e = 0; e < H; ++e) {
+            const uint64_t y = pair(vy, e), hat = hat_of(pair(vh, e), m2, r2), yw = mul2(y, w[k][e]);
+            dw[k][e] = fma2(y, hat, dw[k][e]);
+            if (!RMS) db[k][e] = add2(db[k][e], y);
+            t[0] = fma2(yw, hat, t[0]);
+            if (!RMS) t[1] = add2(t[1], yw);
+            if constexpr (POST) {
+              uint64_t av = f[k][e];
+              if constexpr (GATE == GATE_ROWS) av = mul2(av, pair(vg, e));
+              const uint64_t kx = hat_of(pair(vx, e), pm2, pr2);
+              const uint64_t ae = mul2(av, a.dh ? fma2(r2, yw, pair(vd, e)) : mul2(r2, yw));
+              const uint64_t ah = mul2(av, hat);
+              t[2] = fma2(ae, kx, t[2]);
+              t[3] = fma2(ah, kx, t[3]);
+              if (!RMS) {
+                t[4] = add2(t[4], ae);
+                t[5] = add2(t[5], ah);
+                t[6] = add2(t[6], av);
+                t[7] = fma2(av, kx, t[7]);
+              }
+            }
+          }
+        }
+    }
+    float sums[SUMS];
+#pragma unroll
+    for (int i = 0; i < SUMS; ++i) {
+      const float2 p = of_pair(t[i]);
+      sums[i] = p.x + p.y;
+    }
+    group_sums<G, SUMS>(sums, part, half);
+    if (!live) continue;
+    const float c2 = s.r * sums[0] * inv_d, c1 = RMS ? 0.f : s.r * sums[1] * inv_d;  // r c2, r c1
+    float b1 = 0.f, b2 = 0.f;  // means of a g and of a g k
+    if constexpr (POST) {
+      b2 = fmaf(-c2, sums[3], sums[2]);
+      if constexpr (!RMS) {
+        b2 = fmaf(-c1, sums[7], b2) * inv_d;
+        b1 = fmaf(-c1, sums[6], fmaf(-c2, sums[5], sums[4])) * inv_d;
+      } else {
+        b2 *= inv_d;
+      }
+    }
+    const uint64_t n1 = pair_of(-c1), n2 = pair_of(-c2), o1 = pair_of(-b1), o2 = pair_of(-b2);
+    T* const to_res = static_cast<T*>(a.dres) + row * a.ld_dres;
+    T* const to_x = a.dx ? static_cast<T*>(a.dx) + row * a.ld_dx : nullptr;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (column(k) < d) {
+        const V vy = slot_of(half, 0, k), vh = slot_of(half, 1, k);
+        V vd, vx, vg;
+        if (a.dh) vd = slot_of(half, 2, k);
+        if constexpr (INNER) vx = slot_of(half, 3, k);
+        if constexpr (GATE == GATE_ROWS) vg = slot_of(half, 4, k);
+        float res[2 * H], dx[2 * H], dg[2 * H], pb[2 * H] = {};
+        if constexpr (GATE == GATE_ROWS && POST && !RMS)
+          if (a.dgate && a.post_bias) load_params<N>(a.post_bias, a.param_bf16, column(k), pb);
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+          const uint64_t hat = hat_of(pair(vh, e), m2, r2);
+          uint64_t g = fma2(r2, mul2(pair(vy, e), w[k][e]), fma2(hat, n2, n1));
+          if (a.dh) g = add2(g, pair(vd, e));
+          const float2 gr = of_pair(g);
+          res[2 * e] = gr.x, res[2 * e + 1] = gr.y;
+          uint64_t out = mul2(g, f[k][e]);  // a g, or scale gate g
+          if constexpr (INNER) {
+            const uint64_t kx = POST ? hat_of(pair(vx, e), pm2, pr2) : pair(vx, e);
+            if constexpr (GATE == GATE_ROWS) {
+              // dgate = scale g p, p = k pw + pb: out has scale pw g, or scale g
+              uint64_t v = mul2(out, kx);
+              if (POST && !RMS) v = fma2(mul2(g, scale2), pair_of(pb[2 * e], pb[2 * e + 1]), v);
+              const float2 dv = of_pair(v);
+              dg[2 * e] = dv.x, dg[2 * e + 1] = dv.y;
+              out = mul2(out, pair(vg, e));
+            }
+            if constexpr (POST || GATE == GATE_SHARED) {
+              uint64_t sg = mul2(g, scale2);  // with a gate for every row: its part of q too
+              if constexpr (GATE == GATE_ROWS) sg = mul2(sg, pair(vg, e));
+              e1[k][e] = fma2(sg, kx, e1[k][e]);
+              if (POST && !RMS) e0[k][e] = add2(e0[k][e], sg);
+            }
+            if constexpr (POST) out = mul2(fma2(kx, o2, add2(out, o1)), pr2);
+          }
+          const float2 ov = of_pair(out);
+          dx[2 * e] = ov.x, dx[2 * e + 1] = ov.y;
+        }
+        V p;
+        p.set(res);
+        store_piece<T, N>(to_res + column(k), p);
+        if (to_x) {
+          p.set(dx);
+          store_piece<T, N>(to_x + column(k), p);
+        }
+        if constexpr (GATE == GATE_ROWS) {
+          if (a.dgate) {
+            p.set(dg);
+            store_piece<T, N>(static_cast<T*>(a.dgate) + row * a.ld_dgate + column(k), p);
+          }
+        }
+      }
+  }
+  if (mine == 0) return;
+  if constexpr (GATE == GATE_SHARED) flush(gate_from, from + mine);
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (column(k) < d) {
+      if (a.dweight) store_sums(part_of(a.at_dw), k, dw[k]);
+      if (!RMS && a.dbias) store_sums(part_of(a.at_db), k, db[k]);
+      if constexpr (POST && GATE != GATE_SHARED) {
+        if (a.dpost_weight) store_sums(part_of(a.at_dpw), k, e1[k]);
+        if (!RMS && a.dpost_bias) store_sums(part_of(a.at_dpb), k, e0[k]);
+      }
+    }
+}
+
+// One launch: as many CTAs as the SMs hold at a time, so that each walks over its share of
+// the rows once. *walkers: rows of partial sums it writes.
+template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE>
+cudaError_t resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
+  constexpr int arrays = 3 + (POST || GATE != GATE_NONE) + (GATE == GATE_ROWS);
+  constexpr int smem = 2 * arrays * NV * N * static_cast<int>(sizeof(T)) * G * R;
+  static_assert(smem <= kResNormRing, "shared memory");
+  auto kernel = k_resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE>;
+  static std::atomic<uint64_t> configured{0};
+  static std::atomic<int> per_sm{0};
+  cudaError_t e;
+  const int n = resident_ctas(reinterpret_cast<const void*>(kernel), G * R, smem, configured, per_sm, &e);
+  if (n < 0) return e;
+  // four rows a walker at least, where that leaves the SMs at work: its partial sums are
+  // written and read again
+  int64_t grid = (a.rows + R - 1) / R;
+  if (grid > sms / 2) grid = grid / 4 > sms / 2 ? grid / 4 : sms / 2;
+  const int64_t most = static_cast<int64_t>(n) * sms, room = resnorm_walkers(a, sms) / R;
+  grid = grid < most ? grid : most;
+  grid = grid < room ? grid : room;
+  const int64_t w = grid * R;
+  *walkers = static_cast<int>(w < a.rows ? w : a.rows);
+  kernel<<<static_cast<unsigned>(grid), G * R, smem, s>>>(a, *walkers);
+  return cudaGetLastError();
+}
+
+// A row is given to few threads with several pieces each (see the norm's backward).
+template <typename T, int N, bool RMS, bool POST, int GATE>
+cudaError_t resnorm_bwd_n(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
+  const int64_t pieces = (a.d + N - 1) / N;
+#define RESNORM_CASE(most, NV, G, R) \
+  if (pieces <= most) return resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE>(a, sms, walkers, s);
+  RESNORM_CASE(32, 1, 32, 8)
+  RESNORM_CASE(64, 2, 32, 8)
+  RESNORM_CASE(128, 2, 64, 4)
+  RESNORM_CASE(256, 2, 128, 1)
+  RESNORM_CASE(384, 3, 128, 1)
+  RESNORM_CASE(512, 2, 256, 1)
+  RESNORM_CASE(768, 3, 256, 1)
+  RESNORM_CASE(1024, 2, 512, 1)
+  if constexpr (GATE != GATE_ROWS) RESNORM_CASE(1536, 3, 512, 1)
+#undef RESNORM_CASE
+  return cudaErrorNotSupported;  // longer rows: the caller has another kernel
+}
+
+template <typename T, bool POST>
+cudaError_t resnorm_bwd_kind(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
+  constexpr int N = 16 / static_cast<int>(sizeof(T));
+  const int gate = !a.gate ? GATE_NONE : a.gate_rows == 1 ? GATE_ROWS : GATE_SHARED;
+  if (a.rms)
+    return gate == GATE_NONE     ? resnorm_bwd_n<T, N, true, POST, GATE_NONE>(a, sms, walkers, s)
+           : gate == GATE_SHARED ? resnorm_bwd_n<T, N, true, POST, GATE_SHARED>(a, sms, walkers, s)
+                                 : resnorm_bwd_n<T, N, true, POST, GATE_ROWS>(a, sms, walkers, s);
+  return gate == GATE_NONE     ? resnorm_bwd_n<T, N, false, POST, GATE_NONE>(a, sms, walkers, s)
+         : gate == GATE_SHARED ? resnorm_bwd_n<T, N, false, POST, GATE_SHARED>(a, sms, walkers, s)
+                               : resnorm_bwd_n<T, N, false, POST, GATE_ROWS>(a, sms, walkers, s);
+}
+
+// Of whole pieces; cudaErrorNotSupported for rows that are too long. (A translation unit each.)
+cudaError_t resnorm_bwd_f32(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s);
+cudaError_t resnorm_bwd_f32_post(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s);
+cudaError_t resnorm_bwd_bf16(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s);
+cudaError_t resnorm_bwd_bf16_post(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s);
+
+}  // namespace grpo
