@@ -252,12 +252,13 @@ struct PolicyArgs {
   int reduce;          // 0 sequence, 1 token, 2 constant
   double inv_divisor;
   float beta;
-  // the bounds of the ratio, and their logs in two floats: 1 + clip_high, 1 - clip_low, dual_clip
-  float r_up, r_down, r_far;
+  // the bounds of the ratio less 1, and the bounds' logs in two floats: 1 + clip_high,
+  // 1 - clip_low, dual_clip
+  float e_up, e_down, e_far;
   float up_hi, up_lo, down_hi, down_lo, far_hi, far_lo;
   // set by policy_plan: how the tokens are cut, and the workspace's parts
   int64_t pieces, rows_per_chunk, chunks;
-  int count_ctas;
+  int count_ctas, loss_ctas;
   unsigned* ticket;
   int64_t* cta_count;
   double* partial;
@@ -266,6 +267,7 @@ struct PolicyArgs {
 };
 // Bytes of the workspace; fills in the parts of a.
 size_t policy_plan(PolicyArgs& a, int sms, void* workspace);
+bool policy_counts_first(const PolicyArgs& a);  // by a launch of its own
 cudaError_t launch_policy_count(const PolicyArgs& a, cudaStream_t s);
 cudaError_t launch_policy_loss(const PolicyArgs& a, cudaStream_t s);
 
@@ -314,13 +316,22 @@ struct GradTensor {
   int bf16;
 };
 constexpr int kGradMaxTensors = 1000;  // of one launch (its table is a kernel parameter)
-int grad_parts(int sms);               // partial norms that a launch leaves, at most
-// `t[0..n)`, none of them empty; chunk0 is filled in here.
+// How the parts of a norm are joined, and where the results go.
+struct GradJoin {
+  double* partial;
+  int parts, inf;
+  double max_norm, eps;
+  float* norm;    // null: not written (by a second launch that scales)
+  float* factor;  // may be null
+};
+int grad_parts(int sms);  // partial norms that a launch leaves, at most
+// In each `t[0..n)` are tensors of which none is empty; chunk0 is filled in here.
+bool grad_small(const GradTensor* t, int n);  // whether one launch takes the list
+cudaError_t launch_grad_small(const GradTensor* t, int n, const GradJoin& j, int scale, cudaStream_t s);
 cudaError_t launch_grad_norm(const GradTensor* t, int n, int inf, int sms, double* partial, int* parts, cudaStream_t s);
-cudaError_t launch_grad_join(const double* partial, int parts, int inf, double max_norm, double eps, float* norm, float* factor,
-                             cudaStream_t s);
+cudaError_t launch_grad_join(const GradJoin& j, cudaStream_t s);
 // Joins the first `parts` to one, in their place.
 cudaError_t launch_grad_fold(double* partial, int parts, int inf, cudaStream_t s);
-cudaError_t launch_grad_scale(const GradTensor* t, int n, const float* factor, int sms, cudaStream_t s);
+cudaError_t launch_grad_scale(const GradTensor* t, int n, const GradJoin& j, int sms, cudaStream_t s);
 
 }  // namespace grpo

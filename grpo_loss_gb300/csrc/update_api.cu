@@ -57,9 +57,9 @@ grpo_status policy_args(const grpo_policy_problem* p, PolicyArgs* a) {
   a->beta = static_cast<float>(p->beta);
   const double up = 1.0 + p->clip_high, down = p->clip_low < 1.0 ? 1.0 - p->clip_low : 0.0;
   const double far = p->dual_clip > 0.0 ? p->dual_clip : INFINITY;
-  a->r_up = static_cast<float>(up);
-  a->r_down = static_cast<float>(down);
-  a->r_far = static_cast<float>(far);
+  a->e_up = static_cast<float>(p->clip_high);
+  a->e_down = static_cast<float>(down - 1.0);
+  a->e_far = static_cast<float>(far - 1.0);
   log_bound(up, &a->up_hi, &a->up_lo);
   log_bound(down, &a->down_hi, &a->down_lo);
   log_bound(far, &a->far_hi, &a->far_lo);
@@ -141,26 +141,30 @@ grpo_status clip_grads(const grpo_grad_tensor* tensors, int32_t n_tensors, int32
   if (st != GRPO_OK) return st;
   if (!workspace || !aligned16(workspace) || workspace_bytes < grad_bytes(sms, kGradLaunches))
     return GRPO_ERR_WORKSPACE;
-  double* const partial = static_cast<double*>(workspace);
-  const int inf = norm_type == 0 ? 1 : 0;
+  GradJoin join = {static_cast<double*>(workspace), 0, norm_type == 0 ? 1 : 0, max_norm, eps, norm, factor};
   GradTensor table[kGradMaxTensors];
-  int parts = 0, launches = 0;
+  int launches = 0;
   for (int pass = 0; pass < (scale ? 2 : 1); ++pass) {
     int used = 0;
     for (int32_t i = 0; i <= n_tensors; ++i) {
       if (used == kGradMaxTensors || (i == n_tensors && used > 0)) {
+        if (pass == 0 && launches == 0 && i == n_tensors && grad_small(table, used)) {
+          LAUNCH(K_GRAD_NORM, stream, launch_grad_small(table, used, join, scale ? 1 : 0, stream));
+          return GRPO_OK;
+        }
         if (pass == 0) {
           if (launches == kGradLaunches) {
-            LAUNCH(K_GRAD_JOIN, stream, launch_grad_fold(partial, parts, inf, stream));
-            parts = launches = 1;
+            LAUNCH(K_GRAD_JOIN, stream, launch_grad_fold(join.partial, join.parts, join.inf, stream));
+            join.parts = launches = 1;
           }
           int more = 0;
           LAUNCH(K_GRAD_NORM, stream,
-                 launch_grad_norm(table, used, inf, sms, partial + parts, &more, stream));
-          parts += more;
+                 launch_grad_norm(table, used, join.inf, sms, join.partial + join.parts, &more, stream));
+          join.parts += more;
           ++launches;
         } else {
-          LAUNCH(K_GRAD_SCALE, stream, launch_grad_scale(table, used, factor, sms, stream));
+          LAUNCH(K_GRAD_SCALE, stream, launch_grad_scale(table, used, join, sms, stream));
+          join.norm = nullptr;
         }
         used = 0;
       }
@@ -173,9 +177,8 @@ grpo_status clip_grads(const grpo_grad_tensor* tensors, int32_t n_tensors, int32
       d.chunk0 = 0;
       d.bf16 = tensors[i].dtype == GRPO_BF16 ? 1 : 0;
     }
-    if (pass == 0)
-      LAUNCH(K_GRAD_JOIN, stream,
-             launch_grad_join(partial, parts, inf, max_norm, eps, norm, factor, stream));
+    // (what scales joins the parts by itself; without a tensor there is nothing to scale)
+    if (pass == 0 && (!scale || launches == 0)) LAUNCH(K_GRAD_JOIN, stream, launch_grad_join(join, stream));
   }
   return GRPO_OK;
 }
@@ -229,7 +232,7 @@ grpo_status grpo_policy_loss(const grpo_policy_problem* p, const float* logp, co
   a.loss = loss;
   a.stats = stats;
   a.dlogp = dlogp;
-  LAUNCH(K_POLICY_COUNT, stream, launch_policy_count(a, stream));
+  if (policy_counts_first(a)) LAUNCH(K_POLICY_COUNT, stream, launch_policy_count(a, stream));
   LAUNCH(K_POLICY_LOSS, stream, launch_policy_loss(a, stream));
   return GRPO_OK;
 }
