@@ -250,8 +250,7 @@ struct PolicyArgs {
   float* dlogp;        // may be null
   int token_adv, sequence_ratio;
   int reduce;          // 0 sequence, 1 token, 2 constant
-  double inv_divisor;
-  float beta;
+  float inv_divisor, beta;
   // the bounds of the ratio less 1, and the bounds' logs in two floats: 1 + clip_high,
   // 1 - clip_low, dual_clip
   float e_up, e_down, e_far;

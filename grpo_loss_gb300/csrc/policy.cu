@@ -5,7 +5,7 @@
 // The weight c of a token needs the number of valid tokens (of its sequence, or of all),
 // so that the mask is read first: a launch that counts, and one that does the rest; for few
 // tokens one cluster of CTAs does both, with a barrier between.
-// Bound by memory for many tokens (21 bytes each), with some 70 instructions each beside it.
+// Bound by memory and by the instructions beside it for many tokens (21 bytes each).
 #include <cooperative_groups.h>
 
 #include "f32x2.cuh"
@@ -20,6 +20,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTokens = 8;                   // of a thread at a time: their loads are in flight together
 constexpr int kChunk = kThreads * kTokens;   // tokens a CTA takes at a time, at most
+constexpr int kLossCtas = 3;                 // of an SM, at a time
 constexpr int kCluster = 8;
 constexpr int kSmall = 16 * kChunk;          // tokens that one cluster takes
 
@@ -37,36 +38,52 @@ struct Sum2 {
     lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, z)), __fsub_rn(v, z));
     hi = s;
   }
+  __device__ __forceinline__ void add_product(float a, float b) {
+    const float v = __fmul_rn(a, b);
+    add(v);
+    lo += __fmaf_rn(a, b, -v);
+  }
   __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
 };
 
-// e^x - 1 - x, of which e^x - 1 keeps too few digits near 0: there by the series
-// x^2 (1/2 + x/6 + ... + x^8/10!), whose next term is below 2^-27 of it for |x| < 1/2; of
-// two numbers at once.
-__device__ __forceinline__ uint64_t series2(uint64_t x) {
-  uint64_t p = pair_of(1.f / 3628800.f);
-  p = fma2(p, x, pair_of(1.f / 362880.f));
-  p = fma2(p, x, pair_of(1.f / 40320.f));
-  p = fma2(p, x, pair_of(1.f / 5040.f));
-  p = fma2(p, x, pair_of(1.f / 720.f));
-  p = fma2(p, x, pair_of(1.f / 120.f));
-  p = fma2(p, x, pair_of(1.f / 24.f));
-  p = fma2(p, x, pair_of(1.f / 6.f));
-  p = fma2(p, x, pair_of(0.5f));
-  return mul2(mul2(x, x), p);
-}
-// {e^x - 1, e^x - 1 - x} of each of the pair.
+// e^x - 1 and e^x - 1 - x of two numbers: x = n ln 2 + f with |f| <= ln 2 / 2 (Cody and
+// Waite's reduction, ln 2 in two floats), e^f - 1 - f by its series f^2 (1/2 + f/6 + ... +
+// f^6/8!), whose next term is below 2^-28 of it, and e^x - 1 = 2^n (e^f - 1) + 2^n - 1. Both
+// keep their digits near 0, where e^x less 1 and less x would not.
+template <bool K>
 __device__ __forceinline__ void exponentials(float x0, float x1, float (&em1)[2], float (&k)[2]) {
-  const float2 s = of_pair(series2(pair_of(x0, x1)));
-  k[0] = s.x, k[1] = s.y;
-  em1[0] = x0 + k[0], em1[1] = x1 + k[1];
-  if (!(fabsf(x0) < 0.5f)) {
-    em1[0] = expm1f(x0);
-    k[0] = em1[0] - x0;
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the nearest integer
+  const uint64_t x = pair_of(x0, x1);
+  const uint64_t t = fma2(x, pair_of(1.44269504f), pair_of(kMagic)), n = add2(t, pair_of(-kMagic));
+  const uint64_t f = fma2(n, pair_of(1.90465421e-9f), fma2(n, pair_of(-0.693147182f), x));
+  uint64_t p = pair_of(1.f / 40320.f);
+  p = fma2(p, f, pair_of(1.f / 5040.f));
+  p = fma2(p, f, pair_of(1.f / 720.f));
+  p = fma2(p, f, pair_of(1.f / 120.f));
+  p = fma2(p, f, pair_of(1.f / 24.f));
+  p = fma2(p, f, pair_of(1.f / 6.f));
+  p = fma2(p, f, pair_of(0.5f));
+  const uint64_t kf = mul2(mul2(f, f), p);
+  const float2 tt = of_pair(t), kk = of_pair(kf);
+  const int t0 = __float_as_int(tt.x), t1 = __float_as_int(tt.y);
+  const uint64_t two_n = pair_of(__int_as_float((t0 << 23) + 0x3F800000), __int_as_float((t1 << 23) + 0x3F800000));
+  const float2 e = of_pair(fma2(two_n, add2(f, kf), add2(two_n, pair_of(-1.f))));
+  em1[0] = e.x, em1[1] = e.y;
+  if (K) {
+    const int zero = __float_as_int(kMagic);
+    k[0] = t0 == zero ? kk.x : em1[0] - x0;
+    k[1] = t1 == zero ? kk.y : em1[1] - x1;
   }
-  if (!(fabsf(x1) < 0.5f)) {
-    em1[1] = expm1f(x1);
-    k[1] = em1[1] - x1;
+  // 2^n beyond float32's range, and what is not a number
+  if (!(fabsf(x0) < 80.f && fabsf(x1) < 80.f)) {
+    if (!(fabsf(x0) < 80.f)) {
+      em1[0] = expm1f(x0);
+      if (K) k[0] = em1[0] - x0;
+    }
+    if (!(fabsf(x1) < 80.f)) {
+      em1[1] = expm1f(x1);
+      if (K) k[1] = em1[1] - x1;
+    }
   }
 }
 
@@ -98,7 +115,7 @@ __device__ __forceinline__ double warp_sum(double v) {
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// Sums of a CTA in a fixed order, returned to its first warp.
+// Sums of a CTA in a fixed order, returned to its first thread.
 template <int M>
 __device__ void cta_sums(double (&v)[M]) {
   __shared__ double part[M][kThreads / 32];
@@ -145,7 +162,7 @@ __device__ __forceinline__ int count_bytes(const uint8_t* p, int len, int lane) 
 __device__ void count_phase(const PolicyArgs& a, int cta, int ctas, bool w_too) {
   const int lane = threadIdx.x & 31;
   const int64_t segs = a.B * a.pieces, warps = static_cast<int64_t>(ctas) * (kThreads / 32);
-  double total[1] = {0.0};
+  double total[1] = {0.0};  // (whole numbers)
   const bool thin = a.T < 16;
   for (int64_t i = thin ? static_cast<int64_t>(cta) * kThreads + threadIdx.x
                         : static_cast<int64_t>(cta) * (kThreads / 32) + (threadIdx.x >> 5);
@@ -186,6 +203,7 @@ __device__ void count_phase(const PolicyArgs& a, int cta, int ctas, bool w_too) 
       total[0] += n;
     }
   }
+  if (a.reduce != 1) return;
   cta_sums(total);
   if (threadIdx.x == 0) a.cta_count[cta] = static_cast<int64_t>(total[0]);
 }
@@ -195,176 +213,264 @@ enum : int { S_LOSS, S_KL, S_RATIO, S_LOW, S_HIGH, S_VALID, S_ALL };
 enum : int { W_NONE, W_TOKEN, W_SEQUENCE };
 
 // What a sequence's tokens share: the weight c, the advantage where it is one for all, and
-// the ratio where that is (its sides of the bounds in three bits).
+// the ratio where that is: the difference w's two floats, e^w - 1.
 struct Row {
-  float c, em1;
-  int sides;
+  float c, A, w, lo, em1;
 };
-
-// Which bounds w is beyond: 1 above the upper, 2 below the lower, 4 above the dual one. w
-// rounds a difference (lo: what it lost) and a bound's log is held in two floats: where the
-// first ones are equal the second decide.
-__device__ __forceinline__ int sides_of(const PolicyArgs& a, float w, float lo) {
-  auto above = [&](float hi, float l) { return w > hi || (w == hi && lo > l); };
-  return (above(a.up_hi, a.up_lo) ? 1 : 0) | (w < a.down_hi || (w == a.down_hi && lo < a.down_lo) ? 2 : 0) |
-         (above(a.far_hi, a.far_lo) ? 4 : 0);
+// Which bound a token's ratio is held by.
+struct Side {
+  bool above, below;
+  float held;  // the ratio less 1, held
+};
+// w rounds a difference (lo gives what it lost) and a bound's log is held in two floats:
+// where the first ones are equal the second decide.
+template <typename Lo>
+__device__ __forceinline__ Side side_of(const PolicyArgs& a, float A, float w, float em1, Lo lo) {
+  // the upper bound is 1 + clip_high, or dual_clip for A < 0; the lower one is for A < 0 alone
+  const bool neg = A < 0.f;
+  const float top = neg ? a.far_hi : a.up_hi, bottom = neg ? a.down_hi : -INFINITY;
+  Side s;
+  s.above = w > top;
+  s.below = w < bottom;
+  if (w == top || w == bottom) {
+    const float l = lo();
+    s.above = w == top && l > (neg ? a.far_lo : a.up_lo);
+    s.below = w == bottom && l < (neg ? a.down_lo : 0.f);
+  }
+  s.held = s.above ? (neg ? a.e_far : a.e_up) : s.below ? a.e_down : em1;
+  return s;
 }
 
+// A thread's sums.
+struct Sums {
+  Sum2 loss, kl, ratio;  // ratio: of r - 1
+  int low = 0, high = 0;
+  int64_t valid = 0;
+  double base = 0.0;     // of the loss: -c A of tokens with one advantage for their sequence
+};
+
+// Two tokens (all zeros where masked): their gradients over c, their terms of the loss over
+// c into l, and the statistics.
 template <int W, bool REF>
-__device__ void loss_phase(const PolicyArgs& a, int cta, int ctas, double (&sums)[S_ALL]) {
-  __shared__ Row s_row[kChunk];
-  __shared__ double s_total;
-  __shared__ int s_valid;
-  if (a.reduce == 1) {
-    double v[1] = {0.0};
-    for (int i = threadIdx.x; i < a.count_ctas; i += kThreads) v[0] += static_cast<double>(a.cta_count[i]);
-    cta_sums(v);
-    if (threadIdx.x == 0) s_total = v[0];
-    __syncthreads();
+__device__ __forceinline__ void two_tokens(const PolicyArgs& a, const Row& r0, const Row& r1, const float (&q)[2], const float (&o)[2],
+                                           const float (&p)[2], const float (&A)[2], float (&g)[2], float (&l)[2], float& kls, float& rs,
+                                           Sums& sums) {
+  float em1[2] = {W == W_SEQUENCE ? r0.em1 : 0.f, W == W_SEQUENCE ? r1.em1 : 0.f}, ex[2], kl[2] = {0.f, 0.f}, none[2];
+  float w[2] = {r0.w, r1.w};
+  if (W == W_TOKEN) {
+    w[0] = __fsub_rn(q[0], o[0]), w[1] = __fsub_rn(q[1], o[1]);
+    exponentials<false>(w[0], w[1], em1, none);
   }
+  if (REF) exponentials<true>(p[0] - q[0], p[1] - q[1], ex, kl);
 #pragma unroll
-  for (int m = 0; m < S_ALL; ++m) sums[m] = 0.0;
-  const double same = a.reduce == 1 ? 1.0 / s_total : a.inv_divisor;  // (unused with a weight for each sequence)
-  for (int64_t ch = cta; ch < a.chunks; ch += ctas) {
-    const Chunk k = chunk_of(a, ch);
-    __syncthreads();  // the last chunk's rows have been read
-    if (threadIdx.x == 0) s_valid = 0;
-    __syncthreads();
-    // the rows of the chunk, a thread each (a piece's sequence: one warp, a lane a piece)
-    if (k.rows == 1) {
-      if (threadIdx.x < 32) {
-        double n = 0.0, w = 0.0;
-        for (int64_t p = threadIdx.x; p < a.pieces; p += 32) {
-          n += a.seg_count[k.row0 * a.pieces + p];
-          if (W == W_SEQUENCE) w += a.seg_w[k.row0 * a.pieces + p];
-        }
-        n = warp_sum(n);
-        if (W == W_SEQUENCE) w = warp_sum(w);
-        const int here = a.seg_count[a.pieces > 1 ? ch : k.row0];
-        if (threadIdx.x == 0 && here > 0) {
-          const double c = a.reduce == 0 ? 1.0 / (static_cast<double>(a.B) * n) : same;
-          Row r = {static_cast<float>(c), 0.f, 0};
-          if (W == W_SEQUENCE) {
-            const double mean = w / n;
-            const float hi = static_cast<float>(mean);
-            r.em1 = static_cast<float>(expm1(mean));
-            r.sides = sides_of(a, hi, static_cast<float>(mean - static_cast<double>(hi)));
-          }
-          s_row[0] = r;
-          s_valid = here;
-          sums[S_VALID] += here;
-          if (!a.token_adv) sums[S_LOSS] -= c * here * static_cast<double>(a.adv[k.row0]);
-        }
-      }
-    } else {
-      int some = 0;
-      for (int i = threadIdx.x; i < k.rows; i += kThreads) {
-        const int n = a.seg_count[k.row0 + i];
-        if (n == 0) continue;
-        const double c = a.reduce == 0 ? 1.0 / (static_cast<double>(a.B) * n) : same;
-        Row r = {static_cast<float>(c), 0.f, 0};
-        if (W == W_SEQUENCE) {
-          const double mean = a.seg_w[k.row0 + i] / n;
-          const float hi = static_cast<float>(mean);
-          r.em1 = static_cast<float>(expm1(mean));
-          r.sides = sides_of(a, hi, static_cast<float>(mean - static_cast<double>(hi)));
-        }
-        s_row[i] = r;
-        some = 1;
-        sums[S_VALID] += n;
-        if (!a.token_adv) sums[S_LOSS] -= c * n * static_cast<double>(a.adv[k.row0 + i]);
-      }
-      if (some) s_valid = 1;
+  for (int e = 0; e < 2; ++e) {
+    const Row& r = e ? r1 : r0;
+    Side s = {false, false, em1[e]};
+    if (W != W_NONE) s = side_of(a, A[e], w[e], em1[e], [&] { return W == W_TOKEN ? diff_error(q[e], o[e], w[e]) : r.lo; });
+    const bool some = A[e] != 0.f;
+    l[e] = some ? -A[e] * s.held : 0.f;
+    g[e] = some && !s.above && !s.below ? -fmaf(A[e], em1[e], A[e]) : 0.f;
+    if (REF) {
+      l[e] = fmaf(a.beta, kl[e], l[e]);
+      g[e] = fmaf(-a.beta, ex[e], g[e]);
+      kls += kl[e];
     }
-    __syncthreads();
-    const int all = k.rows * k.len;
-    if (s_valid == 0) {  // nothing but the gradient's zeros
-      if (a.dlogp)
-        for (int i = threadIdx.x; i < all; i += kThreads) {
-          const int r = k.rows == 1 ? 0 : i / k.len;
-          a.dlogp[(k.row0 + r) * a.ld_dlogp + k.t0 + (i - r * k.len)] = 0.f;
+    if (W == W_TOKEN) rs += em1[e];
+    if (W != W_NONE) {
+      sums.low += some && s.below;
+      sums.high += some && s.above;
+    }
+  }
+}
+
+// Sequences of more than kChunk / 2 tokens, by their pieces: a CTA takes a run of these, so
+// that what a sequence shares is mostly known from the piece before.
+template <int W, bool REF>
+__device__ __forceinline__ void long_rows(const PolicyArgs& a, int cta, int ctas, float same, Sums& sums) {
+  const int64_t c0 = a.chunks * cta / ctas, c1 = a.chunks * (cta + 1) / ctas;
+  const int lane = threadIdx.x & 31;
+  int64_t row = -1;
+  Row r = {same, 0.f, 0.f, 0.f, 0.f};
+  for (int64_t ch = c0; ch < c1; ++ch) {
+    const Chunk k = chunk_of(a, ch);
+    const int here = a.seg_count[ch];
+    if (k.row0 != row) {
+      row = k.row0;
+      if (a.reduce == 0 || W == W_SEQUENCE) {
+        int n = 0;
+        double w = 0.0;
+        for (int64_t i = lane; i < a.pieces; i += 32) {
+          n += a.seg_count[row * a.pieces + i];
+          if (W == W_SEQUENCE) w += a.seg_w[row * a.pieces + i];
         }
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (a.reduce == 0) r.c = 1.f / (static_cast<float>(a.B) * static_cast<float>(n));
+        if (W == W_SEQUENCE && n > 0) {
+          const double mean = warp_sum(w) / n;
+          r.w = static_cast<float>(mean);
+          r.lo = static_cast<float>(mean - static_cast<double>(r.w));
+          r.em1 = static_cast<float>(expm1(mean));
+        }
+      }
+      if (!a.token_adv) r.A = a.adv[row];
+    }
+    float* const d = a.dlogp ? a.dlogp + row * a.ld_dlogp + k.t0 : nullptr;
+    if (here == 0) {  // nothing but the gradient's zeros
+      if (d)
+        for (int i = threadIdx.x; i < k.len; i += kThreads) d[i] = 0.f;
       continue;
     }
+    if (threadIdx.x == 0) {
+      sums.valid += here;
+      if (!a.token_adv) sums.base -= static_cast<double>(r.c) * here * static_cast<double>(r.A);
+      if (W == W_SEQUENCE) sums.ratio.add_product(r.em1, static_cast<float>(here));
+    }
+    const uint8_t* m = a.mask + row * a.ld_mask + k.t0;
+    const float* q_in = a.logp + row * a.ld_logp + k.t0;
+    const float* o_in = W == W_TOKEN ? a.old + row * a.ld_old + k.t0 : nullptr;
+    const float* p_in = REF ? a.ref + row * a.ld_ref + k.t0 : nullptr;
+    const float* A_in = a.token_adv ? a.adv + row * a.ld_adv + k.t0 : nullptr;
     float q[kTokens], o[kTokens], p[kTokens], A[kTokens];
     bool valid[kTokens];
-    int at[kTokens], of[kTokens];  // token and row of the chunk
 #pragma unroll
     for (int j = 0; j < kTokens; ++j) {
       const int i = j * kThreads + threadIdx.x;
-      of[j] = k.rows == 1 ? 0 : i / k.len;
-      at[j] = k.t0 + (i - of[j] * k.len);
-      valid[j] = i < all;
+      valid[j] = i < k.len && m[i] != 0;
       q[j] = o[j] = p[j] = A[j] = 0.f;
-      if (valid[j]) {
+      if (i < k.len) {
+        q[j] = q_in[i];
+        if (W == W_TOKEN) o[j] = o_in[i];
+        if (REF) p[j] = p_in[i];
+        if (a.token_adv) A[j] = A_in[i];
+      }
+    }
+    float loss = 0.f, kls = 0.f, rs = 0.f;
+#pragma unroll
+    for (int j = 0; j < kTokens; j += 2) {
+      float qq[2], oo[2], pp[2], AA[2], g[2], l[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        qq[e] = valid[j + e] ? q[j + e] : 0.f;
+        oo[e] = W == W_TOKEN && valid[j + e] ? o[j + e] : 0.f;
+        pp[e] = REF && valid[j + e] ? p[j + e] : 0.f;
+        AA[e] = !valid[j + e] ? 0.f : a.token_adv ? A[j + e] : r.A;
+      }
+      two_tokens<W, REF>(a, r, r, qq, oo, pp, AA, g, l, kls, rs, sums);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        loss += l[e];
+        if (a.token_adv) sums.loss.add_product(-AA[e], r.c);
+        const int i = (j + e) * kThreads + threadIdx.x;
+        if (d && i < k.len) d[i] = r.c * g[e];
+      }
+    }
+    sums.loss.add_product(loss, r.c);
+    if (REF) sums.kl.add(kls);
+    if (W == W_TOKEN) sums.ratio.add(rs);
+  }
+}
+
+// Shorter sequences, several whole ones a chunk; what they share stands in shared memory.
+template <int W, bool REF>
+__device__ __forceinline__ void short_rows(const PolicyArgs& a, int cta, int ctas, float same, Sums& sums) {
+  __shared__ Row s_row[kChunk];
+  const int len = static_cast<int>(a.T);
+  const uint32_t inverse = len > 1 ? static_cast<uint32_t>(0x100000000ull / len) + 1 : 0;  // i / len = i inverse / 2^32 for i < 2^16
+  for (int64_t ch = cta; ch < a.chunks; ch += ctas) {
+    const Chunk k = chunk_of(a, ch);
+    __syncthreads();  // the last chunk's rows have been read
+    for (int i = threadIdx.x; i < k.rows; i += kThreads) {
+      const int n = a.seg_count[k.row0 + i];
+      if (n == 0) continue;
+      Row r = {same, 0.f, 0.f, 0.f, 0.f};
+      if (a.reduce == 0) r.c = 1.f / (static_cast<float>(a.B) * static_cast<float>(n));
+      if (W == W_SEQUENCE) {
+        const double mean = a.seg_w[k.row0 + i] / n;
+        r.w = static_cast<float>(mean);
+        r.lo = static_cast<float>(mean - static_cast<double>(r.w));
+        r.em1 = static_cast<float>(expm1(mean));
+        sums.ratio.add_product(r.em1, static_cast<float>(n));
+      }
+      if (!a.token_adv) {
+        r.A = a.adv[k.row0 + i];
+        sums.loss.add_product(-r.A * static_cast<float>(n), r.c);
+      }
+      sums.valid += n;
+      s_row[i] = r;
+    }
+    __syncthreads();
+    const int all = k.rows * len;
+    float q[kTokens], o[kTokens], p[kTokens], A[kTokens];
+    bool valid[kTokens];
+    int of[kTokens], at[kTokens];
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+      const int i = j * kThreads + threadIdx.x;
+      of[j] = len > 1 ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), inverse)) : i;
+      at[j] = i - of[j] * len;
+      valid[j] = false;
+      q[j] = o[j] = p[j] = A[j] = 0.f;
+      if (i < all) {
         const int64_t row = k.row0 + of[j];
         valid[j] = a.mask[row * a.ld_mask + at[j]] != 0;
         q[j] = a.logp[row * a.ld_logp + at[j]];
         if (W == W_TOKEN) o[j] = a.old[row * a.ld_old + at[j]];
         if (REF) p[j] = a.ref[row * a.ld_ref + at[j]];
-        A[j] = a.adv[a.token_adv ? row * a.ld_adv + at[j] : row];
+        if (a.token_adv) A[j] = a.adv[row * a.ld_adv + at[j]];
       }
     }
-    // float32 sums of a thread's few tokens
-    float loss = 0.f, kls = 0.f, rs = 0.f;
-    Sum2 base;
-    int low = 0, high = 0;
+    float kls = 0.f, rs = 0.f;
 #pragma unroll
     for (int j = 0; j < kTokens; j += 2) {
-      float em1[2] = {0.f, 0.f}, k0[2], x1[2], kl[2] = {0.f, 0.f};
-      float w[2];
+      float qq[2], oo[2], pp[2], AA[2], g[2], l[2];
+      Row r[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        w[e] = valid[j + e] ? __fsub_rn(q[j + e], o[j + e]) : 0.f;
-        x1[e] = REF && valid[j + e] ? p[j + e] - q[j + e] : 0.f;
+        r[e] = {0.f, 0.f, 0.f, 0.f, 0.f};
+        if (valid[j + e]) r[e] = s_row[of[j + e]];
+        qq[e] = valid[j + e] ? q[j + e] : 0.f;
+        oo[e] = W == W_TOKEN && valid[j + e] ? o[j + e] : 0.f;
+        pp[e] = REF && valid[j + e] ? p[j + e] : 0.f;
+        AA[e] = !valid[j + e] ? 0.f : a.token_adv ? A[j + e] : r[e].A;
       }
-      if (W == W_TOKEN) exponentials(w[0], w[1], em1, k0);
-      if (REF) exponentials(x1[0], x1[1], x1, kl);  // x1: now e^x - 1
+      two_tokens<W, REF>(a, r[0], r[1], qq, oo, pp, AA, g, l, kls, rs, sums);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const Row r = s_row[of[j + e]];
-        float d = 0.f;
-        if (valid[j + e]) {
-          int sides = 0;
-          if (W == W_SEQUENCE) {
-            em1[e] = r.em1;
-            sides = r.sides;
-          } else if (W == W_TOKEN) {
-            float lo = 0.f;
-            if (w[e] == a.up_hi || w[e] == a.down_hi || w[e] == a.far_hi) lo = diff_error(q[j + e], o[j + e], w[e]);
-            sides = sides_of(a, w[e], lo);
-          }
-          const float Ae = A[j + e];
-          const bool up = Ae > 0.f && (sides & 1), down = Ae < 0.f && (sides & 2), far = Ae < 0.f && (sides & 4) && !down;
-          const float held = up ? a.e_up : down ? a.e_down : far ? a.e_far : em1[e];  // less 1
-          float l = Ae == 0.f ? 0.f : -Ae * held;
-          float g = up || down || far || Ae == 0.f ? 0.f : -fmaf(Ae, em1[e], Ae);
-          if (REF) {
-            l = fmaf(a.beta, kl[e], l);
-            g = fmaf(-a.beta, x1[e], g);
-          }
-          d = r.c * g;
-          if (a.token_adv) base.add(k.rows == 1 ? Ae : r.c * Ae);
-          loss += k.rows == 1 ? l : r.c * l;
-          kls += kl[e];
-          rs += em1[e];
-          low += down;
-          high += up || far;
-        }
+        sums.loss.add_product(l[e], r[e].c);
+        if (a.token_adv) sums.loss.add_product(-AA[e], r[e].c);
         if (a.dlogp && (j + e) * kThreads + static_cast<int>(threadIdx.x) < all)
-          a.dlogp[(k.row0 + of[j + e]) * a.ld_dlogp + at[j + e]] = d;
+          a.dlogp[(k.row0 + of[j + e]) * a.ld_dlogp + at[j + e]] = r[e].c * g[e];
       }
     }
-    double l = static_cast<double>(loss);
-    if (a.token_adv) l -= base.value();
-    if (k.rows == 1) l *= a.reduce == 0 ? static_cast<double>(s_row[0].c) : same;
-    sums[S_LOSS] += l;
-    if (REF) sums[S_KL] += static_cast<double>(kls);
-    if (W != W_NONE) sums[S_RATIO] += static_cast<double>(rs);
-    sums[S_LOW] += low;
-    sums[S_HIGH] += high;
+    if (REF) sums.kl.add(kls);
+    if (W == W_TOKEN) sums.ratio.add(rs);
   }
-  cta_sums(sums);
+}
+
+template <int W, bool REF>
+__device__ void loss_phase(const PolicyArgs& a, int cta, int ctas, double (&out)[S_ALL]) {
+  __shared__ float s_same;
+  float same = a.inv_divisor;  // (unused with a weight for each sequence)
+  if (a.reduce == 1) {
+    double v[1] = {0.0};
+    for (int i = threadIdx.x; i < a.count_ctas; i += kThreads) v[0] += static_cast<double>(a.cta_count[i]);
+    cta_sums(v);
+    if (threadIdx.x == 0) s_same = static_cast<float>(1.0 / v[0]);
+    __syncthreads();
+    same = s_same;
+  }
+  Sums sums;
+  if (a.rows_per_chunk == 1) long_rows<W, REF>(a, cta, ctas, same, sums);
+  else short_rows<W, REF>(a, cta, ctas, same, sums);
+  // (a sum that is not finite has no second part)
+  auto value = [](const Sum2& s) { return isfinite(s.hi) ? s.value() : static_cast<double>(s.hi); };
+  out[S_LOSS] = value(sums.loss) + sums.base;
+  out[S_KL] = value(sums.kl);
+  out[S_RATIO] = value(sums.ratio);
+  out[S_LOW] = sums.low;
+  out[S_HIGH] = sums.high;
+  out[S_VALID] = static_cast<double>(sums.valid);
+  cta_sums(out);
 }
 
 // By the first thread of the CTA that has every CTA's sums.
@@ -385,7 +491,7 @@ __global__ void __launch_bounds__(kThreads) k_policy_count(PolicyArgs a) {
 }
 
 template <int W, bool REF>
-__global__ void __launch_bounds__(kThreads) k_policy_loss(PolicyArgs a) {
+__global__ void __launch_bounds__(kThreads, kLossCtas) k_policy_loss(PolicyArgs a) {
   __shared__ bool s_last;
   double sums[S_ALL];
   loss_phase<W, REF>(a, blockIdx.x, gridDim.x, sums);
@@ -451,7 +557,7 @@ size_t policy_plan(PolicyArgs& a, int sms, void* workspace) {
   a.rows_per_chunk = a.T > kChunk / 2 || a.T < 1 ? 1 : kChunk / a.T;
   a.chunks = a.pieces > 1 ? a.B * a.pieces : (a.B + a.rows_per_chunk - 1) / a.rows_per_chunk;
   const int64_t most = 8ll * sms;
-  a.loss_ctas = static_cast<int>(a.chunks < 3ll * sms ? a.chunks : 3ll * sms);
+  a.loss_ctas = static_cast<int>(a.chunks < kLossCtas * sms ? a.chunks : kLossCtas * sms);
   const int64_t segs = a.B * a.pieces, want = (segs + kThreads / 32 - 1) / (kThreads / 32);
   a.count_ctas = small(a) ? kCluster : static_cast<int>(want < most ? want : most);
   size_t at = 0;

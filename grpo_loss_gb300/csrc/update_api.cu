@@ -53,7 +53,7 @@ grpo_status policy_args(const grpo_policy_problem* p, PolicyArgs* a) {
   a->token_adv = p->token_adv;
   a->sequence_ratio = p->ratio;
   a->reduce = p->reduce;
-  a->inv_divisor = p->reduce == 2 ? 1.0 / p->divisor : 0.0;
+  a->inv_divisor = p->reduce == 2 ? static_cast<float>(1.0 / p->divisor) : 0.f;
   a->beta = static_cast<float>(p->beta);
   const double up = 1.0 + p->clip_high, down = p->clip_low < 1.0 ? 1.0 - p->clip_low : 0.0;
   const double far = p->dual_clip > 0.0 ? p->dual_clip : INFINITY;
