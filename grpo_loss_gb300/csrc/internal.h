@@ -256,13 +256,13 @@ struct PolicyArgs {
   float e_up, e_down, e_far;
   float up_hi, up_lo, down_hi, down_lo, far_hi, far_lo;
   // set by policy_plan: how the tokens are cut, and the workspace's parts
-  int64_t pieces, rows_per_chunk, chunks;
+  int64_t pieces;
   int count_ctas, loss_ctas;
   unsigned* ticket;
   int64_t* cta_count;
   double* partial;
-  int* seg_count;
-  double* seg_w;
+  int* piece_count;
+  double* piece_w;
 };
 // Bytes of the workspace; fills in the parts of a.
 size_t policy_plan(PolicyArgs& a, int sms, void* workspace);

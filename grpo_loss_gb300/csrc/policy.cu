@@ -17,12 +17,15 @@ namespace grpo {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTokens = 8;                   // of a thread at a time: their loads are in flight together
-constexpr int kChunk = kThreads * kTokens;   // tokens a CTA takes at a time, at most
-constexpr int kLossCtas = 3;                 // of an SM, at a time
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kTokens = 8;               // of a thread at a time: their loads are in flight together
+constexpr int kPiece = 2048;             // tokens of a sequence that are counted together
+constexpr int kUnit = 32 * kTokens;      // tokens that a warp takes at a time
+constexpr int kChunk = kThreads * kTokens;  // of short sequences, that a CTA takes at a time
+constexpr int kShort = 64;               // sequences below this are taken several a warp
+constexpr int kLossCtas = 3;             // of an SM, at a time
 constexpr int kCluster = 8;
-constexpr int kSmall = 16 * kChunk;          // tokens that one cluster takes
+constexpr int64_t kSmall = 16 * kChunk;  // tokens that one cluster takes
 
 // ---------------------------------------------------------------- numbers
 // The rounding error of s = a - b.
@@ -43,13 +46,17 @@ struct Sum2 {
     add(v);
     lo += __fmaf_rn(a, b, -v);
   }
-  __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+  // (a sum that is not finite has no second part)
+  __device__ __forceinline__ double value() const {
+    return isfinite(hi) ? static_cast<double>(hi) + static_cast<double>(lo) : static_cast<double>(hi);
+  }
 };
 
 // e^x - 1 and e^x - 1 - x of two numbers: x = n ln 2 + f with |f| <= ln 2 / 2 (Cody and
 // Waite's reduction, ln 2 in two floats), e^f - 1 - f by its series f^2 (1/2 + f/6 + ... +
 // f^6/8!), whose next term is below 2^-28 of it, and e^x - 1 = 2^n (e^f - 1) + 2^n - 1. Both
-// keep their digits near 0, where e^x less 1 and less x would not.
+// keep their digits near 0, where e^x less 1 and less x would not. For |x| < 80, or NaN.
+constexpr float kFar = 80.f;
 template <bool K>
 __device__ __forceinline__ void exponentials(float x0, float x1, float (&em1)[2], float (&k)[2]) {
   constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the nearest integer
@@ -74,40 +81,6 @@ __device__ __forceinline__ void exponentials(float x0, float x1, float (&em1)[2]
     k[0] = t0 == zero ? kk.x : em1[0] - x0;
     k[1] = t1 == zero ? kk.y : em1[1] - x1;
   }
-  // 2^n beyond float32's range, and what is not a number
-  if (!(fabsf(x0) < 80.f && fabsf(x1) < 80.f)) {
-    if (!(fabsf(x0) < 80.f)) {
-      em1[0] = expm1f(x0);
-      if (K) k[0] = em1[0] - x0;
-    }
-    if (!(fabsf(x1) < 80.f)) {
-      em1[1] = expm1f(x1);
-      if (K) k[1] = em1[1] - x1;
-    }
-  }
-}
-
-// ----------------------------------------------------------------- chunks
-// A chunk: whole sequences of up to half its tokens, or a piece of a longer one.
-struct Chunk {
-  int64_t row0;
-  int t0, rows, len;
-};
-__device__ __forceinline__ Chunk chunk_of(const PolicyArgs& a, int64_t c) {
-  Chunk k;
-  if (a.pieces > 1) {
-    k.row0 = c / a.pieces;
-    const int64_t p = c - k.row0 * a.pieces;
-    k.t0 = static_cast<int>(p * a.T / a.pieces);
-    k.len = static_cast<int>((p + 1) * a.T / a.pieces) - k.t0;
-    k.rows = 1;
-  } else {
-    k.row0 = c * a.rows_per_chunk;
-    k.rows = static_cast<int>(a.B - k.row0 < a.rows_per_chunk ? a.B - k.row0 : a.rows_per_chunk);
-    k.t0 = 0;
-    k.len = static_cast<int>(a.T);
-  }
-  return k;
 }
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -118,7 +91,7 @@ __device__ __forceinline__ double warp_sum(double v) {
 // Sums of a CTA in a fixed order, returned to its first thread.
 template <int M>
 __device__ void cta_sums(double (&v)[M]) {
-  __shared__ double part[M][kThreads / 32];
+  __shared__ double part[M][kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
 #pragma unroll
@@ -130,9 +103,9 @@ __device__ void cta_sums(double (&v)[M]) {
   if (warp == 0) {
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      v[m] = lane < kThreads / 32 ? part[m][lane] : 0.0;
+      v[m] = lane < kWarps ? part[m][lane] : 0.0;
 #pragma unroll
-      for (int o = kThreads / 64; o >= 1; o >>= 1) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+      for (int o = kWarps / 2; o >= 1; o >>= 1) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
     }
   }
 }
@@ -157,49 +130,110 @@ __device__ __forceinline__ int count_bytes(const uint8_t* p, int len, int lane) 
   return n;
 }
 
-// Valid tokens of every segment (a sequence, or its piece), and with a sequence's ratio the
-// sum of w of these: a warp a segment. Rows of few tokens: a thread a row.
-__device__ void count_phase(const PolicyArgs& a, int cta, int ctas, bool w_too) {
+// A sequence's tokens are cut at every kPiece and kUnit of them from `-shift` on: with VEC
+// where quads of four tokens are on 16-byte boundaries, in every operand alike.
+template <bool VEC>
+__device__ __forceinline__ int shift_of(const PolicyArgs& a, int64_t row) {
+  return VEC ? static_cast<int>(row * a.ld_logp & 3) : 0;
+}
+// Eight tokens of a lane, of the 256 from t0 on, of a sequence of T: two quads, or with
+// VEC = false every 32nd.
+template <bool VEC>
+__device__ __forceinline__ int64_t token_at(int64_t t0, int j) {
   const int lane = threadIdx.x & 31;
-  const int64_t segs = a.B * a.pieces, warps = static_cast<int64_t>(ctas) * (kThreads / 32);
-  double total[1] = {0.0};  // (whole numbers)
-  const bool thin = a.T < 16;
-  for (int64_t i = thin ? static_cast<int64_t>(cta) * kThreads + threadIdx.x
-                        : static_cast<int64_t>(cta) * (kThreads / 32) + (threadIdx.x >> 5);
-       i < segs; i += thin ? static_cast<int64_t>(ctas) * kThreads : warps) {
-    const int64_t row = i / a.pieces, p = i - row * a.pieces;
-    const int t0 = static_cast<int>(p * a.T / a.pieces), len = static_cast<int>((p + 1) * a.T / a.pieces) - t0;
-    const uint8_t* m = a.mask + row * a.ld_mask + t0;
-    const int step = thin ? 1 : 32, first = thin ? 0 : lane;
-    int n = 0;
-    Sum2 w;
-    if (w_too) {
-      const float *q = a.logp + row * a.ld_logp + t0, *o = a.old + row * a.ld_old + t0;
-#pragma unroll 8
-      for (int t = first; t < len; t += step) {
-        const bool valid = m[t] != 0;
-        const float u = q[t], v = o[t], s = __fsub_rn(u, v);
-        n += valid;
-        const float z = valid ? s : 0.f;
-        w.add(z);
-        const float e = diff_error(u, v, s);
-        if (valid && isfinite(s)) w.lo += e;
-      }
-    } else if (thin) {
-      for (int t = 0; t < len; ++t) n += m[t] != 0;
+  return VEC ? t0 + 128 * (j / 4) + 4 * lane + j % 4 : t0 + 32 * j + lane;
+}
+template <bool VEC>
+__device__ __forceinline__ void load_tokens(const float* p, int64_t t0, int64_t T, float (&v)[kTokens]) {
+#pragma unroll
+  for (int j = 0; j < kTokens; j += 4) {
+    const int64_t t = token_at<VEC>(t0, j);
+    if (VEC && t >= 0 && t + 4 <= T) {
+      const float4 u = *reinterpret_cast<const float4*>(p + t);
+      v[j] = u.x, v[j + 1] = u.y, v[j + 2] = u.z, v[j + 3] = u.w;
     } else {
-      n = count_bytes(m, len, lane);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t i = token_at<VEC>(t0, j + e);
+        v[j + e] = i >= 0 && i < T ? p[i] : 0.f;
+      }
     }
+  }
+}
+// The mask of the same tokens, a bit each.
+template <bool VEC>
+__device__ __forceinline__ uint32_t load_mask(const uint8_t* p, int64_t t0, int64_t T) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int j = 0; j < kTokens; j += 4) {
+    const int64_t t = token_at<VEC>(t0, j);
+    if (VEC && t >= 0 && t + 4 <= T) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(p + t);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bits |= (w >> (8 * e) & 0xFF) != 0 ? 1u << (j + e) : 0u;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t i = token_at<VEC>(t0, j + e);
+        if (i >= 0 && i < T && p[i] != 0) bits |= 1u << (j + e);
+      }
+    }
+  }
+  return bits;
+}
+
+// Valid tokens of every piece of a sequence, and with a sequence's ratio the sum of w of
+// these: a warp a piece. Sequences of few tokens: a thread each.
+template <bool VEC, bool WTOO>
+__device__ void count_phase(const PolicyArgs& a, int cta, int ctas) {
+  const int lane = threadIdx.x & 31;
+  const bool thin = a.T < 16;
+  const int64_t pieces = a.B * a.pieces, step = static_cast<int64_t>(ctas) * (thin ? kThreads : kWarps);
+  double total[1] = {0.0};  // (whole numbers)
+  for (int64_t i = static_cast<int64_t>(cta) * (thin ? kThreads : kWarps) + (thin ? threadIdx.x : threadIdx.x >> 5); i < pieces; i += step) {
+    const int64_t row = a.pieces == 1 ? i : i / a.pieces, from = (i - row * a.pieces) * kPiece - shift_of<VEC>(a, row);
+    const int64_t to = from + kPiece < a.T && a.pieces > 1 ? from + kPiece : a.T, t0 = from > 0 ? from : 0;
+    const uint8_t* m = a.mask + row * a.ld_mask;
+    const float *q = a.logp + row * a.ld_logp, *o = a.old + row * a.ld_old;
+    int n = 0;
     double sum = 0.0;
-    if (w_too) {
-      // (a sum that is not finite has no second part)
-      sum = isfinite(w.hi) ? w.value() : static_cast<double>(w.hi);
-      if (!thin) sum = warp_sum(sum);
+    if (thin) {
+      Sum2 w;
+      for (int64_t t = 0; t < a.T; ++t) {
+        const bool valid = m[t] != 0;
+        n += valid;
+        if (WTOO && valid) {
+          const float s = __fsub_rn(q[t], o[t]);
+          w.add(s);
+          w.lo += diff_error(q[t], o[t], s);
+        }
+      }
+      sum = w.value();
+    } else if (WTOO) {
+      Sum2 w;
+#pragma unroll 2
+      for (int64_t u = from; u < to; u += kUnit) {
+        float qs[kTokens], os[kTokens];
+        const uint32_t valid = load_mask<VEC>(m, u, to);
+        load_tokens<VEC>(q, u, to, qs);
+        load_tokens<VEC>(o, u, to, os);
+        n += __popc(valid);
+#pragma unroll
+        for (int j = 0; j < kTokens; ++j) {
+          const bool in = valid >> j & 1;
+          const float x = in ? qs[j] : 0.f, y = in ? os[j] : 0.f, s = __fsub_rn(x, y);
+          w.add(s);
+          w.lo += diff_error(x, y, s);
+        }
+      }
+      sum = warp_sum(w.value());
+    } else {
+      n = count_bytes(m + t0, static_cast<int>(to - t0), lane);
     }
     if (!thin) n = __reduce_add_sync(0xffffffffu, n);
     if (thin || lane == 0) {
-      a.seg_count[i] = n;
-      if (w_too) a.seg_w[i] = sum;
+      a.piece_count[i] = n;
+      if (WTOO) a.piece_w[i] = sum;
       total[0] += n;
     }
   }
@@ -212,242 +246,470 @@ __device__ void count_phase(const PolicyArgs& a, int cta, int ctas, bool w_too) 
 enum : int { S_LOSS, S_KL, S_RATIO, S_LOW, S_HIGH, S_VALID, S_ALL };
 enum : int { W_NONE, W_TOKEN, W_SEQUENCE };
 
-// What a sequence's tokens share: the weight c, the advantage where it is one for all, and
-// the ratio where that is: the difference w's two floats, e^w - 1.
-struct Row {
-  float c, A, w, lo, em1;
-};
-// Which bound a token's ratio is held by.
-struct Side {
-  bool above, below;
-  float held;  // the ratio less 1, held
-};
-// w rounds a difference (lo gives what it lost) and a bound's log is held in two floats:
-// where the first ones are equal the second decide.
-template <typename Lo>
-__device__ __forceinline__ Side side_of(const PolicyArgs& a, float A, float w, float em1, Lo lo) {
-  // the upper bound is 1 + clip_high, or dual_clip for A < 0; the lower one is for A < 0 alone
-  const bool neg = A < 0.f;
-  const float top = neg ? a.far_hi : a.up_hi, bottom = neg ? a.down_hi : -INFINITY;
-  Side s;
-  s.above = w > top;
-  s.below = w < bottom;
-  if (w == top || w == bottom) {
-    const float l = lo();
-    s.above = w == top && l > (neg ? a.far_lo : a.up_lo);
-    s.below = w == bottom && l < (neg ? a.down_lo : 0.f);
-  }
-  s.held = s.above ? (neg ? a.e_far : a.e_up) : s.below ? a.e_down : em1;
-  return s;
-}
-
 // A thread's sums.
 struct Sums {
   Sum2 loss, kl, ratio;  // ratio: of r - 1
   int low = 0, high = 0;
   int64_t valid = 0;
-  double base = 0.0;     // of the loss: -c A of tokens with one advantage for their sequence
 };
 
-// Two tokens (all zeros where masked): their gradients over c, their terms of the loss over
-// c into l, and the statistics.
-template <int W, bool REF>
-__device__ __forceinline__ void two_tokens(const PolicyArgs& a, const Row& r0, const Row& r1, const float (&q)[2], const float (&o)[2],
-                                           const float (&p)[2], const float (&A)[2], float (&g)[2], float (&l)[2], float& kls, float& rs,
-                                           Sums& sums) {
-  float em1[2] = {W == W_SEQUENCE ? r0.em1 : 0.f, W == W_SEQUENCE ? r1.em1 : 0.f}, ex[2], kl[2] = {0.f, 0.f}, none[2];
-  float w[2] = {r0.w, r1.w};
-  if (W == W_TOKEN) {
-    w[0] = __fsub_rn(q[0], o[0]), w[1] = __fsub_rn(q[1], o[1]);
-    exponentials<false>(w[0], w[1], em1, none);
-  }
-  if (REF) exponentials<true>(p[0] - q[0], p[1] - q[1], ex, kl);
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const Row& r = e ? r1 : r0;
-    Side s = {false, false, em1[e]};
-    if (W != W_NONE) s = side_of(a, A[e], w[e], em1[e], [&] { return W == W_TOKEN ? diff_error(q[e], o[e], w[e]) : r.lo; });
-    const bool some = A[e] != 0.f;
-    l[e] = some ? -A[e] * s.held : 0.f;
-    g[e] = some && !s.above && !s.below ? -fmaf(A[e], em1[e], A[e]) : 0.f;
-    if (REF) {
-      l[e] = fmaf(a.beta, kl[e], l[e]);
-      g[e] = fmaf(-a.beta, ex[e], g[e]);
-      kls += kl[e];
+// What holds the ratio of tokens of one advantage A: 1 + clip_high, or dual_clip for A < 0,
+// from above, and 1 - clip_low from below for A < 0. w rounds a difference (lo: what it
+// lost) and a bound's log is held in two floats: where the first are equal the second decide.
+struct Bounds {
+  float top, bottom, e_top;  // logs; the ratio less 1
+};
+__device__ __forceinline__ Bounds bounds_of(const PolicyArgs& a, float A) {
+  const bool neg = A < 0.f;
+  return {neg ? a.far_hi : a.up_hi, neg ? a.down_hi : -INFINITY, neg ? a.e_far : a.e_up};
+}
+__device__ __forceinline__ void sides_of(const PolicyArgs& a, float A, const Bounds& b, float w, float lo, bool& above, bool& below) {
+  above = w > b.top || (w == b.top && lo > (A < 0.f ? a.far_lo : a.up_lo));
+  below = w < b.bottom || (w == b.bottom && A < 0.f && lo < a.down_lo);
+}
+
+// What a sequence's tokens share: the weight c, the advantage A and the ratio where they are
+// one for all (e^w - 1, and whether it is held).
+struct Row {
+  float c, A, em1;
+  int held;  // 1 from above, 2 from below
+};
+// From the sums over its pieces. Its terms of the sums that every token shares are added by
+// the caller that takes its `here` tokens.
+template <int W, bool TADV>
+__device__ __forceinline__ Row row_of(const PolicyArgs& a, float same, int64_t row, int n, double w) {
+  Row r = {same, 0.f, 0.f, 0};
+  if (a.reduce == 0) r.c = 1.f / (static_cast<float>(a.B) * static_cast<float>(n));
+  if (!TADV) r.A = a.adv[row];
+  if (W == W_SEQUENCE && n > 0) {
+    const double mean = w / n;
+    const float hi = static_cast<float>(mean);
+    r.em1 = static_cast<float>(expm1(mean));
+    if (!TADV) {
+      bool above, below;
+      sides_of(a, r.A, bounds_of(a, r.A), hi, static_cast<float>(mean - static_cast<double>(hi)), above, below);
+      r.held = above ? 1 : below ? 2 : 0;
+    } else {  // by the sign of the token's: bits 0 and 1 for A > 0, 2 and 3 for A < 0
+      bool above, below;
+      const float lo = static_cast<float>(mean - static_cast<double>(hi));
+      sides_of(a, 1.f, bounds_of(a, 1.f), hi, lo, above, below);
+      r.held = above ? 1 : 0;
+      sides_of(a, -1.f, bounds_of(a, -1.f), hi, lo, above, below);
+      r.held |= above ? 4 : below ? 8 : 0;
     }
-    if (W == W_TOKEN) rs += em1[e];
-    if (W != W_NONE) {
-      sums.low += some && s.below;
-      sums.high += some && s.above;
+  }
+  return r;
+}
+template <int W, bool TADV>
+__device__ __forceinline__ void add_row(const PolicyArgs& a, const Row& r, int here, Sums& sums) {
+  sums.valid += here;
+  const float n = static_cast<float>(here);
+  if (W == W_SEQUENCE) sums.ratio.add_product(r.em1, n);
+  if (!TADV && r.A != 0.f) {
+    const float cA = r.c * r.A;
+    sums.loss.add_product(-cA, n);
+    if (W == W_SEQUENCE) {
+      sums.loss.add_product(-cA * (r.held == 0 ? r.em1 : r.held == 1 ? bounds_of(a, r.A).e_top : a.e_down), n);
+      sums.high += r.held == 1 ? here : 0;
+      sums.low += r.held == 2 ? here : 0;
     }
   }
 }
 
-// Sequences of more than kChunk / 2 tokens, by their pieces: a CTA takes a run of these, so
-// that what a sequence shares is mostly known from the piece before.
+// Where a sequence's tokens are.
+struct Rows {
+  const uint8_t* mask;
+  const float *q, *o, *p, *A;
+  float* d;
+};
+template <int W, bool REF, bool TADV>
+__device__ __forceinline__ Rows rows_of(const PolicyArgs& a, int64_t row, int64_t t0) {
+  return {a.mask + row * a.ld_mask + t0,
+          a.logp + row * a.ld_logp + t0,
+          W == W_TOKEN ? a.old + row * a.ld_old + t0 : nullptr,
+          REF ? a.ref + row * a.ld_ref + t0 : nullptr,
+          TADV ? a.adv + row * a.ld_adv + t0 : nullptr,
+          a.dlogp ? a.dlogp + row * a.ld_dlogp + t0 : nullptr};
+}
+
+// One token's terms.
+struct Term {
+  float d, held, kl, em1;  // the gradient; the ratio less 1, held (0 for A = 0) and not
+  bool above, below;
+};
+// A token whose numbers are too large for the series, infinite, or on a bound.
 template <int W, bool REF>
-__device__ __forceinline__ void long_rows(const PolicyArgs& a, int cta, int ctas, float same, Sums& sums) {
-  const int64_t c0 = a.chunks * cta / ctas, c1 = a.chunks * (cta + 1) / ctas;
-  const int lane = threadIdx.x & 31;
-  int64_t row = -1;
-  Row r = {same, 0.f, 0.f, 0.f, 0.f};
-  for (int64_t ch = c0; ch < c1; ++ch) {
-    const Chunk k = chunk_of(a, ch);
-    const int here = a.seg_count[ch];
-    if (k.row0 != row) {
-      row = k.row0;
-      if (a.reduce == 0 || W == W_SEQUENCE) {
-        int n = 0;
-        double w = 0.0;
-        for (int64_t i = lane; i < a.pieces; i += 32) {
-          n += a.seg_count[row * a.pieces + i];
-          if (W == W_SEQUENCE) w += a.seg_w[row * a.pieces + i];
-        }
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (a.reduce == 0) r.c = 1.f / (static_cast<float>(a.B) * static_cast<float>(n));
-        if (W == W_SEQUENCE && n > 0) {
-          const double mean = warp_sum(w) / n;
-          r.w = static_cast<float>(mean);
-          r.lo = static_cast<float>(mean - static_cast<double>(r.w));
-          r.em1 = static_cast<float>(expm1(mean));
-        }
-      }
-      if (!a.token_adv) r.A = a.adv[row];
+__device__ __noinline__ Term far_token(const PolicyArgs& a, Row r, float A, float q, float o, float p) {
+  Term t = {0.f, 0.f, 0.f, r.em1, false, false};
+  if (W == W_TOKEN) {
+    const float w = __fsub_rn(q, o);
+    t.em1 = expm1f(w);
+    if (A != 0.f) {
+      const Bounds b = bounds_of(a, A);
+      sides_of(a, A, b, w, diff_error(q, o, w), t.above, t.below);
+      t.held = t.above ? b.e_top : t.below ? a.e_down : t.em1;
     }
-    float* const d = a.dlogp ? a.dlogp + row * a.ld_dlogp + k.t0 : nullptr;
-    if (here == 0) {  // nothing but the gradient's zeros
-      if (d)
-        for (int i = threadIdx.x; i < k.len; i += kThreads) d[i] = 0.f;
-      continue;
-    }
-    if (threadIdx.x == 0) {
-      sums.valid += here;
-      if (!a.token_adv) sums.base -= static_cast<double>(r.c) * here * static_cast<double>(r.A);
-      if (W == W_SEQUENCE) sums.ratio.add_product(r.em1, static_cast<float>(here));
-    }
-    const uint8_t* m = a.mask + row * a.ld_mask + k.t0;
-    const float* q_in = a.logp + row * a.ld_logp + k.t0;
-    const float* o_in = W == W_TOKEN ? a.old + row * a.ld_old + k.t0 : nullptr;
-    const float* p_in = REF ? a.ref + row * a.ld_ref + k.t0 : nullptr;
-    const float* A_in = a.token_adv ? a.adv + row * a.ld_adv + k.t0 : nullptr;
-    float q[kTokens], o[kTokens], p[kTokens], A[kTokens];
-    bool valid[kTokens];
+  } else if (W == W_SEQUENCE) {
+    t.held = A != 0.f ? t.em1 : 0.f;  // (the caller holds it)
+  }
+  const float cA = r.c * A;
+  t.d = A != 0.f && !t.above && !t.below ? -fmaf(cA, t.em1, cA) : 0.f;
+  if (REF) {
+    const float x = p - q, e = expm1f(x);
+    t.kl = e - x;
+    t.d = fmaf(-r.c * a.beta, e, t.d);
+  }
+  return t;
+}
+
+// Units of a sequence's tokens.
+__host__ __device__ __forceinline__ int64_t units_of(const PolicyArgs& a, bool vec) { return (a.T + (vec ? 3 : 0) + kUnit - 1) / kUnit; }
+
+// The tokens of a thread, of a sequence each (row_for(j)). `at(j, i)`: where the sequence's
+// are, and which of them token j is; `in(j)`: whether it is one.
+template <int W, bool REF, bool TADV, typename In, typename At, typename RowOf>
+__device__ __forceinline__ void tokens(const PolicyArgs& a, In in, At at, RowOf row_for, Sums& sums) {
+  constexpr bool LOGP = W == W_TOKEN || REF;
+  bool valid[kTokens];
+  float w[kTokens], x[kTokens], A[kTokens];
+  {
+    float q[kTokens], o[kTokens], p[kTokens];
 #pragma unroll
     for (int j = 0; j < kTokens; ++j) {
-      const int i = j * kThreads + threadIdx.x;
-      valid[j] = i < k.len && m[i] != 0;
+      valid[j] = false;
       q[j] = o[j] = p[j] = A[j] = 0.f;
-      if (i < k.len) {
-        q[j] = q_in[i];
-        if (W == W_TOKEN) o[j] = o_in[i];
-        if (REF) p[j] = p_in[i];
-        if (a.token_adv) A[j] = A_in[i];
+      if (in(j)) {
+        int i;
+        const Rows g = at(j, i);
+        valid[j] = g.mask[i] != 0;
+        if (LOGP) q[j] = g.q[i];
+        if (W == W_TOKEN) o[j] = g.o[i];
+        if (REF) p[j] = g.p[i];
+        if (TADV) A[j] = g.A[i];
       }
     }
-    float loss = 0.f, kls = 0.f, rs = 0.f;
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+      w[j] = W == W_TOKEN && valid[j] ? __fsub_rn(q[j], o[j]) : 0.f;
+      x[j] = REF && valid[j] ? p[j] - q[j] : 0.f;
+    }
+  }
+  // numbers that the series does not take, and differences on a bound
+  float most = 0.f;
+  bool far = false;
+#pragma unroll
+  for (int j = 0; j < kTokens; ++j) {
+    most = fmaxf(most, fmaxf(fabsf(w[j]), fabsf(x[j])));
+    if (W == W_TOKEN) far |= w[j] == a.up_hi || w[j] == a.down_hi || w[j] == a.far_hi;
+  }
+  far |= most >= kFar;
+  float kls = 0.f, rs = 0.f;
+#pragma unroll
+  for (int j = 0; j < kTokens; j += 2) {
+    float em1[2] = {0.f, 0.f}, ex[2], kl[2] = {0.f, 0.f}, none[2];
+    if (W == W_TOKEN) exponentials<false>(w[j], w[j + 1], em1, none);
+    if (REF) exponentials<true>(x[j], x[j + 1], ex, kl);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const Row r = row_for(j + e);
+      const float Ae = TADV ? A[j + e] : r.A;
+      if (W == W_SEQUENCE) em1[e] = r.em1;
+      Term t = {0.f, em1[e], kl[e], em1[e], false, false};
+      const float cA = r.c * Ae;
+      if (far && valid[j + e]) {
+        int i;
+        const Rows g = at(j + e, i);
+        t = far_token<W, REF>(a, r, Ae, LOGP ? g.q[i] : 0.f, W == W_TOKEN ? g.o[i] : 0.f, REF ? g.p[i] : 0.f);
+      } else {
+        if (W == W_TOKEN) {
+          const Bounds b = bounds_of(a, Ae);
+          t.above = w[j + e] > b.top;
+          t.below = w[j + e] < b.bottom;
+          t.held = t.above ? b.e_top : t.below ? a.e_down : em1[e];
+        }
+        t.d = t.above || t.below ? 0.f : -fmaf(cA, em1[e], cA);
+        if (Ae == 0.f) t.d = t.held = 0.f, t.above = t.below = false;
+        if (REF) t.d = fmaf(-r.c * a.beta, ex[e], t.d);
+      }
+      if (W == W_SEQUENCE) {  // the ratio's side is known
+        const int side = !TADV ? r.held : Ae > 0.f ? r.held & 3 : Ae < 0.f ? r.held >> 2 : 0;
+        if (side) {
+          t.d = REF ? -r.c * a.beta * (far ? expm1f(x[j + e]) : ex[e]) : 0.f;
+          t.held = Ae == 0.f ? 0.f : side == 1 ? bounds_of(a, Ae).e_top : a.e_down;
+          t.above = side == 1 && Ae != 0.f;
+          t.below = side == 2 && Ae != 0.f;
+        }
+      }
+      if (!valid[j + e]) t.d = 0.f;
+      if (REF) kls += t.kl;
+      if (W == W_TOKEN) rs += t.em1;
+      // the loss: c (-A (1 + held) + beta kl); of one advantage for all, -c A n is the row's
+      if (TADV) {
+        if (valid[j + e] && Ae != 0.f) {
+          sums.loss.add_product(-Ae, r.c);
+          sums.loss.add_product(-Ae * t.held, r.c);
+        }
+      } else if (W == W_TOKEN) {
+        sums.loss.add_product(t.held, -cA);
+      }
+      if (REF) sums.loss.add_product(t.kl, r.c * a.beta);
+      if (W == W_TOKEN || (W == W_SEQUENCE && TADV)) {
+        sums.low += valid[j + e] && t.below;
+        sums.high += valid[j + e] && t.above;
+      }
+      if (a.dlogp && in(j + e)) {
+        int i;
+        const Rows g = at(j + e, i);
+        g.d[i] = t.d;
+      }
+    }
+  }
+  if (REF) sums.kl.add(kls);
+  if (W == W_TOKEN) sums.ratio.add(rs);
+}
+
+// Eight tokens of a lane, all of one sequence.
+template <bool VEC, int W, bool REF, bool TADV>
+__device__ __forceinline__ void unit_tokens(const PolicyArgs& a, const Row& r, const Rows& g, int64_t t0, uint32_t valid, float (&q)[kTokens],
+                                            float (&o)[kTokens], float (&p)[kTokens], float (&A)[kTokens], Sums& sums) {
+  float d[kTokens];
+  // (the differences take the numbers' place: of masked tokens 0)
+  float most = 0.f;
+  bool far = false;
+#pragma unroll
+  for (int j = 0; j < kTokens; ++j) {
+    const bool in = valid >> j & 1;
+    if (REF) p[j] = in ? p[j] - q[j] : 0.f;
+    if (W == W_TOKEN) {
+      const float w = in ? __fsub_rn(q[j], o[j]) : 0.f;
+      o[j] = w;
+      far |= w == a.up_hi || w == a.down_hi || w == a.far_hi;
+      most = fmaxf(most, fabsf(w));
+    }
+    if (REF) most = fmaxf(most, fabsf(p[j]));
+    if (TADV) A[j] = in ? A[j] : 0.f;
+  }
+  const float cb = -r.c * a.beta;
+  if (far || most >= kFar) {  // numbers that the series does not take, or on a bound: one by one
+    float kls = 0.f, rs = 0.f, hs = 0.f;
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+      d[j] = 0.f;
+      if (!(valid >> j & 1)) continue;
+      const int64_t t = token_at<VEC>(t0, j);
+      const float Aj = TADV ? A[j] : r.A;
+      Term x = far_token<W, REF>(a, r, Aj, W == W_TOKEN || REF ? g.q[t] : 0.f, W == W_TOKEN ? g.o[t] : 0.f, REF ? g.p[t] : 0.f);
+      if (W == W_SEQUENCE) {
+        const int side = Aj == 0.f ? 0 : !TADV ? r.held : Aj > 0.f ? r.held & 3 : r.held >> 2;
+        if (side) {
+          x.d = REF ? cb * expm1f(p[j]) : 0.f;
+          x.held = side == 1 ? bounds_of(a, Aj).e_top : a.e_down;
+          x.above = side == 1;
+          x.below = side == 2;
+        }
+      }
+      d[j] = x.d;
+      if (TADV && Aj != 0.f) {
+        sums.loss.add_product(-Aj, r.c);
+        sums.loss.add_product(-Aj * x.held, r.c);
+      }
+      hs += x.held;
+      kls += x.kl;
+      rs += x.em1;
+      if (W == W_TOKEN || (W == W_SEQUENCE && TADV)) {
+        sums.low += x.below;
+        sums.high += x.above;
+      }
+    }
+    if (!TADV && W == W_TOKEN && r.A != 0.f) sums.loss.add_product(hs, -r.c * r.A);
+    if (REF) {
+      sums.loss.add_product(kls, -cb);
+      sums.kl.add(kls);
+    }
+    if (W == W_TOKEN) sums.ratio.add(rs);
+  } else {
+    Bounds b = bounds_of(a, r.A);
+    if (r.A == 0.f) b.top = INFINITY;  // (nothing to hold, or to count)
+    const float cA = r.A == 0.f ? 0.f : r.c * r.A;
+    uint64_t kls = pair_of(0.f), rs = kls, hs = kls;
 #pragma unroll
     for (int j = 0; j < kTokens; j += 2) {
-      float qq[2], oo[2], pp[2], AA[2], g[2], l[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        qq[e] = valid[j + e] ? q[j + e] : 0.f;
-        oo[e] = W == W_TOKEN && valid[j + e] ? o[j + e] : 0.f;
-        pp[e] = REF && valid[j + e] ? p[j + e] : 0.f;
-        AA[e] = !valid[j + e] ? 0.f : a.token_adv ? A[j + e] : r.A;
+      float em1[2] = {r.em1, r.em1}, ex[2], kl[2], held[2], dd[2];
+      if (W == W_TOKEN) {
+        float none[2];
+        exponentials<false>(o[j], o[j + 1], em1, none);
+        rs = add2(rs, pair_of(em1[0], em1[1]));
       }
-      two_tokens<W, REF>(a, r, r, qq, oo, pp, AA, g, l, kls, rs, sums);
+      if (REF) {
+        exponentials<true>(p[j], p[j + 1], ex, kl);
+        kls = add2(kls, pair_of(kl[0], kl[1]));
+      }
+      if (!TADV) {
+        if (W == W_TOKEN) {
+          const float2 gr = of_pair(fma2(pair_of(em1[0], em1[1]), pair_of(-cA), pair_of(-cA)));
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        loss += l[e];
-        if (a.token_adv) sums.loss.add_product(-AA[e], r.c);
-        const int i = (j + e) * kThreads + threadIdx.x;
-        if (d && i < k.len) d[i] = r.c * g[e];
+          for (int e = 0; e < 2; ++e) {
+            const bool above = o[j + e] > b.top, below = o[j + e] < b.bottom;
+            held[e] = above ? b.e_top : below ? a.e_down : em1[e];
+            dd[e] = above || below ? 0.f : e ? gr.y : gr.x;
+            sums.high += above;
+            sums.low += below;
+          }
+          hs = add2(hs, pair_of(held[0], held[1]));
+        } else {
+          dd[0] = dd[1] = r.A == 0.f || (W == W_SEQUENCE && r.held) ? 0.f : -fmaf(cA, r.em1, cA);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float Aj = A[j + e], cAj = r.c * Aj;
+          const Bounds bj = bounds_of(a, Aj);
+          bool above = false, below = false;
+          if (W == W_TOKEN) {
+            above = o[j + e] > bj.top;
+            below = o[j + e] < bj.bottom;
+          } else if (W == W_SEQUENCE) {
+            const int side = Aj > 0.f ? r.held & 3 : r.held >> 2;
+            above = side == 1;
+            below = side == 2;
+          }
+          const bool some = Aj != 0.f;
+          held[e] = above ? bj.e_top : below ? a.e_down : em1[e];
+          dd[e] = above || below || !some ? 0.f : -fmaf(cAj, em1[e], cAj);
+          sums.high += some && above;
+          sums.low += some && below;
+          // c A in full, and of it what the ratio adds
+          sums.loss.add_product(-Aj, r.c);
+          sums.loss.add(some ? -cAj * held[e] : 0.f);
+        }
+      }
+      if (REF) {
+        const float2 t = of_pair(fma2(pair_of(ex[0], ex[1]), pair_of(cb), pair_of(dd[0], dd[1])));
+        dd[0] = t.x, dd[1] = t.y;
+      }
+      d[j] = valid >> j & 1 ? dd[0] : 0.f;
+      d[j + 1] = valid >> (j + 1) & 1 ? dd[1] : 0.f;
+    }
+    const float2 h = of_pair(hs), k = of_pair(kls), x = of_pair(rs);
+    if (!TADV && W == W_TOKEN) sums.loss.add_product(h.x + h.y, -cA);
+    if (REF) {
+      sums.loss.add_product(k.x + k.y, -cb);
+      sums.kl.add(k.x + k.y);
+    }
+    if (W == W_TOKEN) sums.ratio.add(x.x + x.y);
+  }
+  if (!g.d) return;
+#pragma unroll
+  for (int j = 0; j < kTokens; j += 4) {
+    const int64_t t = token_at<VEC>(t0, j);
+    if (VEC && t >= 0 && t + 4 <= a.T) {
+      *reinterpret_cast<float4*>(g.d + t) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t i = token_at<VEC>(t0, j + e);
+        if (i >= 0 && i < a.T) g.d[i] = d[j + e];
       }
     }
-    sums.loss.add_product(loss, r.c);
-    if (REF) sums.kl.add(kls);
-    if (W == W_TOKEN) sums.ratio.add(rs);
   }
 }
 
-// Shorter sequences, several whole ones a chunk; what they share stands in shared memory.
-template <int W, bool REF>
+// A warp takes a run of units of its own, so that what a sequence shares is mostly known
+// from the unit before, and no warp waits for another.
+template <bool VEC, int W, bool REF, bool TADV>
+__device__ __forceinline__ void long_rows(const PolicyArgs& a, int cta, int ctas, float same, Sums& sums) {
+  const int lane = threadIdx.x & 31;
+  const int64_t units = units_of(a, VEC), all = a.B * units;  // of a sequence, and of all
+  const int64_t warps = static_cast<int64_t>(ctas) * kWarps, warp = static_cast<int64_t>(cta) * kWarps + (threadIdx.x >> 5);
+  const int64_t u0 = all / warps * warp + (warp < all % warps ? warp : all % warps), u1 = u0 + all / warps + (warp < all % warps ? 1 : 0);
+  if (u0 >= u1) return;
+  int64_t row = u0 / units, piece = -1;
+  int unit = static_cast<int>(u0 - row * units), here = 0;
+  Row r = {same, 0.f, 0.f, 0};
+  bool fresh = true;
+  for (int64_t u = u0; u < u1; ++u) {
+    const int64_t t0 = static_cast<int64_t>(unit) * kUnit - shift_of<VEC>(a, row);
+    const int64_t now = row * a.pieces + (a.pieces > 1 ? unit / (kPiece / kUnit) : 0);
+    if (now != piece) {
+      piece = now;
+      here = a.piece_count[piece];
+    }
+    const Rows g = rows_of<W, REF, TADV>(a, row, 0);
+    float q[kTokens], o[kTokens], p[kTokens], A[kTokens];
+    uint32_t valid = 0;
+    if (here > 0) {
+      valid = load_mask<VEC>(g.mask, t0, a.T);
+      if (W == W_TOKEN || REF) load_tokens<VEC>(g.q, t0, a.T, q);
+      if (W == W_TOKEN) load_tokens<VEC>(g.o, t0, a.T, o);
+      if (REF) load_tokens<VEC>(g.p, t0, a.T, p);
+      if (TADV) load_tokens<VEC>(g.A, t0, a.T, A);
+    }
+    if (fresh && here > 0) {
+      fresh = false;
+      int n = 0;
+      double w = 0.0;
+      if (a.reduce == 0 || W == W_SEQUENCE) {
+        for (int64_t i = lane; i < a.pieces; i += 32) {
+          n += a.piece_count[row * a.pieces + i];
+          if (W == W_SEQUENCE) w += a.piece_w[row * a.pieces + i];
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (W == W_SEQUENCE) w = warp_sum(w);
+      }
+      r = row_of<W, TADV>(a, same, row, n, w);
+    }
+    if (here > 0) {
+      // (what the piece's tokens share is added with its first unit)
+      if (lane == 0 && (a.pieces > 1 ? unit % (kPiece / kUnit) : unit) == 0) add_row<W, TADV>(a, r, here, sums);
+      unit_tokens<VEC, W, REF, TADV>(a, r, g, t0, valid, q, o, p, A, sums);
+    } else if (g.d) {  // nothing but the gradient's zeros
+#pragma unroll
+      for (int j = 0; j < kTokens; ++j) {
+        const int64_t i = token_at<VEC>(t0, j);
+        if (i >= 0 && i < a.T) g.d[i] = 0.f;
+      }
+    }
+    if (++unit == units) {
+      unit = 0;
+      ++row;
+      fresh = true;
+    }
+  }
+}
+
+// Short sequences, several whole ones a chunk; what they share stands in shared memory.
+template <int W, bool REF, bool TADV>
 __device__ __forceinline__ void short_rows(const PolicyArgs& a, int cta, int ctas, float same, Sums& sums) {
   __shared__ Row s_row[kChunk];
-  const int len = static_cast<int>(a.T);
+  const int len = static_cast<int>(a.T), per = kChunk / len;
   const uint32_t inverse = len > 1 ? static_cast<uint32_t>(0x100000000ull / len) + 1 : 0;  // i / len = i inverse / 2^32 for i < 2^16
-  for (int64_t ch = cta; ch < a.chunks; ch += ctas) {
-    const Chunk k = chunk_of(a, ch);
+  for (int64_t row0 = static_cast<int64_t>(cta) * per; row0 < a.B; row0 += static_cast<int64_t>(ctas) * per) {
+    const int rows = static_cast<int>(a.B - row0 < per ? a.B - row0 : per), all = rows * len;
     __syncthreads();  // the last chunk's rows have been read
-    for (int i = threadIdx.x; i < k.rows; i += kThreads) {
-      const int n = a.seg_count[k.row0 + i];
-      if (n == 0) continue;
-      Row r = {same, 0.f, 0.f, 0.f, 0.f};
-      if (a.reduce == 0) r.c = 1.f / (static_cast<float>(a.B) * static_cast<float>(n));
-      if (W == W_SEQUENCE) {
-        const double mean = a.seg_w[k.row0 + i] / n;
-        r.w = static_cast<float>(mean);
-        r.lo = static_cast<float>(mean - static_cast<double>(r.w));
-        r.em1 = static_cast<float>(expm1(mean));
-        sums.ratio.add_product(r.em1, static_cast<float>(n));
+    for (int i = threadIdx.x; i < rows; i += kThreads) {
+      const int n = a.piece_count[row0 + i];
+      Row r = {0.f, 0.f, 0.f, 0};
+      if (n > 0) {
+        r = row_of<W, TADV>(a, same, row0 + i, n, W == W_SEQUENCE ? a.piece_w[row0 + i] : 0.0);
+        add_row<W, TADV>(a, r, n, sums);
       }
-      if (!a.token_adv) {
-        r.A = a.adv[k.row0 + i];
-        sums.loss.add_product(-r.A * static_cast<float>(n), r.c);
-      }
-      sums.valid += n;
       s_row[i] = r;
     }
     __syncthreads();
-    const int all = k.rows * len;
-    float q[kTokens], o[kTokens], p[kTokens], A[kTokens];
-    bool valid[kTokens];
-    int of[kTokens], at[kTokens];
-#pragma unroll
-    for (int j = 0; j < kTokens; ++j) {
-      const int i = j * kThreads + threadIdx.x;
-      of[j] = len > 1 ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), inverse)) : i;
-      at[j] = i - of[j] * len;
-      valid[j] = false;
-      q[j] = o[j] = p[j] = A[j] = 0.f;
-      if (i < all) {
-        const int64_t row = k.row0 + of[j];
-        valid[j] = a.mask[row * a.ld_mask + at[j]] != 0;
-        q[j] = a.logp[row * a.ld_logp + at[j]];
-        if (W == W_TOKEN) o[j] = a.old[row * a.ld_old + at[j]];
-        if (REF) p[j] = a.ref[row * a.ld_ref + at[j]];
-        if (a.token_adv) A[j] = a.adv[row * a.ld_adv + at[j]];
-      }
-    }
-    float kls = 0.f, rs = 0.f;
-#pragma unroll
-    for (int j = 0; j < kTokens; j += 2) {
-      float qq[2], oo[2], pp[2], AA[2], g[2], l[2];
-      Row r[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        r[e] = {0.f, 0.f, 0.f, 0.f, 0.f};
-        if (valid[j + e]) r[e] = s_row[of[j + e]];
-        qq[e] = valid[j + e] ? q[j + e] : 0.f;
-        oo[e] = W == W_TOKEN && valid[j + e] ? o[j + e] : 0.f;
-        pp[e] = REF && valid[j + e] ? p[j + e] : 0.f;
-        AA[e] = !valid[j + e] ? 0.f : a.token_adv ? A[j + e] : r[e].A;
-      }
-      two_tokens<W, REF>(a, r[0], r[1], qq, oo, pp, AA, g, l, kls, rs, sums);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        sums.loss.add_product(l[e], r[e].c);
-        if (a.token_adv) sums.loss.add_product(-AA[e], r[e].c);
-        if (a.dlogp && (j + e) * kThreads + static_cast<int>(threadIdx.x) < all)
-          a.dlogp[(k.row0 + of[j + e]) * a.ld_dlogp + at[j + e]] = r[e].c * g[e];
-      }
-    }
-    if (REF) sums.kl.add(kls);
-    if (W == W_TOKEN) sums.ratio.add(rs);
+    auto row_in = [&](int j) {
+      const uint32_t i = j * kThreads + threadIdx.x;
+      return len > 1 ? static_cast<int>(__umulhi(i, inverse)) : static_cast<int>(i);
+    };
+    auto in = [&](int j) { return j * kThreads + static_cast<int>(threadIdx.x) < all; };
+    tokens<W, REF, TADV>(a, in, [&](int j, int& i) {
+      const int k = row_in(j);
+      i = j * kThreads + threadIdx.x - k * len;
+      return rows_of<W, REF, TADV>(a, row0 + k, 0);
+    }, [&](int j) { return in(j) ? s_row[row_in(j)] : Row{0.f, 0.f, 0.f, 0}; }, sums);
   }
 }
 
-template <int W, bool REF>
+template <bool VEC, int W, bool REF, bool TADV>
 __device__ void loss_phase(const PolicyArgs& a, int cta, int ctas, double (&out)[S_ALL]) {
   __shared__ float s_same;
   float same = a.inv_divisor;  // (unused with a weight for each sequence)
@@ -460,13 +722,11 @@ __device__ void loss_phase(const PolicyArgs& a, int cta, int ctas, double (&out)
     same = s_same;
   }
   Sums sums;
-  if (a.rows_per_chunk == 1) long_rows<W, REF>(a, cta, ctas, same, sums);
-  else short_rows<W, REF>(a, cta, ctas, same, sums);
-  // (a sum that is not finite has no second part)
-  auto value = [](const Sum2& s) { return isfinite(s.hi) ? s.value() : static_cast<double>(s.hi); };
-  out[S_LOSS] = value(sums.loss) + sums.base;
-  out[S_KL] = value(sums.kl);
-  out[S_RATIO] = value(sums.ratio);
+  if (a.T < kShort) short_rows<W, REF, TADV>(a, cta, ctas, same, sums);
+  else long_rows<VEC, W, REF, TADV>(a, cta, ctas, same, sums);
+  out[S_LOSS] = sums.loss.value();
+  out[S_KL] = sums.kl.value();
+  out[S_RATIO] = sums.ratio.value();
   out[S_LOW] = sums.low;
   out[S_HIGH] = sums.high;
   out[S_VALID] = static_cast<double>(sums.valid);
@@ -485,16 +745,17 @@ __device__ void finish(const PolicyArgs& a, const double (&sums)[S_ALL]) {
   }
 }
 
+template <bool VEC, bool WTOO>
 __global__ void __launch_bounds__(kThreads) k_policy_count(PolicyArgs a) {
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
-  count_phase(a, blockIdx.x, gridDim.x, a.sequence_ratio);
+  count_phase<VEC, WTOO>(a, blockIdx.x, gridDim.x);
 }
 
-template <int W, bool REF>
+template <bool VEC, int W, bool REF, bool TADV>
 __global__ void __launch_bounds__(kThreads, kLossCtas) k_policy_loss(PolicyArgs a) {
   __shared__ bool s_last;
   double sums[S_ALL];
-  loss_phase<W, REF>(a, blockIdx.x, gridDim.x, sums);
+  loss_phase<VEC, W, REF, TADV>(a, blockIdx.x, gridDim.x, sums);
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int m = 0; m < S_ALL; ++m) a.partial[S_ALL * blockIdx.x + m] = sums[m];
@@ -514,16 +775,16 @@ __global__ void __launch_bounds__(kThreads, kLossCtas) k_policy_loss(PolicyArgs 
 }
 
 // Both for few tokens.
-template <int W, bool REF>
+template <bool VEC, int W, bool REF, bool TADV>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) k_policy_small(PolicyArgs a) {
   __shared__ double parts[kCluster][S_ALL];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
-  count_phase(a, rank, kCluster, W == W_SEQUENCE);
+  count_phase<VEC, W == W_SEQUENCE>(a, rank, kCluster);
   __threadfence();
   cluster.sync();
   double sums[S_ALL];
-  loss_phase<W, REF>(a, rank, kCluster, sums);
+  loss_phase<VEC, W, REF, TADV>(a, rank, kCluster, sums);
   if (threadIdx.x == 0) {
     double* to = cluster.map_shared_rank(&parts[0][0], 0);
 #pragma unroll
@@ -542,23 +803,48 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) k_p
 
 bool small(const PolicyArgs& a) { return a.B * a.T <= kSmall; }
 
-template <int W, bool REF>
+// Whether quads of tokens of every operand are on 16-byte boundaries alike.
+bool by_quads(const PolicyArgs& a) {
+  auto fits = [&](const void* p, int64_t ld, int size) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % (4 * size) == 0 && (ld - a.ld_logp) % 4 == 0);
+  };
+  return fits(a.logp, a.ld_logp, 4) && fits(a.old, a.ld_old, 4) && fits(a.ref, a.ld_ref, 4) &&
+         fits(a.token_adv ? a.adv : nullptr, a.ld_adv, 4) && fits(a.mask, a.ld_mask, 1) && fits(a.dlogp, a.ld_dlogp, 4);
+}
+
+template <bool VEC, int W, bool REF, bool TADV>
 cudaError_t loss_launch(const PolicyArgs& a, cudaStream_t s) {
-  if (small(a)) k_policy_small<W, REF><<<kCluster, kThreads, 0, s>>>(a);
-  else k_policy_loss<W, REF><<<a.loss_ctas, kThreads, 0, s>>>(a);
+  if (small(a)) k_policy_small<VEC, W, REF, TADV><<<kCluster, kThreads, 0, s>>>(a);
+  else k_policy_loss<VEC, W, REF, TADV><<<a.loss_ctas, kThreads, 0, s>>>(a);
   return cudaGetLastError();
+}
+template <bool VEC>
+cudaError_t loss_of(const PolicyArgs& a, cudaStream_t s) {
+  const int w = !a.old ? W_NONE : a.sequence_ratio ? W_SEQUENCE : W_TOKEN;
+  switch (4 * w + (a.ref ? 2 : 0) + (a.token_adv ? 1 : 0)) {
+#define POLICY_CASE(W)                                              \
+  case 4 * W: return loss_launch<VEC, W, false, false>(a, s);       \
+  case 4 * W + 1: return loss_launch<VEC, W, false, true>(a, s);    \
+  case 4 * W + 2: return loss_launch<VEC, W, true, false>(a, s);    \
+  case 4 * W + 3: return loss_launch<VEC, W, true, true>(a, s);
+    POLICY_CASE(W_NONE)
+    POLICY_CASE(W_TOKEN)
+    POLICY_CASE(W_SEQUENCE)
+#undef POLICY_CASE
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-// Fills in how the tokens are cut into chunks, and the places in the workspace.
+// Fills in how the tokens are cut, and the places in the workspace.
 size_t policy_plan(PolicyArgs& a, int sms, void* workspace) {
-  a.pieces = a.T > kChunk ? (a.T + kChunk - 1) / kChunk : 1;
-  a.rows_per_chunk = a.T > kChunk / 2 || a.T < 1 ? 1 : kChunk / a.T;
-  a.chunks = a.pieces > 1 ? a.B * a.pieces : (a.B + a.rows_per_chunk - 1) / a.rows_per_chunk;
-  const int64_t most = 8ll * sms;
-  a.loss_ctas = static_cast<int>(a.chunks < kLossCtas * sms ? a.chunks : kLossCtas * sms);
-  const int64_t segs = a.B * a.pieces, want = (segs + kThreads / 32 - 1) / (kThreads / 32);
+  a.pieces = a.T > kPiece ? (a.T + 3 + kPiece - 1) / kPiece : 1;  // (the first may begin up to 3 tokens early)
+  const int64_t pieces = a.B * a.pieces, most = 8ll * sms, all = 1ll * kLossCtas * sms;
+  const int64_t chunks = a.T < 1 ? 1 : a.T < kShort ? (a.B + kChunk / a.T - 1) / (kChunk / a.T)
+                                                    : (a.B * units_of(a, true) + kWarps - 1) / kWarps;
+  const int64_t want = (pieces + kWarps - 1) / kWarps;
+  a.loss_ctas = static_cast<int>(chunks < all ? chunks : all);
   a.count_ctas = small(a) ? kCluster : static_cast<int>(want < most ? want : most);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -569,25 +855,22 @@ size_t policy_plan(PolicyArgs& a, int sms, void* workspace) {
   a.ticket = static_cast<unsigned*>(take(4));
   a.cta_count = static_cast<int64_t*>(take(8 * most));
   a.partial = static_cast<double*>(take(8 * S_ALL * most));
-  a.seg_count = static_cast<int*>(take(4 * segs));
-  a.seg_w = static_cast<double*>(take(a.sequence_ratio ? 8 * segs : 0));
+  a.piece_count = static_cast<int*>(take(4 * pieces));
+  a.piece_w = static_cast<double*>(take(a.sequence_ratio ? 8 * pieces : 0));
   return at;
 }
 
 bool policy_counts_first(const PolicyArgs& a) { return !small(a); }
 cudaError_t launch_policy_count(const PolicyArgs& a, cudaStream_t s) {
-  k_policy_count<<<a.count_ctas, kThreads, 0, s>>>(a);
+  if (by_quads(a)) {
+    if (a.sequence_ratio) k_policy_count<true, true><<<a.count_ctas, kThreads, 0, s>>>(a);
+    else k_policy_count<true, false><<<a.count_ctas, kThreads, 0, s>>>(a);
+  } else {
+    if (a.sequence_ratio) k_policy_count<false, true><<<a.count_ctas, kThreads, 0, s>>>(a);
+    else k_policy_count<false, false><<<a.count_ctas, kThreads, 0, s>>>(a);
+  }
   return cudaGetLastError();
 }
-cudaError_t launch_policy_loss(const PolicyArgs& a, cudaStream_t s) {
-  const int w = !a.old ? W_NONE : a.sequence_ratio ? W_SEQUENCE : W_TOKEN;
-  if (a.ref)
-    return w == W_NONE    ? loss_launch<W_NONE, true>(a, s)
-           : w == W_TOKEN ? loss_launch<W_TOKEN, true>(a, s)
-                          : loss_launch<W_SEQUENCE, true>(a, s);
-  return w == W_NONE    ? loss_launch<W_NONE, false>(a, s)
-         : w == W_TOKEN ? loss_launch<W_TOKEN, false>(a, s)
-                        : loss_launch<W_SEQUENCE, false>(a, s);
-}
+cudaError_t launch_policy_loss(const PolicyArgs& a, cudaStream_t s) { return by_quads(a) ? loss_of<true>(a, s) : loss_of<false>(a, s); }
 
 }  // namespace grpo
