@@ -110,6 +110,50 @@ __device__ void cta_sums(double (&v)[M]) {
   }
 }
 
+// A thread's sums.
+struct Sums {
+  Sum2 loss, kl, ratio;  // ratio: of r - 1
+  int low = 0, high = 0;
+  int64_t valid = 0;
+};
+// A warp's, in the order of the lanes' distances (in two floats: the float64 unit takes 16
+// cycles for a warp's addition).
+__device__ __forceinline__ double warp_total(Sum2 s) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    const float hi = __shfl_xor_sync(0xffffffffu, s.hi, o), lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+    s.add(hi);
+    s.lo += lo;
+  }
+  return s.value();
+}
+// A CTA's, in the order of the warps; returned to its first thread.
+__device__ __forceinline__ void cta_total(const Sums& sums, double (&out)[6]) {
+  __shared__ double part[6][kWarps];
+  const int warp = threadIdx.x >> 5;
+  const double v[3] = {warp_total(sums.loss), warp_total(sums.kl), warp_total(sums.ratio)};
+  const int low = __reduce_add_sync(0xffffffffu, sums.low), high = __reduce_add_sync(0xffffffffu, sums.high);
+  const unsigned v0 = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(sums.valid & 0xFFFFFF));
+  const unsigned v1 = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(sums.valid >> 24));
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int m = 0; m < 3; ++m) part[m][warp] = v[m];
+    part[3][warp] = low;
+    part[4][warp] = high;
+    part[5][warp] = static_cast<double>(v0) + 16777216.0 * static_cast<double>(v1);
+  }
+  __syncthreads();
+  if (threadIdx.x < 6) {  // a thread a sum
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) t += part[threadIdx.x][w];
+    part[threadIdx.x][0] = t;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < 6; ++m) out[m] = part[m][0];
+}
+
 // -------------------------------------------------------------- the count
 __device__ __forceinline__ int nonzero_bytes(uint32_t w) {
   return __popc((((w & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | w) & 0x80808080u);
@@ -139,47 +183,52 @@ __device__ __forceinline__ int shift_of(const PolicyArgs& a, int64_t row) {
 // Eight tokens of a lane, of the 256 from t0 on, of a sequence of T: two quads, or with
 // VEC = false every 32nd.
 template <bool VEC>
-__device__ __forceinline__ int64_t token_at(int64_t t0, int j) {
+__device__ __forceinline__ int token_at(int t0, int j) {
   const int lane = threadIdx.x & 31;
   return VEC ? t0 + 128 * (j / 4) + 4 * lane + j % 4 : t0 + 32 * j + lane;
 }
+// Their values, in pairs; 0 beside the sequence.
+struct Eight {
+  uint64_t v[kTokens / 2];
+  __device__ __forceinline__ float get(int j) const { return j % 2 ? of_pair(v[j / 2]).y : of_pair(v[j / 2]).x; }
+};
 template <bool VEC>
-__device__ __forceinline__ void load_tokens(const float* p, int64_t t0, int64_t T, float (&v)[kTokens]) {
+__device__ __forceinline__ void load_tokens(const float* p, int t0, int T, Eight& e) {
+  if (VEC && t0 >= 0 && t0 + kUnit <= T) {
+    const ulonglong2* q = reinterpret_cast<const ulonglong2*>(p + token_at<VEC>(t0, 0));
+    const ulonglong2 a = q[0], b = q[32];
+    e.v[0] = a.x, e.v[1] = a.y, e.v[2] = b.x, e.v[3] = b.y;
+  } else {
+    float v[kTokens];
 #pragma unroll
-  for (int j = 0; j < kTokens; j += 4) {
-    const int64_t t = token_at<VEC>(t0, j);
-    if (VEC && t >= 0 && t + 4 <= T) {
-      const float4 u = *reinterpret_cast<const float4*>(p + t);
-      v[j] = u.x, v[j + 1] = u.y, v[j + 2] = u.z, v[j + 3] = u.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t i = token_at<VEC>(t0, j + e);
-        v[j + e] = i >= 0 && i < T ? p[i] : 0.f;
-      }
+    for (int j = 0; j < kTokens; ++j) {
+      const int i = token_at<VEC>(t0, j);
+      v[j] = i >= 0 && i < T ? p[i] : 0.f;
     }
+#pragma unroll
+    for (int j = 0; j < kTokens / 2; ++j) e.v[j] = pair_of(v[2 * j], v[2 * j + 1]);
   }
 }
-// The mask of the same tokens, a bit each.
+// The mask of the same tokens, a byte each.
+struct Mask {
+  uint32_t w[2];
+  __device__ __forceinline__ bool operator[](int j) const { return (w[j / 4] & 0xFFu << 8 * (j % 4)) != 0; }
+};
 template <bool VEC>
-__device__ __forceinline__ uint32_t load_mask(const uint8_t* p, int64_t t0, int64_t T) {
-  uint32_t bits = 0;
+__device__ __forceinline__ Mask load_mask(const uint8_t* p, int t0, int T) {
+  Mask m;
+  if (VEC && t0 >= 0 && t0 + kUnit <= T) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p + token_at<VEC>(t0, 0));
+    m.w[0] = q[0], m.w[1] = q[32];
+  } else {
+    m.w[0] = m.w[1] = 0;
 #pragma unroll
-  for (int j = 0; j < kTokens; j += 4) {
-    const int64_t t = token_at<VEC>(t0, j);
-    if (VEC && t >= 0 && t + 4 <= T) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(p + t);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) bits |= (w >> (8 * e) & 0xFF) != 0 ? 1u << (j + e) : 0u;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t i = token_at<VEC>(t0, j + e);
-        if (i >= 0 && i < T && p[i] != 0) bits |= 1u << (j + e);
-      }
+    for (int j = 0; j < kTokens; ++j) {
+      const int i = token_at<VEC>(t0, j);
+      if (i >= 0 && i < T) m.w[j / 4] |= static_cast<uint32_t>(p[i]) << 8 * (j % 4);
     }
   }
-  return bits;
+  return m;
 }
 
 // Valid tokens of every piece of a sequence, and with a sequence's ratio the sum of w of
@@ -191,8 +240,9 @@ __device__ void count_phase(const PolicyArgs& a, int cta, int ctas) {
   const int64_t pieces = a.B * a.pieces, step = static_cast<int64_t>(ctas) * (thin ? kThreads : kWarps);
   double total[1] = {0.0};  // (whole numbers)
   for (int64_t i = static_cast<int64_t>(cta) * (thin ? kThreads : kWarps) + (thin ? threadIdx.x : threadIdx.x >> 5); i < pieces; i += step) {
-    const int64_t row = a.pieces == 1 ? i : i / a.pieces, from = (i - row * a.pieces) * kPiece - shift_of<VEC>(a, row);
-    const int64_t to = from + kPiece < a.T && a.pieces > 1 ? from + kPiece : a.T, t0 = from > 0 ? from : 0;
+    const int64_t row = a.pieces == 1 ? i : i / a.pieces;
+    const int T = static_cast<int>(a.T), from = static_cast<int>(i - row * a.pieces) * kPiece - shift_of<VEC>(a, row);
+    const int to = from + kPiece < T && a.pieces > 1 ? from + kPiece : T, t0 = from > 0 ? from : 0;
     const uint8_t* m = a.mask + row * a.ld_mask;
     const float *q = a.logp + row * a.ld_logp, *o = a.old + row * a.ld_old;
     int n = 0;
@@ -212,23 +262,22 @@ __device__ void count_phase(const PolicyArgs& a, int cta, int ctas) {
     } else if (WTOO) {
       Sum2 w;
 #pragma unroll 2
-      for (int64_t u = from; u < to; u += kUnit) {
-        float qs[kTokens], os[kTokens];
-        const uint32_t valid = load_mask<VEC>(m, u, to);
+      for (int u = from; u < to; u += kUnit) {
+        Eight qs, os;
+        const Mask valid = load_mask<VEC>(m, u, to);
         load_tokens<VEC>(q, u, to, qs);
         load_tokens<VEC>(o, u, to, os);
-        n += __popc(valid);
+        n += nonzero_bytes(valid.w[0]) + nonzero_bytes(valid.w[1]);
 #pragma unroll
         for (int j = 0; j < kTokens; ++j) {
-          const bool in = valid >> j & 1;
-          const float x = in ? qs[j] : 0.f, y = in ? os[j] : 0.f, s = __fsub_rn(x, y);
+          const float x = valid[j] ? qs.get(j) : 0.f, y = valid[j] ? os.get(j) : 0.f, s = __fsub_rn(x, y);
           w.add(s);
           w.lo += diff_error(x, y, s);
         }
       }
-      sum = warp_sum(w.value());
+      sum = warp_total(w);
     } else {
-      n = count_bytes(m + t0, static_cast<int>(to - t0), lane);
+      n = count_bytes(m + t0, to - t0, lane);
     }
     if (!thin) n = __reduce_add_sync(0xffffffffu, n);
     if (thin || lane == 0) {
@@ -245,13 +294,6 @@ __device__ void count_phase(const PolicyArgs& a, int cta, int ctas) {
 // --------------------------------------------------------------- the loss
 enum : int { S_LOSS, S_KL, S_RATIO, S_LOW, S_HIGH, S_VALID, S_ALL };
 enum : int { W_NONE, W_TOKEN, W_SEQUENCE };
-
-// A thread's sums.
-struct Sums {
-  Sum2 loss, kl, ratio;  // ratio: of r - 1
-  int low = 0, high = 0;
-  int64_t valid = 0;
-};
 
 // What holds the ratio of tokens of one advantage A: 1 + clip_high, or dual_clip for A < 0,
 // from above, and 1 - clip_low from below for A < 0. w rounds a difference (lo: what it
@@ -468,148 +510,185 @@ __device__ __forceinline__ void tokens(const PolicyArgs& a, In in, At at, RowOf 
   if (W == W_TOKEN) sums.ratio.add(rs);
 }
 
-// Eight tokens of a lane, all of one sequence.
-template <bool VEC, int W, bool REF, bool TADV>
-__device__ __forceinline__ void unit_tokens(const PolicyArgs& a, const Row& r, const Rows& g, int64_t t0, uint32_t valid, float (&q)[kTokens],
-                                            float (&o)[kTokens], float (&p)[kTokens], float (&A)[kTokens], Sums& sums) {
-  float d[kTokens];
-  // (the differences take the numbers' place: of masked tokens 0)
-  float most = 0.f;
-  bool far = false;
-#pragma unroll
-  for (int j = 0; j < kTokens; ++j) {
-    const bool in = valid >> j & 1;
-    if (REF) p[j] = in ? p[j] - q[j] : 0.f;
-    if (W == W_TOKEN) {
-      const float w = in ? __fsub_rn(q[j], o[j]) : 0.f;
-      o[j] = w;
-      far |= w == a.up_hi || w == a.down_hi || w == a.far_hi;
-      most = fmaxf(most, fabsf(w));
-    }
-    if (REF) most = fmaxf(most, fabsf(p[j]));
-    if (TADV) A[j] = in ? A[j] : 0.f;
+// Sums of a thread's tokens of one sequence, over its weight.
+struct RowSums {
+  uint64_t held, kl, ratio;  // pairs: of the held ratios less 1, of k, of r - 1
+  __device__ __forceinline__ void clear() { held = kl = ratio = pair_of(0.f); }
+};
+template <int W, bool REF, bool TADV>
+__device__ __forceinline__ void fold(const PolicyArgs& a, const Row& r, RowSums& s, Sums& sums) {
+  if (!TADV && W == W_TOKEN && r.A != 0.f) {
+    const float2 h = of_pair(s.held);
+    sums.loss.add_product(h.x + h.y, -r.c * r.A);
   }
-  const float cb = -r.c * a.beta;
-  if (far || most >= kFar) {  // numbers that the series does not take, or on a bound: one by one
-    float kls = 0.f, rs = 0.f, hs = 0.f;
-#pragma unroll
-    for (int j = 0; j < kTokens; ++j) {
-      d[j] = 0.f;
-      if (!(valid >> j & 1)) continue;
-      const int64_t t = token_at<VEC>(t0, j);
-      const float Aj = TADV ? A[j] : r.A;
-      Term x = far_token<W, REF>(a, r, Aj, W == W_TOKEN || REF ? g.q[t] : 0.f, W == W_TOKEN ? g.o[t] : 0.f, REF ? g.p[t] : 0.f);
+  if (REF) {
+    const float2 k = of_pair(s.kl);
+    sums.loss.add_product(k.x + k.y, r.c * a.beta);
+    sums.kl.add(k.x + k.y);
+  }
+  if (W == W_TOKEN) {
+    const float2 x = of_pair(s.ratio);
+    sums.ratio.add(x.x + x.y);
+  }
+  s.clear();
+}
+
+// Eight tokens of a lane, of one sequence, of which some are too far for the series or on a
+// bound: one by one. Their sums are returned, and the gradients written.
+struct FarSums {
+  float held, kl, ratio;
+  Sum2 loss;  // with an advantage for each token
+  int low, high;
+};
+template <bool VEC, int W, bool REF, bool TADV>
+__device__ __noinline__ FarSums far_tokens(const PolicyArgs& a, Row r, Rows g, int t0, Mask valid) {
+  FarSums s = {0.f, 0.f, 0.f, Sum2(), 0, 0};
+#pragma unroll 1
+  for (int j = 0; j < kTokens; ++j) {
+    const int t = token_at<VEC>(t0, j);
+    if (t < 0 || t >= a.T) continue;
+    Term x = {0.f, 0.f, 0.f, 0.f, false, false};
+    if (valid[j]) {
+      const float A = TADV ? g.A[t] : r.A, q = W == W_TOKEN || REF ? g.q[t] : 0.f, p = REF ? g.p[t] : 0.f;
+      x = far_token<W, REF>(a, r, A, q, W == W_TOKEN ? g.o[t] : 0.f, p);
       if (W == W_SEQUENCE) {
-        const int side = Aj == 0.f ? 0 : !TADV ? r.held : Aj > 0.f ? r.held & 3 : r.held >> 2;
+        const int side = A == 0.f ? 0 : !TADV ? r.held : A > 0.f ? r.held & 3 : r.held >> 2;
         if (side) {
-          x.d = REF ? cb * expm1f(p[j]) : 0.f;
-          x.held = side == 1 ? bounds_of(a, Aj).e_top : a.e_down;
+          x.d = REF ? -r.c * a.beta * expm1f(p - q) : 0.f;
+          x.held = side == 1 ? bounds_of(a, A).e_top : a.e_down;
           x.above = side == 1;
           x.below = side == 2;
         }
       }
-      d[j] = x.d;
-      if (TADV && Aj != 0.f) {
-        sums.loss.add_product(-Aj, r.c);
-        sums.loss.add_product(-Aj * x.held, r.c);
-      }
-      hs += x.held;
-      kls += x.kl;
-      rs += x.em1;
-      if (W == W_TOKEN || (W == W_SEQUENCE && TADV)) {
-        sums.low += x.below;
-        sums.high += x.above;
+      if (TADV && A != 0.f) {
+        s.loss.add_product(-A, r.c);
+        s.loss.add_product(-A * x.held, r.c);
       }
     }
-    if (!TADV && W == W_TOKEN && r.A != 0.f) sums.loss.add_product(hs, -r.c * r.A);
+    s.held += x.held;
+    s.kl += x.kl;
+    s.ratio += x.em1;
+    s.low += x.below;
+    s.high += x.above;
+    if (g.d) g.d[t] = x.d;
+  }
+  return s;
+}
+
+// Eight tokens of a lane, all of one sequence.
+template <bool VEC, int W, bool REF, bool TADV>
+__device__ __forceinline__ void unit_tokens(const PolicyArgs& a, const Row& r, const Bounds& b, const Rows& g, int t0, const Mask& valid, Eight& q,
+                                            Eight& o, Eight& p, Eight& A, RowSums& row, Sums& sums) {
+  // the differences, of masked tokens 0, in the numbers' place
+  const uint64_t minus = pair_of(-1.f);
+  float most = 0.f;
+  bool far = false;
+#pragma unroll
+  for (int j = 0; j < kTokens / 2; ++j) {
     if (REF) {
-      sums.loss.add_product(kls, -cb);
-      sums.kl.add(kls);
+      const float2 x = of_pair(fma2(q.v[j], minus, p.v[j]));
+      const float x0 = valid[2 * j] ? x.x : 0.f, x1 = valid[2 * j + 1] ? x.y : 0.f;
+      most = fmaxf(most, fmaxf(fabsf(x0), fabsf(x1)));
+      p.v[j] = pair_of(x0, x1);
     }
-    if (W == W_TOKEN) sums.ratio.add(rs);
-  } else {
-    Bounds b = bounds_of(a, r.A);
-    if (r.A == 0.f) b.top = INFINITY;  // (nothing to hold, or to count)
-    const float cA = r.A == 0.f ? 0.f : r.c * r.A;
-    uint64_t kls = pair_of(0.f), rs = kls, hs = kls;
+    if (W == W_TOKEN) {
+      const float2 w = of_pair(fma2(o.v[j], minus, q.v[j]));
+      const float w0 = valid[2 * j] ? w.x : 0.f, w1 = valid[2 * j + 1] ? w.y : 0.f;
+      most = fmaxf(most, fmaxf(fabsf(w0), fabsf(w1)));
+      if (TADV) far |= w0 == a.up_hi || w0 == a.down_hi || w0 == a.far_hi || w1 == a.up_hi || w1 == a.down_hi || w1 == a.far_hi;
+      else far |= w0 == b.top || w0 == b.bottom || w1 == b.top || w1 == b.bottom;
+      o.v[j] = pair_of(w0, w1);
+    }
+    if (TADV) A.v[j] = pair_of(valid[2 * j] ? A.get(2 * j) : 0.f, valid[2 * j + 1] ? A.get(2 * j + 1) : 0.f);
+  }
+  if (far || most >= kFar) {
+    const FarSums s = far_tokens<VEC, W, REF, TADV>(a, r, g, t0, valid);
+    row.held = add2(row.held, pair_of(s.held, 0.f));
+    row.kl = add2(row.kl, pair_of(s.kl, 0.f));
+    row.ratio = add2(row.ratio, pair_of(s.ratio, 0.f));
+    if (TADV) {
+      sums.loss.add(s.loss.hi);
+      sums.loss.lo += s.loss.lo;
+    }
+    if (W == W_TOKEN || (W == W_SEQUENCE && TADV)) {
+      sums.low += s.low;
+      sums.high += s.high;
+    }
+    return;
+  }
+  const float cb = -r.c * a.beta, cA = r.A == 0.f ? 0.f : r.c * r.A;
+  float d[kTokens];
 #pragma unroll
-    for (int j = 0; j < kTokens; j += 2) {
-      float em1[2] = {r.em1, r.em1}, ex[2], kl[2], held[2], dd[2];
+  for (int j = 0; j < kTokens; j += 2) {
+    float em1[2] = {r.em1, r.em1}, ex[2], kl[2], dd[2];
+    const float2 w = of_pair(o.v[j / 2]), x = of_pair(p.v[j / 2]);
+    if (W == W_TOKEN) {
+      float none[2];
+      exponentials<false>(w.x, w.y, em1, none);
+      row.ratio = add2(row.ratio, pair_of(em1[0], em1[1]));
+    }
+    if (REF) {
+      exponentials<true>(x.x, x.y, ex, kl);
+      row.kl = add2(row.kl, pair_of(kl[0], kl[1]));
+    }
+    if (!TADV) {
       if (W == W_TOKEN) {
-        float none[2];
-        exponentials<false>(o[j], o[j + 1], em1, none);
-        rs = add2(rs, pair_of(em1[0], em1[1]));
-      }
-      if (REF) {
-        exponentials<true>(p[j], p[j + 1], ex, kl);
-        kls = add2(kls, pair_of(kl[0], kl[1]));
-      }
-      if (!TADV) {
-        if (W == W_TOKEN) {
-          const float2 gr = of_pair(fma2(pair_of(em1[0], em1[1]), pair_of(-cA), pair_of(-cA)));
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const bool above = o[j + e] > b.top, below = o[j + e] < b.bottom;
-            held[e] = above ? b.e_top : below ? a.e_down : em1[e];
-            dd[e] = above || below ? 0.f : e ? gr.y : gr.x;
-            sums.high += above;
-            sums.low += below;
-          }
-          hs = add2(hs, pair_of(held[0], held[1]));
-        } else {
-          dd[0] = dd[1] = r.A == 0.f || (W == W_SEQUENCE && r.held) ? 0.f : -fmaf(cA, r.em1, cA);
-        }
-      } else {
+        const float2 gr = of_pair(fma2(pair_of(em1[0], em1[1]), pair_of(-cA), pair_of(-cA)));
+        float held[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float Aj = A[j + e], cAj = r.c * Aj;
-          const Bounds bj = bounds_of(a, Aj);
-          bool above = false, below = false;
-          if (W == W_TOKEN) {
-            above = o[j + e] > bj.top;
-            below = o[j + e] < bj.bottom;
-          } else if (W == W_SEQUENCE) {
-            const int side = Aj > 0.f ? r.held & 3 : r.held >> 2;
-            above = side == 1;
-            below = side == 2;
-          }
-          const bool some = Aj != 0.f;
-          held[e] = above ? bj.e_top : below ? a.e_down : em1[e];
-          dd[e] = above || below || !some ? 0.f : -fmaf(cAj, em1[e], cAj);
-          sums.high += some && above;
-          sums.low += some && below;
-          // c A in full, and of it what the ratio adds
-          sums.loss.add_product(-Aj, r.c);
-          sums.loss.add(some ? -cAj * held[e] : 0.f);
+          const float we = e ? w.y : w.x;
+          const bool above = we > b.top, below = we < b.bottom;
+          held[e] = above ? b.e_top : below ? a.e_down : em1[e];
+          dd[e] = above || below ? 0.f : e ? gr.y : gr.x;
+          if (above) ++sums.high;
+          if (below) ++sums.low;
         }
+        row.held = add2(row.held, pair_of(held[0], held[1]));
+      } else {
+        dd[0] = dd[1] = r.A == 0.f || (W == W_SEQUENCE && r.held) ? 0.f : -fmaf(cA, r.em1, cA);
       }
-      if (REF) {
-        const float2 t = of_pair(fma2(pair_of(ex[0], ex[1]), pair_of(cb), pair_of(dd[0], dd[1])));
-        dd[0] = t.x, dd[1] = t.y;
-      }
-      d[j] = valid >> j & 1 ? dd[0] : 0.f;
-      d[j + 1] = valid >> (j + 1) & 1 ? dd[1] : 0.f;
-    }
-    const float2 h = of_pair(hs), k = of_pair(kls), x = of_pair(rs);
-    if (!TADV && W == W_TOKEN) sums.loss.add_product(h.x + h.y, -cA);
-    if (REF) {
-      sums.loss.add_product(k.x + k.y, -cb);
-      sums.kl.add(k.x + k.y);
-    }
-    if (W == W_TOKEN) sums.ratio.add(x.x + x.y);
-  }
-  if (!g.d) return;
-#pragma unroll
-  for (int j = 0; j < kTokens; j += 4) {
-    const int64_t t = token_at<VEC>(t0, j);
-    if (VEC && t >= 0 && t + 4 <= a.T) {
-      *reinterpret_cast<float4*>(g.d + t) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t i = token_at<VEC>(t0, j + e);
-        if (i >= 0 && i < a.T) g.d[i] = d[j + e];
+      for (int e = 0; e < 2; ++e) {
+        const float Aj = A.get(j + e), cAj = r.c * Aj, we = e ? w.y : w.x;
+        const Bounds bj = bounds_of(a, Aj);
+        bool above = false, below = false;
+        if (W == W_TOKEN) {
+          above = we > bj.top;
+          below = we < bj.bottom;
+        } else if (W == W_SEQUENCE) {
+          const int side = Aj > 0.f ? r.held & 3 : r.held >> 2;
+          above = side == 1;
+          below = side == 2;
+        }
+        const bool some = Aj != 0.f;
+        const float held = above ? bj.e_top : below ? a.e_down : em1[e];
+        dd[e] = above || below || !some ? 0.f : -fmaf(cAj, em1[e], cAj);
+        if (some && above) ++sums.high;
+        if (some && below) ++sums.low;
+        // c A in full, and of it what the ratio adds
+        sums.loss.add_product(-Aj, r.c);
+        sums.loss.lo += some ? -cAj * held : 0.f;
       }
+    }
+    if (REF) {
+      const float2 t = of_pair(fma2(pair_of(ex[0], ex[1]), pair_of(cb), pair_of(dd[0], dd[1])));
+      dd[0] = t.x, dd[1] = t.y;
+    }
+    d[j] = valid[j] ? dd[0] : 0.f;
+    d[j + 1] = valid[j + 1] ? dd[1] : 0.f;
+  }
+  if (!g.d) return;
+  if (VEC && t0 >= 0 && t0 + kUnit <= a.T) {
+    float4* to = reinterpret_cast<float4*>(g.d + token_at<VEC>(t0, 0));
+    to[0] = make_float4(d[0], d[1], d[2], d[3]);
+    to[32] = make_float4(d[4], d[5], d[6], d[7]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+      const int i = token_at<VEC>(t0, j);
+      if (i >= 0 && i < a.T) g.d[i] = d[j];
     }
   }
 }
@@ -625,27 +704,32 @@ __device__ __forceinline__ void long_rows(const PolicyArgs& a, int cta, int ctas
   if (u0 >= u1) return;
   int64_t row = u0 / units, piece = -1;
   int unit = static_cast<int>(u0 - row * units), here = 0;
-  Row r = {same, 0.f, 0.f, 0};
+  const int T = static_cast<int>(a.T);
+  Row r = {0.f, 0.f, 0.f, 0};  // (no token yet)
+  Bounds b = {INFINITY, -INFINITY, 0.f};
+  RowSums row_sums;
+  row_sums.clear();
   bool fresh = true;
   for (int64_t u = u0; u < u1; ++u) {
-    const int64_t t0 = static_cast<int64_t>(unit) * kUnit - shift_of<VEC>(a, row);
+    const int t0 = unit * kUnit - shift_of<VEC>(a, row);
     const int64_t now = row * a.pieces + (a.pieces > 1 ? unit / (kPiece / kUnit) : 0);
     if (now != piece) {
       piece = now;
       here = a.piece_count[piece];
     }
     const Rows g = rows_of<W, REF, TADV>(a, row, 0);
-    float q[kTokens], o[kTokens], p[kTokens], A[kTokens];
-    uint32_t valid = 0;
+    Eight q, o, p, A;
+    Mask valid = {{0, 0}};
     if (here > 0) {
-      valid = load_mask<VEC>(g.mask, t0, a.T);
-      if (W == W_TOKEN || REF) load_tokens<VEC>(g.q, t0, a.T, q);
-      if (W == W_TOKEN) load_tokens<VEC>(g.o, t0, a.T, o);
-      if (REF) load_tokens<VEC>(g.p, t0, a.T, p);
-      if (TADV) load_tokens<VEC>(g.A, t0, a.T, A);
+      valid = load_mask<VEC>(g.mask, t0, T);
+      if (W == W_TOKEN || REF) load_tokens<VEC>(g.q, t0, T, q);
+      if (W == W_TOKEN) load_tokens<VEC>(g.o, t0, T, o);
+      if (REF) load_tokens<VEC>(g.p, t0, T, p);
+      if (TADV) load_tokens<VEC>(g.A, t0, T, A);
     }
     if (fresh && here > 0) {
       fresh = false;
+      fold<W, REF, TADV>(a, r, row_sums, sums);
       int n = 0;
       double w = 0.0;
       if (a.reduce == 0 || W == W_SEQUENCE) {
@@ -657,16 +741,18 @@ __device__ __forceinline__ void long_rows(const PolicyArgs& a, int cta, int ctas
         if (W == W_SEQUENCE) w = warp_sum(w);
       }
       r = row_of<W, TADV>(a, same, row, n, w);
+      b = bounds_of(a, r.A);
+      if (r.A == 0.f) b.top = INFINITY;  // (nothing to hold, or to count)
     }
     if (here > 0) {
       // (what the piece's tokens share is added with its first unit)
       if (lane == 0 && (a.pieces > 1 ? unit % (kPiece / kUnit) : unit) == 0) add_row<W, TADV>(a, r, here, sums);
-      unit_tokens<VEC, W, REF, TADV>(a, r, g, t0, valid, q, o, p, A, sums);
+      unit_tokens<VEC, W, REF, TADV>(a, r, b, g, t0, valid, q, o, p, A, row_sums, sums);
     } else if (g.d) {  // nothing but the gradient's zeros
 #pragma unroll
       for (int j = 0; j < kTokens; ++j) {
-        const int64_t i = token_at<VEC>(t0, j);
-        if (i >= 0 && i < a.T) g.d[i] = 0.f;
+        const int i = token_at<VEC>(t0, j);
+        if (i >= 0 && i < T) g.d[i] = 0.f;
       }
     }
     if (++unit == units) {
@@ -675,6 +761,7 @@ __device__ __forceinline__ void long_rows(const PolicyArgs& a, int cta, int ctas
       fresh = true;
     }
   }
+  fold<W, REF, TADV>(a, r, row_sums, sums);
 }
 
 // Short sequences, several whole ones a chunk; what they share stands in shared memory.
@@ -724,13 +811,8 @@ __device__ void loss_phase(const PolicyArgs& a, int cta, int ctas, double (&out)
   Sums sums;
   if (a.T < kShort) short_rows<W, REF, TADV>(a, cta, ctas, same, sums);
   else long_rows<VEC, W, REF, TADV>(a, cta, ctas, same, sums);
-  out[S_LOSS] = sums.loss.value();
-  out[S_KL] = sums.kl.value();
-  out[S_RATIO] = sums.ratio.value();
-  out[S_LOW] = sums.low;
-  out[S_HIGH] = sums.high;
-  out[S_VALID] = static_cast<double>(sums.valid);
-  cta_sums(out);
+  static_assert(S_ALL == 6 && S_LOSS == 0 && S_KL == 1 && S_RATIO == 2 && S_LOW == 3 && S_HIGH == 4 && S_VALID == 5, "");
+  cta_total(sums, out);
 }
 
 // By the first thread of the CTA that has every CTA's sums.
@@ -746,13 +828,13 @@ __device__ void finish(const PolicyArgs& a, const double (&sums)[S_ALL]) {
 }
 
 template <bool VEC, bool WTOO>
-__global__ void __launch_bounds__(kThreads) k_policy_count(PolicyArgs a) {
+__global__ void __launch_bounds__(kThreads) k_policy_count(const __grid_constant__ PolicyArgs a) {
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   count_phase<VEC, WTOO>(a, blockIdx.x, gridDim.x);
 }
 
 template <bool VEC, int W, bool REF, bool TADV>
-__global__ void __launch_bounds__(kThreads, kLossCtas) k_policy_loss(PolicyArgs a) {
+__global__ void __launch_bounds__(kThreads, kLossCtas) k_policy_loss(const __grid_constant__ PolicyArgs a) {
   __shared__ bool s_last;
   double sums[S_ALL];
   loss_phase<VEC, W, REF, TADV>(a, blockIdx.x, gridDim.x, sums);
@@ -776,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, kLossCtas) k_policy_loss(PolicyArgs 
 
 // Both for few tokens.
 template <bool VEC, int W, bool REF, bool TADV>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) k_policy_small(PolicyArgs a) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) k_policy_small(const __grid_constant__ PolicyArgs a) {
   __shared__ double parts[kCluster][S_ALL];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());

@@ -37,7 +37,7 @@ grpo_status policy_args(const grpo_policy_problem* p, PolicyArgs* a) {
   if (p->reduce < 0 || p->reduce > 2) return GRPO_ERR_INVALID_ARG;
   if (p->token_adv != 0 && p->token_adv != 1) return GRPO_ERR_INVALID_ARG;
   if (p->reduce == 2 && !(p->divisor > 0.0 && isfinite(p->divisor))) return GRPO_ERR_INVALID_ARG;
-  if (p->num_seqs > kMaxRows || p->seq_len > kMaxRows ||
+  if (p->num_seqs > kMaxRows || p->seq_len > kMaxRows - 4095 ||
       p->num_seqs * p->seq_len > static_cast<int64_t>(1) << 40)
     return GRPO_ERR_UNSUPPORTED;
   *a = PolicyArgs();

@@ -515,8 +515,8 @@ grpo_status grpo_adamw_step(const grpo_adamw_config *config, const grpo_adamw_te
  * Row strides ld_* in elements. dlogp may be logp, logp_old, logp_ref or adv [B, T] (same
  * stride). Sums are float64 in a fixed order: results do not vary between calls. B = 0 or T = 0: loss and stats are 0. INVALID_ARG for null pointers,
  * sizes below 0, a stride below T, bounds, beta or divisor outside the above or NaN;
- * UNSUPPORTED for B or T of 2^31 or more, B T above 2^40, and pointers off their element's
- * alignment.
+ * UNSUPPORTED for B of 2^31 or more, T above 2^31 - 4096, B T above 2^40, and pointers off
+ * their element's alignment.
  */
 typedef struct grpo_policy_problem {
   int64_t num_seqs, seq_len;
