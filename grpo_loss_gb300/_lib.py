@@ -7,7 +7,10 @@ the first call raises.
 from __future__ import annotations
 
 import ctypes
+import math
+import operator
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -101,13 +104,6 @@ class ResidualNormProblem(ctypes.Structure):
 class GradTensor(ctypes.Structure):
     """Mirror of ``grpo_grad_tensor``."""
     _fields_ = [("n", ctypes.c_int64), ("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("dtype", ctypes.c_int32)]
-
-
-# The same as columns of an array.
-GRAD_COLUMNS = np.dtype({"names": ["n", "grad", "out", "dtype"], "formats": [np.int64, np.uint64, np.uint64, np.int32],
-                         "offsets": [GradTensor.n.offset, GradTensor.grad.offset, GradTensor.out.offset,
-                                     GradTensor.dtype.offset],
-                         "itemsize": ctypes.sizeof(GradTensor)})
 
 
 def make_problem(num_seqs: int, seq_len: int, d: int, V: int, group_size: int,
@@ -570,8 +566,16 @@ def adamw_step(config: AdamwConfig, tensors, out, n: int, device, stream=None) -
     _call(lib().grpo_adamw_step, "grpo_adamw_step", device, stream, config, tensors, out, n)
 
 
-def _bytes(fn, where: str, dev, *args) -> int:
-    """A workspace's size, asked with ``dev`` current."""
+_sizes = {}
+
+
+def _bytes(key, fn, where: str, dev, *args) -> int:
+    """A workspace's size, asked with ``dev`` current, once for each ``key`` (what it depends
+    on) and device."""
+    key = key, dev.index
+    size = _sizes.get(key)
+    if size is not None:
+        return size
     b = ctypes.c_size_t(0)
     if torch._C._cuda_getDevice() == dev.index:
         status = fn(*args, ctypes.byref(b))
@@ -580,14 +584,19 @@ def _bytes(fn, where: str, dev, *args) -> int:
             status = fn(*args, ctypes.byref(b))
     if status != GRPO_OK:
         raise GrpoError(status, where)
+    if len(_sizes) >= 4096:
+        _sizes.clear()
+    _sizes[key] = b.value
     return b.value
 
 
-def _workspace(workspace, size, dev):
-    """(tensor, pointer, bytes) of a workspace that is given or made of ``size()`` bytes."""
+def _workspace(workspace, size: int, dev):
+    """(tensor, pointer, bytes) of a workspace that is given or made of ``size`` bytes."""
     if workspace is None:
-        workspace = torch.empty(size(), dtype=torch.uint8, device=dev)
-        return workspace, workspace.data_ptr(), workspace.numel()
+        if not size:
+            return None, None, 0
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), size
     return workspace, _vec_ptr(workspace, "workspace", workspace.dtype, workspace.numel(), dev), workspace.nbytes
 
 
@@ -651,8 +660,9 @@ def policy_loss(logp: torch.Tensor, advantages: torch.Tensor, mask: torch.Tensor
     problem = PolicyProblem(B, T, ld, ld_old, ld_ref, ld_adv, ld_mask, ld_d, clip[0], clip[1], dual_clip or 0.0, beta,
                             divisor or 0.0, _RATIOS[ratio], _REDUCES[reduce], 1 if per_token else 0)
     L = lib()
-    _, wp, size = _workspace(workspace, lambda: _bytes(L.grpo_policy_loss_workspace_size,
-                                                       "grpo_policy_loss_workspace_size", dev, problem), dev)
+    size = 0 if workspace is not None else _bytes(("policy", B, T, ratio), L.grpo_policy_loss_workspace_size,
+                                                  "grpo_policy_loss_workspace_size", dev, problem)
+    workspace, wp, size = _workspace(workspace, size, dev)
     _call(L.grpo_policy_loss, "grpo_policy_loss", dev, None, problem, lp, op, rp, ap, mp, out, sp, dp, wp, size)
     _written(given)
     return loss, dlogp, stats
@@ -809,8 +819,10 @@ def residual_norm_bwd(dy: torch.Tensor, dh, h: torch.Tensor, weight: torch.Tenso
     L = lib()
     wsp, size = None, 0
     if wp or bp or pwp or pbp or (dgp and gate_rows > 1):
-        workspace, wsp, size = _workspace(workspace, lambda: _bytes(
-            L.grpo_residual_norm_workspace_size, "grpo_residual_norm_workspace_size", dev, problem), dev)
+        if workspace is None:
+            size = _bytes(("residual_norm", rows, d), L.grpo_residual_norm_workspace_size,
+                          "grpo_residual_norm_workspace_size", dev, problem)
+        workspace, wsp, size = _workspace(workspace, size, dev)
     _call(L.grpo_residual_norm_bwd, "grpo_residual_norm_bwd", dev, None, problem, yp, zp, hp,
           _vec_ptr(weight, "weight", pt, d, dev), None if rms else _vec_ptr(mean, "mean", f32, rows, dev),
           _vec_ptr(rstd, "rstd", f32, rows, dev), xp, _vec_ptr(post_weight, "post_weight", pt, d, dev),
@@ -824,69 +836,74 @@ def residual_norm_bwd(dy: torch.Tensor, dh, h: torch.Tensor, weight: torch.Tenso
 
 _PLAIN = {torch.float32: GRPO_F32, torch.bfloat16: GRPO_BF16}
 _NORM_TYPES = {2: 2, float("inf"): 0}
-_get = torch.Tensor
+_TENSOR = torch.Tensor
+_DTYPE_OF, _SHAPE_OF = operator.attrgetter("dtype"), operator.attrgetter("shape")
+_GRAD_PACKS = {}
+
+
+def _refuse_grads(grads, out, name: str) -> None:
+    """The error of a list that is not contiguous float32 or bf16 CUDA tensors of one device,
+    or of an ``out`` that is not alike."""
+    for i, t in enumerate(grads):
+        if not torch.is_tensor(t):
+            raise ValueError("%s[%d] must be a tensor, got %r" % (name, i, type(t)))
+        _plain_code(t.dtype, "%s[%d]" % (name, i))
+        _device_of(t, "%s[%d]" % (name, i))
+        _vec_ptr(t, "%s[%d]" % (name, i), t.dtype, t.numel(), grads[0].device)
+    for i, (t, g) in enumerate(zip(out or (), grads)):
+        if not torch.is_tensor(t) or t.dtype != g.dtype or t.shape != g.shape or t.device != g.device or \
+                not t.is_contiguous():
+            raise ValueError("out[%d] must be contiguous, of %s[%d]'s shape %s and type %s, on %s" % (
+                i, name, i, tuple(g.shape), g.dtype, g.device))
 
 
 def _grad_table(grads, out, name: str):
-    """(columns of GradTensor, device) of a list of gradients."""
+    """(an array of GradTensor, sizes, gradients' and outs' addresses, types, device)."""
     n = len(grads)
-    table = np.zeros(n, dtype=GRAD_COLUMNS)
     if not n:
-        return table, None
+        return b"", [], [], [], [], None
+    if out is not None and len(out) != n:
+        raise ValueError("expected %d tensors in out, got %d" % (n, len(out)))
     try:
-        dev = grads[0].device
-        at = grads[0].get_device()
-        good = at >= 0 and all(map(_get.is_contiguous, grads)) and not any(map(at.__ne__, map(_get.get_device, grads)))
-        table["dtype"] = [_PLAIN[t.dtype] for t in grads]
-    except (AttributeError, TypeError, KeyError):
+        at, types = grads[0].get_device(), list(map(_DTYPE_OF, grads))
+        codes = list(map(_PLAIN.__getitem__, types))
+        good = at >= 0 and all(map(_TENSOR.is_contiguous, grads)) and \
+            not any(map(at.__ne__, map(_TENSOR.get_device, grads)))
+        if out is not None:
+            good = good and list(map(_DTYPE_OF, out)) == types and list(map(_SHAPE_OF, out)) == \
+                list(map(_SHAPE_OF, grads)) and all(map(_TENSOR.is_contiguous, out)) and \
+                not any(map(at.__ne__, map(_TENSOR.get_device, out)))
+    except (AttributeError, TypeError, KeyError):       # not tensors, or of other types
         good = False
     if not good:
-        for i, t in enumerate(grads):
-            if not torch.is_tensor(t):
-                raise ValueError("%s[%d] must be a tensor, got %r" % (name, i, type(t)))
-            _plain_code(t.dtype, "%s[%d]" % (name, i))
-            _device_of(t, "%s[%d]" % (name, i))
-            _vec_ptr(t, "%s[%d]" % (name, i), t.dtype, t.numel(), grads[0].device)
-    table["n"] = list(map(_get.numel, grads))
-    table["grad"] = list(map(_get.data_ptr, grads))
-    if out is None:
-        table["out"] = table["grad"]
-    else:
-        if len(out) != n:
-            raise ValueError("expected %d tensors in out, got %d" % (n, len(out)))
-        for i, (t, g) in enumerate(zip(out, grads)):
-            if not torch.is_tensor(t) or t.dtype != g.dtype or t.shape != g.shape or t.device != dev or \
-                    not t.is_contiguous():
-                raise ValueError("out[%d] must be contiguous, of %s[%d]'s shape %s and type %s, on %s" % (
-                    i, name, i, tuple(g.shape), g.dtype, dev))
-        table["out"] = list(map(_get.data_ptr, out))
-    return table, dev
+        _refuse_grads(grads, out, name)
+    sizes, places = list(map(_TENSOR.numel, grads)), list(map(_TENSOR.data_ptr, grads))
+    outs = places if out is None else list(map(_TENSOR.data_ptr, out))
+    pack = _GRAD_PACKS.get(n)
+    if pack is None:
+        pack = _GRAD_PACKS[n] = struct.Struct("@" + "qQQi4x" * n)
+    flat = [0] * (4 * n)
+    flat[0::4], flat[1::4], flat[2::4], flat[3::4] = sizes, places, outs, codes
+    return pack.pack(*flat), sizes, places, outs, codes, grads[0].device
 
 
-def _no_overlap(table, given: bool) -> None:
-    """A clipped tensor is written: no other may share its bytes."""
-    sizes = table["n"].astype(np.uint64) * np.where(table["dtype"] == GRPO_F32, 4, 2).astype(np.uint64)
-    some = sizes > 0
-    starts, sizes, index = table["out"][some], sizes[some], np.flatnonzero(some)
-    if given:           # the gradients too, but for those that are their own out
-        own = table["grad"][some] == starts
-        starts, sizes = np.concatenate([starts, table["grad"][some][~own]]), np.concatenate([sizes, sizes[~own]])
-        index = np.concatenate([index, index[~own]])
-        written = np.arange(len(starts)) < int(some.sum())
-    else:
-        written = np.ones(len(starts), dtype=bool)
-    order = np.argsort(starts, kind="stable")
-    ends = np.maximum.accumulate((starts + sizes)[order])
-    # two gradients that are only read may share theirs
-    if np.any(starts[order][1:] < ends[:-1]):
-        last_written = last_any = 0
-        for i in order:
-            if starts[i] < (last_any if written[i] else last_written):
-                raise ValueError("the gradient or out of number %d overlaps another: what is written is one tensor's own"
-                                 % index[i])
-            end = int(starts[i] + sizes[i])
-            last_any = max(last_any, end)
-            last_written = max(last_written, end) if written[i] else last_written
+def _no_overlap(sizes, places, outs, codes) -> None:
+    """A clipped tensor is written: no other may share its bytes (two gradients that are only
+    read may share theirs)."""
+    spans = [(o, o + (n << 2 if c == GRPO_F32 else n << 1), True, i)
+             for i, (n, o, c) in enumerate(zip(sizes, outs, codes)) if n]
+    if outs is not places:
+        spans += [(p, p + (n << 2 if c == GRPO_F32 else n << 1), False, i)
+                  for i, (n, p, o, c) in enumerate(zip(sizes, places, outs, codes)) if n and p != o]
+    spans.sort()
+    last = last_written = 0
+    for start, end, written, i in spans:
+        if start < last and (written or start < last_written):
+            raise ValueError("the gradient or out of number %d overlaps another: what is written is one tensor's own" % i)
+        if end > last:
+            last = end
+        if written and end > last_written:
+            last_written = end
 
 
 def _grad_call(grads, clip: bool, max_norm, norm_type, eps, out, norm, factor, workspace):
@@ -895,23 +912,25 @@ def _grad_call(grads, clip: bool, max_norm, norm_type, eps, out, norm, factor, w
         raise ValueError("norm_type must be 2 or inf, got %r" % (norm_type,))
     if max_norm is not None and not max_norm >= 0.0:
         raise ValueError("max_norm must not be negative, got %r" % (max_norm,))
-    table, dev = _grad_table(grads, out, "grads")
+    table, sizes, places, outs, codes, dev = _grad_table(grads, out, "grads")
     if dev is None:
         given = norm if norm is not None else factor
         dev = given.device if given is not None else torch.device("cuda", torch.cuda.current_device())
     given = norm, factor
-    norm, np_ = _vec_out(norm, "norm", torch.float32, 1, dev)
-    fp = None
-    if factor is not None or max_norm is not None:
-        factor, fp = _vec_out(factor, "factor", torch.float32, 1, dev)
+    norm, at_norm = _vec_out(norm, "norm", torch.float32, 1, dev)
+    at_factor = None
+    if clip or factor is not None or max_norm is not None:
+        factor, at_factor = _vec_out(factor, "factor", torch.float32, 1, dev)
     if clip:
-        _no_overlap(table, out is not None)
-    L = lib()
-    _, wp, size = _workspace(workspace, lambda: _bytes(L.grpo_grad_norm_workspace_size,
-                                                       "grpo_grad_norm_workspace_size", dev), dev)
+        _no_overlap(sizes, places, outs, codes)
+    L, size, n = lib(), 0, len(sizes)
+    # (one launch takes a short list, with no workspace)
+    if workspace is None and not (0 < n <= 8 and sum(sizes) <= 65536 and all(sizes)):
+        size = _bytes("grad_norm", L.grpo_grad_norm_workspace_size, "grpo_grad_norm_workspace_size", dev)
+    workspace, wp, size = _workspace(workspace, size, dev)
     name = "grpo_clip_grad_norm" if clip else "grpo_grad_norm"
-    _call(L.grpo_clip_grad_norm if clip else L.grpo_grad_norm, name, dev, None, table.ctypes.data, len(grads),
-          _NORM_TYPES[norm_type], float("inf") if max_norm is None else max_norm, eps, np_, fp, wp, size)
+    _call(L.grpo_clip_grad_norm if clip else L.grpo_grad_norm, name, dev, None, table, n, _NORM_TYPES[norm_type],
+          math.inf if max_norm is None else max_norm, eps, at_norm, at_factor, wp, size)
     _written(given, (grads if out is None else out) if clip else ())
     return norm, factor
 

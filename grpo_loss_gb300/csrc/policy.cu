@@ -22,7 +22,7 @@ constexpr int kTokens = 8;               // of a thread at a time: their loads a
 constexpr int kPiece = 2048;             // tokens of a sequence that are counted together
 constexpr int kUnit = 32 * kTokens;      // tokens that a warp takes at a time
 constexpr int kChunk = kThreads * kTokens;  // of short sequences, that a CTA takes at a time
-constexpr int kShort = 64;               // sequences below this are taken several a warp
+constexpr int kShort = 128;              // sequences below this are taken several a warp
 constexpr int kLossCtas = 3;             // of an SM, at a time
 constexpr int kCluster = 8;
 constexpr int64_t kSmall = 16 * kChunk;  // tokens that one cluster takes
@@ -231,10 +231,19 @@ __device__ __forceinline__ Mask load_mask(const uint8_t* p, int t0, int T) {
   return m;
 }
 
+// Where the counts are: in the workspace, or in the shared memory of every CTA of a cluster.
+struct Counts {
+  int* n;         // of every piece
+  double* w;      // sums of w
+  int64_t* cta;   // totals of the CTAs that counted
+};
+constexpr int kSmallPieces = 1024;  // that shared memory holds
+
 // Valid tokens of every piece of a sequence, and with a sequence's ratio the sum of w of
-// these: a warp a piece. Sequences of few tokens: a thread each.
-template <bool VEC, bool WTOO>
-__device__ void count_phase(const PolicyArgs& a, int cta, int ctas) {
+// these: a warp a piece. Sequences of few tokens: a thread each. put(pointer, i, value)
+// writes a count.
+template <bool VEC, bool WTOO, typename Put>
+__device__ void count_phase(const PolicyArgs& a, const Counts& to_counts, int cta, int ctas, Put put) {
   const int lane = threadIdx.x & 31;
   const bool thin = a.T < 16;
   const int64_t pieces = a.B * a.pieces, step = static_cast<int64_t>(ctas) * (thin ? kThreads : kWarps);
@@ -275,20 +284,19 @@ __device__ void count_phase(const PolicyArgs& a, int cta, int ctas) {
           w.lo += diff_error(x, y, s);
         }
       }
-      sum = warp_total(w);
+      sum = __shfl_sync(0xffffffffu, warp_total(w), 0);
     } else {
       n = count_bytes(m + t0, to - t0, lane);
     }
     if (!thin) n = __reduce_add_sync(0xffffffffu, n);
-    if (thin || lane == 0) {
-      a.piece_count[i] = n;
-      if (WTOO) a.piece_w[i] = sum;
-      total[0] += n;
-    }
+    put(to_counts.n, i, n, thin);
+    if (WTOO) put(to_counts.w, i, sum, thin);
+    if (thin || lane == 0) total[0] += n;
   }
   if (a.reduce != 1) return;
   cta_sums(total);
-  if (threadIdx.x == 0) a.cta_count[cta] = static_cast<int64_t>(total[0]);
+  total[0] = __shfl_sync(0xffffffffu, total[0], 0);
+  if (threadIdx.x < 32) put(to_counts.cta, cta, static_cast<int64_t>(total[0]), false);
 }
 
 // --------------------------------------------------------------- the loss
@@ -696,7 +704,7 @@ __device__ __forceinline__ void unit_tokens(const PolicyArgs& a, const Row& r, c
 // A warp takes a run of units of its own, so that what a sequence shares is mostly known
 // from the unit before, and no warp waits for another.
 template <bool VEC, int W, bool REF, bool TADV>
-__device__ __forceinline__ void long_rows(const PolicyArgs& a, int cta, int ctas, float same, Sums& sums) {
+__device__ __forceinline__ void long_rows(const PolicyArgs& a, const Counts& counts, int cta, int ctas, float same, Sums& sums) {
   const int lane = threadIdx.x & 31;
   const int64_t units = units_of(a, VEC), all = a.B * units;  // of a sequence, and of all
   const int64_t warps = static_cast<int64_t>(ctas) * kWarps, warp = static_cast<int64_t>(cta) * kWarps + (threadIdx.x >> 5);
@@ -715,7 +723,7 @@ __device__ __forceinline__ void long_rows(const PolicyArgs& a, int cta, int ctas
     const int64_t now = row * a.pieces + (a.pieces > 1 ? unit / (kPiece / kUnit) : 0);
     if (now != piece) {
       piece = now;
-      here = a.piece_count[piece];
+      here = counts.n[piece];
     }
     const Rows g = rows_of<W, REF, TADV>(a, row, 0);
     Eight q, o, p, A;
@@ -734,8 +742,8 @@ __device__ __forceinline__ void long_rows(const PolicyArgs& a, int cta, int ctas
       double w = 0.0;
       if (a.reduce == 0 || W == W_SEQUENCE) {
         for (int64_t i = lane; i < a.pieces; i += 32) {
-          n += a.piece_count[row * a.pieces + i];
-          if (W == W_SEQUENCE) w += a.piece_w[row * a.pieces + i];
+          n += counts.n[row * a.pieces + i];
+          if (W == W_SEQUENCE) w += counts.w[row * a.pieces + i];
         }
         n = __reduce_add_sync(0xffffffffu, n);
         if (W == W_SEQUENCE) w = warp_sum(w);
@@ -766,7 +774,7 @@ __device__ __forceinline__ void long_rows(const PolicyArgs& a, int cta, int ctas
 
 // Short sequences, several whole ones a chunk; what they share stands in shared memory.
 template <int W, bool REF, bool TADV>
-__device__ __forceinline__ void short_rows(const PolicyArgs& a, int cta, int ctas, float same, Sums& sums) {
+__device__ __forceinline__ void short_rows(const PolicyArgs& a, const Counts& counts, int cta, int ctas, float same, Sums& sums) {
   __shared__ Row s_row[kChunk];
   const int len = static_cast<int>(a.T), per = kChunk / len;
   const uint32_t inverse = len > 1 ? static_cast<uint32_t>(0x100000000ull / len) + 1 : 0;  // i / len = i inverse / 2^32 for i < 2^16
@@ -774,10 +782,10 @@ __device__ __forceinline__ void short_rows(const PolicyArgs& a, int cta, int cta
     const int rows = static_cast<int>(a.B - row0 < per ? a.B - row0 : per), all = rows * len;
     __syncthreads();  // the last chunk's rows have been read
     for (int i = threadIdx.x; i < rows; i += kThreads) {
-      const int n = a.piece_count[row0 + i];
+      const int n = counts.n[row0 + i];
       Row r = {0.f, 0.f, 0.f, 0};
       if (n > 0) {
-        r = row_of<W, TADV>(a, same, row0 + i, n, W == W_SEQUENCE ? a.piece_w[row0 + i] : 0.0);
+        r = row_of<W, TADV>(a, same, row0 + i, n, W == W_SEQUENCE ? counts.w[row0 + i] : 0.0);
         add_row<W, TADV>(a, r, n, sums);
       }
       s_row[i] = r;
@@ -797,20 +805,20 @@ __device__ __forceinline__ void short_rows(const PolicyArgs& a, int cta, int cta
 }
 
 template <bool VEC, int W, bool REF, bool TADV>
-__device__ void loss_phase(const PolicyArgs& a, int cta, int ctas, double (&out)[S_ALL]) {
+__device__ void loss_phase(const PolicyArgs& a, const Counts& counts, int cta, int ctas, double (&out)[S_ALL]) {
   __shared__ float s_same;
   float same = a.inv_divisor;  // (unused with a weight for each sequence)
   if (a.reduce == 1) {
     double v[1] = {0.0};
-    for (int i = threadIdx.x; i < a.count_ctas; i += kThreads) v[0] += static_cast<double>(a.cta_count[i]);
+    for (int i = threadIdx.x; i < a.count_ctas; i += kThreads) v[0] += static_cast<double>(counts.cta[i]);
     cta_sums(v);
     if (threadIdx.x == 0) s_same = static_cast<float>(1.0 / v[0]);
     __syncthreads();
     same = s_same;
   }
   Sums sums;
-  if (a.T < kShort) short_rows<W, REF, TADV>(a, cta, ctas, same, sums);
-  else long_rows<VEC, W, REF, TADV>(a, cta, ctas, same, sums);
+  if (a.T < kShort) short_rows<W, REF, TADV>(a, counts, cta, ctas, same, sums);
+  else long_rows<VEC, W, REF, TADV>(a, counts, cta, ctas, same, sums);
   static_assert(S_ALL == 6 && S_LOSS == 0 && S_KL == 1 && S_RATIO == 2 && S_LOW == 3 && S_HIGH == 4 && S_VALID == 5, "");
   cta_total(sums, out);
 }
@@ -830,14 +838,17 @@ __device__ void finish(const PolicyArgs& a, const double (&sums)[S_ALL]) {
 template <bool VEC, bool WTOO>
 __global__ void __launch_bounds__(kThreads) k_policy_count(const __grid_constant__ PolicyArgs a) {
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
-  count_phase<VEC, WTOO>(a, blockIdx.x, gridDim.x);
+  const bool first = (threadIdx.x & 31) == 0;
+  count_phase<VEC, WTOO>(a, {a.piece_count, a.piece_w, a.cta_count}, blockIdx.x, gridDim.x, [&](auto* p, int64_t i, auto v, bool every) {
+    if (every || first) p[i] = v;
+  });
 }
 
 template <bool VEC, int W, bool REF, bool TADV>
 __global__ void __launch_bounds__(kThreads, kLossCtas) k_policy_loss(const __grid_constant__ PolicyArgs a) {
   __shared__ bool s_last;
   double sums[S_ALL];
-  loss_phase<VEC, W, REF, TADV>(a, blockIdx.x, gridDim.x, sums);
+  loss_phase<VEC, W, REF, TADV>(a, {a.piece_count, a.piece_w, a.cta_count}, blockIdx.x, gridDim.x, sums);
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int m = 0; m < S_ALL; ++m) a.partial[S_ALL * blockIdx.x + m] = sums[m];
@@ -856,17 +867,28 @@ __global__ void __launch_bounds__(kThreads, kLossCtas) k_policy_loss(const __gri
   if (threadIdx.x == 0) finish(a, sums);
 }
 
-// Both for few tokens.
+// Both for few tokens: every CTA of the cluster has all counts in its shared memory, and
+// no workspace is needed.
 template <bool VEC, int W, bool REF, bool TADV>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) k_policy_small(const __grid_constant__ PolicyArgs a) {
   __shared__ double parts[kCluster][S_ALL];
+  __shared__ int s_n[kSmallPieces];
+  __shared__ double s_w[W == W_SEQUENCE ? kSmallPieces : 1];
+  __shared__ int64_t s_cta[kCluster];
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = static_cast<int>(cluster.block_rank());
-  count_phase<VEC, W == W_SEQUENCE>(a, rank, kCluster);
-  __threadfence();
+  const int rank = static_cast<int>(cluster.block_rank()), lane = threadIdx.x & 31;
+  const Counts counts = {s_n, s_w, s_cta};
+  cluster.sync();  // every CTA runs: its shared memory may be written
+  count_phase<VEC, W == W_SEQUENCE>(a, counts, rank, kCluster, [&](auto* p, int64_t i, auto v, bool every) {
+    if (every) {
+      for (int c = 0; c < kCluster; ++c) cluster.map_shared_rank(p, c)[i] = v;
+    } else if (lane < kCluster) {
+      cluster.map_shared_rank(p, lane)[i] = v;
+    }
+  });
   cluster.sync();
   double sums[S_ALL];
-  loss_phase<VEC, W, REF, TADV>(a, rank, kCluster, sums);
+  loss_phase<VEC, W, REF, TADV>(a, counts, rank, kCluster, sums);
   if (threadIdx.x == 0) {
     double* to = cluster.map_shared_rank(&parts[0][0], 0);
 #pragma unroll
@@ -883,7 +905,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) k_p
   }
 }
 
-bool small(const PolicyArgs& a) { return a.B * a.T <= kSmall; }
+bool small(const PolicyArgs& a) { return a.B * a.T <= kSmall && a.B * a.pieces <= kSmallPieces; }
 
 // Whether quads of tokens of every operand are on 16-byte boundaries alike.
 bool by_quads(const PolicyArgs& a) {
@@ -928,6 +950,7 @@ size_t policy_plan(PolicyArgs& a, int sms, void* workspace) {
   const int64_t want = (pieces + kWarps - 1) / kWarps;
   a.loss_ctas = static_cast<int>(chunks < all ? chunks : all);
   a.count_ctas = small(a) ? kCluster : static_cast<int>(want < most ? want : most);
+  if (small(a)) return 0;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     char* p = static_cast<char*>(workspace) + at;

@@ -139,8 +139,7 @@ grpo_status clip_grads(const grpo_grad_tensor* tensors, int32_t n_tensors, int32
   int sms = 0;
   const grpo_status st = device_info(&sms);
   if (st != GRPO_OK) return st;
-  if (!workspace || !aligned16(workspace) || workspace_bytes < grad_bytes(sms, kGradLaunches))
-    return GRPO_ERR_WORKSPACE;
+  const bool room = workspace && aligned16(workspace) && workspace_bytes >= grad_bytes(sms, kGradLaunches);
   GradJoin join = {static_cast<double*>(workspace), 0, norm_type == 0 ? 1 : 0, max_norm, eps, norm, factor};
   GradTensor table[kGradMaxTensors];
   int launches = 0;
@@ -152,6 +151,7 @@ grpo_status clip_grads(const grpo_grad_tensor* tensors, int32_t n_tensors, int32
           LAUNCH(K_GRAD_NORM, stream, launch_grad_small(table, used, join, scale ? 1 : 0, stream));
           return GRPO_OK;
         }
+        if (!room) return GRPO_ERR_WORKSPACE;
         if (pass == 0) {
           if (launches == kGradLaunches) {
             LAUNCH(K_GRAD_JOIN, stream, launch_grad_fold(join.partial, join.parts, join.inf, stream));
@@ -178,6 +178,7 @@ grpo_status clip_grads(const grpo_grad_tensor* tensors, int32_t n_tensors, int32
       d.bf16 = tensors[i].dtype == GRPO_BF16 ? 1 : 0;
     }
     // (what scales joins the parts by itself; without a tensor there is nothing to scale)
+    if (pass == 0 && launches == 0 && !room) return GRPO_ERR_WORKSPACE;
     if (pass == 0 && (!scale || launches == 0)) LAUNCH(K_GRAD_JOIN, stream, launch_grad_join(join, stream));
   }
   return GRPO_OK;
@@ -222,7 +223,7 @@ grpo_status grpo_policy_loss(const grpo_policy_problem* p, const float* logp, co
   if ((st = device_info(&sms)) != GRPO_OK) return st;
   if (!logp_old) a.sequence_ratio = 0;
   const size_t need = policy_plan(a, sms, workspace);
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 != 0 || workspace_bytes < need)
+  if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
     return GRPO_ERR_WORKSPACE;
   a.logp = logp;
   a.old = logp_old;

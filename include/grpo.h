@@ -512,6 +512,7 @@ grpo_status grpo_adamw_step(const grpo_adamw_config *config, const grpo_adamw_te
  *   stats  float32 [4], written, may be NULL: the means over valid tokens of k, of whether
  *          the lower and the upper bound took the gradient away, and of r
  *   dlogp  float32 [B, T], written, may be NULL
+ * The workspace holds counts; for few tokens its size is 0 and it may be NULL.
  * Row strides ld_* in elements. dlogp may be logp, logp_old, logp_ref or adv [B, T] (same
  * stride). Sums are float64 in a fixed order: results do not vary between calls. B = 0 or T = 0: loss and stats are 0. INVALID_ARG for null pointers,
  * sizes below 0, a stride below T, bounds, beta or divisor outside the above or NaN;
@@ -633,7 +634,8 @@ grpo_status grpo_residual_norm_bwd(const grpo_residual_norm_problem *problem, co
  * no tensor at all has norm 0. An out must not overlap another tensor's grad or out, nor
  * its own grad except as a whole.
  *   norm, factor  device float32 [1], written; factor may be NULL
- * The workspace (grpo_grad_norm_workspace_size, for the current device) holds partial sums.
+ * The workspace (grpo_grad_norm_workspace_size, for the current device) holds partial sums;
+ * it may be NULL for 1 to 8 tensors, none of them empty, of 65536 elements in all at most.
  * INVALID_ARG for null pointers, n < 0, a max_norm or eps that is negative or NaN, an eps
  * that is infinite, another norm_type or dtype; UNSUPPORTED for pointers off their element's
  * alignment.

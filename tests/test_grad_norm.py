@@ -303,8 +303,8 @@ def test_refuses_wrong_tensors():
             G.clip_grad_norm([g], 1.0, out=out)
     with pytest.raises(ValueError, match="expected 1"):
         G.clip_grad_norm([g], 1.0, out=[])
-    with pytest.raises(L.GrpoError) as e:
-        G.grad_norm([g], workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(L.GrpoError) as e:           # (a short list needs none)
+        G.grad_norm([g] * 40, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 3
     with pytest.raises(ValueError, match="elements"):
         G.grad_norm([g], norm=torch.zeros(2, device="cuda"))

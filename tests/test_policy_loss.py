@@ -73,6 +73,16 @@ def test_many_sequences(B, T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,T", [(1, 32768), (1, 32769), (1024, 32), (1025, 31), (33, 1000), (130, 255), (3, 10001)])
+def test_on_either_side_of_one_launch(B, T):
+    """The most tokens and sequences that one launch takes, and more, with rows on and off
+    16-byte boundaries."""
+    for pad, token_adv, ratio in ((0, False, "token"), (4, True, "sequence"), (1, False, "sequence")):
+        x = inputs(B, T, seed=2, pad=pad, token_adv=token_adv)
+        check(*x, ratio=ratio, reduce="token", beta=0.02, dual_clip=2.0)
+
+
+@pytest.mark.gpu
 def test_what_may_be_left_out():
     import grpo_loss_gb300 as G
     q, adv, mask, old, ref = inputs(6, 300)
@@ -378,7 +388,7 @@ def test_refuses_wrong_arguments(monkeypatch):
 @pytest.mark.gpu
 def test_refuses_a_short_workspace_and_the_host():
     import grpo_loss_gb300 as G
-    q, adv, mask, old, ref = inputs(3, 8)
+    q, adv, mask, old, ref = inputs(300, 800)       # (few tokens need none)
     with pytest.raises(L.GrpoError) as e:
         G.policy_loss(q, adv, mask, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 3

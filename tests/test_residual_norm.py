@@ -366,8 +366,7 @@ def test_repeats_streams_and_graphs():
                                 **(bwd or {}))
         return f + b
     want = both()
-    size = L._bytes(L.lib().grpo_residual_norm_workspace_size, "size", s["x"].device,
-                    L.ResidualNormProblem(900, 1536, *[0] * 10, 100, 1e-5, 1.0, 0, 1, 1, 1))
+    size = L.residual_norm_workspace_size(L.ResidualNormProblem(900, 1536, *[0] * 10, 100, 1e-5, 1.0, 0, 1, 1, 1))
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
     for _ in range(4):
