@@ -164,6 +164,109 @@ __global__ void __launch_bounds__(G * R) k_resnorm_fwd(ResNormArgs a) {
   }
 }
 
+// Rows that do not come in whole pieces: a CTA walks over rows, each staged by the granules
+// it lies in while the one before is worked on; a thread's N columns are G apart, and
+// their parameters stay in registers.
+template <typename T, int N, int G, bool POST>
+__global__ void __launch_bounds__(G) k_resnorm_fwd_strided(ResNormArgs a) {
+  extern __shared__ __align__(16) unsigned char staged[];
+  __shared__ float part[2 * 128];
+  const int tid = threadIdx.x, d = static_cast<int>(a.d), pitch = staged_pitch(d, sizeof(T));
+  const float inv_d = 1.f / d;
+  auto column = [&](int i) { return i * G + tid; };
+  float w[N], pw[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    w[i] = column(i) < d ? param(a.weight, a.param_bf16, column(i)) : 0.f;
+    if (POST) pw[i] = column(i) < d ? param(a.post_weight, a.param_bf16, column(i)) : 0.f;
+  }
+  auto fetch = [&](int64_t row, int half) {
+    if (row < a.rows) {
+      const T *x = static_cast<const T*>(a.x), *res = static_cast<const T*>(a.residual);
+      stage_row<T, G>(staged + 2 * half * pitch, x + row * a.ld_x, x, d, tid);
+      stage_row<T, G>(staged + (2 * half + 1) * pitch, res + row * a.ld_res, res, d, tid);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto values = [&](int which, const void* base, int64_t at) {
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + at) & 15);
+    return reinterpret_cast<const T*>(staged + which * pitch + off);
+  };
+  fetch(blockIdx.x, 0);
+  int half = 0, slot = 0;
+  auto sum = [&](float v) {
+    slot ^= 1;
+    return group_sum<G>(v, part, slot);
+  };
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, half ^= 1) {
+    // this row is here, of every thread's copies, and the last one's place is free
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    fetch(row + gridDim.x, half ^ 1);
+    const T *x = values(2 * half, a.x, row * a.ld_x), *res = values(2 * half + 1, a.residual, row * a.ld_res);
+    float h[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) h[i] = column(i) < d ? ldf(x, column(i)) : 0.f;
+    float pm = 0.f, pr = 1.f;
+    if constexpr (POST) {
+      if (!a.rms) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) s += h[i];
+        pm = sum(s) * inv_d;
+      }
+      float q = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float c = column(i) < d ? h[i] - pm : 0.f;
+        q = fmaf(c, c, q);
+      }
+      pr = rsqrtf(sum(q) * inv_d + a.eps);
+    }
+    T* const to_h = static_cast<T*>(a.h_out) + row * a.ld_h;
+    const int64_t gate_at = a.gate ? row / a.gate_rows * a.ld_gate : 0;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = column(i);
+      if (c >= d) {
+        h[i] = 0.f;
+        continue;
+      }
+      float p = h[i];
+      if constexpr (POST) {
+        p = (p - pm) * pr * pw[i];
+        if (a.post_bias) p += param(a.post_bias, a.param_bf16, c);
+      }
+      if (a.gate) p *= at(a.gate, a.gate_bf16, gate_at + c);
+      h[i] = fmaf(a.scale, p, ldf(res, c));
+      s += h[i];
+      stf(to_h, c, h[i]);
+    }
+    float m = 0.f;
+    if (!a.rms) m = sum(s) * inv_d;
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float c = column(i) < d ? h[i] - m : 0.f;
+      q = fmaf(c, c, q);
+    }
+    const float r = rsqrtf(sum(q) * inv_d + a.eps);
+    T* const to_y = static_cast<T*>(a.y) + row * a.ld_y;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = column(i);
+      if (c < d) stf(to_y, c, fmaf((h[i] - m) * r, w[i], a.bias ? param(a.bias, a.param_bf16, c) : 0.f));
+    }
+    if (tid == 0) {
+      if (a.mean) a.mean[row] = m;
+      if (a.rstd) a.rstd[row] = r;
+      if (a.post_mean) a.post_mean[row] = pm;
+      if (a.post_rstd) a.post_rstd[row] = pr;
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kLong) k_resnorm_fwd_long(ResNormArgs a) {
   extern __shared__ float h[];
   const int d = static_cast<int>(a.d);
@@ -361,8 +464,8 @@ cudaError_t fwd(const ResNormArgs& a, cudaStream_t s) {
 template <typename T, int N>
 cudaError_t fwd_n(const ResNormArgs& a, cudaStream_t s) {
   const int64_t pieces = (a.d + N - 1) / N;
-  if (N > 1 && pieces <= 8) return fwd<T, N, 1, 8, 32>(a, s);
-  if (N > 1 && pieces <= 16) return fwd<T, N, 1, 16, 16>(a, s);
+  if (pieces <= 8) return fwd<T, N, 1, 8, 32>(a, s);
+  if (pieces <= 16) return fwd<T, N, 1, 16, 16>(a, s);
   if (pieces <= 32) return fwd<T, N, 1, 32, 8>(a, s);
   if (pieces <= 64) return fwd<T, N, 2, 32, 4>(a, s);
   if (pieces <= 128) return fwd<T, N, 2, 64, 2>(a, s);
@@ -371,6 +474,31 @@ cudaError_t fwd_n(const ResNormArgs& a, cudaStream_t s) {
   if (pieces <= 1024) return fwd<T, N, 2, 512, 1>(a, s);
   if (pieces <= 2048) return fwd<T, N, 4, 512, 1>(a, s);
   if (pieces <= 4096) return fwd<T, N, 4, 1024, 1>(a, s);
+  return cudaErrorNotSupported;  // longer rows
+}
+
+template <typename T, int N, int G, bool POST>
+cudaError_t fwd_strided(const ResNormArgs& a, int sms, cudaStream_t s) {
+  constexpr int most = 4 * staged_pitch(N * G, sizeof(T));
+  static_assert(most <= kResNormRing, "shared memory");
+  auto kernel = k_resnorm_fwd_strided<T, N, G, POST>;
+  static std::atomic<uint64_t> configured{0};
+  static std::atomic<int> per_sm{0};
+  cudaError_t e;
+  const int n = resident_ctas(reinterpret_cast<const void*>(kernel), G, most, configured, per_sm, &e);
+  if (n < 0) return e;
+  const int64_t all = static_cast<int64_t>(n) * sms;
+  const int smem = 4 * staged_pitch(static_cast<int>(a.d), sizeof(T));
+  kernel<<<static_cast<unsigned>(a.rows < all ? a.rows : all), G, smem, s>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, bool POST>
+cudaError_t fwd_any(const ResNormArgs& a, int sms, cudaStream_t s) {
+  if (a.d <= 256) return fwd_strided<T, 4, 64, POST>(a, sms, s);
+  if (a.d <= 1024) return fwd_strided<T, 8, 128, POST>(a, sms, s);
+  if (a.d <= 2048) return fwd_strided<T, 8, 256, POST>(a, sms, s);
+  if (a.d <= 4096) return fwd_strided<T, 8, 512, POST>(a, sms, s);
+  if (a.d <= 8192) return fwd_strided<T, 8, 1024, POST>(a, sms, s);
   return cudaErrorNotSupported;
 }
 
@@ -389,8 +517,10 @@ int resnorm_walkers(const ResNormArgs& a, int sms) {
 
 cudaError_t launch_resnorm_fwd(const ResNormArgs& a, int sms, cudaStream_t s) {
   const bool pieces = whole(a, true);
-  cudaError_t e = a.bf16 ? (pieces ? fwd_n<__nv_bfloat16, 8>(a, s) : fwd_n<__nv_bfloat16, 1>(a, s))
-                         : (pieces ? fwd_n<float, 4>(a, s) : fwd_n<float, 1>(a, s));
+  cudaError_t e;
+  if (pieces) e = a.bf16 ? fwd_n<__nv_bfloat16, 8>(a, s) : fwd_n<float, 4>(a, s);
+  else if (a.post_weight) e = a.bf16 ? fwd_any<__nv_bfloat16, true>(a, sms, s) : fwd_any<float, true>(a, sms, s);
+  else e = a.bf16 ? fwd_any<__nv_bfloat16, false>(a, sms, s) : fwd_any<float, false>(a, sms, s);
   if (e != cudaErrorNotSupported) return e;
   e = allow_row(reinterpret_cast<const void*>(k_resnorm_fwd_long), kMaxResNormDim);
   if (e != cudaSuccess) return e;
@@ -399,9 +529,10 @@ cudaError_t launch_resnorm_fwd(const ResNormArgs& a, int sms, cudaStream_t s) {
 }
 cudaError_t launch_resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
   cudaError_t e = cudaErrorNotSupported;
-  if (whole(a, false) && !(a.gate && a.gate_rows == 1 && a.gate_bf16 != a.bf16)) {
-    if (a.bf16) e = a.post_weight ? resnorm_bwd_bf16_post(a, sms, walkers, s) : resnorm_bwd_bf16(a, sms, walkers, s);
-    else e = a.post_weight ? resnorm_bwd_f32_post(a, sms, walkers, s) : resnorm_bwd_f32(a, sms, walkers, s);
+  if (!(a.gate && a.gate_rows == 1 && a.gate_bf16 != a.bf16)) {
+    const bool w = whole(a, false);
+    if (a.bf16) e = a.post_weight ? resnorm_bwd_bf16_post(a, w, sms, walkers, s) : resnorm_bwd_bf16(a, w, sms, walkers, s);
+    else e = a.post_weight ? resnorm_bwd_f32_post(a, w, sms, walkers, s) : resnorm_bwd_f32(a, w, sms, walkers, s);
   }
   if (e != cudaErrorNotSupported) return e;
   e = allow_row(reinterpret_cast<const void*>(k_resnorm_bwd_long), kMaxResNormDim);

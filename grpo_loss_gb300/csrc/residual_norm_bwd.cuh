@@ -41,6 +41,23 @@ inline int resident_ctas(const void* kernel, int threads, int smem, std::atomic<
   return per_sm.load();
 }
 
+// Copies a row of d elements by the 16-byte granules it lies in while the G threads go on;
+// `to` has the place of the first granule.
+template <typename T, int G>
+__device__ __forceinline__ void stage_row(unsigned char* to, const T* row, const T* matrix, int d, int tid) {
+  constexpr int es = static_cast<int>(sizeof(T));
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15), bytes = off + d * es;
+  const char* from = reinterpret_cast<const char*>(row) - off;
+  for (int i = tid * 16; i < bytes; i += G * 16) {
+    if (i == 0 && from < reinterpret_cast<const char*>(matrix)) {  // the granule begins before the matrix
+      for (int e = 0; e < d && off + e * es < 16; ++e) reinterpret_cast<T*>(to + off)[e] = row[e];
+    } else {
+      copy_async_zero(to + i, from + i, min(16, bytes - i));
+    }
+  }
+}
+constexpr int staged_pitch(int d, int size) { return (d * size + 31) / 16 * 16; }
+
 // A group of G threads is a walker, R of them a CTA; each thread holds NV pieces of N
 // columns: their values of a row, and their column sums. The next row's pieces are on
 // their way into shared memory meanwhile, whence they are read twice, for the sums and for
@@ -49,13 +66,18 @@ inline int resident_ctas(const void* kernel, int threads, int smem, std::atomic<
 // of which dgate = pw e1 + pb e0, and gate e1 and gate e0 are these rows' parts of the post
 // norm's dweight and dbias: taken when the gate changes, so that a row adds to two sums and
 // not to three.
-template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE>
+// STRIDED: rows that do not come in whole pieces. A row is staged by the 16-byte granules it
+// lies in, and a thread's N columns are G apart, so that a warp's accesses are to
+// consecutive elements wherever the row begins; one more barrier a row lets the threads
+// read what others copied. (RMS norms are told by the arguments then.)
+template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, bool STRIDED>
 __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walkers) {
+  static_assert(!STRIDED || (NV == 1 && R == 1 && !RMS && N % 2 == 0), "");
   constexpr int B = N * static_cast<int>(sizeof(T)), H = (N + 1) / 2;
   constexpr bool INNER = POST || GATE != GATE_NONE;
   constexpr int ARRAYS = 3 + INNER + (GATE == GATE_ROWS);  // dy, h, dh, x, gate
   constexpr int SUMS = POST ? (RMS ? 4 : 8) : 2;
-  using V = Piece<T, N>;
+  using V = Piece<T, STRIDED ? 1 : N>;
   extern __shared__ __align__(16) unsigned char ring_raw[];
   __shared__ float part[2 * (SUMS < 4 ? 128 : 32 * SUMS)];
   V* const ring = reinterpret_cast<V*>(ring_raw) + threadIdx.x;  // [2][ARRAYS][NV][threads]
@@ -67,14 +89,23 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   const int turns = static_cast<int>((a.rows + walkers - 1) / walkers);
 
   uint64_t w[NV][H], f[NV][H], dw[NV][H], db[NV][H], e1[NV][H], e0[NV][H];  // f: a, or scale gate
-  auto load_pairs = [&](const void* p, int bf16, int64_t at, uint64_t (&v)[H]) {
+  // column i of the thread's piece k; a piece's columns are all in the row, or with STRIDED each is
+  auto column = [&](int k, int i = 0) { return STRIDED ? i * G + tid : (k * G + tid) * N + i; };
+  auto inside = [&](int i) { return !STRIDED || column(0, i) < d; };
+  // N parameters from element `at` of p on
+  auto load_pairs = [&](const void* p, int bf16, int64_t at, int k, uint64_t (&v)[H]) {
     float u[2 * H] = {};
-    if (bf16) load_params<N>(static_cast<const __nv_bfloat16*>(p) + at, 1, 0, u);
-    else load_params<N>(static_cast<const float*>(p) + at, 0, 0, u);
+    if constexpr (STRIDED) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (inside(i)) u[i] = bf16 ? ldf(static_cast<const __nv_bfloat16*>(p), at + column(k, i)) : ldf(static_cast<const float*>(p), at + column(k, i));
+    } else {
+      if (bf16) load_params<N>(static_cast<const __nv_bfloat16*>(p) + at, 1, column(k), u);
+      else load_params<N>(static_cast<const float*>(p) + at, 0, column(k), u);
+    }
 #pragma unroll
     for (int e = 0; e < H; ++e) v[e] = pair_of(u[2 * e], u[2 * e + 1]);
   };
-  auto column = [&](int k) { return (k * G + tid) * N; };
   const uint64_t zero = pair_of(0.f, 0.f), scale2 = pair_of(a.scale);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
@@ -84,10 +115,10 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
       f[k][e] = scale2;
     }
     if (column(k) < d) {
-      load_pairs(a.weight, a.param_bf16, column(k), w[k]);
+      load_pairs(a.weight, a.param_bf16, 0, k, w[k]);
       if constexpr (POST && GATE != GATE_SHARED) {
         uint64_t pw[H];
-        load_pairs(a.post_weight, a.param_bf16, column(k), pw);
+        load_pairs(a.post_weight, a.param_bf16, 0, k, pw);
 #pragma unroll
         for (int e = 0; e < H; ++e) f[k][e] = mul2(pw[e], scale2);
       }
@@ -95,17 +126,22 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   }
 
   auto slot_of = [&](int half, int which, int k) -> V& { return ring[((half * ARRAYS + which) * NV + k) * (G * R)]; };
+  const int pitch = staged_pitch(d, sizeof(T));  // of a staged row
   auto fetch = [&](int n, int half) {
     if (n < mine) {
       const int64_t row = from + n;
       auto copy = [&](int which, const void* p, int64_t ld) {
         const T* q = static_cast<const T*>(p) + row * ld;
+        if constexpr (STRIDED) {
+          stage_row<T, G>(ring_raw + (half * ARRAYS + which) * pitch, q, static_cast<const T*>(p), d, tid);
+        } else {
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-          if (column(k) < d) {
-            if constexpr (B >= 4) copy_async<B>(&slot_of(half, which, k), q + column(k));
-            else slot_of(half, which, k) = load_piece<T, N>(q + column(k));
-          }
+          for (int k = 0; k < NV; ++k)
+            if (column(k) < d) {
+              if constexpr (B >= 4) copy_async<B>(&slot_of(half, which, k), q + column(k));
+              else slot_of(half, which, k) = load_piece<T, N>(q + column(k));
+            }
+        }
       };
       copy(0, a.dy, a.ld_dy);
       copy(1, a.h, a.ld_h);
@@ -115,12 +151,44 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // The values of a piece of a row that has arrived, by pairs.
+  struct Values {
+    V v;
+    const T* p;
+  };
+  auto values = [&](int half, int which, int k, const void* base, int64_t ld, int64_t row) {
+    Values u;
+    if constexpr (STRIDED) {
+      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * ld) & 15);
+      u.p = reinterpret_cast<const T*>(ring_raw + (half * ARRAYS + which) * pitch + off);
+    } else {
+      u.v = slot_of(half, which, k);
+    }
+    return u;
+  };
+  auto pair = [&](const Values& u, int e) {
+    if constexpr (STRIDED)
+      return pair_of(inside(2 * e) ? ldf(u.p, column(0, 2 * e)) : 0.f, inside(2 * e + 1) ? ldf(u.p, column(0, 2 * e + 1)) : 0.f);
+    else
+      return pair_of(u.v.get(2 * e), 2 * e + 1 < N ? u.v.get(2 * e + 1) : 0.f);
+  };
+  auto store = [&](T* to, int k, const float* o) {
+    if constexpr (STRIDED) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (inside(i)) stf(to, column(k, i), o[i]);
+    } else {
+      Piece<T, N> p;
+      p.set(o);
+      store_piece<T, N>(to + column(k), p);
+    }
+  };
   auto store_sums = [&](float* to, int k, const uint64_t (&v)[H]) {
 #pragma unroll
     for (int e = 0; e < H; ++e) {
       const float2 p = of_pair(v[e]);
-      to[column(k) + 2 * e] = p.x;
-      if (2 * e + 1 < N) to[column(k) + 2 * e + 1] = p.y;
+      if (inside(2 * e)) to[column(k, 2 * e)] = p.x;
+      if (2 * e + 1 < N && inside(2 * e + 1)) to[column(k, 2 * e + 1)] = p.y;
     }
   };
   auto part_of = [&](int which) { return a.partial + (static_cast<int64_t>(which) * walkers + walker) * d; };
@@ -139,15 +207,15 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
       if (column(k) < d) {
         uint64_t pw[H], g[H], v[H];
         if constexpr (POST) {
-          load_pairs(a.post_weight, a.param_bf16, column(k), pw);
-          load_pairs(a.gate, a.gate_bf16, q * a.ld_gate + column(k), g);
+          load_pairs(a.post_weight, a.param_bf16, 0, k, pw);
+          load_pairs(a.gate, a.gate_bf16, q * a.ld_gate, k, g);
         }
         if (to) {
 #pragma unroll
           for (int e = 0; e < H; ++e) v[e] = POST ? mul2(pw[e], e1[k][e]) : e1[k][e];
           if (POST && !RMS && a.post_bias) {
             uint64_t pb[H];
-            load_pairs(a.post_bias, a.param_bf16, column(k), pb);
+            load_pairs(a.post_bias, a.param_bf16, 0, k, pb);
 #pragma unroll
             for (int e = 0; e < H; ++e) v[e] = fma2(pb[e], e0[k][e], v[e]);
           }
@@ -157,8 +225,9 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
           auto add = [&](float* p, const uint64_t (&s)[H]) {
 #pragma unroll
             for (int e = 0; e < H; ++e) {
-              const int i = column(k) + 2 * e;
-              const uint64_t before = flushed ? pair_of(p[i], 2 * e + 1 < N ? p[i + 1] : 0.f) : zero;
+              const uint64_t before = !flushed ? zero
+                                               : pair_of(inside(2 * e) ? p[column(k, 2 * e)] : 0.f,
+                                                         2 * e + 1 < N && inside(2 * e + 1) ? p[column(k, 2 * e + 1)] : 0.f);
               v[e] = fma2(g[e], s[e], before);
             }
             store_sums(p, k, v);
@@ -179,10 +248,10 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   auto stats_of = [&](int n) {
     Stats s = {0.f, 0.f, 0.f, 1.f};
     if (n < mine) {
-      if (!RMS) s.m = a.mean[from + n];
+      if (!RMS && !(STRIDED && a.rms)) s.m = a.mean[from + n];
       s.r = a.rstd[from + n];
       if (POST) {
-        if (!RMS) s.pm = a.post_mean[from + n];
+        if (!RMS && !(STRIDED && a.rms)) s.pm = a.post_mean[from + n];
         s.pr = a.post_rstd[from + n];
       }
     }
@@ -193,8 +262,15 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   fetch(0, 0);
   int half = 0;
   for (int n = 0; n < turns; ++n, half ^= 1) {
-    fetch(n + 1, half ^ 1);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    if constexpr (STRIDED) {
+      // this row is here, of every thread's copies, and the last one's place is free
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();
+      fetch(n + 1, half ^ 1);
+    } else {
+      fetch(n + 1, half ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    }
     const Stats s = next;
     next = stats_of(n + 1);
     const bool live = n < mine;
@@ -207,16 +283,15 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
 #pragma unroll
         for (int k = 0; k < NV; ++k)
           if (column(k) < d) {
-            load_pairs(a.gate, a.gate_bf16, row / a.gate_rows * a.ld_gate + column(k), f[k]);
+            load_pairs(a.gate, a.gate_bf16, row / a.gate_rows * a.ld_gate, k, f[k]);
             uint64_t pw[H];
-            if constexpr (POST) load_pairs(a.post_weight, a.param_bf16, column(k), pw);
+            if constexpr (POST) load_pairs(a.post_weight, a.param_bf16, 0, k, pw);
 #pragma unroll
             for (int e = 0; e < H; ++e) f[k][e] = POST ? mul2(mul2(pw[e], scale2), f[k][e]) : mul2(f[k][e], scale2);
           }
       }
     }
     const uint64_t r2 = pair_of(s.r), pr2 = pair_of(s.pr), m2 = pair_of(-s.m), pm2 = pair_of(-s.pm);
-    auto pair = [&](const V& v, int e) { return pair_of(v.get(2 * e), 2 * e + 1 < N ? v.get(2 * e + 1) : 0.f); };
     // (x - mean) r, the difference first: x and mean may be large and close
     auto hat_of = [&](uint64_t v, uint64_t m, uint64_t r) { return mul2(RMS ? v : add2(v, m), r); };
     uint64_t t[8];
@@ -226,12 +301,12 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
 #pragma unroll
       for (int k = 0; k < NV; ++k)
         if (column(k) < d) {
-          const V vy = slot_of(half, 0, k), vh = slot_of(half, 1, k);
-          V vd, vx, vg;
+          const Values vy = values(half, 0, k, a.dy, a.ld_dy, row), vh = values(half, 1, k, a.h, a.ld_h, row);
+          Values vd, vx, vg;
           if constexpr (POST) {
-            if (a.dh) vd = slot_of(half, 2, k);
-            vx = slot_of(half, 3, k);
-            if constexpr (GATE == GATE_ROWS) vg = slot_of(half, 4, k);
+            if (a.dh) vd = values(half, 2, k, a.dh, a.ld_dh, row);
+            vx = values(half, 3, k, a.x, a.ld_x, row);
+            if constexpr (GATE == GATE_ROWS) vg = values(half, 4, k, a.gate, a.ld_gate, row);
           }
 #pragma unroll
           for (int e = 0; e < H; ++e) {
@@ -266,13 +341,14 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
     }
     group_sums<G, SUMS>(sums, part, half);
     if (!live) continue;
-    const float c2 = s.r * sums[0] * inv_d, c1 = RMS ? 0.f : s.r * sums[1] * inv_d;  // r c2, r c1
+    // r c2, r c1
+    const float c2 = s.r * sums[0] * inv_d, c1 = RMS || (STRIDED && a.rms) ? 0.f : s.r * sums[1] * inv_d;
     float b1 = 0.f, b2 = 0.f;  // means of a g and of a g k
     if constexpr (POST) {
       b2 = fmaf(-c2, sums[3], sums[2]);
       if constexpr (!RMS) {
         b2 = fmaf(-c1, sums[7], b2) * inv_d;
-        b1 = fmaf(-c1, sums[6], fmaf(-c2, sums[5], sums[4])) * inv_d;
+        if (!STRIDED || !a.rms) b1 = fmaf(-c1, sums[6], fmaf(-c2, sums[5], sums[4])) * inv_d;
       } else {
         b2 *= inv_d;
       }
@@ -283,14 +359,17 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
 #pragma unroll
     for (int k = 0; k < NV; ++k)
       if (column(k) < d) {
-        const V vy = slot_of(half, 0, k), vh = slot_of(half, 1, k);
-        V vd, vx, vg;
-        if (a.dh) vd = slot_of(half, 2, k);
-        if constexpr (INNER) vx = slot_of(half, 3, k);
-        if constexpr (GATE == GATE_ROWS) vg = slot_of(half, 4, k);
-        float res[2 * H], dx[2 * H], dg[2 * H], pb[2 * H] = {};
+        const Values vy = values(half, 0, k, a.dy, a.ld_dy, row), vh = values(half, 1, k, a.h, a.ld_h, row);
+        Values vd, vx, vg;
+        if (a.dh) vd = values(half, 2, k, a.dh, a.ld_dh, row);
+        if constexpr (INNER) vx = values(half, 3, k, a.x, a.ld_x, row);
+        if constexpr (GATE == GATE_ROWS) vg = values(half, 4, k, a.gate, a.ld_gate, row);
+        float res[2 * H], dx[2 * H], dg[2 * H];
+        uint64_t pb[H];
+#pragma unroll
+        for (int e = 0; e < H; ++e) pb[e] = zero;
         if constexpr (GATE == GATE_ROWS && POST && !RMS)
-          if (a.dgate && a.post_bias) load_params<N>(a.post_bias, a.param_bf16, column(k), pb);
+          if (a.dgate && a.post_bias) load_pairs(a.post_bias, a.param_bf16, 0, k, pb);
 #pragma unroll
         for (int e = 0; e < H; ++e) {
           const uint64_t hat = hat_of(pair(vh, e), m2, r2);
@@ -304,7 +383,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
             if constexpr (GATE == GATE_ROWS) {
               // dgate = scale g p, p = k pw + pb: out has scale pw g, or scale g
               uint64_t v = mul2(out, kx);
-              if (POST && !RMS) v = fma2(mul2(g, scale2), pair_of(pb[2 * e], pb[2 * e + 1]), v);
+              if (POST && !RMS) v = fma2(mul2(g, scale2), pb[e], v);
               const float2 dv = of_pair(v);
               dg[2 * e] = dv.x, dg[2 * e + 1] = dv.y;
               out = mul2(out, pair(vg, e));
@@ -320,19 +399,10 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
           const float2 ov = of_pair(out);
           dx[2 * e] = ov.x, dx[2 * e + 1] = ov.y;
         }
-        V p;
-        p.set(res);
-        store_piece<T, N>(to_res + column(k), p);
-        if (to_x) {
-          p.set(dx);
-          store_piece<T, N>(to_x + column(k), p);
-        }
-        if constexpr (GATE == GATE_ROWS) {
-          if (a.dgate) {
-            p.set(dg);
-            store_piece<T, N>(static_cast<T*>(a.dgate) + row * a.ld_dgate + column(k), p);
-          }
-        }
+        store(to_res, k, res);
+        if (to_x) store(to_x, k, dx);
+        if constexpr (GATE == GATE_ROWS)
+          if (a.dgate) store(static_cast<T*>(a.dgate) + row * a.ld_dgate, k, dg);
       }
   }
   if (mine == 0) return;
@@ -351,12 +421,12 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
 
 // One launch: as many CTAs as the SMs hold at a time, so that each walks over its share of
 // the rows once. *walkers: rows of partial sums it writes.
-template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE>
+template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, bool STRIDED = false>
 cudaError_t resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
   constexpr int arrays = 3 + (POST || GATE != GATE_NONE) + (GATE == GATE_ROWS);
-  constexpr int smem = 2 * arrays * NV * N * static_cast<int>(sizeof(T)) * G * R;
+  constexpr int smem = 2 * arrays * (NV * N * static_cast<int>(sizeof(T)) * G * R + (STRIDED ? 32 : 0));
   static_assert(smem <= kResNormRing, "shared memory");
-  auto kernel = k_resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE>;
+  auto kernel = k_resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE, STRIDED>;
   static std::atomic<uint64_t> configured{0};
   static std::atomic<int> per_sm{0};
   cudaError_t e;
@@ -393,11 +463,22 @@ cudaError_t resnorm_bwd_n(const ResNormArgs& a, int sms, int* walkers, cudaStrea
 #undef RESNORM_CASE
   return cudaErrorNotSupported;  // longer rows: the caller has another kernel
 }
+template <typename T, bool POST, int GATE>
+cudaError_t resnorm_bwd_strided(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
+  if (a.d <= 1024) return resnorm_bwd<T, 8, 1, 128, 1, false, POST, GATE, true>(a, sms, walkers, s);
+  if (a.d <= 2048) return resnorm_bwd<T, 8, 1, 256, 1, false, POST, GATE, true>(a, sms, walkers, s);
+  if (a.d <= 4096) return resnorm_bwd<T, 8, 1, 512, 1, false, POST, GATE, true>(a, sms, walkers, s);
+  return cudaErrorNotSupported;
+}
 
 template <typename T, bool POST>
-cudaError_t resnorm_bwd_kind(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
+cudaError_t resnorm_bwd_kind(const ResNormArgs& a, bool whole, int sms, int* walkers, cudaStream_t s) {
   constexpr int N = 16 / static_cast<int>(sizeof(T));
   const int gate = !a.gate ? GATE_NONE : a.gate_rows == 1 ? GATE_ROWS : GATE_SHARED;
+  if (!whole)
+    return gate == GATE_NONE     ? resnorm_bwd_strided<T, POST, GATE_NONE>(a, sms, walkers, s)
+           : gate == GATE_SHARED ? resnorm_bwd_strided<T, POST, GATE_SHARED>(a, sms, walkers, s)
+                                 : resnorm_bwd_strided<T, POST, GATE_ROWS>(a, sms, walkers, s);
   if (a.rms)
     return gate == GATE_NONE     ? resnorm_bwd_n<T, N, true, POST, GATE_NONE>(a, sms, walkers, s)
            : gate == GATE_SHARED ? resnorm_bwd_n<T, N, true, POST, GATE_SHARED>(a, sms, walkers, s)
@@ -407,10 +488,10 @@ cudaError_t resnorm_bwd_kind(const ResNormArgs& a, int sms, int* walkers, cudaSt
                                : resnorm_bwd_n<T, N, false, POST, GATE_ROWS>(a, sms, walkers, s);
 }
 
-// Of whole pieces; cudaErrorNotSupported for rows that are too long. (A translation unit each.)
-cudaError_t resnorm_bwd_f32(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s);
-cudaError_t resnorm_bwd_f32_post(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s);
-cudaError_t resnorm_bwd_bf16(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s);
-cudaError_t resnorm_bwd_bf16_post(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s);
+// Whole: rows in 16-byte pieces. cudaErrorNotSupported for rows that are too long. (A translation unit each.)
+cudaError_t resnorm_bwd_f32(const ResNormArgs& a, bool whole, int sms, int* walkers, cudaStream_t s);
+cudaError_t resnorm_bwd_f32_post(const ResNormArgs& a, bool whole, int sms, int* walkers, cudaStream_t s);
+cudaError_t resnorm_bwd_bf16(const ResNormArgs& a, bool whole, int sms, int* walkers, cudaStream_t s);
+cudaError_t resnorm_bwd_bf16_post(const ResNormArgs& a, bool whole, int sms, int* walkers, cudaStream_t s);
 
 }  // namespace grpo

@@ -3,8 +3,8 @@
 
 namespace grpo {
 
-cudaError_t resnorm_bwd_bf16_post(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
-  return resnorm_bwd_kind<__nv_bfloat16, true>(a, sms, walkers, s);
+cudaError_t resnorm_bwd_bf16_post(const ResNormArgs& a, bool whole, int sms, int* walkers, cudaStream_t s) {
+  return resnorm_bwd_kind<__nv_bfloat16, true>(a, whole, sms, walkers, s);
 }
 
 }  // namespace grpo

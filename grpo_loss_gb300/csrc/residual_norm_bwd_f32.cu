@@ -3,8 +3,8 @@
 
 namespace grpo {
 
-cudaError_t resnorm_bwd_f32(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
-  return resnorm_bwd_kind<float, false>(a, sms, walkers, s);
+cudaError_t resnorm_bwd_f32(const ResNormArgs& a, bool whole, int sms, int* walkers, cudaStream_t s) {
+  return resnorm_bwd_kind<float, false>(a, whole, sms, walkers, s);
 }
 
 }  // namespace grpo
