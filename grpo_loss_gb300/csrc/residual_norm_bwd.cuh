@@ -41,6 +41,12 @@ inline int resident_ctas(const void* kernel, int threads, int smem, std::atomic<
   return per_sm.load();
 }
 
+// Whether layer norms' second sums are in shared memory (see the kernel).
+template <int N, int G, int R, bool RMS, bool STRIDED>
+constexpr bool resnorm_stash() {
+  return !RMS && !STRIDED && N == 8 && G * R <= 256;
+}
+
 // Copies a row of d elements by the 16-byte granules it lies in while the G threads go on;
 // `to` has the place of the first granule.
 template <typename T, int G>
@@ -72,7 +78,7 @@ constexpr int staged_pitch(int d, int size) { return (d * size + 31) / 16 * 16; 
 // read what others copied. (RMS norms are told by the arguments then.)
 template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, bool STRIDED>
 __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walkers) {
-  static_assert(!STRIDED || (NV == 1 && R == 1 && !RMS && N % 2 == 0), "");
+  static_assert(!STRIDED || (NV == 1 && (R == 1 || G == 32) && !RMS && N % 2 == 0), "");
   constexpr int B = N * static_cast<int>(sizeof(T)), H = (N + 1) / 2;
   constexpr bool INNER = POST || GATE != GATE_NONE;
   constexpr int ARRAYS = 3 + INNER + (GATE == GATE_ROWS);  // dy, h, dh, x, gate
@@ -88,7 +94,33 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   // every group of a CTA makes the same number of turns: barriers are the CTA's
   const int turns = static_cast<int>((a.rows + walkers - 1) / walkers);
 
-  uint64_t w[NV][H], f[NV][H], dw[NV][H], db[NV][H], e1[NV][H], e0[NV][H];  // f: a, or scale gate
+  uint64_t w[NV][H], f[NV][H], dw[NV][H], e1[NV][H];  // f: a, or scale gate
+  // The sums of dy and of scale g, that layer norms have beside: in registers, or where these
+  // would leave an SM one CTA in shared memory, each thread its own.
+  constexpr bool STASH = resnorm_stash<N, G, R, RMS, STRIDED>();
+  uint64_t db_reg[STASH ? 1 : NV][H], e0_reg[STASH ? 1 : NV][H];
+  ulonglong2* const stash = reinterpret_cast<ulonglong2*>(ring_raw + 2 * ARRAYS * NV * B * G * R) + threadIdx.x;
+  auto load_sums = [&](int which, int k, uint64_t (&v)[H]) {  // 0: of dy, 1: of scale g
+    if constexpr (STASH) {
+#pragma unroll
+      for (int e = 0; e < H; e += 2) {
+        const ulonglong2 u = stash[((which * NV + k) * (H / 2) + e / 2) * (G * R)];
+        v[e] = u.x, v[e + 1] = u.y;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < H; ++e) v[e] = which ? e0_reg[k][e] : db_reg[k][e];
+    }
+  };
+  auto keep_sums = [&](int which, int k, const uint64_t (&v)[H]) {
+    if constexpr (STASH) {
+#pragma unroll
+      for (int e = 0; e < H; e += 2) stash[((which * NV + k) * (H / 2) + e / 2) * (G * R)] = make_ulonglong2(v[e], v[e + 1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < H; ++e) (which ? e0_reg[k][e] : db_reg[k][e]) = v[e];
+    }
+  };
   // column i of the thread's piece k; a piece's columns are all in the row, or with STRIDED each is
   auto column = [&](int k, int i = 0) { return STRIDED ? i * G + tid : (k * G + tid) * N + i; };
   auto inside = [&](int i) { return !STRIDED || column(0, i) < d; };
@@ -109,11 +141,14 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   const uint64_t zero = pair_of(0.f, 0.f), scale2 = pair_of(a.scale);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
+    uint64_t none[H];
 #pragma unroll
     for (int e = 0; e < H; ++e) {
-      w[k][e] = dw[k][e] = db[k][e] = e1[k][e] = e0[k][e] = zero;
+      w[k][e] = dw[k][e] = e1[k][e] = none[e] = zero;
       f[k][e] = scale2;
     }
+    keep_sums(0, k, none);
+    if constexpr (POST) keep_sums(1, k, none);
     if (column(k) < d) {
       load_pairs(a.weight, a.param_bf16, 0, k, w[k]);
       if constexpr (POST && GATE != GATE_SHARED) {
@@ -126,14 +161,15 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   }
 
   auto slot_of = [&](int half, int which, int k) -> V& { return ring[((half * ARRAYS + which) * NV + k) * (G * R)]; };
-  const int pitch = staged_pitch(d, sizeof(T));  // of a staged row
+  const int pitch = staged_pitch(d, sizeof(T));
+  unsigned char* const staged = ring_raw + threadIdx.x / G * (2 * ARRAYS * pitch);  // the group's
   auto fetch = [&](int n, int half) {
     if (n < mine) {
       const int64_t row = from + n;
       auto copy = [&](int which, const void* p, int64_t ld) {
         const T* q = static_cast<const T*>(p) + row * ld;
         if constexpr (STRIDED) {
-          stage_row<T, G>(ring_raw + (half * ARRAYS + which) * pitch, q, static_cast<const T*>(p), d, tid);
+          stage_row<T, G>(staged + (half * ARRAYS + which) * pitch, q, static_cast<const T*>(p), d, tid);
         } else {
 #pragma unroll
           for (int k = 0; k < NV; ++k)
@@ -160,7 +196,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
     Values u;
     if constexpr (STRIDED) {
       const int off = static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * ld) & 15);
-      u.p = reinterpret_cast<const T*>(ring_raw + (half * ARRAYS + which) * pitch + off);
+      u.p = reinterpret_cast<const T*>(staged + (half * ARRAYS + which) * pitch + off);
     } else {
       u.v = slot_of(half, which, k);
     }
@@ -205,8 +241,9 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
 #pragma unroll
     for (int k = 0; k < NV; ++k)
       if (column(k) < d) {
-        uint64_t pw[H], g[H], v[H];
+        uint64_t pw[H], g[H], v[H], e0[H];
         if constexpr (POST) {
+          load_sums(1, k, e0);
           load_pairs(a.post_weight, a.param_bf16, 0, k, pw);
           load_pairs(a.gate, a.gate_bf16, q * a.ld_gate, k, g);
         }
@@ -217,7 +254,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
             uint64_t pb[H];
             load_pairs(a.post_bias, a.param_bf16, 0, k, pb);
 #pragma unroll
-            for (int e = 0; e < H; ++e) v[e] = fma2(pb[e], e0[k][e], v[e]);
+            for (int e = 0; e < H; ++e) v[e] = fma2(pb[e], e0[e], v[e]);
           }
           store_sums(to, k, v);
         }
@@ -233,10 +270,11 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
             store_sums(p, k, v);
           };
           if (a.dpost_weight) add(part_of(a.at_dpw), e1[k]);
-          if (!RMS && a.dpost_bias) add(part_of(a.at_dpb), e0[k]);
+          if (!RMS && a.dpost_bias) add(part_of(a.at_dpb), e0);
         }
 #pragma unroll
-        for (int e = 0; e < H; ++e) e1[k][e] = e0[k][e] = zero;
+        for (int e = 0; e < H; ++e) e1[k][e] = e0[e] = zero;
+        if constexpr (POST) keep_sums(1, k, e0);
       }
     flushed = 1;
   };
@@ -265,7 +303,8 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
     if constexpr (STRIDED) {
       // this row is here, of every thread's copies, and the last one's place is free
       asm volatile("cp.async.wait_group 0;" ::: "memory");
-      __syncthreads();
+      if constexpr (G == 32) __syncwarp();
+      else __syncthreads();
       fetch(n + 1, half ^ 1);
     } else {
       fetch(n + 1, half ^ 1);
@@ -308,11 +347,13 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
             vx = values(half, 3, k, a.x, a.ld_x, row);
             if constexpr (GATE == GATE_ROWS) vg = values(half, 4, k, a.gate, a.ld_gate, row);
           }
+          uint64_t db[H];
+          if (!RMS) load_sums(0, k, db);
 #pragma unroll
           for (int e = 0; e < H; ++e) {
             const uint64_t y = pair(vy, e), hat = hat_of(pair(vh, e), m2, r2), yw = mul2(y, w[k][e]);
             dw[k][e] = fma2(y, hat, dw[k][e]);
-            if (!RMS) db[k][e] = add2(db[k][e], y);
+            if (!RMS) db[e] = add2(db[e], y);
             t[0] = fma2(yw, hat, t[0]);
             if (!RMS) t[1] = add2(t[1], yw);
             if constexpr (POST) {
@@ -331,6 +372,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
               }
             }
           }
+          if (!RMS) keep_sums(0, k, db);
         }
     }
     float sums[SUMS];
@@ -365,6 +407,8 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
         if constexpr (INNER) vx = values(half, 3, k, a.x, a.ld_x, row);
         if constexpr (GATE == GATE_ROWS) vg = values(half, 4, k, a.gate, a.ld_gate, row);
         float res[2 * H], dx[2 * H], dg[2 * H];
+        uint64_t e0[H];
+        if constexpr (POST && !RMS) load_sums(1, k, e0);
         uint64_t pb[H];
 #pragma unroll
         for (int e = 0; e < H; ++e) pb[e] = zero;
@@ -392,13 +436,14 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
               uint64_t sg = mul2(g, scale2);  // with a gate for every row: its part of q too
               if constexpr (GATE == GATE_ROWS) sg = mul2(sg, pair(vg, e));
               e1[k][e] = fma2(sg, kx, e1[k][e]);
-              if (POST && !RMS) e0[k][e] = add2(e0[k][e], sg);
+              if (POST && !RMS) e0[e] = add2(e0[e], sg);
             }
             if constexpr (POST) out = mul2(fma2(kx, o2, add2(out, o1)), pr2);
           }
           const float2 ov = of_pair(out);
           dx[2 * e] = ov.x, dx[2 * e + 1] = ov.y;
         }
+        if constexpr (POST && !RMS) keep_sums(1, k, e0);
         store(to_res, k, res);
         if (to_x) store(to_x, k, dx);
         if constexpr (GATE == GATE_ROWS)
@@ -411,10 +456,17 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   for (int k = 0; k < NV; ++k)
     if (column(k) < d) {
       if (a.dweight) store_sums(part_of(a.at_dw), k, dw[k]);
-      if (!RMS && a.dbias) store_sums(part_of(a.at_db), k, db[k]);
+      uint64_t v[H];
+      if (!RMS && a.dbias) {
+        load_sums(0, k, v);
+        store_sums(part_of(a.at_db), k, v);
+      }
       if constexpr (POST && GATE != GATE_SHARED) {
         if (a.dpost_weight) store_sums(part_of(a.at_dpw), k, e1[k]);
-        if (!RMS && a.dpost_bias) store_sums(part_of(a.at_dpb), k, e0[k]);
+        if (!RMS && a.dpost_bias) {
+          load_sums(1, k, v);
+          store_sums(part_of(a.at_dpb), k, v);
+        }
       }
     }
 }
@@ -424,7 +476,8 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
 template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, bool STRIDED = false>
 cudaError_t resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
   constexpr int arrays = 3 + (POST || GATE != GATE_NONE) + (GATE == GATE_ROWS);
-  constexpr int smem = 2 * arrays * (NV * N * static_cast<int>(sizeof(T)) * G * R + (STRIDED ? 32 : 0));
+  constexpr int stash = resnorm_stash<N, G, R, RMS, STRIDED>() ? (POST ? 2 : 1) * NV * N * 4 * G * R : 0;
+  constexpr int smem = 2 * arrays * (NV * N * static_cast<int>(sizeof(T)) * G + (STRIDED ? 32 : 0)) * R + stash;
   static_assert(smem <= kResNormRing, "shared memory");
   auto kernel = k_resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE, STRIDED>;
   static std::atomic<uint64_t> configured{0};
@@ -465,9 +518,12 @@ cudaError_t resnorm_bwd_n(const ResNormArgs& a, int sms, int* walkers, cudaStrea
 }
 template <typename T, bool POST, int GATE>
 cudaError_t resnorm_bwd_strided(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
+  if (a.d <= 256) return resnorm_bwd<T, 8, 1, 32, 8, false, POST, GATE, true>(a, sms, walkers, s);
   if (a.d <= 1024) return resnorm_bwd<T, 8, 1, 128, 1, false, POST, GATE, true>(a, sms, walkers, s);
   if (a.d <= 2048) return resnorm_bwd<T, 8, 1, 256, 1, false, POST, GATE, true>(a, sms, walkers, s);
   if (a.d <= 4096) return resnorm_bwd<T, 8, 1, 512, 1, false, POST, GATE, true>(a, sms, walkers, s);
+  if constexpr (sizeof(T) == 2)
+    if (a.d <= 8192) return resnorm_bwd<T, 8, 1, 1024, 1, false, POST, GATE, true>(a, sms, walkers, s);
   return cudaErrorNotSupported;
 }
 
