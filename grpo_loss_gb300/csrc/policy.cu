@@ -109,6 +109,18 @@ __device__ void cta_sums(double (&v)[M]) {
     }
   }
 }
+// A sum of whole numbers, returned to every thread.
+__device__ __forceinline__ int64_t cta_total(int64_t v) {
+  __shared__ int64_t part[kWarps];
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) v += part[w];
+  return v;
+}
 
 // A thread's sums.
 struct Sums {
@@ -247,7 +259,7 @@ __device__ void count_phase(const PolicyArgs& a, const Counts& to_counts, int ct
   const int lane = threadIdx.x & 31;
   const bool thin = a.T < 16;
   const int64_t pieces = a.B * a.pieces, step = static_cast<int64_t>(ctas) * (thin ? kThreads : kWarps);
-  double total[1] = {0.0};  // (whole numbers)
+  int64_t total = 0;
   for (int64_t i = static_cast<int64_t>(cta) * (thin ? kThreads : kWarps) + (thin ? threadIdx.x : threadIdx.x >> 5); i < pieces; i += step) {
     const int64_t row = a.pieces == 1 ? i : i / a.pieces;
     const int T = static_cast<int>(a.T), from = static_cast<int>(i - row * a.pieces) * kPiece - shift_of<VEC>(a, row);
@@ -291,12 +303,11 @@ __device__ void count_phase(const PolicyArgs& a, const Counts& to_counts, int ct
     if (!thin) n = __reduce_add_sync(0xffffffffu, n);
     put(to_counts.n, i, n, thin);
     if (WTOO) put(to_counts.w, i, sum, thin);
-    if (thin || lane == 0) total[0] += n;
+    if (thin || lane == 0) total += n;
   }
   if (a.reduce != 1) return;
-  cta_sums(total);
-  total[0] = __shfl_sync(0xffffffffu, total[0], 0);
-  if (threadIdx.x < 32) put(to_counts.cta, cta, static_cast<int64_t>(total[0]), false);
+  total = cta_total(total);
+  if (threadIdx.x < 32) put(to_counts.cta, cta, total, false);
 }
 
 // --------------------------------------------------------------- the loss
@@ -332,16 +343,22 @@ __device__ __forceinline__ Row row_of(const PolicyArgs& a, float same, int64_t r
   if (a.reduce == 0) r.c = 1.f / (static_cast<float>(a.B) * static_cast<float>(n));
   if (!TADV) r.A = a.adv[row];
   if (W == W_SEQUENCE && n > 0) {
-    const double mean = w / n;
-    const float hi = static_cast<float>(mean);
-    r.em1 = static_cast<float>(expm1(mean));
+    // the mean in two floats, and e^mean - 1 of both (float64's functions would take longer
+    // than the sequence's tokens)
+    float hi = static_cast<float>(w) / static_cast<float>(n), lo = 0.f;
+    if (isfinite(hi)) {
+      const float rest = static_cast<float>(fma(-static_cast<double>(hi), static_cast<double>(n), w)) / static_cast<float>(n);
+      lo = rest - ((hi + rest) - hi);
+      hi += rest;
+    }
+    r.em1 = expm1f(hi);
+    if (isfinite(r.em1)) r.em1 = fmaf(r.em1 + 1.f, lo, r.em1);
     if (!TADV) {
       bool above, below;
-      sides_of(a, r.A, bounds_of(a, r.A), hi, static_cast<float>(mean - static_cast<double>(hi)), above, below);
+      sides_of(a, r.A, bounds_of(a, r.A), hi, lo, above, below);
       r.held = above ? 1 : below ? 2 : 0;
     } else {  // by the sign of the token's: bits 0 and 1 for A > 0, 2 and 3 for A < 0
       bool above, below;
-      const float lo = static_cast<float>(mean - static_cast<double>(hi));
       sides_of(a, 1.f, bounds_of(a, 1.f), hi, lo, above, below);
       r.held = above ? 1 : 0;
       sides_of(a, -1.f, bounds_of(a, -1.f), hi, lo, above, below);
@@ -806,15 +823,11 @@ __device__ __forceinline__ void short_rows(const PolicyArgs& a, const Counts& co
 
 template <bool VEC, int W, bool REF, bool TADV>
 __device__ void loss_phase(const PolicyArgs& a, const Counts& counts, int cta, int ctas, double (&out)[S_ALL]) {
-  __shared__ float s_same;
   float same = a.inv_divisor;  // (unused with a weight for each sequence)
   if (a.reduce == 1) {
-    double v[1] = {0.0};
-    for (int i = threadIdx.x; i < a.count_ctas; i += kThreads) v[0] += static_cast<double>(counts.cta[i]);
-    cta_sums(v);
-    if (threadIdx.x == 0) s_same = static_cast<float>(1.0 / v[0]);
-    __syncthreads();
-    same = s_same;
+    int64_t n = 0;
+    for (int i = threadIdx.x; i < a.count_ctas; i += kThreads) n += counts.cta[i];
+    same = 1.f / static_cast<float>(cta_total(n));
   }
   Sums sums;
   if (a.T < kShort) short_rows<W, REF, TADV>(a, counts, cta, ctas, same, sums);
