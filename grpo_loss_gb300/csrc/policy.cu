@@ -23,7 +23,7 @@ constexpr int kPiece = 2048;             // tokens of a sequence that are counte
 constexpr int kUnit = 32 * kTokens;      // tokens that a warp takes at a time
 constexpr int kChunk = kThreads * kTokens;  // of short sequences, that a CTA takes at a time
 constexpr int kShort = 128;              // sequences below this are taken several a warp
-constexpr int kLossCtas = 3;             // of an SM, at a time
+constexpr int kLossCtas = 2;             // of an SM, at a time
 constexpr int kCluster = 8;
 constexpr int64_t kSmall = 16 * kChunk;  // tokens that one cluster takes
 
@@ -727,52 +727,78 @@ __device__ __forceinline__ void long_rows(const PolicyArgs& a, const Counts& cou
   const int64_t warps = static_cast<int64_t>(ctas) * kWarps, warp = static_cast<int64_t>(cta) * kWarps + (threadIdx.x >> 5);
   const int64_t u0 = all / warps * warp + (warp < all % warps ? warp : all % warps), u1 = u0 + all / warps + (warp < all % warps ? 1 : 0);
   if (u0 >= u1) return;
-  int64_t row = u0 / units, piece = -1;
-  int unit = static_cast<int>(u0 - row * units), here = 0;
   const int T = static_cast<int>(a.T);
+  // Where a unit is, and how many valid tokens its piece has; its operands. The next unit's
+  // are on their way while one is worked on, and the count of the one behind it, which says
+  // whether there is anything to load.
+  struct Place {
+    int64_t row;
+    int unit;
+  };
+  struct Raw {
+    Eight q, o, p, A;
+    Mask valid;
+  };
+  auto step = [&](Place& x) {
+    if (++x.unit == units) x.unit = 0, ++x.row;
+  };
+  auto count_of = [&](const Place& x) { return counts.n[x.row * a.pieces + (a.pieces > 1 ? x.unit / (kPiece / kUnit) : 0)]; };
+  auto first_of = [&](const Place& x) { return x.unit * kUnit - shift_of<VEC>(a, x.row); };
+  auto load = [&](const Place& x, int here, Raw& raw) {
+    if (here == 0) return;
+    const Rows g = rows_of<W, REF, TADV>(a, x.row, 0);
+    const int t0 = first_of(x);
+    raw.valid = load_mask<VEC>(g.mask, t0, T);
+    if (W == W_TOKEN || REF) load_tokens<VEC>(g.q, t0, T, raw.q);
+    if (W == W_TOKEN) load_tokens<VEC>(g.o, t0, T, raw.o);
+    if (REF) load_tokens<VEC>(g.p, t0, T, raw.p);
+    if (TADV) load_tokens<VEC>(g.A, t0, T, raw.A);
+  };
+  Place at = {u0 / units, 0}, ahead;
+  at.unit = static_cast<int>(u0 - at.row * units);
+  ahead = at;
+  int here = count_of(at), here_next = 0;
+  Raw raw, next;
+  load(at, here, raw);
+  if (u0 + 1 < u1) {
+    step(ahead);
+    here_next = count_of(ahead);
+  }
   Row r = {0.f, 0.f, 0.f, 0};  // (no token yet)
   Bounds b = {INFINITY, -INFINITY, 0.f};
   RowSums row_sums;
   row_sums.clear();
-  bool fresh = true;
+  int64_t known = -1;  // the sequence that r is of
   for (int64_t u = u0; u < u1; ++u) {
-    const int t0 = unit * kUnit - shift_of<VEC>(a, row);
-    const int64_t now = row * a.pieces + (a.pieces > 1 ? unit / (kPiece / kUnit) : 0);
-    if (now != piece) {
-      piece = now;
-      here = counts.n[piece];
+    int here_after = 0;
+    if (u + 1 < u1) {
+      load(ahead, here_next, next);
+      step(ahead);
+      if (u + 2 < u1) here_after = count_of(ahead);
     }
-    const Rows g = rows_of<W, REF, TADV>(a, row, 0);
-    Eight q, o, p, A;
-    Mask valid = {{0, 0}};
-    if (here > 0) {
-      valid = load_mask<VEC>(g.mask, t0, T);
-      if (W == W_TOKEN || REF) load_tokens<VEC>(g.q, t0, T, q);
-      if (W == W_TOKEN) load_tokens<VEC>(g.o, t0, T, o);
-      if (REF) load_tokens<VEC>(g.p, t0, T, p);
-      if (TADV) load_tokens<VEC>(g.A, t0, T, A);
-    }
-    if (fresh && here > 0) {
-      fresh = false;
+    if (here > 0 && at.row != known) {
+      known = at.row;
       fold<W, REF, TADV>(a, r, row_sums, sums);
       int n = 0;
       double w = 0.0;
       if (a.reduce == 0 || W == W_SEQUENCE) {
         for (int64_t i = lane; i < a.pieces; i += 32) {
-          n += counts.n[row * a.pieces + i];
-          if (W == W_SEQUENCE) w += counts.w[row * a.pieces + i];
+          n += counts.n[known * a.pieces + i];
+          if (W == W_SEQUENCE) w += counts.w[known * a.pieces + i];
         }
         n = __reduce_add_sync(0xffffffffu, n);
         if (W == W_SEQUENCE) w = warp_sum(w);
       }
-      r = row_of<W, TADV>(a, same, row, n, w);
+      r = row_of<W, TADV>(a, same, known, n, w);
       b = bounds_of(a, r.A);
       if (r.A == 0.f) b.top = INFINITY;  // (nothing to hold, or to count)
     }
+    const Rows g = rows_of<W, REF, TADV>(a, at.row, 0);
+    const int t0 = first_of(at);
     if (here > 0) {
       // (what the piece's tokens share is added with its first unit)
-      if (lane == 0 && (a.pieces > 1 ? unit % (kPiece / kUnit) : unit) == 0) add_row<W, TADV>(a, r, here, sums);
-      unit_tokens<VEC, W, REF, TADV>(a, r, b, g, t0, valid, q, o, p, A, row_sums, sums);
+      if (lane == 0 && (a.pieces > 1 ? at.unit % (kPiece / kUnit) : at.unit) == 0) add_row<W, TADV>(a, r, here, sums);
+      unit_tokens<VEC, W, REF, TADV>(a, r, b, g, t0, raw.valid, raw.q, raw.o, raw.p, raw.A, row_sums, sums);
     } else if (g.d) {  // nothing but the gradient's zeros
 #pragma unroll
       for (int j = 0; j < kTokens; ++j) {
@@ -780,11 +806,10 @@ __device__ __forceinline__ void long_rows(const PolicyArgs& a, const Counts& cou
         if (i >= 0 && i < T) g.d[i] = 0.f;
       }
     }
-    if (++unit == units) {
-      unit = 0;
-      ++row;
-      fresh = true;
-    }
+    step(at);
+    raw = next;
+    here = here_next;
+    here_next = here_after;
   }
   fold<W, REF, TADV>(a, r, row_sums, sums);
 }
