@@ -890,20 +890,26 @@ def _grad_table(grads, out, name: str):
 def _no_overlap(sizes, places, outs, codes) -> None:
     """A clipped tensor is written: no other may share its bytes (two gradients that are only
     read may share theirs)."""
-    spans = [(o, o + (n << 2 if c == GRPO_F32 else n << 1), True, i)
-             for i, (n, o, c) in enumerate(zip(sizes, outs, codes)) if n]
+    ends = [o + (n << 2 if c == GRPO_F32 else n << 1) for n, o, c in zip(sizes, outs, codes)]
+    starts, read = outs, []
     if outs is not places:
-        spans += [(p, p + (n << 2 if c == GRPO_F32 else n << 1), False, i)
-                  for i, (n, p, o, c) in enumerate(zip(sizes, places, outs, codes)) if n and p != o]
-    spans.sort()
+        read = [(p, p + e - o) for p, o, e in zip(places, outs, ends) if p != o]
+        starts, ends = starts + [p for p, _ in read], ends + [e for _, e in read]
+    # (spans are apart where, in order, each begins behind the end before; one of no bytes
+    # may lie anywhere, and only seem not to)
+    if not any(map(operator.lt, sorted(starts)[1:], sorted(ends))):
+        return
+    spans = sorted([(o, o + (n << 2 if c == GRPO_F32 else n << 1), True, i)
+                    for i, (n, o, c) in enumerate(zip(sizes, outs, codes)) if n] +
+                   [(p, e, False, -1) for p, e in read if e > p])
     last = last_written = 0
     for start, end, written, i in spans:
         if start < last and (written or start < last_written):
-            raise ValueError("the gradient or out of number %d overlaps another: what is written is one tensor's own" % i)
-        if end > last:
-            last = end
-        if written and end > last_written:
-            last_written = end
+            raise ValueError("the gradients or out overlap%s: what is written is one tensor's own" %
+                             (" at number %d" % i if written else ""))
+        last = max(last, end)
+        if written:
+            last_written = max(last_written, end)
 
 
 def _grad_call(grads, clip: bool, max_norm, norm_type, eps, out, norm, factor, workspace):

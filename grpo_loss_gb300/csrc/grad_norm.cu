@@ -24,7 +24,8 @@ constexpr int kNormCtas = 3, kScaleCtas = 4;            // of an SM, at a time
 constexpr int kCluster = 8;
 // Lists of up to so many chunks take the one launch.
 constexpr int kSmallChunks = 2 * kCluster;
-constexpr int kSmallTensors = 32;
+// Tables of a launch: a kernel's parameters are copied whole.
+constexpr int kSmallTensors = 32, kSomeTensors = 128;
 
 // The table of one launch, a kernel parameter (a captured launch holds its own).
 template <int MOST>
@@ -343,8 +344,9 @@ cudaError_t launch_grad_small(const GradTensor* t, int n, const GradJoin& j, int
   return cudaGetLastError();
 }
 cudaError_t launch_grad_norm(const GradTensor* t, int n, int inf, int sms, double* partial, int* parts, cudaStream_t s) {
-  return n <= kSmallTensors ? norm_launch<kSmallTensors>(t, n, inf, sms, partial, parts, s)
-                            : norm_launch<kGradMaxTensors>(t, n, inf, sms, partial, parts, s);
+  return n <= kSmallTensors  ? norm_launch<kSmallTensors>(t, n, inf, sms, partial, parts, s)
+         : n <= kSomeTensors ? norm_launch<kSomeTensors>(t, n, inf, sms, partial, parts, s)
+                             : norm_launch<kGradMaxTensors>(t, n, inf, sms, partial, parts, s);
 }
 cudaError_t launch_grad_join(const GradJoin& j, cudaStream_t s) {
   k_grad_join<<<1, kThreads, 0, s>>>(j.partial, j.parts, j.inf, j.max_norm, j.eps, j.norm, j.factor, nullptr);
@@ -355,7 +357,9 @@ cudaError_t launch_grad_fold(double* partial, int parts, int inf, cudaStream_t s
   return cudaGetLastError();
 }
 cudaError_t launch_grad_scale(const GradTensor* t, int n, const GradJoin& j, int sms, cudaStream_t s) {
-  return n <= kSmallTensors ? scale_launch<kSmallTensors>(t, n, j, sms, s) : scale_launch<kGradMaxTensors>(t, n, j, sms, s);
+  return n <= kSmallTensors  ? scale_launch<kSmallTensors>(t, n, j, sms, s)
+         : n <= kSomeTensors ? scale_launch<kSomeTensors>(t, n, j, sms, s)
+                             : scale_launch<kGradMaxTensors>(t, n, j, sms, s);
 }
 
 }  // namespace grpo
