@@ -8,6 +8,8 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "f32x2.cuh"
 #include "internal.h"
 
@@ -101,7 +103,7 @@ __device__ double cta_join(double v, int inf) {
 // of an embedding that no token had, are known by their bits.
 template <bool BF16>
 __device__ __forceinline__ double squares(const uint4 (&v)[kPieces]) {
-  auto sum = [&](uint64_t scale) {
+  auto sum = [&](uint64_t scale, auto scaled) {
     uint64_t s[2] = {pair_of(0.f), pair_of(0.f)};
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
@@ -109,14 +111,14 @@ __device__ __forceinline__ double squares(const uint4 (&v)[kPieces]) {
 #pragma unroll
       for (int e = 0; e < (BF16 ? 4 : 2); ++e) {
         uint64_t p = BF16 ? pair_in(w[e]) : pair_of(w[2 * (e & 1)], w[2 * (e & 1) + 1]);
-        p = mul2(p, scale);
+        if constexpr (decltype(scaled)::value) p = mul2(p, scale);
         s[e & 1] = fma2(p, p, s[e & 1]);
       }
     }
     const float2 a = of_pair(s[0]), b = of_pair(s[1]);
     return (a.x + a.y) + (b.x + b.y);
   };
-  const float s = sum(pair_of(1.f));
+  const float s = sum(0, std::false_type());
   if (s >= 0x1p-60f && s <= 0x1p100f) return s;
   uint32_t top = 0;  // the largest magnitude's bits
 #pragma unroll
@@ -131,7 +133,7 @@ __device__ __forceinline__ double squares(const uint4 (&v)[kPieces]) {
   if (top == 0) return 0.0;
   if (top >= 0x7F800000u) return s;  // an infinity, or a NaN
   const int up = max(min(254 - static_cast<int>(top >> 23), 253), 1);  // exponent byte of the scale: values below 2
-  const float t = sum(pair_of(__uint_as_float(static_cast<uint32_t>(up) << 23)));
+  const float t = sum(pair_of(__uint_as_float(static_cast<uint32_t>(up) << 23)), std::true_type());
   return ldexp(static_cast<double>(t), 2 * (127 - up));
 }
 template <bool BF16>

@@ -522,6 +522,24 @@ cudaError_t fwd_any(const ResNormArgs& a, int sms, cudaStream_t s) {
   return cudaErrorNotSupported;
 }
 
+// The same for gates of which there are many, each shared by few walkers: a thread a
+// column, one CTA row for every border between walkers; the first border inside a gate's
+// rows takes them.
+__global__ void __launch_bounds__(256) k_resnorm_join_gates(ResNormArgs a, int walkers) {
+  const int64_t border = first_row(a.rows, static_cast<int64_t>(blockIdx.y) + 1, walkers), q = border / a.gate_rows;
+  const int64_t q0 = q * a.gate_rows, col = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (border == q0) return;  // no gate has rows on both sides
+  const int64_t w0 = walker_of(a.rows, q0, walkers), w1 = walker_of(a.rows, q0 + a.gate_rows - 1, walkers);
+  if (w0 != static_cast<int64_t>(blockIdx.y) || col >= a.d) return;
+  float sum = 0.f;
+  for (int64_t w = w0; w <= w1; ++w) {
+    const int which = w == w0 && q0 > first_row(a.rows, w0, walkers) ? a.at_tail : a.at_head;
+    sum += a.partial[(static_cast<int64_t>(which) * walkers + w) * a.d + col];
+  }
+  static_cast<float*>(a.dgate)[q * a.d + col] = sum;
+}
+constexpr int64_t kFewGates = 32;
+
 cudaError_t allow_row(const void* kernel, int64_t d) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(d * 4));
 }
@@ -564,8 +582,10 @@ cudaError_t launch_resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cuda
 }
 cudaError_t launch_resnorm_join(const ResNormArgs& a, int walkers, cudaStream_t s) {
   const int64_t gates = a.dgate && a.gate_rows > 1 ? a.rows / a.gate_rows : 0;
-  const dim3 grid(static_cast<unsigned>((a.d + 31) / 32), static_cast<unsigned>(a.at_head + gates));
-  k_resnorm_join<<<grid, 1024, 0, s>>>(a, walkers);
+  const int64_t few = a.at_head + (gates <= kFewGates ? gates : 0);
+  if (few > 0) k_resnorm_join<<<dim3(static_cast<unsigned>((a.d + 31) / 32), static_cast<unsigned>(few)), 1024, 0, s>>>(a, walkers);
+  if (gates > kFewGates && walkers > 1)
+    k_resnorm_join_gates<<<dim3(static_cast<unsigned>((a.d + 255) / 256), static_cast<unsigned>(walkers - 1)), 256, 0, s>>>(a, walkers);
   return cudaGetLastError();
 }
 

@@ -164,3 +164,10 @@ def test_graphs_with_workspaces_of_their_own_overlap():
         torch.cuda.synchronize()
         for _, outs, want, _, _ in made:
             assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.gpu
+def test_the_example_runs_with_several_updates_a_rollout():
+    from tests.test_examples import load
+    rewards, greedy = load().run(2, seed=0, quiet=True, updates=3)
+    assert len(rewards) == 2 and all(0.0 <= r <= 1.0 for r in rewards) and 0.0 <= greedy <= 1.0
