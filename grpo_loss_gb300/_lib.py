@@ -422,6 +422,16 @@ def _vec_out(t, name: str, dtype, numel: int, device):
     return t, _vec_ptr(t, name, dtype, numel, device)
 
 
+def _vec_outs(given, numel: int, device):
+    """[(tensor, pointer)] of float32 outputs that are given, made, or not there: given has
+    (tensor or None, name, whether it is made). Three and more are made at once."""
+    if sum(t is None and made for t, _, made in given) >= 3:
+        rows = iter(torch.empty(len(given), numel, dtype=torch.float32, device=device).unbind(0))
+        given = [(next(rows) if t is None and made else t, name, made) for t, name, made in given]
+    return [(None, None) if t is None and not made else _vec_out(t, name, torch.float32, numel, device)
+            for t, name, made in given]
+
+
 def _call(fn, where: str, device, stream, *args) -> None:
     """fn(*args, stream) with ``device`` current, on ``stream`` or the device's
     current one. The launches of small operators are bound by the host: torch's
@@ -631,6 +641,10 @@ def policy_loss(logp: torch.Tensor, advantages: torch.Tensor, mask: torch.Tensor
                                divisor, need_dlogp, loss, dlogp, stats, workspace)
     if logp.dim() != 2:
         raise ValueError("logp must be 2-D")
+    try:
+        clip_low, clip_high = clip
+    except (TypeError, ValueError):
+        raise ValueError("clip must be two numbers, (low, high), got %r" % (clip,)) from None
     if ratio not in _RATIOS:
         raise ValueError("ratio must be one of %s, got %r" % (sorted(_RATIOS), ratio))
     if reduce not in _REDUCES:
@@ -657,7 +671,7 @@ def policy_loss(logp: torch.Tensor, advantages: torch.Tensor, mask: torch.Tensor
     dp, ld_d = None, 0
     if dlogp is not None or need_dlogp:
         dlogp, dp, ld_d = _rows_out(dlogp, "dlogp", f32, B, T, dev)
-    problem = PolicyProblem(B, T, ld, ld_old, ld_ref, ld_adv, ld_mask, ld_d, clip[0], clip[1], dual_clip or 0.0, beta,
+    problem = PolicyProblem(B, T, ld, ld_old, ld_ref, ld_adv, ld_mask, ld_d, clip_low, clip_high, dual_clip or 0.0, beta,
                             divisor or 0.0, _RATIOS[ratio], _REDUCES[reduce], 1 if per_token else 0)
     L = lib()
     size = 0 if workspace is not None else _bytes(("policy", B, T, ratio), L.grpo_policy_loss_workspace_size,
@@ -739,10 +753,11 @@ def residual_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: torch.Ten
     given = h, y, None if rms else mean, rstd, post_mean if post and not rms else None, post_rstd if post else None
     h, hp, ld_h = _rows_out(h, "h", dt, rows, d, dev)
     y, yp, ld_y = _rows_out(y, "y", dt, rows, d, dev)
-    mean, mp = (None, None) if rms else _vec_out(mean, "mean", f32, rows, dev)
-    rstd, rp = _vec_out(rstd, "rstd", f32, rows, dev)
-    post_mean, pmp = (None, None) if rms or not post else _vec_out(post_mean, "post_mean", f32, rows, dev)
-    post_rstd, prp = _vec_out(post_rstd, "post_rstd", f32, rows, dev) if post else (None, None)
+    layer = not rms
+    (mean, mp), (rstd, rp), (post_mean, pmp), (post_rstd, prp) = _vec_outs(
+        ((mean if layer else None, "mean", layer), (rstd, "rstd", True),
+         (post_mean if layer and post else None, "post_mean", layer and post),
+         (post_rstd if post else None, "post_rstd", post)), rows, dev)
     problem = ResidualNormProblem(rows, d, ld_x, ld_res, ld_h, ld_y, ld_gate, 0, 0, 0, 0, 0, gate_rows, eps, scale,
                                   1 if rms else 0, code, pcode, gcode)
     _call(lib().grpo_residual_norm_fwd, "grpo_residual_norm_fwd", dev, None, problem, xp, sp,
@@ -794,16 +809,11 @@ def residual_norm_bwd(dy: torch.Tensor, dh, h: torch.Tensor, weight: torch.Tenso
     dxp, ld_dx, same = None, 0, not inner and scale == 1.0 and dx is None
     if not same:
         dx, dxp, ld_dx = _rows_out(dx, "dx", dt, rows, d, dev)
-    wp = bp = pwp = pbp = dgp = None
-    ld_dg = 0
-    if dweight is not None or need_params:
-        dweight, wp = _vec_out(dweight, "dweight", f32, d, dev)
-    if dbias is not None or (need_params and bias and not rms):
-        dbias, bp = _vec_out(dbias, "dbias", f32, d, dev)
-    if dpost_weight is not None or (need_params and post):
-        dpost_weight, pwp = _vec_out(dpost_weight, "dpost_weight", f32, d, dev)
-    if dpost_bias is not None or (need_params and post_bias is not None):
-        dpost_bias, pbp = _vec_out(dpost_bias, "dpost_bias", f32, d, dev)
+    (dweight, wp), (dbias, bp), (dpost_weight, pwp), (dpost_bias, pbp) = _vec_outs(
+        ((dweight, "dweight", need_params), (dbias, "dbias", need_params and bias and not rms),
+         (dpost_weight, "dpost_weight", need_params and post),
+         (dpost_bias, "dpost_bias", need_params and post_bias is not None)), d, dev)
+    dgp, ld_dg = None, 0
     if dgate is not None or (gate is not None and need_dgate):
         if gate is None:
             raise ValueError("dgate needs a gate")

@@ -378,7 +378,7 @@ def test_refuses_wrong_arguments(monkeypatch):
     for bad, word in ((dict(logp=q[0]), "2-D"), (dict(logp=q.double()), "float32"), (dict(mask=mask.int()), "bool or uint8"),
                       (dict(mask=mask[:, :5]), "shape"), (dict(advantages=adv[:2]), "elements"),
                       (dict(advantages=torch.zeros(3, 7)), "shape"), (dict(logp_old=old.t().contiguous().t()), "contiguous"),
-                      (dict(ratio="both"), "ratio"), (dict(reduce="sum"), "reduce"), (dict(reduce="constant"), "divisor"),
+                      (dict(clip=0.2), "clip"), (dict(clip=(0.1, 0.2, 0.3)), "clip"), (dict(ratio="both"), "ratio"), (dict(reduce="sum"), "reduce"), (dict(reduce="constant"), "divisor"),
                       (dict(divisor=3.0), "divisor"), (dict(dlogp=torch.zeros(1, 8).expand(3, 8)), "row stride"),
                       (dict(loss=torch.zeros(2)), "elements"), (dict(stats=torch.zeros(3)), "elements")):
         with pytest.raises(ValueError, match=word):
