@@ -164,17 +164,46 @@ __global__ void __launch_bounds__(G * R) k_resnorm_fwd(ResNormArgs a) {
   }
 }
 
-// Rows that do not come in whole pieces: a CTA walks over rows, each staged by the granules
-// it lies in while the one before is worked on; a thread's N columns are G apart, and
-// their parameters stay in registers.
+// Rows that do not come in whole pieces: a group of threads walks over rows, each staged by
+// the granules it lies in while the one before is worked on; a thread's N columns are G
+// apart. The weights of its columns stay in registers; the biases, and a gate as long as it
+// is shared, in shared memory, each thread its own. (99900 x 1001 bf16, RMS with a post norm:
+// 194 us; eight columns a thread, and what is there asked for column by column, 269; single
+// elements from global memory 451.)
+struct StridedLayout {
+  int pitch, arrays;                     // staged rows: x, residual and a gate of the same type
+  bool gate_staged;
+  int gate, bias, post_bias, bytes;      // offsets of the vectors, -1 where there is none; a group's size
+};
+__host__ __device__ __forceinline__ StridedLayout strided_layout(const ResNormArgs& a) {
+  StridedLayout l;
+  const int d = static_cast<int>(a.d);
+  l.pitch = staged_pitch(d, a.bf16 ? 2 : 4);
+  l.gate_staged = a.gate && a.gate_rows == 1 && a.gate_bf16 == a.bf16;
+  l.arrays = l.gate_staged ? 3 : 2;
+  int at = 2 * l.arrays * l.pitch;
+  auto take = [&](bool there) {
+    const int from = there ? at : -1;
+    if (there) at += (d * 4 + 15) / 16 * 16;
+    return from;
+  };
+  l.gate = take(a.gate && !l.gate_staged);
+  l.bias = take(a.bias != nullptr);
+  l.post_bias = take(a.post_bias != nullptr);
+  l.bytes = at;
+  return l;
+}
 template <typename T, int N, int G, int R, bool POST>
-__global__ void __launch_bounds__(G * R) k_resnorm_fwd_strided(ResNormArgs a) {
+__global__ void __launch_bounds__(G * R) k_resnorm_fwd_strided(ResNormArgs a, int walkers) {
   static_assert(R == 1 || G == 32, "");
   extern __shared__ __align__(16) unsigned char staged_raw[];
   __shared__ float part[2 * 128];
-  const int tid = threadIdx.x % G, d = static_cast<int>(a.d), pitch = staged_pitch(d, sizeof(T));
-  unsigned char* const staged = staged_raw + threadIdx.x / G * (4 * pitch);  // the group's
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G, step = static_cast<int64_t>(gridDim.x) * R;
+  const StridedLayout l = strided_layout(a);
+  const int tid = threadIdx.x % G, d = static_cast<int>(a.d), pitch = l.pitch;
+  unsigned char* const staged = staged_raw + threadIdx.x / G * l.bytes;  // the group's
+  const int64_t walker = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
+  if (R > 1 && walker >= walkers) return;  // (no barrier but the warp's)
+  const int64_t from = first_row(a.rows, walker, walkers), to = first_row(a.rows, walker + 1, walkers);
   const float inv_d = 1.f / d;
   auto column = [&](int i) { return i * G + tid; };
   float w[N], pw[N];
@@ -183,85 +212,103 @@ __global__ void __launch_bounds__(G * R) k_resnorm_fwd_strided(ResNormArgs a) {
     w[i] = column(i) < d ? param(a.weight, a.param_bf16, column(i)) : 0.f;
     if (POST) pw[i] = column(i) < d ? param(a.post_weight, a.param_bf16, column(i)) : 0.f;
   }
+  auto vector = [&](int at) { return reinterpret_cast<float*>(staged + at); };
+  auto keep = [&](int at_smem, const void* p, int bf16, int64_t first) {
+    for (int i = 0; i < N; ++i)
+      if (column(i) < d) vector(at_smem)[column(i)] = at(p, bf16, first + column(i));
+  };
+  if (l.bias >= 0) keep(l.bias, a.bias, a.param_bf16, 0);
+  if (POST && l.post_bias >= 0) keep(l.post_bias, a.post_bias, a.param_bf16, 0);
   auto fetch = [&](int64_t row, int half) {
-    if (row < a.rows) {
-      const T *x = static_cast<const T*>(a.x), *res = static_cast<const T*>(a.residual);
-      stage_row<T, G>(staged + 2 * half * pitch, x + row * a.ld_x, x, d, tid);
-      stage_row<T, G>(staged + (2 * half + 1) * pitch, res + row * a.ld_res, res, d, tid);
+    if (row < to) {
+      const T *x = static_cast<const T*>(a.x), *res = static_cast<const T*>(a.residual), *gate = static_cast<const T*>(a.gate);
+      stage_row<T, G>(staged + l.arrays * half * pitch, x + row * a.ld_x, x, d, tid);
+      stage_row<T, G>(staged + (l.arrays * half + 1) * pitch, res + row * a.ld_res, res, d, tid);
+      if (l.gate_staged) stage_row<T, G>(staged + (l.arrays * half + 2) * pitch, gate + row * a.ld_gate, gate, d, tid);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto values = [&](int which, const void* base, int64_t at) {
-    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + at) & 15);
+  auto values = [&](int which, const void* base, int64_t first) {
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + first) & 15);
     return reinterpret_cast<const T*>(staged + which * pitch + off);
   };
-  fetch(row0, 0);
+  fetch(from, 0);
   int half = 0, slot = 0;
+  int64_t gate_to = from;  // the rows that the gate in shared memory is for end here
   auto sum = [&](float v) {
     slot ^= 1;
     return group_sum<G>(v, part, slot);
   };
-  for (int64_t row = row0; row < a.rows; row += step, half ^= 1) {
+  for (int64_t row = from; row < to; ++row, half ^= 1) {
     // this row is here, of every thread's copies, and the last one's place is free
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if constexpr (G == 32) __syncwarp();
     else __syncthreads();
-    fetch(row + step, half ^ 1);
-    const T *x = values(2 * half, a.x, row * a.ld_x), *res = values(2 * half + 1, a.residual, row * a.ld_res);
+    fetch(row + 1, half ^ 1);
+    if (l.gate >= 0 && row >= gate_to) {
+      const int64_t q = row / a.gate_rows;
+      gate_to = (q + 1) * a.gate_rows;
+      keep(l.gate, a.gate, a.gate_bf16, q * a.ld_gate);
+    }
+    const T *x = values(l.arrays * half, a.x, row * a.ld_x), *res = values(l.arrays * half + 1, a.residual, row * a.ld_res);
     float h[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) h[i] = column(i) < d ? ldf(x, column(i)) : 0.f;
-    float pm = 0.f, pr = 1.f;
-    if constexpr (POST) {
-      if (!a.rms) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s += h[i];
-        pm = sum(s) * inv_d;
-      }
+    // (0 beside the row; what is not there for any column is asked for once)
+    auto centred = [&](float mean) {
       float q = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float c = column(i) < d ? h[i] - pm : 0.f;
+        const float c = column(i) < d ? h[i] - mean : 0.f;
         q = fmaf(c, c, q);
       }
-      pr = rsqrtf(sum(q) * inv_d + a.eps);
+      return rsqrtf(sum(q) * inv_d + a.eps);
+    };
+    auto mean_of = [&] {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) s += h[i];
+      return sum(s) * inv_d;
+    };
+    float pm = 0.f, pr = 1.f;
+    if constexpr (POST) {
+      if (!a.rms) pm = mean_of();
+      pr = centred(pm);
+#pragma unroll
+      for (int i = 0; i < N; ++i) h[i] = (h[i] - pm) * pr * pw[i];  // (pw: 0 beside the row)
+      if (l.post_bias >= 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (column(i) < d) h[i] += vector(l.post_bias)[column(i)];
+    }
+    if (l.gate >= 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (column(i) < d) h[i] *= vector(l.gate)[column(i)];
+    } else if (l.gate_staged) {
+      const T* gate = values(l.arrays * half + 2, a.gate, row * a.ld_gate);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (column(i) < d) h[i] *= ldf(gate, column(i));
     }
     T* const to_h = static_cast<T*>(a.h_out) + row * a.ld_h;
-    const int64_t gate_at = a.gate ? row / a.gate_rows * a.ld_gate : 0;
-    float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = column(i);
-      if (c >= d) {
-        h[i] = 0.f;
-        continue;
+    for (int i = 0; i < N; ++i)
+      if (column(i) < d) {
+        h[i] = fmaf(a.scale, h[i], ldf(res, column(i)));
+        stf(to_h, column(i), h[i]);
       }
-      float p = h[i];
-      if constexpr (POST) {
-        p = (p - pm) * pr * pw[i];
-        if (a.post_bias) p += param(a.post_bias, a.param_bf16, c);
-      }
-      if (a.gate) p *= at(a.gate, a.gate_bf16, gate_at + c);
-      h[i] = fmaf(a.scale, p, ldf(res, c));
-      s += h[i];
-      stf(to_h, c, h[i]);
-    }
-    float m = 0.f;
-    if (!a.rms) m = sum(s) * inv_d;
-    float q = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float c = column(i) < d ? h[i] - m : 0.f;
-      q = fmaf(c, c, q);
-    }
-    const float r = rsqrtf(sum(q) * inv_d + a.eps);
+    const float m = a.rms ? 0.f : mean_of(), r = centred(m);
     T* const to_y = static_cast<T*>(a.y) + row * a.ld_y;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = column(i);
-      if (c < d) stf(to_y, c, fmaf((h[i] - m) * r, w[i], a.bias ? param(a.bias, a.param_bf16, c) : 0.f));
-    }
+    for (int i = 0; i < N; ++i) h[i] = (h[i] - m) * r * w[i];
+    if (l.bias >= 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (column(i) < d) h[i] += vector(l.bias)[column(i)];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (column(i) < d) stf(to_y, column(i), h[i]);
     if (tid == 0) {
       if (a.mean) a.mean[row] = m;
       if (a.rstd) a.rstd[row] = r;
@@ -499,26 +546,30 @@ cudaError_t fwd_n(const ResNormArgs& a, cudaStream_t s) {
 
 template <typename T, int N, int G, int R, bool POST>
 cudaError_t fwd_strided(const ResNormArgs& a, int sms, cudaStream_t s) {
-  constexpr int most = 4 * staged_pitch(N * G, sizeof(T)) * R;
-  static_assert(most <= kResNormRing, "shared memory");
   auto kernel = k_resnorm_fwd_strided<T, N, G, R, POST>;
   static std::atomic<uint64_t> configured{0};
   static std::atomic<int> per_sm{0};
   cudaError_t e;
-  const int n = resident_ctas(reinterpret_cast<const void*>(kernel), G * R, most, configured, per_sm, &e);
+  const int smem = strided_layout(a).bytes * R;
+  if (smem > kResNormRing) return cudaErrorNotSupported;
+  // (as many as the registers leave: the shared memory, which differs from call to call, is
+  // counted here)
+  const int n = resident_ctas(reinterpret_cast<const void*>(kernel), G * R, 0, kResNormRing, configured, per_sm, &e);
   if (n < 0) return e;
-  const int64_t all = static_cast<int64_t>(n) * sms, need = (a.rows + R - 1) / R;
-  const int smem = 4 * staged_pitch(static_cast<int>(a.d), sizeof(T)) * R;
-  kernel<<<static_cast<unsigned>(need < all ? need : all), G * R, smem, s>>>(a);
+  const int fit = 228 * 1024 / (smem + 3 * 1024), most = n < fit ? n : fit;
+  const int64_t all = static_cast<int64_t>(most < 1 ? 1 : most) * sms, need = (a.rows + R - 1) / R;
+  const int64_t grid = need < all ? need : all, walkers = grid * R < a.rows ? grid * R : a.rows;
+  kernel<<<static_cast<unsigned>(grid), G * R, smem, s>>>(a, static_cast<int>(walkers));
   return cudaGetLastError();
 }
 template <typename T, bool POST>
 cudaError_t fwd_any(const ResNormArgs& a, int sms, cudaStream_t s) {
   if (a.d <= 256) return fwd_strided<T, 8, 32, 8, POST>(a, sms, s);
-  if (a.d <= 1024) return fwd_strided<T, 8, 128, 1, POST>(a, sms, s);
-  if (a.d <= 2048) return fwd_strided<T, 8, 256, 1, POST>(a, sms, s);
-  if (a.d <= 4096) return fwd_strided<T, 8, 512, 1, POST>(a, sms, s);
-  if (a.d <= 8192) return fwd_strided<T, 8, 1024, 1, POST>(a, sms, s);
+  if (a.d <= 512) return fwd_strided<T, 16, 32, 8, POST>(a, sms, s);
+  if (a.d <= 1024) return fwd_strided<T, 16, 64, 1, POST>(a, sms, s);
+  if (a.d <= 2048) return fwd_strided<T, 16, 128, 1, POST>(a, sms, s);
+  if (a.d <= 4096) return fwd_strided<T, 16, 256, 1, POST>(a, sms, s);
+  if (a.d <= 8192) return fwd_strided<T, 16, 512, 1, POST>(a, sms, s);
   return cudaErrorNotSupported;
 }
 

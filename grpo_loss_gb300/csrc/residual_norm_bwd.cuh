@@ -23,15 +23,16 @@ __device__ __forceinline__ int64_t walker_of(int64_t rows, int64_t row, int64_t 
 enum : int { GATE_NONE, GATE_SHARED, GATE_ROWS };
 constexpr int kResNormRing = 224 * 1024;  // of shared memory, beside the sums
 
-// CTAs of a kernel that an SM holds, asked once a device; -1 where that fails.
-inline int resident_ctas(const void* kernel, int threads, int smem, std::atomic<uint64_t>& configured, std::atomic<int>& per_sm,
+// CTAs of a kernel that an SM holds with `smem` bytes each, asked once a device; -1 where that
+// fails. `most`: the largest shared memory that it is launched with.
+inline int resident_ctas(const void* kernel, int threads, int smem, int most, std::atomic<uint64_t>& configured, std::atomic<int>& per_sm,
                          cudaError_t* e) {
   int dev = 0;
   *e = cudaGetDevice(&dev);
   if (*e != cudaSuccess) return -1;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(configured.load() & bit)) {
-    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     int n = 0;
     if (*e == cudaSuccess) *e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
     if (*e != cudaSuccess) return -1;
@@ -53,14 +54,14 @@ template <typename T, int G>
 __device__ __forceinline__ void stage_row(unsigned char* to, const T* row, const T* matrix, int d, int tid) {
   constexpr int es = static_cast<int>(sizeof(T));
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15), bytes = off + d * es;
-  const char* from = reinterpret_cast<const char*>(row) - off;
-  for (int i = tid * 16; i < bytes; i += G * 16) {
-    if (i == 0 && from < reinterpret_cast<const char*>(matrix)) {  // the granule begins before the matrix
-      for (int e = 0; e < d && off + e * es < 16; ++e) reinterpret_cast<T*>(to + off)[e] = row[e];
-    } else {
-      copy_async_zero(to + i, from + i, min(16, bytes - i));
-    }
+  const char* const from = reinterpret_cast<const char*>(row) - off;
+  int i = tid * 16;
+  if (tid == 0 && from < reinterpret_cast<const char*>(matrix)) {  // the granule begins before the matrix
+    for (int e = 0; e < d && off + e * es < 16; ++e) reinterpret_cast<T*>(to + off)[e] = row[e];
+    i = G * 16;
   }
+#pragma unroll 2
+  for (; i < bytes; i += G * 16) copy_async_zero(to + i, from + i, min(16, bytes - i));
 }
 constexpr int staged_pitch(int d, int size) { return (d * size + 31) / 16 * 16; }
 
@@ -75,10 +76,10 @@ constexpr int staged_pitch(int d, int size) { return (d * size + 31) / 16 * 16; 
 // STRIDED: rows that do not come in whole pieces. A row is staged by the 16-byte granules it
 // lies in, and a thread's N columns are G apart, so that a warp's accesses are to
 // consecutive elements wherever the row begins; one more barrier a row lets the threads
-// read what others copied. (RMS norms are told by the arguments then.)
+// read what others copied.
 template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, bool STRIDED>
 __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walkers) {
-  static_assert(!STRIDED || (NV == 1 && (R == 1 || G == 32) && !RMS && N % 2 == 0), "");
+  static_assert(!STRIDED || (NV == 1 && (R == 1 || G == 32) && N % 2 == 0), "");
   constexpr int B = N * static_cast<int>(sizeof(T)), H = (N + 1) / 2;
   constexpr bool INNER = POST || GATE != GATE_NONE;
   constexpr int ARRAYS = 3 + INNER + (GATE == GATE_ROWS);  // dy, h, dh, x, gate
@@ -286,10 +287,10 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   auto stats_of = [&](int n) {
     Stats s = {0.f, 0.f, 0.f, 1.f};
     if (n < mine) {
-      if (!RMS && !(STRIDED && a.rms)) s.m = a.mean[from + n];
+      if (!RMS) s.m = a.mean[from + n];
       s.r = a.rstd[from + n];
       if (POST) {
-        if (!RMS && !(STRIDED && a.rms)) s.pm = a.post_mean[from + n];
+        if (!RMS) s.pm = a.post_mean[from + n];
         s.pr = a.post_rstd[from + n];
       }
     }
@@ -384,13 +385,13 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
     group_sums<G, SUMS>(sums, part, half);
     if (!live) continue;
     // r c2, r c1
-    const float c2 = s.r * sums[0] * inv_d, c1 = RMS || (STRIDED && a.rms) ? 0.f : s.r * sums[1] * inv_d;
+    const float c2 = s.r * sums[0] * inv_d, c1 = RMS ? 0.f : s.r * sums[1] * inv_d;
     float b1 = 0.f, b2 = 0.f;  // means of a g and of a g k
     if constexpr (POST) {
       b2 = fmaf(-c2, sums[3], sums[2]);
       if constexpr (!RMS) {
         b2 = fmaf(-c1, sums[7], b2) * inv_d;
-        if (!STRIDED || !a.rms) b1 = fmaf(-c1, sums[6], fmaf(-c2, sums[5], sums[4])) * inv_d;
+        b1 = fmaf(-c1, sums[6], fmaf(-c2, sums[5], sums[4])) * inv_d;
       } else {
         b2 *= inv_d;
       }
@@ -483,7 +484,7 @@ cudaError_t resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_
   static std::atomic<uint64_t> configured{0};
   static std::atomic<int> per_sm{0};
   cudaError_t e;
-  const int n = resident_ctas(reinterpret_cast<const void*>(kernel), G * R, smem, configured, per_sm, &e);
+  const int n = resident_ctas(reinterpret_cast<const void*>(kernel), G * R, smem, smem, configured, per_sm, &e);
   if (n < 0) return e;
   // four rows a walker at least, where that leaves the SMs at work: its partial sums are
   // written and read again
@@ -516,14 +517,14 @@ cudaError_t resnorm_bwd_n(const ResNormArgs& a, int sms, int* walkers, cudaStrea
 #undef RESNORM_CASE
   return cudaErrorNotSupported;  // longer rows: the caller has another kernel
 }
-template <typename T, bool POST, int GATE>
+template <typename T, bool RMS, bool POST, int GATE>
 cudaError_t resnorm_bwd_strided(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
-  if (a.d <= 256) return resnorm_bwd<T, 8, 1, 32, 8, false, POST, GATE, true>(a, sms, walkers, s);
-  if (a.d <= 1024) return resnorm_bwd<T, 8, 1, 128, 1, false, POST, GATE, true>(a, sms, walkers, s);
-  if (a.d <= 2048) return resnorm_bwd<T, 8, 1, 256, 1, false, POST, GATE, true>(a, sms, walkers, s);
-  if (a.d <= 4096) return resnorm_bwd<T, 8, 1, 512, 1, false, POST, GATE, true>(a, sms, walkers, s);
+  if (a.d <= 256) return resnorm_bwd<T, 8, 1, 32, 8, RMS, POST, GATE, true>(a, sms, walkers, s);
+  if (a.d <= 1024) return resnorm_bwd<T, 8, 1, 128, 1, RMS, POST, GATE, true>(a, sms, walkers, s);
+  if (a.d <= 2048) return resnorm_bwd<T, 8, 1, 256, 1, RMS, POST, GATE, true>(a, sms, walkers, s);
+  if (a.d <= 4096) return resnorm_bwd<T, 8, 1, 512, 1, RMS, POST, GATE, true>(a, sms, walkers, s);
   if constexpr (sizeof(T) == 2)
-    if (a.d <= 8192) return resnorm_bwd<T, 8, 1, 1024, 1, false, POST, GATE, true>(a, sms, walkers, s);
+    if (a.d <= 8192) return resnorm_bwd<T, 8, 1, 1024, 1, RMS, POST, GATE, true>(a, sms, walkers, s);
   return cudaErrorNotSupported;
 }
 
@@ -531,10 +532,15 @@ template <typename T, bool POST>
 cudaError_t resnorm_bwd_kind(const ResNormArgs& a, bool whole, int sms, int* walkers, cudaStream_t s) {
   constexpr int N = 16 / static_cast<int>(sizeof(T));
   const int gate = !a.gate ? GATE_NONE : a.gate_rows == 1 ? GATE_ROWS : GATE_SHARED;
-  if (!whole)
-    return gate == GATE_NONE     ? resnorm_bwd_strided<T, POST, GATE_NONE>(a, sms, walkers, s)
-           : gate == GATE_SHARED ? resnorm_bwd_strided<T, POST, GATE_SHARED>(a, sms, walkers, s)
-                                 : resnorm_bwd_strided<T, POST, GATE_ROWS>(a, sms, walkers, s);
+  if (!whole) {
+    if (a.rms)
+      return gate == GATE_NONE     ? resnorm_bwd_strided<T, true, POST, GATE_NONE>(a, sms, walkers, s)
+             : gate == GATE_SHARED ? resnorm_bwd_strided<T, true, POST, GATE_SHARED>(a, sms, walkers, s)
+                                   : resnorm_bwd_strided<T, true, POST, GATE_ROWS>(a, sms, walkers, s);
+    return gate == GATE_NONE     ? resnorm_bwd_strided<T, false, POST, GATE_NONE>(a, sms, walkers, s)
+           : gate == GATE_SHARED ? resnorm_bwd_strided<T, false, POST, GATE_SHARED>(a, sms, walkers, s)
+                                 : resnorm_bwd_strided<T, false, POST, GATE_ROWS>(a, sms, walkers, s);
+  }
   if (a.rms)
     return gate == GATE_NONE     ? resnorm_bwd_n<T, N, true, POST, GATE_NONE>(a, sms, walkers, s)
            : gate == GATE_SHARED ? resnorm_bwd_n<T, N, true, POST, GATE_SHARED>(a, sms, walkers, s)
