@@ -18,32 +18,12 @@ namespace grpo {
 
 namespace {
 
-constexpr int kLong = 512;
-
 __device__ __forceinline__ float at(const void* p, int bf16, int64_t i) {
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 __device__ __forceinline__ void put(void* p, int bf16, int64_t i, float v) {
   if (bf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
   else static_cast<float*>(p)[i] = v;
-}
-
-template <int M>
-__device__ void cta_sums(float (&v)[M]) {
-  __shared__ float part[M][kLong / 32];
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
-    if ((threadIdx.x & 31) == 0) part[m][threadIdx.x >> 5] = v[m];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-    v[m] = 0.f;
-    for (int w = 0; w < kLong / 32; ++w) v[m] += part[m][w];
-  }
-  __syncthreads();
 }
 
 __device__ float gate_of(const ResNormArgs& a, int64_t row, int i) {
@@ -318,51 +298,73 @@ __global__ void __launch_bounds__(G * R) k_resnorm_fwd_strided(ResNormArgs a, in
   }
 }
 
+// Rows too long for registers: h stands in shared memory, x is read again, mostly from L2;
+// kMany columns of a thread at a time, so that their loads are in flight together. (9000 x
+// 9999 bf16, RMS with a post norm, floor 108 us: forward 400 us, backward 1697: the loads of
+// one batch are waited for before the next.)
+constexpr int kLong = 512, kWide = 1024, kMany = 4;
+// body(u, i) of a thread's kMany columns i from i0 on, of a CTA of THREADS.
+template <int THREADS, typename F>
+__device__ __forceinline__ void columns(int d, int i0, F body) {
+#pragma unroll
+  for (int u = 0; u < kMany; ++u) {
+    const int i = i0 + u * THREADS;
+    if (i < d) body(u, i);
+  }
+}
+template <typename T>
 __global__ void __launch_bounds__(kLong) k_resnorm_fwd_long(ResNormArgs a) {
   extern __shared__ float h[];
+  __shared__ float part[2 * 128];
   const int d = static_cast<int>(a.d);
   const float inv_d = 1.f / d;
   const int64_t row = blockIdx.x;
+  const T *x = static_cast<const T*>(a.x) + row * a.ld_x, *res = static_cast<const T*>(a.residual) + row * a.ld_res;
+  int slot = 0;
+  auto sum = [&](float v) {
+    slot ^= 1;
+    return group_sum<kLong>(v, part, slot);
+  };
   float pm = 0.f, pr = 1.f;
   if (a.post_weight) {
-    float s[1] = {0.f};
+    float s = 0.f;
     if (!a.rms) {
-      for (int i = threadIdx.x; i < d; i += kLong) s[0] += at(a.x, a.bf16, row * a.ld_x + i);
-      cta_sums(s);
-      pm = s[0] * inv_d;
+#pragma unroll 4
+      for (int i = threadIdx.x; i < d; i += kLong) s += ldf(x, i);
+      pm = sum(s) * inv_d;
     }
-    s[0] = 0.f;
+    s = 0.f;
+#pragma unroll 4
     for (int i = threadIdx.x; i < d; i += kLong) {
-      const float c = at(a.x, a.bf16, row * a.ld_x + i) - pm;
-      s[0] = fmaf(c, c, s[0]);
+      const float c = ldf(x, i) - pm;
+      s = fmaf(c, c, s);
     }
-    cta_sums(s);
-    pr = rsqrtf(s[0] * inv_d + a.eps);
+    pr = rsqrtf(sum(s) * inv_d + a.eps);
   }
-  float s[1] = {0.f};
-  for (int i = threadIdx.x; i < d; i += kLong) {
-    float p = at(a.x, a.bf16, row * a.ld_x + i);
-    if (a.post_weight) {
-      p = (p - pm) * pr * at(a.post_weight, a.param_bf16, i);
-      if (a.post_bias) p += at(a.post_bias, a.param_bf16, i);
-    }
-    h[i] = fmaf(gate_of(a, row, i), p, at(a.residual, a.bf16, row * a.ld_res + i));
-    put(a.h_out, a.bf16, row * a.ld_h + i, h[i]);
-    s[0] += h[i];
+  T* const to_h = static_cast<T*>(a.h_out) + row * a.ld_h;
+  float s = 0.f;
+  for (int i0 = threadIdx.x; i0 < d; i0 += kLong * kMany) {
+    float p[kMany], e[kMany], w[kMany], b[kMany], f[kMany];
+    columns<kLong>(d, i0, [&](int u, int i) {
+      p[u] = ldf(x, i), e[u] = ldf(res, i), f[u] = gate_of(a, row, i);
+      w[u] = a.post_weight ? param(a.post_weight, a.param_bf16, i) : 1.f;
+      b[u] = a.post_bias ? param(a.post_bias, a.param_bf16, i) : 0.f;
+    });
+    columns<kLong>(d, i0, [&](int u, int i) {
+      h[i] = fmaf(f[u], (p[u] - pm) * pr * w[u] + b[u], e[u]);
+      s += h[i];
+      stf(to_h, i, h[i]);
+    });
   }
-  float m = 0.f;
-  if (!a.rms) {
-    cta_sums(s);
-    m = s[0] * inv_d;
-  }
-  s[0] = 0.f;
-  for (int i = threadIdx.x; i < d; i += kLong) s[0] = fmaf(h[i] - m, h[i] - m, s[0]);
-  cta_sums(s);
-  const float r = rsqrtf(s[0] * inv_d + a.eps);
-  for (int i = threadIdx.x; i < d; i += kLong) {
-    float v = (h[i] - m) * r * at(a.weight, a.param_bf16, i);
-    if (a.bias) v += at(a.bias, a.param_bf16, i);
-    put(a.y, a.bf16, row * a.ld_y + i, v);
+  const float m = a.rms ? 0.f : sum(s) * inv_d;
+  s = 0.f;
+  for (int i = threadIdx.x; i < d; i += kLong) s = fmaf(h[i] - m, h[i] - m, s);
+  const float r = rsqrtf(sum(s) * inv_d + a.eps);
+  T* const to_y = static_cast<T*>(a.y) + row * a.ld_y;
+  for (int i0 = threadIdx.x; i0 < d; i0 += kLong * kMany) {
+    float w[kMany], b[kMany];
+    columns<kLong>(d, i0, [&](int u, int i) { w[u] = param(a.weight, a.param_bf16, i), b[u] = a.bias ? param(a.bias, a.param_bf16, i) : 0.f; });
+    columns<kLong>(d, i0, [&](int u, int i) { stf(to_y, i, (h[i] - m) * r * w[u] + b[u]); });
   }
   if (threadIdx.x == 0) {
     if (a.mean) a.mean[row] = m;
@@ -372,78 +374,127 @@ __global__ void __launch_bounds__(kLong) k_resnorm_fwd_long(ResNormArgs a) {
   }
 }
 
-__global__ void __launch_bounds__(kLong) k_resnorm_bwd_long(ResNormArgs a, int walkers) {
+// The same backward. `fit` column sums stand beside g in shared memory, in the order of their first use; others are added
+// up in their partial rows.
+template <typename T>
+__global__ void __launch_bounds__(kWide) k_resnorm_bwd_long(ResNormArgs a, int walkers, int fit) {
   extern __shared__ float g[];
+  __shared__ float red[2 * 256];
   const int d = static_cast<int>(a.d);
   const float inv_d = 1.f / d;
   const int64_t from = first_row(a.rows, blockIdx.x, walkers), to = first_row(a.rows, blockIdx.x + 1, walkers);
   auto part = [&](int which) { return a.partial + (static_cast<int64_t>(which) * walkers + blockIdx.x) * d; };
-  float* const pw = a.dweight ? part(a.at_dw) : nullptr;
-  float* const pb = a.dbias ? part(a.at_db) : nullptr;
-  float* const ppw = a.dpost_weight ? part(a.at_dpw) : nullptr;
-  float* const ppb = a.dpost_bias ? part(a.at_dpb) : nullptr;
+  int used = 0;
+  auto place = [&](bool there, float* global) {
+    if (!there) return static_cast<float*>(nullptr);
+    if (used == fit) return global;
+    return g + static_cast<int64_t>(++used) * d;
+  };
+  float* const pw = place(a.dweight, part(a.at_dw));
+  float* const ppw = place(a.dpost_weight, part(a.at_dpw));
+  float* const pgate = place(a.dgate && a.gate_rows > 1, nullptr);  // null: where it is written in the end
+  float* const pb = place(a.dbias, part(a.at_db));
+  float* const ppb = place(a.dpost_bias, part(a.at_dpb));
+  auto row_of = [](const void* p, int64_t ld, int64_t row) { return static_cast<const T*>(p) + row * ld; };
+  int slot = 0;
   for (int64_t row = from; row < to; ++row) {
     const bool first = row == from;
     const float m = a.rms ? 0.f : a.mean[row], r = a.rstd[row];
+    const T *dy = row_of(a.dy, a.ld_dy, row), *h = row_of(a.h, a.ld_h, row), *dh = a.dh ? row_of(a.dh, a.ld_dh, row) : nullptr;
+    const T* x = a.x ? row_of(a.x, a.ld_x, row) : nullptr;
     float s[2] = {0.f, 0.f};
-    for (int i = threadIdx.x; i < d; i += kLong) {
-      const float v = at(a.dy, a.bf16, row * a.ld_dy + i), k = (at(a.h, a.bf16, row * a.ld_h + i) - m) * r;
-      const float vw = v * at(a.weight, a.param_bf16, i);
-      s[0] += vw;
-      s[1] = fmaf(vw, k, s[1]);
-      if (pw) pw[i] = fmaf(v, k, first ? 0.f : pw[i]);
-      if (pb) pb[i] = v + (first ? 0.f : pb[i]);
+    for (int i0 = threadIdx.x; i0 < d; i0 += kWide * kMany) {
+      float v[kMany], k[kMany], w[kMany];
+      columns<kWide>(d, i0, [&](int u, int i) { v[u] = ldf(dy, i), k[u] = ldf(h, i), w[u] = param(a.weight, a.param_bf16, i); });
+      columns<kWide>(d, i0, [&](int u, int i) {
+        const float hat = (k[u] - m) * r, vw = v[u] * w[u];
+        s[0] += vw;
+        s[1] = fmaf(vw, hat, s[1]);
+        if (pw) pw[i] = fmaf(v[u], hat, first ? 0.f : pw[i]);
+        if (pb) pb[i] = v[u] + (first ? 0.f : pb[i]);
+      });
     }
-    cta_sums(s);
+    group_sums<kWide, 2>(s, red, slot);
+    slot ^= 1;
     const float c1 = a.rms ? 0.f : s[0] * inv_d, c2 = s[1] * inv_d;
-    for (int i = threadIdx.x; i < d; i += kLong) {
-      const float v = at(a.dy, a.bf16, row * a.ld_dy + i), k = (at(a.h, a.bf16, row * a.ld_h + i) - m) * r;
-      const float dz = r * (v * at(a.weight, a.param_bf16, i) - c1 - k * c2);
-      g[i] = a.dh ? dz + at(a.dh, a.bf16, row * a.ld_dh + i) : dz;
-      put(a.dres, a.bf16, row * a.ld_dres + i, g[i]);
+    T* const dres = static_cast<T*>(a.dres) + row * a.ld_dres;
+    for (int i0 = threadIdx.x; i0 < d; i0 += kWide * kMany) {
+      float v[kMany], k[kMany], w[kMany], e[kMany];
+      columns<kWide>(d, i0, [&](int u, int i) {
+        v[u] = ldf(dy, i), k[u] = ldf(h, i), w[u] = param(a.weight, a.param_bf16, i);
+        e[u] = dh ? ldf(dh, i) : 0.f;
+      });
+      columns<kWide>(d, i0, [&](int u, int i) {
+        g[i] = fmaf(r, v[u] * w[u] - c1 - (k[u] - m) * r * c2, e[u]);
+        stf(dres, i, g[i]);
+      });
     }
     if (!a.dx && !a.dgate && !a.dpost_weight && !a.dpost_bias) continue;
     const float pm = a.post_weight && !a.rms ? a.post_mean[row] : 0.f, pr = a.post_weight ? a.post_rstd[row] : 1.f;
     // the rows of a gate that lie in this walker: its first and its last may be shared
     const int64_t q = a.gate ? row / a.gate_rows : 0, q0 = q * a.gate_rows, q1 = q0 + a.gate_rows;
-    float* dgate = nullptr;
-    if (a.dgate && a.gate_rows > 1)
+    float *dgate = nullptr, *sum_gate = nullptr;
+    if (a.dgate && a.gate_rows > 1) {
       dgate = q0 >= from && q1 <= to ? static_cast<float*>(a.dgate) + q * d : part(q0 <= from ? a.at_head : a.at_tail);
-    const bool first_of_gate = first || row == q0;
+      sum_gate = pgate ? pgate : dgate;
+    }
+    const bool first_of_gate = first || row == q0, last_of_gate = row + 1 == to || row + 1 == q1;
     s[0] = s[1] = 0.f;
-    for (int i = threadIdx.x; i < d; i += kLong) {
-      const float x = a.x ? at(a.x, a.bf16, row * a.ld_x + i) : 0.f;
-      const float k = (x - pm) * pr, w = a.post_weight ? at(a.post_weight, a.param_bf16, i) : 1.f;
-      if (a.dgate) {
-        const float p = a.post_bias ? fmaf(k, w, at(a.post_bias, a.param_bf16, i)) : k * w;
-        const float v = a.scale * g[i] * p;
-        if (a.gate_rows > 1) dgate[i] = v + (first_of_gate ? 0.f : dgate[i]);
-        else put(a.dgate, a.gate_bf16, row * a.ld_dgate + i, v);
-      }
-      const float qv = g[i] * gate_of(a, row, i);
-      g[i] = qv;
-      if (a.post_weight) {
-        s[0] = fmaf(qv, w, s[0]);
-        s[1] = fmaf(qv * w, k, s[1]);
-        if (ppw) ppw[i] = fmaf(qv, k, first ? 0.f : ppw[i]);
-        if (ppb) ppb[i] = qv + (first ? 0.f : ppb[i]);
-      }
+    for (int i0 = threadIdx.x; i0 < d; i0 += kWide * kMany) {
+      float xs[kMany], w[kMany], gt[kMany], pb_[kMany];
+      columns<kWide>(d, i0, [&](int u, int i) {
+        xs[u] = x ? ldf(x, i) : 0.f;
+        w[u] = a.post_weight ? param(a.post_weight, a.param_bf16, i) : 1.f;
+        gt[u] = gate_of(a, row, i);
+        pb_[u] = a.post_bias && a.dgate ? param(a.post_bias, a.param_bf16, i) : 0.f;
+      });
+      columns<kWide>(d, i0, [&](int u, int i) {
+        const float k = (xs[u] - pm) * pr;
+        if (a.dgate) {
+          const float v = a.scale * g[i] * fmaf(k, w[u], pb_[u]);
+          if (sum_gate) {
+            const float sum = v + (first_of_gate ? 0.f : sum_gate[i]);
+            sum_gate[i] = sum;
+            if (pgate && last_of_gate) dgate[i] = sum;
+          } else {
+            put(a.dgate, a.gate_bf16, row * a.ld_dgate + i, v);
+          }
+        }
+        const float qv = g[i] * gt[u];
+        g[i] = qv;
+        if (a.post_weight) {
+          s[0] = fmaf(qv, w[u], s[0]);
+          s[1] = fmaf(qv * w[u], k, s[1]);
+          if (ppw) ppw[i] = fmaf(qv, k, first ? 0.f : ppw[i]);
+          if (ppb) ppb[i] = qv + (first ? 0.f : ppb[i]);
+        }
+      });
     }
     if (a.post_weight) {
-      cta_sums(s);
+      group_sums<kWide, 2>(s, red, slot);
+      slot ^= 1;
       s[0] = a.rms ? 0.f : s[0] * inv_d;
       s[1] *= inv_d;
     }
-    if (a.dx)
-      for (int i = threadIdx.x; i < d; i += kLong) {
-        float v = g[i];
-        if (a.post_weight) {
-          const float k = (at(a.x, a.bf16, row * a.ld_x + i) - pm) * pr;
-          v = pr * (v * at(a.post_weight, a.param_bf16, i) - s[0] - k * s[1]);
-        }
-        put(a.dx, a.bf16, row * a.ld_dx + i, v);
-      }
+    if (!a.dx) continue;
+    T* const dx = static_cast<T*>(a.dx) + row * a.ld_dx;
+    for (int i0 = threadIdx.x; i0 < d; i0 += kWide * kMany) {
+      float xs[kMany], w[kMany];
+      if (a.post_weight) columns<kWide>(d, i0, [&](int u, int i) { xs[u] = ldf(x, i), w[u] = param(a.post_weight, a.param_bf16, i); });
+      columns<kWide>(d, i0, [&](int u, int i) {
+        stf(dx, i, a.post_weight ? pr * (g[i] * w[u] - s[0] - (xs[u] - pm) * pr * s[1]) : g[i]);
+      });
+    }
   }
+  // (each thread's own columns)
+  auto leave = [&](const float* sums, bool there, int which) {
+    if (!there || sums == part(which)) return;
+    for (int i = threadIdx.x; i < d; i += kWide) part(which)[i] = sums[i];
+  };
+  leave(pw, a.dweight, a.at_dw);
+  leave(ppw, a.dpost_weight, a.at_dpw);
+  leave(pb, a.dbias, a.at_db);
+  leave(ppb, a.dpost_bias, a.at_dpb);
 }
 
 // Joins the walkers' partial sums of a column: one after the other in a fixed order.
@@ -591,10 +642,6 @@ __global__ void __launch_bounds__(256) k_resnorm_join_gates(ResNormArgs a, int w
 }
 constexpr int64_t kFewGates = 32;
 
-cudaError_t allow_row(const void* kernel, int64_t d) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(d * 4));
-}
-
 }  // namespace
 
 int resnorm_walkers(const ResNormArgs& a, int sms) {
@@ -611,9 +658,10 @@ cudaError_t launch_resnorm_fwd(const ResNormArgs& a, int sms, cudaStream_t s) {
   else if (a.post_weight) e = a.bf16 ? fwd_any<__nv_bfloat16, true>(a, sms, s) : fwd_any<float, true>(a, sms, s);
   else e = a.bf16 ? fwd_any<__nv_bfloat16, false>(a, sms, s) : fwd_any<float, false>(a, sms, s);
   if (e != cudaErrorNotSupported) return e;
-  e = allow_row(reinterpret_cast<const void*>(k_resnorm_fwd_long), kMaxResNormDim);
+  auto kernel = a.bf16 ? k_resnorm_fwd_long<__nv_bfloat16> : k_resnorm_fwd_long<float>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxResNormDim * 4));
   if (e != cudaSuccess) return e;
-  k_resnorm_fwd_long<<<static_cast<unsigned>(a.rows), kLong, a.d * 4, s>>>(a);
+  kernel<<<static_cast<unsigned>(a.rows), kLong, a.d * 4, s>>>(a);
   return cudaGetLastError();
 }
 cudaError_t launch_resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
@@ -624,11 +672,17 @@ cudaError_t launch_resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cuda
     else e = a.post_weight ? resnorm_bwd_f32_post(a, w, sms, walkers, s) : resnorm_bwd_f32(a, w, sms, walkers, s);
   }
   if (e != cudaErrorNotSupported) return e;
-  e = allow_row(reinterpret_cast<const void*>(k_resnorm_bwd_long), kMaxResNormDim);
+  // every sum that fits beside the row, one CTA an SM then
+  const int sums = (a.dweight != nullptr) + (a.dbias != nullptr) + (a.dpost_weight != nullptr) + (a.dpost_bias != nullptr) +
+                   (a.dgate && a.gate_rows > 1);
+  const int room = static_cast<int>(kResNormRing / (a.d * 4)) - 1, fit = sums < room ? sums : room;
+  const int smem = static_cast<int>(a.d * 4) * (1 + fit);
+  auto kernel = a.bf16 ? k_resnorm_bwd_long<__nv_bfloat16> : k_resnorm_bwd_long<float>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kResNormRing);
   if (e != cudaSuccess) return e;
-  const int64_t most = 2ll * sms;
+  const int64_t most = sms;
   *walkers = static_cast<int>(a.rows < most ? a.rows : most);
-  k_resnorm_bwd_long<<<*walkers, kLong, a.d * 4, s>>>(a, *walkers);
+  kernel<<<*walkers, kWide, smem, s>>>(a, *walkers, fit);
   return cudaGetLastError();
 }
 cudaError_t launch_resnorm_join(const ResNormArgs& a, int walkers, cudaStream_t s) {
