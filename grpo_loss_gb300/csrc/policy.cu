@@ -8,6 +8,8 @@
 // Bound by memory and by the instructions beside it for many tokens (21 bytes each).
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "f32x2.cuh"
 #include "internal.h"
 
@@ -24,8 +26,10 @@ constexpr int kUnit = 32 * kTokens;      // tokens that a warp takes at a time
 constexpr int kChunk = kThreads * kTokens;  // of short sequences, that a CTA takes at a time
 constexpr int kShort = 128;              // sequences below this are taken several a warp
 constexpr int kLossCtas = 2;             // of an SM, at a time
-constexpr int kCluster = 8;
-constexpr int64_t kSmall = 16 * kChunk;  // tokens that one cluster takes
+constexpr int kCluster = 16;
+// Tokens that one cluster takes: at 8 x 20480 its 16 SMs take as long as two launches over
+// all, which cost the host one more and a workspace.
+constexpr int64_t kSmall = 96 * kChunk;
 
 // ---------------------------------------------------------------- numbers
 // The rounding error of s = a - b.
@@ -956,8 +960,22 @@ bool by_quads(const PolicyArgs& a) {
 
 template <bool VEC, int W, bool REF, bool TADV>
 cudaError_t loss_launch(const PolicyArgs& a, cudaStream_t s) {
-  if (small(a)) k_policy_small<VEC, W, REF, TADV><<<kCluster, kThreads, 0, s>>>(a);
-  else k_policy_loss<VEC, W, REF, TADV><<<a.loss_ctas, kThreads, 0, s>>>(a);
+  if (small(a)) {
+    auto kernel = k_policy_small<VEC, W, REF, TADV>;
+    // clusters of more than 8 are asked for once a device
+    static std::atomic<uint64_t> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (e == cudaSuccess && !(configured.load() & bit)) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e == cudaSuccess) configured.fetch_or(bit);
+    }
+    if (e != cudaSuccess) return e;
+    kernel<<<kCluster, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  k_policy_loss<VEC, W, REF, TADV><<<a.loss_ctas, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 template <bool VEC>

@@ -73,7 +73,7 @@ def test_many_sequences(B, T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("B,T", [(1, 32768), (1, 32769), (1024, 32), (1025, 31), (33, 1000), (130, 255), (3, 10001)])
+@pytest.mark.parametrize("B,T", [(1, 32768), (1, 32769), (1024, 32), (1025, 31), (33, 1000), (130, 255), (3, 10001), (8, 24576), (8, 24577), (500, 393)])
 def test_on_either_side_of_one_launch(B, T):
     """The most tokens and sequences that one launch takes, and more, with rows on and off
     16-byte boundaries."""
