@@ -113,6 +113,30 @@ enum KernelKind : int {
   K_NUM_KINDS
 };
 
+// Launches a kernel that takes what the kernel before it on the stream leaves, so that its
+// CTAs may be set up while that one's last are at work: it calls after_previous() before it
+// reads anything of it, and the one before calls let_next() as soon as a CTA of it runs.
+// (The policy loss' two launches: a call 39.3 -> 37.6 us. Waiting CTAs take room from those
+// at work: the norms' joins gained 1 %, the clipping of small tensors lost 3 us of 13.)
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t config = {};
+  config.gridDim = grid;
+  config.blockDim = dim3(static_cast<unsigned>(threads));
+  config.dynamicSmemBytes = smem;
+  config.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, args...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
+
 // ------------------------------------------------------------- gemm_tc.cu
 size_t gemm_smem_bytes();
 cudaError_t gemm_configure();  // sets the dynamic shared memory limit once

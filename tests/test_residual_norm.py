@@ -102,6 +102,16 @@ def test_sizes_and_types(rows, d, kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,d", [(50, 512), (33, 257), (9, 5000), (2, 32768)])
+def test_a_gate_of_another_type_than_the_rows(rows, d):
+    for dtype, gdtype, gate in ((BF16, F32, rows), (F32, BF16, rows), (BF16, F32, 1), (F32, BF16, 1)):
+        s = inputs(rows, d, dtype, F32)
+        s["gate"] = torch.randn(gate, d, device="cuda", generator=torch.Generator("cuda").manual_seed(d)).to(gdtype)
+        _, back = check(s, scale=0.7)
+        assert back["dgate"].dtype == (gdtype if gate == rows else F32)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,per", [(2, 1), (303, 101), (304, 2), (608, 76), (609, 3), (2500, 100), (2400, 7 * 0 + 800), (5000, 1250)])
 def test_gates_over_row_counts(rows, per):
     """Gates whose rows are shared by a few rows and by many, and end anywhere."""
