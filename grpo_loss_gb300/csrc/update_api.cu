@@ -118,6 +118,8 @@ size_t grad_bytes(int sms, int launches) { return sizeof(double) * grad_parts(sm
 // Launches whose partial norms the workspace holds; more tensors than these have are
 // taken in turns, each joined to what the former left.
 constexpr int kGradLaunches = 16;
+// Of a list, so that its chunks' numbers are 32 bits.
+constexpr int64_t kMaxGradElements = static_cast<int64_t>(1) << 40;
 
 grpo_status clip_grads(const grpo_grad_tensor* tensors, int32_t n_tensors, int32_t norm_type,
                        double max_norm, double eps, float* norm, float* factor, bool scale,
@@ -127,14 +129,16 @@ grpo_status clip_grads(const grpo_grad_tensor* tensors, int32_t n_tensors, int32
   if (norm_type != 2 && norm_type != 0) return GRPO_ERR_INVALID_ARG;
   if (!(max_norm >= 0.0) || !(eps >= 0.0) || !isfinite(eps)) return GRPO_ERR_INVALID_ARG;
   if (!aligned_to(norm, 4) || !aligned_to(factor, 4)) return GRPO_ERR_UNSUPPORTED;
+  int64_t all = 0;
   for (int32_t i = 0; i < n_tensors; ++i) {
     const grpo_grad_tensor& t = tensors[i];
     if (t.n < 0 || !is_f32_or_bf16(t.dtype)) return GRPO_ERR_INVALID_ARG;
     if (t.n == 0) continue;
     if (!t.grad || (scale && !t.out)) return GRPO_ERR_INVALID_ARG;
     if (!aligned_to(t.grad, elem_size(t.dtype)) || (scale && !aligned_to(t.out, elem_size(t.dtype))) ||
-        t.n > static_cast<int64_t>(1) << 40)
+        t.n > kMaxGradElements - all)
       return GRPO_ERR_UNSUPPORTED;
+    all += t.n;
   }
   int sms = 0;
   const grpo_status st = device_info(&sms);

@@ -638,7 +638,7 @@ grpo_status grpo_residual_norm_bwd(const grpo_residual_norm_problem *problem, co
  * it may be NULL for 1 to 8 tensors, none of them empty, of 65536 elements in all at most.
  * INVALID_ARG for null pointers, n < 0, a max_norm or eps that is negative or NaN, an eps
  * that is infinite, another norm_type or dtype; UNSUPPORTED for pointers off their element's
- * alignment.
+ * alignment, and for more than 2^40 elements in all.
  */
 typedef struct grpo_grad_tensor {
   int64_t n;

@@ -274,6 +274,15 @@ def test_refuses_bad_calls_on_the_host(lib):
         table[0].out = 512
 
 
+def test_refuses_more_elements_than_their_chunks_can_be_counted(lib):
+    table = (L.GradTensor * 64)()
+    for t in table:
+        t.n, t.grad, t.out, t.dtype = (1 << 34) + 1, 256, 256, L.GRPO_BF16
+    at = ctypes.c_void_p(256)
+    for fn in (lib.grpo_grad_norm, lib.grpo_clip_grad_norm):
+        assert fn(ctypes.addressof(table), 64, 2, 1.0, 0.0, at, at, at, 1 << 40, None) == 2
+
+
 @pytest.mark.parametrize("call", ["grad_norm", "clip_grad_norm"])
 def test_refuses_wrong_tensors_on_the_host(monkeypatch, call):
     import grpo_loss_gb300 as G
