@@ -103,7 +103,7 @@ __device__ __forceinline__ void load_params(const void* p, int bf16, int i, floa
   }
 }
 
-__device__ __forceinline__ float param(const void* p, int bf16, int i) {
+__device__ __forceinline__ float param(const void* p, int bf16, int64_t i) {
   return bf16 ? ldf(static_cast<const __nv_bfloat16*>(p), i) : ldf(static_cast<const float*>(p), i);
 }
 

@@ -18,16 +18,13 @@ namespace grpo {
 
 namespace {
 
-__device__ __forceinline__ float at(const void* p, int bf16, int64_t i) {
-  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
-}
 __device__ __forceinline__ void put(void* p, int bf16, int64_t i, float v) {
   if (bf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
   else static_cast<float*>(p)[i] = v;
 }
 
 __device__ float gate_of(const ResNormArgs& a, int64_t row, int i) {
-  return a.gate ? a.scale * at(a.gate, a.gate_bf16, row / a.gate_rows * a.ld_gate + i) : a.scale;
+  return a.gate ? a.scale * param(a.gate, a.gate_bf16, row / a.gate_rows * a.ld_gate + i) : a.scale;
 }
 
 // A group of G threads takes a row, R rows a CTA; each thread holds NV pieces of N values
@@ -193,9 +190,9 @@ __global__ void __launch_bounds__(G * R) k_resnorm_fwd_strided(ResNormArgs a, in
     if (POST) pw[i] = column(i) < d ? param(a.post_weight, a.param_bf16, column(i)) : 0.f;
   }
   auto vector = [&](int at) { return reinterpret_cast<float*>(staged + at); };
-  auto keep = [&](int at_smem, const void* p, int bf16, int64_t first) {
+  auto keep = [&](int place, const void* p, int bf16, int64_t first) {
     for (int i = 0; i < N; ++i)
-      if (column(i) < d) vector(at_smem)[column(i)] = at(p, bf16, first + column(i));
+      if (column(i) < d) vector(place)[column(i)] = param(p, bf16, first + column(i));
   };
   if (l.bias >= 0) keep(l.bias, a.bias, a.param_bf16, 0);
   if (POST && l.post_bias >= 0) keep(l.post_bias, a.post_bias, a.param_bf16, 0);
@@ -565,7 +562,7 @@ cudaError_t fwd(const ResNormArgs& a, cudaStream_t s) {
 }
 template <typename T, int N>
 cudaError_t fwd_n(const ResNormArgs& a, cudaStream_t s) {
-  const int64_t pieces = (a.d + N - 1) / N;
+  const int64_t pieces = a.d / N;
   // Few threads with several pieces each, as far as their registers leave four rows an SM: the
   // fewer warps join their sums, the better (163840 x 4096 bf16, RMS with a post norm: 256
   // threads with two pieces 867 us, 128 with four 755, 64 with eight 796).

@@ -79,8 +79,9 @@ constexpr int staged_pitch(int d, int size) { return (d * size + 31) / 16 * 16; 
 // read what others copied.
 template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, bool STRIDED>
 __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walkers) {
-  static_assert(!STRIDED || (NV == 1 && (R == 1 || G == 32) && N % 2 == 0), "");
-  constexpr int B = N * static_cast<int>(sizeof(T)), H = (N + 1) / 2;
+  static_assert(!STRIDED || (NV == 1 && (R == 1 || G == 32)), "");
+  constexpr int B = N * static_cast<int>(sizeof(T)), H = N / 2;
+  static_assert(STRIDED || B == 16, "");
   constexpr bool INNER = POST || GATE != GATE_NONE;
   constexpr int ARRAYS = 3 + INNER + (GATE == GATE_ROWS);  // dy, h, dh, x, gate
   constexpr int SUMS = POST ? (RMS ? 4 : 8) : 2;
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   auto inside = [&](int i) { return !STRIDED || column(0, i) < d; };
   // N parameters from element `at` of p on
   auto load_pairs = [&](const void* p, int bf16, int64_t at, int k, uint64_t (&v)[H]) {
-    float u[2 * H] = {};
+    float u[N] = {};
     if constexpr (STRIDED) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
@@ -174,10 +175,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
         } else {
 #pragma unroll
           for (int k = 0; k < NV; ++k)
-            if (column(k) < d) {
-              if constexpr (B >= 4) copy_async<B>(&slot_of(half, which, k), q + column(k));
-              else slot_of(half, which, k) = load_piece<T, N>(q + column(k));
-            }
+            if (column(k) < d) copy_async<B>(&slot_of(half, which, k), q + column(k));
         }
       };
       copy(0, a.dy, a.ld_dy);
@@ -207,7 +205,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
     if constexpr (STRIDED)
       return pair_of(inside(2 * e) ? ldf(u.p, column(0, 2 * e)) : 0.f, inside(2 * e + 1) ? ldf(u.p, column(0, 2 * e + 1)) : 0.f);
     else
-      return pair_of(u.v.get(2 * e), 2 * e + 1 < N ? u.v.get(2 * e + 1) : 0.f);
+      return pair_of(u.v.get(2 * e), u.v.get(2 * e + 1));
   };
   auto store = [&](T* to, int k, const float* o) {
     if constexpr (STRIDED) {
@@ -225,7 +223,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
     for (int e = 0; e < H; ++e) {
       const float2 p = of_pair(v[e]);
       if (inside(2 * e)) to[column(k, 2 * e)] = p.x;
-      if (2 * e + 1 < N && inside(2 * e + 1)) to[column(k, 2 * e + 1)] = p.y;
+      if (inside(2 * e + 1)) to[column(k, 2 * e + 1)] = p.y;
     }
   };
   auto part_of = [&](int which) { return a.partial + (static_cast<int64_t>(which) * walkers + walker) * d; };
@@ -265,7 +263,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
             for (int e = 0; e < H; ++e) {
               const uint64_t before = !flushed ? zero
                                                : pair_of(inside(2 * e) ? p[column(k, 2 * e)] : 0.f,
-                                                         2 * e + 1 < N && inside(2 * e + 1) ? p[column(k, 2 * e + 1)] : 0.f);
+                                                         inside(2 * e + 1) ? p[column(k, 2 * e + 1)] : 0.f);
               v[e] = fma2(g[e], s[e], before);
             }
             store_sums(p, k, v);
@@ -407,7 +405,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
         if (a.dh) vd = values(half, 2, k, a.dh, a.ld_dh, row);
         if constexpr (INNER) vx = values(half, 3, k, a.x, a.ld_x, row);
         if constexpr (GATE == GATE_ROWS) vg = values(half, 4, k, a.gate, a.ld_gate, row);
-        float res[2 * H], dx[2 * H], dg[2 * H];
+        float res[N], dx[N], dg[N];
         uint64_t e0[H];
         if constexpr (POST && !RMS) load_sums(1, k, e0);
         uint64_t pb[H];
@@ -502,7 +500,7 @@ cudaError_t resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_
 // A row is given to few threads with several pieces each (see the norm's backward).
 template <typename T, int N, bool RMS, bool POST, int GATE>
 cudaError_t resnorm_bwd_n(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
-  const int64_t pieces = (a.d + N - 1) / N;
+  const int64_t pieces = a.d / N;
 #define RESNORM_CASE(most, NV, G, R) \
   if (pieces <= most) return resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE>(a, sms, walkers, s);
   RESNORM_CASE(32, 1, 32, 8)
