@@ -662,20 +662,18 @@ cudaError_t launch_resnorm_fwd(const ResNormArgs& a, int sms, cudaStream_t s) {
   return cudaGetLastError();
 }
 cudaError_t launch_resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
-  cudaError_t e = cudaErrorNotSupported;
   if (!(a.gate && a.gate_rows == 1 && a.gate_bf16 != a.bf16)) {
     const bool w = whole(a, false);
-    if (a.bf16) e = a.post_weight ? resnorm_bwd_bf16_post(a, w, sms, walkers, s) : resnorm_bwd_bf16(a, w, sms, walkers, s);
-    else e = a.post_weight ? resnorm_bwd_f32_post(a, w, sms, walkers, s) : resnorm_bwd_f32(a, w, sms, walkers, s);
+    if (a.bf16) return a.post_weight ? resnorm_bwd_bf16_post(a, w, sms, walkers, s) : resnorm_bwd_bf16(a, w, sms, walkers, s);
+    return a.post_weight ? resnorm_bwd_f32_post(a, w, sms, walkers, s) : resnorm_bwd_f32(a, w, sms, walkers, s);
   }
-  if (e != cudaErrorNotSupported) return e;
   // every sum that fits beside the row, one CTA an SM then
   const int sums = (a.dweight != nullptr) + (a.dbias != nullptr) + (a.dpost_weight != nullptr) + (a.dpost_bias != nullptr) +
                    (a.dgate && a.gate_rows > 1);
   const int room = static_cast<int>(kResNormRing / (a.d * 4)) - 1, fit = sums < room ? sums : room;
   const int smem = static_cast<int>(a.d * 4) * (1 + fit);
   auto kernel = a.bf16 ? k_resnorm_bwd_long<__nv_bfloat16> : k_resnorm_bwd_long<float>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kResNormRing);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kResNormRing);
   if (e != cudaSuccess) return e;
   const int64_t most = sms;
   *walkers = static_cast<int>(a.rows < most ? a.rows : most);

@@ -8,6 +8,8 @@
 // so that all sums of a row (8, or 3 of RMS norms) are taken in one pass and joined once.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include <atomic>
 
 #include "f32x2.cuh"
@@ -22,6 +24,10 @@ __device__ __forceinline__ int64_t walker_of(int64_t rows, int64_t row, int64_t 
 
 enum : int { GATE_NONE, GATE_SHARED, GATE_ROWS };
 constexpr int kResNormRing = 224 * 1024;  // of shared memory, beside the sums
+constexpr int kResNormCluster = 8;        // CTAs that share a row, at most
+// Columns of each CTA of a cluster, whole pieces of n; the last one's may be fewer. (Clustered
+// rows have over a thousand pieces, so that it has some.)
+__host__ __device__ __forceinline__ int resnorm_share(int d, int n, int ranks) { return (d / n + ranks - 1) / ranks * n; }
 
 // CTAs of a kernel that an SM holds with `smem` bytes each, asked once a device; -1 where that
 // fails. `most`: the largest shared memory that it is launched with.
@@ -77,9 +83,13 @@ constexpr int staged_pitch(int d, int size) { return (d * size + 31) / 16 * 16; 
 // lies in, and a thread's N columns are G apart, so that a warp's accesses are to
 // consecutive elements wherever the row begins; one more barrier a row lets the threads
 // read what others copied.
-template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, bool STRIDED>
+// CLUSTER: rows too long for one CTA's shared memory. A cluster is a walker, each of its CTAs
+// has an equal run of the columns, and a row's sums are exchanged by one cluster barrier
+// while the next row is on its way.
+template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, bool STRIDED, bool CLUSTER>
 __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walkers) {
   static_assert(!STRIDED || (NV == 1 && (R == 1 || G == 32)), "");
+  static_assert(!CLUSTER || R == 1, "");
   constexpr int B = N * static_cast<int>(sizeof(T)), H = N / 2;
   static_assert(STRIDED || B == 16, "");
   constexpr bool INNER = POST || GATE != GATE_NONE;
@@ -89,14 +99,20 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   extern __shared__ __align__(16) unsigned char ring_raw[];
   __shared__ float part[2 * (SUMS < 4 ? 128 : 32 * SUMS)];
   V* const ring = reinterpret_cast<V*>(ring_raw) + threadIdx.x;  // [2][ARRAYS][NV][threads]
+  __shared__ float rank_sums[2][CLUSTER ? kResNormCluster : 1][SUMS];  // of every CTA of the cluster
   const int tid = threadIdx.x % G, d = static_cast<int>(a.d);
-  const int64_t walker = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
+  auto cluster = cooperative_groups::this_cluster();
+  const int ranks = CLUSTER ? static_cast<int>(cluster.num_blocks()) : 1, rank = CLUSTER ? static_cast<int>(cluster.block_rank()) : 0;
+  // the CTA's columns
+  const int share = CLUSTER ? resnorm_share(d, STRIDED ? 1 : N, ranks) : d, first = rank * share;
+  const int edge = !CLUSTER || d < first + share ? d : first + share;
+  const int64_t walker = CLUSTER ? blockIdx.x / ranks : static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
   const int64_t from = walker < walkers ? first_row(a.rows, walker, walkers) : 0;
   const int mine = walker < walkers ? static_cast<int>(first_row(a.rows, walker + 1, walkers) - from) : 0;
   // every group of a CTA makes the same number of turns: barriers are the CTA's
   const int turns = static_cast<int>((a.rows + walkers - 1) / walkers);
 
-  uint64_t w[NV][H], f[NV][H], dw[NV][H], e1[NV][H];  // f: a, or scale gate
+  uint64_t w[NV][H], f[NV][H], dw[NV][H], e1[NV][H];  // f: a; scale gate without a post norm; pw with a gate for each row
   // The sums of dy and of scale g, that layer norms have beside: in registers, or where these
   // would leave an SM one CTA in shared memory, each thread its own.
   constexpr bool STASH = resnorm_stash<N, G, R, RMS, STRIDED>();
@@ -123,9 +139,9 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
       for (int e = 0; e < H; ++e) (which ? e0_reg[k][e] : db_reg[k][e]) = v[e];
     }
   };
-  // column i of the thread's piece k; a piece's columns are all in the row, or with STRIDED each is
-  auto column = [&](int k, int i = 0) { return STRIDED ? i * G + tid : (k * G + tid) * N + i; };
-  auto inside = [&](int i) { return !STRIDED || column(0, i) < d; };
+  // column i of the thread's piece k; a piece's columns are all in the CTA's, or with STRIDED each is
+  auto column = [&](int k, int i = 0) { return first + (STRIDED ? i * G + tid : (k * G + tid) * N + i); };
+  auto inside = [&](int i) { return !STRIDED || column(0, i) < edge; };
   // N parameters from element `at` of p on
   auto load_pairs = [&](const void* p, int bf16, int64_t at, int k, uint64_t (&v)[H]) {
     float u[N] = {};
@@ -151,19 +167,19 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
     }
     keep_sums(0, k, none);
     if constexpr (POST) keep_sums(1, k, none);
-    if (column(k) < d) {
+    if (column(k) < edge) {
       load_pairs(a.weight, a.param_bf16, 0, k, w[k]);
       if constexpr (POST && GATE != GATE_SHARED) {
         uint64_t pw[H];
         load_pairs(a.post_weight, a.param_bf16, 0, k, pw);
 #pragma unroll
-        for (int e = 0; e < H; ++e) f[k][e] = mul2(pw[e], scale2);
+        for (int e = 0; e < H; ++e) f[k][e] = GATE == GATE_ROWS ? pw[e] : mul2(pw[e], scale2);
       }
     }
   }
 
   auto slot_of = [&](int half, int which, int k) -> V& { return ring[((half * ARRAYS + which) * NV + k) * (G * R)]; };
-  const int pitch = staged_pitch(d, sizeof(T));
+  const int pitch = staged_pitch(share, sizeof(T));
   unsigned char* const staged = ring_raw + threadIdx.x / G * (2 * ARRAYS * pitch);  // the group's
   auto fetch = [&](int n, int half) {
     if (n < mine) {
@@ -171,11 +187,11 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
       auto copy = [&](int which, const void* p, int64_t ld) {
         const T* q = static_cast<const T*>(p) + row * ld;
         if constexpr (STRIDED) {
-          stage_row<T, G>(staged + (half * ARRAYS + which) * pitch, q, static_cast<const T*>(p), d, tid);
+          stage_row<T, G>(staged + (half * ARRAYS + which) * pitch, q + first, static_cast<const T*>(p), edge - first, tid);
         } else {
 #pragma unroll
           for (int k = 0; k < NV; ++k)
-            if (column(k) < d) copy_async<B>(&slot_of(half, which, k), q + column(k));
+            if (column(k) < edge) copy_async<B>(&slot_of(half, which, k), q + column(k));
         }
       };
       copy(0, a.dy, a.ld_dy);
@@ -194,7 +210,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   auto values = [&](int half, int which, int k, const void* base, int64_t ld, int64_t row) {
     Values u;
     if constexpr (STRIDED) {
-      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * ld) & 15);
+      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * ld + first) & 15);
       u.p = reinterpret_cast<const T*>(staged + (half * ARRAYS + which) * pitch + off);
     } else {
       u.v = slot_of(half, which, k);
@@ -203,7 +219,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   };
   auto pair = [&](const Values& u, int e) {
     if constexpr (STRIDED)
-      return pair_of(inside(2 * e) ? ldf(u.p, column(0, 2 * e)) : 0.f, inside(2 * e + 1) ? ldf(u.p, column(0, 2 * e + 1)) : 0.f);
+      return pair_of(inside(2 * e) ? ldf(u.p, column(0, 2 * e) - first) : 0.f, inside(2 * e + 1) ? ldf(u.p, column(0, 2 * e + 1) - first) : 0.f);
     else
       return pair_of(u.v.get(2 * e), u.v.get(2 * e + 1));
   };
@@ -239,7 +255,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
                                       : part_of(a.at_tail);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (column(k) < d) {
+      if (column(k) < edge) {
         uint64_t pw[H], g[H], v[H], e0[H];
         if constexpr (POST) {
           load_sums(1, k, e0);
@@ -297,6 +313,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   int64_t gate_from = from, gate_to = GATE == GATE_SHARED ? from : 0;  // the rows of the gate in f
   Stats next = stats_of(0);
   fetch(0, 0);
+  if constexpr (CLUSTER) cluster.sync();  // every CTA runs: its shared memory may be written
   int half = 0;
   for (int n = 0; n < turns; ++n, half ^= 1) {
     if constexpr (STRIDED) {
@@ -320,7 +337,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
         gate_to = (row / a.gate_rows + 1) * a.gate_rows;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-          if (column(k) < d) {
+          if (column(k) < edge) {
             load_pairs(a.gate, a.gate_bf16, row / a.gate_rows * a.ld_gate, k, f[k]);
             uint64_t pw[H];
             if constexpr (POST) load_pairs(a.post_weight, a.param_bf16, 0, k, pw);
@@ -338,7 +355,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
     if (live) {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-        if (column(k) < d) {
+        if (column(k) < edge) {
           const Values vy = values(half, 0, k, a.dy, a.ld_dy, row), vh = values(half, 1, k, a.h, a.ld_h, row);
           Values vd, vx, vg;
           if constexpr (POST) {
@@ -381,7 +398,25 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
       sums[i] = p.x + p.y;
     }
     group_sums<G, SUMS>(sums, part, half);
+    if constexpr (CLUSTER) {
+      // (a half is written again two rows on, behind a barrier that its readers have reached)
+      if (tid < ranks) {
+        float* const to = cluster.map_shared_rank(&rank_sums[half][rank][0], tid);
+#pragma unroll
+        for (int i = 0; i < SUMS; ++i) to[i] = sums[i];
+      }
+      cluster.sync();
+#pragma unroll
+      for (int i = 0; i < SUMS; ++i) {
+        sums[i] = rank_sums[half][0][i];
+        for (int c = 1; c < ranks; ++c) sums[i] += rank_sums[half][c][i];
+      }
+    }
     if (!live) continue;
+    if constexpr (POST && GATE == GATE_ROWS) {  // (of a over scale)
+#pragma unroll
+      for (int i = 2; i < SUMS; ++i) sums[i] *= a.scale;
+    }
     // r c2, r c1
     const float c2 = s.r * sums[0] * inv_d, c1 = RMS ? 0.f : s.r * sums[1] * inv_d;
     float b1 = 0.f, b2 = 0.f;  // means of a g and of a g k
@@ -399,7 +434,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
     T* const to_x = a.dx ? static_cast<T*>(a.dx) + row * a.ld_dx : nullptr;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (column(k) < d) {
+      if (column(k) < edge) {
         const Values vy = values(half, 0, k, a.dy, a.ld_dy, row), vh = values(half, 1, k, a.h, a.ld_h, row);
         Values vd, vx, vg;
         if (a.dh) vd = values(half, 2, k, a.dh, a.ld_dh, row);
@@ -420,22 +455,20 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
           if (a.dh) g = add2(g, pair(vd, e));
           const float2 gr = of_pair(g);
           res[2 * e] = gr.x, res[2 * e + 1] = gr.y;
-          uint64_t out = mul2(g, f[k][e]);  // a g, or scale gate g
+          const uint64_t sg = mul2(g, scale2);
+          uint64_t out = POST && GATE == GATE_ROWS ? mul2(sg, f[k][e]) : mul2(g, f[k][e]);  // a g, or scale gate g
           if constexpr (INNER) {
             const uint64_t kx = POST ? hat_of(pair(vx, e), pm2, pr2) : pair(vx, e);
             if constexpr (GATE == GATE_ROWS) {
-              // dgate = scale g p, p = k pw + pb: out has scale pw g, or scale g
-              uint64_t v = mul2(out, kx);
-              if (POST && !RMS) v = fma2(mul2(g, scale2), pb[e], v);
-              const float2 dv = of_pair(v);
+              // dgate = scale g p; p = k pw + pb is rounded once, for its parts may cancel
+              const float2 dv = of_pair(POST ? mul2(sg, RMS ? mul2(kx, f[k][e]) : fma2(kx, f[k][e], pb[e])) : mul2(out, kx));
               dg[2 * e] = dv.x, dg[2 * e + 1] = dv.y;
               out = mul2(out, pair(vg, e));
             }
             if constexpr (POST || GATE == GATE_SHARED) {
-              uint64_t sg = mul2(g, scale2);  // with a gate for every row: its part of q too
-              if constexpr (GATE == GATE_ROWS) sg = mul2(sg, pair(vg, e));
-              e1[k][e] = fma2(sg, kx, e1[k][e]);
-              if (POST && !RMS) e0[e] = add2(e0[e], sg);
+              const uint64_t part_g = GATE == GATE_ROWS ? mul2(sg, pair(vg, e)) : sg;  // with a gate for every row: of q
+              e1[k][e] = fma2(part_g, kx, e1[k][e]);
+              if (POST && !RMS) e0[e] = add2(e0[e], part_g);
             }
             if constexpr (POST) out = mul2(fma2(kx, o2, add2(out, o1)), pr2);
           }
@@ -453,7 +486,7 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   if constexpr (GATE == GATE_SHARED) flush(gate_from, from + mine);
 #pragma unroll
   for (int k = 0; k < NV; ++k)
-    if (column(k) < d) {
+    if (column(k) < edge) {
       if (a.dweight) store_sums(part_of(a.at_dw), k, dw[k]);
       uint64_t v[H];
       if (!RMS && a.dbias) {
@@ -478,7 +511,7 @@ cudaError_t resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_
   constexpr int stash = resnorm_stash<N, G, R, RMS, STRIDED>() ? (POST ? 2 : 1) * NV * N * 4 * G * R : 0;
   constexpr int smem = 2 * arrays * (NV * N * static_cast<int>(sizeof(T)) * G + (STRIDED ? 32 : 0)) * R + stash;
   static_assert(smem <= kResNormRing, "shared memory");
-  auto kernel = k_resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE, STRIDED>;
+  auto kernel = k_resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE, STRIDED, false>;
   static std::atomic<uint64_t> configured{0};
   static std::atomic<int> per_sm{0};
   cudaError_t e;
@@ -497,6 +530,51 @@ cudaError_t resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_
   return cudaGetLastError();
 }
 
+// The same with a cluster of 2, 4 or 8 CTAs for a row, as few as hold it.
+template <typename T, int N, int NV, int G, bool RMS, bool POST, int GATE, bool STRIDED>
+cudaError_t resnorm_bwd_cluster(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
+  constexpr int arrays = 3 + (POST || GATE != GATE_NONE) + (GATE == GATE_ROWS);
+  constexpr int smem = 2 * arrays * (NV * N * static_cast<int>(sizeof(T)) * G + (STRIDED ? 32 : 0));
+  static_assert(smem <= kResNormRing && !resnorm_stash<N, G, 1, RMS, STRIDED>(), "shared memory");
+  static_assert(kMaxResNormDim <= static_cast<int64_t>(kResNormCluster) * NV * N * G, "the longest rows");
+  auto kernel = k_resnorm_bwd<T, N, NV, G, 1, RMS, POST, GATE, STRIDED, true>;
+  int ranks = 2, log = 0;
+  while (resnorm_share(static_cast<int>(a.d), STRIDED ? 1 : N, ranks) > NV * N * G) ranks *= 2, ++log;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(static_cast<unsigned>(ranks));
+  config.blockDim = dim3(G);
+  config.dynamicSmemBytes = smem;
+  config.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  config.attrs = attr;
+  config.numAttrs = 1;
+  // clusters that the GPU holds at a time, asked once a device and size
+  static std::atomic<uint64_t> configured[3];
+  static std::atomic<int> clusters[3];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(configured[log].load() & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    int n = 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &config);
+    if (e != cudaSuccess) return e;
+    clusters[log].store(n < 1 ? 1 : n);
+    configured[log].fetch_or(bit);
+  }
+  const int64_t most = clusters[log].load(), half = sms / ranks / 2;
+  int64_t w = a.rows;  // (rows a walker as above)
+  if (w > half) w = w / 4 > half ? w / 4 : half;
+  w = w < most ? w : most;
+  *walkers = static_cast<int>(w);
+  config.gridDim = dim3(static_cast<unsigned>(w * ranks));
+  return cudaLaunchKernelEx(&config, kernel, a, *walkers);
+}
+
 // A row is given to few threads with several pieces each (see the norm's backward).
 template <typename T, int N, bool RMS, bool POST, int GATE>
 cudaError_t resnorm_bwd_n(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
@@ -513,7 +591,7 @@ cudaError_t resnorm_bwd_n(const ResNormArgs& a, int sms, int* walkers, cudaStrea
   RESNORM_CASE(1024, 2, 512, 1)
   if constexpr (GATE != GATE_ROWS) RESNORM_CASE(1536, 3, 512, 1)
 #undef RESNORM_CASE
-  return cudaErrorNotSupported;  // longer rows: the caller has another kernel
+  return resnorm_bwd_cluster<T, N, 2, 512, RMS, POST, GATE, false>(a, sms, walkers, s);
 }
 template <typename T, bool RMS, bool POST, int GATE>
 cudaError_t resnorm_bwd_strided(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
@@ -523,7 +601,7 @@ cudaError_t resnorm_bwd_strided(const ResNormArgs& a, int sms, int* walkers, cud
   if (a.d <= 4096) return resnorm_bwd<T, 8, 1, 512, 1, RMS, POST, GATE, true>(a, sms, walkers, s);
   if constexpr (sizeof(T) == 2)
     if (a.d <= 8192) return resnorm_bwd<T, 8, 1, 1024, 1, RMS, POST, GATE, true>(a, sms, walkers, s);
-  return cudaErrorNotSupported;
+  return resnorm_bwd_cluster<T, 8, 1, sizeof(T) == 2 ? 1024 : 512, RMS, POST, GATE, true>(a, sms, walkers, s);
 }
 
 template <typename T, bool POST>
@@ -548,7 +626,7 @@ cudaError_t resnorm_bwd_kind(const ResNormArgs& a, bool whole, int sms, int* wal
                                : resnorm_bwd_n<T, N, false, POST, GATE_ROWS>(a, sms, walkers, s);
 }
 
-// Whole: rows in 16-byte pieces. cudaErrorNotSupported for rows that are too long. (A translation unit each.)
+// Whole: rows in 16-byte pieces. (A translation unit each.)
 cudaError_t resnorm_bwd_f32(const ResNormArgs& a, bool whole, int sms, int* walkers, cudaStream_t s);
 cudaError_t resnorm_bwd_f32_post(const ResNormArgs& a, bool whole, int sms, int* walkers, cudaStream_t s);
 cudaError_t resnorm_bwd_bf16(const ResNormArgs& a, bool whole, int sms, int* walkers, cudaStream_t s);

@@ -102,6 +102,18 @@ def test_sizes_and_types(rows, d, kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("dtype,rows,d", [(F32, 480, 4099), (F32, 300, 8200), (BF16, 480, 8195), (BF16, 300, 16392), (BF16, 75, 30001),
+                                          (F32, 75, 20004)])
+def test_long_rows(dtype, rows, d, kind):
+    """Several rows to each of those that work at a time, whole pieces and not."""
+    s = inputs(rows, d, dtype, **of_kind(kind, rows))
+    _, first = check(s, scale=0.7, rms=kind.get("rms", False))
+    _, again = check(s, scale=0.7, rms=kind.get("rms", False))
+    assert all(torch.equal(first[k], again[k]) for k in BWD if first[k] is not None)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,d", [(50, 512), (33, 257), (9, 5000), (2, 32768)])
 def test_a_gate_of_another_type_than_the_rows(rows, d):
     for dtype, gdtype, gate in ((BF16, F32, rows), (F32, BF16, rows), (BF16, F32, 1), (F32, BF16, 1)):
