@@ -295,6 +295,179 @@ __global__ void __launch_bounds__(G * R) k_resnorm_fwd_strided(ResNormArgs a, in
   }
 }
 
+// Rows that lie in their granules alike: a walker's threads have whole pieces that keep their
+// columns (see the backward). The weights of these stay in registers; the biases, and a gate
+// that all rows share, in shared memory, each thread its own.
+struct ShiftedLayout {
+  bool gate_rows;
+  int arrays, bias, post_bias, gate, vectors;  // staged rows; the vectors' places, and how many
+};
+__host__ __device__ __forceinline__ ShiftedLayout shifted_layout(const ResNormArgs& a) {
+  ShiftedLayout l;
+  l.gate_rows = a.gate && a.gate_rows == 1;
+  l.arrays = l.gate_rows ? 3 : 2;
+  l.bias = 0;
+  l.post_bias = l.bias + (a.bias != nullptr);
+  l.gate = l.post_bias + (a.post_bias != nullptr);
+  l.vectors = l.gate + (a.gate && !l.gate_rows);
+  return l;
+}
+template <typename T, int N, int NV, int G, int R, bool POST>
+__global__ void __launch_bounds__(G * R) k_resnorm_fwd_shifted(ResNormArgs a, int walkers, int step) {
+  extern __shared__ __align__(16) unsigned char ring_raw[];
+  __shared__ float part[2 * 128];
+  using V = Piece<T, N>;
+  constexpr int es = static_cast<int>(sizeof(T)), THREADS = G * R;
+  const int tid = threadIdx.x % G, d = static_cast<int>(a.d);
+  const int64_t walker = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
+  const Walk walk = shifted_walk(a, a.ld_x, walker, walkers, step, es);
+  const float inv_d = 1.f / d;
+  const ShiftedLayout l = shifted_layout(a);
+  const bool gate_rows = l.gate_rows;
+  auto column = [&](int k) { return (k * G + tid) * N - walk.shift; };
+  auto there = [&](int k) { return column(k) < d; };
+  auto inside = [&](int k, int e) { return static_cast<unsigned>(column(k) + e) < static_cast<unsigned>(d); };
+  auto inside_all = [&](int k) { return column(k) >= 0 && column(k) + N <= d; };
+  V* const ring = reinterpret_cast<V*>(ring_raw) + threadIdx.x;  // [2][x, residual, a gate][NV][threads]
+  auto slot_of = [&](int half, int which, int k) -> V& { return ring[((half * l.arrays + which) * NV + k) * THREADS]; };
+  float* const vectors = reinterpret_cast<float*>(ring_raw + 2 * l.arrays * NV * 16 * THREADS) + threadIdx.x;  // [vectors][NV][N][threads]
+  auto kept = [&](int which, int k, int e) -> float& { return vectors[((which * NV + k) * N + e) * THREADS]; };
+  float w[NV][N], pw[NV][N];
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const bool in = inside(k, e);
+      const int c = column(k) + e;
+      w[k][e] = in ? param(a.weight, a.param_bf16, c) : 0.f;
+      if (POST) pw[k][e] = in ? param(a.post_weight, a.param_bf16, c) : 0.f;
+      if (a.bias) kept(l.bias, k, e) = in ? param(a.bias, a.param_bf16, c) : 0.f;
+      if (POST && a.post_bias) kept(l.post_bias, k, e) = in ? param(a.post_bias, a.param_bf16, c) : 0.f;
+      if (a.gate && !gate_rows) kept(l.gate, k, e) = in ? param(a.gate, a.gate_bf16, c) : 0.f;
+    }
+  auto row_at = [&](int n) { return walk.from + static_cast<int64_t>(n) * step; };
+  auto fetch = [&](int n, int half) {
+    if (n < walk.mine) {
+      const int64_t row = row_at(n);
+      auto copy = [&](int which, const void* p, int64_t ld) {
+        const T* const q = static_cast<const T*>(p) + row * ld;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          if (there(k)) copy_async_zero(&slot_of(half, which, k), q + column(k), min(16, (d - column(k)) * es));
+      };
+      copy(0, a.x, a.ld_x);
+      copy(1, a.residual, a.ld_res);
+      if (gate_rows) copy(2, a.gate, a.ld_gate);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int slot = 0;
+  auto sum = [&](float v) {
+    slot ^= 1;
+    return group_sum<G>(v, part, slot);
+  };
+  fetch(0, 0);
+  int half = 0;
+  for (int n = 0; n < walk.turns; ++n, half ^= 1) {
+    fetch(n + 1, half ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const bool live = n < walk.mine;
+    const int64_t row = row_at(n);
+    if (live && column(0) < 0)  // the row before
+      for (int which = 0; which < 2 + gate_rows; ++which)
+        for (int i = 0; i < walk.shift; ++i) reinterpret_cast<T*>(&slot_of(half, which, 0))[i] = T(0.f);
+    float h[NV][N];  // 0 beside the row
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      V v;
+      if (live && there(k)) v = slot_of(half, 0, k);
+#pragma unroll
+      for (int e = 0; e < N; ++e) h[k][e] = live && there(k) ? v.get(e) : 0.f;
+    }
+    auto mean_of = [&] {
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < N; ++e) s += h[k][e];
+      return sum(s) * inv_d;
+    };
+    auto rstd_of = [&](float mean) {
+      float q = 0.f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (a.rms || inside_all(k)) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) q = fmaf(h[k][e] - mean, h[k][e] - mean, q);
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (inside(k, e)) q = fmaf(h[k][e] - mean, h[k][e] - mean, q);
+        }
+      }
+      return rsqrtf(sum(q) * inv_d + a.eps);
+    };
+    auto store = [&](void* p, int64_t ld, int k, const float* v) {
+      T* const to = static_cast<T*>(p) + row * ld + column(k);
+      if (inside_all(k)) {
+        V o;
+        o.set(v);
+        store_piece(to, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (inside(k, e)) stf(to, e, v[e]);
+      }
+    };
+    float pm = 0.f, pr = 1.f;
+    if constexpr (POST) {
+      if (!a.rms) pm = mean_of();
+      pr = rstd_of(pm);
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          h[k][e] = (h[k][e] - pm) * pr * pw[k][e];
+          if (a.post_bias) h[k][e] += kept(l.post_bias, k, e);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (live && there(k)) {
+        if (gate_rows) {
+          const V g = slot_of(half, 2, k);
+#pragma unroll
+          for (int e = 0; e < N; ++e) h[k][e] *= g.get(e);
+        } else if (a.gate) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) h[k][e] *= kept(l.gate, k, e);
+        }
+        const V v = slot_of(half, 1, k);
+#pragma unroll
+        for (int e = 0; e < N; ++e) h[k][e] = fmaf(a.scale, h[k][e], v.get(e));
+        store(a.h_out, a.ld_h, k, h[k]);
+      }
+    const float m = a.rms ? 0.f : mean_of(), r = rstd_of(m);
+    if (!live) continue;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (there(k)) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          h[k][e] = (h[k][e] - m) * r * w[k][e];
+          if (a.bias) h[k][e] += kept(l.bias, k, e);
+        }
+        store(a.y, a.ld_y, k, h[k]);
+      }
+    if (tid == 0) {
+      if (a.mean) a.mean[row] = m;
+      if (a.rstd) a.rstd[row] = r;
+      if (a.post_mean) a.post_mean[row] = pm;
+      if (a.post_rstd) a.post_rstd[row] = pr;
+    }
+  }
+}
+
 // Rows too long for registers: h stands in shared memory, x is read again, mostly from L2;
 // kMany columns of a thread at a time, so that their loads are in flight together. (9000 x
 // 9999 bf16, RMS with a post norm, floor 108 us: forward 400 us, backward 1697: the loads of
@@ -610,8 +783,42 @@ cudaError_t fwd_strided(const ResNormArgs& a, int sms, cudaStream_t s) {
   kernel<<<static_cast<unsigned>(grid), G * R, smem, s>>>(a, static_cast<int>(walkers));
   return cudaGetLastError();
 }
+template <typename T, int N, int NV, int G, int R, bool POST>
+cudaError_t fwd_shifted(const ResNormArgs& a, int step, int sms, cudaStream_t s) {
+  auto kernel = k_resnorm_fwd_shifted<T, N, NV, G, R, POST>;
+  static_assert((2 * 3 * 16 + 3 * N * 4) * NV * G * R <= kResNormRing, "shared memory");
+  static std::atomic<uint64_t> configured{0};
+  static std::atomic<int> per_sm{0};
+  cudaError_t e;
+  const ShiftedLayout l = shifted_layout(a);
+  const int smem = (2 * l.arrays * 16 + l.vectors * N * 4) * NV * G * R;
+  // (as many as the registers leave, and this call's shared memory)
+  const int n = resident_ctas(reinterpret_cast<const void*>(kernel), G * R, 0, kResNormRing, configured, per_sm, &e);
+  if (n < 0) return e;
+  const int fit = kResNormRing / (smem + 3 * 1024), most = n < fit ? n : fit;
+  const int64_t need = (a.rows + R - 1) / R, all = static_cast<int64_t>(most < 1 ? 1 : most) * sms, grid = need < all ? need : all;
+  const int64_t walkers = (grid * R < a.rows ? grid * R : a.rows) / step * step;
+  kernel<<<static_cast<unsigned>(grid), G * R, smem, s>>>(a, static_cast<int>(walkers), step);
+  return cudaGetLastError();
+}
+template <typename T, int N, bool POST>
+cudaError_t fwd_shifted_n(const ResNormArgs& a, int step, int sms, cudaStream_t s) {
+  const int64_t pieces = (a.d + 2 * N - 2) / N;  // a row begins up to N - 1 elements late
+  if (pieces <= 32) return cudaErrorNotSupported;  // few columns: sooner done as strided rows
+  if (pieces <= 64) return fwd_shifted<T, N, 2, 32, 4, POST>(a, step, sms, s);
+  if (pieces <= 128) return fwd_shifted<T, N, 2, 64, 1, POST>(a, step, sms, s);
+  if (pieces <= 256) return fwd_shifted<T, N, 2, 128, 1, POST>(a, step, sms, s);
+  if (pieces <= 384) return fwd_shifted<T, N, 3, 128, 1, POST>(a, step, sms, s);
+  if (pieces <= 512) return fwd_shifted<T, N, 2, 256, 1, POST>(a, step, sms, s);
+  if (pieces <= 1024) return fwd_shifted<T, N, 2, 512, 1, POST>(a, step, sms, s);
+  return cudaErrorNotSupported;
+}
 template <typename T, bool POST>
 cudaError_t fwd_any(const ResNormArgs& a, int sms, cudaStream_t s) {
+  if (const int step = resnorm_step(a, true)) {
+    const cudaError_t e = fwd_shifted_n<T, 16 / static_cast<int>(sizeof(T)), POST>(a, step, sms, s);
+    if (e != cudaErrorNotSupported) return e;
+  }
   if (a.d <= 256) return fwd_strided<T, 8, 32, 8, POST>(a, sms, s);
   if (a.d <= 512) return fwd_strided<T, 16, 32, 8, POST>(a, sms, s);
   if (a.d <= 1024) return fwd_strided<T, 16, 64, 1, POST>(a, sms, s);

@@ -23,8 +23,60 @@ __device__ __forceinline__ int64_t first_row(int64_t rows, int64_t w, int64_t n)
 __device__ __forceinline__ int64_t walker_of(int64_t rows, int64_t row, int64_t n) { return ((row + 1) * n - 1) / rows; }
 
 enum : int { GATE_NONE, GATE_SHARED, GATE_ROWS };
+enum : int { ROWS_WHOLE, ROWS_SHIFTED, ROWS_STRIDED };
 constexpr int kResNormRing = 224 * 1024;  // of shared memory, beside the sums
 constexpr int kResNormCluster = 8;        // CTAs that share a row, at most
+// Rows that lie in their granules alike, in every operand: how many rows on they do so again. 0
+// where the operands differ; where a gate has some of the rows, for what a walker takes is not
+// contiguous; and where there are few rows of a step.
+constexpr int kShiftedRows = 256;
+inline int resnorm_step(const ResNormArgs& a, bool fwd) {
+  if (a.gate && a.gate_rows > 1 && a.gate_rows != a.rows) return 0;
+  const int64_t es = a.bf16 ? 2 : 4, cut = (fwd ? a.ld_x : a.ld_h) * es % 16;
+  bool alike = true;
+  auto rows = [&](const void* p, int64_t ld) {
+    if (p) alike = alike && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == cut;
+  };
+  rows(a.x, a.ld_x);
+  if (fwd) {
+    rows(a.residual, a.ld_res);
+    rows(a.h_out, a.ld_h);
+    rows(a.y, a.ld_y);
+  } else {
+    rows(a.h, a.ld_h);
+    rows(a.dy, a.ld_dy);
+    rows(a.dh, a.ld_dh);
+    rows(a.dx, a.ld_dx);
+    rows(a.dres, a.ld_dres);
+  }
+  if (a.gate && a.gate_rows == 1) {
+    if (a.gate_bf16 != a.bf16) return 0;
+    rows(a.gate, a.ld_gate);
+    rows(a.dgate, a.ld_dgate);
+  }
+  int step = 1;
+  while (cut * step % 16) step *= 2;
+  return alike && a.rows >= kShiftedRows * step ? step : 0;
+}
+// The rows that a walker has of those: from, from + step, ..., `mine` of them.
+struct Walk {
+  int64_t from;
+  int mine, turns;  // turns: the most that a walker has
+  int shift;        // elements of the first granule that are not the row's
+};
+__device__ __forceinline__ Walk shifted_walk(const ResNormArgs& a, int64_t ld, int64_t walker, int walkers, int step, int size) {
+  const int64_t run = walker / step, runs = walkers / step;
+  Walk w = {0, 0, static_cast<int>(((a.rows + runs - 1) / runs + step - 1) / step), 0};
+  if (walker < walkers) {
+    const int64_t to = first_row(a.rows, run + 1, runs);
+    w.from = first_row(a.rows, run, runs);
+    w.from += (walker % step + step - w.from % step) % step;
+    w.mine = w.from < to ? static_cast<int>((to - w.from + step - 1) / step) : 0;
+  }
+  w.shift = static_cast<int>((w.from * ld * size) & 15) / size;
+  return w;
+}
+
 // Columns of each CTA of a cluster, whole pieces of n; the last one's may be fewer. (Clustered
 // rows have over a thousand pieces, so that it has some.)
 __host__ __device__ __forceinline__ int resnorm_share(int d, int n, int ranks) { return (d / n + ranks - 1) / ranks * n; }
@@ -49,9 +101,9 @@ inline int resident_ctas(const void* kernel, int threads, int smem, int most, st
 }
 
 // Whether layer norms' second sums are in shared memory (see the kernel).
-template <int N, int G, int R, bool RMS, bool STRIDED>
+template <int N, int G, int R, bool RMS, int MODE>
 constexpr bool resnorm_stash() {
-  return !RMS && !STRIDED && N == 8 && G * R <= 256;
+  return !RMS && MODE != ROWS_STRIDED && N == 8 && G * R <= 256;
 }
 
 // Copies a row of d elements by the 16-byte granules it lies in while the G threads go on;
@@ -79,17 +131,22 @@ constexpr int staged_pitch(int d, int size) { return (d * size + 31) / 16 * 16; 
 // of which dgate = pw e1 + pb e0, and gate e1 and gate e0 are these rows' parts of the post
 // norm's dweight and dbias: taken when the gate changes, so that a row adds to two sums and
 // not to three.
-// STRIDED: rows that do not come in whole pieces. A row is staged by the 16-byte granules it
+// ROWS_SHIFTED: rows that begin and end inside a 16-byte granule, at the same place in every
+// operand. A walker takes every step-th row of a run, whose granules are cut alike, so that
+// its threads' pieces are granules and keep their columns: the first one may have elements of
+// the row before, which are cleared as they arrive.
+// ROWS_STRIDED: others that do not come in whole pieces. A row is staged by the 16-byte granules it
 // lies in, and a thread's N columns are G apart, so that a warp's accesses are to
 // consecutive elements wherever the row begins; one more barrier a row lets the threads
 // read what others copied.
 // CLUSTER: rows too long for one CTA's shared memory. A cluster is a walker, each of its CTAs
 // has an equal run of the columns, and a row's sums are exchanged by one cluster barrier
 // while the next row is on its way.
-template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, bool STRIDED, bool CLUSTER>
-__global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walkers) {
+template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, int MODE, bool CLUSTER>
+__global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walkers, int steps) {
+  constexpr bool STRIDED = MODE == ROWS_STRIDED, SHIFTED = MODE == ROWS_SHIFTED;
   static_assert(!STRIDED || (NV == 1 && (R == 1 || G == 32)), "");
-  static_assert(!CLUSTER || R == 1, "");
+  static_assert(!CLUSTER || (R == 1 && !SHIFTED), "");
   constexpr int B = N * static_cast<int>(sizeof(T)), H = N / 2;
   static_assert(STRIDED || B == 16, "");
   constexpr bool INNER = POST || GATE != GATE_NONE;
@@ -107,15 +164,24 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   const int share = CLUSTER ? resnorm_share(d, STRIDED ? 1 : N, ranks) : d, first = rank * share;
   const int edge = !CLUSTER || d < first + share ? d : first + share;
   const int64_t walker = CLUSTER ? blockIdx.x / ranks : static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
-  const int64_t from = walker < walkers ? first_row(a.rows, walker, walkers) : 0;
-  const int mine = walker < walkers ? static_cast<int>(first_row(a.rows, walker + 1, walkers) - from) : 0;
-  // every group of a CTA makes the same number of turns: barriers are the CTA's
-  const int turns = static_cast<int>((a.rows + walkers - 1) / walkers);
+  // its rows: from, from + step, ..., `mine` of them; every group of a CTA makes the same
+  // number of turns: barriers are the CTA's
+  int64_t from;
+  int mine, turns, shift = 0;
+  const int step = SHIFTED ? steps : 1;
+  if constexpr (SHIFTED) {
+    const Walk walk = shifted_walk(a, a.ld_h, walker, walkers, step, static_cast<int>(sizeof(T)));
+    from = walk.from, mine = walk.mine, turns = walk.turns, shift = walk.shift;
+  } else {
+    from = walker < walkers ? first_row(a.rows, walker, walkers) : 0;
+    mine = walker < walkers ? static_cast<int>(first_row(a.rows, walker + 1, walkers) - from) : 0;
+    turns = static_cast<int>((a.rows + walkers - 1) / walkers);
+  }
 
   uint64_t w[NV][H], f[NV][H], dw[NV][H], e1[NV][H];  // f: a; scale gate without a post norm; pw with a gate for each row
   // The sums of dy and of scale g, that layer norms have beside: in registers, or where these
   // would leave an SM one CTA in shared memory, each thread its own.
-  constexpr bool STASH = resnorm_stash<N, G, R, RMS, STRIDED>();
+  constexpr bool STASH = resnorm_stash<N, G, R, RMS, MODE>();
   uint64_t db_reg[STASH ? 1 : NV][H], e0_reg[STASH ? 1 : NV][H];
   ulonglong2* const stash = reinterpret_cast<ulonglong2*>(ring_raw + 2 * ARRAYS * NV * B * G * R) + threadIdx.x;
   auto load_sums = [&](int which, int k, uint64_t (&v)[H]) {  // 0: of dy, 1: of scale g
@@ -139,16 +205,17 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
       for (int e = 0; e < H; ++e) (which ? e0_reg[k][e] : db_reg[k][e]) = v[e];
     }
   };
-  // column i of the thread's piece k; a piece's columns are all in the CTA's, or with STRIDED each is
-  auto column = [&](int k, int i = 0) { return first + (STRIDED ? i * G + tid : (k * G + tid) * N + i); };
-  auto inside = [&](int i) { return !STRIDED || column(0, i) < edge; };
+  // column i of the thread's piece k; a piece's columns are all in the CTA's, or each is looked at
+  auto column = [&](int k, int i = 0) { return first + (STRIDED ? i * G + tid : (k * G + tid) * N + i - shift); };
+  auto inside = [&](int k, int i) { return STRIDED ? column(0, i) < edge : !SHIFTED || static_cast<unsigned>(column(k, i)) < static_cast<unsigned>(d); };
+  auto inside_all = [&](int k) { return !SHIFTED || (column(k) >= 0 && column(k) + N <= d); };
   // N parameters from element `at` of p on
   auto load_pairs = [&](const void* p, int bf16, int64_t at, int k, uint64_t (&v)[H]) {
     float u[N] = {};
-    if constexpr (STRIDED) {
+    if constexpr (STRIDED || SHIFTED) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (inside(i)) u[i] = bf16 ? ldf(static_cast<const __nv_bfloat16*>(p), at + column(k, i)) : ldf(static_cast<const float*>(p), at + column(k, i));
+        if (inside(k, i)) u[i] = bf16 ? ldf(static_cast<const __nv_bfloat16*>(p), at + column(k, i)) : ldf(static_cast<const float*>(p), at + column(k, i));
     } else {
       if (bf16) load_params<N>(static_cast<const __nv_bfloat16*>(p) + at, 1, column(k), u);
       else load_params<N>(static_cast<const float*>(p) + at, 0, column(k), u);
@@ -183,15 +250,18 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   unsigned char* const staged = ring_raw + threadIdx.x / G * (2 * ARRAYS * pitch);  // the group's
   auto fetch = [&](int n, int half) {
     if (n < mine) {
-      const int64_t row = from + n;
+      const int64_t row = from + static_cast<int64_t>(n) * step;
       auto copy = [&](int which, const void* p, int64_t ld) {
-        const T* q = static_cast<const T*>(p) + row * ld;
+        const T* q = static_cast<const T*>(p) + row * ld;  // (with `shift` before it in its granule)
         if constexpr (STRIDED) {
           stage_row<T, G>(staged + (half * ARRAYS + which) * pitch, q + first, static_cast<const T*>(p), edge - first, tid);
         } else {
 #pragma unroll
           for (int k = 0; k < NV; ++k)
-            if (column(k) < edge) copy_async<B>(&slot_of(half, which, k), q + column(k));
+            if (column(k) < edge) {
+              if constexpr (SHIFTED) copy_async_zero(&slot_of(half, which, k), q + column(k), min(B, (d - column(k)) * static_cast<int>(sizeof(T))));
+              else copy_async<B>(&slot_of(half, which, k), q + column(k));
+            }
         }
       };
       copy(0, a.dy, a.ld_dy);
@@ -219,27 +289,27 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   };
   auto pair = [&](const Values& u, int e) {
     if constexpr (STRIDED)
-      return pair_of(inside(2 * e) ? ldf(u.p, column(0, 2 * e) - first) : 0.f, inside(2 * e + 1) ? ldf(u.p, column(0, 2 * e + 1) - first) : 0.f);
+      return pair_of(inside(0, 2 * e) ? ldf(u.p, column(0, 2 * e) - first) : 0.f, inside(0, 2 * e + 1) ? ldf(u.p, column(0, 2 * e + 1) - first) : 0.f);
     else
       return pair_of(u.v.get(2 * e), u.v.get(2 * e + 1));
   };
   auto store = [&](T* to, int k, const float* o) {
-    if constexpr (STRIDED) {
+    if (!STRIDED && inside_all(k)) {
+      V p;
+      p.set(o);
+      store_piece(to + column(k), p);
+    } else {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (inside(i)) stf(to, column(k, i), o[i]);
-    } else {
-      Piece<T, N> p;
-      p.set(o);
-      store_piece<T, N>(to + column(k), p);
+        if (inside(k, i)) stf(to, column(k, i), o[i]);
     }
   };
   auto store_sums = [&](float* to, int k, const uint64_t (&v)[H]) {
 #pragma unroll
     for (int e = 0; e < H; ++e) {
       const float2 p = of_pair(v[e]);
-      if (inside(2 * e)) to[column(k, 2 * e)] = p.x;
-      if (inside(2 * e + 1)) to[column(k, 2 * e + 1)] = p.y;
+      if (inside(k, 2 * e)) to[column(k, 2 * e)] = p.x;
+      if (inside(k, 2 * e + 1)) to[column(k, 2 * e + 1)] = p.y;
     }
   };
   auto part_of = [&](int which) { return a.partial + (static_cast<int64_t>(which) * walkers + walker) * d; };
@@ -249,7 +319,9 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   auto flush = [&](int64_t begin, int64_t end) {
     const int64_t q = begin / a.gate_rows, q0 = q * a.gate_rows;
     // written whole, or left as a part: a gate's last rows, or its first ones
+    // (shifted rows: one gate has all rows)
     float* const to = !a.dgate ? nullptr
+                      : SHIFTED ? (walkers == 1 ? static_cast<float*>(a.dgate) : part_of(a.at_head))
                       : q0 == begin && q0 + a.gate_rows == end ? static_cast<float*>(a.dgate) + q * d
                       : begin == from ? part_of(a.at_head)
                                       : part_of(a.at_tail);
@@ -278,8 +350,8 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
 #pragma unroll
             for (int e = 0; e < H; ++e) {
               const uint64_t before = !flushed ? zero
-                                               : pair_of(inside(2 * e) ? p[column(k, 2 * e)] : 0.f,
-                                                         inside(2 * e + 1) ? p[column(k, 2 * e + 1)] : 0.f);
+                                               : pair_of(inside(k, 2 * e) ? p[column(k, 2 * e)] : 0.f,
+                                                         inside(k, 2 * e + 1) ? p[column(k, 2 * e + 1)] : 0.f);
               v[e] = fma2(g[e], s[e], before);
             }
             store_sums(p, k, v);
@@ -301,11 +373,12 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
   auto stats_of = [&](int n) {
     Stats s = {0.f, 0.f, 0.f, 1.f};
     if (n < mine) {
-      if (!RMS) s.m = a.mean[from + n];
-      s.r = a.rstd[from + n];
+      const int64_t row = from + static_cast<int64_t>(n) * step;
+      if (!RMS) s.m = a.mean[row];
+      s.r = a.rstd[row];
       if (POST) {
-        if (!RMS) s.pm = a.post_mean[from + n];
-        s.pr = a.post_rstd[from + n];
+        if (!RMS) s.pm = a.post_mean[row];
+        s.pr = a.post_rstd[row];
       }
     }
     return s;
@@ -325,11 +398,15 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
     } else {
       fetch(n + 1, half ^ 1);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if (SHIFTED && n < mine && column(0) < 0) {
+        for (int which = 0; which < ARRAYS; ++which)
+          for (int i = 0; i < shift; ++i) reinterpret_cast<T*>(&slot_of(half, which, 0))[i] = T(0.f);
+      }
     }
     const Stats s = next;
     next = stats_of(n + 1);
     const bool live = n < mine;
-    const int64_t row = from + n;
+    const int64_t row = from + static_cast<int64_t>(n) * step;
     if constexpr (GATE == GATE_SHARED) {
       if (live && row >= gate_to) {
         if (n > 0) flush(gate_from, gate_to);
@@ -505,13 +582,14 @@ __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walker
 
 // One launch: as many CTAs as the SMs hold at a time, so that each walks over its share of
 // the rows once. *walkers: rows of partial sums it writes.
-template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, bool STRIDED = false>
-cudaError_t resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
+template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, int MODE>
+cudaError_t resnorm_bwd(const ResNormArgs& a, int step, int sms, int* walkers, cudaStream_t s) {
   constexpr int arrays = 3 + (POST || GATE != GATE_NONE) + (GATE == GATE_ROWS);
-  constexpr int stash = resnorm_stash<N, G, R, RMS, STRIDED>() ? (POST ? 2 : 1) * NV * N * 4 * G * R : 0;
+  constexpr bool STRIDED = MODE == ROWS_STRIDED;
+  constexpr int stash = resnorm_stash<N, G, R, RMS, MODE>() ? (POST ? 2 : 1) * NV * N * 4 * G * R : 0;
   constexpr int smem = 2 * arrays * (NV * N * static_cast<int>(sizeof(T)) * G + (STRIDED ? 32 : 0)) * R + stash;
   static_assert(smem <= kResNormRing, "shared memory");
-  auto kernel = k_resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE, STRIDED, false>;
+  auto kernel = k_resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE, MODE, false>;
   static std::atomic<uint64_t> configured{0};
   static std::atomic<int> per_sm{0};
   cudaError_t e;
@@ -524,20 +602,21 @@ cudaError_t resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cudaStream_
   const int64_t most = static_cast<int64_t>(n) * sms, room = resnorm_walkers(a, sms) / R;
   grid = grid < most ? grid : most;
   grid = grid < room ? grid : room;
-  const int64_t w = grid * R;
-  *walkers = static_cast<int>(w < a.rows ? w : a.rows);
-  kernel<<<static_cast<unsigned>(grid), G * R, smem, s>>>(a, *walkers);
+  const int64_t w = grid * R < a.rows ? grid * R : a.rows;
+  *walkers = static_cast<int>(w / step * step);
+  kernel<<<static_cast<unsigned>(grid), G * R, smem, s>>>(a, *walkers, step);
   return cudaGetLastError();
 }
 
 // The same with a cluster of 2, 4 or 8 CTAs for a row, as few as hold it.
-template <typename T, int N, int NV, int G, bool RMS, bool POST, int GATE, bool STRIDED>
+template <typename T, int N, int NV, int G, bool RMS, bool POST, int GATE, int MODE>
 cudaError_t resnorm_bwd_cluster(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
   constexpr int arrays = 3 + (POST || GATE != GATE_NONE) + (GATE == GATE_ROWS);
+  constexpr bool STRIDED = MODE == ROWS_STRIDED;
   constexpr int smem = 2 * arrays * (NV * N * static_cast<int>(sizeof(T)) * G + (STRIDED ? 32 : 0));
-  static_assert(smem <= kResNormRing && !resnorm_stash<N, G, 1, RMS, STRIDED>(), "shared memory");
+  static_assert(smem <= kResNormRing && !resnorm_stash<N, G, 1, RMS, MODE>(), "shared memory");
   static_assert(kMaxResNormDim <= static_cast<int64_t>(kResNormCluster) * NV * N * G, "the longest rows");
-  auto kernel = k_resnorm_bwd<T, N, NV, G, 1, RMS, POST, GATE, STRIDED, true>;
+  auto kernel = k_resnorm_bwd<T, N, NV, G, 1, RMS, POST, GATE, MODE, true>;
   int ranks = 2, log = 0;
   while (resnorm_share(static_cast<int>(a.d), STRIDED ? 1 : N, ranks) > NV * N * G) ranks *= 2, ++log;
   cudaLaunchConfig_t config = {};
@@ -572,18 +651,27 @@ cudaError_t resnorm_bwd_cluster(const ResNormArgs& a, int sms, int* walkers, cud
   w = w < most ? w : most;
   *walkers = static_cast<int>(w);
   config.gridDim = dim3(static_cast<unsigned>(w * ranks));
-  return cudaLaunchKernelEx(&config, kernel, a, *walkers);
+  return cudaLaunchKernelEx(&config, kernel, a, *walkers, 1);
 }
 
-// A row is given to few threads with several pieces each (see the norm's backward).
+// A row is given to few threads with several pieces each (see the norm's backward). Short rows
+// to as many groups a CTA as make 256 threads, or 128 of bf16: most of their kernels have
+// 130 to 170 registers, of which an SM holds one CTA of 256 or three of 128 (320000 x 1000 bf16
+// with a post norm: layer norms 990 us with 256 threads, 717 with 128; RMS norms 649 and 674;
+// 800000 x 512 float32 1500 and 1545).
+template <int N>
+constexpr int resnorm_few() {
+  return N == 8 ? 4 : 8;
+}
 template <typename T, int N, bool RMS, bool POST, int GATE>
 cudaError_t resnorm_bwd_n(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
   const int64_t pieces = a.d / N;
+  constexpr int few = resnorm_few<N>();
 #define RESNORM_CASE(most, NV, G, R) \
-  if (pieces <= most) return resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE>(a, sms, walkers, s);
+  if (pieces <= most) return resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE, ROWS_WHOLE>(a, 1, sms, walkers, s);
   RESNORM_CASE(32, 1, 32, 8)
-  RESNORM_CASE(64, 2, 32, 8)
-  RESNORM_CASE(128, 2, 64, 4)
+  RESNORM_CASE(64, 2, 32, few)
+  RESNORM_CASE(128, 2, 64, few / 2)
   RESNORM_CASE(256, 2, 128, 1)
   RESNORM_CASE(384, 3, 128, 1)
   RESNORM_CASE(512, 2, 256, 1)
@@ -591,17 +679,38 @@ cudaError_t resnorm_bwd_n(const ResNormArgs& a, int sms, int* walkers, cudaStrea
   RESNORM_CASE(1024, 2, 512, 1)
   if constexpr (GATE != GATE_ROWS) RESNORM_CASE(1536, 3, 512, 1)
 #undef RESNORM_CASE
-  return resnorm_bwd_cluster<T, N, 2, 512, RMS, POST, GATE, false>(a, sms, walkers, s);
+  return resnorm_bwd_cluster<T, N, 2, 512, RMS, POST, GATE, ROWS_WHOLE>(a, sms, walkers, s);
+}
+template <typename T, int N, bool RMS, bool POST, int GATE>
+cudaError_t resnorm_bwd_shifted(const ResNormArgs& a, int step, int sms, int* walkers, cudaStream_t s) {
+  const int64_t pieces = (a.d + 2 * N - 2) / N;  // a row begins up to N - 1 elements late
+  constexpr int few = resnorm_few<N>();
+#define RESNORM_CASE(most, NV, G, R) \
+  if (pieces <= most) return resnorm_bwd<T, N, NV, G, R, RMS, POST, GATE, ROWS_SHIFTED>(a, step, sms, walkers, s);
+  RESNORM_CASE(32, 1, 32, 8)
+  RESNORM_CASE(64, 2, 32, few)
+  RESNORM_CASE(128, 2, 64, few / 2)
+  RESNORM_CASE(256, 2, 128, 1)
+  RESNORM_CASE(384, 3, 128, 1)
+  RESNORM_CASE(512, 2, 256, 1)
+  RESNORM_CASE(1024, 2, 512, 1)
+  if constexpr (GATE != GATE_ROWS) RESNORM_CASE(1536, 3, 512, 1)
+#undef RESNORM_CASE
+  return cudaErrorNotSupported;
 }
 template <typename T, bool RMS, bool POST, int GATE>
 cudaError_t resnorm_bwd_strided(const ResNormArgs& a, int sms, int* walkers, cudaStream_t s) {
-  if (a.d <= 256) return resnorm_bwd<T, 8, 1, 32, 8, RMS, POST, GATE, true>(a, sms, walkers, s);
-  if (a.d <= 1024) return resnorm_bwd<T, 8, 1, 128, 1, RMS, POST, GATE, true>(a, sms, walkers, s);
-  if (a.d <= 2048) return resnorm_bwd<T, 8, 1, 256, 1, RMS, POST, GATE, true>(a, sms, walkers, s);
-  if (a.d <= 4096) return resnorm_bwd<T, 8, 1, 512, 1, RMS, POST, GATE, true>(a, sms, walkers, s);
+  if (const int step = resnorm_step(a, false)) {
+    const cudaError_t e = resnorm_bwd_shifted<T, 16 / static_cast<int>(sizeof(T)), RMS, POST, GATE>(a, step, sms, walkers, s);
+    if (e != cudaErrorNotSupported) return e;  // (longer rows)
+  }
+  if (a.d <= 256) return resnorm_bwd<T, 8, 1, 32, 8, RMS, POST, GATE, ROWS_STRIDED>(a, 1, sms, walkers, s);
+  if (a.d <= 1024) return resnorm_bwd<T, 8, 1, 128, 1, RMS, POST, GATE, ROWS_STRIDED>(a, 1, sms, walkers, s);
+  if (a.d <= 2048) return resnorm_bwd<T, 8, 1, 256, 1, RMS, POST, GATE, ROWS_STRIDED>(a, 1, sms, walkers, s);
+  if (a.d <= 4096) return resnorm_bwd<T, 8, 1, 512, 1, RMS, POST, GATE, ROWS_STRIDED>(a, 1, sms, walkers, s);
   if constexpr (sizeof(T) == 2)
-    if (a.d <= 8192) return resnorm_bwd<T, 8, 1, 1024, 1, RMS, POST, GATE, true>(a, sms, walkers, s);
-  return resnorm_bwd_cluster<T, 8, 1, sizeof(T) == 2 ? 1024 : 512, RMS, POST, GATE, true>(a, sms, walkers, s);
+    if (a.d <= 8192) return resnorm_bwd<T, 8, 1, 1024, 1, RMS, POST, GATE, ROWS_STRIDED>(a, 1, sms, walkers, s);
+  return resnorm_bwd_cluster<T, 8, 1, sizeof(T) == 2 ? 1024 : 512, RMS, POST, GATE, ROWS_STRIDED>(a, sms, walkers, s);
 }
 
 template <typename T, bool POST>

@@ -244,6 +244,57 @@ def test_odd_widths_over_many_rows(rows, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", [k for k in KINDS if k.get("gate") != "seq"] + [dict(post=True, gate=1)], ids=str)
+@pytest.mark.parametrize("dtype,rows,d,ld", [(BF16, 2051, 1001, 1001), (BF16, 1030, 254, 258), (F32, 1027, 1003, 1003), (F32, 600, 66, 70),
+                                             (BF16, 300, 508, 512), (BF16, 2049, 2047, 2049), (BF16, 2050, 8177, 8177), (F32, 1031, 4089, 4091)])
+def test_rows_that_are_cut_alike(dtype, rows, d, ld, kind):
+    """Rows in granules that hold the end of the row before, or what is beside the rows."""
+    def laid(t):
+        flat = torch.full((rows, ld), float("nan"), dtype=t.dtype, device="cuda")
+        flat[:, :d] = t
+        return flat[:, :d]
+
+    s = inputs(rows, d, dtype, BF16, laid=laid, **of_kind(kind, rows))
+    kw = dict(scale=0.6, rms=kind.get("rms", False))
+    new = lambda: laid(torch.zeros(rows, d, dtype=dtype, device="cuda"))  # noqa: E731
+    fwd, bwd = dict(h=new(), y=new()), dict(dx=new(), dresidual=new())
+    got, back = check(s, fwd=fwd, bwd=bwd, **kw)
+    for o in (fwd["h"], fwd["y"], bwd["dx"], bwd["dresidual"]):
+        assert torch.isnan(o.as_strided((rows, ld), (ld, 1))[:, d:]).all()
+    # a row that is not finite is its own affair
+    bad, at = dict(s), rows // 2
+    for k in ("x", "residual", "dy", "dh"):
+        bad[k] = laid(s[k])
+        bad[k][at] = float("inf")
+    import grpo_loss_gb300 as G
+    args = [bad[k] for k in ("x", "residual", "weight", "bias", "post_weight", "post_bias", "gate")]
+    # (laid out as those it is compared with: sums of rows that are cut otherwise run in another order)
+    h, y, mean, rstd, pm, pr = G.residual_norm_fwd(*args, h=new(), y=new(), **kw)
+    dx, dr = G.residual_norm_bwd(bad["dy"], bad["dh"], h, s["weight"], mean, rstd, x=bad["x"], post_weight=s["post_weight"],
+                                 post_bias=s["post_bias"], post_mean=pm, post_rstd=pr, gate=s["gate"], dx=new(), dresidual=new(), **kw)[:2]
+    others = torch.arange(rows, device="cuda") != at
+    for t, want in ((h, got["h"]), (y, got["y"]), (dx, back["dx"]), (dr, back["dresidual"])):
+        assert torch.equal(t[others], want[others])
+
+
+@pytest.mark.gpu
+def test_in_place_where_rows_share_granules():
+    import grpo_loss_gb300 as G
+    s = inputs(2500, 1021, BF16, BF16, gate=1)
+    got, back = check(s, scale=0.5)
+    args = lambda x, r: (x, r, s["weight"], s["bias"], s["post_weight"], s["post_bias"], s["gate"], 0.5)  # noqa: E731
+    for _ in range(5):
+        x, r = s["x"].clone(), s["residual"].clone()
+        h, y = G.residual_norm_fwd(*args(x, r), h=r, y=x)[:2]
+        assert torch.equal(h, got["h"]) and torch.equal(y, got["y"])
+        dy, dh = s["dy"].clone(), s["dh"].clone()
+        dx, dr = G.residual_norm_bwd(dy, dh, h, s["weight"], got["mean"], got["rstd"], x=s["x"], post_weight=s["post_weight"],
+                                     post_bias=s["post_bias"], post_mean=got["post_mean"], post_rstd=got["post_rstd"],
+                                     gate=s["gate"], scale=0.5, dx=dy, dresidual=dh)[:2]
+        assert torch.equal(dx, back["dx"]) and torch.equal(dr, back["dresidual"])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,d", [(50, 1024), (50, 1021), (3, 32768)])
 def test_in_place(rows, d):
     import grpo_loss_gb300 as G
