@@ -6,10 +6,12 @@
 //   dx = post_norm'(q) or q
 // with norm'(v) = r (v w - mean(v w) - k mean(v w k)), k = (h - m) r.
 // Bound by memory: the forward reads x and the residual and writes h and y, the backward
-// (residual_norm_bwd.cuh) reads dy, dh, h and x and writes both gradients, each once. Here
-// stand the forward, what takes rows that do not come in whole 16-byte pieces or are too
-// long for them (a CTA a row, what its passes share in shared memory), and the join of
-// the walkers' column sums.
+// (residual_norm_bwd.cuh) reads dy, dh, h and x and writes both gradients, each once:
+// 163840 x 4096 bf16, RMS with a post norm, 754 us forward (7.1 TB/s) and 1210 backward (6.7).
+// Here stand the forward, the backward with gates of another type than the rows, and the join
+// of the walkers' column sums. Four ways for a row: registers, in whole 16-byte pieces; pieces
+// that are cut (ROWS_SHIFTED of the backward); staged and taken column by column; and, what is
+// too long for these, a CTA a row with h in shared memory.
 #include <cuda_bf16.h>
 
 #include "residual_norm_bwd.cuh"
@@ -297,7 +299,8 @@ __global__ void __launch_bounds__(G * R) k_resnorm_fwd_strided(ResNormArgs a, in
 
 // Rows that lie in their granules alike: a walker's threads have whole pieces that keep their
 // columns (see the backward). The weights of these stay in registers; the biases, and a gate
-// that all rows share, in shared memory, each thread its own.
+// that all rows share, in shared memory, each thread its own. (30000 x 2881 bf16, RMS with a
+// post norm: 173 us, as strided rows 277; with two pieces a thread 203.)
 struct ShiftedLayout {
   bool gate_rows;
   int arrays, bias, post_bias, gate, vectors;  // staged rows; the vectors' places, and how many
@@ -470,8 +473,8 @@ __global__ void __launch_bounds__(G * R) k_resnorm_fwd_shifted(ResNormArgs a, in
 
 // Rows too long for registers: h stands in shared memory, x is read again, mostly from L2;
 // kMany columns of a thread at a time, so that their loads are in flight together. (9000 x
-// 9999 bf16, RMS with a post norm, floor 108 us: forward 400 us, backward 1697: the loads of
-// one batch are waited for before the next.)
+// 16383 bf16, RMS with a post norm, floor 176 us: 620: the loads of one batch are waited for
+// before the next.)
 constexpr int kLong = 512, kWide = 1024, kMany = 4;
 // body(u, i) of a thread's kMany columns i from i0 on, of a CTA of THREADS.
 template <int THREADS, typename F>
@@ -544,8 +547,9 @@ __global__ void __launch_bounds__(kLong) k_resnorm_fwd_long(ResNormArgs a) {
   }
 }
 
-// The same backward. `fit` column sums stand beside g in shared memory, in the order of their first use; others are added
-// up in their partial rows.
+// The backward with a gate for each row that is of another type than these: a CTA a row, g in
+// shared memory. `fit` column sums stand beside g, in the order of their first use; others are
+// added up in their partial rows.
 template <typename T>
 __global__ void __launch_bounds__(kWide) k_resnorm_bwd_long(ResNormArgs a, int walkers, int fit) {
   extern __shared__ float g[];
@@ -562,7 +566,6 @@ __global__ void __launch_bounds__(kWide) k_resnorm_bwd_long(ResNormArgs a, int w
   };
   float* const pw = place(a.dweight, part(a.at_dw));
   float* const ppw = place(a.dpost_weight, part(a.at_dpw));
-  float* const pgate = place(a.dgate && a.gate_rows > 1, nullptr);  // null: where it is written in the end
   float* const pb = place(a.dbias, part(a.at_db));
   float* const ppb = place(a.dpost_bias, part(a.at_dpb));
   auto row_of = [](const void* p, int64_t ld, int64_t row) { return static_cast<const T*>(p) + row * ld; };
@@ -571,7 +574,7 @@ __global__ void __launch_bounds__(kWide) k_resnorm_bwd_long(ResNormArgs a, int w
     const bool first = row == from;
     const float m = a.rms ? 0.f : a.mean[row], r = a.rstd[row];
     const T *dy = row_of(a.dy, a.ld_dy, row), *h = row_of(a.h, a.ld_h, row), *dh = a.dh ? row_of(a.dh, a.ld_dh, row) : nullptr;
-    const T* x = a.x ? row_of(a.x, a.ld_x, row) : nullptr;
+    const T* x = row_of(a.x, a.ld_x, row);
     float s[2] = {0.f, 0.f};
     for (int i0 = threadIdx.x; i0 < d; i0 += kWide * kMany) {
       float v[kMany], k[kMany], w[kMany];
@@ -601,35 +604,18 @@ __global__ void __launch_bounds__(kWide) k_resnorm_bwd_long(ResNormArgs a, int w
     }
     if (!a.dx && !a.dgate && !a.dpost_weight && !a.dpost_bias) continue;
     const float pm = a.post_weight && !a.rms ? a.post_mean[row] : 0.f, pr = a.post_weight ? a.post_rstd[row] : 1.f;
-    // the rows of a gate that lie in this walker: its first and its last may be shared
-    const int64_t q = a.gate ? row / a.gate_rows : 0, q0 = q * a.gate_rows, q1 = q0 + a.gate_rows;
-    float *dgate = nullptr, *sum_gate = nullptr;
-    if (a.dgate && a.gate_rows > 1) {
-      dgate = q0 >= from && q1 <= to ? static_cast<float*>(a.dgate) + q * d : part(q0 <= from ? a.at_head : a.at_tail);
-      sum_gate = pgate ? pgate : dgate;
-    }
-    const bool first_of_gate = first || row == q0, last_of_gate = row + 1 == to || row + 1 == q1;
     s[0] = s[1] = 0.f;
     for (int i0 = threadIdx.x; i0 < d; i0 += kWide * kMany) {
       float xs[kMany], w[kMany], gt[kMany], pb_[kMany];
       columns<kWide>(d, i0, [&](int u, int i) {
-        xs[u] = x ? ldf(x, i) : 0.f;
+        xs[u] = ldf(x, i);
         w[u] = a.post_weight ? param(a.post_weight, a.param_bf16, i) : 1.f;
         gt[u] = gate_of(a, row, i);
         pb_[u] = a.post_bias && a.dgate ? param(a.post_bias, a.param_bf16, i) : 0.f;
       });
       columns<kWide>(d, i0, [&](int u, int i) {
         const float k = (xs[u] - pm) * pr;
-        if (a.dgate) {
-          const float v = a.scale * g[i] * fmaf(k, w[u], pb_[u]);
-          if (sum_gate) {
-            const float sum = v + (first_of_gate ? 0.f : sum_gate[i]);
-            sum_gate[i] = sum;
-            if (pgate && last_of_gate) dgate[i] = sum;
-          } else {
-            put(a.dgate, a.gate_bf16, row * a.ld_dgate + i, v);
-          }
-        }
+        if (a.dgate) put(a.dgate, a.gate_bf16, row * a.ld_dgate + i, a.scale * g[i] * fmaf(k, w[u], pb_[u]));
         const float qv = g[i] * gt[u];
         g[i] = qv;
         if (a.post_weight) {
@@ -786,12 +772,12 @@ cudaError_t fwd_strided(const ResNormArgs& a, int sms, cudaStream_t s) {
 template <typename T, int N, int NV, int G, int R, bool POST>
 cudaError_t fwd_shifted(const ResNormArgs& a, int step, int sms, cudaStream_t s) {
   auto kernel = k_resnorm_fwd_shifted<T, N, NV, G, R, POST>;
-  static_assert((2 * 3 * 16 + 3 * N * 4) * NV * G * R <= kResNormRing, "shared memory");
   static std::atomic<uint64_t> configured{0};
   static std::atomic<int> per_sm{0};
   cudaError_t e;
   const ShiftedLayout l = shifted_layout(a);
   const int smem = (2 * l.arrays * 16 + l.vectors * N * 4) * NV * G * R;
+  if (smem > kResNormRing) return cudaErrorNotSupported;  // a long row with biases and a gate
   // (as many as the registers leave, and this call's shared memory)
   const int n = resident_ctas(reinterpret_cast<const void*>(kernel), G * R, 0, kResNormRing, configured, per_sm, &e);
   if (n < 0) return e;
@@ -811,6 +797,9 @@ cudaError_t fwd_shifted_n(const ResNormArgs& a, int step, int sms, cudaStream_t 
   if (pieces <= 384) return fwd_shifted<T, N, 3, 128, 1, POST>(a, step, sms, s);
   if (pieces <= 512) return fwd_shifted<T, N, 2, 256, 1, POST>(a, step, sms, s);
   if (pieces <= 1024) return fwd_shifted<T, N, 2, 512, 1, POST>(a, step, sms, s);
+  if (pieces <= 1536) return fwd_shifted<T, N, 3, 512, 1, POST>(a, step, sms, s);
+  if constexpr (N == 4)
+    if (pieces <= 2048) return fwd_shifted<T, N, 4, 512, 1, POST>(a, step, sms, s);
   return cudaErrorNotSupported;
 }
 template <typename T, bool POST>
@@ -875,8 +864,7 @@ cudaError_t launch_resnorm_bwd(const ResNormArgs& a, int sms, int* walkers, cuda
     return a.post_weight ? resnorm_bwd_f32_post(a, w, sms, walkers, s) : resnorm_bwd_f32(a, w, sms, walkers, s);
   }
   // every sum that fits beside the row, one CTA an SM then
-  const int sums = (a.dweight != nullptr) + (a.dbias != nullptr) + (a.dpost_weight != nullptr) + (a.dpost_bias != nullptr) +
-                   (a.dgate && a.gate_rows > 1);
+  const int sums = (a.dweight != nullptr) + (a.dbias != nullptr) + (a.dpost_weight != nullptr) + (a.dpost_bias != nullptr);
   const int room = static_cast<int>(kResNormRing / (a.d * 4)) - 1, fit = sums < room ? sums : room;
   const int smem = static_cast<int>(a.d * 4) * (1 + fit);
   auto kernel = a.bf16 ? k_resnorm_bwd_long<__nv_bfloat16> : k_resnorm_bwd_long<float>;

@@ -28,7 +28,8 @@ constexpr int kResNormRing = 224 * 1024;  // of shared memory, beside the sums
 constexpr int kResNormCluster = 8;        // CTAs that share a row, at most
 // Rows that lie in their granules alike, in every operand: how many rows on they do so again. 0
 // where the operands differ; where a gate has some of the rows, for what a walker takes is not
-// contiguous; and where there are few rows of a step.
+// contiguous; and where there are few rows of a step (8191 bf16 columns: 600 rows 72 us for 62 as
+// strided ones, 20000 rows 646 for 723; 30000 x 2881 236 for 468).
 constexpr int kShiftedRows = 256;
 inline int resnorm_step(const ResNormArgs& a, bool fwd) {
   if (a.gate && a.gate_rows > 1 && a.gate_rows != a.rows) return 0;
@@ -141,7 +142,8 @@ constexpr int staged_pitch(int d, int size) { return (d * size + 31) / 16 * 16; 
 // read what others copied.
 // CLUSTER: rows too long for one CTA's shared memory. A cluster is a walker, each of its CTAs
 // has an equal run of the columns, and a row's sums are exchanged by one cluster barrier
-// while the next row is on its way.
+// while the next row is on its way. (40960 x 8192 float32, RMS with a post norm, floor 1204 us:
+// 1501; a CTA a row that waits for its loads 5030. 40960 x 16384 bf16: 2106 for 11700.)
 template <typename T, int N, int NV, int G, int R, bool RMS, bool POST, int GATE, int MODE, bool CLUSTER>
 __global__ void __launch_bounds__(G * R) k_resnorm_bwd(ResNormArgs a, int walkers, int steps) {
   constexpr bool STRIDED = MODE == ROWS_STRIDED, SHIFTED = MODE == ROWS_SHIFTED;

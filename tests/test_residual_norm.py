@@ -246,7 +246,7 @@ def test_odd_widths_over_many_rows(rows, d):
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", [k for k in KINDS if k.get("gate") != "seq"] + [dict(post=True, gate=1)], ids=str)
 @pytest.mark.parametrize("dtype,rows,d,ld", [(BF16, 2051, 1001, 1001), (BF16, 1030, 254, 258), (F32, 1027, 1003, 1003), (F32, 600, 66, 70),
-                                             (BF16, 300, 508, 512), (BF16, 2049, 2047, 2049), (BF16, 2050, 8177, 8177), (F32, 1031, 4089, 4091)])
+                                             (BF16, 300, 508, 512), (BF16, 2049, 2047, 2049), (BF16, 2050, 8177, 8177), (F32, 1031, 4089, 4091), (F32, 1025, 8150, 8150), (BF16, 2049, 9001, 9001)])
 def test_rows_that_are_cut_alike(dtype, rows, d, ld, kind):
     """Rows in granules that hold the end of the row before, or what is beside the rows."""
     def laid(t):
