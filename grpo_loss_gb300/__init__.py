@@ -290,8 +290,15 @@ def clipped_policy_loss(logp: torch.Tensor, advantages: torch.Tensor, mask: torc
                         logp_ref=None, clip=(0.2, 0.2), dual_clip: Optional[float] = None, beta: float = 0.0,
                         ratio: str = "token", reduce: str = "sequence", divisor: Optional[float] = None):
     """Autograd entry of ``policy_loss``: (loss, stats), the loss with a gradient for
-    ``logp``. The gradient is formed with the loss, and has none of its own (asking for it is
-    an error). Capture ``policy_loss`` into a CUDA graph rather than this."""
+    ``logp``, which comes from a head of the caller's own (``GRPOLoss`` keeps no graph of
+    its ``logp_pol``: there ``policy_loss``'s dlogp goes to ``backward``). The gradient is
+    formed with the loss, and has none of its own (asking for it is an error). It is the
+    loss's, but of advantages [B, T] with the ratio of a sequence, for which
+    ``ratio="sequence_token"`` asks: that of the surrogate. Capture ``policy_loss`` into a
+    CUDA graph rather than this."""
+    if ratio == "sequence" and advantages.dim() == 2:
+        raise ValueError("ratio=\"sequence\" with an advantage for each token has the gradient of another objective than "
+                         "the loss: ask for it as ratio=\"sequence_token\"")
     kw = dict(logp_old=logp_old, logp_ref=logp_ref, clip=clip, dual_clip=dual_clip, beta=beta, ratio=ratio,
               reduce=reduce, divisor=divisor)
     return _PolicyLossFn.apply(logp, advantages, mask, kw)

@@ -610,7 +610,8 @@ def _workspace(workspace, size: int, dev):
     return workspace, _vec_ptr(workspace, "workspace", workspace.dtype, workspace.numel(), dev), workspace.nbytes
 
 
-_RATIOS, _REDUCES = {"token": 0, "sequence": 1}, {"sequence": 0, "token": 1, "constant": 2}
+_RATIOS = {"token": 0, "sequence": 1, "sequence_token": 1}
+_REDUCES = {"sequence": 0, "token": 1, "constant": 2}
 
 
 def policy_workspace_size(problem: PolicyProblem) -> int:
@@ -629,8 +630,12 @@ def policy_loss(logp: torch.Tensor, advantages: torch.Tensor, mask: torch.Tensor
     be strided, as those of every [B, T] here): (loss float32 [1], dlogp float32 [B, T],
     stats float32 [4]); see grpo_policy_loss for the definition. ``advantages`` is float32
     [B] or [B, T]; ``mask`` bool or uint8 [B, T]; ``logp_old`` and ``logp_ref`` float32
-    [B, T], optional: ratio 1, and no KL term. ``clip`` is (low, high); ``ratio`` "token" or
-    "sequence"; ``reduce`` "sequence" (the mean over each sequence's tokens, then over
+    [B, T], optional: ratio 1, and no KL term. ``clip`` is (low, high); ``ratio`` "token",
+    "sequence" or "sequence_token". The last two have the ratio of the mean over a sequence,
+    with the same loss; dlogp is the loss's gradient where the advantages are [B], and where
+    they are [B, T] that of the surrogate in which each token has the sequence's ratio times
+    its own probability over itself held constant (its name is "sequence_token"; "sequence"
+    is taken for it here). ``reduce`` "sequence" (the mean over each sequence's tokens, then over
     sequences), "token" (over all tokens) or "constant" (the sum over ``divisor``).
     ``stats`` are means over valid tokens: the KL estimate, the shares of tokens whose
     gradient the lower and the upper bound took away, the ratio. dlogp is None without

@@ -2,6 +2,8 @@
 //   w = logp - old (or its mean over the sequence), r = e^w,  x = ref - logp
 //   l = -A min(r, 1 + hi) for A > 0,  -A max(min(r, dual), 1 - lo) for A < 0
 //   loss = sum c (l + beta (e^x - 1 - x)),  dlogp = c (-A r [not clipped] - beta (e^x - 1))
+// (with the mean's ratio and an advantage for each token, dlogp is the gradient where token t
+// has the ratio r times its own probability over itself held constant)
 // The weight c of a token needs the number of valid tokens (of its sequence, or of all),
 // so that the mask is read first: a launch that counts, and one that does the rest; for few
 // tokens one cluster of CTAs does both, with a barrier between.

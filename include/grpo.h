@@ -490,17 +490,23 @@ grpo_status grpo_adamw_step(const grpo_adamw_config *config, const grpo_adamw_te
  * policy's log-probability q, the drawing policy's o, the reference's p and the
  * advantage A:
  *   w = q - o                 (ratio = 0), or the mean of q - o over the sequence's valid
- *                             tokens (ratio = 1);  w = 0 without logp_old
+ *                             tokens (ratio = 1);  w = 0 without logp_old: o is then q
+ *                             itself, held constant
  *   r = exp(w)
  *   l = -A min(r, 1 + clip_high)                        for A > 0
  *       -A max(min(r, dual_clip), 1 - clip_low)         for A < 0;  0 for A = 0
  *   x = p - q,  k = exp(x) - 1 - x                      (0 without logp_ref)
  *   loss  = sum c (l + beta k)
  *   dlogp = c (-A r [r within the bound that applies] - beta (exp(x) - 1))
- * and 0 at masked tokens, of which nothing but the mask is read. The gradient of a mean
- * ratio reaches a sequence's tokens alike, so that dlogp has the same form; where a token
- * is on a bound, the gradient flows. A token's side of a bound is decided by the exact
- * difference q - o and the bound's log to 48 bits. The weight c is
+ * and 0 at masked tokens, of which nothing but the mask is read. With ratio = 0, and with
+ * ratio = 1 and an advantage for each sequence, dlogp is the gradient of loss: the n tokens
+ * of a sequence each move its mean by 1/n, and n equal terms with it. With ratio = 1 and
+ * token_adv it is not: it is that of the surrogate of the same value in which token t has the
+ * ratio r_t = [r] exp(q_t - [q_t]), [] held constant, so that a token's advantage reaches
+ * that token (the loss's own gradient would be one number for all of a sequence's tokens,
+ * the mean of their terms). Where a token is on a bound, the gradient flows. A token's side
+ * of a bound is decided by the exact difference q - o and the bound's log to 48 bits. The
+ * weight c is
  *   reduce = 0   1 / (B cnt_b), cnt_b the valid tokens of its sequence
  *   reduce = 1   1 / (all valid tokens)
  *   reduce = 2   1 / divisor
