@@ -829,6 +829,8 @@ def residual_norm_bwd(dy: torch.Tensor, dh, h: torch.Tensor, weight: torch.Tenso
             if dgate is None:
                 dgate = torch.empty(n, d, dtype=f32, device=dev)
             dgp = _vec_ptr(dgate, "dgate", f32, n * d, dev)
+        if rows == 0:       # sums of none (the library cannot tell how many rows the gate has)
+            dgate.zero_()
     problem = ResidualNormProblem(rows, d, ld_x, 0, ld_h, 0, ld_gate, ld_dy, ld_dh, ld_dx, ld_s, ld_dg, gate_rows, 0.0,
                                   scale, 1 if rms else 0, code, pcode, gcode)
     L = lib()

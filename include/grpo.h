@@ -596,7 +596,8 @@ grpo_status grpo_loss_bwd_dlogp_e4m3(const grpo_problem *problem, const uint8_t 
  * dh or h; dx may be dy, dh, h or x, and not dresidual (same strides). The backward's
  * workspace (grpo_residual_norm_workspace_size, for the current device) holds partial
  * column sums; it may be NULL when there are none to take. rows = 0 writes zeros to the
- * column sums. INVALID_ARG for null pointers, rows < 0, d < 1, a stride below d, a gate_rows
+ * column sums, and nothing to dgate, whose number of rows is not known then: its caller
+ * clears it. INVALID_ARG for null pointers, rows < 0, d < 1, a stride below d, a gate_rows
  * that does not divide rows, eps that is negative or not finite, a scale that is not finite,
  * another dtype; UNSUPPORTED for d > 32768, rows of 2^31 or more and pointers off their
  * element's alignment.
