@@ -339,18 +339,39 @@ def _residual_norm_grads(dh, dy, h, weight, mean, rstd, x, post_weight, post_bia
             dpb.to(post_bias.dtype) if need_pb else None, dg.to(gate.dtype) if need_gate else None)
 
 
+def _check_gate(gate, x) -> None:
+    """Shapes of a gate whose rows, laid out one behind the other, are each for a run of x's."""
+    lead, rows = gate[:-1], x[:-1]
+    same = 0
+    while same < len(lead) and same < len(rows) and lead[same] == rows[same]:
+        same += 1
+    n, of = lead.numel(), rows.numel()
+    fits = all(k == 1 for k in lead[same:])         # leading dimensions, and nothing for those behind
+    fits = fits or (len(lead) == 1 and n == of)     # a row for every row, flat
+    fits = fits or (len(rows) <= 1 and n > 0 and of % n == 0)
+    if not gate or gate[-1] != x[-1] or not fits:
+        raise ValueError("gate must have leading dimensions of x's %s, each row for all that follow, got %s" % (
+            tuple(x), tuple(gate)))
+
+
 def residual_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
                   bias: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
                   post_bias: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, scale: float = 1.0,
                   eps: float = 1e-5, rms: bool = False):
     """Autograd entry of the norms around a block over the last dimension: (h, y) with
     h = residual + scale * gate * post_norm(x) and y = norm(h), of x's shape; see
-    ``residual_norm_fwd``. The gate is one for each channel ([d]), or has the rows that
-    divide x's (of its leading dimensions: [sequences, d] for x [sequences, tokens, d]).
+    ``residual_norm_fwd``. ``residual`` has x's shape. The gate is one for each channel
+    ([d]), or has x's leading dimensions, each row of it for all that follow ([sequences, d]
+    or [sequences, 1, d] for x [sequences, tokens, d]; not [tokens, d]), or all of x's rows;
+    of x [rows, d], as many rows as divide x's.
     Gradients for every tensor, which have none of their own (asking for them is an error).
     Capture ``residual_norm_fwd`` and ``residual_norm_bwd`` into a CUDA graph rather than
     this."""
     d = x.shape[-1]
+    if residual.shape != x.shape:
+        raise ValueError("residual must have x's shape %s, got %s" % (tuple(x.shape), tuple(residual.shape)))
+    if gate is not None:
+        _check_gate(gate.shape, x.shape)
     h, y = _ResidualNormFn.apply(x.reshape(-1, d), residual.reshape(-1, d), weight, bias, post_weight, post_bias,
                                  None if gate is None else gate.reshape(-1, d), scale, eps, rms)
     return h.view(x.shape), y.view(x.shape)

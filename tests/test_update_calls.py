@@ -51,3 +51,54 @@ def test_no_rows_leave_no_gradient_of_a_gate(dtype, post):
     h, y = G.residual_norm(xs, xs.detach(), w, post_weight=w if post else None, gate=leaf)
     (h.float().sum() + y.float().sum()).backward()
     assert (leaf.grad == 2).all() and xs.grad.shape == xs.shape
+
+
+def _stand_in(monkeypatch):
+    """residual_norm's forward by its formula on the host, without the norms."""
+    import grpo_loss_gb300 as G
+
+    def fwd(x, r, w, b, pw, pb, gate, scale, eps, rms):
+        g = 1.0 if gate is None else gate.repeat_interleave(len(x) // len(gate), 0)
+        return r + scale * g * x, r * w, None, None, None, None
+    monkeypatch.setattr(G, "residual_norm_fwd", fwd)
+    return G.residual_norm
+
+
+@pytest.mark.parametrize("lead,gate", [
+    ((2, 6), ()), ((2, 6), (2,)), ((2, 6), (2, 1)), ((2, 6), (1, 1)), ((2, 6), (1,)), ((2, 6), (2, 6)), ((2, 6), (12,)),
+    ((4, 3, 5), (4, 3)), ((4, 3, 5), (4,)), ((4, 3, 5), (4, 3, 1)), ((4, 3, 5), (4, 1, 1)), ((4, 3, 5), (4, 3, 5)), ((4, 3, 5), (60,)),
+    ((12,), (4,)), ((12,), (12,)), ((12,), (1,)), ((12,), (4, 3)), ((12,), (4, 1)), ((), ()), ((), (1,)), ((1, 6), (1, 6)),
+    ((1, 6), (6,)), ((3, 3), (3,))])
+def test_gates_that_have_leading_dimensions(monkeypatch, lead, gate):
+    """A gate's dimensions are x's leading ones, and count for all that follow; x that is
+    flat takes gates whose rows divide its own."""
+    f = _stand_in(monkeypatch)
+    g = torch.Generator().manual_seed(1)
+    x, r, s = (torch.randn(*v, 8, generator=g, dtype=torch.float64) for v in (lead, lead, gate))
+    w = torch.ones(8, dtype=torch.float64)
+    rows, n = math.prod(lead), math.prod(gate)
+    each = s.reshape(n, 1, 8).expand(n, rows // n, 8).reshape(x.shape)
+    h, _ = f(x, r, w, gate=s, scale=0.5)
+    assert h.shape == x.shape and torch.equal(h, r + 0.5 * each * x)
+
+
+@pytest.mark.parametrize("lead,gate", [
+    ((2, 6), (6,)), ((2, 6), (1, 6)), ((2, 6), (3,)), ((2, 6), (4,)), ((2, 6), (6, 1)), ((2, 6), (6, 2)), ((2, 6), (2, 3)),
+    ((4, 3, 5), (3,)), ((4, 3, 5), (12,)), ((4, 3, 5), (1, 3)), ((4, 3, 5), (1, 3, 5)), ((4, 3, 5), (4, 1, 5)), ((4, 3, 5), (3, 4)),
+    ((4, 3, 5), (5,)), ((12,), (5,)), ((12,), (24,)), ((12,), (0,))])
+def test_gates_that_lie_otherwise_are_refused(monkeypatch, lead, gate):
+    """A gate for each position of x [sequences, positions, d], above all: its rows divide
+    x's, but are not shared by runs of them."""
+    f = _stand_in(monkeypatch)
+    with pytest.raises(ValueError, match="gate"):
+        f(torch.zeros(*lead, 8), torch.zeros(*lead, 8), torch.ones(8), gate=torch.ones(*gate, 8))
+
+
+def test_a_residual_of_another_shape_is_refused(monkeypatch):
+    f = _stand_in(monkeypatch)
+    x = torch.zeros(2, 6, 8)
+    for shape in ((6, 2, 8), (12, 8), (1, 12, 8), (2, 6, 4), (2, 3, 8)):
+        with pytest.raises(ValueError, match="residual"):
+            f(x, torch.zeros(shape), torch.ones(8))
+    with pytest.raises(ValueError, match="gate"):
+        f(x, x, torch.ones(8), gate=torch.ones(2, 6, 4))
