@@ -176,6 +176,7 @@ __device__ __forceinline__ void add_chunk(const Chunk& c, int inf, double& sum) 
 }
 
 __device__ __forceinline__ float factor_of(double norm, double max_norm, double eps) {
+  if (norm != norm) return __int_as_float(0x7FFFFFFF);  // whatever the bound
   const double f = max_norm / (norm + eps);
   return f > 1.0 || max_norm == INFINITY ? 1.f : static_cast<float>(f);
 }

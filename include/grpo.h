@@ -634,7 +634,8 @@ grpo_status grpo_residual_norm_bwd(const grpo_residual_norm_problem *problem, co
  *   norm   = sqrt(sum g^2) (norm_type = 2) or max |g| (norm_type = 0: infinity)
  *   factor = min(1, max_norm / (norm + eps)), 1 for an infinite max_norm
  *   out    = g * factor, rounded once (grpo_clip_grad_norm; out may be grad)
- * An infinity makes the norm infinite, a NaN makes it and the factor NaN. Squares neither
+ * An infinity makes the norm infinite, a NaN makes it and the factor NaN whatever max_norm
+ * (and so does 0 / 0, of max_norm = eps = 0 and gradients of zeros). Squares neither
  * overflow nor underflow; sums run in a fixed order, so that the norm does not vary
  * between calls. Where factor is 1, tensors that are their own out are not written.
  * `tensors` is host memory, read before the call returns. Tensors with n = 0 are skipped;

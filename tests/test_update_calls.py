@@ -102,3 +102,26 @@ def test_a_residual_of_another_shape_is_refused(monkeypatch):
             f(x, torch.zeros(shape), torch.ones(8))
     with pytest.raises(ValueError, match="gate"):
         f(x, x, torch.ones(8), gate=torch.ones(2, 6, 4))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [100, 300000, 3000000])
+def test_a_nan_reaches_the_factor_of_an_infinite_bound(n):
+    """In one launch, and in several."""
+    import grpo_loss_gb300 as G
+    for dtype in (F32, BF16):
+        for norm_type in (2.0, math.inf):
+            for at in (None, 0, 37, n - 1):
+                g = torch.ones(n, device="cuda", dtype=dtype)
+                if at is not None:
+                    g[at] = math.nan
+                grads, some = [g[:n // 2], g[n // 2:]], at is not None
+                norm, factor = G.grad_norm(grads, norm_type, max_norm=math.inf)
+                assert math.isnan(norm.item()) == math.isnan(factor.item()) == some and (some or factor.item() == 1)
+                out, f = [torch.zeros_like(t) for t in grads], torch.zeros(1, device="cuda")
+                norm = G.clip_grad_norm(grads, math.inf, norm_type, out=out, factor=f)
+                assert math.isnan(norm.item()) == math.isnan(f.item()) == some
+                assert all(torch.isnan(t).all() if some else torch.equal(t, u) for t, u in zip(out, grads))
+                g[0] = math.inf                      # (an infinite norm under an infinite bound: not clipped)
+                _, factor = G.grad_norm(grads, norm_type, max_norm=math.inf)
+                assert math.isnan(factor.item()) if some and at != 0 else factor.item() == 1
