@@ -877,10 +877,10 @@ def _refuse_grads(grads, out, name: str) -> None:
 def _grad_table(grads, out, name: str):
     """(an array of GradTensor, sizes, gradients' and outs' addresses, types, device)."""
     n = len(grads)
-    if not n:
-        return b"", [], [], [], [], None
     if out is not None and len(out) != n:
         raise ValueError("expected %d tensors in out, got %d" % (n, len(out)))
+    if not n:
+        return b"", [], [], [], [], None
     try:
         at, types = grads[0].get_device(), list(map(_DTYPE_OF, grads))
         codes = list(map(_PLAIN.__getitem__, types))
@@ -937,8 +937,8 @@ def _grad_call(grads, clip: bool, max_norm, norm_type, eps, out, norm, factor, w
         raise ValueError("max_norm must not be negative, got %r" % (max_norm,))
     table, sizes, places, outs, codes, dev = _grad_table(grads, out, "grads")
     if dev is None:
-        given = norm if norm is not None else factor
-        dev = given.device if given is not None else torch.device("cuda", torch.cuda.current_device())
+        given, which = (norm, "norm") if norm is not None else (factor, "factor")
+        dev = _device_of(given, which) if given is not None else torch.device("cuda", torch.cuda.current_device())
     given = norm, factor
     norm, at_norm = _vec_out(norm, "norm", torch.float32, 1, dev)
     at_factor = None

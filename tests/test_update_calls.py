@@ -125,3 +125,16 @@ def test_a_nan_reaches_the_factor_of_an_infinite_bound(n):
                 g[0] = math.inf                      # (an infinite norm under an infinite bound: not clipped)
                 _, factor = G.grad_norm(grads, norm_type, max_norm=math.inf)
                 assert math.isnan(factor.item()) if some and at != 0 else factor.item() == 1
+
+
+def test_lists_of_nothing_are_looked_at(monkeypatch):
+    """Outputs beside no gradients, and results that are not on a GPU."""
+    import grpo_loss_gb300 as G
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="expected 0 tensors in out, got 1"):
+        G.clip_grad_norm([], 1.0, out=[torch.zeros(3)])
+    for kw in (dict(norm=torch.zeros(1)), dict(factor=torch.zeros(1)), dict(norm=torch.zeros(1), workspace=torch.zeros(1 << 20))):
+        with pytest.raises(ValueError, match="CUDA"):
+            G.clip_grad_norm([], 1.0, **kw)
+        with pytest.raises(ValueError, match="CUDA"):
+            G.grad_norm([], max_norm=1.0, **kw)
