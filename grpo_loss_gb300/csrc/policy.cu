@@ -651,7 +651,8 @@ __device__ __forceinline__ void unit_tokens(const PolicyArgs& a, const Row& r, c
     }
     return;
   }
-  const float cb = -r.c * a.beta, cA = r.A == 0.f ? 0.f : r.c * r.A;
+  const bool none = r.A == 0.f;  // no advantage, no gradient, whatever the ratio
+  const float cb = -r.c * a.beta, cA = none ? 0.f : r.c * r.A;
   float d[kTokens];
 #pragma unroll
   for (int j = 0; j < kTokens; j += 2) {
@@ -675,13 +676,13 @@ __device__ __forceinline__ void unit_tokens(const PolicyArgs& a, const Row& r, c
           const float we = e ? w.y : w.x;
           const bool above = we > b.top, below = we < b.bottom;
           held[e] = above ? b.e_top : below ? a.e_down : em1[e];
-          dd[e] = above || below ? 0.f : e ? gr.y : gr.x;
+          dd[e] = above || below || none ? 0.f : e ? gr.y : gr.x;
           if (above) ++sums.high;
           if (below) ++sums.low;
         }
         row.held = add2(row.held, pair_of(held[0], held[1]));
       } else {
-        dd[0] = dd[1] = r.A == 0.f || (W == W_SEQUENCE && r.held) ? 0.f : -fmaf(cA, r.em1, cA);
+        dd[0] = dd[1] = none || (W == W_SEQUENCE && r.held) ? 0.f : -fmaf(cA, r.em1, cA);
       }
     } else {
 #pragma unroll
