@@ -545,17 +545,18 @@ __device__ __forceinline__ void tokens(const PolicyArgs& a, In in, At at, RowOf 
   if (W == W_TOKEN) sums.ratio.add(rs);
 }
 
-// Sums of a thread's tokens of one sequence, over its weight.
+// Sums of a thread's tokens of one sequence, over its weight, for up to a piece of it (9
+// units: 36 additions each, so that float32 loses 36 half steps of them at most).
 struct RowSums {
-  uint64_t held, kl, ratio;  // pairs: of the held ratios less 1, of k, of r - 1
+  // pairs: of the held ratios less 1 (with an advantage for each token, times c A), of k, of r - 1
+  uint64_t held, kl, ratio;
   __device__ __forceinline__ void clear() { held = kl = ratio = pair_of(0.f); }
 };
 template <int W, bool REF, bool TADV>
 __device__ __forceinline__ void fold(const PolicyArgs& a, const Row& r, RowSums& s, Sums& sums) {
-  if (!TADV && W == W_TOKEN && r.A != 0.f) {
-    const float2 h = of_pair(s.held);
-    sums.loss.add_product(h.x + h.y, -r.c * r.A);
-  }
+  const float2 h = of_pair(s.held);
+  if (TADV) sums.loss.add(-(h.x + h.y));
+  else if (W == W_TOKEN && r.A != 0.f) sums.loss.add_product(h.x + h.y, -r.c * r.A);
   if (REF) {
     const float2 k = of_pair(s.kl);
     sums.loss.add_product(k.x + k.y, r.c * a.beta);
@@ -638,7 +639,7 @@ __device__ __forceinline__ void unit_tokens(const PolicyArgs& a, const Row& r, c
   }
   if (far || most >= kFar) {
     const FarSums s = far_tokens<VEC, W, REF, TADV>(a, r, g, t0, valid);
-    row.held = add2(row.held, pair_of(s.held, 0.f));
+    if (!TADV) row.held = add2(row.held, pair_of(s.held, 0.f));
     row.kl = add2(row.kl, pair_of(s.kl, 0.f));
     row.ratio = add2(row.ratio, pair_of(s.ratio, 0.f));
     if (TADV) {
@@ -685,6 +686,7 @@ __device__ __forceinline__ void unit_tokens(const PolicyArgs& a, const Row& r, c
         dd[0] = dd[1] = none || (W == W_SEQUENCE && r.held) ? 0.f : -fmaf(cA, r.em1, cA);
       }
     } else {
+      float more[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float Aj = A.get(j + e), cAj = r.c * Aj, we = e ? w.y : w.x;
@@ -705,8 +707,9 @@ __device__ __forceinline__ void unit_tokens(const PolicyArgs& a, const Row& r, c
         if (some && below) ++sums.low;
         // c A in full, and of it what the ratio adds
         sums.loss.add_product(-Aj, r.c);
-        sums.loss.lo += some ? -cAj * held : 0.f;
+        more[e] = some ? cAj * held : 0.f;
       }
+      row.held = add2(row.held, pair_of(more[0], more[1]));
     }
     if (REF) {
       const float2 t = of_pair(fma2(pair_of(ex[0], ex[1]), pair_of(cb), pair_of(dd[0], dd[1])));
@@ -787,9 +790,10 @@ __device__ __forceinline__ void long_rows(const PolicyArgs& a, const Counts& cou
       step(ahead);
       if (u + 2 < u1) here_after = count_of(ahead);
     }
+    const bool begins = (a.pieces > 1 ? at.unit % (kPiece / kUnit) : at.unit) == 0;  // a piece, or a sequence
+    if (here > 0 && (begins || at.row != known)) fold<W, REF, TADV>(a, r, row_sums, sums);
     if (here > 0 && at.row != known) {
       known = at.row;
-      fold<W, REF, TADV>(a, r, row_sums, sums);
       int n = 0;
       double w = 0.0;
       if (a.reduce == 0 || W == W_SEQUENCE) {
@@ -808,7 +812,7 @@ __device__ __forceinline__ void long_rows(const PolicyArgs& a, const Counts& cou
     const int t0 = first_of(at);
     if (here > 0) {
       // (what the piece's tokens share is added with its first unit)
-      if (lane == 0 && (a.pieces > 1 ? at.unit % (kPiece / kUnit) : at.unit) == 0) add_row<W, TADV>(a, r, here, sums);
+      if (lane == 0 && begins) add_row<W, TADV>(a, r, here, sums);
       unit_tokens<VEC, W, REF, TADV>(a, r, b, g, t0, raw.valid, raw.q, raw.o, raw.p, raw.A, row_sums, sums);
     } else if (g.d) {  // nothing but the gradient's zeros
 #pragma unroll

@@ -520,7 +520,9 @@ grpo_status grpo_adamw_step(const grpo_adamw_config *config, const grpo_adamw_te
  *   dlogp  float32 [B, T], written, may be NULL
  * The workspace holds counts; for few tokens its size is 0 and it may be NULL.
  * Row strides ld_* in elements. dlogp may be logp, logp_old, logp_ref or adv [B, T] (same
- * stride). Sums are float64 in a fixed order: results do not vary between calls. B = 0 or T = 0: loss and stats are 0. INVALID_ARG for null pointers,
+ * stride). Sums run in a fixed order, so that results do not vary between calls: float32
+ * for 72 terms at most, these in two floats, and float64; c and c A are rounded to float32.
+ * B = 0 or T = 0: loss and stats are 0. INVALID_ARG for null pointers,
  * sizes below 0, a stride below T, bounds, beta or divisor outside the above or NaN;
  * UNSUPPORTED for B of 2^31 or more, T above 2^31 - 4096, B T above 2^40, and pointers off
  * their element's alignment.
