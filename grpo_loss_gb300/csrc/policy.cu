@@ -670,14 +670,14 @@ __device__ __forceinline__ void unit_tokens(const PolicyArgs& a, const Row& r, c
     }
     if (!TADV) {
       if (W == W_TOKEN) {
-        const float2 gr = of_pair(fma2(pair_of(em1[0], em1[1]), pair_of(-cA), pair_of(-cA)));
+        const float2 gr = of_pair(none ? pair_of(0.f) : fma2(pair_of(em1[0], em1[1]), pair_of(-cA), pair_of(-cA)));
         float held[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float we = e ? w.y : w.x;
           const bool above = we > b.top, below = we < b.bottom;
           held[e] = above ? b.e_top : below ? a.e_down : em1[e];
-          dd[e] = above || below || none ? 0.f : e ? gr.y : gr.x;
+          dd[e] = above || below ? 0.f : e ? gr.y : gr.x;
           if (above) ++sums.high;
           if (below) ++sums.low;
         }
