@@ -837,7 +837,7 @@ def residual_norm_bwd(dy: torch.Tensor, dh, h: torch.Tensor, weight: torch.Tenso
     wsp, size = None, 0
     if wp or bp or pwp or pbp or (dgp and gate_rows > 1):
         if workspace is None:
-            size = _bytes(("residual_norm", rows, d), L.grpo_residual_norm_workspace_size,
+            size = _bytes(("residual_norm", rows, d, rms, gate_rows > 1), L.grpo_residual_norm_workspace_size,
                           "grpo_residual_norm_workspace_size", dev, problem)
         workspace, wsp, size = _workspace(workspace, size, dev)
     _call(L.grpo_residual_norm_bwd, "grpo_residual_norm_bwd", dev, None, problem, yp, zp, hp,

@@ -839,8 +839,10 @@ constexpr int64_t kFewGates = 32;
 
 int resnorm_walkers(const ResNormArgs& a, int sms) {
   // A bound that does not depend on addresses (the workspace is sized before they are
-  // known): up to 8 walkers a CTA, 32 an SM for short rows and 8 for others.
-  const int64_t most = 8ll * sms * (a.d <= 512 ? 4 : 1), need = (a.rows + 7) / 8 * 8;
+  // known): up to 8 walkers a CTA, 32 an SM for short rows, 8 for others, and for long ones
+  // no more than an SM holds of their CTAs: 4 of 256 threads, 2 of 512 or of 1024.
+  const int64_t each = a.d <= 512 ? 32 : a.d <= 4096 ? 8 : a.d <= 8192 ? 4 : 2;
+  const int64_t most = each * sms, need = (a.rows + 7) / 8 * 8;
   return static_cast<int>(need < most ? need : most);
 }
 

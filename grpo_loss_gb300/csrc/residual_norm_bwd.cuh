@@ -650,7 +650,9 @@ cudaError_t resnorm_bwd_cluster(const ResNormArgs& a, int sms, int* walkers, cud
   const int64_t most = clusters[log].load(), half = sms / ranks / 2;
   int64_t w = a.rows;  // (rows a walker as above)
   if (w > half) w = w / 4 > half ? w / 4 : half;
+  const int64_t room = resnorm_walkers(a, sms);
   w = w < most ? w : most;
+  w = w < room ? w : room;
   *walkers = static_cast<int>(w);
   config.gridDim = dim3(static_cast<unsigned>(w * ranks));
   return cudaLaunchKernelEx(&config, kernel, a, *walkers, 1);

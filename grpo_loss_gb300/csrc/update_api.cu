@@ -107,10 +107,11 @@ bool gate_fits(const ResNormArgs& a, const void* gate) {
   return !gate || a.rows == 0 || (a.gate_rows >= 1 && a.rows % a.gate_rows == 0);
 }
 
-// Bytes for the most arrays of partial sums that a call can have: four parameters', and a
+// Bytes for the most arrays of partial sums that a call can have: the parameters', and a
 // shared gate's two.
 size_t resnorm_bytes(const ResNormArgs& a, int sms) {
-  return sizeof(float) * 6 * static_cast<size_t>(resnorm_walkers(a, sms)) * static_cast<size_t>(a.d);
+  const size_t arrays = (a.rms ? 2 : 4) + (a.gate_rows > 1 ? 2 : 0);
+  return sizeof(float) * arrays * static_cast<size_t>(resnorm_walkers(a, sms)) * static_cast<size_t>(a.d);
 }
 
 // -------------------------------------------------------------- gradients

@@ -596,7 +596,8 @@ grpo_status grpo_loss_bwd_dlogp_e4m3(const grpo_problem *problem, const uint8_t 
  *           is there
  * h may be residual or x, y may be residual or x, and not each other; dresidual may be dy,
  * dh or h; dx may be dy, dh, h or x, and not dresidual (same strides). The backward's
- * workspace (grpo_residual_norm_workspace_size, for the current device) holds partial
+ * workspace (grpo_residual_norm_workspace_size, for the current device and the problem's
+ * rows, d, rms and gate_rows, 0 or 1 for a call without a shared gate) holds partial
  * column sums; it may be NULL when there are none to take. rows = 0 writes zeros to the
  * column sums, and nothing to dgate, whose number of rows is not known then: its caller
  * clears it. INVALID_ARG for null pointers, rows < 0, d < 1, a stride below d, a gate_rows
