@@ -784,7 +784,7 @@ def residual_norm_bwd(dy: torch.Tensor, dh, h: torch.Tensor, weight: torch.Tenso
     and ``scale`` is 1, dx is dresidual, the same tensor unless one is given. The column
     sums are float32 [d]: None without ``need_params``, dbias also without ``bias`` or with
     ``rms``, dpost_bias without ``post_bias``. dgate is float32 of the gate's shape, or of
-    its type where the gate has a row for every row. ``x`` is needed for a gate or a post norm. Outputs and a workspace that
+    its type where the gate has a row for every row (a single row's gate too). ``x`` is needed for a gate or a post norm. Outputs and a workspace that
     are not given belong to ``stream``."""
     if stream is not None:
         with torch.cuda.stream(stream):

@@ -7,9 +7,9 @@
 // The weight c of a token needs the number of valid tokens (of its sequence, or of all),
 // so that the mask is read first: a launch that counts, and one that does the rest; for few
 // tokens one cluster of CTAs does both, with a barrier between.
-// Many tokens (21 bytes each) are bound by the instructions and by latency at the 16 warps an
-// SM holds beside the bytes: 256 x 32768 tokens with a KL term 38 us for the loss and 6 for
-// the count, 4.0 TB/s (one token a thread at a time with float64 sums 207 us).
+// Many tokens (17 bytes each with a KL term) are bound by the instructions and by latency at the
+// 16 warps an SM holds beside the bytes: 256 x 32768 tokens 39 us for both launches in a graph,
+// 3.6 TB/s (one token a thread at a time with float64 sums 207 us).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -35,6 +35,7 @@ constexpr int kLossCtas = 2;
 constexpr int kCluster = 16;
 // Tokens that one cluster takes: at 8 x 20480 its 16 SMs take 16.7 us where two launches over
 // all take 13.3, but those cost the host a launch and a workspace more: a call 23.7 us for 28.3.
+// (The limit is by that size alone; a call that is captured pays the difference.)
 constexpr int64_t kSmall = 96 * kChunk;
 
 // ---------------------------------------------------------------- numbers

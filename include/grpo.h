@@ -466,7 +466,9 @@ typedef struct grpo_adamw_config {
   int32_t state_bits;     /* 32 or 8 */
   int64_t step;           /* 1 for the first step */
   const float *factor;    /* device float32 [1], or NULL: multiplies grad_scale (the clip
-                             factor of grpo_grad_norm, which the host need not wait for) */
+                             factor of grpo_grad_norm, which the host need not wait for).
+                             The last field, and younger than the others: a caller compiled
+                             without it passes what lies behind its struct */
 } grpo_adamw_config;
 
 grpo_status grpo_adamw_step(const grpo_adamw_config *config, const grpo_adamw_tensor *tensors,
@@ -498,7 +500,7 @@ grpo_status grpo_adamw_step(const grpo_adamw_config *config, const grpo_adamw_te
  *   x = p - q,  k = exp(x) - 1 - x                      (0 without logp_ref)
  *   loss  = sum c (l + beta k)
  *   dlogp = c (-A r [r within the bound that applies] - beta (exp(x) - 1))
- * and 0 at masked tokens, of which nothing but the mask is read. With ratio = 0, and with
+ * and 0 at masked tokens, whose other values do not count, finite or not. With ratio = 0, and with
  * ratio = 1 and an advantage for each sequence, dlogp is the gradient of loss: the n tokens
  * of a sequence each move its mean by 1/n, and n equal terms with it. With ratio = 1 and
  * token_adv it is not: it is that of the surrogate of the same value in which token t has the
@@ -590,7 +592,7 @@ grpo_status grpo_loss_bwd_dlogp_e4m3(const grpo_problem *problem, const uint8_t 
  *   dweight, dbias, dpost_weight, dpost_bias  float32 [d], written, each may be NULL, and
  *           must be without the parameter's norm (dbias and dpost_bias: with rms)
  *   dgate   written, may be NULL: float32 [rows / gate_rows, d] contiguous, or with
- *           gate_rows = 1 of gate_dtype with row stride ld_dgate
+ *           gate_rows = 1 (a single row's gate too) of gate_dtype with row stride ld_dgate
  *   dx      may be NULL where it is not needed (it is dresidual when there is no gate and
  *           no post_weight, and scale = 1); x may be NULL when neither gate nor post_weight
  *           is there
